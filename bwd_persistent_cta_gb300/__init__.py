@@ -7,7 +7,9 @@ backward-weights runs in the library's CUDA kernels.  PyTorch is used for
 device memory and the current stream.
 
 ``RNN`` is a convenience wrapper that allocates the workspace / reserve with
-torch and calls the same entry points.
+torch and calls the same entry points; ``DeltaRule`` (the gated delta rule) and
+``BlockNorm`` (the norms, gate and residual around a block) do the same for
+theirs (``lm.py``).
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ RNN_OK, RNN_BAD_PARAM, RNN_NOT_SUPPORTED, RNN_CUDA_ERROR, RNN_TIMEOUT, RNN_BAD_W
 RNN_LSTM, RNN_GRU, RNN_RNN_RELU, RNN_RNN_TANH = 0, 1, 2, 3
 RNN_F32, RNN_BF16 = 0, 1
 RNN_ALGO_AUTO, RNN_ALGO_PERSIST_TC, RNN_ALGO_PERSIST_SIMT = 0, 1, 2
+RNN_GATE_NONE, RNN_GATE_SILU, RNN_GATE_SIGMOID = 0, 1, 2
 
 
 class rnn_desc_t(ctypes.Structure):
@@ -29,6 +32,28 @@ class rnn_desc_t(ctypes.Structure):
                 ("bidirectional", ctypes.c_int), ("num_layers", ctypes.c_int), ("seq_len", ctypes.c_int),
                 ("batch", ctypes.c_int), ("input_size", ctypes.c_int), ("hidden_size", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("batch_first", ctypes.c_int), ("algo", ctypes.c_int)]
+
+
+class rnn_delta_desc_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("seq_len", ctypes.c_int), ("heads_k", ctypes.c_int),
+                ("heads_v", ctypes.c_int), ("dim_k", ctypes.c_int), ("dim_v", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("batch_first", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class rnn_delta_in_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta")] +
+                [(n, ctypes.c_int64) for n in ("q_row", "k_row", "v_row", "g_row", "beta_row")])
+
+
+class rnn_norm_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("groups", ctypes.c_int), ("cols", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("norm_in", ctypes.c_int), ("gate", ctypes.c_int), ("residual", ctypes.c_int),
+                ("norm_out", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class rnn_norm_in_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("y", "z", "x", "w_in", "scale", "w_out")] +
+                [(n, ctypes.c_int64) for n in ("y_row", "z_row", "x_row")])
 
 
 class RnnError(RuntimeError):
@@ -71,6 +96,20 @@ _SIGS = {
                                          ctypes.POINTER(ctypes.c_double)]),
     "rnn_forward_noalloc": (ctypes.c_int, [ctypes.POINTER(rnn_desc_t)] + [_P] * 7 + [ctypes.c_int, _P]),
     "rnn_noalloc_status": (ctypes.c_int, [_P]),
+    "rnn_delta_create": (ctypes.c_int, [ctypes.POINTER(rnn_delta_desc_t), ctypes.POINTER(_P)]),
+    "rnn_delta_destroy": (ctypes.c_int, [_P]),
+    "rnn_delta_get_sizes": (ctypes.c_int, [_P] + [ctypes.POINTER(ctypes.c_size_t)] * 3),
+    "rnn_delta_set_seq_lengths": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int)]),
+    "rnn_delta_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t)] + [_P] * 6),
+    "rnn_delta_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t)] + [_P] * 11),
+    "rnn_delta_step": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t), _P, ctypes.c_int, _P, _P, _P]),
+    "rnn_delta_launch_count": (ctypes.c_uint64, [_P]),
+    "rnn_norm_create": (ctypes.c_int, [ctypes.POINTER(rnn_norm_desc_t), ctypes.POINTER(_P)]),
+    "rnn_norm_destroy": (ctypes.c_int, [_P]),
+    "rnn_norm_get_sizes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rnn_norm_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 3),
+    "rnn_norm_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 10),
+    "rnn_norm_launch_count": (ctypes.c_uint64, [_P]),
     "rnn_debug_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int,
                                       _P, ctypes.c_int64, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int, _P,
                                       ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int), ctypes.c_int,
@@ -480,3 +519,9 @@ class RNN:
 
     def debug_skip_arrival(self, cta: int):
         self._check(rnn_debug_skip_arrival(self.handle, cta), "rnn_debug_skip_arrival")
+
+
+from .lm import (  # noqa: E402
+    BlockNorm, DeltaRule, rnn_delta_backward, rnn_delta_create, rnn_delta_destroy, rnn_delta_forward,
+    rnn_delta_get_sizes, rnn_delta_launch_count, rnn_delta_set_seq_lengths, rnn_delta_step, rnn_norm_backward,
+    rnn_norm_create, rnn_norm_destroy, rnn_norm_forward, rnn_norm_get_sizes, rnn_norm_launch_count)

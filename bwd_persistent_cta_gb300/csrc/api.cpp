@@ -29,6 +29,7 @@
 
 using namespace rnn;
 
+#include "device_guard.h"
 #include "handle.h"
 
 namespace {
@@ -384,29 +385,6 @@ int init_handle_host(rnn_handle_s* h, const rnn_desc_t* desc) {
 }
 
 }  // namespace rnn
-
-namespace {
-
-// Makes the handle's device current for one call and puts the caller's
-// current device back afterwards (nothing to do when it already is current).
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    int cur = 0;
-    if (cudaGetDevice(&cur) != cudaSuccess) { ok = false; return; }
-    if (cur == dev) return;
-    if (cudaSetDevice(dev) != cudaSuccess) { ok = false; return; }
-    prev = cur;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-  DeviceGuard(const DeviceGuard&) = delete;
-  DeviceGuard& operator=(const DeviceGuard&) = delete;
-};
-
-}  // namespace
 
 namespace rnn {
 namespace {

@@ -1,0 +1,71 @@
+// delta.h - internal layouts and launch interfaces of the gated delta rule.
+//
+// Per (sequence b, value head h) = bh = b * Hv + h, with chunks of C tokens
+// counted from the start of the sequence (nc = ceil(T / C)):
+//   S0  [bh][chunk][Dv][Dk]   the state before each chunk
+//   E   [bh][t][Dv] fp32      e_t = v_t - a_t S_{t-1} k_t
+//   dS1 [bh][chunk][Dv][Dk]   the gradient of the state after each chunk
+//   Y   [bh][t][Dv] fp32      y_t, the gradient of u_t = beta_t e_t
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "rnn.h"
+
+namespace rnn {
+
+struct DeltaArgs {
+  int B, T, Hk, Hv, Dk, Dv;
+  int bfirst;
+  float scale;
+  const int* len;              // [B] valid tokens, or null = T
+  const void *q, *k, *v, *g, *beta;
+  int64_t q_row, k_row, v_row, g_row, beta_row;
+
+  __host__ __device__ int64_t row(int b, int t) const {
+    return bfirst ? static_cast<int64_t>(b) * T + t : static_cast<int64_t>(t) * B + b;
+  }
+};
+
+// exp(kDecayFloor) is below the smallest fp32 subnormal, so a decay that is
+// not representable (g = -inf included) acts as a reset: the floor keeps
+// differences of cumulative decays free of inf - inf.
+constexpr float kDecayFloor = -110.f;
+
+// --- fp32 kernels: every type and size --------------------------------------
+constexpr int kSimtChunk = 32;
+
+struct DeltaRecurArgs {
+  DeltaArgs a;
+  const float* s_in;           // [slot][Hv][Dv][Dk] or null = zero
+  float* s_out;                // same layout, or null
+  const int* slots;            // [B] or null = b
+  int num_slots;
+  void* o;
+  float* ckpt;                 // S0 of every chunk, or null
+  float* e;                    // E, or null
+};
+int launch_delta_recur(const DeltaRecurArgs& r, int is_bf16, cudaStream_t s);
+
+struct DeltaRecurBwdArgs {
+  DeltaArgs a;
+  const void* dout;
+  const float* e;              // unused here but for the chunk kernel
+  const float* dsT;            // or null
+  float* ds0;                  // or null
+  float* ckpt;                 // dS1 of every chunk
+  float* y;
+};
+int launch_delta_recur_bwd(const DeltaRecurBwdArgs& r, int is_bf16, cudaStream_t s);
+
+struct DeltaChunkBwdArgs {
+  DeltaArgs a;
+  const void* dout;
+  const float *s0, *ds1, *e, *y;
+  void *dq, *dk, *dv, *dg, *dbeta;
+};
+int launch_delta_chunk_bwd(const DeltaChunkBwdArgs& r, int is_bf16, cudaStream_t s);
+
+}  // namespace rnn

@@ -1,0 +1,580 @@
+// delta_simt.cu - the gated delta rule in fp32 arithmetic, for every storage
+// type and width: the token-by-token recurrence (which is also the serving
+// step), its reverse, and the chunk kernel that turns both states into the
+// gradients.
+#include "common.cuh"
+#include "delta.h"
+
+namespace rnn {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 4;      // warps of a recurrence CTA
+
+// Sums N values (N a power of two, at most 32) over the warp, each step
+// exchanging half of what is left, so N values cost about N + log2(32 / N)
+// shuffles instead of 5 N.  The sum of value i ends in every lane whose top
+// log2 N bits, read from bit 4 down, spell i.
+template <int N>
+__device__ __forceinline__ float warp_sum_many(float (&v)[N], int lane) {
+  int w = 16;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1, w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[i + n / 2] : v[i];
+      const float give = up ? v[i] : v[i + n / 2];
+      v[i] = keep + __shfl_xor_sync(kFull, give, w);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (; w; w >>= 1) x += __shfl_xor_sync(kFull, x, w);
+  return x;
+}
+// The lane that holds value i of warp_sum_many<N>.
+template <int N>
+__device__ __forceinline__ constexpr int sum_lane(int i) {
+  return i * (32 / N);
+}
+
+// VPL consecutive elements as fp32 (zero beyond the row).
+template <typename T, int VPL>
+__device__ __forceinline__ void load_vec(const T* p, bool in, float (&v)[VPL]) {
+  if (!in) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = 0.f;
+    return;
+  }
+  if constexpr (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) {
+      float t[4];
+      Vec4<T>::load(p + i, t);
+      v[i] = t[0]; v[i + 1] = t[1]; v[i + 2] = t[2]; v[i + 3] = t[3];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = to_f<T>(p[i]);
+  }
+}
+
+template <int VPL>
+__device__ __forceinline__ void store_state(float* p, const float (&v)[VPL]) {
+  if constexpr (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) Vec4<float>::store(p + i, {v[i], v[i + 1], v[i + 2], v[i + 3]});
+  } else if constexpr (VPL == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else {
+    p[0] = v[0];
+  }
+}
+
+// The recurrence.  A warp owns R rows of one head's state (row = one value
+// column, all of Dk across the lanes, VPL elements each); rows are independent,
+// so there is nothing to exchange but the two dot products S k and S q inside
+// the warp.  Both are taken of the old state: S_t q = a (S q) + u (k . q).
+// One token costs the chain exp -> dot -> shuffles -> update; the next token's
+// rows are loaded meanwhile.
+template <typename T, int VPL, int R>
+__global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRecurArgs r) {
+  const DeltaArgs& a = r.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (a.Dv + kWarps * R - 1) / (kWarps * R);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups);
+  const int h = static_cast<int>(bid / groups % a.Hv), b = static_cast<int>(bid / groups / a.Hv);
+  const int dv0 = (grp * kWarps + warp) * R;
+  if (dv0 >= a.Dv) return;
+  const int hk = h / (a.Hv / a.Hk);
+  const int dk0 = lane * VPL;
+  const bool in = dk0 < a.Dk;
+  int len = a.len ? a.len[b] : a.T;
+  int64_t slot = b;
+  bool live = true;
+  if (r.slots) {
+    slot = r.slots[b];
+    live = slot >= 0 && slot < r.num_slots;
+  } else if (r.num_slots >= 0 && b >= r.num_slots) {
+    live = false;
+  }
+  if (!live) len = 0;
+  const int64_t head_elems = static_cast<int64_t>(a.Dv) * a.Dk;
+  const int64_t s_off = (slot * a.Hv + h) * head_elems;
+
+  T* o = static_cast<T*>(r.o) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.Dk + dk0;
+  const T* k = static_cast<const T*>(a.k) + static_cast<int64_t>(hk) * a.Dk + dk0;
+  const T* v = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const T* g = static_cast<const T*>(a.g) + h;
+  const T* be = static_cast<const T*>(a.beta) + h;
+  const bool vin = lane < R && dv0 + lane < a.Dv;   // this lane loads / stores value row dv0 + lane
+
+  float S[R][VPL];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool ok = in && live && r.s_in != nullptr && dv0 + i < a.Dv;
+    load_vec<float, VPL>(r.s_in + s_off + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, S[i]);
+  }
+  float kc[VPL], qc[VPL], vc = 0.f, gc = 0.f, bc = 0.f;
+  if (len > 0) {
+    const int64_t row = a.row(b, 0);
+    load_vec<T, VPL>(k + row * a.k_row, in, kc);
+    load_vec<T, VPL>(q + row * a.q_row, in, qc);
+    vc = vin ? to_f<T>(v[row * a.v_row + lane]) : 0.f;
+    gc = to_f<T>(g[row * a.g_row]);
+    bc = to_f<T>(be[row * a.beta_row]);
+  }
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
+  const int nc = (a.T + kSimtChunk - 1) / kSimtChunk;
+  for (int t = 0; t < len; ++t) {
+    if (r.ckpt && t % kSimtChunk == 0 && in) {
+      float* c = r.ckpt + (bh * nc + t / kSimtChunk) * head_elems + dk0;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, S[i]);
+    }
+    float kn[VPL], qn[VPL], vn = 0.f, gn = 0.f, bn = 0.f;
+    if (t + 1 < len) {
+      const int64_t row = a.row(b, t + 1);
+      load_vec<T, VPL>(k + row * a.k_row, in, kn);
+      load_vec<T, VPL>(q + row * a.q_row, in, qn);
+      vn = vin ? to_f<T>(v[row * a.v_row + lane]) : 0.f;
+      gn = to_f<T>(g[row * a.g_row]);
+      bn = to_f<T>(be[row * a.beta_row]);
+    }
+    const float al = expf(gc);
+    float d[2 * R], kq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) d[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      kq = fmaf(kc[j], qc[j], kq);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        d[i] = fmaf(S[i][j], kc[j], d[i]);
+        d[R + i] = fmaf(S[i][j], qc[j], d[R + i]);
+      }
+    }
+    const float sum = warp_sum_many<2 * R>(d, lane);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) kq += __shfl_xor_sync(kFull, kq, w);
+    // lane i < R finishes value row dv0 + i
+    const int src = lane < R ? lane : 0;
+    const float sk = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * src);
+    const float sq = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * (R + src));
+    const float e = vc - al * sk;
+    const float u = bc * e;
+    if (vin) {
+      const int64_t row = a.row(b, t);
+      o[row * o_row + lane] = from_f<T>(a.scale * fmaf(al, sq, u * kq));
+      if (r.e) r.e[(bh * a.T + t) * a.Dv + dv0 + lane] = e;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float ui = __shfl_sync(kFull, u, i);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(ui, kc[j], al * S[i][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
+    vc = vn; gc = gn; bc = bn;
+  }
+  for (int t = len; t < a.T; ++t)
+    if (vin) o[a.row(b, t) * o_row + lane] = from_f<T>(0.f);
+  // a skipped sequence has no slot to write; one without tokens keeps its state
+  if (r.s_out && live && in && !(len == 0 && r.s_out == r.s_in)) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (dv0 + i < a.Dv) store_state<VPL>(r.s_out + s_off + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, S[i]);
+  }
+}
+
+// The reverse recurrence of the state gradient, same ownership:
+//   dS += scale do_t q_t^T;  y_t = dS k_t;  dS -= beta_t y_t k_t^T;  dS *= a_t.
+template <typename T, int VPL, int R>
+__global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const DeltaRecurBwdArgs r) {
+  const DeltaArgs& a = r.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (a.Dv + kWarps * R - 1) / (kWarps * R);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups);
+  const int h = static_cast<int>(bid / groups % a.Hv), b = static_cast<int>(bid / groups / a.Hv);
+  const int dv0 = (grp * kWarps + warp) * R;
+  if (dv0 >= a.Dv) return;
+  const int hk = h / (a.Hv / a.Hk);
+  const int dk0 = lane * VPL;
+  const bool in = dk0 < a.Dk;
+  const int len = a.len ? a.len[b] : a.T;
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
+  const int64_t head_elems = static_cast<int64_t>(a.Dv) * a.Dk;
+  const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.Dk + dk0;
+  const T* k = static_cast<const T*>(a.k) + static_cast<int64_t>(hk) * a.Dk + dk0;
+  const T* dout = static_cast<const T*>(r.dout) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const T* g = static_cast<const T*>(a.g) + h;
+  const T* be = static_cast<const T*>(a.beta) + h;
+  const bool vin = lane < R && dv0 + lane < a.Dv;
+  const int nc = (a.T + kSimtChunk - 1) / kSimtChunk;
+
+  float dS[R][VPL];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool ok = in && r.dsT != nullptr && dv0 + i < a.Dv;
+    load_vec<float, VPL>(r.dsT + bh * head_elems + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, dS[i]);
+  }
+  float kc[VPL], qc[VPL], dc = 0.f, gc = 0.f, bc = 0.f;
+  if (len > 0) {
+    const int64_t row = a.row(b, len - 1);
+    load_vec<T, VPL>(k + row * a.k_row, in, kc);
+    load_vec<T, VPL>(q + row * a.q_row, in, qc);
+    dc = vin ? to_f<T>(dout[row * o_row + lane]) : 0.f;
+    gc = to_f<T>(g[row * a.g_row]);
+    bc = to_f<T>(be[row * a.beta_row]);
+  }
+  for (int t = len - 1; t >= 0; --t) {
+    if ((t % kSimtChunk == kSimtChunk - 1 || t == len - 1) && in) {
+      float* c = r.ckpt + (bh * nc + t / kSimtChunk) * head_elems + dk0;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, dS[i]);
+    }
+    float kn[VPL], qn[VPL], dn = 0.f, gn = 0.f, bn = 0.f;
+    if (t > 0) {
+      const int64_t row = a.row(b, t - 1);
+      load_vec<T, VPL>(k + row * a.k_row, in, kn);
+      load_vec<T, VPL>(q + row * a.q_row, in, qn);
+      dn = vin ? to_f<T>(dout[row * o_row + lane]) : 0.f;
+      gn = to_f<T>(g[row * a.g_row]);
+      bn = to_f<T>(be[row * a.beta_row]);
+    }
+    const float al = expf(gc);
+    float d[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float di = a.scale * __shfl_sync(kFull, dc, i);
+      d[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        dS[i][j] = fmaf(di, qc[j], dS[i][j]);
+        d[i] = fmaf(dS[i][j], kc[j], d[i]);
+      }
+    }
+    const float sum = warp_sum_many<R>(d, lane);
+    const float y = __shfl_sync(kFull, sum, sum_lane<R>(1) * (lane < R ? lane : 0));
+    if (vin) r.y[(bh * a.T + t) * a.Dv + dv0 + lane] = y;
+    const float de = bc * y;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float ei = __shfl_sync(kFull, de, i);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) dS[i][j] = al * fmaf(-ei, kc[j], dS[i][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
+    dc = dn; gc = gn; bc = bn;
+  }
+  if (r.ds0 && in) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (dv0 + i < a.Dv) store_state<VPL>(r.ds0 + bh * head_elems + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, dS[i]);
+  }
+}
+
+// Gradients of one chunk of C = 32 tokens, one key head and all value heads
+// that share it, from the state before the chunk (S0), the state gradient after
+// it (dS1), e and y.  With G the cumulative decay inside the chunk and
+// D_ij = exp(G_i - G_j) for j <= i:
+//   N = Y E^T, Pm = dO E^T
+//   mP_ij = scale D_ij beta_j Pm_ij (j <= i),  mA_ij = -D_ij beta_i beta_j N_ij (j < i)
+//   dq = scale e^G dO S0 + mP K
+//   dk = -e^G beta Y S0 + e^{G_C - G} beta E dS1 + mP^T Q + mA K + mA^T K
+//   dv = beta Y,  dbeta = diag N
+//   dG_i = sums over row i minus column i of (mP * Q K^T + mA * K K^T), plus the
+//          products of q and k with the terms through S0, minus k with the
+//          term through dS1;  dg = suffix sums of dG plus <S1, dS1>.
+// The decay gradient uses the pair sums, not q . dq - k . dk of whole rows, so
+// that a pair on one side of a token cancels exactly instead of to rounding.
+// Thread (i, l) of 256 owns token i and key columns l, l + 8, ...; the value
+// columns pass in slices of 16.
+constexpr int kCb = kSimtChunk;      // tokens
+constexpr int kSlice = 16;           // value columns a pass
+
+template <int DKM>
+struct ChunkBwdSmem {
+  static constexpr int P = DKM + 8;  // row pitch: four tokens of a warp fall on different banks
+  float K[kCb][P], Q[kCb][P], dK[kCb][P], dQ[kCb][P];
+  float S0[kSlice][P], dS[kSlice][P];
+  float E[kCb][kSlice + 1], Y[kCb][kSlice + 1], dO[kCb][kSlice + 1];
+  float mP[kCb][kCb + 1], mA[kCb][kCb + 1], X[kCb][kCb + 1];
+  float G[kCb], eG[kCb], eE[kCb], beta[kCb], dG[kCb], w[kCb];
+  float red[8];
+};
+
+template <typename T, int DKM>
+__global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBwdArgs r) {
+  constexpr int M = DKM / 8;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  ChunkBwdSmem<DKM>& sm = *reinterpret_cast<ChunkBwdSmem<DKM>*>(smem_raw);
+  const DeltaArgs& a = r.a;
+  const int tid = threadIdx.x, i = tid >> 3, l = tid & 7, lane = tid & 31;
+  const int nc = (a.T + kCb - 1) / kCb;
+  const int64_t bid = blockIdx.x;
+  const int c = static_cast<int>(bid % nc);
+  const int hk = static_cast<int>(bid / nc % a.Hk), b = static_cast<int>(bid / nc / a.Hk);
+  const int t0 = c * kCb;
+  const int len = a.len ? a.len[b] : a.T;
+  const int nt = min(kCb, len - t0);            // valid tokens here, may be <= 0
+  const int span = min(kCb, a.T - t0);          // rows that exist
+  const int per = a.Hv / a.Hk;
+  const int64_t qk_row = static_cast<int64_t>(a.Hk) * a.Dk, v_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const int64_t head_elems = static_cast<int64_t>(a.Dv) * a.Dk;
+  const int64_t trow = a.row(b, t0 + i < a.T ? t0 + i : 0);   // this thread's token
+
+  for (int x = tid; x < kCb * a.Dk; x += 256) {
+    const int ti = x / a.Dk, d = x - ti * a.Dk;
+    const bool ok = ti < nt;
+    const int64_t row = a.row(b, t0 + (ok ? ti : 0));
+    sm.K[ti][d] = ok ? to_f<T>(static_cast<const T*>(a.k)[row * a.k_row + hk * a.Dk + d]) : 0.f;
+    sm.Q[ti][d] = ok ? to_f<T>(static_cast<const T*>(a.q)[row * a.q_row + hk * a.Dk + d]) : 0.f;
+    sm.dK[ti][d] = 0.f;
+    sm.dQ[ti][d] = 0.f;
+  }
+  __syncthreads();
+  float kk[4], qk[4];
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj) kk[jj] = qk[jj] = 0.f;
+  for (int d = 0; d < a.Dk; ++d) {
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const float kj = sm.K[l + 8 * jj][d];
+      kk[jj] = fmaf(sm.K[i][d], kj, kk[jj]);
+      qk[jj] = fmaf(sm.Q[i][d], kj, qk[jj]);
+    }
+  }
+
+  for (int hh = 0; hh < per && nt > 0; ++hh) {
+    const int h = hk * per + hh;
+    const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
+    if (tid < 32) {
+      const bool ok = tid < nt;
+      const int64_t row = a.row(b, t0 + (ok ? tid : 0));
+      float gg = ok ? to_f<T>(static_cast<const T*>(a.g)[row * a.g_row + h]) : 0.f;
+      gg = gg < kDecayFloor ? kDecayFloor : gg;
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        const float up = __shfl_up_sync(kFull, gg, w);
+        if (tid >= w) gg += up;
+      }
+      sm.G[tid] = gg;
+      sm.eG[tid] = expf(gg);
+      sm.eE[tid] = expf(__shfl_sync(kFull, gg, 31) - gg);
+      sm.beta[tid] = ok ? to_f<T>(static_cast<const T*>(a.beta)[row * a.beta_row + h]) : 0.f;
+    }
+    float N[4], Pm[4], dq1[M], dk1[M], dk3[M], frob = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) N[jj] = Pm[jj] = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) dq1[m] = dk1[m] = dk3[m] = 0.f;
+    for (int v0 = 0; v0 < a.Dv; v0 += kSlice) {
+      __syncthreads();
+      for (int x = tid; x < kCb * kSlice; x += 256) {
+        const int ti = x / kSlice, d = x % kSlice;
+        const bool ok = ti < nt && v0 + d < a.Dv;
+        const int64_t at = ok ? (bh * a.T + t0 + ti) * a.Dv + v0 + d : 0;
+        const int64_t row = a.row(b, t0 + (ok ? ti : 0));
+        const float be = ok ? sm.beta[ti] : 0.f;
+        const float y = ok ? r.y[at] : 0.f;
+        sm.E[ti][d] = ok ? r.e[at] : 0.f;
+        sm.Y[ti][d] = y;
+        sm.dO[ti][d] = ok ? to_f<T>(static_cast<const T*>(r.dout)[row * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d]) : 0.f;
+        if (ok) static_cast<T*>(r.dv)[row * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d] = from_f<T>(be * y);
+      }
+      for (int x = tid; x < kSlice * a.Dk; x += 256) {
+        const int d = x / a.Dk, kx = x - d * a.Dk;
+        const bool ok = v0 + d < a.Dv;
+        const int64_t at = (bh * nc + c) * head_elems + static_cast<int64_t>(ok ? v0 + d : 0) * a.Dk + kx;
+        const float s0 = ok ? r.s0[at] : 0.f, ds = ok ? r.ds1[at] : 0.f;
+        sm.S0[d][kx] = s0;
+        sm.dS[d][kx] = ds;
+        frob = fmaf(s0, ds, frob);
+      }
+      __syncthreads();
+      for (int d = 0; d < kSlice; ++d) {
+        const float y = sm.Y[i][d], e = sm.E[i][d], dO = sm.dO[i][d];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const float ej = sm.E[l + 8 * jj][d];
+          N[jj] = fmaf(y, ej, N[jj]);
+          Pm[jj] = fmaf(dO, ej, Pm[jj]);
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const float s0 = sm.S0[d][l + 8 * m], ds = sm.dS[d][l + 8 * m];
+          dq1[m] = fmaf(dO, s0, dq1[m]);
+          dk1[m] = fmaf(y, s0, dk1[m]);
+          dk3[m] = fmaf(e, ds, dk3[m]);
+        }
+      }
+    }
+    // columns beyond Dk hold stale shared memory: mask them
+    const float bi = sm.beta[i], eG = sm.eG[i];
+    float own = 0.f, thru = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const bool ok = l + 8 * m < a.Dk;
+      dq1[m] = ok ? dq1[m] * a.scale * eG : 0.f;
+      dk1[m] = ok ? -dk1[m] * eG * bi : 0.f;
+      dk3[m] = ok ? dk3[m] * sm.eE[i] * bi : 0.f;
+      const float qv = ok ? sm.Q[i][l + 8 * m] : 0.f, kv = ok ? sm.K[i][l + 8 * m] : 0.f;
+      own = fmaf(qv, dq1[m], fmaf(kv, dk1[m], own));
+      thru = fmaf(kv, dk3[m], thru);
+    }
+#pragma unroll
+    for (int w = 1; w < 8; w <<= 1) {
+      own += __shfl_xor_sync(kFull, own, w);
+      thru += __shfl_xor_sync(kFull, thru, w);
+    }
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) frob += __shfl_xor_sync(kFull, frob, w);
+    if (lane == 0) sm.red[tid >> 5] = frob;
+    float rows = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const int j = l + 8 * jj;
+      const float D = j <= i ? expf(sm.G[i] - sm.G[j]) : 0.f;
+      const float mp = D * a.scale * sm.beta[j] * Pm[jj];
+      const float ma = j < i ? -D * bi * sm.beta[j] * N[jj] : 0.f;
+      sm.mP[i][j] = mp;
+      sm.mA[i][j] = ma;
+      const float x = mp * qk[jj] + ma * kk[jj];
+      sm.X[i][j] = x;
+      rows += x;
+      if (j == i && i < nt) static_cast<T*>(r.dbeta)[trow * a.Hv + h] = from_f<T>(N[jj]);
+    }
+#pragma unroll
+    for (int w = 1; w < 8; w <<= 1) rows += __shfl_xor_sync(kFull, rows, w);
+    __syncthreads();
+    float cols = 0.f;
+    for (int j = l; j < kCb; j += 8) cols += sm.X[j][i];
+#pragma unroll
+    for (int w = 1; w < 8; w <<= 1) cols += __shfl_xor_sync(kFull, cols, w);
+    if (l == 0) {
+      sm.dG[i] = rows - cols + own - thru;
+      sm.w[i] = thru;
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int d = l + 8 * m;
+      if (d >= a.Dk) continue;
+      float dq = dq1[m], dk = dk1[m] + dk3[m];
+      for (int j = 0; j < kCb; ++j) {
+        dq = fmaf(sm.mP[i][j], sm.K[j][d], dq);
+        dk = fmaf(sm.mP[j][i], sm.Q[j][d], dk);
+        dk = fmaf(sm.mA[i][j] + sm.mA[j][i], sm.K[j][d], dk);
+      }
+      sm.dQ[i][d] += dq;
+      sm.dK[i][d] += dk;
+    }
+    __syncthreads();
+    if (tid < 32) {
+      float x = sm.dG[tid], w = sm.w[tid], f = tid < 8 ? sm.red[tid] : 0.f;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const float dn = __shfl_down_sync(kFull, x, s);
+        if (tid + s < 32) x += dn;
+        w += __shfl_xor_sync(kFull, w, s);
+        f += __shfl_xor_sync(kFull, f, s);
+      }
+      x += w + sm.eG[kCb - 1] * f;
+      if (tid < nt) static_cast<T*>(r.dg)[a.row(b, t0 + tid) * a.Hv + h] = from_f<T>(x);
+    }
+    __syncthreads();
+  }
+  // gradients of masked tokens are zero
+  for (int ti = max(nt, 0); ti < span; ++ti) {
+    const int64_t row = a.row(b, t0 + ti);
+    for (int hh = 0; hh < per; ++hh) {
+      const int h = hk * per + hh;
+      for (int d = tid; d < a.Dv; d += 256)
+        static_cast<T*>(r.dv)[row * v_row + static_cast<int64_t>(h) * a.Dv + d] = from_f<T>(0.f);
+      if (tid == 0) {
+        static_cast<T*>(r.dg)[row * a.Hv + h] = from_f<T>(0.f);
+        static_cast<T*>(r.dbeta)[row * a.Hv + h] = from_f<T>(0.f);
+      }
+    }
+  }
+  for (int x = tid; x < span * a.Dk; x += 256) {
+    const int ti = x / a.Dk, d = x - ti * a.Dk;
+    const int64_t at = a.row(b, t0 + ti) * qk_row + hk * a.Dk + d;
+    static_cast<T*>(r.dq)[at] = from_f<T>(sm.dQ[ti][d]);
+    static_cast<T*>(r.dk)[at] = from_f<T>(sm.dK[ti][d]);
+  }
+}
+
+int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
+
+int vpl_of(int Dk) { return Dk <= 32 ? 1 : Dk <= 64 ? 2 : Dk <= 128 ? 4 : 8; }
+
+template <typename T, int VPL, int R>
+int recur(const DeltaRecurArgs& r, cudaStream_t s) {
+  const int64_t groups = (r.a.Dv + kWarps * R - 1) / (kWarps * R);
+  delta_recur_kernel<T, VPL, R><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
+  return check_launch();
+}
+template <typename T>
+int recur_t(const DeltaRecurArgs& r, cudaStream_t s) {
+  switch (vpl_of(r.a.Dk)) {
+    case 1: return recur<T, 1, 4>(r, s);
+    case 2: return recur<T, 2, 4>(r, s);
+    case 4: return recur<T, 4, 4>(r, s);
+    default: return recur<T, 8, 4>(r, s);
+  }
+}
+template <typename T, int VPL, int R>
+int recur_bwd(const DeltaRecurBwdArgs& r, cudaStream_t s) {
+  const int64_t groups = (r.a.Dv + kWarps * R - 1) / (kWarps * R);
+  delta_recur_bwd_kernel<T, VPL, R><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
+  return check_launch();
+}
+template <typename T>
+int recur_bwd_t(const DeltaRecurBwdArgs& r, cudaStream_t s) {
+  switch (vpl_of(r.a.Dk)) {
+    case 1: return recur_bwd<T, 1, 4>(r, s);
+    case 2: return recur_bwd<T, 2, 4>(r, s);
+    case 4: return recur_bwd<T, 4, 4>(r, s);
+    default: return recur_bwd<T, 8, 4>(r, s);
+  }
+}
+template <typename T, int DKM>
+int chunk_bwd(const DeltaChunkBwdArgs& r, cudaStream_t s) {
+  const int smem = sizeof(ChunkBwdSmem<DKM>);
+  if (cudaFuncSetAttribute(delta_chunk_bwd_kernel<T, DKM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return RNN_CUDA_ERROR;
+  const int64_t nc = (r.a.T + kCb - 1) / kCb;
+  delta_chunk_bwd_kernel<T, DKM><<<static_cast<unsigned>(nc * r.a.Hk * r.a.B), 256, smem, s>>>(r);
+  return check_launch();
+}
+template <typename T>
+int chunk_bwd_t(const DeltaChunkBwdArgs& r, cudaStream_t s) {
+  return r.a.Dk <= 64 ? chunk_bwd<T, 64>(r, s) : r.a.Dk <= 128 ? chunk_bwd<T, 128>(r, s) : chunk_bwd<T, 256>(r, s);
+}
+
+}  // namespace
+
+int launch_delta_recur(const DeltaRecurArgs& r, int is_bf16, cudaStream_t s) {
+  return is_bf16 ? recur_t<__nv_bfloat16>(r, s) : recur_t<float>(r, s);
+}
+int launch_delta_recur_bwd(const DeltaRecurBwdArgs& r, int is_bf16, cudaStream_t s) {
+  return is_bf16 ? recur_bwd_t<__nv_bfloat16>(r, s) : recur_bwd_t<float>(r, s);
+}
+int launch_delta_chunk_bwd(const DeltaChunkBwdArgs& r, int is_bf16, cudaStream_t s) {
+  return is_bf16 ? chunk_bwd_t<__nv_bfloat16>(r, s) : chunk_bwd_t<float>(r, s);
+}
+
+}  // namespace rnn

@@ -340,6 +340,172 @@ rnn_status_t rnn_forward_noalloc(const rnn_desc_t* desc, const void* x, const vo
  * stream cannot be synchronised. */
 rnn_status_t rnn_noalloc_status(void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: the linear recurrence with a matrix state.  Per sequence
+ * and value head, with the state S [dim_v, dim_k] and a_t = exp(g_t):
+ *     e_t = v_t - a_t S_{t-1} k_t
+ *     S_t = a_t S_{t-1} + beta_t e_t k_t^T
+ *     o_t = scale * S_t q_t
+ * g is the log of the decay (g <= 0 in use; -inf resets the state), beta the
+ * write strength; keys are expected to have about unit length (beta |k|^2 < 2
+ * keeps the recurrence stable).  Value head h reads key head
+ * h / (heads_v / heads_k).
+ *
+ * Sequences are [T, B, heads, dim], or [B, T, heads, dim] with batch_first;
+ * g and beta are [T, B, heads_v] (or [B, T, heads_v]).  Element type of
+ * q, k, v, g, beta, o and their gradients is desc.dtype.  States (s0, sT, the
+ * pool of rnn_delta_step, ds0, dsT) are fp32 [B, heads_v, dim_v, dim_k], and
+ * every sum and state is held in fp32.
+ * The conventions at the top of this file hold, with one exception: no kernel
+ * of these operators waits for another CTA, so they need no resident grid and
+ * report nothing to a status word. */
+typedef struct {
+  int batch;           /* B >= 1                                                       */
+  int seq_len;         /* T >= 1                                                       */
+  int heads_k;         /* query / key heads, >= 1                                      */
+  int heads_v;         /* value heads, a multiple of heads_k                           */
+  int dim_k;           /* 8..256, a multiple of 8                                      */
+  int dim_v;           /* 8..256, a multiple of 8                                      */
+  int dtype;           /* rnn_dtype_t                                                  */
+  int batch_first;     /* 0 = [T,B,...], 1 = [B,T,...]                                 */
+  float scale;         /* of the output; 0 = dim_k^-1/2                                */
+} rnn_delta_desc_t;
+
+typedef struct rnn_delta_s* rnn_delta_t;
+
+/* The sequence inputs of one call.  *_row: elements from one (t, b) row to the
+ * next, so that q, k, v (and g, beta) may be slices of one packed projection;
+ * 0 = dense (heads * dim, or heads_v).  q, k and v must be 16-byte aligned
+ * with rows that are multiples of 16 bytes; g and beta need only the alignment
+ * of their element. */
+typedef struct {
+  const void* q;       /* [.., heads_k, dim_k] */
+  const void* k;       /* [.., heads_k, dim_k] */
+  const void* v;       /* [.., heads_v, dim_v] */
+  const void* g;       /* [.., heads_v]        */
+  const void* beta;    /* [.., heads_v]        */
+  int64_t q_row, k_row, v_row, g_row, beta_row;
+} rnn_delta_in_t;
+
+/* Validate ``desc`` and make a handle on the current device.  RNN_BAD_PARAM for
+ * an invalid descriptor (seq_len * batch above 2^30 included), checked before
+ * any device call; RNN_NOT_SUPPORTED when the GPU is not sm_103;
+ * RNN_CUDA_ERROR without a device.  ``*handle`` is NULL after any failure. */
+rnn_status_t rnn_delta_create(const rnn_delta_desc_t* desc, rnn_delta_t* handle);
+
+/* Free the handle.  NULL is accepted. */
+rnn_status_t rnn_delta_destroy(rnn_delta_t handle);
+
+/* Device bytes the caller provides (256-byte aligned): scratch of a forward
+ * call, scratch of a backward call, and the reserve that a training forward
+ * writes and the backward reads.  Any output pointer may be NULL. */
+rnn_status_t rnn_delta_get_sizes(rnn_delta_t handle, size_t* workspace_bytes,
+                                 size_t* backward_workspace_bytes, size_t* reserve_bytes);
+
+/* Valid tokens per sequence, as rnn_set_seq_lengths: a host array of batch
+ * ints in [0, seq_len], or NULL for full length.  Tokens at t >= lengths[b]
+ * are not read: the state stays as it was, o is zero there and so are all
+ * gradients; with length 0 the state passes through. */
+rnn_status_t rnn_delta_set_seq_lengths(rnn_delta_t handle, const int* lengths);
+
+/* Forward over whole sequences.
+ *   s0 (device, in, may be NULL = zero)   sT (device, out, may be NULL)
+ *   o  [.., heads_v, dim_v] (device, out, dense)
+ *   workspace (workspace_bytes)
+ *   reserve (reserve_bytes, out) - NULL runs inference. */
+rnn_status_t rnn_delta_forward(rnn_delta_t handle, const rnn_delta_in_t* in, const float* s0, void* o,
+                               float* sT, void* workspace, void* reserve, void* stream);
+
+/* Gradients.  Needs the reserve written by rnn_delta_forward with the same
+ * inputs and lengths (s0 is not read again: the reserve holds what is needed).
+ *   do_  gradient of o (dense)            dsT gradient of sT (may be NULL = zero)
+ *   dq, dk [.., heads_k, dim_k], dv, dg, dbeta (device, out, dense; dq and dk are
+ *   summed over the value heads of a key head)
+ *   ds0 (device, out, may be NULL)
+ *   workspace (backward_workspace_bytes) */
+rnn_status_t rnn_delta_backward(rnn_delta_t handle, const rnn_delta_in_t* in, const void* do_,
+                                const float* dsT, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                                float* ds0, void* workspace, const void* reserve, void* stream);
+
+/* The recurrent form for serving: seq_len new tokens (1 in plain decoding) of
+ * each sequence against a pool of states, updated in place.
+ *   state [num_slots, heads_v, dim_v, dim_k] fp32 (device, in and out)
+ *   slots  device int32 [B]: the state of each sequence, or NULL = sequence b
+ *          uses slot b.  A sequence whose slot lies outside [0, num_slots) is
+ *          skipped: its o is zero and no state changes.  No two sequences may
+ *          name the same slot.
+ *   o      as rnn_delta_forward. */
+rnn_status_t rnn_delta_step(rnn_delta_t handle, const rnn_delta_in_t* in, float* state, int num_slots,
+                            const int* slots, void* o, void* stream);
+
+/* Number of kernels this handle has launched since it was created. */
+uint64_t rnn_delta_launch_count(rnn_delta_t handle);
+
+/* ---------------------------------------------------------------------------
+ * Block norm: the norms after and before a block, fused with the block's gate
+ * and the scaled residual.  Per row of ``cols`` elements:
+ *     a  = y * rsqrt(mean(y^2) + eps) * w_in        (a = y without norm_in)
+ *     b  = a * act(z)                               (b = a without a gate)
+ *     x' = x + scale * b                            (x' = b without residual)
+ *     n  = x' * rsqrt(mean(x'^2) + eps) * w_out     (with norm_out)
+ * act is silu(z) = z sigma(z), or sigma(z).  n is computed from the unrounded
+ * x'.  Element type of all rows and of the weights is desc.dtype; the weights'
+ * gradients are fp32. */
+typedef enum { RNN_GATE_NONE = 0, RNN_GATE_SILU = 1, RNN_GATE_SIGMOID = 2 } rnn_gate_t;
+
+typedef struct {
+  int rows;            /* >= 1                                                         */
+  int groups;          /* >= 1: a row holds ``groups`` independent groups of cols
+                          elements (heads); the weights [cols] are shared              */
+  int cols;            /* 8..8192, a multiple of 8                                     */
+  int dtype;           /* rnn_dtype_t                                                  */
+  int norm_in;         /* 0 or 1                                                       */
+  int gate;            /* rnn_gate_t                                                   */
+  int residual;        /* 0 or 1                                                       */
+  int norm_out;        /* 0 or 1                                                       */
+  float eps;           /* > 0                                                          */
+} rnn_norm_desc_t;
+
+typedef struct rnn_norm_s* rnn_norm_t;
+
+/* The inputs of one call.  *_row: elements from one row to the next (0 = dense,
+ * groups * cols); 16-byte alignment as everywhere, row strides included. */
+typedef struct {
+  const void* y;       /* [rows, groups * cols]: the block's output                    */
+  const void* z;       /* the gate; read with desc.gate only                           */
+  const void* x;       /* the residual stream; read with desc.residual only            */
+  const void* w_in;    /* [cols] or NULL = ones                                        */
+  const void* scale;   /* [cols] or NULL = ones; read with desc.residual only          */
+  const void* w_out;   /* [cols] or NULL = ones                                        */
+  int64_t y_row, z_row, x_row;
+} rnn_norm_in_t;
+
+/* As rnn_delta_create / _destroy.  rows * groups is at most 2^30. */
+rnn_status_t rnn_norm_create(const rnn_norm_desc_t* desc, rnn_norm_t* handle);
+rnn_status_t rnn_norm_destroy(rnn_norm_t handle);
+
+/* Scratch bytes of rnn_norm_backward (the forward needs none). */
+rnn_status_t rnn_norm_get_sizes(rnn_norm_t handle, size_t* workspace_bytes);
+
+/* x_out [rows, groups * cols] (out; may be the dense x itself, updated in
+ * place), n_out (out; required with norm_out, else NULL). */
+rnn_status_t rnn_norm_forward(rnn_norm_t handle, const rnn_norm_in_t* in, void* x_out, void* n_out,
+                              void* stream);
+
+/* Gradients.  ``in`` holds the inputs of the forward (x as it was before).
+ *   dx_out, dn_out  gradients of x_out and n_out (dense; either may be NULL =
+ *                   zero, not both; dn_out is read with norm_out only)
+ *   dy, dz, dx      dense (out, each may be NULL)
+ *   dw_in, dscale, dw_out  fp32 [cols] (out, overwritten, each may be NULL;
+ *                   summed in a fixed order)
+ *   workspace       required when a weight gradient is asked for */
+rnn_status_t rnn_norm_backward(rnn_norm_t handle, const rnn_norm_in_t* in, const void* dx_out,
+                               const void* dn_out, void* dy, void* dz, void* dx, float* dw_in,
+                               float* dscale, float* dw_out, void* workspace, void* stream);
+
+/* Number of kernels this handle has launched since it was created. */
+uint64_t rnn_norm_launch_count(rnn_norm_t handle);
+
 /* Static text for a status code. */
 const char* rnn_status_string(rnn_status_t status);
 
