@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librnn.so")
 SOURCES = ["api.cpp", "tmap.cpp", "layout.cu", "gemm_simt.cu", "gemm_tc.cu",
            "persist_simt.cu", "persist_tc.cu", "persist_tc_fwd.cu", "persist_tc_bwd.cu",
-           "noalloc.cu", "lm_api.cpp", "delta_simt.cu", "norm.cu"]
+           "noalloc.cu", "lm_api.cpp", "delta_simt.cu", "delta_tc.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,1561 @@
+// delta_tc.cu - the gated delta rule by chunks of 64 tokens on tensor cores.
+//
+// With G the cumulative decay of a chunk (a token's own included),
+// D_ij = exp(G_i - G_j) for j <= i, A the strictly lower part of D * K K^T and
+// P = scale D * Q K^T (lower part with the diagonal):
+//   r = v - e^G S0 k                     e = (I + A diag(beta))^-1 r
+//   o = scale e^G S0 q + P (beta e)      S1 = e^{G_C} S0 + sum_j e^{G_C - G_j} beta_j e_j k_j^T
+// so one kernel (prep) computes what does not depend on the state, all chunks
+// at once, and one (scan) walks the chunks of a head.  Value columns are
+// independent: a warp of the scan owns 16 of them and keeps its part of the
+// state, S [16][Dk], in the accumulator fragments of mma.m16n8k16.  The
+// accumulator fragment of one product is the A operand of the next,
+//   S K^T [16][64] -> r -> r T^T [16][64] -> u -> u K [16][Dk] -> S,
+// so nothing passes through shared memory or another warp inside a chunk, which
+// is what the length of the chain (T / 64 chunks) asks for.
+//
+// Operands are fp16 scaled by a power of two that brings the largest element of
+// the tile (of a warp's 16 rows) to [2^13, 2^14); the scale leaves the product
+// in fp32.  bf16 inputs are exact that way (8 of 11 bits; what lies more than
+// 2^-29 below the tile's largest element loses bits).  Values computed here are
+// split into a high and a low fp16 part, 22 bits, where they reach the state:
+// S, r, u and the inverse; the output takes the high part alone, 11 bits where
+// its own rounding keeps 8.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "delta_tc.h"
+
+namespace rnn {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// --- scales and fragments -----------------------------------------------------
+// The power of two that brings m to [2^13, 2^14), and its inverse.
+__device__ __forceinline__ float up_scale(float m) {
+  int f = 267 - ((__float_as_int(m) >> 23) & 255);
+  f = f < 1 ? 1 : f > 253 ? 253 : f;
+  return __int_as_float(f << 23);
+}
+__device__ __forceinline__ float inv_scale(float f) { return __int_as_float((254 << 23) - __float_as_int(f)); }
+
+__device__ __forceinline__ uint32_t pack_h(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_h(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+__device__ __forceinline__ float2 unpack_b(uint32_t v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+// x = hi + lo to 22 bits.
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_h(x, y);
+  const float2 h = unpack_h(hi);
+  lo = pack_h(x - h.x, y - h.y);
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, w));
+  return m;
+}
+
+__device__ __forceinline__ void mma_h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_b(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held as fragments.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// Sixteen bytes, or zeros.
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+// Byte offset of 16-byte piece ``p`` of row ``r`` in a tile of PITCH-byte rows.
+template <int PITCH>
+__device__ __forceinline__ uint32_t swz(int r, int p) {
+  return static_cast<uint32_t>(r * PITCH + ((p ^ (r & 7)) << 4));
+}
+
+// B operand of two neighbouring n-tiles (n0, n0 + 8) and one k-step of 16, from
+// a tile whose rows are n (k along the row): b[0..1] and b[2..3].
+template <int PITCH>
+__device__ __forceinline__ void load_b_rows_n(uint32_t (&b)[4], uint32_t tile, int n0, int kk, int lane) {
+  ldsm(b, tile + swz<PITCH>(n0 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+}
+// The same from a tile whose rows are k (n along the row).
+template <int PITCH>
+__device__ __forceinline__ void load_b_rows_k(uint32_t (&b)[4], uint32_t tile, int n0, int kk, int lane) {
+  ldsm_t(b, tile + swz<PITCH>(16 * kk + (lane & 7) + (((lane >> 3) & 1) << 3), (n0 >> 3) + (lane >> 4)));
+}
+
+// Value column (of a warp's 16) behind row r of its fragments; row r + 8 is two
+// further.  A transposed fragment pair then holds four neighbouring columns.
+__device__ __forceinline__ int dv_of_row(int r) { return 4 * (r >> 1) + (r & 1); }
+
+// ---------------------------------------------------------------------------
+// prep: everything of a chunk that does not depend on the state
+// ---------------------------------------------------------------------------
+constexpr int kXP = 66;              // pitch of the fp32 64 x 64 matrices
+struct TwoF {
+  float h, l;
+};
+// (a + b) as an unevaluated sum of two floats.
+__device__ __forceinline__ TwoF two_add(TwoF a, TwoF b) {
+  const float s = a.h + b.h, bb = s - a.h;
+  const float err = (a.h - (s - bb)) + (b.h - bb);
+  const float l = err + (a.l + b.l);
+  const float h = s + l;
+  return {h, l - (h - s)};
+}
+
+// C[n][n] (+)= X Y for n = 16 or 32 on fp32 tiles in shared memory, thread t of
+// (n / 4)^2 owning 4 x 4 of C; ``neg`` negates; row k of Y is weighted by yw[k]
+// and row i of the result by cw[i] where given.  X is lower triangular with
+// KX_LOW (k <= i), Y with KY_LOW (k >= j).
+template <int N, bool X_LOW, bool Y_LOW>
+__device__ __forceinline__ void block_mul(float* C, const float* X, const float* Y, const float* yw, const float* cw,
+                                          float sign, int t) {
+  const int i0 = t / (N / 4) * 4, j0 = t % (N / 4) * 4;
+  float acc[4][4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[a][b] = 0.f;
+  const int k0 = Y_LOW ? j0 : 0, k1 = X_LOW ? i0 + 4 : N;
+  for (int k = k0; k < k1; ++k) {
+    float x[4], y[4];
+    const float w = yw ? yw[k] : 1.f;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) x[a] = X_LOW && k > i0 + a ? 0.f : X[(i0 + a) * kXP + k];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) y[b] = Y_LOW && k < j0 + b ? 0.f : w * Y[k * kXP + j0 + b];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(x[a], y[b], acc[a][b]);
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) C[(i0 + a) * kXP + j0 + b] = sign * (cw ? cw[i0 + a] : 1.f) * acc[a][b];
+}
+
+template <int DK>
+struct PrepSmem {
+  union {
+    struct {
+      unsigned char K[kTc * DK * 2], Q[kTc * DK * 2];
+    } in;
+    float X[2][kTc * kXP];           // the two inverses
+  };
+  float A[kTc * kXP];
+  float Gh[kTc], Gl[kTc], beta[kTc];
+  float red[4][4];
+};
+
+// Largest |X_ij| over the block's threads (each gives its own), for channel ch.
+__device__ __forceinline__ float block_max4(float (*red)[4], int ch, float m) {
+  m = warp_max(m);
+  if ((threadIdx.x & 31) == 0) red[ch][threadIdx.x >> 5] = m;
+  __syncthreads();
+  return fmaxf(fmaxf(red[ch][0], red[ch][1]), fmaxf(red[ch][2], red[ch][3]));
+}
+
+// One CTA of 128 threads per chunk and value head.  K K^T and Q K^T run on the
+// tensor cores from the exact bf16 inputs (warp w: rows 16 w .. 16 w + 15, the
+// blocks at or below the diagonal).  The unit triangular inverses are taken in
+// fp32: 16 x 16 diagonal blocks by substitution, a thread a column, then blocks
+// joined twice, [[X, 0], [-Y L X, Y]].  No power of L appears, so keys that are
+// all alike (L with entries near one) cost no accuracy.
+// With training, threads 0..63 work on (I + A beta)^-1 and 64..127 on
+// (I + beta A)^-1, else the second half idles in the inverse.
+template <int DK, bool TRAIN>
+__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
+  constexpr int PK = DK * 2;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nc = (a.T + kTc - 1) / kTc;
+  const int64_t bid = blockIdx.x;
+  const int c = static_cast<int>(bid % nc), h = static_cast<int>(bid / nc % a.Hv), b = static_cast<int>(bid / nc / a.Hv);
+  const int len = a.len ? a.len[b] : a.T;
+  const int t0 = c * kTc, nt = len - t0;
+  if (nt <= 0) return;
+  const int per = a.Hv / a.Hk, hk = h / per;
+  const int64_t bhc = (static_cast<int64_t>(b) * a.Hv + h) * nc + c, bkc = (static_cast<int64_t>(b) * a.Hk + hk) * nc + c;
+  const uint32_t ks = smem_u32(sm.in.K), qs = smem_u32(sm.in.Q);
+
+  for (int x = tid; x < kTc * DK / 8; x += 128) {
+    const int t = x / (DK / 8), ch = x % (DK / 8);
+    const bool ok = t < nt;
+    const int64_t row = a.row(b, t0 + (ok ? t : 0));
+    cp16_or_zero(ks + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.k) + row * a.k_row + hk * DK + ch * 8, ok);
+    cp16_or_zero(qs + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row + hk * DK + ch * 8, ok);
+  }
+  cp_commit();
+  // cumulative decay in two floats: D_ij stays exact to fp32 however large G
+  float* sc = p.w.sc + bhc * kSc;
+  if (warp == 0) {
+    TwoF g2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      const bool ok = t < nt;
+      const int64_t row = a.row(b, t0 + (ok ? t : 0));
+      float g = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[row * a.g_row + h]) : 0.f;
+      g2[i] = {g < kDecayFloor ? kDecayFloor : g, 0.f};
+      const float be = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[row * a.beta_row + h]) : 0.f;
+      sm.beta[t] = be;
+      sc[128 + t] = be;
+    }
+    TwoF pair = two_add(g2[0], g2[1]);
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const TwoF up = {__shfl_up_sync(kFull, pair.h, w), __shfl_up_sync(kFull, pair.l, w)};
+      if (lane >= w) pair = two_add(up, pair);
+    }
+    TwoF before = {__shfl_up_sync(kFull, pair.h, 1), __shfl_up_sync(kFull, pair.l, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const TwoF end = {__shfl_sync(kFull, pair.h, 31), __shfl_sync(kFull, pair.l, 31)};
+    g2[0] = two_add(before, g2[0]);
+    g2[1] = pair;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      sm.Gh[t] = g2[i].h;
+      sm.Gl[t] = g2[i].l;
+      sc[t] = expf(g2[i].h + g2[i].l);
+      sc[64 + t] = expf((end.h - g2[i].h) + (end.l - g2[i].l));
+      sc[192 + t] = g2[i].h;
+    }
+    if (lane == 0) sc[kScEnd] = expf(end.h + end.l);
+  }
+  cp_wait<0>();
+  __syncthreads();
+
+  // scales of the key and query tiles, and their fp16 copies (one head of a group writes)
+  float km = 0.f, qm = 0.f;
+  for (int x = tid; x < kTc * DK / 8; x += 128) {
+    const uint4 kv = *reinterpret_cast<const uint4*>(sm.in.K + x * 16), qv = *reinterpret_cast<const uint4*>(sm.in.Q + x * 16);
+    const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_b(kw[i]), g = unpack_b(qw[i]);
+      km = fmaxf(km, fmaxf(fabsf(f.x), fabsf(f.y)));
+      qm = fmaxf(qm, fmaxf(fabsf(g.x), fabsf(g.y)));
+    }
+  }
+  km = warp_max(km);
+  qm = warp_max(qm);
+  if (lane == 0) {
+    sm.red[0][warp] = km;
+    sm.red[1][warp] = qm;
+  }
+  __syncthreads();
+  const float kf = up_scale(fmaxf(fmaxf(sm.red[0][0], sm.red[0][1]), fmaxf(sm.red[0][2], sm.red[0][3])));
+  const float qf = up_scale(fmaxf(fmaxf(sm.red[1][0], sm.red[1][1]), fmaxf(sm.red[1][2], sm.red[1][3])));
+  if (tid == 0) {
+    sc[kScK] = inv_scale(kf);
+    sc[kScQ] = inv_scale(qf);
+  }
+  if (h % per == 0) {
+    unsigned char* ko = static_cast<unsigned char*>(p.w.k16) + bkc * kTc * PK;
+    unsigned char* qo = static_cast<unsigned char*>(p.w.q16) + bkc * kTc * PK;
+    for (int x = tid; x < kTc * DK / 8; x += 128) {
+      // piece j = 4 m + i of the permuted row: columns 32 m + 8 c + 2 i, c = 0..3
+      const int t = x / (DK / 8), j = x % (DK / 8), m = j >> 2, i = j & 3;
+      uint32_t kw[4], qw[4];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const uint32_t at = swz<PK>(t, 4 * m + cc) + 4 * i;
+        const float2 f = unpack_b(*reinterpret_cast<const uint32_t*>(sm.in.K + at));
+        const float2 g = unpack_b(*reinterpret_cast<const uint32_t*>(sm.in.Q + at));
+        kw[cc] = pack_h(f.x * kf, f.y * kf);
+        qw[cc] = pack_h(g.x * qf, g.y * qf);
+      }
+      *reinterpret_cast<uint4*>(ko + swz<PK>(t, j)) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
+      *reinterpret_cast<uint4*>(qo + swz<PK>(t, j)) = make_uint4(qw[0], qw[1], qw[2], qw[3]);
+    }
+  }
+
+  // K K^T and Q K^T
+  float kk[8][4], qk[8][4];
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
+#pragma unroll
+  for (int s = 0; s < DK / 16; ++s) {
+    uint32_t ak[4], aq[4];
+    const uint32_t at = swz<PK>(16 * warp + (lane & 15), 2 * s + (lane >> 4));
+    ldsm(ak, ks + at);
+    ldsm(aq, qs + at);
+#pragma unroll
+    for (int n = 0; n < 8; n += 2) {
+      if (n > 2 * warp) continue;
+      uint32_t bb[4];
+      load_b_rows_n<PK>(bb, ks, 8 * n, s, lane);
+      mma_b(kk[n], ak, bb[0], bb[1]);
+      mma_b(kk[n + 1], ak, bb[2], bb[3]);
+      mma_b(qk[n], aq, bb[0], bb[1]);
+      mma_b(qk[n + 1], aq, bb[2], bb[3]);
+    }
+  }
+  __syncthreads();                    // K and Q are read: X may take their place
+  float pm = 0.f;
+  const int r = lane >> 2, cc = 2 * (lane & 3);
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    if (n > 2 * warp + 1) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * warp + r + (e >> 1) * 8, j = 8 * n + cc + (e & 1);
+      const float d = j <= i ? expf((sm.Gh[i] - sm.Gh[j]) + (sm.Gl[i] - sm.Gl[j])) : 0.f;
+      sm.A[i * kXP + j] = j < i ? d * kk[n][e] : 0.f;
+      qk[n][e] = j <= i ? a.scale * d * qk[n][e] : 0.f;
+      pm = fmaxf(pm, fabsf(qk[n][e]));
+    }
+  }
+  const float pf = up_scale(block_max4(sm.red, 2, pm));
+  if (tid == 0) sc[kScP] = inv_scale(pf);
+  unsigned char* po = static_cast<unsigned char*>(p.w.p) + bhc * (TRAIN ? 2 : 1) * kTile * 2;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    if (n > 2 * warp + 1) continue;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const int i = 16 * warp + r + (e >> 1) * 8;
+      uint32_t hi, lo;
+      split(qk[n][e] * pf, qk[n][e + 1] * pf, hi, lo);
+      *reinterpret_cast<uint32_t*>(po + swz<128>(i, n) + 2 * cc) = hi;
+      if (TRAIN) *reinterpret_cast<uint32_t*>(po + kTile * 2 + swz<128>(i, n) + 2 * cc) = lo;
+    }
+  }
+
+  // the inverses: which = 0: L_ij = A_ij beta_j, which = 1: L_ij = beta_i A_ij
+  const int which = tid >> 6, col = tid & 63;
+  float* X = sm.X[which];
+  const bool mine = TRAIN || which == 0;
+  if (mine) {
+    const int b0 = col & ~15, jc = col & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == jc ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        const float w = which ? sm.beta[b0 + i] : sm.beta[b0 + j];
+        s = fmaf(-sm.A[(b0 + i) * kXP + b0 + j] * w, x[j], s);
+      }
+      x[i] = i < jc ? 0.f : s;
+      X[(b0 + i) * kXP + col] = x[i];
+    }
+  }
+  __syncthreads();
+  // pairs of 16: threads 0..31 of each half; the product L X waits in the block above the diagonal
+  const int t64 = tid & 63;
+  {
+    const int o = (t64 >> 4) * 32, t = t64 & 15;
+    float* tmp = X + o * kXP + o + 16;
+    if (mine && t64 < 32)
+      block_mul<16, false, true>(tmp, sm.A + (o + 16) * kXP + o, X + o * kXP + o, which ? nullptr : sm.beta + o,
+                                 which ? sm.beta + o + 16 : nullptr, 1.f, t);
+    __syncthreads();
+    if (mine && t64 < 32)
+      block_mul<16, true, false>(X + (o + 16) * kXP + o, X + (o + 16) * kXP + o + 16, tmp, nullptr, nullptr, -1.f, t);
+    __syncthreads();
+  }
+  // the pair of 32; its left factor's upper blocks hold the products above, which the triangular loops skip
+  float* tmp = X + 32;
+  if (mine)
+    block_mul<32, false, true>(tmp, sm.A + 32 * kXP, X, which ? nullptr : sm.beta, which ? sm.beta + 32 : nullptr, 1.f, t64);
+  __syncthreads();
+  if (mine) block_mul<32, true, false>(X + 32 * kXP, X + 32 * kXP + 32, tmp, nullptr, nullptr, -1.f, t64);
+  __syncthreads();
+  // strictly lower part, high and low
+  float xm = 0.f;
+  if (mine)
+    for (int x = t64; x < kTile; x += 64) {
+      const int i = x >> 6, j = x & 63;
+      if (j < i) xm = fmaxf(xm, fabsf(X[i * kXP + j]));
+    }
+  xm = warp_max(xm);
+  if (lane == 0) sm.red[3][warp] = xm;
+  __syncthreads();
+  if (!mine) return;
+  const float xf = up_scale(fmaxf(sm.red[3][2 * which], sm.red[3][2 * which + 1]));
+  if (t64 == 0) sc[which ? kScTB : kScTH] = inv_scale(xf);
+  unsigned char* xo = static_cast<unsigned char*>(which ? p.w.tb : p.w.th) + bhc * 2 * kTile * 2;
+  for (int x = t64; x < kTile / 8; x += 64) {
+    const int i = x >> 3, ch = x & 7;
+    if (8 * ch >= (i | 15)) continue;                 // blocks above the diagonal are not read
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = 8 * ch + 2 * k;
+      split(j < i ? X[i * kXP + j] * xf : 0.f, j + 1 < i ? X[i * kXP + j + 1] * xf : 0.f, hi[k], lo[k]);
+    }
+    *reinterpret_cast<uint4*>(xo + swz<128>(i, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(xo + kTile * 2 + swz<128>(i, ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// pieces of the scans
+// ---------------------------------------------------------------------------
+// A thread's part of a state: tile j holds, for rows r and r + 8 of the warp's
+// 16 value columns, the state columns behind positions 8 j + 2 (lane & 3).
+template <int DK>
+struct State {
+  float v[DK / 8][4];
+};
+
+// fp32 state rows <-> fragments: 8 neighbouring columns a thread, row and m.
+template <int DK>
+__device__ __forceinline__ void state_load(State<DK>& S, const float* base, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const float* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m) {
+      const float4 x = *reinterpret_cast<const float4*>(p + 32 * m), y = *reinterpret_cast<const float4*>(p + 32 * m + 4);
+      S.v[4 * m][2 * half] = x.x; S.v[4 * m][2 * half + 1] = x.y;
+      S.v[4 * m + 1][2 * half] = x.z; S.v[4 * m + 1][2 * half + 1] = x.w;
+      S.v[4 * m + 2][2 * half] = y.x; S.v[4 * m + 2][2 * half + 1] = y.y;
+      S.v[4 * m + 3][2 * half] = y.z; S.v[4 * m + 3][2 * half + 1] = y.w;
+    }
+  }
+}
+template <int DK>
+__device__ __forceinline__ void state_store(const State<DK>& S, float* base, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m) {
+      *reinterpret_cast<float4*>(p + 32 * m) = make_float4(S.v[4 * m][2 * half], S.v[4 * m][2 * half + 1],
+                                                           S.v[4 * m + 1][2 * half], S.v[4 * m + 1][2 * half + 1]);
+      *reinterpret_cast<float4*>(p + 32 * m + 4) = make_float4(S.v[4 * m + 2][2 * half], S.v[4 * m + 2][2 * half + 1],
+                                                               S.v[4 * m + 3][2 * half], S.v[4 * m + 3][2 * half + 1]);
+    }
+  }
+}
+template <int DK>
+__device__ __forceinline__ float state_max(const State<DK>& S) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S.v[j][i]));
+  return warp_max(m);
+}
+// fp16 copy of the state, scaled by f.
+template <int DK>
+__device__ __forceinline__ void state_store_half(const State<DK>& S, float f, __half* base, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __half* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_h(S.v[4 * m + i][2 * half] * f, S.v[4 * m + i][2 * half + 1] * f);
+      *reinterpret_cast<uint4*>(p + 32 * m) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// X[8][4] is [16 value columns][64 tokens] as accumulator tiles over tokens.
+using Frag = float[8][4];
+__device__ __forceinline__ void zero(Frag& x) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+}
+__device__ __forceinline__ float frag_max(const Frag& x) {
+  float m = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(x[n][i]));
+  return warp_max(m);
+}
+// A operand (k = tokens 16 kk ..) of a fragment scaled by f, high and low part.
+__device__ __forceinline__ void frag_a(const Frag& x, int kk, float f, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split(x[2 * kk][0] * f, x[2 * kk][1] * f, hi[0], lo[0]);
+  split(x[2 * kk][2] * f, x[2 * kk][3] * f, hi[1], lo[1]);
+  split(x[2 * kk + 1][0] * f, x[2 * kk + 1][1] * f, hi[2], lo[2]);
+  split(x[2 * kk + 1][2] * f, x[2 * kk + 1][3] * f, hi[3], lo[3]);
+}
+__device__ __forceinline__ void frag_a_hi(const Frag& x, int kk, float f, uint32_t (&hi)[4]) {
+  hi[0] = pack_h(x[2 * kk][0] * f, x[2 * kk][1] * f);
+  hi[1] = pack_h(x[2 * kk][2] * f, x[2 * kk][3] * f);
+  hi[2] = pack_h(x[2 * kk + 1][0] * f, x[2 * kk + 1][1] * f);
+  hi[3] = pack_h(x[2 * kk + 1][2] * f, x[2 * kk + 1][3] * f);
+}
+
+// A warp's [64 tokens][16 columns] slice of a bf16 row-major sequence: thread
+// (lane / 4, lane % 4) of tile n holds token 8 n + lane / 4, columns 4 (lane % 4)
+// .. + 3 (the columns of fragment rows 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c).
+struct Slice {
+  uint2 v[8];
+};
+__device__ __forceinline__ void slice_load(Slice& s, const __nv_bfloat16* base, const DeltaArgs& a, int64_t stride, int b,
+                                           int t0, int len, int lane) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const int t = t0 + 8 * n + (lane >> 2);
+    s.v[n] = t < len ? *reinterpret_cast<const uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) : make_uint2(0u, 0u);
+  }
+}
+// Fragment tile n (fp32) of a slice.
+__device__ __forceinline__ void slice_frag(const Slice& s, int n, float (&x)[4]) {
+  const float2 lo = unpack_b(transpose8(s.v[n].x)), hi = unpack_b(transpose8(s.v[n].y));
+  x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+}
+
+__device__ __forceinline__ float2 pair_of(const float* p, int n, int lane) {
+  return *reinterpret_cast<const float2*>(p + 8 * n + 2 * (lane & 3));
+}
+
+// Copies nbytes (a multiple of 16) of a tile, as it is, by all of the CTA's threads.
+__device__ __forceinline__ void tile_copy(uint32_t dst, const void* src, int nbytes, int nthreads) {
+  const char* s = static_cast<const char*>(src);
+  for (int i = threadIdx.x * 16; i < nbytes; i += nthreads * 16) cp16(dst + i, s + i);
+}
+
+// Z (+)= S X^T over the key columns, X = K16 or Q16: [16][64 tokens].
+template <int DK, bool BOTH>
+__device__ __forceinline__ void state_times(const State<DK>& S, float f, uint32_t x, uint32_t x2, Frag& z, Frag& z2,
+                                            int lane) {
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; ++kk) {
+    uint32_t hi[4], lo[4];
+    split(S.v[2 * kk][0] * f, S.v[2 * kk][1] * f, hi[0], lo[0]);
+    split(S.v[2 * kk][2] * f, S.v[2 * kk][3] * f, hi[1], lo[1]);
+    split(S.v[2 * kk + 1][0] * f, S.v[2 * kk + 1][1] * f, hi[2], lo[2]);
+    split(S.v[2 * kk + 1][2] * f, S.v[2 * kk + 1][3] * f, hi[3], lo[3]);
+#pragma unroll
+    for (int n = 0; n < 8; n += 2) {
+      uint32_t bb[4];
+      load_b_rows_n<DK * 2>(bb, x, 8 * n, kk, lane);
+      mma_h(z[n], hi, bb[0], bb[1]);
+      mma_h(z[n + 1], hi, bb[2], bb[3]);
+      mma_h(z[n], lo, bb[0], bb[1]);
+      mma_h(z[n + 1], lo, bb[2], bb[3]);
+      if (BOTH) {
+        load_b_rows_n<DK * 2>(bb, x2, 8 * n, kk, lane);
+        mma_h(z2[n], hi, bb[0], bb[1]);
+        mma_h(z2[n + 1], hi, bb[2], bb[3]);
+      }
+    }
+  }
+}
+
+// S = decay S + sum_t X[.][t] B[t][.], with X scaled by f, B one or two tiles of
+// 64 tokens, each with its own X; ``g`` undoes the scales.
+template <int DK>
+__device__ __forceinline__ void state_update(State<DK>& S, float decay, const Frag& x, float f, uint32_t tile, float g,
+                                             int lane) {
+  uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) frag_a(x, kk, f, hi[kk], lo[kk]);
+#pragma unroll
+  for (int j = 0; j < DK / 8; j += 4) {
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t bb[4];
+        load_b_rows_k<DK * 2>(bb, tile, 8 * (j + i), kk, lane);
+        mma_h(acc[i], hi[kk], bb[0], bb[1]);
+        mma_h(acc[i + 1], hi[kk], bb[2], bb[3]);
+        mma_h(acc[i], lo[kk], bb[0], bb[1]);
+        mma_h(acc[i + 1], lo[kk], bb[2], bb[3]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S.v[j + i][e] = fmaf(acc[i][e], g, decay * S.v[j + i][e]);
+  }
+}
+
+// Writes a fragment as fp16 rows [64][Dv] scaled by f (a warp's 16 columns).
+__device__ __forceinline__ void frag_store_half(const Frag& x, float f, __half* base, int pitch, int lane) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const uint32_t lo = transpose8(pack_h(x[n][0] * f, x[n][1] * f)), hi = transpose8(pack_h(x[n][2] * f, x[n][3] * f));
+    *reinterpret_cast<uint2*>(base + static_cast<int64_t>(8 * n + (lane >> 2)) * pitch + 4 * (lane & 3)) = make_uint2(lo, hi);
+  }
+}
+// Writes a fragment to a dense bf16 sequence.
+__device__ __forceinline__ void frag_store_seq(const Frag& x, __nv_bfloat16* base, const DeltaArgs& a, int64_t stride,
+                                               int b, int t0, int lane) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const uint32_t lo = transpose8(pack_b(x[n][0], x[n][1])), hi = transpose8(pack_b(x[n][2], x[n][3]));
+    const int t = t0 + 8 * n + (lane >> 2);
+    if (t < a.T) *reinterpret_cast<uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) = make_uint2(lo, hi);
+  }
+}
+// Zero rows t0 .. T-1 of a warp's columns.
+__device__ __forceinline__ void zero_rows(__nv_bfloat16* base, const DeltaArgs& a, int64_t stride, int b, int t0, int lane) {
+  for (int t = t0 + (lane >> 2); t < a.T; t += 8)
+    *reinterpret_cast<uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) = make_uint2(0u, 0u);
+}
+
+// ---------------------------------------------------------------------------
+// the forward scan
+// ---------------------------------------------------------------------------
+template <int DK>
+struct FwdStage {
+  unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[2][kTile * 2], P[kTile * 2];
+  float sc[kSc];
+};
+
+// blockDim.x / 32 warps of one value head, 16 value columns each.
+template <int DK, bool TRAIN>
+__global__ void __launch_bounds__(256) delta_scan_fwd_kernel(const DeltaTcArgs p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  FwdStage<DK>* st = reinterpret_cast<FwdStage<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthr = blockDim.x;
+  const int groups = a.Dv / (nthr / 2);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
+            b = static_cast<int>(bid / groups / a.Hv);
+  const int slice = grp * (nthr >> 5) + warp, dv0 = slice * 16;
+  const int hk = h / (a.Hv / a.Hk);
+  const int len = a.len ? a.len[b] : a.T;
+  const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t s_off = (bh * a.Dv + dv0) * DK;
+
+  auto fetch = [&](int c) {
+    FwdStage<DK>& s = st[c & 1];
+    tile_copy(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
+    tile_copy(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
+    tile_copy(smem_u32(s.T), static_cast<const char*>(p.w.th) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
+    tile_copy(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * (TRAIN ? 4 : 2), kTile * 2, nthr);
+    tile_copy(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc, kSc * 4, nthr);
+    cp_commit();
+  };
+
+  State<DK> S;
+  if (p.s_in) {
+    state_load<DK>(S, p.s_in + s_off, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
+  }
+  Slice vs;
+  if (ncb > 0) {
+    fetch(0);
+    slice_load(vs, v, a, a.v_row, b, 0, len, lane);
+  }
+  for (int c = 0; c < ncb; ++c) {
+    cp_wait<0>();
+    __syncthreads();                       // chunk c is here, and nobody reads the other stage
+    if (c + 1 < ncb) fetch(c + 1);
+    const FwdStage<DK>& s = st[c & 1];
+    const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
+
+    const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
+    if (TRAIN) {
+      state_store_half<DK>(S, sf, static_cast<__half*>(p.w.s0) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
+      if (lane == 0) p.w.s0_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
+    }
+    Frag z, oq;
+    zero(z);
+    zero(oq);
+    state_times<DK, true>(S, sf, ks, qs, z, oq, lane);
+    // r = v - e^G S0 k
+    const float zk = si * s.sc[kScK], zq = si * s.sc[kScQ] * a.scale;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 eg = pair_of(s.sc, n, lane);
+      float x[4];
+      slice_frag(vs, n, x);
+      z[n][0] = fmaf(-eg.x * zk, z[n][0], x[0]);
+      z[n][1] = fmaf(-eg.y * zk, z[n][1], x[1]);
+      z[n][2] = fmaf(-eg.x * zk, z[n][2], x[2]);
+      z[n][3] = fmaf(-eg.y * zk, z[n][3], x[3]);
+      oq[n][0] *= eg.x * zq; oq[n][1] *= eg.y * zq; oq[n][2] *= eg.x * zq; oq[n][3] *= eg.y * zq;
+    }
+    if (c + 1 < ncb) slice_load(vs, v, a, a.v_row, b, (c + 1) * kTc, len, lane);
+    // e = r + (T - I) r: the identity stays in fp32
+    Frag acc;
+    zero(acc);
+    const float rf = up_scale(frag_max(z));
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      frag_a(z, kk, rf, hi, lo);
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        if (n < 2 * kk) continue;          // j <= i
+        uint32_t bh_[4], bl_[4];
+        load_b_rows_n<128>(bh_, ts, 8 * n, kk, lane);
+        load_b_rows_n<128>(bl_, ts + kTile * 2, 8 * n, kk, lane);
+        mma_h(acc[n], hi, bh_[0], bh_[1]);
+        mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        mma_h(acc[n], lo, bh_[0], bh_[1]);
+        mma_h(acc[n + 1], lo, bh_[2], bh_[3]);
+        mma_h(acc[n], hi, bl_[0], bl_[1]);
+        mma_h(acc[n + 1], hi, bl_[2], bl_[3]);
+      }
+    }
+    const float ti = inv_scale(rf) * s.sc[kScTH];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[n][i], ti, z[n][i]);
+    if (TRAIN) {
+      const float ef = up_scale(frag_max(z));
+      frag_store_half(z, ef, static_cast<__half*>(p.w.e) + (bh * nc + c) * kTc * a.Dv + dv0, a.Dv, lane);
+      if (lane == 0) p.w.e_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(ef);
+    }
+    // u = beta e; o = scale e^G S0 q + P u
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 be = pair_of(s.sc + 128, n, lane);
+      z[n][0] *= be.x; z[n][1] *= be.y; z[n][2] *= be.x; z[n][3] *= be.y;
+    }
+    const float uf = up_scale(frag_max(z));
+    zero(acc);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4];
+      frag_a_hi(z, kk, uf, hi);
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        if (n < 2 * kk) continue;
+        uint32_t bb[4];
+        load_b_rows_n<128>(bb, ps, 8 * n, kk, lane);
+        mma_h(acc[n], hi, bb[0], bb[1]);
+        mma_h(acc[n + 1], hi, bb[2], bb[3]);
+      }
+    }
+    const float pi = inv_scale(uf) * s.sc[kScP];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) oq[n][i] = fmaf(acc[n][i], pi, oq[n][i]);
+    frag_store_seq(oq, o, a, o_row, b, c * kTc, lane);
+    // S1 = e^{G_C} S0 + (e^{G_C - G} u) k
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 ee = pair_of(s.sc + 64, n, lane);
+      z[n][0] *= ee.x; z[n][1] *= ee.y; z[n][2] *= ee.x; z[n][3] *= ee.y;
+    }
+    const float wf = up_scale(frag_max(z));
+    state_update<DK>(S, s.sc[kScEnd], z, wf, ks, inv_scale(wf) * s.sc[kScK], lane);
+  }
+  zero_rows(o, a, o_row, b, ncb * kTc, lane);
+  if (p.s_out) state_store<DK>(S, p.s_out + s_off, lane);
+}
+
+int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
+
+// Warps of a scan CTA (16 value columns each): as many as share the chunk's
+// tiles without leaving SMs idle.
+int scan_warps(const DeltaArgs& a, int num_sms) {
+  const int n = a.Dv / 16;
+  for (int w = 8; w > 2; w >>= 1)
+    if (n % w == 0 && static_cast<int64_t>(a.B) * a.Hv * (n / w) >= num_sms * 3 / 4) return w;
+  return 2;
+}
+
+template <typename F>
+int set_smem(F* f, int bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? 0 : RNN_CUDA_ERROR;
+}
+
+template <int DK, bool TRAIN>
+int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
+  const int nc = (t.a.T + kTc - 1) / kTc;
+  const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>);
+  if (set_smem(delta_prep_kernel<DK, TRAIN>, psm) || set_smem(delta_scan_fwd_kernel<DK, TRAIN>, fsm)) return RNN_CUDA_ERROR;
+  delta_prep_kernel<DK, TRAIN><<<static_cast<unsigned>(static_cast<int64_t>(nc) * t.a.Hv * t.a.B), 128, psm, s>>>(t);
+  int rc = check_launch();
+  if (rc) return rc;
+  ++*launches;
+  const int w = scan_warps(t.a, t.num_sms);
+  const int64_t grid = static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w));
+  delta_scan_fwd_kernel<DK, TRAIN><<<static_cast<unsigned>(grid), 32 * w, fsm, s>>>(t);
+  rc = check_launch();
+  if (!rc) ++*launches;
+  return rc;
+}
+
+// ---------------------------------------------------------------------------
+// the reverse scan
+// ---------------------------------------------------------------------------
+// The same ownership for the state gradient, chunks in reverse:
+//   du = P^T do + e^{G_C - G} dS1 k          y = (I + beta A)^-T du
+//   dS0 = e^{G_C} dS1 + (scale e^G do) q^T - (e^G beta y) k^T,   dv = beta y
+template <int DK>
+struct BwdStage {
+  unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[2][kTile * 2], P[2][kTile * 2];
+  float sc[kSc];
+};
+
+template <int DK>
+__global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArgs p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  BwdStage<DK>* st = reinterpret_cast<BwdStage<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthr = blockDim.x;
+  const int groups = a.Dv / (nthr / 2);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
+            b = static_cast<int>(bid / groups / a.Hv);
+  const int slice = grp * (nthr >> 5) + warp, dv0 = slice * 16;
+  const int hk = h / (a.Hv / a.Hk);
+  const int len = a.len ? a.len[b] : a.T;
+  const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(p.dout) + static_cast<int64_t>(h) * a.Dv + dv0;
+  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t s_off = (bh * a.Dv + dv0) * DK;
+
+  auto fetch = [&](int c) {
+    BwdStage<DK>& s = st[c & 1];
+    tile_copy(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
+    tile_copy(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
+    tile_copy(smem_u32(s.T), static_cast<const char*>(p.w.tb) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
+    tile_copy(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
+    tile_copy(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc, kSc * 4, nthr);
+    cp_commit();
+  };
+
+  State<DK> S;
+  if (p.dsT) {
+    state_load<DK>(S, p.dsT + s_off, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
+  }
+  Slice ds;
+  if (ncb > 0) {
+    fetch(ncb - 1);
+    slice_load(ds, dout, a, o_row, b, (ncb - 1) * kTc, len, lane);
+  }
+  for (int c = ncb - 1; c >= 0; --c) {
+    cp_wait<0>();
+    __syncthreads();
+    if (c > 0) fetch(c - 1);
+    const BwdStage<DK>& s = st[c & 1];
+    const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
+
+    const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
+    state_store_half<DK>(S, sf, static_cast<__half*>(p.ds1) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
+    if (lane == 0) p.ds1_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
+    Frag z, acc;
+    zero(z);
+    state_times<DK, false>(S, sf, ks, ks, z, z, lane);
+    // P^T do: do is exact in fp16 once scaled
+    zero(acc);
+    float dm = 0.f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 x = unpack_b(ds.v[n].x), y = unpack_b(ds.v[n].y);
+      dm = fmaxf(fmaxf(dm, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
+    }
+    const float df = up_scale(warp_max(dm));
+    if (lane == 0) p.do_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(df);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      float x[4], y[4];
+      slice_frag(ds, 2 * kk, x);
+      slice_frag(ds, 2 * kk + 1, y);
+      const uint32_t ad[4] = {pack_h(x[0] * df, x[1] * df), pack_h(x[2] * df, x[3] * df), pack_h(y[0] * df, y[1] * df),
+                              pack_h(y[2] * df, y[3] * df)};
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        if (n > 2 * kk) continue;          // j <= i
+        uint32_t bh_[4], bl_[4];
+        load_b_rows_k<128>(bh_, ps, 8 * n, kk, lane);
+        load_b_rows_k<128>(bl_, ps + kTile * 2, 8 * n, kk, lane);
+        mma_h(acc[n], ad, bh_[0], bh_[1]);
+        mma_h(acc[n + 1], ad, bh_[2], bh_[3]);
+        mma_h(acc[n], ad, bl_[0], bl_[1]);
+        mma_h(acc[n + 1], ad, bl_[2], bl_[3]);
+      }
+    }
+    const float zk = si * s.sc[kScK], pi = inv_scale(df) * s.sc[kScP];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 ee = pair_of(s.sc + 64, n, lane);
+      z[n][0] = fmaf(acc[n][0], pi, ee.x * zk * z[n][0]);
+      z[n][1] = fmaf(acc[n][1], pi, ee.y * zk * z[n][1]);
+      z[n][2] = fmaf(acc[n][2], pi, ee.x * zk * z[n][2]);
+      z[n][3] = fmaf(acc[n][3], pi, ee.y * zk * z[n][3]);
+    }
+    // y = du + (T - I)^T du
+    zero(acc);
+    const float uf = up_scale(frag_max(z));
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      frag_a(z, kk, uf, hi, lo);
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        if (n > 2 * kk) continue;
+        uint32_t bh_[4], bl_[4];
+        load_b_rows_k<128>(bh_, ts, 8 * n, kk, lane);
+        load_b_rows_k<128>(bl_, ts + kTile * 2, 8 * n, kk, lane);
+        mma_h(acc[n], hi, bh_[0], bh_[1]);
+        mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        mma_h(acc[n], lo, bh_[0], bh_[1]);
+        mma_h(acc[n + 1], lo, bh_[2], bh_[3]);
+        mma_h(acc[n], hi, bl_[0], bl_[1]);
+        mma_h(acc[n + 1], hi, bl_[2], bl_[3]);
+      }
+    }
+    const float ti = inv_scale(uf) * s.sc[kScTB];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[n][i], ti, z[n][i]);
+    const float yf = up_scale(frag_max(z));
+    frag_store_half(z, yf, static_cast<__half*>(p.y) + (bh * nc + c) * kTc * a.Dv + dv0, a.Dv, lane);
+    if (lane == 0) p.y_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(yf);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 be = pair_of(s.sc + 128, n, lane);
+      z[n][0] *= be.x; z[n][1] *= be.y; z[n][2] *= be.x; z[n][3] *= be.y;
+    }
+    frag_store_seq(z, dv, a, o_row, b, c * kTc, lane);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 eg = pair_of(s.sc, n, lane);
+      float x[4];
+      slice_frag(ds, n, x);
+      acc[n][0] = a.scale * eg.x * x[0]; acc[n][1] = a.scale * eg.y * x[1];
+      acc[n][2] = a.scale * eg.x * x[2]; acc[n][3] = a.scale * eg.y * x[3];
+      z[n][0] *= -eg.x; z[n][1] *= -eg.y; z[n][2] *= -eg.x; z[n][3] *= -eg.y;
+    }
+    if (c > 0) slice_load(ds, dout, a, o_row, b, (c - 1) * kTc, len, lane);
+    const float af = up_scale(frag_max(acc)), xf = up_scale(frag_max(z));
+    state_update<DK>(S, s.sc[kScEnd], acc, af, qs, inv_scale(af) * s.sc[kScQ], lane);
+    state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], lane);
+  }
+  zero_rows(dv, a, o_row, b, ncb * kTc, lane);
+  if (p.ds0) state_store<DK>(S, p.ds0 + s_off, lane);
+}
+
+// ---------------------------------------------------------------------------
+// the gradients of q, k, g and beta, all chunks at once
+// ---------------------------------------------------------------------------
+// The sums of delta_chunk_bwd_kernel (delta_simt.cu) on the tensor cores, with
+// single fp16 operands: every output is rounded to bf16, 8 times coarser.  A CTA
+// walks chunks of a key head with a stride; per value head the value columns
+// pass in slices of 64 through two stages, the next one (and the next chunk's
+// keys and queries) arriving while this one is multiplied.  Warp (rg, cq) of
+// 2 x 4 owns rows 32 rg .. + 31 and a quarter of the columns of every product.
+// The fp16 copies of S0, dS1, e, y and do carry one scale per 16 value columns,
+// i.e. per k-step of the products that sum over value columns; the ratio to the
+// head's largest is applied to the A operand, exactly (a power of two).
+template <int DK>
+struct GradSmem {
+  struct Stage {
+    unsigned char dO[kTc * 128], E[kTc * 128], Y[kTc * 128];     // [64 tokens][64 columns]
+    unsigned char S0[64 * DK * 2], dS[64 * DK * 2];              // [64 value columns][Dk]
+  } st[2];
+  unsigned char K[2][kTc * DK * 2], Q[2][kTc * DK * 2];
+  unsigned char mP[kTile * 2], mA[kTile * 2];
+  float eG[kTc], eE[kTc], beta[kTc], G[kTc];
+  // ratios per k-step (fp16 pairs) and inverse scales of the five products of a head
+  uint32_t ratio[5][16];
+  float inv[5];
+  float own[4][kTc], thru[4][kTc], row[4][kTc], col[2][kTc];
+  float red[8], mx[2][8];
+};
+enum { kRq = 0, kRk1, kRk3, kRn, kRp };
+
+struct GradPos {
+  int64_t item;        // (b * Hk + hk) * nc + c
+  int hh, sl;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p) {
+  constexpr int PK = DK * 2, NQ = DK / 32;     // n-tiles of a warp's quarter
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  GradSmem<DK>& sm = *reinterpret_cast<GradSmem<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = warp >> 2, cq = warp & 3;
+  const int r = lane >> 2, cc = 2 * (lane & 3);
+  const int nc = (a.T + kTc - 1) / kTc, per = a.Hv / a.Hk, ns = (a.Dv + 63) / 64, n16 = a.Dv / 16;
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * nc;
+  const int64_t qk_row = static_cast<int64_t>(a.Hk) * DK, v_row = static_cast<int64_t>(a.Hv) * a.Dv;
+
+  auto tokens = [&](int64_t item) {
+    const int b = static_cast<int>(item / nc / a.Hk);
+    return (a.len ? a.len[b] : a.T) - static_cast<int>(item % nc) * kTc;
+  };
+  auto next_item = [&](int64_t item) {
+    while (item < items && tokens(item) <= 0) item += gridDim.x;
+    return item;
+  };
+  // this CTA's chunks without tokens: zeros
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    if (tokens(item) > 0) continue;
+    const int b = static_cast<int>(item / nc / a.Hk), hk = static_cast<int>(item / nc % a.Hk), t0 = static_cast<int>(item % nc) * kTc;
+    const int span = min(kTc, a.T - t0);
+    for (int x = tid; x < span * DK / 8; x += 256) {
+      const int64_t at = a.row(b, t0 + x / (DK / 8)) * qk_row + hk * DK + x % (DK / 8) * 8;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + at) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int x = tid; x < span * per; x += 256) {
+      const int64_t at = a.row(b, t0 + x / per) * a.Hv + hk * per + x % per;
+      static_cast<__nv_bfloat16*>(p.dg)[at] = __float2bfloat16_rn(0.f);
+      static_cast<__nv_bfloat16*>(p.dbeta)[at] = __float2bfloat16_rn(0.f);
+    }
+  }
+
+  auto head_chunk = [&](const GradPos& g) {
+    const int64_t bk = g.item / nc;
+    return ((bk / a.Hk * a.Hv + bk % a.Hk * per + g.hh) * nc) + g.item % nc;
+  };
+  auto fetch = [&](const GradPos& g, int stage, int kq) {
+    const int b = static_cast<int>(g.item / nc / a.Hk), hk = static_cast<int>(g.item / nc % a.Hk),
+              t0 = static_cast<int>(g.item % nc) * kTc, nt = tokens(g.item);
+    const int64_t bhc = head_chunk(g);
+    typename GradSmem<DK>::Stage& s = sm.st[stage];
+    const uint32_t dO = smem_u32(s.dO), E = smem_u32(s.E), Y = smem_u32(s.Y), S0 = smem_u32(s.S0), dS = smem_u32(s.dS);
+    const int v0 = g.sl * 64;
+#pragma unroll
+    for (int x = tid; x < kTc * 8; x += 256) {
+      const int t = x >> 3, ch = x & 7;
+      const bool in = v0 + ch * 8 < a.Dv;
+      const int64_t at = (bhc * kTc + t) * a.Dv + (in ? v0 + ch * 8 : 0);
+      const bool ok = in && t < nt;
+      const int64_t row = a.row(b, t0 + (ok ? t : 0)) * v_row + static_cast<int64_t>(hk * per + g.hh) * a.Dv + (in ? v0 + ch * 8 : 0);
+      cp16_or_zero(dO + swz<128>(t, ch), static_cast<const __nv_bfloat16*>(p.dout) + row, ok);
+      cp16_or_zero(E + swz<128>(t, ch), static_cast<const __half*>(p.w.e) + at, in);
+      cp16_or_zero(Y + swz<128>(t, ch), static_cast<const __half*>(p.y) + at, in);
+    }
+#pragma unroll
+    for (int x = tid; x < 64 * DK / 8; x += 256) {
+      const int d = x / (DK / 8), ch = x % (DK / 8);
+      const bool in = v0 + d < a.Dv;
+      const int64_t at = (bhc * a.Dv + (in ? v0 + d : 0)) * DK + ch * 8;
+      cp16_or_zero(S0 + swz<PK>(d, ch), static_cast<const __half*>(p.w.s0) + at, in);
+      cp16_or_zero(dS + swz<PK>(d, ch), static_cast<const __half*>(p.ds1) + at, in);
+    }
+    if (g.hh == 0 && g.sl == 0) {
+      const uint32_t ks = smem_u32(sm.K[kq]), qs = smem_u32(sm.Q[kq]);
+#pragma unroll
+      for (int x = tid; x < kTc * DK / 8; x += 256) {
+        const int t = x / (DK / 8), ch = x % (DK / 8);
+        const bool ok = t < nt;
+        const int64_t row = a.row(b, t0 + (ok ? t : 0));
+        cp16_or_zero(ks + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.k) + row * a.k_row + hk * DK + ch * 8, ok);
+        cp16_or_zero(qs + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row + hk * DK + ch * 8, ok);
+      }
+    }
+    cp_commit();
+  };
+  // bf16 -> fp16 times f, in place (each thread the pieces it copied itself)
+  auto to_half = [&](unsigned char* at, float f) {
+    uint4 v = *reinterpret_cast<uint4*>(at);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack_b(w[i]);
+      w[i] = pack_h(x.x * f, x.y * f);
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+
+  GradPos cur{next_item(blockIdx.x), 0, 0};
+  int stage = 0, kq = 0;
+  if (cur.item < items) fetch(cur, 0, 0);
+  float dq[2][NQ][4], dk[2][NQ][4];
+  float N[2][2][4], Pm[2][2][4];
+  float own[2][2], thru[2][2], frob = 0.f;
+  while (cur.item < items) {
+    const int b = static_cast<int>(cur.item / nc / a.Hk), hk = static_cast<int>(cur.item / nc % a.Hk),
+              t0 = static_cast<int>(cur.item % nc) * kTc, nt = tokens(cur.item), h = hk * per + cur.hh;
+    const int64_t bhc = head_chunk(cur);
+    const float* sc = p.w.sc + bhc * kSc;
+    typename GradSmem<DK>::Stage& s = sm.st[stage];
+    const uint32_t ks = smem_u32(sm.K[kq]), qs = smem_u32(sm.Q[kq]);
+    const bool new_item = cur.hh == 0 && cur.sl == 0, new_head = cur.sl == 0;
+    if (new_item) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dq[mt][n][e] = dk[mt][n][e] = 0.f;
+    }
+    if (new_head) {
+      if (tid < kTc) {
+        sm.eG[tid] = sc[tid];
+        sm.eE[tid] = sc[64 + tid];
+        sm.beta[tid] = sc[128 + tid];
+        sm.G[tid] = sc[192 + tid];
+      }
+      if (warp >= 3) {
+        // exponents of the product of two inverse scales, per 16 value columns
+        const int w = warp - 3;
+        const float* x = w == kRq || w == kRp ? p.do_scale : w == kRk3 ? p.w.e_scale : p.y_scale;
+        const float* y = w == kRq || w == kRk1 ? p.w.s0_scale : w == kRk3 ? p.ds1_scale : p.w.e_scale;
+        int e = -1000;
+        if (lane < n16)
+          e = (__float_as_int(x[bhc * n16 + lane]) >> 23) + (__float_as_int(y[bhc * n16 + lane]) >> 23) - 254;
+        int m = e;
+#pragma unroll
+        for (int k = 8; k; k >>= 1) m = max(m, __shfl_xor_sync(kFull, m, k));
+        if (lane < 16) {
+          const int d = e - m;                          // 2^d as fp16: zero below 2^-24
+          const float f = d < -24 ? 0.f : __int_as_float((127 + d) << 23);
+          sm.ratio[w][lane] = pack_h(f, f);
+        }
+        if (lane == 0) sm.inv[w] = m < -126 ? 0.f : __int_as_float((127 + min(m, 127)) << 23);
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) N[mt][n][e] = Pm[mt][n][e] = 0.f;
+        own[mt][0] = own[mt][1] = thru[mt][0] = thru[mt][1] = 0.f;
+      }
+      frob = 0.f;
+    }
+    cp_wait<0>();
+    // this thread's own pieces: do to fp16, <S0, dS1>, and a new chunk's keys and queries to fp16
+#pragma unroll
+    for (int x = tid; x < kTc * 8; x += 256) {
+      const int t = x >> 3, ch = x & 7, sl16 = cur.sl * 4 + (ch >> 1);
+      if (sl16 < n16) to_half(s.dO + swz<128>(t, ch), inv_scale(p.do_scale[bhc * n16 + sl16]));
+    }
+#pragma unroll
+    for (int x = tid; x < 64 * DK / 8; x += 256) {
+      const int d = x / (DK / 8), ch = x % (DK / 8), sl16 = cur.sl * 4 + (d >> 4);
+      if (sl16 >= n16) continue;
+      const uint4 u = *reinterpret_cast<const uint4*>(s.S0 + swz<PK>(d, ch)), w = *reinterpret_cast<const uint4*>(s.dS + swz<PK>(d, ch));
+      const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+      float f = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 m = unpack_h(uu[i]), n = unpack_h(ww[i]);
+        f = fmaf(m.x, n.x, fmaf(m.y, n.y, f));
+      }
+      frob = fmaf(f * p.w.s0_scale[bhc * n16 + sl16], p.ds1_scale[bhc * n16 + sl16], frob);
+    }
+    if (new_item) {
+      const float kf = inv_scale(sc[kScK]), qf = inv_scale(sc[kScQ]);
+#pragma unroll
+      for (int x = tid; x < kTc * DK / 8; x += 256) {
+        const uint32_t at = swz<PK>(x / (DK / 8), x % (DK / 8));
+        to_half(sm.K[kq] + at, kf);
+        to_half(sm.Q[kq] + at, qf);
+      }
+    }
+    __syncthreads();
+    GradPos nxt = cur;
+    int nkq = kq;
+    if (++nxt.sl == ns) {
+      nxt.sl = 0;
+      if (++nxt.hh == per) {
+        nxt.hh = 0;
+        nxt.item = next_item(cur.item + gridDim.x);
+        nkq = kq ^ 1;
+      }
+    }
+    if (nxt.item < items) fetch(nxt, stage ^ 1, nkq);
+
+    // products over this slice of value columns
+    const uint32_t dO = smem_u32(s.dO), E = smem_u32(s.E), Y = smem_u32(s.Y), S0 = smem_u32(s.S0), dS = smem_u32(s.dS);
+    auto load_a = [&](uint32_t (&f)[4], uint32_t tile, int mt, int kk, uint32_t ratio) {
+      ldsm(f, tile + swz<128>(32 * rg + 16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+      const __half2 m = *reinterpret_cast<const __half2*>(&ratio);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&f[i]), m);
+        f[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    };
+    float t_[2][NQ][4];
+    // t_ = X . Z over the slice: X tokens x value columns, Z value columns x key columns
+    auto through = [&](uint32_t X, uint32_t Z, int which) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t_[mt][n][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t ratio = sm.ratio[which][(cur.sl * 4 + kk) & 15];
+        uint32_t f0[4], f1[4];
+        load_a(f0, X, 0, kk, ratio);
+        load_a(f1, X, 1, kk, ratio);
+#pragma unroll
+        for (int n = 0; n < NQ; n += 2) {
+          uint32_t bb[4];
+          load_b_rows_k<PK>(bb, Z, cq * (DK / 4) + 8 * n, kk, lane);
+          mma_h(t_[0][n], f0, bb[0], bb[1]);
+          mma_h(t_[0][n + 1], f0, bb[2], bb[3]);
+          mma_h(t_[1][n], f1, bb[0], bb[1]);
+          mma_h(t_[1][n + 1], f1, bb[2], bb[3]);
+        }
+      }
+    };
+    // adds t_ times w[row] to acc, and its product with the rows of X16 to dot
+    auto fold = [&](float (&acc)[2][NQ][4], float (&dot)[2][2], const float* w, const float* w2, float f, const unsigned char* X16,
+                    float xi) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int i = 32 * rg + 16 * mt + 8 * half + r;
+          const float g = f * w[i] * (w2 ? w2[i] : 1.f);
+          float d = 0.f;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            const int col = cq * (DK / 4) + 8 * n;
+            const float2 x = unpack_h(*reinterpret_cast<const uint32_t*>(X16 + swz<PK>(i, col >> 3) + 2 * cc));
+            const float u = t_[mt][n][2 * half] * g, v = t_[mt][n][2 * half + 1] * g;
+            acc[mt][n][2 * half] += u;
+            acc[mt][n][2 * half + 1] += v;
+            d = fmaf(u, x.x, fmaf(v, x.y, d));
+          }
+          dot[mt][half] = fmaf(d, xi, dot[mt][half]);
+        }
+    };
+    const float ki = sc[kScK], qi = sc[kScQ];
+    through(dO, S0, kRq);
+    fold(dq, own, sm.eG, nullptr, a.scale * sm.inv[kRq], sm.Q[kq], qi);
+    through(Y, S0, kRk1);
+    fold(dk, own, sm.eG, sm.beta, -sm.inv[kRk1], sm.K[kq], ki);
+    through(E, dS, kRk3);
+    fold(dk, thru, sm.eE, sm.beta, sm.inv[kRk3], sm.K[kq], ki);
+    if (16 * cq < 32 * rg + 32) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t rn = sm.ratio[kRn][(cur.sl * 4 + kk) & 15], rp = sm.ratio[kRp][(cur.sl * 4 + kk) & 15];
+        uint32_t bb[4];
+        load_b_rows_n<128>(bb, E, 16 * cq, kk, lane);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t fy[4], fo[4];
+          load_a(fy, Y, mt, kk, rn);
+          load_a(fo, dO, mt, kk, rp);
+          mma_h(N[mt][0], fy, bb[0], bb[1]);
+          mma_h(N[mt][1], fy, bb[2], bb[3]);
+          mma_h(Pm[mt][0], fo, bb[0], bb[1]);
+          mma_h(Pm[mt][1], fo, bb[2], bb[3]);
+        }
+      }
+    }
+
+    if (cur.sl == ns - 1) {
+      // the head is complete: K K^T and Q K^T of this warp's block, the pair weights, their sums
+      float kk_[2][2][4], qk_[2][2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) kk_[mt][n][e] = qk_[mt][n][e] = 0.f;
+      if (16 * cq < 32 * rg + 32) {
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          uint32_t bb[4];
+          load_b_rows_n<PK>(bb, ks, 16 * cq, k, lane);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t fk[4], fq[4];
+            const uint32_t at = swz<PK>(32 * rg + 16 * mt + (lane & 15), 2 * k + (lane >> 4));
+            ldsm(fk, ks + at);
+            ldsm(fq, qs + at);
+            mma_h(kk_[mt][0], fk, bb[0], bb[1]);
+            mma_h(kk_[mt][1], fk, bb[2], bb[3]);
+            mma_h(qk_[mt][0], fq, bb[0], bb[1]);
+            mma_h(qk_[mt][1], fq, bb[2], bb[3]);
+          }
+        }
+      }
+      float rows[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, cols[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, mp = 0.f, ma = 0.f;
+      const float kk2 = ki * ki, qk2 = qi * ki;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 32 * rg + 16 * mt + 8 * (e >> 1) + r, j = 16 * cq + 8 * n + cc + (e & 1);
+            const float D = j <= i ? expf(sm.G[i] - sm.G[j]) : 0.f, bj = sm.beta[j], bi = sm.beta[i];
+            const float nn = N[mt][n][e] * sm.inv[kRn];
+            const float wp = D * a.scale * bj * Pm[mt][n][e] * sm.inv[kRp];
+            const float wa = j < i ? -D * bi * bj * nn : 0.f;
+            if (i == j && i < nt)
+              static_cast<__nv_bfloat16*>(p.dbeta)[a.row(b, t0 + i) * a.Hv + h] = __float2bfloat16_rn(nn);
+            Pm[mt][n][e] = wp;
+            N[mt][n][e] = wa;
+            mp = fmaxf(mp, fabsf(wp));
+            ma = fmaxf(ma, fabsf(wa));
+            const float x = wp * (qk_[mt][n][e] * qk2) + wa * (kk_[mt][n][e] * kk2);
+            rows[mt][e >> 1] += x;
+            cols[n][e & 1] += x;
+          }
+      mp = warp_max(mp);
+      ma = warp_max(ma);
+#pragma unroll
+      for (int w = 16; w; w >>= 1) frob += __shfl_xor_sync(kFull, frob, w);
+      if (lane == 0) {
+        sm.mx[0][warp] = mp;
+        sm.mx[1][warp] = ma;
+        sm.red[warp] = frob;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int w = 1; w < 4; w <<= 1) {
+            rows[mt][half] += __shfl_xor_sync(kFull, rows[mt][half], w);
+            own[mt][half] += __shfl_xor_sync(kFull, own[mt][half], w);
+            thru[mt][half] += __shfl_xor_sync(kFull, thru[mt][half], w);
+          }
+          if ((lane & 3) == 0) {
+            const int i = 32 * rg + 16 * mt + 8 * half + r;
+            sm.row[cq][i] = rows[mt][half];
+            sm.own[cq][i] = own[mt][half];
+            sm.thru[cq][i] = thru[mt][half];
+          }
+        }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) cols[n][e] += __shfl_xor_sync(kFull, cols[n][e], w);
+          if (lane < 4) sm.col[rg][16 * cq + 8 * n + cc + e] = cols[n][e];
+        }
+      __syncthreads();
+      mp = ma = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        mp = fmaxf(mp, sm.mx[0][w]);
+        ma = fmaxf(ma, sm.mx[1][w]);
+      }
+      const float pf = up_scale(mp), af = up_scale(ma);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int i = 32 * rg + 16 * mt + 8 * half + r;
+            const uint32_t at = swz<128>(i, 2 * cq + n) + 2 * cc;
+            *reinterpret_cast<uint32_t*>(sm.mP + at) = pack_h(Pm[mt][n][2 * half] * pf, Pm[mt][n][2 * half + 1] * pf);
+            *reinterpret_cast<uint32_t*>(sm.mA + at) = pack_h(N[mt][n][2 * half] * af, N[mt][n][2 * half + 1] * af);
+          }
+      if (warp == 0) {
+        // dg: suffix sums of dG, two tokens a lane
+        float x[2], w = 0.f, f = lane < 8 ? sm.red[lane] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * lane + e;
+          const float th = sm.thru[0][i] + sm.thru[1][i] + sm.thru[2][i] + sm.thru[3][i];
+          x[e] = (sm.row[0][i] + sm.row[1][i] + sm.row[2][i] + sm.row[3][i]) - (sm.col[0][i] + sm.col[1][i]) +
+                 (sm.own[0][i] + sm.own[1][i] + sm.own[2][i] + sm.own[3][i]) - th;
+          w += th;
+        }
+        float pair = x[0] + x[1];
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const float dn = __shfl_down_sync(kFull, pair, k);
+          if (lane + k < 32) pair += dn;
+          w += __shfl_xor_sync(kFull, w, k);
+          f += __shfl_xor_sync(kFull, f, k);
+        }
+        const float last = w + sc[kScEnd] * f;
+        const float out[2] = {pair + last, pair - x[0] + last};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (2 * lane + e < nt)
+            static_cast<__nv_bfloat16*>(p.dg)[a.row(b, t0 + 2 * lane + e) * a.Hv + h] = __float2bfloat16_rn(out[e]);
+      }
+      if (warp == 1) {
+        for (int t = max(nt, 0) + lane; t < min(kTc, a.T - t0); t += 32) {
+          static_cast<__nv_bfloat16*>(p.dg)[a.row(b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+          static_cast<__nv_bfloat16*>(p.dbeta)[a.row(b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+        }
+      }
+      __syncthreads();
+      const uint32_t mPs = smem_u32(sm.mP), mAs = smem_u32(sm.mA);
+      // acc += f * (M B) with M taken as stored (rows i) or transposed (rows j)
+      auto pairs = [&](uint32_t M, uint32_t B, bool trans) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t fa[2][4];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const int m0 = 32 * rg + 16 * mt;
+            if (trans)
+              ldsm_t(fa[mt], M + swz<128>(16 * kk + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1)));
+            else
+              ldsm(fa[mt], M + swz<128>(m0 + (lane & 15), 2 * kk + (lane >> 4)));
+          }
+#pragma unroll
+          for (int n = 0; n < NQ; n += 2) {
+            uint32_t bb[4];
+            load_b_rows_k<PK>(bb, B, cq * (DK / 4) + 8 * n, kk, lane);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const int blk = 2 * rg + mt;                       // 16-blocks on the far side of the diagonal are zero
+              if (trans ? kk < blk : kk > blk) continue;
+              mma_h(t_[mt][n], fa[mt], bb[0], bb[1]);
+              mma_h(t_[mt][n + 1], fa[mt], bb[2], bb[3]);
+            }
+          }
+        }
+      };
+      auto clear = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t_[mt][n][e] = 0.f;
+      };
+      auto add = [&](float (&acc)[2][NQ][4], float f) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][n][e] = fmaf(t_[mt][n][e], f, acc[mt][n][e]);
+      };
+      clear();
+      pairs(mPs, ks, false);
+      add(dq, inv_scale(pf) * ki);
+      clear();
+      pairs(mPs, qs, true);
+      add(dk, inv_scale(pf) * qi);
+      clear();
+      pairs(mAs, ks, false);
+      pairs(mAs, ks, true);
+      add(dk, inv_scale(af) * ki);
+      if (cur.hh == per - 1) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int t = t0 + 32 * rg + 16 * mt + 8 * half + r;
+            if (t >= a.T) continue;
+            const int64_t at = a.row(b, t) * qk_row + hk * DK + cq * (DK / 4) + cc;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.dq) + at + 8 * n) =
+                  pack_b(dq[mt][n][2 * half], dq[mt][n][2 * half + 1]);
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.dk) + at + 8 * n) =
+                  pack_b(dk[mt][n][2 * half], dk[mt][n][2 * half + 1]);
+            }
+          }
+      }
+    }
+    __syncthreads();              // everyone is done with this stage (and with the head's shared sums)
+    cur = nxt;
+    stage ^= 1;
+    kq = nkq;
+  }
+}
+
+template <int DK>
+int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
+  const int bsm = 2 * sizeof(BwdStage<DK>), gsm = sizeof(GradSmem<DK>);
+  if (set_smem(delta_scan_bwd_kernel<DK>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)) return RNN_CUDA_ERROR;
+  const int w = scan_warps(t.a, t.num_sms);
+  const int64_t grid = static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w));
+  delta_scan_bwd_kernel<DK><<<static_cast<unsigned>(grid), 32 * w, bsm, s>>>(t);
+  int rc = check_launch();
+  if (rc) return rc;
+  ++*launches;
+  const int64_t items = static_cast<int64_t>(t.a.B) * t.a.Hk * ((t.a.T + kTc - 1) / kTc);
+  delta_grad_kernel<DK><<<static_cast<unsigned>(items < t.num_sms ? items : t.num_sms), 256, gsm, s>>>(t);
+  rc = check_launch();
+  if (!rc) ++*launches;
+  return rc;
+}
+
+}  // namespace
+
+bool delta_tc_supported(int Dk, int Dv, int is_bf16) { return is_bf16 && (Dk == 64 || Dk == 128) && Dv % 32 == 0; }
+
+int launch_delta_tc_forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
+  *launches = 0;
+  if (t.a.Dk == 64) return t.train ? forward<64, true>(t, s, launches) : forward<64, false>(t, s, launches);
+  return t.train ? forward<128, true>(t, s, launches) : forward<128, false>(t, s, launches);
+}
+
+int launch_delta_tc_backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
+  *launches = 0;
+  return t.a.Dk == 64 ? backward<64>(t, s, launches) : backward<128>(t, s, launches);
+}
+
+}  // namespace rnn

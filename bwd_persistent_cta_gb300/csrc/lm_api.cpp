@@ -7,6 +7,7 @@
 #include <new>
 
 #include "delta.h"
+#include "delta_tc.h"
 #include "device_guard.h"
 #include "norm.h"
 #include "rnn.h"
@@ -17,15 +18,18 @@ struct rnn_delta_s {
   rnn_delta_desc_t desc;
   float scale;
   int device, num_sms, bf16;
+  int tc;                      // the tensor-core kernels run whole sequences
   size_t es;
   int* d_len;
   int has_len;
   uint64_t launches;
-  // reserve (bytes): states before each chunk, e
-  size_t r_s0, r_e, reserve_bytes;
-  // backward workspace (bytes): state gradients after each chunk, y
-  size_t w_ds1, w_y, bwd_workspace_bytes;
-  size_t workspace_bytes;
+  // byte offsets.  Forward workspace (tensor cores): the tiles of prep; a
+  // training forward keeps all of them but th in the reserve
+  size_t w_k16, w_q16, w_th, w_p, w_sc, workspace_bytes;
+  // reserve: states before each chunk and e (with their scales), and those tiles
+  size_t r_s0, r_e, r_s0s, r_es, r_k16, r_q16, r_tb, r_p, r_sc, reserve_bytes;
+  // backward workspace: state gradients after each chunk and y, with scales
+  size_t b_ds1, b_y, b_ds1s, b_ys, b_dos, bwd_workspace_bytes;
 };
 
 struct rnn_norm_s {
@@ -79,18 +83,57 @@ rnn_status_t pick_device(int* dev, int* sms) {
   return major == 10 && minor == 3 ? RNN_OK : RNN_NOT_SUPPORTED;
 }
 
+// From this many tokens on the chunk kernels beat the recurrence.
+constexpr int kTcMinTokens = 16;
+
+struct Bump {
+  size_t off = 0;
+  size_t take(size_t bytes) {
+    const size_t o = off;
+    off = al(off + bytes);
+    return o;
+  }
+};
+
 void delta_layout(rnn_delta_s* h) {
   const rnn_delta_desc_t& d = h->desc;
   const size_t bh = static_cast<size_t>(d.batch) * d.heads_v;
-  const size_t nc = (d.seq_len + kSimtChunk - 1) / kSimtChunk;
-  const size_t states = bh * nc * d.dim_v * d.dim_k * 4, vectors = bh * d.seq_len * d.dim_v * 4;
-  h->workspace_bytes = 0;
-  h->r_s0 = 0;
-  h->r_e = al(states);
-  h->reserve_bytes = h->r_e + al(vectors);
-  h->w_ds1 = 0;
-  h->w_y = al(states);
-  h->bwd_workspace_bytes = h->w_y + al(vectors);
+  Bump w, r, b;
+  if (!h->tc) {
+    const size_t nc = (d.seq_len + kSimtChunk - 1) / kSimtChunk;
+    const size_t states = bh * nc * d.dim_v * d.dim_k * 4, vectors = bh * d.seq_len * d.dim_v * 4;
+    h->r_s0 = r.take(states);
+    h->r_e = r.take(vectors);
+    h->b_ds1 = b.take(states);
+    h->b_y = b.take(vectors);
+  } else {
+    const size_t nc = (d.seq_len + kTc - 1) / kTc;
+    const size_t vc = bh * nc, kc = static_cast<size_t>(d.batch) * d.heads_k * nc;
+    const size_t keys = kc * kTc * d.dim_k * 2, tile = vc * kTile * 2, sc = vc * kSc * 4;
+    const size_t states = vc * d.dim_v * d.dim_k * 2, vectors = vc * kTc * d.dim_v * 2, scales = vc * (d.dim_v / 16) * 4;
+    h->w_th = w.take(2 * tile);
+    h->w_k16 = w.take(keys);
+    h->w_q16 = w.take(keys);
+    h->w_p = w.take(tile);
+    h->w_sc = w.take(sc);
+    h->r_k16 = r.take(keys);
+    h->r_q16 = r.take(keys);
+    h->r_tb = r.take(2 * tile);
+    h->r_p = r.take(2 * tile);
+    h->r_sc = r.take(sc);
+    h->r_s0 = r.take(states);
+    h->r_s0s = r.take(scales);
+    h->r_e = r.take(vectors);
+    h->r_es = r.take(scales);
+    h->b_ds1 = b.take(states);
+    h->b_ds1s = b.take(scales);
+    h->b_y = b.take(vectors);
+    h->b_ys = b.take(scales);
+    h->b_dos = b.take(scales);
+  }
+  h->workspace_bytes = w.off;
+  h->reserve_bytes = r.off;
+  h->bwd_workspace_bytes = b.off;
 }
 
 // A row stride in elements: 0 = dense; otherwise at least a row, and a
@@ -123,6 +166,28 @@ rnn_status_t delta_args(const rnn_delta_s* h, const rnn_delta_in_t* in, DeltaArg
 template <typename T>
 T* at(const void* base, size_t off) {
   return reinterpret_cast<T*>(const_cast<char*>(static_cast<const char*>(base)) + off);
+}
+
+DeltaTcBufs tc_bufs(const rnn_delta_s* h, void* workspace, const void* reserve) {
+  DeltaTcBufs w{};
+  w.th = workspace ? at<void>(workspace, h->w_th) : nullptr;
+  if (!reserve) {
+    w.k16 = at<void>(workspace, h->w_k16);
+    w.q16 = at<void>(workspace, h->w_q16);
+    w.p = at<void>(workspace, h->w_p);
+    w.sc = at<float>(workspace, h->w_sc);
+    return w;
+  }
+  w.k16 = at<void>(reserve, h->r_k16);
+  w.q16 = at<void>(reserve, h->r_q16);
+  w.tb = at<void>(reserve, h->r_tb);
+  w.p = at<void>(reserve, h->r_p);
+  w.sc = at<float>(reserve, h->r_sc);
+  w.s0 = at<void>(reserve, h->r_s0);
+  w.s0_scale = at<float>(reserve, h->r_s0s);
+  w.e = at<void>(reserve, h->r_e);
+  w.e_scale = at<float>(reserve, h->r_es);
+  return w;
 }
 
 rnn_status_t norm_args(const rnn_norm_s* h, const rnn_norm_in_t* in, NormArgs* a) {
@@ -172,6 +237,7 @@ rnn_status_t rnn_delta_create(const rnn_delta_desc_t* desc, rnn_delta_t* out) {
   h->d_len = nullptr;
   h->has_len = 0;
   h->launches = 0;
+  h->tc = desc->seq_len >= kTcMinTokens && delta_tc_supported(desc->dim_k, desc->dim_v, h->bf16);
   delta_layout(h);
   *out = h;
   return RNN_OK;
@@ -222,6 +288,20 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
   if ((h->workspace_bytes && !workspace) || !aligned16(workspace) || !aligned16(reserve)) return RNN_BAD_WORKSPACE;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
+  if (h->tc) {
+    DeltaTcArgs t{};
+    t.a = r.a;
+    t.w = tc_bufs(h, workspace, reserve);
+    t.s_in = s0;
+    t.s_out = sT;
+    t.o = o;
+    t.train = reserve != nullptr;
+    t.num_sms = h->num_sms;
+    int n = 0;
+    const int e = launch_delta_tc_forward(t, static_cast<cudaStream_t>(stream), &n);
+    h->launches += n;
+    return static_cast<rnn_status_t>(e);
+  }
   r.s_in = s0;
   r.s_out = sT;
   r.num_slots = -1;
@@ -248,13 +328,32 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   DeviceGuard guard(h->device);
   if (!guard.ok) return RNN_CUDA_ERROR;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (h->tc) {
+    DeltaTcBwdArgs t{};
+    t.a = a;
+    t.w = tc_bufs(h, nullptr, reserve);
+    t.dout = do_;
+    t.dsT = dsT;
+    t.ds0 = ds0;
+    t.ds1 = at<void>(workspace, h->b_ds1);
+    t.ds1_scale = at<float>(workspace, h->b_ds1s);
+    t.y = at<void>(workspace, h->b_y);
+    t.y_scale = at<float>(workspace, h->b_ys);
+    t.do_scale = at<float>(workspace, h->b_dos);
+    t.dq = dq; t.dk = dk; t.dv = dv; t.dg = dg; t.dbeta = dbeta;
+    t.num_sms = h->num_sms;
+    int n = 0;
+    const int e = launch_delta_tc_backward(t, s, &n);
+    h->launches += n;
+    return static_cast<rnn_status_t>(e);
+  }
   DeltaRecurBwdArgs b{};
   b.a = a;
   b.dout = do_;
   b.dsT = dsT;
   b.ds0 = ds0;
-  b.ckpt = at<float>(workspace, h->w_ds1);
-  b.y = at<float>(workspace, h->w_y);
+  b.ckpt = at<float>(workspace, h->b_ds1);
+  b.y = at<float>(workspace, h->b_y);
   int e = launch_delta_recur_bwd(b, h->bf16, s);
   if (e) return static_cast<rnn_status_t>(e);
   ++h->launches;
