@@ -827,7 +827,6 @@ template <int DK, bool TRAIN>
 int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   const int nc = (t.a.T + kTc - 1) / kTc;
   const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>);
-  if (set_smem(delta_prep_kernel<DK, TRAIN>, psm) || set_smem(delta_scan_fwd_kernel<DK, TRAIN>, fsm)) return RNN_CUDA_ERROR;
   delta_prep_kernel<DK, TRAIN><<<static_cast<unsigned>(static_cast<int64_t>(nc) * t.a.Hv * t.a.B), 128, psm, s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
@@ -1529,7 +1528,6 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
 template <int DK>
 int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   const int bsm = 2 * sizeof(BwdStage<DK>), gsm = sizeof(GradSmem<DK>);
-  if (set_smem(delta_scan_bwd_kernel<DK>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)) return RNN_CUDA_ERROR;
   const int w = scan_warps(t.a, t.num_sms);
   const int64_t grid = static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w));
   delta_scan_bwd_kernel<DK><<<static_cast<unsigned>(grid), 32 * w, bsm, s>>>(t);
@@ -1543,7 +1541,20 @@ int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   return rc;
 }
 
+template <int DK>
+int init() {
+  const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>), bsm = 2 * sizeof(BwdStage<DK>),
+            gsm = sizeof(GradSmem<DK>);
+  return set_smem(delta_prep_kernel<DK, false>, psm) || set_smem(delta_prep_kernel<DK, true>, psm) ||
+                 set_smem(delta_scan_fwd_kernel<DK, false>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true>, fsm) ||
+                 set_smem(delta_scan_bwd_kernel<DK>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)
+             ? RNN_CUDA_ERROR
+             : 0;
+}
+
 }  // namespace
+
+int delta_tc_init(int Dk) { return Dk == 64 ? init<64>() : init<128>(); }
 
 bool delta_tc_supported(int Dk, int Dv, int is_bf16) { return is_bf16 && (Dk == 64 || Dk == 128) && Dv % 32 == 0; }
 

@@ -44,6 +44,8 @@ struct DeltaTcArgs {
   void* o;
   int train, num_sms;
 };
+// Once per device and handle: the kernels' shared memory limits.
+int delta_tc_init(int Dk);
 bool delta_tc_supported(int Dk, int Dv, int is_bf16);
 int launch_delta_tc_forward(const DeltaTcArgs& t, cudaStream_t s, int* launches);
 

@@ -238,6 +238,10 @@ rnn_status_t rnn_delta_create(const rnn_delta_desc_t* desc, rnn_delta_t* out) {
   h->has_len = 0;
   h->launches = 0;
   h->tc = desc->seq_len >= kTcMinTokens && delta_tc_supported(desc->dim_k, desc->dim_v, h->bf16);
+  if (h->tc && delta_tc_init(desc->dim_k)) {
+    delete h;
+    return RNN_CUDA_ERROR;
+  }
   delta_layout(h);
   *out = h;
   return RNN_OK;

@@ -5,9 +5,10 @@ the definitions."""
 from __future__ import annotations
 
 import ctypes
+import math
 
-from . import (RNN_BF16, RNN_F32, RNN_GATE_NONE, RNN_GATE_SIGMOID, RNN_GATE_SILU, RNN_OK, RnnError, _p, _P, _stream,
-               lib, rnn_delta_desc_t, rnn_delta_in_t, rnn_norm_desc_t, rnn_norm_in_t)
+from . import (RNN_BF16, RNN_F32, RNN_GATE_NONE, RNN_GATE_SIGMOID, RNN_GATE_SILU, RNN_OK, RnnError, _p, _P, lib,
+                rnn_delta_desc_t, rnn_delta_in_t, rnn_norm_desc_t, rnn_norm_in_t)
 
 
 # --- the C entry points, same names -----------------------------------------
@@ -133,46 +134,71 @@ class _Op:
         self._like(t, name, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.data_ptr() % 16:
+        if t.data_ptr() & 15:
             raise ValueError(f"{name} must start on a 16-byte boundary")
 
     def _like(self, t, name: str, shape, dtype=None):
+        # one pass over what is usually right; what is wrong is found again below
+        try:
+            if t.dtype is (dtype or self.tdtype) and t.shape == shape and t.device == self.device:
+                return
+        except AttributeError:
+            pass
         if not isinstance(t, self.torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}; the handle is on {self.device}")
-        if t.dtype != (self.tdtype if dtype is None else dtype):
-            raise ValueError(f"{name} has dtype {t.dtype}; expected {self.tdtype if dtype is None else dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+        if t.dtype != (dtype or self.tdtype):
+            raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype or self.tdtype}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+
+    def _on(self, stream) -> int:
+        """The cudaStream_t of a call: ``stream``, else the device's current stream (its handle alone: making the
+        Stream object costs as much as the launch)."""
+        if stream is not None:
+            return stream.cuda_stream
+        return self.torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def _rows(self, t, name: str, shape, lead: int, align: bool) -> int:
         """Row stride (elements) of ``t``: its first ``lead`` dimensions run over rows of one stride, the others are
         dense."""
         self._like(t, name, shape)
+        dense = math.prod(shape[lead:])
         if t.is_contiguous():
-            row = 1
-            for n in shape[lead:]:
-                row *= n
+            row = dense
         else:
-            st, dense = t.stride(), 1
-            for n, s in zip(reversed(shape[lead:]), reversed(st[lead:])):
-                if n > 1 and s != dense:
-                    raise ValueError(f"{name}: the elements of a row must be contiguous")
-                dense *= n
-            row, want = dense, None
-            for n, s in zip(reversed(shape[:lead]), reversed(st[:lead])):
-                if n > 1:
-                    if want is None:
-                        row = s
-                    elif s != want:
-                        raise ValueError(f"{name}: consecutive rows must have one stride")
-                    want = n * s
-            if row < dense:
-                raise ValueError(f"{name}: rows must not overlap")
-        if align and (t.data_ptr() % 16 or row * t.element_size() % 16):
+            st = t.stride()
+            row = st[lead - 1]
+            inner = st[-1] == 1 and (len(shape) == lead + 1 or st[lead] == shape[-1])
+            if not (inner and row >= dense and (lead == 1 or st[0] == shape[1] * row)):
+                row = self._slow_rows(st, name, shape, lead, dense)
+        if align and (t.data_ptr() & 15 or (row * t.element_size()) & 15):
             raise ValueError(f"{name}: rows must start on 16-byte boundaries")
         return row
+
+    @staticmethod
+    def _slow_rows(st, name, shape, lead, dense):
+        """_rows where dimensions of one element carry any stride, or where something is wrong."""
+        size = 1
+        for n, s in zip(reversed(shape[lead:]), reversed(st[lead:])):
+            if n > 1 and s != size:
+                raise ValueError(f"{name}: the elements of a row must be contiguous")
+            size *= n
+        row, want = dense, None
+        for n, s in zip(reversed(shape[:lead]), reversed(st[:lead])):
+            if n > 1:
+                if want is None:
+                    row = s
+                elif s != want:
+                    raise ValueError(f"{name}: consecutive rows must have one stride")
+                want = n * s
+        if row < dense:
+            raise ValueError(f"{name}: rows must not overlap")
+        return row
+
+    def _dense_like(self, t):
+        """A new dense tensor of ``t``'s shape and dtype."""
+        return self.torch.empty_like(t, memory_format=self.torch.contiguous_format)
 
     def _check(self, rc, what):
         if rc != RNN_OK:
@@ -220,10 +246,16 @@ class DeltaRule(_Op):
                 self._rows(beta, "beta", self._g, 2, False))
         return rnn_delta_in_t(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), *rows)
 
-    def _new(self, t, name, shape, dtype=None):
+    def _out(self, t, name, shape, like):
         if t is None:
-            return self.torch.empty(shape, dtype=dtype or self.tdtype, device=self.device)
-        self._want(t, name, shape, dtype)
+            return self._dense_like(like)
+        self._want(t, name, shape)
+        return t
+
+    def _state(self, t, name):
+        if t is None:
+            return self.torch.empty(self._s, dtype=self.torch.float32, device=self.device)
+        self._want(t, name, self._s, self.torch.float32)
         return t
 
     def forward(self, q, k, v, g, beta, s0=None, train=True, o=None, sT=None, stream=None):
@@ -231,10 +263,10 @@ class DeltaRule(_Op):
         f32 = self.torch.float32
         x = self._inputs(q, k, v, g, beta)
         self._want(s0, "s0", self._s, f32)
-        o, sT = self._new(o, "o", self._v), self._new(sT, "sT", self._s, f32)
+        o, sT = self._out(o, "o", self._v, v), self._state(sT, "sT")
         ws = self._scratch("workspace", self.workspace_bytes)
         rs = self._scratch("reserve", self.reserve_bytes) if train else None
-        rc = rnn_delta_forward(self.handle, x, _p(s0), _p(o), _p(sT), _p(ws), _p(rs), _stream(stream, self.device))
+        rc = rnn_delta_forward(self.handle, x, _p(s0), _p(o), _p(sT), _p(ws), _p(rs), self._on(stream))
         self._check(rc, "rnn_delta_forward")
         return o, sT
 
@@ -249,13 +281,11 @@ class DeltaRule(_Op):
             raise ValueError("do is required")
         self._want(do, "do", self._v)
         self._want(dsT, "dsT", self._s, f32)
-        dq, dk = self._new(None, "dq", self._qk), self._new(None, "dk", self._qk)
-        dv = self._new(None, "dv", self._v)
-        dg, dbeta = self._new(None, "dg", self._g), self._new(None, "dbeta", self._g)
-        ds0 = self._new(ds0, "ds0", self._s, f32)
+        dq, dk, dv, dg, dbeta = (self._dense_like(t) for t in (q, k, v, g, beta))
+        ds0 = self._state(ds0, "ds0")
         ws = self._scratch("backward_workspace", self.backward_workspace_bytes)
         rc = rnn_delta_backward(self.handle, x, _p(do), _p(dsT), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta), _p(ds0),
-                                _p(ws), _p(self.reserve), _stream(stream, self.device))
+                                _p(ws), _p(self.reserve), self._on(stream))
         self._check(rc, "rnn_delta_backward")
         return dq, dk, dv, dg, dbeta, ds0
 
@@ -275,8 +305,8 @@ class DeltaRule(_Op):
             self._like(slots, "slots", (d.batch,), torch.int32)
             if not slots.is_contiguous():
                 raise ValueError("slots must be contiguous")
-        o = self._new(o, "o", self._v)
-        rc = rnn_delta_step(self.handle, x, state.data_ptr(), n, _p(slots), o.data_ptr(), _stream(stream, self.device))
+        o = self._out(o, "o", self._v, v)
+        rc = rnn_delta_step(self.handle, x, state.data_ptr(), n, _p(slots), o.data_ptr(), self._on(stream))
         self._check(rc, "rnn_delta_step")
         return o
 
@@ -329,19 +359,18 @@ class BlockNorm(_Op):
         if y is None:
             raise ValueError("y is required")
         a = self._inputs(y, z, x, w_in, scale, w_out)
-        empty = self.torch.empty
         if x_out is None:
-            x_out = empty(self._full, dtype=self.tdtype, device=self.device)
+            x_out = self._dense_like(y)
         else:
             self._want(x_out, "x_out", self._full)
         if not self.desc.norm_out:
             if n_out is not None:
                 raise ValueError("n_out is not used by this handle")
         elif n_out is None:
-            n_out = empty(self._full, dtype=self.tdtype, device=self.device)
+            n_out = self._dense_like(y)
         else:
             self._want(n_out, "n_out", self._full)
-        rc = rnn_norm_forward(self.handle, a, x_out.data_ptr(), _p(n_out), _stream(stream, self.device))
+        rc = rnn_norm_forward(self.handle, a, x_out.data_ptr(), _p(n_out), self._on(stream))
         self._check(rc, "rnn_norm_forward")
         return x_out, n_out
 
@@ -359,16 +388,14 @@ class BlockNorm(_Op):
         self._want(dx_out, "dx_out", self._full)
         self._want(dn_out, "dn_out", self._full)
 
-        def new(on, shape, dtype):
-            return torch.empty(shape, dtype=dtype, device=self.device) if on else None
-
-        out = {"dy": new(True, self._full, self.tdtype), "dz": new(d.gate, self._full, self.tdtype),
-               "dx": new(d.residual, self._full, self.tdtype)}
+        out = {"dy": self._dense_like(y), "dz": self._dense_like(y) if d.gate else None,
+               "dx": self._dense_like(y) if d.residual else None}
+        weights = False
         for name, t in (("dw_in", w_in), ("dscale", scale), ("dw_out", w_out)):
-            out[name] = new(t is not None, self._w, torch.float32)
-        weights = any(out[n] is not None for n in ("dw_in", "dscale", "dw_out"))
+            out[name] = None if t is None else torch.empty_like(t, dtype=torch.float32)
+            weights = weights or t is not None
         ws = self._scratch("workspace", self.workspace_bytes) if weights else None
         rc = rnn_norm_backward(self.handle, a, _p(dx_out), _p(dn_out), *(_p(t) for t in out.values()), _p(ws),
-                               _stream(stream, self.device))
+                               self._on(stream))
         self._check(rc, "rnn_norm_backward")
         return out
