@@ -41,6 +41,14 @@ __device__ __forceinline__ float up_scale(float m) {
 }
 __device__ __forceinline__ float inv_scale(float f) { return __int_as_float((254 << 23) - __float_as_int(f)); }
 
+// A power of two, at most one, that keeps products with a factor of at most m
+// below twice their other factor.
+__device__ __forceinline__ float below_inverse(float m) {
+  int f = 254 - ((__float_as_int(m) >> 23) & 255);
+  f = f < 27 ? 27 : f > 127 ? 127 : f;
+  return __int_as_float(f << 23);
+}
+
 __device__ __forceinline__ uint32_t pack_h(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -53,19 +61,50 @@ __device__ __forceinline__ float2 unpack_h(uint32_t v) { return __half22float2(*
 __device__ __forceinline__ float2 unpack_b(uint32_t v) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
-// x = hi + lo to 22 bits.
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_h(x, y);
-  const float2 h = unpack_h(hi);
-  lo = pack_h(x - h.x, y - h.y);
-}
 
+// Largest of non-negative values over the warp: their bits order as integers.
 __device__ __forceinline__ float warp_max(float m) {
-#pragma unroll
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, w));
-  return m;
+  return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 lo2(const float (&x)[4]) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ float2 hi2(const float (&x)[4]) { return make_float2(x[2], x[3]); }
+__device__ __forceinline__ void set4(float (&x)[4], float2 lo, float2 hi) {
+  x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+}
+
+// x = hi + lo to 22 bits.
+__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_h(x.x, x.y);
+  const float2 l = fma2(unpack_h(hi), both(-1.f), x);
+  lo = pack_h(l.x, l.y);
+}
+__device__ __forceinline__ uint32_t pack_h(float2 x) { return pack_h(x.x, x.y); }
+
+// D = A B: the first product of a sum.
+__device__ __forceinline__ void mma_h0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -123,6 +162,35 @@ __device__ __forceinline__ void load_b_rows_n(uint32_t (&b)[4], uint32_t tile, i
 template <int PITCH>
 __device__ __forceinline__ void load_b_rows_k(uint32_t (&b)[4], uint32_t tile, int n0, int kk, int lane) {
   ldsm_t(b, tile + swz<PITCH>(16 * kk + (lane & 7) + (((lane >> 3) & 1) << 3), (n0 >> 3) + (lane >> 4)));
+}
+
+// The same operands of the scans, which read many of a chunk's tiles: the
+// lane's part of the address is computed once, and the rest are constants.  A
+// piece index 2 kk + b exchanged by x = lane & 7 is ((2 kk & 7) + b ^ x) with the
+// higher bits untouched, so four offsets serve a row of any length.
+struct LaneOffsets {
+  uint32_t n[2][4], k[2][4];     // by row pitch (128 bytes, Dk * 2 bytes)
+  __device__ __forceinline__ void init(int dk_pitch, int lane) {
+    const int x = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pn = ((2 * i + ((lane >> 3) & 1)) ^ x) << 4, pk = ((2 * i + (lane >> 4)) ^ x) << 4;
+      const int rn = x + ((lane >> 4) << 3), rk = x + (((lane >> 3) & 1) << 3);
+      n[0][i] = rn * 128 + pn;
+      n[1][i] = rn * dk_pitch + pn;
+      k[0][i] = rk * 128 + pk;
+      k[1][i] = rk * dk_pitch + pk;
+    }
+  }
+};
+// rows n: tiles n0, n0 + 8 and k-step kk; rows k likewise (n0 a multiple of 16)
+template <int PITCH>
+__device__ __forceinline__ void scan_b_n(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
+  ldsm(b, tile + o.n[PITCH != 128][kk & 3] + n0 * PITCH + (kk >> 2) * 128);
+}
+template <int PITCH>
+__device__ __forceinline__ void scan_b_k(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
+  ldsm_t(b, tile + o.k[PITCH != 128][(n0 >> 4) & 3] + 16 * kk * PITCH + (n0 >> 6) * 128);
 }
 
 // Value column (of a warp's 16) behind row r of its fragments; row r + 8 is two
@@ -257,16 +325,30 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
     const TwoF end = {__shfl_sync(kFull, pair.h, 31), __shfl_sync(kFull, pair.l, 31)};
     g2[0] = two_add(before, g2[0]);
     g2[1] = pair;
+    float bu = 0.f, by = 0.f, bo = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       sm.Gh[t] = g2[i].h;
       sm.Gl[t] = g2[i].l;
-      sc[t] = expf(g2[i].h + g2[i].l);
-      sc[64 + t] = expf((end.h - g2[i].h) + (end.l - g2[i].l));
+      const float eg = expf(g2[i].h + g2[i].l), ee = expf((end.h - g2[i].h) + (end.l - g2[i].l));
+      const float be = fabsf(sm.beta[t]);
+      sc[t] = eg;
+      sc[64 + t] = ee;
       sc[192 + t] = g2[i].h;
+      bu = fmaxf(bu, be * fmaxf(1.f, ee));
+      by = fmaxf(by, be * eg);
+      bo = fmaxf(bo, fabsf(a.scale) * eg);
     }
-    if (lane == 0) sc[kScEnd] = expf(end.h + end.l);
+    bu = warp_max(bu);
+    by = warp_max(by);
+    bo = warp_max(bo);
+    if (lane == 0) {
+      sc[kScEnd] = expf(end.h + end.l);
+      sc[kScBu] = below_inverse(bu);
+      sc[kScBy] = below_inverse(by);
+      sc[kScBo] = below_inverse(bo);
+    }
   }
   cp_wait<0>();
   __syncthreads();
@@ -364,7 +446,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
     for (int e = 0; e < 4; e += 2) {
       const int i = 16 * warp + r + (e >> 1) * 8;
       uint32_t hi, lo;
-      split(qk[n][e] * pf, qk[n][e + 1] * pf, hi, lo);
+      split(make_float2(qk[n][e] * pf, qk[n][e + 1] * pf), hi, lo);
       *reinterpret_cast<uint32_t*>(po + swz<128>(i, n) + 2 * cc) = hi;
       if (TRAIN) *reinterpret_cast<uint32_t*>(po + kTile * 2 + swz<128>(i, n) + 2 * cc) = lo;
     }
@@ -431,7 +513,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int j = 8 * ch + 2 * k;
-      split(j < i ? X[i * kXP + j] * xf : 0.f, j + 1 < i ? X[i * kXP + j + 1] * xf : 0.f, hi[k], lo[k]);
+      split(make_float2(j < i ? X[i * kXP + j] * xf : 0.f, j + 1 < i ? X[i * kXP + j + 1] * xf : 0.f), hi[k], lo[k]);
     }
     *reinterpret_cast<uint4*>(xo + swz<128>(i, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(xo + kTile * 2 + swz<128>(i, ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -500,7 +582,7 @@ __device__ __forceinline__ void state_store_half(const State<DK>& S, float f, __
     for (int m = 0; m < DK / 32; ++m) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_h(S.v[4 * m + i][2 * half] * f, S.v[4 * m + i][2 * half + 1] * f);
+      for (int i = 0; i < 4; ++i) w[i] = pack_h(mul2(half ? hi2(S.v[4 * m + i]) : lo2(S.v[4 * m + i]), both(f)));
       *reinterpret_cast<uint4*>(p + 32 * m) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -508,12 +590,6 @@ __device__ __forceinline__ void state_store_half(const State<DK>& S, float f, __
 
 // X[8][4] is [16 value columns][64 tokens] as accumulator tiles over tokens.
 using Frag = float[8][4];
-__device__ __forceinline__ void zero(Frag& x) {
-#pragma unroll
-  for (int n = 0; n < 8; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
-}
 __device__ __forceinline__ float frag_max(const Frag& x) {
   float m = 0.f;
 #pragma unroll
@@ -522,18 +598,34 @@ __device__ __forceinline__ float frag_max(const Frag& x) {
     for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(x[n][i]));
   return warp_max(m);
 }
+// x[.][t] *= w[t] for per-token factors in shared memory, times f.
+__device__ __forceinline__ float2 pair_of(const float* p, int n, int lane) {
+  return *reinterpret_cast<const float2*>(p + 8 * n + 2 * (lane & 3));
+}
+__device__ __forceinline__ void frag_scale(Frag& x, const float* w, int lane) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float2 f = pair_of(w, n, lane);
+    set4(x[n], mul2(lo2(x[n]), f), mul2(hi2(x[n]), f));
+  }
+}
+// x += f y
+__device__ __forceinline__ void frag_add(Frag& x, const Frag& y, float f) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) set4(x[n], fma2(lo2(y[n]), both(f), lo2(x[n])), fma2(hi2(y[n]), both(f), hi2(x[n])));
+}
 // A operand (k = tokens 16 kk ..) of a fragment scaled by f, high and low part.
 __device__ __forceinline__ void frag_a(const Frag& x, int kk, float f, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split(x[2 * kk][0] * f, x[2 * kk][1] * f, hi[0], lo[0]);
-  split(x[2 * kk][2] * f, x[2 * kk][3] * f, hi[1], lo[1]);
-  split(x[2 * kk + 1][0] * f, x[2 * kk + 1][1] * f, hi[2], lo[2]);
-  split(x[2 * kk + 1][2] * f, x[2 * kk + 1][3] * f, hi[3], lo[3]);
+  split(mul2(lo2(x[2 * kk]), both(f)), hi[0], lo[0]);
+  split(mul2(hi2(x[2 * kk]), both(f)), hi[1], lo[1]);
+  split(mul2(lo2(x[2 * kk + 1]), both(f)), hi[2], lo[2]);
+  split(mul2(hi2(x[2 * kk + 1]), both(f)), hi[3], lo[3]);
 }
 __device__ __forceinline__ void frag_a_hi(const Frag& x, int kk, float f, uint32_t (&hi)[4]) {
-  hi[0] = pack_h(x[2 * kk][0] * f, x[2 * kk][1] * f);
-  hi[1] = pack_h(x[2 * kk][2] * f, x[2 * kk][3] * f);
-  hi[2] = pack_h(x[2 * kk + 1][0] * f, x[2 * kk + 1][1] * f);
-  hi[3] = pack_h(x[2 * kk + 1][2] * f, x[2 * kk + 1][3] * f);
+  hi[0] = pack_h(mul2(lo2(x[2 * kk]), both(f)));
+  hi[1] = pack_h(mul2(hi2(x[2 * kk]), both(f)));
+  hi[2] = pack_h(mul2(lo2(x[2 * kk + 1]), both(f)));
+  hi[3] = pack_h(mul2(hi2(x[2 * kk + 1]), both(f)));
 }
 
 // A warp's [64 tokens][16 columns] slice of a bf16 row-major sequence: thread
@@ -542,63 +634,75 @@ __device__ __forceinline__ void frag_a_hi(const Frag& x, int kk, float f, uint32
 struct Slice {
   uint2 v[8];
 };
-__device__ __forceinline__ void slice_load(Slice& s, const __nv_bfloat16* base, const DeltaArgs& a, int64_t stride, int b,
-                                           int t0, int len, int lane) {
+// ``p`` points at the thread's columns of the chunk's token lane / 4, ``step``
+// elements lead 8 tokens further; ``left`` tokens of the chunk are valid.
+__device__ __forceinline__ void slice_load(Slice& s, const __nv_bfloat16* p, int64_t step, int left, int lane) {
+  const int t = lane >> 2;
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const int t = t0 + 8 * n + (lane >> 2);
-    s.v[n] = t < len ? *reinterpret_cast<const uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) : make_uint2(0u, 0u);
-  }
+  for (int n = 0; n < 8; ++n)
+    s.v[n] = t + 8 * n < left ? *reinterpret_cast<const uint2*>(p + n * step) : make_uint2(0u, 0u);
 }
 // Fragment tile n (fp32) of a slice.
-__device__ __forceinline__ void slice_frag(const Slice& s, int n, float (&x)[4]) {
-  const float2 lo = unpack_b(transpose8(s.v[n].x)), hi = unpack_b(transpose8(s.v[n].y));
-  x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+__device__ __forceinline__ void slice_frag(const Slice& s, int n, float2& lo, float2& hi) {
+  lo = unpack_b(transpose8(s.v[n].x));
+  hi = unpack_b(transpose8(s.v[n].y));
 }
 
-__device__ __forceinline__ float2 pair_of(const float* p, int n, int lane) {
-  return *reinterpret_cast<const float2*>(p + 8 * n + 2 * (lane & 3));
+// Copies BYTES of a tile, as it is, by the CTA's NT threads.
+template <int BYTES, int NT>
+__device__ __forceinline__ void tile_copy(uint32_t dst, const void* src) {
+  const char* s = static_cast<const char*>(src) + threadIdx.x * 16;
+  dst += threadIdx.x * 16;
+#pragma unroll
+  for (int i = 0; i < BYTES / (NT * 16); ++i) cp16(dst + i * NT * 16, s + i * NT * 16);
+  if (BYTES % (NT * 16) && threadIdx.x * 16 < BYTES % (NT * 16))
+    cp16(dst + BYTES / (NT * 16) * NT * 16, s + BYTES / (NT * 16) * NT * 16);
 }
 
-// Copies nbytes (a multiple of 16) of a tile, as it is, by all of the CTA's threads.
-__device__ __forceinline__ void tile_copy(uint32_t dst, const void* src, int nbytes, int nthreads) {
-  const char* s = static_cast<const char*>(src);
-  for (int i = threadIdx.x * 16; i < nbytes; i += nthreads * 16) cp16(dst + i, s + i);
-}
-
-// Z (+)= S X^T over the key columns, X = K16 or Q16: [16][64 tokens].
+// Z = S X^T over the key columns, X = K16 ([16][64 tokens]), from both parts of
+// S; with BOTH also Z2 = S X2^T, X2 = Q16, from the high part.
 template <int DK, bool BOTH>
 __device__ __forceinline__ void state_times(const State<DK>& S, float f, uint32_t x, uint32_t x2, Frag& z, Frag& z2,
-                                            int lane) {
+                                            const LaneOffsets& lo_) {
 #pragma unroll
   for (int kk = 0; kk < DK / 16; ++kk) {
     uint32_t hi[4], lo[4];
-    split(S.v[2 * kk][0] * f, S.v[2 * kk][1] * f, hi[0], lo[0]);
-    split(S.v[2 * kk][2] * f, S.v[2 * kk][3] * f, hi[1], lo[1]);
-    split(S.v[2 * kk + 1][0] * f, S.v[2 * kk + 1][1] * f, hi[2], lo[2]);
-    split(S.v[2 * kk + 1][2] * f, S.v[2 * kk + 1][3] * f, hi[3], lo[3]);
+    split(mul2(lo2(S.v[2 * kk]), both(f)), hi[0], lo[0]);
+    split(mul2(hi2(S.v[2 * kk]), both(f)), hi[1], lo[1]);
+    split(mul2(lo2(S.v[2 * kk + 1]), both(f)), hi[2], lo[2]);
+    split(mul2(hi2(S.v[2 * kk + 1]), both(f)), hi[3], lo[3]);
 #pragma unroll
     for (int n = 0; n < 8; n += 2) {
       uint32_t bb[4];
-      load_b_rows_n<DK * 2>(bb, x, 8 * n, kk, lane);
-      mma_h(z[n], hi, bb[0], bb[1]);
-      mma_h(z[n + 1], hi, bb[2], bb[3]);
+      scan_b_n<DK * 2>(bb, x, lo_, 8 * n, kk);
+      if (kk == 0) {
+        mma_h0(z[n], hi, bb[0], bb[1]);
+        mma_h0(z[n + 1], hi, bb[2], bb[3]);
+      } else {
+        mma_h(z[n], hi, bb[0], bb[1]);
+        mma_h(z[n + 1], hi, bb[2], bb[3]);
+      }
       mma_h(z[n], lo, bb[0], bb[1]);
       mma_h(z[n + 1], lo, bb[2], bb[3]);
       if (BOTH) {
-        load_b_rows_n<DK * 2>(bb, x2, 8 * n, kk, lane);
-        mma_h(z2[n], hi, bb[0], bb[1]);
-        mma_h(z2[n + 1], hi, bb[2], bb[3]);
+        scan_b_n<DK * 2>(bb, x2, lo_, 8 * n, kk);
+        if (kk == 0) {
+          mma_h0(z2[n], hi, bb[0], bb[1]);
+          mma_h0(z2[n + 1], hi, bb[2], bb[3]);
+        } else {
+          mma_h(z2[n], hi, bb[0], bb[1]);
+          mma_h(z2[n + 1], hi, bb[2], bb[3]);
+        }
       }
     }
   }
 }
 
-// S = decay S + sum_t X[.][t] B[t][.], with X scaled by f, B one or two tiles of
-// 64 tokens, each with its own X; ``g`` undoes the scales.
+// S = decay S + sum_t X[.][t] B[t][.], with X scaled by f and B a tile of 64
+// tokens; ``g`` undoes the scales.
 template <int DK>
 __device__ __forceinline__ void state_update(State<DK>& S, float decay, const Frag& x, float f, uint32_t tile, float g,
-                                             int lane) {
+                                             const LaneOffsets& lo_) {
   uint32_t hi[4][4], lo[4][4];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) frag_a(x, kk, f, hi[kk], lo[kk]);
@@ -606,43 +710,43 @@ __device__ __forceinline__ void state_update(State<DK>& S, float decay, const Fr
   for (int j = 0; j < DK / 8; j += 4) {
     float acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
         uint32_t bb[4];
-        load_b_rows_k<DK * 2>(bb, tile, 8 * (j + i), kk, lane);
-        mma_h(acc[i], hi[kk], bb[0], bb[1]);
-        mma_h(acc[i + 1], hi[kk], bb[2], bb[3]);
+        scan_b_k<DK * 2>(bb, tile, lo_, 8 * (j + i), kk);
+        if (kk == 0) {
+          mma_h0(acc[i], hi[kk], bb[0], bb[1]);
+          mma_h0(acc[i + 1], hi[kk], bb[2], bb[3]);
+        } else {
+          mma_h(acc[i], hi[kk], bb[0], bb[1]);
+          mma_h(acc[i + 1], hi[kk], bb[2], bb[3]);
+        }
         mma_h(acc[i], lo[kk], bb[0], bb[1]);
         mma_h(acc[i + 1], lo[kk], bb[2], bb[3]);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S.v[j + i][e] = fmaf(acc[i][e], g, decay * S.v[j + i][e]);
+      set4(S.v[j + i], fma2(lo2(acc[i]), both(g), mul2(lo2(S.v[j + i]), both(decay))),
+           fma2(hi2(acc[i]), both(g), mul2(hi2(S.v[j + i]), both(decay))));
   }
 }
 
 // Writes a fragment as fp16 rows [64][Dv] scaled by f (a warp's 16 columns).
 __device__ __forceinline__ void frag_store_half(const Frag& x, float f, __half* base, int pitch, int lane) {
+  __half* p = base + (lane >> 2) * pitch + 4 * (lane & 3);
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const uint32_t lo = transpose8(pack_h(x[n][0] * f, x[n][1] * f)), hi = transpose8(pack_h(x[n][2] * f, x[n][3] * f));
-    *reinterpret_cast<uint2*>(base + static_cast<int64_t>(8 * n + (lane >> 2)) * pitch + 4 * (lane & 3)) = make_uint2(lo, hi);
-  }
+  for (int n = 0; n < 8; ++n)
+    *reinterpret_cast<uint2*>(p + 8 * n * pitch) =
+        make_uint2(transpose8(pack_h(mul2(lo2(x[n]), both(f)))), transpose8(pack_h(mul2(hi2(x[n]), both(f)))));
 }
-// Writes a fragment to a dense bf16 sequence.
-__device__ __forceinline__ void frag_store_seq(const Frag& x, __nv_bfloat16* base, const DeltaArgs& a, int64_t stride,
-                                               int b, int t0, int lane) {
+// Writes a fragment to a dense bf16 sequence, addressed as in slice_load.
+__device__ __forceinline__ void frag_store_seq(const Frag& x, __nv_bfloat16* p, int64_t step, int left, int lane) {
+  const int t = lane >> 2;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     const uint32_t lo = transpose8(pack_b(x[n][0], x[n][1])), hi = transpose8(pack_b(x[n][2], x[n][3]));
-    const int t = t0 + 8 * n + (lane >> 2);
-    if (t < a.T) *reinterpret_cast<uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) = make_uint2(lo, hi);
+    if (t + 8 * n < left) *reinterpret_cast<uint2*>(p + n * step) = make_uint2(lo, hi);
   }
 }
 // Zero rows t0 .. T-1 of a warp's columns.
@@ -660,34 +764,42 @@ struct FwdStage {
   float sc[kSc];
 };
 
-// blockDim.x / 32 warps of one value head, 16 value columns each.
-template <int DK, bool TRAIN>
-__global__ void __launch_bounds__(256) delta_scan_fwd_kernel(const DeltaTcArgs p) {
+// W warps of one value head, 16 value columns each.
+template <int DK, bool TRAIN, int W>
+__global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArgs p) {
+  constexpr int NT = 32 * W;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   FwdStage<DK>* st = reinterpret_cast<FwdStage<DK>*>(smem_raw);
   const DeltaArgs& a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthr = blockDim.x;
-  const int groups = a.Dv / (nthr / 2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = a.Dv / (16 * W);
   const int64_t bid = blockIdx.x;
   const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
             b = static_cast<int>(bid / groups / a.Hv);
-  const int slice = grp * (nthr >> 5) + warp, dv0 = slice * 16;
+  const int slice = grp * W + warp, dv0 = slice * 16;
   const int hk = h / (a.Hv / a.Hk);
   const int len = a.len ? a.len[b] : a.T;
   const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
   const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + static_cast<int64_t>(h) * a.Dv + dv0;
   const int64_t s_off = (bh * a.Dv + dv0) * DK;
+  // token strides, and this thread's place in the first chunk
+  const int64_t ts_ = a.bfirst ? 1 : a.B, t_first = a.row(b, lane >> 2);
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0 + 4 * (lane & 3);
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t v_step = 8 * ts_ * a.v_row, o_step = 8 * ts_ * o_row;
+  v += t_first * a.v_row;
+  __nv_bfloat16* ow = o + t_first * o_row + 4 * (lane & 3);
+  LaneOffsets off;
+  off.init(DK * 2, lane);
 
   auto fetch = [&](int c) {
     FwdStage<DK>& s = st[c & 1];
-    tile_copy(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
-    tile_copy(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
-    tile_copy(smem_u32(s.T), static_cast<const char*>(p.w.th) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
-    tile_copy(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * (TRAIN ? 4 : 2), kTile * 2, nthr);
-    tile_copy(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc, kSc * 4, nthr);
+    tile_copy<kTc * DK * 2, NT>(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2);
+    tile_copy<kTc * DK * 2, NT>(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2);
+    tile_copy<kTile * 4, NT>(smem_u32(s.T), static_cast<const char*>(p.w.th) + (bh * nc + c) * kTile * 4);
+    tile_copy<kTile * 2, NT>(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * (TRAIN ? 4 : 2));
+    tile_copy<kSc * 4, NT>(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc);
     cp_commit();
   };
 
@@ -703,7 +815,7 @@ __global__ void __launch_bounds__(256) delta_scan_fwd_kernel(const DeltaTcArgs p
   Slice vs;
   if (ncb > 0) {
     fetch(0);
-    slice_load(vs, v, a, a.v_row, b, 0, len, lane);
+    slice_load(vs, v, v_step, len, lane);
   }
   for (int c = 0; c < ncb; ++c) {
     cp_wait<0>();
@@ -717,91 +829,77 @@ __global__ void __launch_bounds__(256) delta_scan_fwd_kernel(const DeltaTcArgs p
       state_store_half<DK>(S, sf, static_cast<__half*>(p.w.s0) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
       if (lane == 0) p.w.s0_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
     }
-    Frag z, oq;
-    zero(z);
-    zero(oq);
-    state_times<DK, true>(S, sf, ks, qs, z, oq, lane);
+    Frag z, oq, acc;
+    state_times<DK, true>(S, sf, ks, qs, z, oq, off);
     // r = v - e^G S0 k
-    const float zk = si * s.sc[kScK], zq = si * s.sc[kScQ] * a.scale;
+    const float zk = -si * s.sc[kScK], zq = si * s.sc[kScQ] * a.scale;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const float2 eg = pair_of(s.sc, n, lane);
-      float x[4];
-      slice_frag(vs, n, x);
-      z[n][0] = fmaf(-eg.x * zk, z[n][0], x[0]);
-      z[n][1] = fmaf(-eg.y * zk, z[n][1], x[1]);
-      z[n][2] = fmaf(-eg.x * zk, z[n][2], x[2]);
-      z[n][3] = fmaf(-eg.y * zk, z[n][3], x[3]);
-      oq[n][0] *= eg.x * zq; oq[n][1] *= eg.y * zq; oq[n][2] *= eg.x * zq; oq[n][3] *= eg.y * zq;
+      const float2 eg = pair_of(s.sc, n, lane), ek = mul2(eg, both(zk)), eq = mul2(eg, both(zq));
+      float2 lo, hi;
+      slice_frag(vs, n, lo, hi);
+      set4(z[n], fma2(lo2(z[n]), ek, lo), fma2(hi2(z[n]), ek, hi));
+      set4(oq[n], mul2(lo2(oq[n]), eq), mul2(hi2(oq[n]), eq));
     }
-    if (c + 1 < ncb) slice_load(vs, v, a, a.v_row, b, (c + 1) * kTc, len, lane);
+    v += 8 * v_step;
+    if (c + 1 < ncb) slice_load(vs, v, v_step, len - (c + 1) * kTc, lane);
     // e = r + (T - I) r: the identity stays in fp32
-    Frag acc;
-    zero(acc);
     const float rf = up_scale(frag_max(z));
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t hi[4], lo[4];
       frag_a(z, kk, rf, hi, lo);
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        if (n < 2 * kk) continue;          // j <= i
+      for (int n = 2 * kk; n < 8; n += 2) {     // j <= i
         uint32_t bh_[4], bl_[4];
-        load_b_rows_n<128>(bh_, ts, 8 * n, kk, lane);
-        load_b_rows_n<128>(bl_, ts + kTile * 2, 8 * n, kk, lane);
-        mma_h(acc[n], hi, bh_[0], bh_[1]);
-        mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        scan_b_n<128>(bh_, ts, off, 8 * n, kk);
+        scan_b_n<128>(bl_, ts + kTile * 2, off, 8 * n, kk);
+        if (kk == 0) {
+          mma_h0(acc[n], hi, bh_[0], bh_[1]);
+          mma_h0(acc[n + 1], hi, bh_[2], bh_[3]);
+        } else {
+          mma_h(acc[n], hi, bh_[0], bh_[1]);
+          mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        }
         mma_h(acc[n], lo, bh_[0], bh_[1]);
         mma_h(acc[n + 1], lo, bh_[2], bh_[3]);
         mma_h(acc[n], hi, bl_[0], bl_[1]);
         mma_h(acc[n + 1], hi, bl_[2], bl_[3]);
       }
     }
-    const float ti = inv_scale(rf) * s.sc[kScTH];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[n][i], ti, z[n][i]);
+    frag_add(z, acc, inv_scale(rf) * s.sc[kScTH]);
+    const float ef = up_scale(frag_max(z));
     if (TRAIN) {
-      const float ef = up_scale(frag_max(z));
       frag_store_half(z, ef, static_cast<__half*>(p.w.e) + (bh * nc + c) * kTc * a.Dv + dv0, a.Dv, lane);
       if (lane == 0) p.w.e_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(ef);
     }
-    // u = beta e; o = scale e^G S0 q + P u
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 be = pair_of(s.sc + 128, n, lane);
-      z[n][0] *= be.x; z[n][1] *= be.y; z[n][2] *= be.x; z[n][3] *= be.y;
-    }
-    const float uf = up_scale(frag_max(z));
-    zero(acc);
+    // u = beta e; o = scale e^G S0 q + P u.  The scale of e times a bound on the
+    // weights (kScBu) serves u and e^{G_C - G} u.
+    const float uf = ef * s.sc[kScBu], ui = inv_scale(uf);
+    frag_scale(z, s.sc + 128, lane);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t hi[4];
       frag_a_hi(z, kk, uf, hi);
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        if (n < 2 * kk) continue;
+      for (int n = 2 * kk; n < 8; n += 2) {
         uint32_t bb[4];
-        load_b_rows_n<128>(bb, ps, 8 * n, kk, lane);
-        mma_h(acc[n], hi, bb[0], bb[1]);
-        mma_h(acc[n + 1], hi, bb[2], bb[3]);
+        scan_b_n<128>(bb, ps, off, 8 * n, kk);
+        if (kk == 0) {
+          mma_h0(acc[n], hi, bb[0], bb[1]);
+          mma_h0(acc[n + 1], hi, bb[2], bb[3]);
+        } else {
+          mma_h(acc[n], hi, bb[0], bb[1]);
+          mma_h(acc[n + 1], hi, bb[2], bb[3]);
+        }
       }
     }
-    const float pi = inv_scale(uf) * s.sc[kScP];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) oq[n][i] = fmaf(acc[n][i], pi, oq[n][i]);
-    frag_store_seq(oq, o, a, o_row, b, c * kTc, lane);
+    frag_add(oq, acc, ui * s.sc[kScP]);
+    frag_store_seq(oq, ow, o_step, a.T - c * kTc, lane);
+    ow += 8 * o_step;
     // S1 = e^{G_C} S0 + (e^{G_C - G} u) k
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 ee = pair_of(s.sc + 64, n, lane);
-      z[n][0] *= ee.x; z[n][1] *= ee.y; z[n][2] *= ee.x; z[n][3] *= ee.y;
-    }
-    const float wf = up_scale(frag_max(z));
-    state_update<DK>(S, s.sc[kScEnd], z, wf, ks, inv_scale(wf) * s.sc[kScK], lane);
+    frag_scale(z, s.sc + 64, lane);
+    state_update<DK>(S, s.sc[kScEnd], z, uf, ks, ui * s.sc[kScK], off);
   }
   zero_rows(o, a, o_row, b, ncb * kTc, lane);
   if (p.s_out) state_store<DK>(S, p.s_out + s_off, lane);
@@ -832,8 +930,10 @@ int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   if (rc) return rc;
   ++*launches;
   const int w = scan_warps(t.a, t.num_sms);
-  const int64_t grid = static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w));
-  delta_scan_fwd_kernel<DK, TRAIN><<<static_cast<unsigned>(grid), 32 * w, fsm, s>>>(t);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
+  if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, fsm, s>>>(t);
+  else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, fsm, s>>>(t);
+  else delta_scan_fwd_kernel<DK, TRAIN, 2><<<grid, 64, fsm, s>>>(t);
   rc = check_launch();
   if (!rc) ++*launches;
   return rc;
@@ -851,33 +951,39 @@ struct BwdStage {
   float sc[kSc];
 };
 
-template <int DK>
-__global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArgs p) {
+template <int DK, int W>
+__global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwdArgs p) {
+  constexpr int NT = 32 * W;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   BwdStage<DK>* st = reinterpret_cast<BwdStage<DK>*>(smem_raw);
   const DeltaArgs& a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nthr = blockDim.x;
-  const int groups = a.Dv / (nthr / 2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = a.Dv / (16 * W);
   const int64_t bid = blockIdx.x;
   const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
             b = static_cast<int>(bid / groups / a.Hv);
-  const int slice = grp * (nthr >> 5) + warp, dv0 = slice * 16;
+  const int slice = grp * W + warp, dv0 = slice * 16;
   const int hk = h / (a.Hv / a.Hk);
   const int len = a.len ? a.len[b] : a.T;
   const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
   const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
-  const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(p.dout) + static_cast<int64_t>(h) * a.Dv + dv0;
-  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0;
   const int64_t s_off = (bh * a.Dv + dv0) * DK;
+  const int64_t ts_ = a.bfirst ? 1 : a.B, o_step = 8 * ts_ * o_row;
+  const int64_t last = a.row(b, (lane >> 2) + (ncb > 0 ? ncb - 1 : 0) * kTc) * o_row + static_cast<int64_t>(h) * a.Dv + dv0 +
+                       4 * (lane & 3);
+  const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(p.dout) + last;
+  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + last;
+  LaneOffsets off;
+  off.init(DK * 2, lane);
 
   auto fetch = [&](int c) {
     BwdStage<DK>& s = st[c & 1];
-    tile_copy(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
-    tile_copy(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2, kTc * DK * 2, nthr);
-    tile_copy(smem_u32(s.T), static_cast<const char*>(p.w.tb) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
-    tile_copy(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * 4, kTile * 4, nthr);
-    tile_copy(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc, kSc * 4, nthr);
+    tile_copy<kTc * DK * 2, NT>(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2);
+    tile_copy<kTc * DK * 2, NT>(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2);
+    tile_copy<kTile * 4, NT>(smem_u32(s.T), static_cast<const char*>(p.w.tb) + (bh * nc + c) * kTile * 4);
+    tile_copy<kTile * 4, NT>(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * 4);
+    tile_copy<kSc * 4, NT>(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc);
     cp_commit();
   };
 
@@ -893,7 +999,7 @@ __global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArg
   Slice ds;
   if (ncb > 0) {
     fetch(ncb - 1);
-    slice_load(ds, dout, a, o_row, b, (ncb - 1) * kTc, len, lane);
+    slice_load(ds, dout, o_step, len - (ncb - 1) * kTc, lane);
   }
   for (int c = ncb - 1; c >= 0; --c) {
     cp_wait<0>();
@@ -906,10 +1012,8 @@ __global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArg
     state_store_half<DK>(S, sf, static_cast<__half*>(p.ds1) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
     if (lane == 0) p.ds1_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
     Frag z, acc;
-    zero(z);
-    state_times<DK, false>(S, sf, ks, ks, z, z, lane);
+    state_times<DK, false>(S, sf, ks, ks, z, z, off);
     // P^T do: do is exact in fp16 once scaled
-    zero(acc);
     float dm = 0.f;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -920,19 +1024,23 @@ __global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArg
     if (lane == 0) p.do_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(df);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      float x[4], y[4];
-      slice_frag(ds, 2 * kk, x);
-      slice_frag(ds, 2 * kk + 1, y);
-      const uint32_t ad[4] = {pack_h(x[0] * df, x[1] * df), pack_h(x[2] * df, x[3] * df), pack_h(y[0] * df, y[1] * df),
-                              pack_h(y[2] * df, y[3] * df)};
+      float2 x0, x1, y0, y1;
+      slice_frag(ds, 2 * kk, x0, x1);
+      slice_frag(ds, 2 * kk + 1, y0, y1);
+      const uint32_t ad[4] = {pack_h(mul2(x0, both(df))), pack_h(mul2(x1, both(df))), pack_h(mul2(y0, both(df))),
+                              pack_h(mul2(y1, both(df)))};
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        if (n > 2 * kk) continue;          // j <= i
+      for (int n = 0; n <= 2 * kk; n += 2) {      // j <= i
         uint32_t bh_[4], bl_[4];
-        load_b_rows_k<128>(bh_, ps, 8 * n, kk, lane);
-        load_b_rows_k<128>(bl_, ps + kTile * 2, 8 * n, kk, lane);
-        mma_h(acc[n], ad, bh_[0], bh_[1]);
-        mma_h(acc[n + 1], ad, bh_[2], bh_[3]);
+        scan_b_k<128>(bh_, ps, off, 8 * n, kk);
+        scan_b_k<128>(bl_, ps + kTile * 2, off, 8 * n, kk);
+        if (n == 2 * kk) {
+          mma_h0(acc[n], ad, bh_[0], bh_[1]);
+          mma_h0(acc[n + 1], ad, bh_[2], bh_[3]);
+        } else {
+          mma_h(acc[n], ad, bh_[0], bh_[1]);
+          mma_h(acc[n + 1], ad, bh_[2], bh_[3]);
+        }
         mma_h(acc[n], ad, bl_[0], bl_[1]);
         mma_h(acc[n + 1], ad, bl_[2], bl_[3]);
       }
@@ -940,62 +1048,57 @@ __global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaTcBwdArg
     const float zk = si * s.sc[kScK], pi = inv_scale(df) * s.sc[kScP];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const float2 ee = pair_of(s.sc + 64, n, lane);
-      z[n][0] = fmaf(acc[n][0], pi, ee.x * zk * z[n][0]);
-      z[n][1] = fmaf(acc[n][1], pi, ee.y * zk * z[n][1]);
-      z[n][2] = fmaf(acc[n][2], pi, ee.x * zk * z[n][2]);
-      z[n][3] = fmaf(acc[n][3], pi, ee.y * zk * z[n][3]);
+      const float2 ee = mul2(pair_of(s.sc + 64, n, lane), both(zk));
+      set4(z[n], fma2(lo2(acc[n]), both(pi), mul2(lo2(z[n]), ee)), fma2(hi2(acc[n]), both(pi), mul2(hi2(z[n]), ee)));
     }
     // y = du + (T - I)^T du
-    zero(acc);
     const float uf = up_scale(frag_max(z));
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t hi[4], lo[4];
       frag_a(z, kk, uf, hi, lo);
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        if (n > 2 * kk) continue;
+      for (int n = 0; n <= 2 * kk; n += 2) {
         uint32_t bh_[4], bl_[4];
-        load_b_rows_k<128>(bh_, ts, 8 * n, kk, lane);
-        load_b_rows_k<128>(bl_, ts + kTile * 2, 8 * n, kk, lane);
-        mma_h(acc[n], hi, bh_[0], bh_[1]);
-        mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        scan_b_k<128>(bh_, ts, off, 8 * n, kk);
+        scan_b_k<128>(bl_, ts + kTile * 2, off, 8 * n, kk);
+        if (n == 2 * kk) {
+          mma_h0(acc[n], hi, bh_[0], bh_[1]);
+          mma_h0(acc[n + 1], hi, bh_[2], bh_[3]);
+        } else {
+          mma_h(acc[n], hi, bh_[0], bh_[1]);
+          mma_h(acc[n + 1], hi, bh_[2], bh_[3]);
+        }
         mma_h(acc[n], lo, bh_[0], bh_[1]);
         mma_h(acc[n + 1], lo, bh_[2], bh_[3]);
         mma_h(acc[n], hi, bl_[0], bl_[1]);
         mma_h(acc[n + 1], hi, bl_[2], bl_[3]);
       }
     }
-    const float ti = inv_scale(uf) * s.sc[kScTB];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[n][i] = fmaf(acc[n][i], ti, z[n][i]);
+    frag_add(z, acc, inv_scale(uf) * s.sc[kScTB]);
     const float yf = up_scale(frag_max(z));
     frag_store_half(z, yf, static_cast<__half*>(p.y) + (bh * nc + c) * kTc * a.Dv + dv0, a.Dv, lane);
     if (lane == 0) p.y_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(yf);
+    frag_scale(z, s.sc + 128, lane);
+    frag_store_seq(z, dv, o_step, a.T - c * kTc, lane);
+    dv -= 8 * o_step;
+    // -e^G beta y and scale e^G do; their scales follow from those of y and do
+    // and bounds on the weights (kScBy, kScBo)
+    const float xf = yf * s.sc[kScBy], af = df * s.sc[kScBo];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const float2 be = pair_of(s.sc + 128, n, lane);
-      z[n][0] *= be.x; z[n][1] *= be.y; z[n][2] *= be.x; z[n][3] *= be.y;
+      const float2 eg = pair_of(s.sc, n, lane), es = mul2(eg, both(a.scale)), em = mul2(eg, both(-1.f));
+      float2 lo, hi;
+      slice_frag(ds, n, lo, hi);
+      set4(acc[n], mul2(lo, es), mul2(hi, es));
+      set4(z[n], mul2(lo2(z[n]), em), mul2(hi2(z[n]), em));
     }
-    frag_store_seq(z, dv, a, o_row, b, c * kTc, lane);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 eg = pair_of(s.sc, n, lane);
-      float x[4];
-      slice_frag(ds, n, x);
-      acc[n][0] = a.scale * eg.x * x[0]; acc[n][1] = a.scale * eg.y * x[1];
-      acc[n][2] = a.scale * eg.x * x[2]; acc[n][3] = a.scale * eg.y * x[3];
-      z[n][0] *= -eg.x; z[n][1] *= -eg.y; z[n][2] *= -eg.x; z[n][3] *= -eg.y;
-    }
-    if (c > 0) slice_load(ds, dout, a, o_row, b, (c - 1) * kTc, len, lane);
-    const float af = up_scale(frag_max(acc)), xf = up_scale(frag_max(z));
-    state_update<DK>(S, s.sc[kScEnd], acc, af, qs, inv_scale(af) * s.sc[kScQ], lane);
-    state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], lane);
+    dout -= 8 * o_step;
+    if (c > 0) slice_load(ds, dout, o_step, kTc, lane);
+    state_update<DK>(S, s.sc[kScEnd], acc, af, qs, inv_scale(af) * s.sc[kScQ], off);
+    state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
   }
-  zero_rows(dv, a, o_row, b, ncb * kTc, lane);
+  zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, ncb * kTc, lane);
   if (p.ds0) state_store<DK>(S, p.ds0 + s_off, lane);
 }
 
@@ -1529,8 +1632,10 @@ template <int DK>
 int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   const int bsm = 2 * sizeof(BwdStage<DK>), gsm = sizeof(GradSmem<DK>);
   const int w = scan_warps(t.a, t.num_sms);
-  const int64_t grid = static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w));
-  delta_scan_bwd_kernel<DK><<<static_cast<unsigned>(grid), 32 * w, bsm, s>>>(t);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
+  if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, bsm, s>>>(t);
+  else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, bsm, s>>>(t);
+  else delta_scan_bwd_kernel<DK, 2><<<grid, 64, bsm, s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
@@ -1546,8 +1651,11 @@ int init() {
   const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>), bsm = 2 * sizeof(BwdStage<DK>),
             gsm = sizeof(GradSmem<DK>);
   return set_smem(delta_prep_kernel<DK, false>, psm) || set_smem(delta_prep_kernel<DK, true>, psm) ||
-                 set_smem(delta_scan_fwd_kernel<DK, false>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true>, fsm) ||
-                 set_smem(delta_scan_bwd_kernel<DK>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)
+                 set_smem(delta_scan_fwd_kernel<DK, false, 2>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 2>, fsm) ||
+                 set_smem(delta_scan_fwd_kernel<DK, false, 4>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 4>, fsm) ||
+                 set_smem(delta_scan_fwd_kernel<DK, false, 8>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 8>, fsm) ||
+                 set_smem(delta_scan_bwd_kernel<DK, 2>, bsm) || set_smem(delta_scan_bwd_kernel<DK, 4>, bsm) ||
+                 set_smem(delta_scan_bwd_kernel<DK, 8>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)
              ? RNN_CUDA_ERROR
              : 0;
 }

@@ -27,7 +27,7 @@ namespace rnn {
 constexpr int kTc = 64;              // tokens a chunk
 constexpr int kTile = kTc * kTc;     // elements of a 64 x 64 tile
 // SC: [0,64) e^G, [64,128) e^{G_C - G}, [128,192) beta, [192,256) G, then
-enum { kScK = 256, kScQ, kScTH, kScTB, kScP, kScEnd, kSc = 264 };
+enum { kScK = 256, kScQ, kScTH, kScTB, kScP, kScEnd, kScBu, kScBy, kScBo, kSc = 268 };
 
 struct DeltaTcBufs {
   void *k16, *q16, *th, *tb, *p;
