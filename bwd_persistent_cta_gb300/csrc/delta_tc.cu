@@ -117,6 +117,12 @@ __device__ __forceinline__ void mma_b(float (&d)[4], const uint32_t (&a)[4], uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_t(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
@@ -200,7 +206,7 @@ __device__ __forceinline__ int dv_of_row(int r) { return 4 * (r >> 1) + (r & 1);
 // ---------------------------------------------------------------------------
 // prep: everything of a chunk that does not depend on the state
 // ---------------------------------------------------------------------------
-constexpr int kXP = 66;              // pitch of the fp32 64 x 64 matrices
+constexpr int kXP = 68;              // pitch of the fp32 64 x 64 matrices: fragment rows on different banks
 struct TwoF {
   float h, l;
 };
@@ -213,36 +219,50 @@ __device__ __forceinline__ TwoF two_add(TwoF a, TwoF b) {
   return {h, l - (h - s)};
 }
 
-// C[n][n] (+)= X Y for n = 16 or 32 on fp32 tiles in shared memory, thread t of
-// (n / 4)^2 owning 4 x 4 of C; ``neg`` negates; row k of Y is weighted by yw[k]
-// and row i of the result by cw[i] where given.  X is lower triangular with
-// KX_LOW (k <= i), Y with KY_LOW (k >= j).
-template <int N, bool X_LOW, bool Y_LOW>
-__device__ __forceinline__ void block_mul(float* C, const float* X, const float* Y, const float* yw, const float* cw,
-                                          float sign, int t) {
-  const int i0 = t / (N / 4) * 4, j0 = t % (N / 4) * 4;
-  float acc[4][4];
+// C[16][8 NB] = sign cw (A (yw B)) by one warp, on fp32 matrices in shared memory
+// (pitch kXP): A [16][8 KB], row k of B weighted by yw[k] and row i of the result
+// by cw[i] where given.  Each factor is split into two tf32 parts (11 + 10 bits)
+// and the product of the low parts dropped: 2^-21 of the product, whatever the
+// scale of the factors.
+template <int KB, int NB>
+__device__ __forceinline__ void warp_mul(float* C, const float* A, const float* B, const float* yw, const float* cw,
+                                         float sign, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+  float acc[NB][4];
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[a][b] = 0.f;
-  const int k0 = Y_LOW ? j0 : 0, k1 = X_LOW ? i0 + 4 : N;
-  for (int k = k0; k < k1; ++k) {
-    float x[4], y[4];
-    const float w = yw ? yw[k] : 1.f;
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) x[a] = X_LOW && k > i0 + a ? 0.f : X[(i0 + a) * kXP + k];
+  for (int k = 0; k < KB; ++k) {
+    float x[4];
+    x[0] = A[r * kXP + 8 * k + c];
+    x[1] = A[(r + 8) * kXP + 8 * k + c];
+    x[2] = A[r * kXP + 8 * k + c + 4];
+    x[3] = A[(r + 8) * kXP + 8 * k + c + 4];
+    uint32_t ah[4], al[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) y[b] = Y_LOW && k < j0 + b ? 0.f : w * Y[k * kXP + j0 + b];
+    for (int i = 0; i < 4; ++i) {
+      ah[i] = __float_as_uint(x[i]) & 0xffffe000u;
+      al[i] = __float_as_uint(x[i] - __uint_as_float(ah[i]));
+    }
+    const float w0 = yw ? yw[8 * k + c] : 1.f, w1 = yw ? yw[8 * k + c + 4] : 1.f;
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(x[a], y[b], acc[a][b]);
+    for (int n = 0; n < NB; ++n) {
+      const float y0 = w0 * B[(8 * k + c) * kXP + 8 * n + r], y1 = w1 * B[(8 * k + c + 4) * kXP + 8 * n + r];
+      const uint32_t b0 = __float_as_uint(y0) & 0xffffe000u, b1 = __float_as_uint(y1) & 0xffffe000u;
+      const uint32_t l0 = __float_as_uint(y0 - __uint_as_float(b0)), l1 = __float_as_uint(y1 - __uint_as_float(b1));
+      mma_t(acc[n], al, b0, b1);
+      mma_t(acc[n], ah, l0, l1);
+      mma_t(acc[n], ah, b0, b1);
+    }
   }
+  const float s0 = sign * (cw ? cw[r] : 1.f), s1 = sign * (cw ? cw[r + 8] : 1.f);
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) C[(i0 + a) * kXP + j0 + b] = sign * (cw ? cw[i0 + a] : 1.f) * acc[a][b];
+  for (int n = 0; n < NB; ++n) {
+    *reinterpret_cast<float2*>(C + r * kXP + 8 * n + 2 * c) = make_float2(s0 * acc[n][0], s0 * acc[n][1]);
+    *reinterpret_cast<float2*>(C + (r + 8) * kXP + 8 * n + 2 * c) = make_float2(s1 * acc[n][2], s1 * acc[n][3]);
+  }
 }
 
 template <int DK>
@@ -268,11 +288,11 @@ __device__ __forceinline__ float block_max4(float (*red)[4], int ch, float m) {
 
 // One CTA of 128 threads per chunk and value head.  K K^T and Q K^T run on the
 // tensor cores from the exact bf16 inputs (warp w: rows 16 w .. 16 w + 15, the
-// blocks at or below the diagonal).  The unit triangular inverses are taken in
-// fp32: 16 x 16 diagonal blocks by substitution, a thread a column, then blocks
-// joined twice, [[X, 0], [-Y L X, Y]].  No power of L appears, so keys that are
-// all alike (L with entries near one) cost no accuracy.
-// With training, threads 0..63 work on (I + A beta)^-1 and 64..127 on
+// blocks at or below the diagonal).  The unit triangular inverses start from
+// 16 x 16 diagonal blocks by substitution in fp32, a thread a column; then blocks
+// are joined twice, [[X, 0], [-Y L X, Y]], on the tensor cores.  No power of L
+// appears, so keys that are all alike (L with entries near one) cost no accuracy.
+// With training, warps 0 and 1 work on (I + A beta)^-1 and 2 and 3 on
 // (I + beta A)^-1, else the second half idles in the inverse.
 template <int DK, bool TRAIN>
 __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
@@ -472,25 +492,29 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
     }
   }
   __syncthreads();
-  // pairs of 16: threads 0..31 of each half; the product L X waits in the block above the diagonal
-  const int t64 = tid & 63;
-  {
-    const int o = (t64 >> 4) * 32, t = t64 & 15;
-    float* tmp = X + o * kXP + o + 16;
-    if (mine && t64 < 32)
-      block_mul<16, false, true>(tmp, sm.A + (o + 16) * kXP + o, X + o * kXP + o, which ? nullptr : sm.beta + o,
-                                 which ? sm.beta + o + 16 : nullptr, 1.f, t);
-    __syncthreads();
-    if (mine && t64 < 32)
-      block_mul<16, true, false>(X + (o + 16) * kXP + o, X + (o + 16) * kXP + o + 16, tmp, nullptr, nullptr, -1.f, t);
-    __syncthreads();
+  // Two of 16 make one of 32: a warp a pair.  The product L X waits in the block
+  // above the diagonal, which is zeroed again for the next join.
+  const int t64 = tid & 63, half = warp & 1;
+  if (mine) {
+    const int o = 32 * half;
+    float* above = X + o * kXP + o + 16;
+    warp_mul<2, 2>(above, sm.A + (o + 16) * kXP + o, X + o * kXP + o, which ? nullptr : sm.beta + o,
+                   which ? sm.beta + o + 16 : nullptr, 1.f, lane);
+    __syncwarp();
+    warp_mul<2, 2>(X + (o + 16) * kXP + o, X + (o + 16) * kXP + o + 16, above, nullptr, nullptr, -1.f, lane);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float4*>(above + (lane >> 2) * kXP + 8 * i * kXP + 4 * (lane & 3)) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // the pair of 32; its left factor's upper blocks hold the products above, which the triangular loops skip
-  float* tmp = X + 32;
-  if (mine)
-    block_mul<32, false, true>(tmp, sm.A + 32 * kXP, X, which ? nullptr : sm.beta, which ? sm.beta + 32 : nullptr, 1.f, t64);
   __syncthreads();
-  if (mine) block_mul<32, true, false>(X + 32 * kXP, X + 32 * kXP + 32, tmp, nullptr, nullptr, -1.f, t64);
+  // two of 32 make the whole: a warp 16 rows
+  if (mine)
+    warp_mul<4, 4>(X + 16 * half * kXP + 32, sm.A + (32 + 16 * half) * kXP, X, which ? nullptr : sm.beta,
+                   which ? sm.beta + 32 + 16 * half : nullptr, 1.f, lane);
+  __syncthreads();
+  if (mine)
+    warp_mul<4, 4>(X + (32 + 16 * half) * kXP, X + (32 + 16 * half) * kXP + 32, X + 32, nullptr, nullptr, -1.f, lane);
   __syncthreads();
   // strictly lower part, high and low
   float xm = 0.f;
@@ -1110,12 +1134,13 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
 // walks chunks of a key head with a stride; per value head the value columns
 // pass in slices of 64 through two stages, the next one (and the next chunk's
 // keys and queries) arriving while this one is multiplied.  Warp (rg, cq) of
-// 2 x 4 owns rows 32 rg .. + 31 and a quarter of the columns of every product.
+// 2 x Dk / 16 owns rows 32 rg .. + 31 and 16 of the key columns of every product.
 // The fp16 copies of S0, dS1, e, y and do carry one scale per 16 value columns,
 // i.e. per k-step of the products that sum over value columns; the ratio to the
 // head's largest is applied to the A operand, exactly (a power of two).
 template <int DK>
 struct GradSmem {
+  static constexpr int NW = DK / 8, NT = 32 * NW;                // warps, threads
   struct Stage {
     unsigned char dO[kTc * 128], E[kTc * 128], Y[kTc * 128];     // [64 tokens][64 columns]
     unsigned char S0[64 * DK * 2], dS[64 * DK * 2];              // [64 value columns][Dk]
@@ -1126,127 +1151,146 @@ struct GradSmem {
   // ratios per k-step (fp16 pairs) and inverse scales of the five products of a head
   uint32_t ratio[5][16];
   float inv[5];
-  float own[4][kTc], thru[4][kTc], row[4][kTc], col[2][kTc];
-  float red[8], mx[2][8];
+  float own[NW / 2][kTc], thru[NW / 2][kTc], row[NW / 2][kTc], col[2][kTc];
+  float red[NW], mx[2][NW];
 };
 enum { kRq = 0, kRk1, kRk3, kRn, kRp };
 
+// A place in a CTA's walk: chunk c of (batch b, key head hk), value head hh of
+// the group, slice sl; t0 and nt its first token and valid tokens.
 struct GradPos {
-  int64_t item;        // (b * Hk + hk) * nc + c
-  int hh, sl;
+  int item, b, hk, c, nt, hh, sl;
 };
 
 template <int DK>
-__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p) {
-  constexpr int PK = DK * 2, NQ = DK / 32;     // n-tiles of a warp's quarter
+__global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const DeltaTcBwdArgs p) {
+  using SM = GradSmem<DK>;
+  constexpr int PK = DK * 2, NT = SM::NT, NW = SM::NW, CQ = NW / 2;
+  constexpr int NJ = 8 / CQ;                   // n-tiles of a warp in the pair matrices
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  GradSmem<DK>& sm = *reinterpret_cast<GradSmem<DK>*>(smem_raw);
+  SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const DeltaArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = warp >> 2, cq = warp & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = warp / CQ, cq = warp % CQ;
   const int r = lane >> 2, cc = 2 * (lane & 3);
   const int nc = (a.T + kTc - 1) / kTc, per = a.Hv / a.Hk, ns = (a.Dv + 63) / 64, n16 = a.Dv / 16;
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * nc;
+  const int items = a.B * a.Hk * nc;           // below 2^31: checked when the handle is made
   const int64_t qk_row = static_cast<int64_t>(a.Hk) * DK, v_row = static_cast<int64_t>(a.Hv) * a.Dv;
 
-  auto tokens = [&](int64_t item) {
-    const int b = static_cast<int>(item / nc / a.Hk);
-    return (a.len ? a.len[b] : a.T) - static_cast<int>(item % nc) * kTc;
+  auto at_item = [&](GradPos& g, int item) {
+    g.item = item;
+    const int bk = item / nc;
+    g.c = item - bk * nc;
+    g.b = bk / a.Hk;
+    g.hk = bk - g.b * a.Hk;
+    g.nt = item < items ? (a.len ? a.len[g.b] : a.T) - g.c * kTc : 1;
+    g.hh = g.sl = 0;
   };
-  auto next_item = [&](int64_t item) {
-    while (item < items && tokens(item) <= 0) item += gridDim.x;
-    return item;
+  auto next_item = [&](GradPos& g, int item) {
+    at_item(g, item);
+    while (g.nt <= 0) at_item(g, item += gridDim.x);
   };
   // this CTA's chunks without tokens: zeros
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    if (tokens(item) > 0) continue;
-    const int b = static_cast<int>(item / nc / a.Hk), hk = static_cast<int>(item / nc % a.Hk), t0 = static_cast<int>(item % nc) * kTc;
-    const int span = min(kTc, a.T - t0);
-    for (int x = tid; x < span * DK / 8; x += 256) {
-      const int64_t at = a.row(b, t0 + x / (DK / 8)) * qk_row + hk * DK + x % (DK / 8) * 8;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + at) = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + at) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    for (int x = tid; x < span * per; x += 256) {
-      const int64_t at = a.row(b, t0 + x / per) * a.Hv + hk * per + x % per;
-      static_cast<__nv_bfloat16*>(p.dg)[at] = __float2bfloat16_rn(0.f);
-      static_cast<__nv_bfloat16*>(p.dbeta)[at] = __float2bfloat16_rn(0.f);
+  if (a.len) {
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      GradPos g;
+      at_item(g, item);
+      if (g.nt > 0) continue;
+      const int t0 = g.c * kTc, span = min(kTc, a.T - t0);
+      for (int x = tid; x < span * DK / 8; x += NT) {
+        const int64_t at = a.row(g.b, t0 + x / (DK / 8)) * qk_row + g.hk * DK + x % (DK / 8) * 8;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      for (int x = tid; x < span * per; x += NT) {
+        const int64_t at = a.row(g.b, t0 + x / per) * a.Hv + g.hk * per + x % per;
+        static_cast<__nv_bfloat16*>(p.dg)[at] = __float2bfloat16_rn(0.f);
+        static_cast<__nv_bfloat16*>(p.dbeta)[at] = __float2bfloat16_rn(0.f);
+      }
     }
   }
 
   auto head_chunk = [&](const GradPos& g) {
-    const int64_t bk = g.item / nc;
-    return ((bk / a.Hk * a.Hv + bk % a.Hk * per + g.hh) * nc) + g.item % nc;
+    return (static_cast<int64_t>(g.b) * a.Hv + g.hk * per + g.hh) * nc + g.c;
   };
+  const int64_t tstep = a.bfirst ? 1 : a.B;
   auto fetch = [&](const GradPos& g, int stage, int kq) {
-    const int b = static_cast<int>(g.item / nc / a.Hk), hk = static_cast<int>(g.item / nc % a.Hk),
-              t0 = static_cast<int>(g.item % nc) * kTc, nt = tokens(g.item);
-    const int64_t bhc = head_chunk(g);
-    typename GradSmem<DK>::Stage& s = sm.st[stage];
+    const int64_t bhc = head_chunk(g), row0 = a.row(g.b, g.c * kTc);
+    typename SM::Stage& s = sm.st[stage];
     const uint32_t dO = smem_u32(s.dO), E = smem_u32(s.E), Y = smem_u32(s.Y), S0 = smem_u32(s.S0), dS = smem_u32(s.dS);
     const int v0 = g.sl * 64;
-#pragma unroll
-    for (int x = tid; x < kTc * 8; x += 256) {
-      const int t = x >> 3, ch = x & 7;
+    {
+      // piece ch of tokens t, t + NT / 8, ...
+      const int ch = tid & 7;
       const bool in = v0 + ch * 8 < a.Dv;
-      const int64_t at = (bhc * kTc + t) * a.Dv + (in ? v0 + ch * 8 : 0);
-      const bool ok = in && t < nt;
-      const int64_t row = a.row(b, t0 + (ok ? t : 0)) * v_row + static_cast<int64_t>(hk * per + g.hh) * a.Dv + (in ? v0 + ch * 8 : 0);
-      cp16_or_zero(dO + swz<128>(t, ch), static_cast<const __nv_bfloat16*>(p.dout) + row, ok);
-      cp16_or_zero(E + swz<128>(t, ch), static_cast<const __half*>(p.w.e) + at, in);
-      cp16_or_zero(Y + swz<128>(t, ch), static_cast<const __half*>(p.y) + at, in);
-    }
+      const int col = in ? v0 + ch * 8 : 0;
+      const __nv_bfloat16* dop = static_cast<const __nv_bfloat16*>(p.dout) + row0 * v_row +
+                                 static_cast<int64_t>(g.hk * per + g.hh) * a.Dv + col;
+      const __half *ep = static_cast<const __half*>(p.w.e) + bhc * kTc * a.Dv + col,
+                   *yp = static_cast<const __half*>(p.y) + bhc * kTc * a.Dv + col;
 #pragma unroll
-    for (int x = tid; x < 64 * DK / 8; x += 256) {
-      const int d = x / (DK / 8), ch = x % (DK / 8);
-      const bool in = v0 + d < a.Dv;
-      const int64_t at = (bhc * a.Dv + (in ? v0 + d : 0)) * DK + ch * 8;
-      cp16_or_zero(S0 + swz<PK>(d, ch), static_cast<const __half*>(p.w.s0) + at, in);
-      cp16_or_zero(dS + swz<PK>(d, ch), static_cast<const __half*>(p.ds1) + at, in);
+      for (int i = 0; i < kTc * 8 / NT; ++i) {
+        const int t = (tid >> 3) + i * (NT / 8);
+        const uint32_t at = swz<128>(t, ch);
+        const bool ok = in && t < g.nt;
+        cp16_or_zero(dO + at, dop + (ok ? t * tstep * v_row : 0), ok);
+        cp16_or_zero(E + at, ep + t * a.Dv, in);
+        cp16_or_zero(Y + at, yp + t * a.Dv, in);
+      }
     }
-    if (g.hh == 0 && g.sl == 0) {
-      const uint32_t ks = smem_u32(sm.K[kq]), qs = smem_u32(sm.Q[kq]);
+    {
+      constexpr int PR = DK / 8;
+      const int ch = tid % PR;
+      const int64_t base = (bhc * a.Dv + v0) * DK + ch * 8;
 #pragma unroll
-      for (int x = tid; x < kTc * DK / 8; x += 256) {
-        const int t = x / (DK / 8), ch = x % (DK / 8);
-        const bool ok = t < nt;
-        const int64_t row = a.row(b, t0 + (ok ? t : 0));
-        cp16_or_zero(ks + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.k) + row * a.k_row + hk * DK + ch * 8, ok);
-        cp16_or_zero(qs + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row + hk * DK + ch * 8, ok);
+      for (int i = 0; i < 64 * PR / NT; ++i) {
+        const int d = tid / PR + i * (NT / PR);
+        const bool in = v0 + d < a.Dv;
+        const int64_t at = in ? base + d * DK : 0;
+        cp16_or_zero(S0 + swz<PK>(d, ch), static_cast<const __half*>(p.w.s0) + at, in);
+        cp16_or_zero(dS + swz<PK>(d, ch), static_cast<const __half*>(p.ds1) + at, in);
+      }
+      if (g.hh == 0 && g.sl == 0) {
+        const uint32_t ks = smem_u32(sm.K[kq]), qs = smem_u32(sm.Q[kq]);
+        const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(a.k) + row0 * a.k_row + g.hk * DK + ch * 8,
+                            *qp = static_cast<const __nv_bfloat16*>(a.q) + row0 * a.q_row + g.hk * DK + ch * 8;
+#pragma unroll
+        for (int i = 0; i < kTc * PR / NT; ++i) {
+          const int t = tid / PR + i * (NT / PR);
+          const bool ok = t < g.nt;
+          const int64_t dt = ok ? t * tstep : 0;
+          cp16_or_zero(ks + swz<PK>(t, ch), kp + dt * a.k_row, ok);
+          cp16_or_zero(qs + swz<PK>(t, ch), qp + dt * a.q_row, ok);
+        }
       }
     }
     cp_commit();
   };
   // bf16 -> fp16 times f, in place (each thread the pieces it copied itself)
   auto to_half = [&](unsigned char* at, float f) {
-    uint4 v = *reinterpret_cast<uint4*>(at);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack_b(w[i]);
-      w[i] = pack_h(x.x * f, x.y * f);
-    }
-    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    const uint4 v = *reinterpret_cast<uint4*>(at);
+    *reinterpret_cast<uint4*>(at) = make_uint4(pack_h(mul2(unpack_b(v.x), both(f))), pack_h(mul2(unpack_b(v.y), both(f))),
+                                               pack_h(mul2(unpack_b(v.z), both(f))), pack_h(mul2(unpack_b(v.w), both(f))));
   };
 
-  GradPos cur{next_item(blockIdx.x), 0, 0};
+  GradPos cur;
+  next_item(cur, blockIdx.x);
   int stage = 0, kq = 0;
   if (cur.item < items) fetch(cur, 0, 0);
-  float dq[2][NQ][4], dk[2][NQ][4];
-  float N[2][2][4], Pm[2][2][4];
-  float own[2][2], thru[2][2], frob = 0.f;
+  float dq[2][2][4], dk[2][2][4];
+  float N[2][NJ][4], Pm[2][NJ][4];
+  float2 own[2][2], thru[2][2], frob2 = both(0.f);
   while (cur.item < items) {
-    const int b = static_cast<int>(cur.item / nc / a.Hk), hk = static_cast<int>(cur.item / nc % a.Hk),
-              t0 = static_cast<int>(cur.item % nc) * kTc, nt = tokens(cur.item), h = hk * per + cur.hh;
+    const int t0 = cur.c * kTc, nt = cur.nt, h = cur.hk * per + cur.hh;
     const int64_t bhc = head_chunk(cur);
     const float* sc = p.w.sc + bhc * kSc;
-    typename GradSmem<DK>::Stage& s = sm.st[stage];
+    typename SM::Stage& s = sm.st[stage];
     const uint32_t ks = smem_u32(sm.K[kq]), qs = smem_u32(sm.Q[kq]);
-    const bool new_item = cur.hh == 0 && cur.sl == 0, new_head = cur.sl == 0;
+    const bool new_head = cur.sl == 0, new_item = new_head && cur.hh == 0;
     if (new_item) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) dq[mt][n][e] = dk[mt][n][e] = 0.f;
     }
@@ -1257,7 +1301,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
         sm.beta[tid] = sc[128 + tid];
         sm.G[tid] = sc[192 + tid];
       }
-      if (warp >= 3) {
+      if (warp >= 3 && warp < 8) {
         // exponents of the product of two inverse scales, per 16 value columns
         const int w = warp - 3;
         const float* x = w == kRq || w == kRp ? p.do_scale : w == kRk3 ? p.w.e_scale : p.y_scale;
@@ -1265,9 +1309,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
         int e = -1000;
         if (lane < n16)
           e = (__float_as_int(x[bhc * n16 + lane]) >> 23) + (__float_as_int(y[bhc * n16 + lane]) >> 23) - 254;
-        int m = e;
-#pragma unroll
-        for (int k = 8; k; k >>= 1) m = max(m, __shfl_xor_sync(kFull, m, k));
+        const int m = __reduce_max_sync(kFull, e);
         if (lane < 16) {
           const int d = e - m;                          // 2^d as fp16: zero below 2^-24
           const float f = d < -24 ? 0.f : __int_as_float((127 + d) << 23);
@@ -1278,41 +1320,43 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) N[mt][n][e] = Pm[mt][n][e] = 0.f;
-        own[mt][0] = own[mt][1] = thru[mt][0] = thru[mt][1] = 0.f;
+        own[mt][0] = own[mt][1] = thru[mt][0] = thru[mt][1] = both(0.f);
       }
-      frob = 0.f;
+      frob2 = both(0.f);
     }
     cp_wait<0>();
     // this thread's own pieces: do to fp16, <S0, dS1>, and a new chunk's keys and queries to fp16
+    {
+      const int ch = tid & 7, s16 = cur.sl * 4 + (ch >> 1);
+      if (s16 < n16) {
+        const float f = inv_scale(p.do_scale[bhc * n16 + s16]);
 #pragma unroll
-    for (int x = tid; x < kTc * 8; x += 256) {
-      const int t = x >> 3, ch = x & 7, sl16 = cur.sl * 4 + (ch >> 1);
-      if (sl16 < n16) to_half(s.dO + swz<128>(t, ch), inv_scale(p.do_scale[bhc * n16 + sl16]));
-    }
-#pragma unroll
-    for (int x = tid; x < 64 * DK / 8; x += 256) {
-      const int d = x / (DK / 8), ch = x % (DK / 8), sl16 = cur.sl * 4 + (d >> 4);
-      if (sl16 >= n16) continue;
-      const uint4 u = *reinterpret_cast<const uint4*>(s.S0 + swz<PK>(d, ch)), w = *reinterpret_cast<const uint4*>(s.dS + swz<PK>(d, ch));
-      const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-      float f = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 m = unpack_h(uu[i]), n = unpack_h(ww[i]);
-        f = fmaf(m.x, n.x, fmaf(m.y, n.y, f));
+        for (int i = 0; i < kTc * 8 / NT; ++i) to_half(s.dO + swz<128>((tid >> 3) + i * (NT / 8), ch), f);
       }
-      frob = fmaf(f * p.w.s0_scale[bhc * n16 + sl16], p.ds1_scale[bhc * n16 + sl16], frob);
-    }
-    if (new_item) {
-      const float kf = inv_scale(sc[kScK]), qf = inv_scale(sc[kScQ]);
+      constexpr int PR = DK / 8;
+      const int cp_ = tid % PR;
 #pragma unroll
-      for (int x = tid; x < kTc * DK / 8; x += 256) {
-        const uint32_t at = swz<PK>(x / (DK / 8), x % (DK / 8));
-        to_half(sm.K[kq] + at, kf);
-        to_half(sm.Q[kq] + at, qf);
+      for (int i = 0; i < 64 * PR / NT; ++i) {
+        const int d = tid / PR + i * (NT / PR), d16 = cur.sl * 4 + (d >> 4);
+        if (d16 >= n16) continue;
+        const uint4 u = *reinterpret_cast<const uint4*>(s.S0 + swz<PK>(d, cp_)), w = *reinterpret_cast<const uint4*>(s.dS + swz<PK>(d, cp_));
+        float2 f = mul2(unpack_h(u.x), unpack_h(w.x));
+        f = fma2(unpack_h(u.y), unpack_h(w.y), f);
+        f = fma2(unpack_h(u.z), unpack_h(w.z), f);
+        f = fma2(unpack_h(u.w), unpack_h(w.w), f);
+        frob2 = fma2(mul2(f, both(p.w.s0_scale[bhc * n16 + d16])), both(p.ds1_scale[bhc * n16 + d16]), frob2);
+      }
+      if (new_item) {
+        const float kf = inv_scale(sc[kScK]), qf = inv_scale(sc[kScQ]);
+#pragma unroll
+        for (int i = 0; i < kTc * PR / NT; ++i) {
+          const uint32_t at = swz<PK>(tid / PR + i * (NT / PR), cp_);
+          to_half(sm.K[kq] + at, kf);
+          to_half(sm.Q[kq] + at, qf);
+        }
       }
     }
     __syncthreads();
@@ -1321,8 +1365,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
     if (++nxt.sl == ns) {
       nxt.sl = 0;
       if (++nxt.hh == per) {
-        nxt.hh = 0;
-        nxt.item = next_item(cur.item + gridDim.x);
+        next_item(nxt, cur.item + gridDim.x);
         nkq = kq ^ 1;
       }
     }
@@ -1339,52 +1382,49 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
         f[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
     };
-    float t_[2][NQ][4];
+    float t_[2][2][4];
     // t_ = X . Z over the slice: X tokens x value columns, Z value columns x key columns
     auto through = [&](uint32_t X, uint32_t Z, int which) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t_[mt][n][e] = 0.f;
-#pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint32_t ratio = sm.ratio[which][(cur.sl * 4 + kk) & 15];
-        uint32_t f0[4], f1[4];
+        uint32_t f0[4], f1[4], bb[4];
         load_a(f0, X, 0, kk, ratio);
         load_a(f1, X, 1, kk, ratio);
-#pragma unroll
-        for (int n = 0; n < NQ; n += 2) {
-          uint32_t bb[4];
-          load_b_rows_k<PK>(bb, Z, cq * (DK / 4) + 8 * n, kk, lane);
-          mma_h(t_[0][n], f0, bb[0], bb[1]);
-          mma_h(t_[0][n + 1], f0, bb[2], bb[3]);
-          mma_h(t_[1][n], f1, bb[0], bb[1]);
-          mma_h(t_[1][n + 1], f1, bb[2], bb[3]);
+        load_b_rows_k<PK>(bb, Z, cq * 16, kk, lane);
+        if (kk == 0) {
+          mma_h0(t_[0][0], f0, bb[0], bb[1]);
+          mma_h0(t_[0][1], f0, bb[2], bb[3]);
+          mma_h0(t_[1][0], f1, bb[0], bb[1]);
+          mma_h0(t_[1][1], f1, bb[2], bb[3]);
+        } else {
+          mma_h(t_[0][0], f0, bb[0], bb[1]);
+          mma_h(t_[0][1], f0, bb[2], bb[3]);
+          mma_h(t_[1][0], f1, bb[0], bb[1]);
+          mma_h(t_[1][1], f1, bb[2], bb[3]);
         }
       }
     };
-    // adds t_ times w[row] to acc, and its product with the rows of X16 to dot
-    auto fold = [&](float (&acc)[2][NQ][4], float (&dot)[2][2], const float* w, const float* w2, float f, const unsigned char* X16,
-                    float xi) {
+    // adds t_ times f w[row] to acc, and the product of that with the rows of X16 (true scale by xi) to dot
+    auto fold = [&](float (&acc)[2][2][4], float2 (&dot)[2][2], const float* w, const float* w2, float f,
+                    const unsigned char* X16, float xi) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int i = 32 * rg + 16 * mt + 8 * half + r;
-          const float g = f * w[i] * (w2 ? w2[i] : 1.f);
-          float d = 0.f;
+          const float2 g = both(w2 ? f * w[i] * w2[i] : f * w[i]);
+          float2 d = both(0.f);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            const int col = cq * (DK / 4) + 8 * n;
-            const float2 x = unpack_h(*reinterpret_cast<const uint32_t*>(X16 + swz<PK>(i, col >> 3) + 2 * cc));
-            const float u = t_[mt][n][2 * half] * g, v = t_[mt][n][2 * half + 1] * g;
-            acc[mt][n][2 * half] += u;
-            acc[mt][n][2 * half + 1] += v;
-            d = fmaf(u, x.x, fmaf(v, x.y, d));
+          for (int n = 0; n < 2; ++n) {
+            float* x = &acc[mt][n][2 * half];
+            const float2 t = make_float2(t_[mt][n][2 * half], t_[mt][n][2 * half + 1]);
+            const float2 y = fma2(t, g, make_float2(x[0], x[1]));
+            x[0] = y.x;
+            x[1] = y.y;
+            d = fma2(t, unpack_h(*reinterpret_cast<const uint32_t*>(X16 + swz<PK>(i, 2 * cq + n) + 2 * cc)), d);
           }
-          dot[mt][half] = fmaf(d, xi, dot[mt][half]);
+          dot[mt][half] = fma2(d, mul2(g, both(xi)), dot[mt][half]);
         }
     };
     const float ki = sc[kScK], qi = sc[kScQ];
@@ -1394,67 +1434,90 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
     fold(dk, own, sm.eG, sm.beta, -sm.inv[kRk1], sm.K[kq], ki);
     through(E, dS, kRk3);
     fold(dk, thru, sm.eE, sm.beta, sm.inv[kRk3], sm.K[kq], ki);
-    if (16 * cq < 32 * rg + 32) {
+    if (8 * NJ * cq < 32 * rg + 32) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t rn = sm.ratio[kRn][(cur.sl * 4 + kk) & 15], rp = sm.ratio[kRp][(cur.sl * 4 + kk) & 15];
-        uint32_t bb[4];
-        load_b_rows_n<128>(bb, E, 16 * cq, kk, lane);
+      for (int k2 = 0; k2 < 4; k2 += 2) {
+        uint32_t be[2][4];              // [k-step][tile: 2 words]
+        if (NJ == 1) {
+          uint32_t q4[4];
+          ldsm(q4, E + swz<128>(8 * cq + (lane & 7), 2 * k2 + (lane >> 3)));
+          be[0][0] = q4[0]; be[0][1] = q4[1]; be[1][0] = q4[2]; be[1][1] = q4[3];
+        } else {
+          load_b_rows_n<128>(be[0], E, 16 * cq, k2, lane);
+          load_b_rows_n<128>(be[1], E, 16 * cq, k2 + 1, lane);
+        }
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          uint32_t fy[4], fo[4];
-          load_a(fy, Y, mt, kk, rn);
-          load_a(fo, dO, mt, kk, rp);
-          mma_h(N[mt][0], fy, bb[0], bb[1]);
-          mma_h(N[mt][1], fy, bb[2], bb[3]);
-          mma_h(Pm[mt][0], fo, bb[0], bb[1]);
-          mma_h(Pm[mt][1], fo, bb[2], bb[3]);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t rn = sm.ratio[kRn][(cur.sl * 4 + k2 + i) & 15], rp = sm.ratio[kRp][(cur.sl * 4 + k2 + i) & 15];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t fy[4], fo[4];
+            load_a(fy, Y, mt, k2 + i, rn);
+            load_a(fo, dO, mt, k2 + i, rp);
+#pragma unroll
+            for (int n = 0; n < NJ; ++n) {
+              mma_h(N[mt][n], fy, be[i][2 * n], be[i][2 * n + 1]);
+              mma_h(Pm[mt][n], fo, be[i][2 * n], be[i][2 * n + 1]);
+            }
+          }
         }
       }
     }
 
     if (cur.sl == ns - 1) {
       // the head is complete: K K^T and Q K^T of this warp's block, the pair weights, their sums
-      float kk_[2][2][4], qk_[2][2][4];
+      float kk_[2][NJ][4], qk_[2][NJ][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) kk_[mt][n][e] = qk_[mt][n][e] = 0.f;
-      if (16 * cq < 32 * rg + 32) {
+      if (8 * NJ * cq < 32 * rg + 32) {
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          uint32_t bb[4];
-          load_b_rows_n<PK>(bb, ks, 16 * cq, k, lane);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            uint32_t fk[4], fq[4];
-            const uint32_t at = swz<PK>(32 * rg + 16 * mt + (lane & 15), 2 * k + (lane >> 4));
-            ldsm(fk, ks + at);
-            ldsm(fq, qs + at);
-            mma_h(kk_[mt][0], fk, bb[0], bb[1]);
-            mma_h(kk_[mt][1], fk, bb[2], bb[3]);
-            mma_h(qk_[mt][0], fq, bb[0], bb[1]);
-            mma_h(qk_[mt][1], fq, bb[2], bb[3]);
+        for (int k2 = 0; k2 < DK / 16; k2 += 2) {
+          uint32_t be[2][4];
+          if (NJ == 1) {
+            uint32_t q4[4];
+            ldsm(q4, ks + swz<PK>(8 * cq + (lane & 7), 2 * k2 + (lane >> 3)));
+            be[0][0] = q4[0]; be[0][1] = q4[1]; be[1][0] = q4[2]; be[1][1] = q4[3];
+          } else {
+            load_b_rows_n<PK>(be[0], ks, 16 * cq, k2, lane);
+            load_b_rows_n<PK>(be[1], ks, 16 * cq, k2 + 1, lane);
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              uint32_t fk[4], fq[4];
+              const uint32_t at = swz<PK>(32 * rg + 16 * mt + (lane & 15), 2 * (k2 + i) + (lane >> 4));
+              ldsm(fk, ks + at);
+              ldsm(fq, qs + at);
+#pragma unroll
+              for (int n = 0; n < NJ; ++n) {
+                mma_h(kk_[mt][n], fk, be[i][2 * n], be[i][2 * n + 1]);
+                mma_h(qk_[mt][n], fq, be[i][2 * n], be[i][2 * n + 1]);
+              }
+            }
         }
       }
-      float rows[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, cols[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, mp = 0.f, ma = 0.f;
-      const float kk2 = ki * ki, qk2 = qi * ki;
+      float rows[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, cols[NJ][2], mp = 0.f, ma = 0.f;
+#pragma unroll
+      for (int n = 0; n < NJ; ++n) cols[n][0] = cols[n][1] = 0.f;
+      const float kk2 = ki * ki, qk2 = qi * ki, sP = a.scale * sm.inv[kRp], sN = sm.inv[kRn];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = 32 * rg + 16 * mt + 8 * (e >> 1) + r, j = 16 * cq + 8 * n + cc + (e & 1);
-            const float D = j <= i ? expf(sm.G[i] - sm.G[j]) : 0.f, bj = sm.beta[j], bi = sm.beta[i];
-            const float nn = N[mt][n][e] * sm.inv[kRn];
-            const float wp = D * a.scale * bj * Pm[mt][n][e] * sm.inv[kRp];
-            const float wa = j < i ? -D * bi * bj * nn : 0.f;
+            const int i = 32 * rg + 16 * mt + 8 * (e >> 1) + r, j = 8 * (NJ * cq + n) + cc + (e & 1);
+            const float Db = j <= i ? __expf(sm.G[i] - sm.G[j]) * sm.beta[j] : 0.f;
+            const float nn = N[mt][n][e] * sN;
+            const float wp = Db * (Pm[mt][n][e] * sP);
+            const float wa = j < i ? -Db * sm.beta[i] * nn : 0.f;
             if (i == j && i < nt)
-              static_cast<__nv_bfloat16*>(p.dbeta)[a.row(b, t0 + i) * a.Hv + h] = __float2bfloat16_rn(nn);
+              static_cast<__nv_bfloat16*>(p.dbeta)[a.row(cur.b, t0 + i) * a.Hv + h] = __float2bfloat16_rn(nn);
             Pm[mt][n][e] = wp;
             N[mt][n][e] = wa;
             mp = fmaxf(mp, fabsf(wp));
@@ -1465,6 +1528,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
           }
       mp = warp_max(mp);
       ma = warp_max(ma);
+      float frob = frob2.x + frob2.y;
 #pragma unroll
       for (int w = 16; w; w >>= 1) frob += __shfl_xor_sync(kFull, frob, w);
       if (lane == 0) {
@@ -1476,55 +1540,57 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          float ow = own[mt][half].x + own[mt][half].y, th = thru[mt][half].x + thru[mt][half].y;
 #pragma unroll
           for (int w = 1; w < 4; w <<= 1) {
             rows[mt][half] += __shfl_xor_sync(kFull, rows[mt][half], w);
-            own[mt][half] += __shfl_xor_sync(kFull, own[mt][half], w);
-            thru[mt][half] += __shfl_xor_sync(kFull, thru[mt][half], w);
+            ow += __shfl_xor_sync(kFull, ow, w);
+            th += __shfl_xor_sync(kFull, th, w);
           }
           if ((lane & 3) == 0) {
             const int i = 32 * rg + 16 * mt + 8 * half + r;
             sm.row[cq][i] = rows[mt][half];
-            sm.own[cq][i] = own[mt][half];
-            sm.thru[cq][i] = thru[mt][half];
+            sm.own[cq][i] = ow;
+            sm.thru[cq][i] = th;
           }
         }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NJ; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) cols[n][e] += __shfl_xor_sync(kFull, cols[n][e], w);
-          if (lane < 4) sm.col[rg][16 * cq + 8 * n + cc + e] = cols[n][e];
+          if (lane < 4) sm.col[rg][8 * (NJ * cq + n) + cc + e] = cols[n][e];
         }
       __syncthreads();
-      mp = ma = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        mp = fmaxf(mp, sm.mx[0][w]);
-        ma = fmaxf(ma, sm.mx[1][w]);
-      }
+      mp = warp_max(sm.mx[0][lane % NW]);
+      ma = warp_max(sm.mx[1][lane % NW]);
       const float pf = up_scale(mp), af = up_scale(ma);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int i = 32 * rg + 16 * mt + 8 * half + r;
-            const uint32_t at = swz<128>(i, 2 * cq + n) + 2 * cc;
+            const uint32_t at = swz<128>(i, NJ * cq + n) + 2 * cc;
             *reinterpret_cast<uint32_t*>(sm.mP + at) = pack_h(Pm[mt][n][2 * half] * pf, Pm[mt][n][2 * half + 1] * pf);
             *reinterpret_cast<uint32_t*>(sm.mA + at) = pack_h(N[mt][n][2 * half] * af, N[mt][n][2 * half + 1] * af);
           }
       if (warp == 0) {
         // dg: suffix sums of dG, two tokens a lane
-        float x[2], w = 0.f, f = lane < 8 ? sm.red[lane] : 0.f;
+        float x[2], w = 0.f, f = lane < NW ? sm.red[lane] : 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * lane + e;
-          const float th = sm.thru[0][i] + sm.thru[1][i] + sm.thru[2][i] + sm.thru[3][i];
-          x[e] = (sm.row[0][i] + sm.row[1][i] + sm.row[2][i] + sm.row[3][i]) - (sm.col[0][i] + sm.col[1][i]) +
-                 (sm.own[0][i] + sm.own[1][i] + sm.own[2][i] + sm.own[3][i]) - th;
+          float th = 0.f;
+          x[e] = -(sm.col[0][i] + sm.col[1][i]);
+#pragma unroll
+          for (int q = 0; q < CQ; ++q) {
+            x[e] += sm.row[q][i] + sm.own[q][i];
+            th += sm.thru[q][i];
+          }
+          x[e] -= th;
           w += th;
         }
         float pair = x[0] + x[1];
@@ -1540,40 +1606,33 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (2 * lane + e < nt)
-            static_cast<__nv_bfloat16*>(p.dg)[a.row(b, t0 + 2 * lane + e) * a.Hv + h] = __float2bfloat16_rn(out[e]);
+            static_cast<__nv_bfloat16*>(p.dg)[a.row(cur.b, t0 + 2 * lane + e) * a.Hv + h] = __float2bfloat16_rn(out[e]);
       }
       if (warp == 1) {
         for (int t = max(nt, 0) + lane; t < min(kTc, a.T - t0); t += 32) {
-          static_cast<__nv_bfloat16*>(p.dg)[a.row(b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
-          static_cast<__nv_bfloat16*>(p.dbeta)[a.row(b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+          static_cast<__nv_bfloat16*>(p.dg)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+          static_cast<__nv_bfloat16*>(p.dbeta)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
         }
       }
       __syncthreads();
       const uint32_t mPs = smem_u32(sm.mP), mAs = smem_u32(sm.mA);
-      // acc += f * (M B) with M taken as stored (rows i) or transposed (rows j)
+      // t_ += M B with M taken as stored (rows i) or transposed (rows j)
       auto pairs = [&](uint32_t M, uint32_t B, bool trans) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          uint32_t fa[2][4];
+          uint32_t bb[4];
+          load_b_rows_k<PK>(bb, B, cq * 16, kk, lane);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            const int m0 = 32 * rg + 16 * mt;
+            const int blk = 2 * rg + mt, m0 = 16 * blk;          // 16-blocks on the far side of the diagonal are zero
+            if (trans ? kk < blk : kk > blk) continue;
+            uint32_t fa[4];
             if (trans)
-              ldsm_t(fa[mt], M + swz<128>(16 * kk + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1)));
+              ldsm_t(fa, M + swz<128>(16 * kk + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1)));
             else
-              ldsm(fa[mt], M + swz<128>(m0 + (lane & 15), 2 * kk + (lane >> 4)));
-          }
-#pragma unroll
-          for (int n = 0; n < NQ; n += 2) {
-            uint32_t bb[4];
-            load_b_rows_k<PK>(bb, B, cq * (DK / 4) + 8 * n, kk, lane);
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const int blk = 2 * rg + mt;                       // 16-blocks on the far side of the diagonal are zero
-              if (trans ? kk < blk : kk > blk) continue;
-              mma_h(t_[mt][n], fa[mt], bb[0], bb[1]);
-              mma_h(t_[mt][n + 1], fa[mt], bb[2], bb[3]);
-            }
+              ldsm(fa, M + swz<128>(m0 + (lane & 15), 2 * kk + (lane >> 4)));
+            mma_h(t_[mt][0], fa, bb[0], bb[1]);
+            mma_h(t_[mt][1], fa, bb[2], bb[3]);
           }
         }
       };
@@ -1581,17 +1640,16 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) t_[mt][n][e] = 0.f;
       };
-      auto add = [&](float (&acc)[2][NQ][4], float f) {
+      auto add = [&](float (&acc)[2][2][4], float f) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][n][e] = fmaf(t_[mt][n][e], f, acc[mt][n][e]);
+          for (int n = 0; n < 2; ++n)
+            set4(acc[mt][n], fma2(lo2(t_[mt][n]), both(f), lo2(acc[mt][n])), fma2(hi2(t_[mt][n]), both(f), hi2(acc[mt][n])));
       };
       clear();
       pairs(mPs, ks, false);
@@ -1604,20 +1662,23 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaTcBwdArgs p)
       pairs(mAs, ks, true);
       add(dk, inv_scale(af) * ki);
       if (cur.hh == per - 1) {
+        // lanes of a quad swap halves, so that each writes 8 bytes of one tile
+        const bool odd = lane & 1;
+        const int col = cq * 16 + (odd ? 8 : 0) + 2 * (cc & 4 ? 2 : 0);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int t = t0 + 32 * rg + 16 * mt + 8 * half + r;
-            if (t >= a.T) continue;
-            const int64_t at = a.row(b, t) * qk_row + hk * DK + cq * (DK / 4) + cc;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.dq) + at + 8 * n) =
-                  pack_b(dq[mt][n][2 * half], dq[mt][n][2 * half + 1]);
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.dk) + at + 8 * n) =
-                  pack_b(dk[mt][n][2 * half], dk[mt][n][2 * half + 1]);
-            }
+            const int64_t at = t < a.T ? a.row(cur.b, t) * qk_row + cur.hk * DK + col : 0;
+            auto write = [&](void* out, const float (&x)[2][2][4]) {
+              const uint32_t w0 = pack_b(x[mt][0][2 * half], x[mt][0][2 * half + 1]), w1 = pack_b(x[mt][1][2 * half], x[mt][1][2 * half + 1]);
+              const uint32_t got = __shfl_xor_sync(kFull, odd ? w0 : w1, 1);
+              if (t < a.T)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = odd ? make_uint2(got, w1) : make_uint2(w0, got);
+            };
+            write(p.dq, dq);
+            write(p.dk, dk);
           }
       }
     }
@@ -1640,7 +1701,7 @@ int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   if (rc) return rc;
   ++*launches;
   const int64_t items = static_cast<int64_t>(t.a.B) * t.a.Hk * ((t.a.T + kTc - 1) / kTc);
-  delta_grad_kernel<DK><<<static_cast<unsigned>(items < t.num_sms ? items : t.num_sms), 256, gsm, s>>>(t);
+  delta_grad_kernel<DK><<<static_cast<unsigned>(items < t.num_sms ? items : t.num_sms), GradSmem<DK>::NT, gsm, s>>>(t);
   rc = check_launch();
   if (!rc) ++*launches;
   return rc;
