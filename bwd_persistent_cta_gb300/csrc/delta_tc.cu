@@ -311,12 +311,20 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   const int64_t bhc = (static_cast<int64_t>(b) * a.Hv + h) * nc + c, bkc = (static_cast<int64_t>(b) * a.Hk + hk) * nc + c;
   const uint32_t ks = smem_u32(sm.in.K), qs = smem_u32(sm.in.Q);
 
-  for (int x = tid; x < kTc * DK / 8; x += 128) {
-    const int t = x / (DK / 8), ch = x % (DK / 8);
-    const bool ok = t < nt;
-    const int64_t row = a.row(b, t0 + (ok ? t : 0));
-    cp16_or_zero(ks + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.k) + row * a.k_row + hk * DK + ch * 8, ok);
-    cp16_or_zero(qs + swz<PK>(t, ch), static_cast<const __nv_bfloat16*>(a.q) + row * a.q_row + hk * DK + ch * 8, ok);
+  constexpr int PR = DK / 8, STEP = 128 / PR;         // pieces of a row; rows between a thread's pieces
+  const int pt = tid / PR, pch = tid % PR;
+  {
+    const int64_t row0 = a.row(b, t0), tstep = a.bfirst ? 1 : a.B;
+    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(a.k) + row0 * a.k_row + hk * DK + pch * 8,
+                        *qp = static_cast<const __nv_bfloat16*>(a.q) + row0 * a.q_row + hk * DK + pch * 8;
+#pragma unroll
+    for (int i = 0; i < kTc / STEP; ++i) {
+      const int t = pt + i * STEP;
+      const bool ok = t < nt;
+      const int64_t dt = ok ? t * tstep : 0;
+      cp16_or_zero(ks + swz<PK>(t, pch), kp + dt * a.k_row, ok);
+      cp16_or_zero(qs + swz<PK>(t, pch), qp + dt * a.q_row, ok);
+    }
   }
   cp_commit();
   // cumulative decay in two floats: D_ij stays exact to fp32 however large G
@@ -374,19 +382,19 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   __syncthreads();
 
   // scales of the key and query tiles, and their fp16 copies (one head of a group writes)
-  float km = 0.f, qm = 0.f;
-  for (int x = tid; x < kTc * DK / 8; x += 128) {
-    const uint4 kv = *reinterpret_cast<const uint4*>(sm.in.K + x * 16), qv = *reinterpret_cast<const uint4*>(sm.in.Q + x * 16);
-    const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+  float km, qm;
+  {
+    // bf16 magnitudes order as 16-bit integers, two at a time
+    uint32_t kx = 0, qx = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_b(kw[i]), g = unpack_b(qw[i]);
-      km = fmaxf(km, fmaxf(fabsf(f.x), fabsf(f.y)));
-      qm = fmaxf(qm, fmaxf(fabsf(g.x), fabsf(g.y)));
+    for (int i = 0; i < kTc / STEP; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(sm.in.K + (tid + i * 128) * 16), w = *reinterpret_cast<const uint4*>(sm.in.Q + (tid + i * 128) * 16);
+      kx = __vmaxu2(__vmaxu2(kx, __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu)), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+      qx = __vmaxu2(__vmaxu2(qx, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
     }
+    km = warp_max(__uint_as_float(max(kx >> 16, kx & 0xffffu) << 16));
+    qm = warp_max(__uint_as_float(max(qx >> 16, qx & 0xffffu) << 16));
   }
-  km = warp_max(km);
-  qm = warp_max(qm);
   if (lane == 0) {
     sm.red[0][warp] = km;
     sm.red[1][warp] = qm;
@@ -401,20 +409,23 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   if (h % per == 0) {
     unsigned char* ko = static_cast<unsigned char*>(p.w.k16) + bkc * kTc * PK;
     unsigned char* qo = static_cast<unsigned char*>(p.w.q16) + bkc * kTc * PK;
-    for (int x = tid; x < kTc * DK / 8; x += 128) {
-      // piece j = 4 m + i of the permuted row: columns 32 m + 8 c + 2 i, c = 0..3
-      const int t = x / (DK / 8), j = x % (DK / 8), m = j >> 2, i = j & 3;
-      uint32_t kw[4], qw[4];
+    // piece 4 m + i of the permuted row holds words i of pieces 4 m .. 4 m + 3
+    auto permute = [&](const unsigned char* in, unsigned char* out, float f, int t, int m) {
+      uint4 w[4];
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const uint32_t at = swz<PK>(t, 4 * m + cc) + 4 * i;
-        const float2 f = unpack_b(*reinterpret_cast<const uint32_t*>(sm.in.K + at));
-        const float2 g = unpack_b(*reinterpret_cast<const uint32_t*>(sm.in.Q + at));
-        kw[cc] = pack_h(f.x * kf, f.y * kf);
-        qw[cc] = pack_h(g.x * qf, g.y * qf);
-      }
-      *reinterpret_cast<uint4*>(ko + swz<PK>(t, j)) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-      *reinterpret_cast<uint4*>(qo + swz<PK>(t, j)) = make_uint4(qw[0], qw[1], qw[2], qw[3]);
+      for (int c4 = 0; c4 < 4; ++c4) w[c4] = *reinterpret_cast<const uint4*>(in + swz<PK>(t, 4 * m + c4));
+      auto half2_of = [&](uint32_t v) { return pack_h(mul2(unpack_b(v), both(f))); };
+      *reinterpret_cast<uint4*>(out + swz<PK>(t, 4 * m)) = make_uint4(half2_of(w[0].x), half2_of(w[1].x), half2_of(w[2].x), half2_of(w[3].x));
+      *reinterpret_cast<uint4*>(out + swz<PK>(t, 4 * m + 1)) = make_uint4(half2_of(w[0].y), half2_of(w[1].y), half2_of(w[2].y), half2_of(w[3].y));
+      *reinterpret_cast<uint4*>(out + swz<PK>(t, 4 * m + 2)) = make_uint4(half2_of(w[0].z), half2_of(w[1].z), half2_of(w[2].z), half2_of(w[3].z));
+      *reinterpret_cast<uint4*>(out + swz<PK>(t, 4 * m + 3)) = make_uint4(half2_of(w[0].w), half2_of(w[1].w), half2_of(w[2].w), half2_of(w[3].w));
+    };
+    constexpr int MR = DK / 32;
+#pragma unroll
+    for (int i = 0; i < kTc * MR / 128; ++i) {
+      const int t = (tid + i * 128) / MR, m = (tid + i * 128) % MR;
+      permute(sm.in.K, ko, kf, t, m);
+      permute(sm.in.Q, qo, qf, t, m);
     }
   }
 
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * warp + r + (e >> 1) * 8, j = 8 * n + cc + (e & 1);
-      const float d = j <= i ? expf((sm.Gh[i] - sm.Gh[j]) + (sm.Gl[i] - sm.Gl[j])) : 0.f;
+      const float d = j <= i ? __expf((sm.Gh[i] - sm.Gh[j]) + (sm.Gl[i] - sm.Gl[j])) : 0.f;
       sm.A[i * kXP + j] = j < i ? d * kk[n][e] : 0.f;
       qk[n][e] = j <= i ? a.scale * d * qk[n][e] : 0.f;
       pm = fmaxf(pm, fabsf(qk[n][e]));
@@ -481,14 +492,18 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == jc ? 1.f : 0.f;
+      float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int j = 0; j < i; ++j) {
-        const float w = which ? sm.beta[b0 + i] : sm.beta[b0 + j];
-        s = fmaf(-sm.A[(b0 + i) * kXP + b0 + j] * w, x[j], s);
+        // which = 0: y_j = beta_j x_j is kept; which = 1: the row's beta after the sum
+        s0 = j & 1 ? s0 : fmaf(-sm.A[(b0 + i) * kXP + b0 + j], x[j], s0);
+        s1 = j & 1 ? fmaf(-sm.A[(b0 + i) * kXP + b0 + j], x[j], s1) : s1;
       }
-      x[i] = i < jc ? 0.f : s;
-      X[(b0 + i) * kXP + col] = x[i];
+      const float bi = sm.beta[b0 + i];
+      const float one = i == jc ? 1.f : 0.f;
+      const float v = i < jc ? 0.f : which ? fmaf(bi, s0 + s1, one) : s0 + s1 + one;
+      x[i] = which ? v : bi * v;
+      X[(b0 + i) * kXP + col] = v;
     }
   }
   __syncthreads();
@@ -516,13 +531,21 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   if (mine)
     warp_mul<4, 4>(X + (32 + 16 * half) * kXP, X + (32 + 16 * half) * kXP + 32, X + 32, nullptr, nullptr, -1.f, lane);
   __syncthreads();
-  // strictly lower part, high and low
+  // strictly lower part, high and low: the diagonal goes, the blocks above it are not read
+  if (mine) X[t64 * (kXP + 1)] = 0.f;
+  __syncthreads();
+  // piece ch of rows i, i + 8, ..: rows of 16-block i / 16 have 2 (i / 16) + 2 pieces
+  const int wi = t64 >> 3, wch = t64 & 7;
   float xm = 0.f;
-  if (mine)
-    for (int x = t64; x < kTile; x += 64) {
-      const int i = x >> 6, j = x & 63;
-      if (j < i) xm = fmaxf(xm, fabsf(X[i * kXP + j]));
+  if (mine) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      if (wch > (n | 1)) continue;
+      const float4 u = *reinterpret_cast<const float4*>(X + (wi + 8 * n) * kXP + 8 * wch), w = *reinterpret_cast<const float4*>(X + (wi + 8 * n) * kXP + 8 * wch + 4);
+      xm = fmaxf(xm, fmaxf(fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))),
+                           fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w)))));
     }
+  }
   xm = warp_max(xm);
   if (lane == 0) sm.red[3][warp] = xm;
   __syncthreads();
@@ -530,17 +553,17 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   const float xf = up_scale(fmaxf(sm.red[3][2 * which], sm.red[3][2 * which + 1]));
   if (t64 == 0) sc[which ? kScTB : kScTH] = inv_scale(xf);
   unsigned char* xo = static_cast<unsigned char*>(which ? p.w.tb : p.w.th) + bhc * 2 * kTile * 2;
-  for (int x = t64; x < kTile / 8; x += 64) {
-    const int i = x >> 3, ch = x & 7;
-    if (8 * ch >= (i | 15)) continue;                 // blocks above the diagonal are not read
-    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = 8 * ch + 2 * k;
-      split(make_float2(j < i ? X[i * kXP + j] * xf : 0.f, j + 1 < i ? X[i * kXP + j + 1] * xf : 0.f), hi[k], lo[k]);
-    }
-    *reinterpret_cast<uint4*>(xo + swz<128>(i, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(xo + kTile * 2 + swz<128>(i, ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  for (int n = 0; n < 8; ++n) {
+    if (wch > (n | 1)) continue;
+    const float4 u = *reinterpret_cast<const float4*>(X + (wi + 8 * n) * kXP + 8 * wch), w = *reinterpret_cast<const float4*>(X + (wi + 8 * n) * kXP + 8 * wch + 4);
+    uint4 hi, lo;
+    split(mul2(make_float2(u.x, u.y), both(xf)), hi.x, lo.x);
+    split(mul2(make_float2(u.z, u.w), both(xf)), hi.y, lo.y);
+    split(mul2(make_float2(w.x, w.y), both(xf)), hi.z, lo.z);
+    split(mul2(make_float2(w.z, w.w), both(xf)), hi.w, lo.w);
+    *reinterpret_cast<uint4*>(xo + swz<128>(wi + 8 * n, wch)) = hi;
+    *reinterpret_cast<uint4*>(xo + kTile * 2 + swz<128>(wi + 8 * n, wch)) = lo;
   }
 }
 
@@ -1135,9 +1158,9 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
 // pass in slices of 64 through two stages, the next one (and the next chunk's
 // keys and queries) arriving while this one is multiplied.  Warp (rg, cq) of
 // 2 x Dk / 16 owns rows 32 rg .. + 31 and 16 of the key columns of every product.
-// The fp16 copies of S0, dS1, e, y and do carry one scale per 16 value columns,
-// i.e. per k-step of the products that sum over value columns; the ratio to the
-// head's largest is applied to the A operand, exactly (a power of two).
+// The fp16 copies of S0, dS1, e, y and do carry one scale per 16 value columns;
+// each piece is brought to the head's largest as it arrives, exactly (a power of
+// two), so that one accumulator takes the sum over all value columns.
 template <int DK>
 struct GradSmem {
   static constexpr int NW = DK / 8, NT = 32 * NW;                // warps, threads
@@ -1148,13 +1171,14 @@ struct GradSmem {
   unsigned char K[2][kTc * DK * 2], Q[2][kTc * DK * 2];
   unsigned char mP[kTile * 2], mA[kTile * 2];
   float eG[kTc], eE[kTc], beta[kTc], G[kTc];
-  // ratios per k-step (fp16 pairs) and inverse scales of the five products of a head
+  // per 16 value columns: the fp16 pair that brings S0, dS1, e, y to the head's
+  // scale, the fp32 factor that does so from bf16 for do; and the head's inverse scales
   uint32_t ratio[5][16];
   float inv[5];
   float own[NW / 2][kTc], thru[NW / 2][kTc], row[NW / 2][kTc], col[2][kTc];
   float red[NW], mx[2][NW];
 };
-enum { kRq = 0, kRk1, kRk3, kRn, kRp };
+enum { kRs = 0, kRd, kRe, kRy, kRo };
 
 // A place in a CTA's walk: chunk c of (batch b, key head hk), value head hh of
 // the group, slice sl; t0 and nt its first token and valid tokens.
@@ -1278,7 +1302,8 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
   if (cur.item < items) fetch(cur, 0, 0);
   float dq[2][2][4], dk[2][2][4];
   float N[2][NJ][4], Pm[2][NJ][4];
-  float2 own[2][2], thru[2][2], frob2 = both(0.f);
+  float t_[3][2][2][4];            // do S0, y S0, e dS1 of the head
+  float2 frob2 = both(0.f);
   while (cur.item < items) {
     const int t0 = cur.c * kTc, nt = cur.nt, h = cur.hk * per + cur.hh;
     const int64_t bhc = head_chunk(cur);
@@ -1302,39 +1327,60 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
         sm.G[tid] = sc[192 + tid];
       }
       if (warp >= 3 && warp < 8) {
-        // exponents of the product of two inverse scales, per 16 value columns
         const int w = warp - 3;
-        const float* x = w == kRq || w == kRp ? p.do_scale : w == kRk3 ? p.w.e_scale : p.y_scale;
-        const float* y = w == kRq || w == kRk1 ? p.w.s0_scale : w == kRk3 ? p.ds1_scale : p.w.e_scale;
-        int e = -1000;
-        if (lane < n16)
-          e = (__float_as_int(x[bhc * n16 + lane]) >> 23) + (__float_as_int(y[bhc * n16 + lane]) >> 23) - 254;
+        const float* x = w == kRs ? p.w.s0_scale : w == kRd ? p.ds1_scale : w == kRe ? p.w.e_scale : w == kRy ? p.y_scale : p.do_scale;
+        const int e = lane < n16 ? __float_as_int(x[bhc * n16 + lane]) >> 23 : 0;       // of the inverse scales
         const int m = __reduce_max_sync(kFull, e);
         if (lane < 16) {
           const int d = e - m;                          // 2^d as fp16: zero below 2^-24
           const float f = d < -24 ? 0.f : __int_as_float((127 + d) << 23);
-          sm.ratio[w][lane] = pack_h(f, f);
+          sm.ratio[w][lane] = w == kRo ? __float_as_uint(__int_as_float((254 - m) << 23)) : pack_h(f, f);
         }
-        if (lane == 0) sm.inv[w] = m < -126 ? 0.f : __int_as_float((127 + min(m, 127)) << 23);
+        if (lane == 0) sm.inv[w] = __int_as_float(m << 23);
       }
+      // the stage's pieces are scaled with these below
+      __syncthreads();
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
         for (int n = 0; n < NJ; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) N[mt][n][e] = Pm[mt][n][e] = 0.f;
-        own[mt][0] = own[mt][1] = thru[mt][0] = thru[mt][1] = both(0.f);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t_[i][mt][n][e] = 0.f;
       }
       frob2 = both(0.f);
     }
     cp_wait<0>();
-    // this thread's own pieces: do to fp16, <S0, dS1>, and a new chunk's keys and queries to fp16
+    // this thread's own pieces: do to fp16, the others to the head's scale, <S0, dS1>, and a new chunk's keys and
+    // queries to fp16
+    auto rescale = [&](unsigned char* at, uint32_t ratio) {
+      uint4 v = *reinterpret_cast<uint4*>(at);
+      const __half2 m = *reinterpret_cast<const __half2*>(&ratio);
+      auto mul = [&](uint32_t x) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), m);
+        return *reinterpret_cast<const uint32_t*>(&y);
+      };
+      v = make_uint4(mul(v.x), mul(v.y), mul(v.z), mul(v.w));
+      *reinterpret_cast<uint4*>(at) = v;
+      return v;
+    };
     {
       const int ch = tid & 7, s16 = cur.sl * 4 + (ch >> 1);
       if (s16 < n16) {
-        const float f = inv_scale(p.do_scale[bhc * n16 + s16]);
+        const float f = __uint_as_float(sm.ratio[kRo][s16]);
+        const uint32_t re = sm.ratio[kRe][s16], ry = sm.ratio[kRy][s16];
 #pragma unroll
-        for (int i = 0; i < kTc * 8 / NT; ++i) to_half(s.dO + swz<128>((tid >> 3) + i * (NT / 8), ch), f);
+        for (int i = 0; i < kTc * 8 / NT; ++i) {
+          const uint32_t at = swz<128>((tid >> 3) + i * (NT / 8), ch);
+          to_half(s.dO + at, f);
+          rescale(s.E + at, re);
+          rescale(s.Y + at, ry);
+        }
       }
       constexpr int PR = DK / 8;
       const int cp_ = tid % PR;
@@ -1342,12 +1388,12 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
       for (int i = 0; i < 64 * PR / NT; ++i) {
         const int d = tid / PR + i * (NT / PR), d16 = cur.sl * 4 + (d >> 4);
         if (d16 >= n16) continue;
-        const uint4 u = *reinterpret_cast<const uint4*>(s.S0 + swz<PK>(d, cp_)), w = *reinterpret_cast<const uint4*>(s.dS + swz<PK>(d, cp_));
-        float2 f = mul2(unpack_h(u.x), unpack_h(w.x));
-        f = fma2(unpack_h(u.y), unpack_h(w.y), f);
-        f = fma2(unpack_h(u.z), unpack_h(w.z), f);
-        f = fma2(unpack_h(u.w), unpack_h(w.w), f);
-        frob2 = fma2(mul2(f, both(p.w.s0_scale[bhc * n16 + d16])), both(p.ds1_scale[bhc * n16 + d16]), frob2);
+        const uint32_t at = swz<PK>(d, cp_);
+        const uint4 u = rescale(s.S0 + at, sm.ratio[kRs][d16]), w = rescale(s.dS + at, sm.ratio[kRd][d16]);
+        frob2 = fma2(unpack_h(u.x), unpack_h(w.x), frob2);
+        frob2 = fma2(unpack_h(u.y), unpack_h(w.y), frob2);
+        frob2 = fma2(unpack_h(u.z), unpack_h(w.z), frob2);
+        frob2 = fma2(unpack_h(u.w), unpack_h(w.w), frob2);
       }
       if (new_item) {
         const float kf = inv_scale(sc[kScK]), qf = inv_scale(sc[kScQ]);
@@ -1373,99 +1419,74 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
 
     // products over this slice of value columns
     const uint32_t dO = smem_u32(s.dO), E = smem_u32(s.E), Y = smem_u32(s.Y), S0 = smem_u32(s.S0), dS = smem_u32(s.dS);
-    auto load_a = [&](uint32_t (&f)[4], uint32_t tile, int mt, int kk, uint32_t ratio) {
+    auto load_a = [&](uint32_t (&f)[4], uint32_t tile, int mt, int kk) {
       ldsm(f, tile + swz<128>(32 * rg + 16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
-      const __half2 m = *reinterpret_cast<const __half2*>(&ratio);
+    };
+    // do S0, y S0 and e dS1: tokens x key columns; y e^T and do e^T: tokens x tokens
+    const bool lower = 8 * NJ * cq < 32 * rg + 32;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&f[i]), m);
-        f[i] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t bs[4], bd[4], be[4];
+      load_b_rows_k<PK>(bs, S0, cq * 16, kk, lane);
+      load_b_rows_k<PK>(bd, dS, cq * 16, kk, lane);
+      if (lower) {
+        if (NJ == 1) ldsm(be, E + swz<128>(8 * cq + (lane & 7), 2 * kk + ((lane >> 3) & 1)));
+        else load_b_rows_n<128>(be, E, 16 * cq, kk, lane);
       }
-    };
-    float t_[2][2][4];
-    // t_ = X . Z over the slice: X tokens x value columns, Z value columns x key columns
-    auto through = [&](uint32_t X, uint32_t Z, int which) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t ratio = sm.ratio[which][(cur.sl * 4 + kk) & 15];
-        uint32_t f0[4], f1[4], bb[4];
-        load_a(f0, X, 0, kk, ratio);
-        load_a(f1, X, 1, kk, ratio);
-        load_b_rows_k<PK>(bb, Z, cq * 16, kk, lane);
-        if (kk == 0) {
-          mma_h0(t_[0][0], f0, bb[0], bb[1]);
-          mma_h0(t_[0][1], f0, bb[2], bb[3]);
-          mma_h0(t_[1][0], f1, bb[0], bb[1]);
-          mma_h0(t_[1][1], f1, bb[2], bb[3]);
-        } else {
-          mma_h(t_[0][0], f0, bb[0], bb[1]);
-          mma_h(t_[0][1], f0, bb[2], bb[3]);
-          mma_h(t_[1][0], f1, bb[0], bb[1]);
-          mma_h(t_[1][1], f1, bb[2], bb[3]);
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t fo[4], fy[4], fe[4];
+        load_a(fo, dO, mt, kk);
+        load_a(fy, Y, mt, kk);
+        load_a(fe, E, mt, kk);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma_h(t_[0][mt][n], fo, bs[2 * n], bs[2 * n + 1]);
+          mma_h(t_[1][mt][n], fy, bs[2 * n], bs[2 * n + 1]);
+          mma_h(t_[2][mt][n], fe, bd[2 * n], bd[2 * n + 1]);
         }
-      }
-    };
-    // adds t_ times f w[row] to acc, and the product of that with the rows of X16 (true scale by xi) to dot
-    auto fold = [&](float (&acc)[2][2][4], float2 (&dot)[2][2], const float* w, const float* w2, float f,
-                    const unsigned char* X16, float xi) {
+        if (lower)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int i = 32 * rg + 16 * mt + 8 * half + r;
-          const float2 g = both(w2 ? f * w[i] * w2[i] : f * w[i]);
-          float2 d = both(0.f);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float* x = &acc[mt][n][2 * half];
-            const float2 t = make_float2(t_[mt][n][2 * half], t_[mt][n][2 * half + 1]);
-            const float2 y = fma2(t, g, make_float2(x[0], x[1]));
-            x[0] = y.x;
-            x[1] = y.y;
-            d = fma2(t, unpack_h(*reinterpret_cast<const uint32_t*>(X16 + swz<PK>(i, 2 * cq + n) + 2 * cc)), d);
+          for (int n = 0; n < NJ; ++n) {
+            mma_h(N[mt][n], fy, be[2 * n], be[2 * n + 1]);
+            mma_h(Pm[mt][n], fo, be[2 * n], be[2 * n + 1]);
           }
-          dot[mt][half] = fma2(d, mul2(g, both(xi)), dot[mt][half]);
-        }
-    };
-    const float ki = sc[kScK], qi = sc[kScQ];
-    through(dO, S0, kRq);
-    fold(dq, own, sm.eG, nullptr, a.scale * sm.inv[kRq], sm.Q[kq], qi);
-    through(Y, S0, kRk1);
-    fold(dk, own, sm.eG, sm.beta, -sm.inv[kRk1], sm.K[kq], ki);
-    through(E, dS, kRk3);
-    fold(dk, thru, sm.eE, sm.beta, sm.inv[kRk3], sm.K[kq], ki);
-    if (8 * NJ * cq < 32 * rg + 32) {
-#pragma unroll
-      for (int k2 = 0; k2 < 4; k2 += 2) {
-        uint32_t be[2][4];              // [k-step][tile: 2 words]
-        if (NJ == 1) {
-          uint32_t q4[4];
-          ldsm(q4, E + swz<128>(8 * cq + (lane & 7), 2 * k2 + (lane >> 3)));
-          be[0][0] = q4[0]; be[0][1] = q4[1]; be[1][0] = q4[2]; be[1][1] = q4[3];
-        } else {
-          load_b_rows_n<128>(be[0], E, 16 * cq, k2, lane);
-          load_b_rows_n<128>(be[1], E, 16 * cq, k2 + 1, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t rn = sm.ratio[kRn][(cur.sl * 4 + k2 + i) & 15], rp = sm.ratio[kRp][(cur.sl * 4 + k2 + i) & 15];
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            uint32_t fy[4], fo[4];
-            load_a(fy, Y, mt, k2 + i, rn);
-            load_a(fo, dO, mt, k2 + i, rp);
-#pragma unroll
-            for (int n = 0; n < NJ; ++n) {
-              mma_h(N[mt][n], fy, be[i][2 * n], be[i][2 * n + 1]);
-              mma_h(Pm[mt][n], fo, be[i][2 * n], be[i][2 * n + 1]);
-            }
-          }
-        }
       }
     }
 
     if (cur.sl == ns - 1) {
-      // the head is complete: K K^T and Q K^T of this warp's block, the pair weights, their sums
+      // the head is complete.  Adds t times f w[row] to acc; returns in dot the product of that with the rows of X16
+      // (true scale by xi)
+      auto fold = [&](const float (&t)[2][2][4], float (&acc)[2][2][4], float2 (&dot)[2][2], const float* w, const float* w2,
+                      float f, const unsigned char* X16, float xi) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int i = 32 * rg + 16 * mt + 8 * half + r;
+            const float2 g = both(w2 ? f * w[i] * w2[i] : f * w[i]);
+            float2 d = both(0.f);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              float* x = &acc[mt][n][2 * half];
+              const float2 tt = make_float2(t[mt][n][2 * half], t[mt][n][2 * half + 1]);
+              const float2 y = fma2(tt, g, make_float2(x[0], x[1]));
+              x[0] = y.x;
+              x[1] = y.y;
+              d = fma2(tt, unpack_h(*reinterpret_cast<const uint32_t*>(X16 + swz<PK>(i, 2 * cq + n) + 2 * cc)), d);
+            }
+            dot[mt][half] = fma2(d, mul2(g, both(xi)), dot[mt][half]);
+          }
+      };
+      const float ki = sc[kScK], qi = sc[kScQ];
+      const float iS = sm.inv[kRs], iD = sm.inv[kRd], iE = sm.inv[kRe], iY = sm.inv[kRy], iO = sm.inv[kRo];
+      float2 own[2][2], thru[2][2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) own[mt][0] = own[mt][1] = thru[mt][0] = thru[mt][1] = both(0.f);
+      fold(t_[0], dq, own, sm.eG, nullptr, a.scale * iO * iS, sm.Q[kq], qi);
+      fold(t_[1], dk, own, sm.eG, sm.beta, -(iY * iS), sm.K[kq], ki);
+      fold(t_[2], dk, thru, sm.eE, sm.beta, iE * iD, sm.K[kq], ki);
+      // K K^T and Q K^T of this warp's block, the pair weights, their sums
       float kk_[2][NJ][4], qk_[2][NJ][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
@@ -1504,7 +1525,7 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
       float rows[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, cols[NJ][2], mp = 0.f, ma = 0.f;
 #pragma unroll
       for (int n = 0; n < NJ; ++n) cols[n][0] = cols[n][1] = 0.f;
-      const float kk2 = ki * ki, qk2 = qi * ki, sP = a.scale * sm.inv[kRp], sN = sm.inv[kRn];
+      const float kk2 = ki * ki, qk2 = qi * ki, sP = a.scale * iO * iE, sN = iY * iE;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -1528,7 +1549,7 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
           }
       mp = warp_max(mp);
       ma = warp_max(ma);
-      float frob = frob2.x + frob2.y;
+      float frob = (frob2.x + frob2.y) * iS * iD;
 #pragma unroll
       for (int w = 16; w; w >>= 1) frob += __shfl_xor_sync(kFull, frob, w);
       if (lane == 0) {
@@ -1616,8 +1637,8 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
       }
       __syncthreads();
       const uint32_t mPs = smem_u32(sm.mP), mAs = smem_u32(sm.mA);
-      // t_ += M B with M taken as stored (rows i) or transposed (rows j)
-      auto pairs = [&](uint32_t M, uint32_t B, bool trans) {
+      // x += M B with M taken as stored (rows i) or transposed (rows j)
+      auto pairs = [&](float (&x)[2][2][4], uint32_t M, uint32_t B, bool trans) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           uint32_t bb[4];
@@ -1631,36 +1652,36 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
               ldsm_t(fa, M + swz<128>(16 * kk + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1)));
             else
               ldsm(fa, M + swz<128>(m0 + (lane & 15), 2 * kk + (lane >> 4)));
-            mma_h(t_[mt][0], fa, bb[0], bb[1]);
-            mma_h(t_[mt][1], fa, bb[2], bb[3]);
+            mma_h(x[mt][0], fa, bb[0], bb[1]);
+            mma_h(x[mt][1], fa, bb[2], bb[3]);
           }
         }
       };
-      auto clear = [&]() {
+      auto clear = [&](float (&x)[2][2][4]) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t_[mt][n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) x[mt][n][e] = 0.f;
       };
-      auto add = [&](float (&acc)[2][2][4], float f) {
+      auto add = [&](float (&acc)[2][2][4], const float (&x)[2][2][4], float f) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
-            set4(acc[mt][n], fma2(lo2(t_[mt][n]), both(f), lo2(acc[mt][n])), fma2(hi2(t_[mt][n]), both(f), hi2(acc[mt][n])));
+            set4(acc[mt][n], fma2(lo2(x[mt][n]), both(f), lo2(acc[mt][n])), fma2(hi2(x[mt][n]), both(f), hi2(acc[mt][n])));
       };
-      clear();
-      pairs(mPs, ks, false);
-      add(dq, inv_scale(pf) * ki);
-      clear();
-      pairs(mPs, qs, true);
-      add(dk, inv_scale(pf) * qi);
-      clear();
-      pairs(mAs, ks, false);
-      pairs(mAs, ks, true);
-      add(dk, inv_scale(af) * ki);
+      clear(t_[0]);
+      clear(t_[1]);
+      clear(t_[2]);
+      pairs(t_[0], mPs, ks, false);
+      pairs(t_[1], mPs, qs, true);
+      pairs(t_[2], mAs, ks, false);
+      pairs(t_[2], mAs, ks, true);
+      add(dq, t_[0], inv_scale(pf) * ki);
+      add(dk, t_[1], inv_scale(pf) * qi);
+      add(dk, t_[2], inv_scale(af) * ki);
       if (cur.hh == per - 1) {
         // lanes of a quad swap halves, so that each writes 8 bytes of one tile
         const bool odd = lane & 1;
