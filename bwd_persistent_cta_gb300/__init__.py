@@ -103,6 +103,7 @@ _SIGS = {
     "rnn_delta_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t)] + [_P] * 6),
     "rnn_delta_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t)] + [_P] * 11),
     "rnn_delta_step": (ctypes.c_int, [_P, ctypes.POINTER(rnn_delta_in_t), _P, ctypes.c_int, _P, _P, _P]),
+    "rnn_delta_sync_status": (ctypes.c_int, [_P, _P]),
     "rnn_delta_launch_count": (ctypes.c_uint64, [_P]),
     "rnn_norm_create": (ctypes.c_int, [ctypes.POINTER(rnn_norm_desc_t), ctypes.POINTER(_P)]),
     "rnn_norm_destroy": (ctypes.c_int, [_P]),
@@ -523,5 +524,6 @@ class RNN:
 
 from .lm import (  # noqa: E402
     BlockNorm, DeltaRule, rnn_delta_backward, rnn_delta_create, rnn_delta_destroy, rnn_delta_forward,
-    rnn_delta_get_sizes, rnn_delta_launch_count, rnn_delta_set_seq_lengths, rnn_delta_step, rnn_norm_backward,
+    rnn_delta_get_sizes, rnn_delta_launch_count, rnn_delta_set_seq_lengths, rnn_delta_step,
+    rnn_delta_sync_status, rnn_norm_backward,
     rnn_norm_create, rnn_norm_destroy, rnn_norm_forward, rnn_norm_get_sizes, rnn_norm_launch_count)

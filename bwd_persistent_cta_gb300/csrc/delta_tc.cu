@@ -31,6 +31,7 @@ namespace rnn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr uint64_t kScanTimeoutNs = 2000000000ull;     // of a wait for a chunk's copies
 
 // --- scales and fragments -----------------------------------------------------
 // The power of two that brings m to [2^13, 2^14), and its inverse.
@@ -100,25 +101,25 @@ __device__ __forceinline__ uint32_t pack_h(float2 x) { return pack_h(x.x, x.y); 
 
 // D = A B: the first product of a sum.
 __device__ __forceinline__ void mma_h0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_b(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_t(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -138,9 +139,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
 // Sixteen bytes, or zeros.
 __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool ok) {
   const int n = ok ? 16 : 0;
@@ -189,6 +187,18 @@ struct LaneOffsets {
     }
   }
 };
+// A lower triangular 64 x 64 tile in two fp16 parts, its ten 16 x 16 blocks (b, kb),
+// kb <= b, packed into 80 lines of 128 bytes: block row 1 in lines 16..31 (high |
+// low), block row 3 in 48..63 and 64..79, block row 2 in 32..47 with what does
+// not fit beside block row 0 in lines 0..15.  A block's rows are 16 lines from
+// tri_line, two pieces from tri_piece; pieces are exchanged by (line & 7).  10 KB
+// instead of 16 let two CTAs of a scan share an SM.
+__host__ __device__ constexpr int tri_line(int b, int kb, int part) {
+  return b < 2 ? 16 * b : b == 2 ? (part && kb ? 0 : 32) : 48 + 16 * part;
+}
+__host__ __device__ constexpr int tri_piece(int b, int kb, int part) {
+  return b == 0 ? 2 * part : b == 1 ? 2 * kb + 4 * part : b == 2 ? (part ? (kb ? 2 + 2 * kb : 6) : 2 * kb) : 2 * kb;
+}
 // rows n: tiles n0, n0 + 8 and k-step kk; rows k likewise (n0 a multiple of 16)
 template <int PITCH>
 __device__ __forceinline__ void scan_b_n(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
@@ -197,6 +207,14 @@ __device__ __forceinline__ void scan_b_n(uint32_t (&b)[4], uint32_t tile, const 
 template <int PITCH>
 __device__ __forceinline__ void scan_b_k(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
   ldsm_t(b, tile + o.k[PITCH != 128][(n0 >> 4) & 3] + 16 * kk * PITCH + (n0 >> 6) * 128);
+}
+
+// The same of a packed triangular tile: block row n0 / 16, k-step kk = its column (rows n), or the reverse (rows k).
+__device__ __forceinline__ void scan_tri_n(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk, int part) {
+  ldsm(b, tile + o.n[0][tri_piece(n0 >> 4, kk, part) >> 1] + tri_line(n0 >> 4, kk, part) * 128);
+}
+__device__ __forceinline__ void scan_tri_k(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk, int part) {
+  ldsm_t(b, tile + o.k[0][tri_piece(kk, n0 >> 4, part) >> 1] + tri_line(kk, n0 >> 4, part) * 128);
 }
 
 // Value column (of a warp's 16) behind row r of its fragments; row r + 8 is two
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   }
   const float pf = up_scale(block_max4(sm.red, 2, pm));
   if (tid == 0) sc[kScP] = inv_scale(pf);
-  unsigned char* po = static_cast<unsigned char*>(p.w.p) + bhc * (TRAIN ? 2 : 1) * kTile * 2;
+  unsigned char* po = static_cast<unsigned char*>(p.w.p) + bhc * kTri;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     if (n > 2 * warp + 1) continue;
@@ -478,8 +496,11 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
       const int i = 16 * warp + r + (e >> 1) * 8;
       uint32_t hi, lo;
       split(make_float2(qk[n][e] * pf, qk[n][e + 1] * pf), hi, lo);
-      *reinterpret_cast<uint32_t*>(po + swz<128>(i, n) + 2 * cc) = hi;
-      if (TRAIN) *reinterpret_cast<uint32_t*>(po + kTile * 2 + swz<128>(i, n) + 2 * cc) = lo;
+      auto at = [&](int part) {
+        return swz<128>(tri_line(warp, n >> 1, part) + (i & 15), tri_piece(warp, n >> 1, part) + (n & 1)) + 2 * cc;
+      };
+      *reinterpret_cast<uint32_t*>(po + at(0)) = hi;
+      if (TRAIN) *reinterpret_cast<uint32_t*>(po + at(1)) = lo;
     }
   }
 
@@ -552,7 +573,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
   if (!mine) return;
   const float xf = up_scale(fmaxf(sm.red[3][2 * which], sm.red[3][2 * which + 1]));
   if (t64 == 0) sc[which ? kScTB : kScTH] = inv_scale(xf);
-  unsigned char* xo = static_cast<unsigned char*>(which ? p.w.tb : p.w.th) + bhc * 2 * kTile * 2;
+  unsigned char* xo = static_cast<unsigned char*>(which ? p.w.tb : p.w.th) + bhc * kTri;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     if (wch > (n | 1)) continue;
@@ -562,8 +583,11 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
     split(mul2(make_float2(u.z, u.w), both(xf)), hi.y, lo.y);
     split(mul2(make_float2(w.x, w.y), both(xf)), hi.z, lo.z);
     split(mul2(make_float2(w.z, w.w), both(xf)), hi.w, lo.w);
-    *reinterpret_cast<uint4*>(xo + swz<128>(wi + 8 * n, wch)) = hi;
-    *reinterpret_cast<uint4*>(xo + kTile * 2 + swz<128>(wi + 8 * n, wch)) = lo;
+    auto at = [&](int part) {
+      return swz<128>(tri_line(n >> 1, wch >> 1, part) + wi + 8 * (n & 1), tri_piece(n >> 1, wch >> 1, part) + (wch & 1));
+    };
+    *reinterpret_cast<uint4*>(xo + at(0)) = hi;
+    *reinterpret_cast<uint4*>(xo + at(1)) = lo;
   }
 }
 
@@ -675,19 +699,24 @@ __device__ __forceinline__ void frag_a_hi(const Frag& x, int kk, float f, uint32
   hi[3] = pack_h(mul2(hi2(x[2 * kk + 1]), both(f)));
 }
 
-// A warp's [64 tokens][16 columns] slice of a bf16 row-major sequence: thread
+// A warp's [64 tokens][16 columns] slice of a chunk of a bf16 sequence: thread
 // (lane / 4, lane % 4) of tile n holds token 8 n + lane / 4, columns 4 (lane % 4)
 // .. + 3 (the columns of fragment rows 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c).
 struct Slice {
   uint2 v[8];
 };
-// ``p`` points at the thread's columns of the chunk's token lane / 4, ``step``
-// elements lead 8 tokens further; ``left`` tokens of the chunk are valid.
-__device__ __forceinline__ void slice_load(Slice& s, const __nv_bfloat16* p, int64_t step, int left, int lane) {
-  const int t = lane >> 2;
+// Rows of W slices in shared memory, 32 bytes further apart than they are long:
+// the four rows that half a warp reads at a time fall on different banks.
+template <int W>
+struct SeqTile {
+  static constexpr int PITCH = 32 * W + 32;
+  unsigned char row[kTc][PITCH];
+};
+template <int W>
+__device__ __forceinline__ void slice_load(Slice& s, const SeqTile<W>& t, int warp, int lane) {
+  const unsigned char* p = t.row[lane >> 2] + 32 * warp + 8 * (lane & 3);
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
-    s.v[n] = t + 8 * n < left ? *reinterpret_cast<const uint2*>(p + n * step) : make_uint2(0u, 0u);
+  for (int n = 0; n < 8; ++n) s.v[n] = *reinterpret_cast<const uint2*>(p + 8 * n * SeqTile<W>::PITCH);
 }
 // Fragment tile n (fp32) of a slice.
 __device__ __forceinline__ void slice_frag(const Slice& s, int n, float2& lo, float2& hi) {
@@ -695,15 +724,66 @@ __device__ __forceinline__ void slice_frag(const Slice& s, int n, float2& lo, fl
   hi = unpack_b(transpose8(s.v[n].y));
 }
 
-// Copies BYTES of a tile, as it is, by the CTA's NT threads.
-template <int BYTES, int NT>
-__device__ __forceinline__ void tile_copy(uint32_t dst, const void* src) {
-  const char* s = static_cast<const char*>(src) + threadIdx.x * 16;
-  dst += threadIdx.x * 16;
+// A chunk's tiles arrive by bulk copies that one thread issues and an mbarrier
+// counts, its rows of a sequence by one 16-byte copy in four a thread: loads into
+// registers, with the few scoreboards a warp has, would hold up the shared memory
+// reads issued after them.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+// What one chunk of a scan reads: the tiles of prep and W slices of a sequence.
+template <int DK, int W>
+struct ScanStage {
+  unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[kTri], P[kTri];
+  float sc[kSc];
+  SeqTile<W> x;
+};
+template <int DK, int W>
+struct alignas(128) ScanSmem {
+  ScanStage<DK, W> st[2];
+  uint64_t full[2];
+};
+struct ScanSource {
+  const char *k, *q, *t, *p, *sc;        // of chunk 0
+  const __nv_bfloat16* x;                // this thread's piece of the first 16 tokens
+  int64_t x_step;                        // elements 16 tokens further
+};
+// By every thread, once all have left the stage.  ``left`` tokens of the sequence
+// start here; rows beyond them are zeros.
+template <int DK, int W>
+__device__ __forceinline__ void scan_fetch(ScanStage<DK, W>& st, uint64_t* bar, const ScanSource& src, int c, int left) {
+  if (threadIdx.x == 0) {
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar, 2 * kTc * DK * 2 + 2 * kTri + kSc * 4);
+    bulk_copy(smem_u32(st.K), src.k + static_cast<int64_t>(c) * kTc * DK * 2, kTc * DK * 2, bar);
+    bulk_copy(smem_u32(st.Q), src.q + static_cast<int64_t>(c) * kTc * DK * 2, kTc * DK * 2, bar);
+    bulk_copy(smem_u32(st.T), src.t + static_cast<int64_t>(c) * kTri, kTri, bar);
+    bulk_copy(smem_u32(st.P), src.p + static_cast<int64_t>(c) * kTri, kTri, bar);
+    bulk_copy(smem_u32(st.sc), src.sc + static_cast<int64_t>(c) * kSc * 4, kSc * 4, bar);
+  }
+  const int t = threadIdx.x / (2 * W), ch = threadIdx.x % (2 * W);
+  const __nv_bfloat16* x = src.x + 4 * c * src.x_step;
+  const uint32_t dst = smem_u32(st.x.row[t]) + 16 * ch;
 #pragma unroll
-  for (int i = 0; i < BYTES / (NT * 16); ++i) cp16(dst + i * NT * 16, s + i * NT * 16);
-  if (BYTES % (NT * 16) && threadIdx.x * 16 < BYTES % (NT * 16))
-    cp16(dst + BYTES / (NT * 16) * NT * 16, s + BYTES / (NT * 16) * NT * 16);
+  for (int i = 0; i < 4; ++i) {
+    const bool ok = t + 16 * i < left;
+    cp16_or_zero(dst + i * 16 * SeqTile<W>::PITCH, x + (ok ? i * src.x_step : 0), ok);
+  }
+  cp_commit();
+}
+// Waits for turn ``it`` of a scan; true when it did not come in time, for every
+// thread of the CTA.  Nobody reads the other stage any more then.
+__device__ __forceinline__ bool scan_arrive(uint64_t* full, int it, unsigned int* status) {
+  cp_wait<0>();
+  const bool late = !mbar_wait(&full[it & 1], (it >> 1) & 1, kScanTimeoutNs);
+  if (!__syncthreads_or(late)) return false;
+  // a copy that is still under way keeps the CTA for as long again
+  if (threadIdx.x == 0) {
+    atomicCAS(status, 0u, static_cast<unsigned int>(RNN_TIMEOUT));
+    mbar_wait(&full[it & 1], (it >> 1) & 1, kScanTimeoutNs);
+  }
+  return true;
 }
 
 // Z = S X^T over the key columns, X = K16 ([16][64 tokens]), from both parts of
@@ -787,7 +867,9 @@ __device__ __forceinline__ void frag_store_half(const Frag& x, float f, __half* 
     *reinterpret_cast<uint2*>(p + 8 * n * pitch) =
         make_uint2(transpose8(pack_h(mul2(lo2(x[n]), both(f)))), transpose8(pack_h(mul2(hi2(x[n]), both(f)))));
 }
-// Writes a fragment to a dense bf16 sequence, addressed as in slice_load.
+// Writes a fragment to a dense bf16 sequence: ``p`` points at the thread's columns
+// of the chunk's token lane / 4, ``step`` elements lead 8 tokens further, and
+// ``left`` tokens of the sequence start here.
 __device__ __forceinline__ void frag_store_seq(const Frag& x, __nv_bfloat16* p, int64_t step, int left, int lane) {
   const int t = lane >> 2;
 #pragma unroll
@@ -805,18 +887,11 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16* base, const DeltaArgs& 
 // ---------------------------------------------------------------------------
 // the forward scan
 // ---------------------------------------------------------------------------
-template <int DK>
-struct FwdStage {
-  unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[2][kTile * 2], P[kTile * 2];
-  float sc[kSc];
-};
-
 // W warps of one value head, 16 value columns each.
 template <int DK, bool TRAIN, int W>
 __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArgs p) {
-  constexpr int NT = 32 * W;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  FwdStage<DK>* st = reinterpret_cast<FwdStage<DK>*>(smem_raw);
+  ScanSmem<DK, W>& sm = *reinterpret_cast<ScanSmem<DK, W>*>(smem_raw);
   const DeltaArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = a.Dv / (16 * W);
@@ -830,26 +905,29 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
   const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
   const int64_t s_off = (bh * a.Dv + dv0) * DK;
-  // token strides, and this thread's place in the first chunk
-  const int64_t ts_ = a.bfirst ? 1 : a.B, t_first = a.row(b, lane >> 2);
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0 + 4 * (lane & 3);
+  const int64_t ts_ = a.bfirst ? 1 : a.B;           // rows from token to token
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + static_cast<int64_t>(h) * a.Dv + dv0;
-  const int64_t v_step = 8 * ts_ * a.v_row, o_step = 8 * ts_ * o_row;
-  v += t_first * a.v_row;
-  __nv_bfloat16* ow = o + t_first * o_row + 4 * (lane & 3);
+  const int64_t o_step = 8 * ts_ * o_row;
+  __nv_bfloat16* ow = o + a.row(b, lane >> 2) * o_row + 4 * (lane & 3);
   LaneOffsets off;
   off.init(DK * 2, lane);
+  ScanSource src;
+  src.k = static_cast<const char*>(p.w.k16) + bk * nc * kTc * DK * 2;
+  src.q = static_cast<const char*>(p.w.q16) + bk * nc * kTc * DK * 2;
+  src.t = static_cast<const char*>(p.w.th) + bh * nc * kTri;
+  src.p = static_cast<const char*>(p.w.p) + bh * nc * kTri;
+  src.sc = reinterpret_cast<const char*>(p.w.sc) + bh * nc * kSc * 4;
+  src.x = static_cast<const __nv_bfloat16*>(a.v) + a.row(b, threadIdx.x / (2 * W)) * a.v_row + static_cast<int64_t>(h) * a.Dv +
+          grp * 16 * W + 8 * (threadIdx.x % (2 * W));
+  src.x_step = 16 * ts_ * a.v_row;
 
-  auto fetch = [&](int c) {
-    FwdStage<DK>& s = st[c & 1];
-    tile_copy<kTc * DK * 2, NT>(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2);
-    tile_copy<kTc * DK * 2, NT>(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2);
-    tile_copy<kTile * 4, NT>(smem_u32(s.T), static_cast<const char*>(p.w.th) + (bh * nc + c) * kTile * 4);
-    tile_copy<kTile * 2, NT>(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * (TRAIN ? 4 : 2));
-    tile_copy<kSc * 4, NT>(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc);
-    cp_commit();
-  };
-
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full[0], 1);
+    mbar_init(&sm.full[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ncb > 0) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, 0, len);
   State<DK> S;
   if (p.s_in) {
     state_load<DK>(S, p.s_in + s_off, lane);
@@ -859,16 +937,10 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
   }
-  Slice vs;
-  if (ncb > 0) {
-    fetch(0);
-    slice_load(vs, v, v_step, len, lane);
-  }
   for (int c = 0; c < ncb; ++c) {
-    cp_wait<0>();
-    __syncthreads();                       // chunk c is here, and nobody reads the other stage
-    if (c + 1 < ncb) fetch(c + 1);
-    const FwdStage<DK>& s = st[c & 1];
+    if (scan_arrive(sm.full, c, p.status)) return;
+    if (c + 1 < ncb) scan_fetch<DK, W>(sm.st[(c + 1) & 1], &sm.full[(c + 1) & 1], src, c + 1, len - (c + 1) * kTc);
+    const ScanStage<DK, W>& s = sm.st[c & 1];
     const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
 
     const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
@@ -880,6 +952,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
     state_times<DK, true>(S, sf, ks, qs, z, oq, off);
     // r = v - e^G S0 k
     const float zk = -si * s.sc[kScK], zq = si * s.sc[kScQ] * a.scale;
+    Slice vs;
+    slice_load<W>(vs, s.x, warp, lane);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       const float2 eg = pair_of(s.sc, n, lane), ek = mul2(eg, both(zk)), eq = mul2(eg, both(zq));
@@ -888,8 +962,6 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
       set4(z[n], fma2(lo2(z[n]), ek, lo), fma2(hi2(z[n]), ek, hi));
       set4(oq[n], mul2(lo2(oq[n]), eq), mul2(hi2(oq[n]), eq));
     }
-    v += 8 * v_step;
-    if (c + 1 < ncb) slice_load(vs, v, v_step, len - (c + 1) * kTc, lane);
     // e = r + (T - I) r: the identity stays in fp32
     const float rf = up_scale(frag_max(z));
 #pragma unroll
@@ -899,8 +971,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
 #pragma unroll
       for (int n = 2 * kk; n < 8; n += 2) {     // j <= i
         uint32_t bh_[4], bl_[4];
-        scan_b_n<128>(bh_, ts, off, 8 * n, kk);
-        scan_b_n<128>(bl_, ts + kTile * 2, off, 8 * n, kk);
+        scan_tri_n(bh_, ts, off, 8 * n, kk, 0);
+        scan_tri_n(bl_, ts, off, 8 * n, kk, 1);
         if (kk == 0) {
           mma_h0(acc[n], hi, bh_[0], bh_[1]);
           mma_h0(acc[n + 1], hi, bh_[2], bh_[3]);
@@ -931,7 +1003,7 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
 #pragma unroll
       for (int n = 2 * kk; n < 8; n += 2) {
         uint32_t bb[4];
-        scan_b_n<128>(bb, ps, off, 8 * n, kk);
+        scan_tri_n(bb, ps, off, 8 * n, kk, 0);
         if (kk == 0) {
           mma_h0(acc[n], hi, bb[0], bb[1]);
           mma_h0(acc[n + 1], hi, bb[2], bb[3]);
@@ -955,7 +1027,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
 
 // Warps of a scan CTA (16 value columns each): as many as share the chunk's
-// tiles without leaving SMs idle.
+// tiles without leaving SMs idle.  A chunk takes a lone pair of warps 3.3 us, four
+// a SM 4.2 and eight 7.2, so a half-filled GPU is better used by small CTAs.
 int scan_warps(const DeltaArgs& a, int num_sms) {
   const int n = a.Dv / 16;
   for (int w = 8; w > 2; w >>= 1)
@@ -971,16 +1044,16 @@ int set_smem(F* f, int bytes) {
 template <int DK, bool TRAIN>
 int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   const int nc = (t.a.T + kTc - 1) / kTc;
-  const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>);
+  const int psm = sizeof(PrepSmem<DK>);
   delta_prep_kernel<DK, TRAIN><<<static_cast<unsigned>(static_cast<int64_t>(nc) * t.a.Hv * t.a.B), 128, psm, s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
   const int w = scan_warps(t.a, t.num_sms);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
-  if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, fsm, s>>>(t);
-  else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, fsm, s>>>(t);
-  else delta_scan_fwd_kernel<DK, TRAIN, 2><<<grid, 64, fsm, s>>>(t);
+  if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
+  else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
+  else delta_scan_fwd_kernel<DK, TRAIN, 2><<<grid, 64, sizeof(ScanSmem<DK, 2>), s>>>(t);
   rc = check_launch();
   if (!rc) ++*launches;
   return rc;
@@ -992,17 +1065,10 @@ int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
 // The same ownership for the state gradient, chunks in reverse:
 //   du = P^T do + e^{G_C - G} dS1 k          y = (I + beta A)^-T du
 //   dS0 = e^{G_C} dS1 + (scale e^G do) q^T - (e^G beta y) k^T,   dv = beta y
-template <int DK>
-struct BwdStage {
-  unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[2][kTile * 2], P[2][kTile * 2];
-  float sc[kSc];
-};
-
 template <int DK, int W>
 __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwdArgs p) {
-  constexpr int NT = 32 * W;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  BwdStage<DK>* st = reinterpret_cast<BwdStage<DK>*>(smem_raw);
+  ScanSmem<DK, W>& sm = *reinterpret_cast<ScanSmem<DK, W>*>(smem_raw);
   const DeltaArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = a.Dv / (16 * W);
@@ -1017,23 +1083,27 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
   const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
   const int64_t s_off = (bh * a.Dv + dv0) * DK;
   const int64_t ts_ = a.bfirst ? 1 : a.B, o_step = 8 * ts_ * o_row;
-  const int64_t last = a.row(b, (lane >> 2) + (ncb > 0 ? ncb - 1 : 0) * kTc) * o_row + static_cast<int64_t>(h) * a.Dv + dv0 +
-                       4 * (lane & 3);
-  const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(p.dout) + last;
-  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + last;
+  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0 + 4 * (lane & 3) +
+                      a.row(b, (lane >> 2) + (ncb > 0 ? ncb - 1 : 0) * kTc) * o_row;
   LaneOffsets off;
   off.init(DK * 2, lane);
+  ScanSource src;
+  src.k = static_cast<const char*>(p.w.k16) + bk * nc * kTc * DK * 2;
+  src.q = static_cast<const char*>(p.w.q16) + bk * nc * kTc * DK * 2;
+  src.t = static_cast<const char*>(p.w.tb) + bh * nc * kTri;
+  src.p = static_cast<const char*>(p.w.p) + bh * nc * kTri;
+  src.sc = reinterpret_cast<const char*>(p.w.sc) + bh * nc * kSc * 4;
+  src.x = static_cast<const __nv_bfloat16*>(p.dout) + a.row(b, threadIdx.x / (2 * W)) * o_row + static_cast<int64_t>(h) * a.Dv +
+          grp * 16 * W + 8 * (threadIdx.x % (2 * W));
+  src.x_step = 16 * ts_ * o_row;
 
-  auto fetch = [&](int c) {
-    BwdStage<DK>& s = st[c & 1];
-    tile_copy<kTc * DK * 2, NT>(smem_u32(s.K), static_cast<const char*>(p.w.k16) + (bk * nc + c) * kTc * DK * 2);
-    tile_copy<kTc * DK * 2, NT>(smem_u32(s.Q), static_cast<const char*>(p.w.q16) + (bk * nc + c) * kTc * DK * 2);
-    tile_copy<kTile * 4, NT>(smem_u32(s.T), static_cast<const char*>(p.w.tb) + (bh * nc + c) * kTile * 4);
-    tile_copy<kTile * 4, NT>(smem_u32(s.P), static_cast<const char*>(p.w.p) + (bh * nc + c) * kTile * 4);
-    tile_copy<kSc * 4, NT>(smem_u32(s.sc), p.w.sc + (bh * nc + c) * kSc);
-    cp_commit();
-  };
-
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full[0], 1);
+    mbar_init(&sm.full[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ncb > 0) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, ncb - 1, len - (ncb - 1) * kTc);
   State<DK> S;
   if (p.dsT) {
     state_load<DK>(S, p.dsT + s_off, lane);
@@ -1043,16 +1113,11 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
 #pragma unroll
       for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
   }
-  Slice ds;
-  if (ncb > 0) {
-    fetch(ncb - 1);
-    slice_load(ds, dout, o_step, len - (ncb - 1) * kTc, lane);
-  }
-  for (int c = ncb - 1; c >= 0; --c) {
-    cp_wait<0>();
-    __syncthreads();
-    if (c > 0) fetch(c - 1);
-    const BwdStage<DK>& s = st[c & 1];
+  for (int it = 0; it < ncb; ++it) {
+    const int c = ncb - 1 - it;
+    if (scan_arrive(sm.full, it, p.status)) return;
+    if (c > 0) scan_fetch<DK, W>(sm.st[(it + 1) & 1], &sm.full[(it + 1) & 1], src, c - 1, kTc);
+    const ScanStage<DK, W>& s = sm.st[it & 1];
     const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
 
     const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
@@ -1061,6 +1126,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
     Frag z, acc;
     state_times<DK, false>(S, sf, ks, ks, z, z, off);
     // P^T do: do is exact in fp16 once scaled
+    Slice ds;
+    slice_load<W>(ds, s.x, warp, lane);
     float dm = 0.f;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -1079,8 +1146,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
 #pragma unroll
       for (int n = 0; n <= 2 * kk; n += 2) {      // j <= i
         uint32_t bh_[4], bl_[4];
-        scan_b_k<128>(bh_, ps, off, 8 * n, kk);
-        scan_b_k<128>(bl_, ps + kTile * 2, off, 8 * n, kk);
+        scan_tri_k(bh_, ps, off, 8 * n, kk, 0);
+        scan_tri_k(bl_, ps, off, 8 * n, kk, 1);
         if (n == 2 * kk) {
           mma_h0(acc[n], ad, bh_[0], bh_[1]);
           mma_h0(acc[n + 1], ad, bh_[2], bh_[3]);
@@ -1107,8 +1174,8 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
 #pragma unroll
       for (int n = 0; n <= 2 * kk; n += 2) {
         uint32_t bh_[4], bl_[4];
-        scan_b_k<128>(bh_, ts, off, 8 * n, kk);
-        scan_b_k<128>(bl_, ts + kTile * 2, off, 8 * n, kk);
+        scan_tri_k(bh_, ts, off, 8 * n, kk, 0);
+        scan_tri_k(bl_, ts, off, 8 * n, kk, 1);
         if (n == 2 * kk) {
           mma_h0(acc[n], hi, bh_[0], bh_[1]);
           mma_h0(acc[n + 1], hi, bh_[2], bh_[3]);
@@ -1140,8 +1207,6 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
       set4(acc[n], mul2(lo, es), mul2(hi, es));
       set4(z[n], mul2(lo2(z[n]), em), mul2(hi2(z[n]), em));
     }
-    dout -= 8 * o_step;
-    if (c > 0) slice_load(ds, dout, o_step, kTc, lane);
     state_update<DK>(S, s.sc[kScEnd], acc, af, qs, inv_scale(af) * s.sc[kScQ], off);
     state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
   }
@@ -1169,7 +1234,7 @@ struct GradSmem {
     unsigned char S0[64 * DK * 2], dS[64 * DK * 2];              // [64 value columns][Dk]
   } st[2];
   unsigned char K[2][kTc * DK * 2], Q[2][kTc * DK * 2];
-  unsigned char mP[kTile * 2], mA[kTile * 2];
+  unsigned char mP[kTc * 128], mA[kTc * 128];
   float eG[kTc], eE[kTc], beta[kTc], G[kTc];
   // per 16 value columns: the fp16 pair that brings S0, dS1, e, y to the head's
   // scale, the fp32 factor that does so from bf16 for do; and the head's inverse scales
@@ -1712,12 +1777,12 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
 
 template <int DK>
 int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
-  const int bsm = 2 * sizeof(BwdStage<DK>), gsm = sizeof(GradSmem<DK>);
+  const int gsm = sizeof(GradSmem<DK>);
   const int w = scan_warps(t.a, t.num_sms);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
-  if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, bsm, s>>>(t);
-  else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, bsm, s>>>(t);
-  else delta_scan_bwd_kernel<DK, 2><<<grid, 64, bsm, s>>>(t);
+  if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
+  else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
+  else delta_scan_bwd_kernel<DK, 2><<<grid, 64, sizeof(ScanSmem<DK, 2>), s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
@@ -1728,16 +1793,17 @@ int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   return rc;
 }
 
+template <int DK, int W>
+int init_scans() {
+  const int smem = sizeof(ScanSmem<DK, W>);
+  return set_smem(delta_scan_fwd_kernel<DK, false, W>, smem) || set_smem(delta_scan_fwd_kernel<DK, true, W>, smem) ||
+         set_smem(delta_scan_bwd_kernel<DK, W>, smem);
+}
 template <int DK>
 int init() {
-  const int psm = sizeof(PrepSmem<DK>), fsm = 2 * sizeof(FwdStage<DK>), bsm = 2 * sizeof(BwdStage<DK>),
-            gsm = sizeof(GradSmem<DK>);
+  const int psm = sizeof(PrepSmem<DK>), gsm = sizeof(GradSmem<DK>);
   return set_smem(delta_prep_kernel<DK, false>, psm) || set_smem(delta_prep_kernel<DK, true>, psm) ||
-                 set_smem(delta_scan_fwd_kernel<DK, false, 2>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 2>, fsm) ||
-                 set_smem(delta_scan_fwd_kernel<DK, false, 4>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 4>, fsm) ||
-                 set_smem(delta_scan_fwd_kernel<DK, false, 8>, fsm) || set_smem(delta_scan_fwd_kernel<DK, true, 8>, fsm) ||
-                 set_smem(delta_scan_bwd_kernel<DK, 2>, bsm) || set_smem(delta_scan_bwd_kernel<DK, 4>, bsm) ||
-                 set_smem(delta_scan_bwd_kernel<DK, 8>, bsm) || set_smem(delta_grad_kernel<DK>, gsm)
+                 init_scans<DK, 2>() || init_scans<DK, 4>() || init_scans<DK, 8>() || set_smem(delta_grad_kernel<DK>, gsm)
              ? RNN_CUDA_ERROR
              : 0;
 }

@@ -9,9 +9,9 @@
 //            fragments (position 32 m + 8 i + 2 c + w holds column
 //            32 m + 8 c + 2 i + w), so that a thread's state columns are
 //            eight neighbours
-//   TH       [bh][chunk][2][64][64]  (I + A diag(beta))^-1 - I, high and low part
-//   TB       [bh][chunk][2][64][64]  (I + diag(beta) A)^-1 - I   (training)
-//   P        [bh][chunk][2][64][64]  scale D * Q K^T; the low part in training
+//   TH       [bh][chunk] packed tile (tri_line) of (I + A diag(beta))^-1 - I
+//   TB       [bh][chunk] packed tile of (I + diag(beta) A)^-1 - I   (training)
+//   P        [bh][chunk] packed tile of scale D * Q K^T; the low part in training
 //   SC       [bh][chunk][kSc]        per-token factors and tile scales
 // Training, kept for the backward:
 //   S0       [bh][chunk][Dv][Dk] fp16, one scale per 16 value columns
@@ -25,7 +25,7 @@
 namespace rnn {
 
 constexpr int kTc = 64;              // tokens a chunk
-constexpr int kTile = kTc * kTc;     // elements of a 64 x 64 tile
+constexpr int kTri = 80 * 128;       // bytes of a packed triangular tile
 // SC: [0,64) e^G, [64,128) e^{G_C - G}, [128,192) beta, [192,256) G, then
 enum { kScK = 256, kScQ, kScTH, kScTB, kScP, kScEnd, kScBu, kScBy, kScBo, kSc = 268 };
 
@@ -42,6 +42,7 @@ struct DeltaTcArgs {
   const float* s_in;
   float* s_out;
   void* o;
+  unsigned int* status;              // first rnn_status_t a kernel reports
   int train, num_sms;
 };
 // Once per device and handle: the kernels' shared memory limits.
@@ -58,6 +59,7 @@ struct DeltaTcBwdArgs {
   void *ds1, *y;
   float *ds1_scale, *y_scale, *do_scale;   // do_scale: of the fp16 copy of do, made where it is used
   void *dq, *dk, *dv, *dg, *dbeta;
+  unsigned int* status;
   int num_sms;
 };
 int launch_delta_tc_backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches);

@@ -22,6 +22,7 @@ struct rnn_delta_s {
   size_t es;
   int* d_len;
   int has_len;
+  unsigned int* status;        // device word
   uint64_t launches;
   // byte offsets.  Forward workspace (tensor cores): the tiles of prep; a
   // training forward keeps all of them but th in the reserve
@@ -109,17 +110,17 @@ void delta_layout(rnn_delta_s* h) {
   } else {
     const size_t nc = (d.seq_len + kTc - 1) / kTc;
     const size_t vc = bh * nc, kc = static_cast<size_t>(d.batch) * d.heads_k * nc;
-    const size_t keys = kc * kTc * d.dim_k * 2, tile = vc * kTile * 2, sc = vc * kSc * 4;
+    const size_t keys = kc * kTc * d.dim_k * 2, tile = vc * kTri, sc = vc * kSc * 4;
     const size_t states = vc * d.dim_v * d.dim_k * 2, vectors = vc * kTc * d.dim_v * 2, scales = vc * (d.dim_v / 16) * 4;
-    h->w_th = w.take(2 * tile);
+    h->w_th = w.take(tile);
     h->w_k16 = w.take(keys);
     h->w_q16 = w.take(keys);
     h->w_p = w.take(tile);
     h->w_sc = w.take(sc);
     h->r_k16 = r.take(keys);
     h->r_q16 = r.take(keys);
-    h->r_tb = r.take(2 * tile);
-    h->r_p = r.take(2 * tile);
+    h->r_tb = r.take(tile);
+    h->r_p = r.take(tile);
     h->r_sc = r.take(sc);
     h->r_s0 = r.take(states);
     h->r_s0s = r.take(scales);
@@ -242,6 +243,15 @@ rnn_status_t rnn_delta_create(const rnn_delta_desc_t* desc, rnn_delta_t* out) {
     delete h;
     return RNN_CUDA_ERROR;
   }
+  if (cudaMalloc(&h->status, sizeof(unsigned int)) != cudaSuccess) {
+    delete h;
+    return RNN_CUDA_ERROR;
+  }
+  if (cudaMemset(h->status, 0, sizeof(unsigned int)) != cudaSuccess) {
+    cudaFree(h->status);
+    delete h;
+    return RNN_CUDA_ERROR;
+  }
   delta_layout(h);
   *out = h;
   return RNN_OK;
@@ -251,6 +261,7 @@ rnn_status_t rnn_delta_destroy(rnn_delta_t h) {
   if (!h) return RNN_OK;
   DeviceGuard dg(h->device);
   if (h->d_len) cudaFree(h->d_len);
+  cudaFree(h->status);
   delete h;
   return RNN_OK;
 }
@@ -299,6 +310,7 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
     t.s_in = s0;
     t.s_out = sT;
     t.o = o;
+    t.status = h->status;
     t.train = reserve != nullptr;
     t.num_sms = h->num_sms;
     int n = 0;
@@ -344,6 +356,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
     t.y = at<void>(workspace, h->b_y);
     t.y_scale = at<float>(workspace, h->b_ys);
     t.do_scale = at<float>(workspace, h->b_dos);
+    t.status = h->status;
     t.dq = dq; t.dk = dk; t.dv = dv; t.dg = dg; t.dbeta = dbeta;
     t.num_sms = h->num_sms;
     int n = 0;
@@ -391,6 +404,20 @@ rnn_status_t rnn_delta_step(rnn_delta_t h, const rnn_delta_in_t* in, float* stat
   const int e = launch_delta_recur(r, h->bf16, static_cast<cudaStream_t>(stream));
   if (!e) ++h->launches;
   return static_cast<rnn_status_t>(e);
+}
+
+rnn_status_t rnn_delta_sync_status(rnn_delta_t h, void* stream) {
+  if (!h) return RNN_BAD_PARAM;
+  DeviceGuard dg(h->device);
+  if (!dg.ok) return RNN_CUDA_ERROR;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  unsigned int v = 0;
+  if (cudaMemcpyAsync(&v, h->status, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return RNN_CUDA_ERROR;
+  if (v && (cudaMemsetAsync(h->status, 0, sizeof v, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
+    return RNN_CUDA_ERROR;
+  return static_cast<rnn_status_t>(v);
 }
 
 uint64_t rnn_delta_launch_count(rnn_delta_t h) { return h ? h->launches : 0; }

@@ -55,6 +55,10 @@ def rnn_delta_step(handle, inputs: rnn_delta_in_t, state, num_slots, slots, o, s
     return lib().rnn_delta_step(handle, ctypes.byref(inputs), state, num_slots, slots, o, stream)
 
 
+def rnn_delta_sync_status(handle, stream=None) -> int:
+    return lib().rnn_delta_sync_status(handle, stream)
+
+
 def rnn_delta_launch_count(handle) -> int:
     return int(lib().rnn_delta_launch_count(handle))
 
@@ -233,6 +237,10 @@ class DeltaRule(_Op):
 
     def launches(self) -> int:
         return rnn_delta_launch_count(self.handle)
+
+    def sync(self, stream=None):
+        """Wait for the stream and raise what a kernel reported."""
+        self._check(rnn_delta_sync_status(self.handle, self._on(stream)), "rnn_delta_sync_status")
 
     def set_seq_lengths(self, lengths):
         """Valid tokens per sequence (batch ints), or None for full length."""

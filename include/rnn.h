@@ -356,9 +356,10 @@ rnn_status_t rnn_noalloc_status(void* stream);
  * q, k, v, g, beta, o and their gradients is desc.dtype.  States (s0, sT, the
  * pool of rnn_delta_step, ds0, dsT) are fp32 [B, heads_v, dim_v, dim_k], and
  * every sum and state is held in fp32.
- * The conventions at the top of this file hold, with one exception: no kernel
- * of these operators waits for another CTA, so they need no resident grid and
- * report nothing to a status word. */
+ * The conventions at the top of this file hold.  No kernel of these operators
+ * waits for another CTA, so they need no resident grid and may overlap other
+ * kernels; the chunk kernels' waits for their own copies are bounded all the
+ * same (rnn_delta_sync_status). */
 typedef struct {
   int batch;           /* B >= 1                                                       */
   int seq_len;         /* T >= 1                                                       */
@@ -437,6 +438,11 @@ rnn_status_t rnn_delta_backward(rnn_delta_t handle, const rnn_delta_in_t* in, co
  *   o      as rnn_delta_forward. */
 rnn_status_t rnn_delta_step(rnn_delta_t handle, const rnn_delta_in_t* in, float* state, int num_slots,
                             const int* slots, void* o, void* stream);
+
+/* Synchronise ``stream`` and return (then clear) the handle's device status
+ * word: RNN_OK, RNN_TIMEOUT when a bounded wait gave up (the call's outputs are
+ * then invalid), or RNN_CUDA_ERROR. */
+rnn_status_t rnn_delta_sync_status(rnn_delta_t handle, void* stream);
 
 /* Number of kernels this handle has launched since it was created. */
 uint64_t rnn_delta_launch_count(rnn_delta_t handle);
