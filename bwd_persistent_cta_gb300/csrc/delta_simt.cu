@@ -73,25 +73,84 @@ __device__ __forceinline__ void store_state(float* p, const float (&v)[VPL]) {
   }
 }
 
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+// Tokens on their way to a recurrence CTA: kAhead of them a stage, two stages
+// (at most 34 KB).  A token's chain of dependent arithmetic is shorter than one
+// trip to memory, so what it reads has to be asked for many tokens earlier.
+template <typename T, int VPL, int R>
+struct TokenStage {
+  static constexpr int kAhead = sizeof(T) * VPL > 16 ? 8 : 16;
+  T k[kAhead][32 * VPL], q[kAhead][32 * VPL], x[kAhead][kWarps * R];   // x: v, or do
+  float g[kAhead], beta[kAhead];
+};
+struct TokenSource {
+  const void *k, *q, *x;       // of this CTA's heads and value columns, token 0
+  const void *g, *beta;
+  int64_t k_step, q_step, x_step, g_step, beta_step;   // elements from token to token
+  int dk, cols;                // valid columns of k / q and of x
+};
+// Asks for tokens t0, t0 + dir, ... (those in [0, len)) into st; the scalars of
+// this thread's token come back in gb.
+template <typename T, int VPL, int R>
+__device__ __forceinline__ float2 stage_fetch(TokenStage<T, VPL, R>& st, const TokenSource& s, int t0, int dir, int len) {
+  constexpr int E = 16 / sizeof(T), kAhead = TokenStage<T, VPL, R>::kAhead;
+  const int per = s.dk / E;
+  for (int i = threadIdx.x; i < kAhead * per; i += kWarps * 32) {
+    const int n = i / per, c = (i - n * per) * E, t = t0 + dir * n;
+    const bool ok = t >= 0 && t < len;
+    copy16(&st.k[n][c], static_cast<const T*>(s.k) + (ok ? t * s.k_step + c : 0), ok);
+    copy16(&st.q[n][c], static_cast<const T*>(s.q) + (ok ? t * s.q_step + c : 0), ok);
+  }
+  constexpr int XP = kWarps * R / E;
+  for (int i = threadIdx.x; i < kAhead * XP; i += kWarps * 32) {
+    const int n = i / XP, c = (i % XP) * E, t = t0 + dir * n;
+    const bool ok = t >= 0 && t < len && c < s.cols;
+    copy16(&st.x[n][c], static_cast<const T*>(s.x) + (ok ? t * s.x_step + c : 0), ok);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  float2 gb = make_float2(0.f, 0.f);
+  const int t = t0 + dir * static_cast<int>(threadIdx.x);
+  if (threadIdx.x < kAhead && t >= 0 && t < len) {
+    gb.x = to_f<T>(static_cast<const T*>(s.g)[t * s.g_step]);
+    gb.y = to_f<T>(static_cast<const T*>(s.beta)[t * s.beta_step]);
+  }
+  return gb;
+}
+// Lets the tokens asked for last be read by the CTA.
+template <typename T, int VPL, int R>
+__device__ __forceinline__ void stage_ready(TokenStage<T, VPL, R>& st, float2 gb) {
+  if (threadIdx.x < TokenStage<T, VPL, R>::kAhead) {
+    st.g[threadIdx.x] = gb.x;
+    st.beta[threadIdx.x] = gb.y;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+}
+
 // The recurrence.  A warp owns R rows of one head's state (row = one value
 // column, all of Dk across the lanes, VPL elements each); rows are independent,
 // so there is nothing to exchange but the two dot products S k and S q inside
 // the warp.  Both are taken of the old state: S_t q = a (S q) + u (k . q).
-// One token costs the chain exp -> dot -> shuffles -> update; the next token's
-// rows are loaded meanwhile.
-template <typename T, int VPL, int R>
+// One token costs the chain exp -> dot -> shuffles -> update.  AHEAD: tokens come
+// through shared memory a stage early (sequences); otherwise each is loaded one
+// token early (the serving step, where the state is what takes time).
+template <typename T, int VPL, int R, bool AHEAD>
 __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRecurArgs r) {
+  constexpr int kAhead = TokenStage<T, VPL, R>::kAhead;
+  __shared__ __align__(16) TokenStage<T, VPL, R> st[AHEAD ? 2 : 1];
   const DeltaArgs& a = r.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (a.Dv + kWarps * R - 1) / (kWarps * R);
-  const int64_t bid = blockIdx.x;
-  const int grp = static_cast<int>(bid % groups);
-  const int h = static_cast<int>(bid / groups % a.Hv), b = static_cast<int>(bid / groups / a.Hv);
+  const int bid = blockIdx.x;
+  const int grp = bid % groups, h = bid / groups % a.Hv, b = bid / groups / a.Hv;
   const int dv0 = (grp * kWarps + warp) * R;
-  if (dv0 >= a.Dv) return;
   const int hk = h / (a.Hv / a.Hk);
   const int dk0 = lane * VPL;
-  const bool in = dk0 < a.Dk;
+  const bool mine = dv0 < a.Dv, in = mine && dk0 < a.Dk;
   int len = a.len ? a.len[b] : a.T;
   int64_t slot = b;
   bool live = true;
@@ -104,16 +163,24 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
   if (!live) len = 0;
   const int64_t head_elems = static_cast<int64_t>(a.Dv) * a.Dk;
   const int64_t s_off = (slot * a.Hv + h) * head_elems;
+  const int64_t ts = a.bfirst ? 1 : a.B, row0 = a.row(b, 0);      // rows from token to token
 
-  T* o = static_cast<T*>(r.o) + static_cast<int64_t>(h) * a.Dv + dv0;
   const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
-  const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.Dk + dk0;
-  const T* k = static_cast<const T*>(a.k) + static_cast<int64_t>(hk) * a.Dk + dk0;
-  const T* v = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * a.Dv + dv0;
-  const T* g = static_cast<const T*>(a.g) + h;
-  const T* be = static_cast<const T*>(a.beta) + h;
+  T* o = static_cast<T*>(r.o) + row0 * o_row + static_cast<int64_t>(h) * a.Dv + dv0;
+  TokenSource src;
+  src.k = static_cast<const T*>(a.k) + row0 * a.k_row + static_cast<int64_t>(hk) * a.Dk;
+  src.q = static_cast<const T*>(a.q) + row0 * a.q_row + static_cast<int64_t>(hk) * a.Dk;
+  src.x = static_cast<const T*>(a.v) + row0 * a.v_row + static_cast<int64_t>(h) * a.Dv + grp * kWarps * R;
+  src.g = static_cast<const T*>(a.g) + row0 * a.g_row + h;
+  src.beta = static_cast<const T*>(a.beta) + row0 * a.beta_row + h;
+  src.k_step = ts * a.k_row; src.q_step = ts * a.q_row; src.x_step = ts * a.v_row;
+  src.g_step = ts * a.g_row; src.beta_step = ts * a.beta_row;
+  src.dk = a.Dk;
+  src.cols = a.Dv - grp * kWarps * R;
   const bool vin = lane < R && dv0 + lane < a.Dv;   // this lane loads / stores value row dv0 + lane
 
+  float2 gb = make_float2(0.f, 0.f);
+  if (AHEAD && len > 0) gb = stage_fetch<T, VPL, R>(st[0], src, 0, 1, len);
   float S[R][VPL];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -121,31 +188,41 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
     load_vec<float, VPL>(r.s_in + s_off + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, S[i]);
   }
   float kc[VPL], qc[VPL], vc = 0.f, gc = 0.f, bc = 0.f;
-  if (len > 0) {
-    const int64_t row = a.row(b, 0);
-    load_vec<T, VPL>(k + row * a.k_row, in, kc);
-    load_vec<T, VPL>(q + row * a.q_row, in, qc);
-    vc = vin ? to_f<T>(v[row * a.v_row + lane]) : 0.f;
-    gc = to_f<T>(g[row * a.g_row]);
-    bc = to_f<T>(be[row * a.beta_row]);
-  }
+  float kn[VPL], qn[VPL], vn = 0.f, gn = 0.f, bn = 0.f;
+  auto direct = [&](int t) {
+    load_vec<T, VPL>(static_cast<const T*>(src.k) + t * src.k_step + dk0, in, kn);
+    load_vec<T, VPL>(static_cast<const T*>(src.q) + t * src.q_step + dk0, in, qn);
+    vn = vin ? to_f<T>(static_cast<const T*>(src.x)[t * src.x_step + warp * R + lane]) : 0.f;
+    gn = to_f<T>(static_cast<const T*>(src.g)[t * src.g_step]);
+    bn = to_f<T>(static_cast<const T*>(src.beta)[t * src.beta_step]);
+  };
+  if (!AHEAD && len > 0) direct(0);
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
   const int nc = (a.T + kSimtChunk - 1) / kSimtChunk;
   for (int t = 0; t < len; ++t) {
+    if (AHEAD) {
+      const int n = t % kAhead;
+      if (n == 0) {
+        stage_ready<T, VPL, R>(st[(t / kAhead) & 1], gb);      // and the other stage is free
+        if (t + kAhead < len) gb = stage_fetch<T, VPL, R>(st[(t / kAhead + 1) & 1], src, t + kAhead, 1, len);
+      }
+      const TokenStage<T, VPL, R>& s = st[(t / kAhead) & 1];
+      load_vec<T, VPL>(&s.k[n][dk0], in, kc);
+      load_vec<T, VPL>(&s.q[n][dk0], in, qc);
+      vc = vin ? to_f<T>(s.x[n][warp * R + lane]) : 0.f;
+      gc = s.g[n];
+      bc = s.beta[n];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
+      vc = vn; gc = gn; bc = bn;
+      if (t + 1 < len) direct(t + 1);
+    }
     if (r.ckpt && t % kSimtChunk == 0 && in) {
       float* c = r.ckpt + (bh * nc + t / kSimtChunk) * head_elems + dk0;
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, S[i]);
-    }
-    float kn[VPL], qn[VPL], vn = 0.f, gn = 0.f, bn = 0.f;
-    if (t + 1 < len) {
-      const int64_t row = a.row(b, t + 1);
-      load_vec<T, VPL>(k + row * a.k_row, in, kn);
-      load_vec<T, VPL>(q + row * a.q_row, in, qn);
-      vn = vin ? to_f<T>(v[row * a.v_row + lane]) : 0.f;
-      gn = to_f<T>(g[row * a.g_row]);
-      bn = to_f<T>(be[row * a.beta_row]);
     }
     const float al = expf(gc);
     float d[2 * R], kq = 0.f;
@@ -164,14 +241,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 #pragma unroll
     for (int w = 16; w; w >>= 1) kq += __shfl_xor_sync(kFull, kq, w);
     // lane i < R finishes value row dv0 + i
-    const int src = lane < R ? lane : 0;
-    const float sk = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * src);
-    const float sq = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * (R + src));
+    const int src_lane = lane < R ? lane : 0;
+    const float sk = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * src_lane);
+    const float sq = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * (R + src_lane));
     const float e = vc - al * sk;
     const float u = bc * e;
     if (vin) {
-      const int64_t row = a.row(b, t);
-      o[row * o_row + lane] = from_f<T>(a.scale * fmaf(al, sq, u * kq));
+      o[t * ts * o_row + lane] = from_f<T>(a.scale * fmaf(al, sq, u * kq));
       if (r.e) r.e[(bh * a.T + t) * a.Dv + dv0 + lane] = e;
     }
 #pragma unroll
@@ -180,12 +256,9 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 #pragma unroll
       for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(ui, kc[j], al * S[i][j]);
     }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
-    vc = vn; gc = gn; bc = bn;
   }
   for (int t = len; t < a.T; ++t)
-    if (vin) o[a.row(b, t) * o_row + lane] = from_f<T>(0.f);
+    if (vin) o[t * ts * o_row + lane] = from_f<T>(0.f);
   // a skipped sequence has no slot to write; one without tokens keeps its state
   if (r.s_out && live && in && !(len == 0 && r.s_out == r.s_in)) {
 #pragma unroll
@@ -198,59 +271,58 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 //   dS += scale do_t q_t^T;  y_t = dS k_t;  dS -= beta_t y_t k_t^T;  dS *= a_t.
 template <typename T, int VPL, int R>
 __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const DeltaRecurBwdArgs r) {
+  constexpr int kAhead = TokenStage<T, VPL, R>::kAhead;
+  __shared__ __align__(16) TokenStage<T, VPL, R> st[2];
   const DeltaArgs& a = r.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (a.Dv + kWarps * R - 1) / (kWarps * R);
-  const int64_t bid = blockIdx.x;
-  const int grp = static_cast<int>(bid % groups);
-  const int h = static_cast<int>(bid / groups % a.Hv), b = static_cast<int>(bid / groups / a.Hv);
+  const int bid = blockIdx.x;
+  const int grp = bid % groups, h = bid / groups % a.Hv, b = bid / groups / a.Hv;
   const int dv0 = (grp * kWarps + warp) * R;
-  if (dv0 >= a.Dv) return;
   const int hk = h / (a.Hv / a.Hk);
   const int dk0 = lane * VPL;
-  const bool in = dk0 < a.Dk;
+  const bool in = dv0 < a.Dv && dk0 < a.Dk;
   const int len = a.len ? a.len[b] : a.T;
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
   const int64_t head_elems = static_cast<int64_t>(a.Dv) * a.Dk;
-  const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.Dk + dk0;
-  const T* k = static_cast<const T*>(a.k) + static_cast<int64_t>(hk) * a.Dk + dk0;
-  const T* dout = static_cast<const T*>(r.dout) + static_cast<int64_t>(h) * a.Dv + dv0;
-  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
-  const T* g = static_cast<const T*>(a.g) + h;
-  const T* be = static_cast<const T*>(a.beta) + h;
+  const int64_t ts = a.bfirst ? 1 : a.B, row0 = a.row(b, 0), o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  TokenSource src;
+  src.k = static_cast<const T*>(a.k) + row0 * a.k_row + static_cast<int64_t>(hk) * a.Dk;
+  src.q = static_cast<const T*>(a.q) + row0 * a.q_row + static_cast<int64_t>(hk) * a.Dk;
+  src.x = static_cast<const T*>(r.dout) + row0 * o_row + static_cast<int64_t>(h) * a.Dv + grp * kWarps * R;
+  src.g = static_cast<const T*>(a.g) + row0 * a.g_row + h;
+  src.beta = static_cast<const T*>(a.beta) + row0 * a.beta_row + h;
+  src.k_step = ts * a.k_row; src.q_step = ts * a.q_row; src.x_step = ts * o_row;
+  src.g_step = ts * a.g_row; src.beta_step = ts * a.beta_row;
+  src.dk = a.Dk;
+  src.cols = a.Dv - grp * kWarps * R;
   const bool vin = lane < R && dv0 + lane < a.Dv;
   const int nc = (a.T + kSimtChunk - 1) / kSimtChunk;
 
+  float2 gb = make_float2(0.f, 0.f);
+  if (len > 0) gb = stage_fetch<T, VPL, R>(st[0], src, len - 1, -1, len);
   float dS[R][VPL];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const bool ok = in && r.dsT != nullptr && dv0 + i < a.Dv;
     load_vec<float, VPL>(r.dsT + bh * head_elems + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, dS[i]);
   }
-  float kc[VPL], qc[VPL], dc = 0.f, gc = 0.f, bc = 0.f;
-  if (len > 0) {
-    const int64_t row = a.row(b, len - 1);
-    load_vec<T, VPL>(k + row * a.k_row, in, kc);
-    load_vec<T, VPL>(q + row * a.q_row, in, qc);
-    dc = vin ? to_f<T>(dout[row * o_row + lane]) : 0.f;
-    gc = to_f<T>(g[row * a.g_row]);
-    bc = to_f<T>(be[row * a.beta_row]);
-  }
-  for (int t = len - 1; t >= 0; --t) {
-    if ((t % kSimtChunk == kSimtChunk - 1 || t == len - 1) && in) {
+  for (int it = 0; it < len; ++it) {
+    const int t = len - 1 - it, n = it % kAhead;
+    if (n == 0) {
+      stage_ready<T, VPL, R>(st[(it / kAhead) & 1], gb);
+      if (it + kAhead < len) gb = stage_fetch<T, VPL, R>(st[(it / kAhead + 1) & 1], src, t - kAhead, -1, len);
+    }
+    const TokenStage<T, VPL, R>& s = st[(it / kAhead) & 1];
+    float kc[VPL], qc[VPL];
+    load_vec<T, VPL>(&s.k[n][dk0], in, kc);
+    load_vec<T, VPL>(&s.q[n][dk0], in, qc);
+    const float dc = vin ? to_f<T>(s.x[n][warp * R + lane]) : 0.f, gc = s.g[n], bc = s.beta[n];
+    if ((t % kSimtChunk == kSimtChunk - 1 || it == 0) && in) {
       float* c = r.ckpt + (bh * nc + t / kSimtChunk) * head_elems + dk0;
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, dS[i]);
-    }
-    float kn[VPL], qn[VPL], dn = 0.f, gn = 0.f, bn = 0.f;
-    if (t > 0) {
-      const int64_t row = a.row(b, t - 1);
-      load_vec<T, VPL>(k + row * a.k_row, in, kn);
-      load_vec<T, VPL>(q + row * a.q_row, in, qn);
-      dn = vin ? to_f<T>(dout[row * o_row + lane]) : 0.f;
-      gn = to_f<T>(g[row * a.g_row]);
-      bn = to_f<T>(be[row * a.beta_row]);
     }
     const float al = expf(gc);
     float d[R];
@@ -274,9 +346,6 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
 #pragma unroll
       for (int j = 0; j < VPL; ++j) dS[i][j] = al * fmaf(-ei, kc[j], dS[i][j]);
     }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
-    dc = dn; gc = gn; bc = bn;
   }
   if (r.ds0 && in) {
 #pragma unroll
@@ -520,19 +589,29 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 
 int vpl_of(int Dk) { return Dk <= 32 ? 1 : Dk <= 64 ? 2 : Dk <= 128 ? 4 : 8; }
 
-template <typename T, int VPL, int R>
+// Sequences of at least this many tokens are staged.
+constexpr int kAheadFrom = 8;
+
+template <typename T, int VPL, int R, bool AHEAD>
 int recur(const DeltaRecurArgs& r, cudaStream_t s) {
   const int64_t groups = (r.a.Dv + kWarps * R - 1) / (kWarps * R);
-  delta_recur_kernel<T, VPL, R><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
+  delta_recur_kernel<T, VPL, R, AHEAD><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
   return check_launch();
+}
+template <typename T, int VPL>
+int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
+  if (r.a.T >= kAheadFrom) return recur<T, VPL, 4, true>(r, s);
+  // a step: with many states to move, eight rows a warp keep more bytes on their way
+  const int64_t rows = static_cast<int64_t>(r.a.B) * r.a.Hv * r.a.Dv;
+  return rows >= (1 << 17) ? recur<T, VPL, 8, false>(r, s) : recur<T, VPL, 4, false>(r, s);
 }
 template <typename T>
 int recur_t(const DeltaRecurArgs& r, cudaStream_t s) {
   switch (vpl_of(r.a.Dk)) {
-    case 1: return recur<T, 1, 4>(r, s);
-    case 2: return recur<T, 2, 4>(r, s);
-    case 4: return recur<T, 4, 4>(r, s);
-    default: return recur<T, 8, 4>(r, s);
+    case 1: return recur_v<T, 1>(r, s);
+    case 2: return recur_v<T, 2>(r, s);
+    case 4: return recur_v<T, 4>(r, s);
+    default: return recur_v<T, 8>(r, s);
   }
 }
 template <typename T, int VPL, int R>
