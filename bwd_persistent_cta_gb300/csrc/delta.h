@@ -46,13 +46,15 @@ struct DeltaRecurArgs {
   void* o;
   float* ckpt;                 // S0 of every chunk, or null
   float* e;                    // E, or null
+  // the serving step: where a bounded wait reports, and the GPU's size
+  unsigned int* status;
+  int num_sms;
 };
 int launch_delta_recur(const DeltaRecurArgs& r, int is_bf16, cudaStream_t s);
 
 struct DeltaRecurBwdArgs {
   DeltaArgs a;
   const void* dout;
-  const float* e;              // unused here but for the chunk kernel
   const float* dsT;            // or null
   float* ds0;                  // or null
   float* ckpt;                 // dS1 of every chunk

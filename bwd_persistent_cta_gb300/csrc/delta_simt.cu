@@ -267,6 +267,158 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
   }
 }
 
+// The serving step over many states: all it does is move them, 8 Dk Dv bytes a
+// head against 6 Dk Dv operations, so what counts is bytes on their way.  A CTA
+// walks units of 32 state rows with a stride; a unit (contiguous, 128 Dk bytes) is
+// fetched by one bulk copy kUnits units early, its token inputs one unit early.
+// Warp w computes rows 8 w .. 8 w + 7 and writes them back from registers.
+constexpr int kUnits = 4;
+constexpr int kUnitRows = 32;
+constexpr uint64_t kStepTimeoutNs = 2000000000ull;     // of a wait for a unit's copy
+
+template <int VPL>
+struct StepSmem {
+  float S[kUnits][kUnitRows * 32 * VPL];
+  uint64_t full[kUnits];
+};
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kWarps * 32) delta_step_kernel(const DeltaRecurArgs r) {
+  constexpr int R = kUnitRows / kWarps;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  StepSmem<VPL>& sm = *reinterpret_cast<StepSmem<VPL>*>(smem_raw);
+  const DeltaArgs& a = r.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (a.Dv + kUnitRows - 1) / kUnitRows, per = a.Hv / a.Hk;
+  const int units = groups * a.Hv * a.B, stride = gridDim.x;
+  const int dk0 = lane * VPL;
+  const bool in = dk0 < a.Dk;
+  const int64_t ts = a.bfirst ? 1 : a.B, o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+
+  struct Unit {
+    int b, h, dv0, rows, len;
+    float* S;
+  };
+  auto at = [&](int u) {
+    Unit x;
+    const int bh = u / groups;
+    x.dv0 = (u - bh * groups) * kUnitRows;
+    x.b = bh / a.Hv;
+    x.h = bh - x.b * a.Hv;
+    x.rows = min(kUnitRows, a.Dv - x.dv0);
+    const int64_t slot = r.slots ? r.slots[x.b] : x.b;
+    const bool live = slot >= 0 && slot < r.num_slots;
+    x.len = live ? (a.len ? a.len[x.b] : a.T) : 0;
+    x.S = r.s_out + ((slot * a.Hv + x.h) * a.Dv + x.dv0) * a.Dk;
+    return x;
+  };
+  // by thread 0, once nobody reads the stage; a unit without tokens only turns the barrier's phase
+  auto fetch = [&](int u, int stage) {
+    const Unit x = at(u);
+    const uint32_t bytes = x.len ? x.rows * a.Dk * 4 : 0;
+    mbar_arrive_expect_tx(&sm.full[stage], bytes);
+    if (bytes) {
+      fence_proxy_async_smem();
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                   :: "r"(smem_u32(sm.S[stage])), "l"(x.S), "r"(bytes), "r"(smem_u32(&sm.full[stage])) : "memory");
+    }
+  };
+  float kn[VPL], qn[VPL], vn = 0.f, gn = 0.f, bn = 0.f;
+  const int vrow = warp * R + lane;           // of the unit, lanes below R
+  auto token = [&](const Unit& x, int t) {
+    const int64_t row = a.row(x.b, t);
+    const int hk = x.h / per;
+    load_vec<T, VPL>(static_cast<const T*>(a.k) + row * a.k_row + hk * a.Dk + dk0, in, kn);
+    load_vec<T, VPL>(static_cast<const T*>(a.q) + row * a.q_row + hk * a.Dk + dk0, in, qn);
+    vn = lane < R && vrow < x.rows ? to_f<T>(static_cast<const T*>(a.v)[row * a.v_row + static_cast<int64_t>(x.h) * a.Dv + x.dv0 + vrow]) : 0.f;
+    gn = to_f<T>(static_cast<const T*>(a.g)[row * a.g_row + x.h]);
+    bn = to_f<T>(static_cast<const T*>(a.beta)[row * a.beta_row + x.h]);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kUnits; ++i) mbar_init(&sm.full[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < kUnits; ++i)
+      if (static_cast<int64_t>(blockIdx.x) + i * stride < units) fetch(blockIdx.x + i * stride, i);
+  }
+  __syncthreads();
+  Unit cur{}, nxt = at(min(static_cast<int>(blockIdx.x), units - 1));
+  if (nxt.len) token(nxt, 0);
+  int turn = 0;
+  for (int64_t u = blockIdx.x; u < units; u += stride, ++turn) {
+    cur = nxt;
+    const int stage = turn % kUnits;
+    const bool late = !mbar_wait(&sm.full[stage], (turn / kUnits) & 1, kStepTimeoutNs);
+    float S[R][VPL];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      load_vec<float, VPL>(&sm.S[stage][(warp * R + i) * a.Dk + dk0], in && cur.len && warp * R + i < cur.rows, S[i]);
+    if (__syncthreads_or(late)) {
+      // a copy that is still under way keeps the CTA for as long again
+      if (threadIdx.x == 0) {
+        atomicCAS(r.status, 0u, static_cast<unsigned int>(RNN_TIMEOUT));
+        for (int i = 0; i < kUnits; ++i) mbar_wait(&sm.full[i], (turn + i) / kUnits & 1, kStepTimeoutNs);
+      }
+      return;
+    }
+    if (threadIdx.x == 0 && u + static_cast<int64_t>(kUnits) * stride < units) fetch(static_cast<int>(u) + kUnits * stride, stage);
+    float kc[VPL], qc[VPL], vc, gc, bc;
+    auto take = [&]() {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
+      vc = vn; gc = gn; bc = bn;
+    };
+    auto next_unit = [&]() {
+      if (u + stride < units) {
+        nxt = at(static_cast<int>(u) + stride);
+        if (nxt.len) token(nxt, 0);
+      }
+    };
+    T* o = static_cast<T*>(r.o) + a.row(cur.b, 0) * o_row + static_cast<int64_t>(cur.h) * a.Dv + cur.dv0 + vrow;
+    const bool vin = lane < R && vrow < cur.rows;
+    for (int t = 0; t < cur.len; ++t) {
+      take();
+      if (t + 1 < cur.len) token(cur, t + 1);
+      else next_unit();
+      const float al = expf(gc);
+      float d[2 * R], kq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * R; ++i) d[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        kq = fmaf(kc[j], qc[j], kq);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          d[i] = fmaf(S[i][j], kc[j], d[i]);
+          d[R + i] = fmaf(S[i][j], qc[j], d[R + i]);
+        }
+      }
+      const float sum = warp_sum_many<2 * R>(d, lane);
+#pragma unroll
+      for (int w = 16; w; w >>= 1) kq += __shfl_xor_sync(kFull, kq, w);
+      const int src_lane = lane < R ? lane : 0;
+      const float sk = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * src_lane);
+      const float sq = __shfl_sync(kFull, sum, sum_lane<2 * R>(1) * (R + src_lane));
+      const float uu = bc * (vc - al * sk);
+      if (vin) o[t * ts * o_row] = from_f<T>(a.scale * fmaf(al, sq, uu * kq));
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float ui = __shfl_sync(kFull, uu, i);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(ui, kc[j], al * S[i][j]);
+      }
+    }
+    for (int t = cur.len; t < a.T; ++t)
+      if (vin) o[t * ts * o_row] = from_f<T>(0.f);
+    if (!cur.len) next_unit();
+    if (in && cur.len) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (warp * R + i < cur.rows) store_state<VPL>(cur.S + static_cast<int64_t>(warp * R + i) * a.Dk + dk0, S[i]);
+    }
+  }
+}
+
 // The reverse recurrence of the state gradient, same ownership:
 //   dS += scale do_t q_t^T;  y_t = dS k_t;  dS -= beta_t y_t k_t^T;  dS *= a_t.
 template <typename T, int VPL, int R>
@@ -601,9 +753,21 @@ int recur(const DeltaRecurArgs& r, cudaStream_t s) {
 template <typename T, int VPL>
 int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
   if (r.a.T >= kAheadFrom) return recur<T, VPL, 4, true>(r, s);
-  // a step: with many states to move, eight rows a warp keep more bytes on their way
-  const int64_t rows = static_cast<int64_t>(r.a.B) * r.a.Hv * r.a.Dv;
-  return rows >= (1 << 17) ? recur<T, VPL, 8, false>(r, s) : recur<T, VPL, 4, false>(r, s);
+  if constexpr (VPL <= 4) {
+    // A step over more units than three CTAs an SM take in two turns.  With more
+    // than two tokens the chain of a unit is longer than its transfer and the
+    // recurrence's larger number of warps wins (256 sequences x 32 heads x 128 x 128,
+    // one token: 173 us against 203; 48 x 16, four tokens: 30.0 against 27.7).
+    const int64_t units = static_cast<int64_t>((r.a.Dv + kUnitRows - 1) / kUnitRows) * r.a.Hv * r.a.B;
+    if (r.status && r.a.T <= 2 && units >= 6 * r.num_sms && units + 3ll * kUnits * r.num_sms < (1ll << 31)) {
+      const int smem = sizeof(StepSmem<VPL>);
+      if (cudaFuncSetAttribute(delta_step_kernel<T, VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return RNN_CUDA_ERROR;
+      delta_step_kernel<T, VPL><<<3 * r.num_sms, kWarps * 32, smem, s>>>(r);
+      return check_launch();
+    }
+  }
+  return recur<T, VPL, 4, false>(r, s);
 }
 template <typename T>
 int recur_t(const DeltaRecurArgs& r, cudaStream_t s) {

@@ -173,17 +173,18 @@ __device__ __forceinline__ void load_b_rows_k(uint32_t (&b)[4], uint32_t tile, i
 // piece index 2 kk + b exchanged by x = lane & 7 is ((2 kk & 7) + b ^ x) with the
 // higher bits untouched, so four offsets serve a row of any length.
 struct LaneOffsets {
-  uint32_t n[2][4], k[2][4];     // by row pitch (128 bytes, Dk * 2 bytes)
-  __device__ __forceinline__ void init(int dk_pitch, int lane) {
+  uint32_t n[2][4], k[2][4];     // of packed tiles, of rows of Dk columns
+  // ``first``: the first of the warp's pieces in the rows of Dk columns, 0 or 4 of 8
+  __device__ __forceinline__ void init(int dk_pitch, int lane, int first = 0) {
     const int x = lane & 7;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t pn = ((2 * i + ((lane >> 3) & 1)) ^ x) << 4, pk = ((2 * i + (lane >> 4)) ^ x) << 4;
+      const int an = 2 * i + ((lane >> 3) & 1), ak = 2 * i + (lane >> 4);
       const int rn = x + ((lane >> 4) << 3), rk = x + (((lane >> 3) & 1) << 3);
-      n[0][i] = rn * 128 + pn;
-      n[1][i] = rn * dk_pitch + pn;
-      k[0][i] = rk * 128 + pk;
-      k[1][i] = rk * dk_pitch + pk;
+      n[0][i] = rn * 128 + ((an ^ x) << 4);
+      n[1][i] = rn * dk_pitch + (((an ^ first) ^ x) << 4);
+      k[0][i] = rk * 128 + ((ak ^ x) << 4);
+      k[1][i] = rk * dk_pitch + (((ak ^ first) ^ x) << 4);
     }
   }
 };
@@ -202,11 +203,11 @@ __host__ __device__ constexpr int tri_piece(int b, int kb, int part) {
 // rows n: tiles n0, n0 + 8 and k-step kk; rows k likewise (n0 a multiple of 16)
 template <int PITCH>
 __device__ __forceinline__ void scan_b_n(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
-  ldsm(b, tile + o.n[PITCH != 128][kk & 3] + n0 * PITCH + (kk >> 2) * 128);
+  ldsm(b, tile + o.n[1][kk & 3] + n0 * PITCH + (kk >> 2) * 128);
 }
 template <int PITCH>
 __device__ __forceinline__ void scan_b_k(uint32_t (&b)[4], uint32_t tile, const LaneOffsets& o, int n0, int kk) {
-  ldsm_t(b, tile + o.k[PITCH != 128][(n0 >> 4) & 3] + 16 * kk * PITCH + (n0 >> 6) * 128);
+  ldsm_t(b, tile + o.k[1][(n0 >> 4) & 3] + 16 * kk * PITCH + (n0 >> 6) * 128);
 }
 
 // The same of a packed triangular tile: block row n0 / 16, k-step kk = its column (rows n), or the reverse (rows k).
@@ -602,14 +603,14 @@ struct State {
 };
 
 // fp32 state rows <-> fragments: 8 neighbouring columns a thread, row and m.
-template <int DK>
-__device__ __forceinline__ void state_load(State<DK>& S, const float* base, int lane) {
+template <int DKW>
+__device__ __forceinline__ void state_load(State<DKW>& S, const float* base, int pitch, int lane) {
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const float* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+    const float* p = base + (dv_of_row(r) + 2 * half) * pitch + 8 * c;
 #pragma unroll
-    for (int m = 0; m < DK / 32; ++m) {
+    for (int m = 0; m < DKW / 32; ++m) {
       const float4 x = *reinterpret_cast<const float4*>(p + 32 * m), y = *reinterpret_cast<const float4*>(p + 32 * m + 4);
       S.v[4 * m][2 * half] = x.x; S.v[4 * m][2 * half + 1] = x.y;
       S.v[4 * m + 1][2 * half] = x.z; S.v[4 * m + 1][2 * half + 1] = x.w;
@@ -618,14 +619,14 @@ __device__ __forceinline__ void state_load(State<DK>& S, const float* base, int 
     }
   }
 }
-template <int DK>
-__device__ __forceinline__ void state_store(const State<DK>& S, float* base, int lane) {
+template <int DKW>
+__device__ __forceinline__ void state_store(const State<DKW>& S, float* base, int pitch, int lane) {
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+    float* p = base + (dv_of_row(r) + 2 * half) * pitch + 8 * c;
 #pragma unroll
-    for (int m = 0; m < DK / 32; ++m) {
+    for (int m = 0; m < DKW / 32; ++m) {
       *reinterpret_cast<float4*>(p + 32 * m) = make_float4(S.v[4 * m][2 * half], S.v[4 * m][2 * half + 1],
                                                            S.v[4 * m + 1][2 * half], S.v[4 * m + 1][2 * half + 1]);
       *reinterpret_cast<float4*>(p + 32 * m + 4) = make_float4(S.v[4 * m + 2][2 * half], S.v[4 * m + 2][2 * half + 1],
@@ -634,7 +635,7 @@ __device__ __forceinline__ void state_store(const State<DK>& S, float* base, int
   }
 }
 template <int DK>
-__device__ __forceinline__ float state_max(const State<DK>& S) {
+__device__ __forceinline__ float state_max(const State<DK>& S) {      // over the warp
   float m = 0.f;
 #pragma unroll
   for (int j = 0; j < DK / 8; ++j)
@@ -643,14 +644,14 @@ __device__ __forceinline__ float state_max(const State<DK>& S) {
   return warp_max(m);
 }
 // fp16 copy of the state, scaled by f.
-template <int DK>
-__device__ __forceinline__ void state_store_half(const State<DK>& S, float f, __half* base, int lane) {
+template <int DKW>
+__device__ __forceinline__ void state_store_half(const State<DKW>& S, float f, __half* base, int pitch, int lane) {
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    __half* p = base + (dv_of_row(r) + 2 * half) * DK + 8 * c;
+    __half* p = base + (dv_of_row(r) + 2 * half) * pitch + 8 * c;
 #pragma unroll
-    for (int m = 0; m < DK / 32; ++m) {
+    for (int m = 0; m < DKW / 32; ++m) {
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = pack_h(mul2(half ? hi2(S.v[4 * m + i]) : lo2(S.v[4 * m + i]), both(f)));
@@ -743,6 +744,7 @@ template <int DK, int W>
 struct alignas(128) ScanSmem {
   ScanStage<DK, W> st[2];
   uint64_t full[2];
+  float smax[2][W];                  // of the warps' states, by turn
 };
 struct ScanSource {
   const char *k, *q, *t, *p, *sc;        // of chunk 0
@@ -788,11 +790,11 @@ __device__ __forceinline__ bool scan_arrive(uint64_t* full, int it, unsigned int
 
 // Z = S X^T over the key columns, X = K16 ([16][64 tokens]), from both parts of
 // S; with BOTH also Z2 = S X2^T, X2 = Q16, from the high part.
-template <int DK, bool BOTH>
-__device__ __forceinline__ void state_times(const State<DK>& S, float f, uint32_t x, uint32_t x2, Frag& z, Frag& z2,
+template <int DK, bool BOTH, int DKW>
+__device__ __forceinline__ void state_times(const State<DKW>& S, float f, uint32_t x, uint32_t x2, Frag& z, Frag& z2,
                                             const LaneOffsets& lo_) {
 #pragma unroll
-  for (int kk = 0; kk < DK / 16; ++kk) {
+  for (int kk = 0; kk < DKW / 16; ++kk) {
     uint32_t hi[4], lo[4];
     split(mul2(lo2(S.v[2 * kk]), both(f)), hi[0], lo[0]);
     split(mul2(hi2(S.v[2 * kk]), both(f)), hi[1], lo[1]);
@@ -827,14 +829,14 @@ __device__ __forceinline__ void state_times(const State<DK>& S, float f, uint32_
 
 // S = decay S + sum_t X[.][t] B[t][.], with X scaled by f and B a tile of 64
 // tokens; ``g`` undoes the scales.
-template <int DK>
-__device__ __forceinline__ void state_update(State<DK>& S, float decay, const Frag& x, float f, uint32_t tile, float g,
+template <int DK, int DKW>
+__device__ __forceinline__ void state_update(State<DKW>& S, float decay, const Frag& x, float f, uint32_t tile, float g,
                                              const LaneOffsets& lo_) {
   uint32_t hi[4][4], lo[4][4];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) frag_a(x, kk, f, hi[kk], lo[kk]);
 #pragma unroll
-  for (int j = 0; j < DK / 8; j += 4) {
+  for (int j = 0; j < DKW / 8; j += 4) {
     float acc[4][4];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
   if (ncb > 0) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, 0, len);
   State<DK> S;
   if (p.s_in) {
-    state_load<DK>(S, p.s_in + s_off, lane);
+    state_load<DK>(S, p.s_in + s_off, DK, lane);
   } else {
 #pragma unroll
     for (int j = 0; j < DK / 8; ++j)
@@ -938,14 +940,20 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
       for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
   }
   for (int c = 0; c < ncb; ++c) {
+    // one scale for the states of the CTA: their copies then need none of their own in the gradients
+    const float own_max = state_max<DK>(S);
+    if (lane == 0) sm.smax[c & 1][warp] = own_max;
     if (scan_arrive(sm.full, c, p.status)) return;
+    float smax = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) smax = fmaxf(smax, sm.smax[c & 1][w]);
     if (c + 1 < ncb) scan_fetch<DK, W>(sm.st[(c + 1) & 1], &sm.full[(c + 1) & 1], src, c + 1, len - (c + 1) * kTc);
     const ScanStage<DK, W>& s = sm.st[c & 1];
     const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
 
-    const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
+    const float sf = up_scale(smax), si = inv_scale(sf);
     if (TRAIN) {
-      state_store_half<DK>(S, sf, static_cast<__half*>(p.w.s0) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
+      state_store_half<DK>(S, sf, static_cast<__half*>(p.w.s0) + ((bh * nc + c) * a.Dv + dv0) * DK, DK, lane);
       if (lane == 0) p.w.s0_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
     }
     Frag z, oq, acc;
@@ -1021,7 +1029,242 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
     state_update<DK>(S, s.sc[kScEnd], z, uf, ks, ui * s.sc[kScK], off);
   }
   zero_rows(o, a, o_row, b, ncb * kTc, lane);
-  if (p.s_out) state_store<DK>(S, p.s_out + s_off, lane);
+  if (p.s_out) state_store<DK>(S, p.s_out + s_off, DK, lane);
+}
+
+// ---------------------------------------------------------------------------
+// the scans with two warps to 16 value columns
+// ---------------------------------------------------------------------------
+// Where there are too few heads to fill the GPU, a chunk's time is one warp's
+// chain.  Two warps then share 16 value columns: each keeps half of the state's
+// key columns (half the products with the state, and half of its update) and
+// finishes half of the token blocks, 0 and 3 or 1 and 2 (the same number of
+// triangular products).  Partial sums and finished blocks cross through shared
+// memory, two exchanges a chunk forward and three backward, on a barrier of the
+// two warps.
+template <int DK>
+struct alignas(128) PairSmem {
+  static constexpr int W = 2;
+  ScanStage<DK, W> st[2];
+  uint64_t full[2];
+  float smax[2][2 * W];
+  float4 a[W][2][12][32], b[W][2][4][32];
+};
+template <int N>
+struct Blk {
+  static constexpr int v = N;
+};
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" :: "r"(pair + 1) : "memory"); }
+__device__ __forceinline__ float4 as4(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void from4(float (&x)[4], float4 v) { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
+__device__ __forceinline__ void add4(float (&x)[4], float4 v) { x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w; }
+// Calls f with this warp's token blocks and its partner's.
+template <typename F>
+__device__ __forceinline__ void with_blocks(int half, F f) {
+  if (half) f(Blk<1>(), Blk<2>(), Blk<0>(), Blk<3>());
+  else f(Blk<0>(), Blk<3>(), Blk<1>(), Blk<2>());
+}
+// Sends this warp's two blocks of x and takes the partner's.
+template <typename B0, typename B1, typename P0, typename P1>
+__device__ __forceinline__ void swap_blocks(Frag& x, float4 (*mine)[32], float4 (*theirs)[32], int pair, int lane, B0, B1, P0, P1) {
+  mine[0][lane] = as4(x[2 * B0::v]); mine[1][lane] = as4(x[2 * B0::v + 1]);
+  mine[2][lane] = as4(x[2 * B1::v]); mine[3][lane] = as4(x[2 * B1::v + 1]);
+  pair_sync(pair);
+  from4(x[2 * P0::v], theirs[0][lane]); from4(x[2 * P0::v + 1], theirs[1][lane]);
+  from4(x[2 * P1::v], theirs[2][lane]); from4(x[2 * P1::v + 1], theirs[3][lane]);
+}
+// acc of block b = the triangular product of a split fragment: rows n (kk <= b) or rows k (kk >= b)
+template <bool ROWS_N, bool LOW_A, typename BB>
+__device__ __forceinline__ void tri_block(Frag& acc, const uint32_t (&hi)[4][4], const uint32_t (&lo)[4][4], uint32_t tile,
+                                          const LaneOffsets& off, bool low_b, BB) {
+  constexpr int b = BB::v, n = 2 * b;
+#pragma unroll
+  for (int i = 0; i <= (ROWS_N ? b : 3 - b); ++i) {
+    const int kk = ROWS_N ? i : b + i;
+    uint32_t t[4];
+    if (ROWS_N) scan_tri_n(t, tile, off, 8 * n, kk, 0);
+    else scan_tri_k(t, tile, off, 8 * n, kk, 0);
+    if (i == 0) {
+      mma_h0(acc[n], hi[kk], t[0], t[1]);
+      mma_h0(acc[n + 1], hi[kk], t[2], t[3]);
+    } else {
+      mma_h(acc[n], hi[kk], t[0], t[1]);
+      mma_h(acc[n + 1], hi[kk], t[2], t[3]);
+    }
+    if (LOW_A) {
+      mma_h(acc[n], lo[kk], t[0], t[1]);
+      mma_h(acc[n + 1], lo[kk], t[2], t[3]);
+    }
+    if (low_b) {
+      if (ROWS_N) scan_tri_n(t, tile, off, 8 * n, kk, 1);
+      else scan_tri_k(t, tile, off, 8 * n, kk, 1);
+      mma_h(acc[n], hi[kk], t[0], t[1]);
+      mma_h(acc[n + 1], hi[kk], t[2], t[3]);
+    }
+  }
+}
+// Stores of one 16-token block.
+template <typename BB>
+__device__ __forceinline__ void block_store_half(const Frag& x, float f, __half* base, int pitch, int lane, BB) {
+  __half* p = base + (lane >> 2) * pitch + 4 * (lane & 3);
+#pragma unroll
+  for (int n = 2 * BB::v; n < 2 * BB::v + 2; ++n)
+    *reinterpret_cast<uint2*>(p + 8 * n * pitch) =
+        make_uint2(transpose8(pack_h(mul2(lo2(x[n]), both(f)))), transpose8(pack_h(mul2(hi2(x[n]), both(f)))));
+}
+template <typename BB>
+__device__ __forceinline__ void block_store_seq(const Frag& x, __nv_bfloat16* p, int64_t step, int left, int lane, BB) {
+#pragma unroll
+  for (int n = 2 * BB::v; n < 2 * BB::v + 2; ++n) {
+    const uint32_t lo = transpose8(pack_b(x[n][0], x[n][1])), hi = transpose8(pack_b(x[n][2], x[n][3]));
+    if ((lane >> 2) + 8 * n < left) *reinterpret_cast<uint2*>(p + n * step) = make_uint2(lo, hi);
+  }
+}
+
+template <int DK, bool TRAIN>
+__global__ void __launch_bounds__(128) delta_pair_fwd_kernel(const DeltaTcArgs p) {
+  constexpr int W = 2, DKW = DK / 2;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  PairSmem<DK>& sm = *reinterpret_cast<PairSmem<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
+  const int groups = a.Dv / (16 * W);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
+            b = static_cast<int>(bid / groups / a.Hv);
+  const int slice = grp * W + pair, dv0 = slice * 16;
+  const int hk = h / (a.Hv / a.Hk);
+  const int len = a.len ? a.len[b] : a.T;
+  const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const int64_t s_off = (bh * a.Dv + dv0) * DK + DKW * half;
+  const int64_t ts_ = a.bfirst ? 1 : a.B;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + static_cast<int64_t>(h) * a.Dv + dv0;
+  const int64_t o_step = 8 * ts_ * o_row;
+  __nv_bfloat16* ow = o + a.row(b, lane >> 2) * o_row + 4 * (lane & 3);
+  // this warp's half of the key columns: 128 bytes further, or the other four pieces of a 128-byte row
+  LaneOffsets off;
+  off.init(DK * 2, lane, DK == 64 ? 4 * half : 0);
+  const uint32_t koff = DK == 128 ? 128 * half : 0;
+  ScanSource src;
+  src.k = static_cast<const char*>(p.w.k16) + bk * nc * kTc * DK * 2;
+  src.q = static_cast<const char*>(p.w.q16) + bk * nc * kTc * DK * 2;
+  src.t = static_cast<const char*>(p.w.th) + bh * nc * kTri;
+  src.p = static_cast<const char*>(p.w.p) + bh * nc * kTri;
+  src.sc = reinterpret_cast<const char*>(p.w.sc) + bh * nc * kSc * 4;
+  const int piece = threadIdx.x & 63;              // the first 64 threads fetch
+  src.x = static_cast<const __nv_bfloat16*>(a.v) + a.row(b, piece / (2 * W)) * a.v_row + static_cast<int64_t>(h) * a.Dv +
+          grp * 16 * W + 8 * (piece % (2 * W));
+  src.x_step = 16 * ts_ * a.v_row;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full[0], 1);
+    mbar_init(&sm.full[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ncb > 0 && threadIdx.x < 64) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, 0, len);
+  State<DKW> S;
+  if (p.s_in) {
+    state_load<DKW>(S, p.s_in + s_off, DK, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < DKW / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
+  }
+  for (int c = 0; c < ncb; ++c) {
+    const float own_max = state_max<DKW>(S);
+    if (lane == 0) sm.smax[c & 1][warp] = own_max;
+    if (scan_arrive(sm.full, c, p.status)) return;
+    if (c + 1 < ncb && threadIdx.x < 64)
+      scan_fetch<DK, W>(sm.st[(c + 1) & 1], &sm.full[(c + 1) & 1], src, c + 1, len - (c + 1) * kTc);
+    float smax = 0.f;
+#pragma unroll
+    for (int w = 0; w < 2 * W; ++w) smax = fmaxf(smax, sm.smax[c & 1][w]);
+    const ScanStage<DK, W>& s = sm.st[c & 1];
+    const uint32_t ks = smem_u32(s.K) + koff, qs = smem_u32(s.Q) + koff, ts = smem_u32(s.T), ps = smem_u32(s.P);
+    float4 (*xa)[32] = sm.a[pair][half], (*ya)[32] = sm.a[pair][half ^ 1], (*xb)[32] = sm.b[pair][half],
+           (*yb)[32] = sm.b[pair][half ^ 1];
+
+    const float sf = up_scale(smax), si = inv_scale(sf);
+    if (TRAIN) {
+      state_store_half<DKW>(S, sf, static_cast<__half*>(p.w.s0) + ((bh * nc + c) * a.Dv + dv0) * DK + DKW * half, DK, lane);
+      if (lane == 0 && half == 0) p.w.s0_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
+    }
+    Frag z, oq, acc;
+    state_times<DK, true>(S, sf, ks, qs, z, oq, off);
+    with_blocks(half, [&](auto, auto, auto p0, auto p1) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) xa[n][lane] = as4(z[n]);
+      xa[8][lane] = as4(oq[2 * decltype(p0)::v]); xa[9][lane] = as4(oq[2 * decltype(p0)::v + 1]);
+      xa[10][lane] = as4(oq[2 * decltype(p1)::v]); xa[11][lane] = as4(oq[2 * decltype(p1)::v + 1]);
+    });
+    pair_sync(pair);
+    const float zk = -si * s.sc[kScK], zq = si * s.sc[kScQ] * a.scale;
+    Slice vs;
+    slice_load<W>(vs, s.x, pair, lane);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      add4(z[n], ya[n][lane]);
+      const float2 ek = mul2(pair_of(s.sc, n, lane), both(zk));
+      float2 lo, hi;
+      slice_frag(vs, n, lo, hi);
+      set4(z[n], fma2(lo2(z[n]), ek, lo), fma2(hi2(z[n]), ek, hi));
+    }
+    const float rf = up_scale(frag_max(z));
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) frag_a(z, kk, rf, hi[kk], lo[kk]);
+    const float ti = inv_scale(rf) * s.sc[kScTH];
+    with_blocks(half, [&](auto b0, auto b1, auto p0, auto p1) {
+      constexpr int n0 = 2 * decltype(b0)::v, n1 = 2 * decltype(b1)::v;
+      add4(oq[n0], ya[8][lane]); add4(oq[n0 + 1], ya[9][lane]);
+      add4(oq[n1], ya[10][lane]); add4(oq[n1 + 1], ya[11][lane]);
+      tri_block<true, true>(acc, hi, lo, ts, off, true, b0);
+      tri_block<true, true>(acc, hi, lo, ts, off, true, b1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        set4(z[n0 + i], fma2(lo2(acc[n0 + i]), both(ti), lo2(z[n0 + i])), fma2(hi2(acc[n0 + i]), both(ti), hi2(z[n0 + i])));
+        set4(z[n1 + i], fma2(lo2(acc[n1 + i]), both(ti), lo2(z[n1 + i])), fma2(hi2(acc[n1 + i]), both(ti), hi2(z[n1 + i])));
+      }
+      swap_blocks(z, xb, yb, pair, lane, b0, b1, p0, p1);
+    });
+    const float ef = up_scale(frag_max(z));
+    if (TRAIN) {
+      __half* e = static_cast<__half*>(p.w.e) + (bh * nc + c) * kTc * a.Dv + dv0;
+      with_blocks(half, [&](auto b0, auto b1, auto, auto) {
+        block_store_half(z, ef, e, a.Dv, lane, b0);
+        block_store_half(z, ef, e, a.Dv, lane, b1);
+      });
+      if (lane == 0 && half == 0) p.w.e_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(ef);
+    }
+    const float uf = ef * s.sc[kScBu], ui = inv_scale(uf);
+    frag_scale(z, s.sc + 128, lane);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) frag_a_hi(z, kk, uf, hi[kk]);
+    const float pi = ui * s.sc[kScP];
+    with_blocks(half, [&](auto b0, auto b1, auto, auto) {
+      tri_block<true, false>(acc, hi, lo, ps, off, false, b0);
+      tri_block<true, false>(acc, hi, lo, ps, off, false, b1);
+      auto finish = [&](auto bb) {
+#pragma unroll
+        for (int n = 2 * decltype(bb)::v; n < 2 * decltype(bb)::v + 2; ++n) {
+          const float2 eq = mul2(pair_of(s.sc, n, lane), both(zq));
+          set4(oq[n], fma2(lo2(acc[n]), both(pi), mul2(lo2(oq[n]), eq)), fma2(hi2(acc[n]), both(pi), mul2(hi2(oq[n]), eq)));
+        }
+        block_store_seq(oq, ow, o_step, a.T - c * kTc, lane, bb);
+      };
+      finish(b0);
+      finish(b1);
+    });
+    ow += 8 * o_step;
+    frag_scale(z, s.sc + 64, lane);
+    state_update<DK>(S, s.sc[kScEnd], z, uf, ks, ui * s.sc[kScK], off);
+  }
+  if (half == 0) zero_rows(o, a, o_row, b, ncb * kTc, lane);
+  if (p.s_out) state_store<DKW>(S, p.s_out + s_off, DK, lane);
 }
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
@@ -1053,7 +1296,7 @@ int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
   if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
   else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
-  else delta_scan_fwd_kernel<DK, TRAIN, 2><<<grid, 64, sizeof(ScanSmem<DK, 2>), s>>>(t);
+  else delta_pair_fwd_kernel<DK, TRAIN><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
   rc = check_launch();
   if (!rc) ++*launches;
   return rc;
@@ -1106,7 +1349,7 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
   if (ncb > 0) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, ncb - 1, len - (ncb - 1) * kTc);
   State<DK> S;
   if (p.dsT) {
-    state_load<DK>(S, p.dsT + s_off, lane);
+    state_load<DK>(S, p.dsT + s_off, DK, lane);
   } else {
 #pragma unroll
     for (int j = 0; j < DK / 8; ++j)
@@ -1115,13 +1358,18 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
   }
   for (int it = 0; it < ncb; ++it) {
     const int c = ncb - 1 - it;
+    const float own_max = state_max<DK>(S);
+    if (lane == 0) sm.smax[it & 1][warp] = own_max;
     if (scan_arrive(sm.full, it, p.status)) return;
+    float smax = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) smax = fmaxf(smax, sm.smax[it & 1][w]);
     if (c > 0) scan_fetch<DK, W>(sm.st[(it + 1) & 1], &sm.full[(it + 1) & 1], src, c - 1, kTc);
     const ScanStage<DK, W>& s = sm.st[it & 1];
     const uint32_t ks = smem_u32(s.K), qs = smem_u32(s.Q), ts = smem_u32(s.T), ps = smem_u32(s.P);
 
-    const float sf = up_scale(state_max<DK>(S)), si = inv_scale(sf);
-    state_store_half<DK>(S, sf, static_cast<__half*>(p.ds1) + ((bh * nc + c) * a.Dv + dv0) * DK, lane);
+    const float sf = up_scale(smax), si = inv_scale(sf);
+    state_store_half<DK>(S, sf, static_cast<__half*>(p.ds1) + ((bh * nc + c) * a.Dv + dv0) * DK, DK, lane);
     if (lane == 0) p.ds1_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
     Frag z, acc;
     state_times<DK, false>(S, sf, ks, ks, z, z, off);
@@ -1211,7 +1459,166 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
     state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
   }
   zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, ncb * kTc, lane);
-  if (p.ds0) state_store<DK>(S, p.ds0 + s_off, lane);
+  if (p.ds0) state_store<DK>(S, p.ds0 + s_off, DK, lane);
+}
+
+template <int DK>
+__global__ void __launch_bounds__(128) delta_pair_bwd_kernel(const DeltaTcBwdArgs p) {
+  constexpr int W = 2, DKW = DK / 2;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  PairSmem<DK>& sm = *reinterpret_cast<PairSmem<DK>*>(smem_raw);
+  const DeltaArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
+  const int groups = a.Dv / (16 * W);
+  const int64_t bid = blockIdx.x;
+  const int grp = static_cast<int>(bid % groups), h = static_cast<int>(bid / groups % a.Hv),
+            b = static_cast<int>(bid / groups / a.Hv);
+  const int slice = grp * W + pair, dv0 = slice * 16;
+  const int hk = h / (a.Hv / a.Hk);
+  const int len = a.len ? a.len[b] : a.T;
+  const int nc = (a.T + kTc - 1) / kTc, ncb = (len + kTc - 1) / kTc;
+  const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, bk = static_cast<int64_t>(b) * a.Hk + hk;
+  const int64_t o_row = static_cast<int64_t>(a.Hv) * a.Dv;
+  const int64_t s_off = (bh * a.Dv + dv0) * DK + DKW * half;
+  const int64_t ts_ = a.bfirst ? 1 : a.B, o_step = 8 * ts_ * o_row;
+  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0 + 4 * (lane & 3) +
+                      a.row(b, (lane >> 2) + (ncb > 0 ? ncb - 1 : 0) * kTc) * o_row;
+  LaneOffsets off;
+  off.init(DK * 2, lane, DK == 64 ? 4 * half : 0);
+  const uint32_t koff = DK == 128 ? 128 * half : 0;
+  ScanSource src;
+  src.k = static_cast<const char*>(p.w.k16) + bk * nc * kTc * DK * 2;
+  src.q = static_cast<const char*>(p.w.q16) + bk * nc * kTc * DK * 2;
+  src.t = static_cast<const char*>(p.w.tb) + bh * nc * kTri;
+  src.p = static_cast<const char*>(p.w.p) + bh * nc * kTri;
+  src.sc = reinterpret_cast<const char*>(p.w.sc) + bh * nc * kSc * 4;
+  const int piece = threadIdx.x & 63;
+  src.x = static_cast<const __nv_bfloat16*>(p.dout) + a.row(b, piece / (2 * W)) * o_row + static_cast<int64_t>(h) * a.Dv +
+          grp * 16 * W + 8 * (piece % (2 * W));
+  src.x_step = 16 * ts_ * o_row;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full[0], 1);
+    mbar_init(&sm.full[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ncb > 0 && threadIdx.x < 64) scan_fetch<DK, W>(sm.st[0], &sm.full[0], src, ncb - 1, len - (ncb - 1) * kTc);
+  State<DKW> S;
+  if (p.dsT) {
+    state_load<DKW>(S, p.dsT + s_off, DK, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < DKW / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.v[j][i] = 0.f;
+  }
+  for (int it = 0; it < ncb; ++it) {
+    const int c = ncb - 1 - it;
+    const float own_max = state_max<DKW>(S);
+    if (lane == 0) sm.smax[it & 1][warp] = own_max;
+    if (scan_arrive(sm.full, it, p.status)) return;
+    if (c > 0 && threadIdx.x < 64) scan_fetch<DK, W>(sm.st[(it + 1) & 1], &sm.full[(it + 1) & 1], src, c - 1, kTc);
+    float smax = 0.f;
+#pragma unroll
+    for (int w = 0; w < 2 * W; ++w) smax = fmaxf(smax, sm.smax[it & 1][w]);
+    const ScanStage<DK, W>& s = sm.st[it & 1];
+    const uint32_t ks = smem_u32(s.K) + koff, qs = smem_u32(s.Q) + koff, ts = smem_u32(s.T), ps = smem_u32(s.P);
+    float4 (*xa)[32] = sm.a[pair][half], (*ya)[32] = sm.a[pair][half ^ 1], (*xb)[32] = sm.b[pair][half],
+           (*yb)[32] = sm.b[pair][half ^ 1];
+
+    const float sf = up_scale(smax), si = inv_scale(sf);
+    state_store_half<DKW>(S, sf, static_cast<__half*>(p.ds1) + ((bh * nc + c) * a.Dv + dv0) * DK + DKW * half, DK, lane);
+    if (lane == 0 && half == 0) p.ds1_scale[(bh * nc + c) * (a.Dv / 16) + slice] = si;
+    Frag z, acc;
+    state_times<DK, false>(S, sf, ks, ks, z, z, off);
+    // the partner's blocks of this half's sum
+    with_blocks(half, [&](auto, auto, auto p0, auto p1) {
+      constexpr int n0 = 2 * decltype(p0)::v, n1 = 2 * decltype(p1)::v;
+      xa[0][lane] = as4(z[n0]); xa[1][lane] = as4(z[n0 + 1]);
+      xa[2][lane] = as4(z[n1]); xa[3][lane] = as4(z[n1 + 1]);
+    });
+    Slice ds;
+    slice_load<W>(ds, s.x, pair, lane);
+    float dm = 0.f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 x = unpack_b(ds.v[n].x), y = unpack_b(ds.v[n].y);
+      dm = fmaxf(fmaxf(dm, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
+    }
+    const float df = up_scale(warp_max(dm));
+    if (lane == 0 && half == 0) p.do_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(df);
+    Frag x;                                   // do, for the operand here and the update below
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      float2 lo, hi;
+      slice_frag(ds, n, lo, hi);
+      set4(x[n], lo, hi);
+    }
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) frag_a_hi(x, kk, df, hi[kk]);
+    const float zk = si * s.sc[kScK], pi = inv_scale(df) * s.sc[kScP];
+    with_blocks(half, [&](auto b0, auto b1, auto p0, auto p1) {
+      tri_block<false, false>(acc, hi, lo, ps, off, true, b0);
+      tri_block<false, false>(acc, hi, lo, ps, off, true, b1);
+      pair_sync(pair);
+      auto join = [&](auto bb, int at) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = 2 * decltype(bb)::v + i;
+          add4(z[n], ya[at + i][lane]);
+          const float2 ee = mul2(pair_of(s.sc + 64, n, lane), both(zk));
+          set4(z[n], fma2(lo2(acc[n]), both(pi), mul2(lo2(z[n]), ee)), fma2(hi2(acc[n]), both(pi), mul2(hi2(z[n]), ee)));
+        }
+      };
+      join(b0, 0);
+      join(b1, 2);
+      swap_blocks(z, xb, yb, pair, lane, b0, b1, p0, p1);
+    });
+    // y = du + (T - I)^T du
+    const float uf = up_scale(frag_max(z)), ti = inv_scale(uf) * s.sc[kScTB];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) frag_a(z, kk, uf, hi[kk], lo[kk]);
+    with_blocks(half, [&](auto b0, auto b1, auto p0, auto p1) {
+      tri_block<false, true>(acc, hi, lo, ts, off, true, b0);
+      tri_block<false, true>(acc, hi, lo, ts, off, true, b1);
+      constexpr int n0 = 2 * decltype(b0)::v, n1 = 2 * decltype(b1)::v;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        set4(z[n0 + i], fma2(lo2(acc[n0 + i]), both(ti), lo2(z[n0 + i])), fma2(hi2(acc[n0 + i]), both(ti), hi2(z[n0 + i])));
+        set4(z[n1 + i], fma2(lo2(acc[n1 + i]), both(ti), lo2(z[n1 + i])), fma2(hi2(acc[n1 + i]), both(ti), hi2(z[n1 + i])));
+      }
+      swap_blocks(z, xa + 4, ya + 4, pair, lane, b0, b1, p0, p1);
+    });
+    const float yf = up_scale(frag_max(z));
+    {
+      __half* y = static_cast<__half*>(p.y) + (bh * nc + c) * kTc * a.Dv + dv0;
+      with_blocks(half, [&](auto b0, auto b1, auto, auto) {
+        block_store_half(z, yf, y, a.Dv, lane, b0);
+        block_store_half(z, yf, y, a.Dv, lane, b1);
+      });
+      if (lane == 0 && half == 0) p.y_scale[(bh * nc + c) * (a.Dv / 16) + slice] = inv_scale(yf);
+    }
+    frag_scale(z, s.sc + 128, lane);
+    with_blocks(half, [&](auto b0, auto b1, auto, auto) {
+      block_store_seq(z, dv, o_step, a.T - c * kTc, lane, b0);
+      block_store_seq(z, dv, o_step, a.T - c * kTc, lane, b1);
+    });
+    dv -= 8 * o_step;
+    const float xf = yf * s.sc[kScBy], af = df * s.sc[kScBo];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float2 eg = pair_of(s.sc, n, lane), es = mul2(eg, both(a.scale)), em = mul2(eg, both(-1.f));
+      set4(x[n], mul2(lo2(x[n]), es), mul2(hi2(x[n]), es));
+      set4(z[n], mul2(lo2(z[n]), em), mul2(hi2(z[n]), em));
+    }
+    state_update<DK>(S, s.sc[kScEnd], x, af, qs, inv_scale(af) * s.sc[kScQ], off);
+    state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
+  }
+  if (half == 0)
+    zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, ncb * kTc, lane);
+  if (p.ds0) state_store<DKW>(S, p.ds0 + s_off, DK, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1242,6 +1649,8 @@ struct GradSmem {
   float inv[5];
   float own[NW / 2][kTc], thru[NW / 2][kTc], row[NW / 2][kTc], col[2][kTc];
   float red[NW], mx[2][NW];
+  alignas(16) float dG[kTc];     // read in pairs
+  float w[kTc];
 };
 enum { kRs = 0, kRd, kRe, kRy, kRo };
 
@@ -1425,6 +1834,7 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
     // queries to fp16
     auto rescale = [&](unsigned char* at, uint32_t ratio) {
       uint4 v = *reinterpret_cast<uint4*>(at);
+      if (ratio == 0x3c003c00u) return v;               // ones
       const __half2 m = *reinterpret_cast<const __half2*>(&ratio);
       auto mul = [&](uint32_t x) {
         const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), m);
@@ -1663,23 +2073,28 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
             *reinterpret_cast<uint32_t*>(sm.mP + at) = pack_h(Pm[mt][n][2 * half] * pf, Pm[mt][n][2 * half + 1] * pf);
             *reinterpret_cast<uint32_t*>(sm.mA + at) = pack_h(N[mt][n][2 * half] * af, N[mt][n][2 * half + 1] * af);
           }
-      if (warp == 0) {
-        // dg: suffix sums of dG, two tokens a lane
-        float x[2], w = 0.f, f = lane < NW ? sm.red[lane] : 0.f;
+      if (tid < kTc) {
+        // dG of a token, and its part of <S1, dS1>
+        float x = -(sm.col[0][tid] + sm.col[1][tid]), th = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * lane + e;
-          float th = 0.f;
-          x[e] = -(sm.col[0][i] + sm.col[1][i]);
-#pragma unroll
-          for (int q = 0; q < CQ; ++q) {
-            x[e] += sm.row[q][i] + sm.own[q][i];
-            th += sm.thru[q][i];
-          }
-          x[e] -= th;
-          w += th;
+        for (int q = 0; q < CQ; ++q) {
+          x += sm.row[q][tid] + sm.own[q][tid];
+          th += sm.thru[q][tid];
         }
-        float pair = x[0] + x[1];
+        sm.dG[tid] = x - th;
+        sm.w[tid] = th;
+      }
+      if (warp == 2) {
+        for (int t = max(nt, 0) + lane; t < min(kTc, a.T - t0); t += 32) {
+          static_cast<__nv_bfloat16*>(p.dg)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+          static_cast<__nv_bfloat16*>(p.dbeta)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
+        }
+      }
+      __syncthreads();
+      if (warp == NW - 1) {
+        // dg: suffix sums of dG, two tokens a lane
+        const float2 x = *reinterpret_cast<const float2*>(sm.dG + 2 * lane), w2 = *reinterpret_cast<const float2*>(sm.w + 2 * lane);
+        float w = w2.x + w2.y, f = lane < NW ? sm.red[lane] : 0.f, pair = x.x + x.y;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
           const float dn = __shfl_down_sync(kFull, pair, k);
@@ -1688,19 +2103,12 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
           f += __shfl_xor_sync(kFull, f, k);
         }
         const float last = w + sc[kScEnd] * f;
-        const float out[2] = {pair + last, pair - x[0] + last};
+        const float out[2] = {pair + last, pair - x.x + last};
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (2 * lane + e < nt)
             static_cast<__nv_bfloat16*>(p.dg)[a.row(cur.b, t0 + 2 * lane + e) * a.Hv + h] = __float2bfloat16_rn(out[e]);
       }
-      if (warp == 1) {
-        for (int t = max(nt, 0) + lane; t < min(kTc, a.T - t0); t += 32) {
-          static_cast<__nv_bfloat16*>(p.dg)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
-          static_cast<__nv_bfloat16*>(p.dbeta)[a.row(cur.b, t0 + t) * a.Hv + h] = __float2bfloat16_rn(0.f);
-        }
-      }
-      __syncthreads();
       const uint32_t mPs = smem_u32(sm.mP), mAs = smem_u32(sm.mA);
       // x += M B with M taken as stored (rows i) or transposed (rows j)
       auto pairs = [&](float (&x)[2][2][4], uint32_t M, uint32_t B, bool trans) {
@@ -1782,7 +2190,7 @@ int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
   if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
   else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
-  else delta_scan_bwd_kernel<DK, 2><<<grid, 64, sizeof(ScanSmem<DK, 2>), s>>>(t);
+  else delta_pair_bwd_kernel<DK><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
@@ -1803,7 +2211,9 @@ template <int DK>
 int init() {
   const int psm = sizeof(PrepSmem<DK>), gsm = sizeof(GradSmem<DK>);
   return set_smem(delta_prep_kernel<DK, false>, psm) || set_smem(delta_prep_kernel<DK, true>, psm) ||
-                 init_scans<DK, 2>() || init_scans<DK, 4>() || init_scans<DK, 8>() || set_smem(delta_grad_kernel<DK>, gsm)
+                 init_scans<DK, 4>() || init_scans<DK, 8>() || set_smem(delta_grad_kernel<DK>, gsm) ||
+                 set_smem(delta_pair_fwd_kernel<DK, false>, sizeof(PairSmem<DK>)) ||
+                 set_smem(delta_pair_fwd_kernel<DK, true>, sizeof(PairSmem<DK>)) || set_smem(delta_pair_bwd_kernel<DK>, sizeof(PairSmem<DK>))
              ? RNN_CUDA_ERROR
              : 0;
 }

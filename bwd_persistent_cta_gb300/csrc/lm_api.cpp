@@ -400,6 +400,8 @@ rnn_status_t rnn_delta_step(rnn_delta_t h, const rnn_delta_in_t* in, float* stat
   r.s_out = state;
   r.slots = slots;
   r.num_slots = num_slots;
+  r.status = h->status;
+  r.num_sms = h->num_sms;
   r.o = o;
   const int e = launch_delta_recur(r, h->bf16, static_cast<cudaStream_t>(stream));
   if (!e) ++h->launches;

@@ -296,6 +296,53 @@ def test_step(T, B, Hk, Hv, Dk, Dv, dtype):
     np.testing.assert_array_equal(st[untouched], state[untouched])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,Hk,Hv,Dk,Dv", [(1, 70, 2, 8, 128, 128), (2, 61, 4, 8, 64, 128), (1, 130, 3, 3, 96, 72),
+                                             (2, 80, 8, 8, 24, 40), (3, 61, 4, 8, 64, 128), (1, 40, 8, 8, 256, 128)])
+def test_step_many(T, B, Hk, Hv, Dk, Dv, dtype):
+    """Enough states for every CTA to walk several: odd widths, a different number of tokens (none included) for each
+    sequence, slots outside the pool, garbage behind the masks."""
+    import bwd_persistent_cta_gb300 as R
+    torch = _torch()
+    inp = _inputs(T, B, Hk, Hv, Dk, Dv, dtype, 300 + B)
+    lens = [(b * 5 + 1) % (T + 1) if T > 1 else 1 for b in range(B)]
+    for b, n in enumerate(lens):
+        for name in ("q", "k", "v", "g", "beta"):
+            inp[name][n:, b] = np.nan
+    pool = B + 9
+    rng = np.random.default_rng(8)
+    state = rng.normal(size=(pool, Hv, Dv, Dk)).astype(np.float32)
+    slots = rng.permutation(pool)[:B].astype(np.int32)
+    skipped = {3: -1, 17: pool, 30: 2 ** 31 - 1}
+    for b, s in skipped.items():
+        slots[b] = s
+    op = R.DeltaRule(B, T, Hk, Hv, Dk, Dv, dtype=dtype, batch_first=True)
+    op.set_seq_lengths(lens)
+    st = torch.from_numpy(state.copy()).cuda()
+    x = [_dev(inp[n], dtype, bfirst=True, packed=True) for n in ("q", "k", "v", "g", "beta")]
+    sl = torch.from_numpy(slots).cuda()
+    o = _host(op.step(*x, st, slots=sl), True)
+    op.sync()
+    st = st.cpu().numpy()
+    a = [np.nan_to_num(inp[n]) for n in ("q", "k", "v", "g", "beta")]
+    ok = [b for b in range(B) if b not in skipped]
+    s0 = np.stack([state[s] if 0 <= s < pool else np.zeros_like(state[0]) for s in slots])
+    wo, ws, _ = O.delta_forward(*a, s0, lens)
+    want = state.astype(np.float64)
+    for b in ok:
+        want[slots[b]] = ws[b]
+    for b in skipped:
+        wo[:, b] = 0.0
+    _close(o, wo, TOL[dtype], "o")
+    _close(st.astype(np.float64), want, TOL["f32"], "state")
+    for b in range(B):
+        assert np.all(o[lens[b]:, b] == 0.0)
+        if lens[b] == 0 and b not in skipped:
+            np.testing.assert_array_equal(st[slots[b]], state[slots[b]])
+    for b in skipped:
+        assert np.all(o[:, b] == 0.0)
+
+
 def test_step_lengths():
     """A different number of accepted tokens for each sequence, none of them included."""
     import bwd_persistent_cta_gb300 as R
