@@ -284,15 +284,17 @@ __device__ __forceinline__ void warp_mul(float* C, const float* A, const float* 
   }
 }
 
-template <int DK>
+template <int DK, bool TRAIN>
 struct PrepSmem {
   union {
     struct {
       unsigned char K[kTc * DK * 2], Q[kTc * DK * 2];
     } in;
-    float X[2][kTc * kXP];           // the two inverses
+    struct {                         // once K and Q are multiplied
+      float A[kTc * kXP];
+      float X[TRAIN ? 2 : 1][kTc * kXP];   // the inverses
+    };
   };
-  float A[kTc * kXP];
   float Gh[kTc], Gl[kTc], beta[kTc];
   float red[4][4];
 };
@@ -314,10 +316,10 @@ __device__ __forceinline__ float block_max4(float (*red)[4], int ch, float m) {
 // With training, warps 0 and 1 work on (I + A beta)^-1 and 2 and 3 on
 // (I + beta A)^-1, else the second half idles in the inverse.
 template <int DK, bool TRAIN>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
+__global__ void __launch_bounds__(128, TRAIN ? 4 : 6) delta_prep_kernel(const DeltaTcArgs p) {
   constexpr int PK = DK * 2;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  PrepSmem<DK>& sm = *reinterpret_cast<PrepSmem<DK>*>(smem_raw);
+  PrepSmem<DK, TRAIN>& sm = *reinterpret_cast<PrepSmem<DK, TRAIN>*>(smem_raw);
   const DeltaArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nc = (a.T + kTc - 1) / kTc;
@@ -507,8 +509,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaTcArgs p) {
 
   // the inverses: which = 0: L_ij = A_ij beta_j, which = 1: L_ij = beta_i A_ij
   const int which = tid >> 6, col = tid & 63;
-  float* X = sm.X[which];
   const bool mine = TRAIN || which == 0;
+  float* X = sm.X[TRAIN ? which : 0];
   if (mine) {
     const int b0 = col & ~15, jc = col & 15;
     float x[16];
@@ -1269,14 +1271,26 @@ __global__ void __launch_bounds__(128) delta_pair_fwd_kernel(const DeltaTcArgs p
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
 
-// Warps of a scan CTA (16 value columns each): as many as share the chunk's
-// tiles without leaving SMs idle.  A chunk takes a lone pair of warps 3.3 us, four
-// a SM 4.2 and eight 7.2, so a half-filled GPU is better used by small CTAs.
-int scan_warps(const DeltaArgs& a, int num_sms) {
+// 16-column slices a scan CTA takes: 8 or 4, a warp each, or 2 with two warps
+// each.  One CTA is resident on an SM, and a chunk of D = 128 takes it 5.4, 3.25
+// or 2.5 us (measured, inference; the training forward and the reverse scan keep
+// the order), so what counts is the number of turns times that.
+int scan_slices(const DeltaArgs& a, int num_sms) {
   const int n = a.Dv / 16;
-  for (int w = 8; w > 2; w >>= 1)
-    if (n % w == 0 && static_cast<int64_t>(a.B) * a.Hv * (n / w) >= num_sms * 3 / 4) return w;
-  return 2;
+  const int take[3] = {8, 4, 2};
+  const double us[3] = {5.4, 3.25, 2.5};
+  int best = 2;
+  double least = 1e30;
+  for (int i = 0; i < 3; ++i) {
+    if (n % take[i]) continue;
+    const int64_t ctas = static_cast<int64_t>(a.B) * a.Hv * (n / take[i]);
+    const double cost = static_cast<double>((ctas + num_sms - 1) / num_sms) * us[i];
+    if (cost < least) {
+      least = cost;
+      best = take[i];
+    }
+  }
+  return best;
 }
 
 template <typename F>
@@ -1287,12 +1301,12 @@ int set_smem(F* f, int bytes) {
 template <int DK, bool TRAIN>
 int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   const int nc = (t.a.T + kTc - 1) / kTc;
-  const int psm = sizeof(PrepSmem<DK>);
+  const int psm = sizeof(PrepSmem<DK, TRAIN>);
   delta_prep_kernel<DK, TRAIN><<<static_cast<unsigned>(static_cast<int64_t>(nc) * t.a.Hv * t.a.B), 128, psm, s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
-  const int w = scan_warps(t.a, t.num_sms);
+  const int w = scan_slices(t.a, t.num_sms);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
   if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
   else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
@@ -2186,7 +2200,7 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
 template <int DK>
 int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   const int gsm = sizeof(GradSmem<DK>);
-  const int w = scan_warps(t.a, t.num_sms);
+  const int w = scan_slices(t.a, t.num_sms);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
   if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
   else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
@@ -2209,8 +2223,9 @@ int init_scans() {
 }
 template <int DK>
 int init() {
-  const int psm = sizeof(PrepSmem<DK>), gsm = sizeof(GradSmem<DK>);
-  return set_smem(delta_prep_kernel<DK, false>, psm) || set_smem(delta_prep_kernel<DK, true>, psm) ||
+  const int gsm = sizeof(GradSmem<DK>);
+  return set_smem(delta_prep_kernel<DK, false>, sizeof(PrepSmem<DK, false>)) ||
+                 set_smem(delta_prep_kernel<DK, true>, sizeof(PrepSmem<DK, true>)) ||
                  init_scans<DK, 4>() || init_scans<DK, 8>() || set_smem(delta_grad_kernel<DK>, gsm) ||
                  set_smem(delta_pair_fwd_kernel<DK, false>, sizeof(PairSmem<DK>)) ||
                  set_smem(delta_pair_fwd_kernel<DK, true>, sizeof(PairSmem<DK>)) || set_smem(delta_pair_bwd_kernel<DK>, sizeof(PairSmem<DK>))
