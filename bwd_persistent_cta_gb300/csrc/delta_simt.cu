@@ -55,6 +55,9 @@ __device__ __forceinline__ void load_vec(const T* p, bool in, float (&v)[VPL]) {
       Vec4<T>::load(p + i, t);
       v[i] = t[0]; v[i + 1] = t[1]; v[i + 2] = t[2]; v[i + 3] = t[3];
     }
+  } else if constexpr (VPL == 2 && sizeof(T) == 4) {
+    const float2 t = *reinterpret_cast<const float2*>(p);
+    v[0] = t.x; v[1] = t.y;
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = to_f<T>(p[i]);
@@ -199,6 +202,8 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
   if (!AHEAD && len > 0) direct(0);
   const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
   const int nc = (a.T + kSimtChunk - 1) / kSimtChunk;
+  T* ot = o + lane;                         // this token's output and e
+  float* et = r.e + (bh * a.T * a.Dv + dv0 + lane);
   for (int t = 0; t < len; ++t) {
     if (AHEAD) {
       const int n = t % kAhead;
@@ -247,9 +252,11 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
     const float e = vc - al * sk;
     const float u = bc * e;
     if (vin) {
-      o[t * ts * o_row + lane] = from_f<T>(a.scale * fmaf(al, sq, u * kq));
-      if (r.e) r.e[(bh * a.T + t) * a.Dv + dv0 + lane] = e;
+      *ot = from_f<T>(a.scale * fmaf(al, sq, u * kq));
+      if (r.e) *et = e;
     }
+    ot += ts * o_row;
+    et += a.Dv;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float ui = __shfl_sync(kFull, u, i);
@@ -459,6 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
     const bool ok = in && r.dsT != nullptr && dv0 + i < a.Dv;
     load_vec<float, VPL>(r.dsT + bh * head_elems + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, dS[i]);
   }
+  float* yt = r.y + ((bh * a.T + len - 1) * a.Dv + dv0 + lane);
   for (int it = 0; it < len; ++it) {
     const int t = len - 1 - it, n = it % kAhead;
     if (n == 0) {
@@ -490,7 +498,8 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
     }
     const float sum = warp_sum_many<R>(d, lane);
     const float y = __shfl_sync(kFull, sum, sum_lane<R>(1) * (lane < R ? lane : 0));
-    if (vin) r.y[(bh * a.T + t) * a.Dv + dv0 + lane] = y;
+    if (vin) *yt = y;
+    yt -= a.Dv;
     const float de = bc * y;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -601,30 +610,50 @@ __global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBw
     for (int jj = 0; jj < 4; ++jj) N[jj] = Pm[jj] = 0.f;
 #pragma unroll
     for (int m = 0; m < M; ++m) dq1[m] = dk1[m] = dk3[m] = 0.f;
-    for (int v0 = 0; v0 < a.Dv; v0 += kSlice) {
-      __syncthreads();
-      for (int x = tid; x < kCb * kSlice; x += 256) {
-        const int ti = x / kSlice, d = x % kSlice;
+    // a slice waits in registers while the one before it is multiplied
+    constexpr int NV = kCb * kSlice / 256, NS = kSlice * DKM / 256;
+    float re[NV], ry[NV], ro[NV], rs[NS], rd[NS];
+    auto fetch = [&](int v0) {
+#pragma unroll
+      for (int p = 0; p < NV; ++p) {
+        const int x = tid + p * 256, ti = x / kSlice, d = x % kSlice;
         const bool ok = ti < nt && v0 + d < a.Dv;
         const int64_t at = ok ? (bh * a.T + t0 + ti) * a.Dv + v0 + d : 0;
         const int64_t row = a.row(b, t0 + (ok ? ti : 0));
-        const float be = ok ? sm.beta[ti] : 0.f;
-        const float y = ok ? r.y[at] : 0.f;
-        sm.E[ti][d] = ok ? r.e[at] : 0.f;
-        sm.Y[ti][d] = y;
-        sm.dO[ti][d] = ok ? to_f<T>(static_cast<const T*>(r.dout)[row * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d]) : 0.f;
-        if (ok) static_cast<T*>(r.dv)[row * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d] = from_f<T>(be * y);
+        ry[p] = ok ? r.y[at] : 0.f;
+        re[p] = ok ? r.e[at] : 0.f;
+        ro[p] = ok ? to_f<T>(static_cast<const T*>(r.dout)[row * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d]) : 0.f;
       }
-      for (int x = tid; x < kSlice * a.Dk; x += 256) {
-        const int d = x / a.Dk, kx = x - d * a.Dk;
-        const bool ok = v0 + d < a.Dv;
-        const int64_t at = (bh * nc + c) * head_elems + static_cast<int64_t>(ok ? v0 + d : 0) * a.Dk + kx;
-        const float s0 = ok ? r.s0[at] : 0.f, ds = ok ? r.ds1[at] : 0.f;
-        sm.S0[d][kx] = s0;
-        sm.dS[d][kx] = ds;
-        frob = fmaf(s0, ds, frob);
+#pragma unroll
+      for (int p = 0; p < NS; ++p) {
+        const int x = tid + p * 256, d = x / DKM, kx = x % DKM;
+        const bool ok = v0 + d < a.Dv && kx < a.Dk;
+        const int64_t at = ok ? (bh * nc + c) * head_elems + static_cast<int64_t>(v0 + d) * a.Dk + kx : 0;
+        rs[p] = ok ? r.s0[at] : 0.f;
+        rd[p] = ok ? r.ds1[at] : 0.f;
+      }
+    };
+    fetch(0);
+    for (int v0 = 0; v0 < a.Dv; v0 += kSlice) {
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < NV; ++p) {
+        const int x = tid + p * 256, ti = x / kSlice, d = x % kSlice;
+        sm.E[ti][d] = re[p];
+        sm.Y[ti][d] = ry[p];
+        sm.dO[ti][d] = ro[p];
+        if (ti < nt && v0 + d < a.Dv)
+          static_cast<T*>(r.dv)[a.row(b, t0 + ti) * v_row + static_cast<int64_t>(h) * a.Dv + v0 + d] = from_f<T>(sm.beta[ti] * ry[p]);
+      }
+#pragma unroll
+      for (int p = 0; p < NS; ++p) {
+        const int x = tid + p * 256, d = x / DKM, kx = x % DKM;
+        sm.S0[d][kx] = rs[p];
+        sm.dS[d][kx] = rd[p];
+        frob = fmaf(rs[p], rd[p], frob);
       }
       __syncthreads();
+      if (v0 + kSlice < a.Dv) fetch(v0 + kSlice);
       for (int d = 0; d < kSlice; ++d) {
         const float y = sm.Y[i][d], e = sm.E[i][d], dO = sm.dO[i][d];
 #pragma unroll
@@ -642,7 +671,7 @@ __global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBw
         }
       }
     }
-    // columns beyond Dk hold stale shared memory: mask them
+    // columns beyond Dk: keys and queries there are not loaded
     const float bi = sm.beta[i], eG = sm.eG[i];
     float own = 0.f, thru = 0.f;
 #pragma unroll
