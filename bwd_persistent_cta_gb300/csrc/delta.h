@@ -46,8 +46,7 @@ struct DeltaRecurArgs {
   void* o;
   float* ckpt;                 // S0 of every chunk, or null
   float* e;                    // E, or null
-  // the serving step: where a bounded wait reports, and the GPU's size
-  unsigned int* status;
+  unsigned int* status;        // the serving step: where a bounded wait reports
   int num_sms;
 };
 int launch_delta_recur(const DeltaRecurArgs& r, int is_bf16, cudaStream_t s);
@@ -59,6 +58,7 @@ struct DeltaRecurBwdArgs {
   float* ds0;                  // or null
   float* ckpt;                 // dS1 of every chunk
   float* y;
+  int num_sms;
 };
 int launch_delta_recur_bwd(const DeltaRecurBwdArgs& r, int is_bf16, cudaStream_t s);
 

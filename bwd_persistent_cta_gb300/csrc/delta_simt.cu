@@ -140,7 +140,9 @@ __device__ __forceinline__ void stage_ready(TokenStage<T, VPL, R>& st, float2 gb
 // the warp.  Both are taken of the old state: S_t q = a (S q) + u (k . q).
 // One token costs the chain exp -> dot -> shuffles -> update.  AHEAD: tokens come
 // through shared memory a stage early (sequences); otherwise each is loaded one
-// token early (the serving step, where the state is what takes time).
+// token early (the serving step, where the state is what takes time).  Bound by
+// that chain: 0.29 us a token at 1024 rows of 64 in fp32 (0.56 when each token
+// was loaded one token early); the reverse below 0.27.
 template <typename T, int VPL, int R, bool AHEAD>
 __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRecurArgs r) {
   constexpr int kAhead = TokenStage<T, VPL, R>::kAhead;
@@ -279,6 +281,8 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 // walks units of 32 state rows with a stride; a unit (contiguous, 128 Dk bytes) is
 // fetched by one bulk copy kUnits units early, its token inputs one unit early.
 // Warp w computes rows 8 w .. 8 w + 7 and writes them back from registers.
+// 256 sequences of 32 heads of 128 x 128 (1.08 GB): 173 us, 6.2 TB/s; loads into
+// registers without the pipeline took 203 (8 rows a warp) to 213 us (4).
 constexpr int kUnits = 4;
 constexpr int kUnitRows = 32;
 constexpr uint64_t kStepTimeoutNs = 2000000000ull;     // of a wait for a unit's copy
@@ -530,7 +534,9 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
 // The decay gradient uses the pair sums, not q . dq - k . dk of whole rows, so
 // that a pair on one side of a token cancels exactly instead of to rounding.
 // Thread (i, l) of 256 owns token i and key columns l, l + 8, ...; the value
-// columns pass in slices of 16.
+// columns pass in slices of 16, the next one on its way meanwhile.  Bound by
+// shared memory reads, one for each multiply-add or two: 62 us for 68 chunks of
+// two heads of 64 x 128 (110 before slices were fetched early).
 constexpr int kCb = kSimtChunk;      // tokens
 constexpr int kSlice = 16;           // value columns a pass
 
@@ -770,6 +776,12 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 
 int vpl_of(int Dk) { return Dk <= 32 ? 1 : Dk <= 64 ? 2 : Dk <= 128 ? 4 : 8; }
 
+// Where four rows a warp would leave schedulers without one, two: a token's
+// chain is then shorter (fp32, 1024 rows of 64, 513 tokens: 149 against 168 us).
+bool few_rows(const DeltaArgs& a, int num_sms) {
+  return static_cast<int64_t>(a.B) * a.Hv * a.Dv <= 16ll * num_sms;
+}
+
 // Sequences of at least this many tokens are staged.
 constexpr int kAheadFrom = 8;
 
@@ -781,7 +793,7 @@ int recur(const DeltaRecurArgs& r, cudaStream_t s) {
 }
 template <typename T, int VPL>
 int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
-  if (r.a.T >= kAheadFrom) return recur<T, VPL, 4, true>(r, s);
+  if (r.a.T >= kAheadFrom) return few_rows(r.a, r.num_sms) ? recur<T, VPL, 2, true>(r, s) : recur<T, VPL, 4, true>(r, s);
   if constexpr (VPL <= 4) {
     // A step over more units than three CTAs an SM take in two turns.  With more
     // than two tokens the chain of a unit is longer than its transfer and the
@@ -813,13 +825,17 @@ int recur_bwd(const DeltaRecurBwdArgs& r, cudaStream_t s) {
   delta_recur_bwd_kernel<T, VPL, R><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
   return check_launch();
 }
+template <typename T, int VPL>
+int recur_bwd_v(const DeltaRecurBwdArgs& r, cudaStream_t s) {
+  return few_rows(r.a, r.num_sms) ? recur_bwd<T, VPL, 2>(r, s) : recur_bwd<T, VPL, 4>(r, s);
+}
 template <typename T>
 int recur_bwd_t(const DeltaRecurBwdArgs& r, cudaStream_t s) {
   switch (vpl_of(r.a.Dk)) {
-    case 1: return recur_bwd<T, 1, 4>(r, s);
-    case 2: return recur_bwd<T, 2, 4>(r, s);
-    case 4: return recur_bwd<T, 4, 4>(r, s);
-    default: return recur_bwd<T, 8, 4>(r, s);
+    case 1: return recur_bwd_v<T, 1>(r, s);
+    case 2: return recur_bwd_v<T, 2>(r, s);
+    case 4: return recur_bwd_v<T, 4>(r, s);
+    default: return recur_bwd_v<T, 8>(r, s);
   }
 }
 template <typename T, int DKM>

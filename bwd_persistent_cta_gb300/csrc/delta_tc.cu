@@ -315,6 +315,9 @@ __device__ __forceinline__ float block_max4(float (*red)[4], int ch, float m) {
 // appears, so keys that are all alike (L with entries near one) cost no accuracy.
 // With training, warps 0 and 1 work on (I + A beta)^-1 and 2 and 3 on
 // (I + beta A)^-1, else the second half idles in the inverse.
+// Bound by latency: short phases between barriers, four to six CTAs an SM.  Chunks
+// of D = 128: 4096 in 123 us (training), 8192 in 170 us (inference); joining the
+// inverses in fp32 on the CUDA cores took 157 and 245.
 template <int DK, bool TRAIN>
 __global__ void __launch_bounds__(128, TRAIN ? 4 : 6) delta_prep_kernel(const DeltaTcArgs p) {
   constexpr int PK = DK * 2;
@@ -891,7 +894,10 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16* base, const DeltaArgs& 
 // ---------------------------------------------------------------------------
 // the forward scan
 // ---------------------------------------------------------------------------
-// W warps of one value head, 16 value columns each.
+// W warps of one value head, 16 value columns each.  A chunk of D = 128 is 400
+// products m16n8k16 a warp, 8.2 cycles each on a scheduler: 1.7 us of the 3.25
+// (W = 4, inference); with two warps a scheduler (W = 8) 3.5 of 5.4.  The rest is
+// the chain of scaling and splitting between dependent products.
 template <int DK, bool TRAIN, int W>
 __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArgs p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -1041,7 +1047,9 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
 // chain.  Two warps then share 16 value columns: each keeps half of the state's
 // key columns (half the products with the state, and half of its update) and
 // finishes half of the token blocks, 0 and 3 or 1 and 2 (the same number of
-// triangular products).  Partial sums and finished blocks cross through shared
+// triangular products).  A chunk of D = 128 takes 2.4 us instead of 3.0 for a lone
+// warp (16384 tokens, 32 heads: 623 against 772 us), not half: both warps split
+// the whole of r and u.  Partial sums and finished blocks cross through shared
 // memory, two exchanges a chunk forward and three backward, on a barrier of the
 // two warps.
 template <int DK>
@@ -1638,6 +1646,10 @@ __global__ void __launch_bounds__(128) delta_pair_bwd_kernel(const DeltaTcBwdArg
 // ---------------------------------------------------------------------------
 // the gradients of q, k, g and beta, all chunks at once
 // ---------------------------------------------------------------------------
+// Bound by what surrounds the products, not by them (24 % of the tensor pipe) nor
+// by memory (1.6 of 6.8 TB/s): ldmatrix and its waits, scaling, sums across warps.
+// 4096 chunks of D = 128 in 362 us.  Eight warps with tiles of 32 x 32 took 428;
+// rescaling A operands in the products instead of pieces on arrival 407.
 // The sums of delta_chunk_bwd_kernel (delta_simt.cu) on the tensor cores, with
 // single fp16 operands: every output is rounded to bf16, 8 times coarser.  A CTA
 // walks chunks of a key head with a stride; per value head the value columns

@@ -321,6 +321,7 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
   r.s_in = s0;
   r.s_out = sT;
   r.num_slots = -1;
+  r.num_sms = h->num_sms;
   r.o = o;
   r.ckpt = reserve ? at<float>(reserve, h->r_s0) : nullptr;
   r.e = reserve ? at<float>(reserve, h->r_e) : nullptr;
@@ -371,6 +372,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   b.ds0 = ds0;
   b.ckpt = at<float>(workspace, h->b_ds1);
   b.y = at<float>(workspace, h->b_y);
+  b.num_sms = h->num_sms;
   int e = launch_delta_recur_bwd(b, h->bf16, s);
   if (e) return static_cast<rnn_status_t>(e);
   ++h->launches;

@@ -190,6 +190,8 @@ struct Walk {
 // with a residual or an outgoing norm (else both are compiled out).  A thread
 // keeps its columns' weights, and loads its next row before it works on this
 // one (IT = 1), which keeps the memory busy through the row sums.
+// bf16, all parts on, 16384 rows of 2048: 60 us, 5.6 TB/s; 262144 groups of 128
+// with a gate: 37 us, 5.4 TB/s.
 template <typename T, int kVec, int TPR, int IT, bool FULL>
 __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(const NormArgs a) {
   constexpr int RPB = (TPR > kBlock ? TPR : kBlock) / TPR, V2 = kVec / 2;
@@ -290,7 +292,10 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(c
 // keeps its columns' weight gradients in registers; the CTAs' partial sums are
 // added by a second kernel in a fixed order.  A row costs three dependent sums,
 // so its rows to come wait in shared memory (NS deep, each thread its own slots,
-// no barrier), not in registers: three CTAs an SM hide the sums.
+// no barrier), not in registers: three CTAs an SM hide the sums.  bf16, all parts
+// on, 16384 rows of 2048: 124 us, 4.3 TB/s, 60 % of the issue slots (rows ahead in
+// registers, two CTAs: 142 us; half the columns a thread: 187 us); 262144 groups
+// of 128 with a gate: 56 us, 6.0 TB/s.
 template <typename T, int V, int TPR, int IT, bool FULL>
 struct BwdSmem {
   static constexpr int NT = TPR > kBlock ? TPR : kBlock, STREAMS = FULL ? 5 : 3, WEIGHTS = FULL ? 3 : 1;

@@ -156,6 +156,23 @@ def test_shapes(shape, dtype):
     _compare(_run(inp, dtype), _want(inp), dtype)
 
 
+@pytest.mark.parametrize("shape", [(100, 1, 1, 2, 64, 96), (90, 1, 1, 1, 128, 32), (70, 2, 1, 1, 128, 160),
+                                   (66, 1, 2, 2, 64, 256)], ids=str)
+def test_value_widths_on_tensor_cores(shape):
+    inp = _inputs(*shape, "bf16", 15 + shape[5])
+    _compare(_run(inp, "bf16"), _want(inp), "bf16")
+
+
+@pytest.mark.parametrize("shape", [(130, 2, 25, 50, 64, 128), (130, 1, 25, 50, 128, 128), (130, 1, 20, 80, 64, 64),
+                                   (70, 2, 80, 80, 128, 128)], ids=str)
+def test_many_heads(shape):
+    """Enough heads that one CTA takes four and eight slices of a head's value columns, and more than one turn."""
+    T, B = shape[:2]
+    inp = _inputs(*shape, "bf16", 17)
+    lens = [T, T - 37][:B]
+    _compare(_run(inp, "bf16", bfirst=True, lens=lens), _want(inp, lens), "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bfirst", [False, True])
 def test_packed_rows_and_masked_garbage(dtype, bfirst):
