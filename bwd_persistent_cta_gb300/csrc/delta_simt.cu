@@ -798,7 +798,7 @@ int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
     // A step over more units than three CTAs an SM take in two turns.  With more
     // than two tokens the chain of a unit is longer than its transfer and the
     // recurrence's larger number of warps wins (256 sequences x 32 heads x 128 x 128,
-    // one token: 173 us against 203; 48 x 16, four tokens: 30.0 against 27.7).
+    // one token: 173 us against 203; 48 x 16, four tokens: 30.0 against 25.6).
     const int64_t units = static_cast<int64_t>((r.a.Dv + kUnitRows - 1) / kUnitRows) * r.a.Hv * r.a.B;
     if (r.status && r.a.T <= 2 && units >= 6 * r.num_sms && units + 3ll * kUnits * r.num_sms < (1ll << 31)) {
       const int smem = sizeof(StepSmem<VPL>);
@@ -807,6 +807,11 @@ int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
       delta_step_kernel<T, VPL><<<3 * r.num_sms, kWarps * 32, smem, s>>>(r);
       return check_launch();
     }
+  }
+  if constexpr (VPL <= 4) {
+    // several tokens for many states: bound by issue, where eight rows share a
+    // token's work (48 sequences x 16 heads, four tokens: 25.6 against 27.6 us)
+    if (static_cast<int64_t>(r.a.B) * r.a.Hv * r.a.Dv >= 256ll * r.num_sms && r.a.T > 1) return recur<T, VPL, 8, false>(r, s);
   }
   return recur<T, VPL, 4, false>(r, s);
 }
