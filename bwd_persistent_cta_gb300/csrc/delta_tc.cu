@@ -34,11 +34,14 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr uint64_t kScanTimeoutNs = 2000000000ull;     // of a wait for a chunk's copies
 
 // --- scales and fragments -----------------------------------------------------
-// The power of two that brings m to [2^13, 2^14), and its inverse.
+// The power of two that brings m to [2^13, 2^14), and its inverse.  NaN when m is
+// an infinity or NaN: the whole tile then shows it, instead of its other values
+// losing their bits to a scale of no use.
 __device__ __forceinline__ float up_scale(float m) {
-  int f = 267 - ((__float_as_int(m) >> 23) & 255);
+  const int e = (__float_as_int(m) >> 23) & 255;
+  int f = 267 - e;
   f = f < 1 ? 1 : f > 253 ? 253 : f;
-  return __int_as_float(f << 23);
+  return __int_as_float(e == 255 ? 0x7fc00000 : f << 23);
 }
 __device__ __forceinline__ float inv_scale(float f) { return __int_as_float((254 << 23) - __float_as_int(f)); }
 

@@ -218,6 +218,36 @@ def test_resets_strong_decay_and_no_writes(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta"])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_bad_values_show(dtype, name, bad):
+    """A NaN or an infinity in a valid token reaches that token's output or its state, and nothing turns into a wrong
+    finite number: what is finite is right, and earlier chunks and other sequences are untouched."""
+    import bwd_persistent_cta_gb300 as R
+    torch = _torch()
+    T, B, H, D = 150, 2, 1, 64
+    inp = _inputs(T, B, H, H, D, D, dtype, 45)
+    a = [inp[n] for n in ("q", "k", "v", "g", "beta")]
+    wo, ws, _ = O.delta_forward(*a, inp["s0"])
+    x = {n: inp[n].copy() for n in ("q", "k", "v", "g", "beta")}
+    x[name][70, 0] = bad
+    op = R.DeltaRule(B, T, H, H, D, D, dtype=dtype)
+    o, sT = op.forward(*(_dev(x[n], dtype) for n in ("q", "k", "v", "g", "beta")), s0=torch.from_numpy(inp["s0"]).cuda(),
+                       train=False)
+    o, sT = _host(o), _host(sT)
+    _close(o[:64, 0], wo[:64, 0], TOL[dtype], "earlier chunk")
+    _close(o[:, 1], wo[:, 1], TOL[dtype], "other sequence")
+    _close(sT[1], ws[1], STATE_TOL[dtype], "other state")
+    assert not np.all(np.isfinite(o[70, 0]))
+    fine = np.isfinite(o[64:70, 0])
+    d = np.abs(o[64:70, 0] - wo[64:70, 0])[fine]
+    assert np.all(d <= 40 * TOL[dtype] * np.abs(wo).max())
+    if name != "q":
+        assert not np.all(np.isfinite(o[71:, 0])) and not np.all(np.isfinite(sT[0]))
+        assert not np.any(np.isfinite(o[128:, 0]).all(-1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_equal_keys(dtype):
     """One key repeated with full write strength, the worst case for the inverse inside a chunk: the state holds the last
     value exactly."""
