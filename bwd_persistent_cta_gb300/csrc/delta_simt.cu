@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
     for (int i = 0; i < R; ++i) {
       const float ui = __shfl_sync(kFull, u, i);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(ui, kc[j], al * S[i][j]);
+      for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(al, S[i][j], ui * kc[j]);      // one rounding of the state's size
     }
   }
   for (int t = len; t < a.T; ++t)
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_step_kernel(const DeltaRecu
       for (int i = 0; i < R; ++i) {
         const float ui = __shfl_sync(kFull, uu, i);
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(ui, kc[j], al * S[i][j]);
+        for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(al, S[i][j], ui * kc[j]);      // one rounding of the state's size
       }
     }
     for (int t = cur.len; t < a.T; ++t)
@@ -489,16 +489,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
         if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, dS[i]);
     }
     const float al = expf(gc);
-    float d[R];
+    float d[R], dd[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float di = a.scale * __shfl_sync(kFull, dc, i);
+      dd[i] = a.scale * __shfl_sync(kFull, dc, i);
       d[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        dS[i][j] = fmaf(di, qc[j], dS[i][j]);
-        d[i] = fmaf(dS[i][j], kc[j], d[i]);
-      }
+      for (int j = 0; j < VPL; ++j) d[i] = fmaf(fmaf(dd[i], qc[j], dS[i][j]), kc[j], d[i]);
     }
     const float sum = warp_sum_many<R>(d, lane);
     const float y = __shfl_sync(kFull, sum, sum_lane<R>(1) * (lane < R ? lane : 0));
@@ -509,7 +506,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
     for (int i = 0; i < R; ++i) {
       const float ei = __shfl_sync(kFull, de, i);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) dS[i][j] = al * fmaf(-ei, kc[j], dS[i][j]);
+      for (int j = 0; j < VPL; ++j) dS[i][j] = fmaf(al, dS[i][j], al * fmaf(dd[i], qc[j], -ei * kc[j]));
     }
   }
   if (r.ds0 && in) {
