@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <new>
 
+#include "call_order.h"
 #include "delta.h"
 #include "delta_tc.h"
 #include "device_guard.h"
@@ -22,6 +23,7 @@ struct rnn_delta_s {
   size_t es;
   int* d_len;
   int has_len;
+  CallOrder order;             // of the calls that read d_len
   unsigned int* status;        // device word
   uint64_t launches;
   // byte offsets.  Forward workspace (tensor cores): the tiles of prep; a
@@ -164,6 +166,23 @@ rnn_status_t delta_args(const rnn_delta_s* h, const rnn_delta_in_t* in, DeltaArg
   return RNN_OK;
 }
 
+// A call's place among the handle's calls that read the lengths (others share
+// nothing on the device that they change).
+struct Ordered {
+  rnn_delta_s* h;
+  cudaStream_t s;
+  bool on;
+  rnn_status_t rc = RNN_OK;
+  Ordered(rnn_delta_s* h_, cudaStream_t s_) : h(h_), s(s_), on(h_->has_len) {
+    if (on) rc = h->order.enter(s);
+  }
+  // The call's status; what was launched before a failure counts as well.
+  rnn_status_t done(int e) {
+    const rnn_status_t l = on ? h->order.leave(s) : RNN_OK;
+    return e ? static_cast<rnn_status_t>(e) : l;
+  }
+};
+
 template <typename T>
 T* at(const void* base, size_t off) {
   return reinterpret_cast<T*>(const_cast<char*>(static_cast<const char*>(base)) + off);
@@ -247,7 +266,7 @@ rnn_status_t rnn_delta_create(const rnn_delta_desc_t* desc, rnn_delta_t* out) {
     delete h;
     return RNN_CUDA_ERROR;
   }
-  if (cudaMemset(h->status, 0, sizeof(unsigned int)) != cudaSuccess) {
+  if (cudaMemset(h->status, 0, sizeof(unsigned int)) != cudaSuccess || h->order.create() != RNN_OK) {
     cudaFree(h->status);
     delete h;
     return RNN_CUDA_ERROR;
@@ -262,6 +281,7 @@ rnn_status_t rnn_delta_destroy(rnn_delta_t h) {
   DeviceGuard dg(h->device);
   if (h->d_len) cudaFree(h->d_len);
   cudaFree(h->status);
+  h->order.destroy();
   delete h;
   return RNN_OK;
 }
@@ -289,7 +309,13 @@ rnn_status_t rnn_delta_set_seq_lengths(rnn_delta_t h, const int* lengths) {
     h->d_len = nullptr;
     return RNN_CUDA_ERROR;
   }
-  if (cudaMemcpy(h->d_len, lengths, sizeof(int) * B, cudaMemcpyHostToDevice) != cudaSuccess) return RNN_CUDA_ERROR;
+  // no call may still read the old lengths, and none may start before the new
+  // ones have landed: a copy from pageable memory can return earlier, and streams
+  // that do not wait for the legacy stream would not wait for it either
+  if (h->order.wait() != RNN_OK ||
+      cudaMemcpy(h->d_len, lengths, sizeof(int) * B, cudaMemcpyHostToDevice) != cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)
+    return RNN_CUDA_ERROR;
   h->has_len = 1;
   return RNN_OK;
 }
@@ -303,6 +329,9 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
   if ((h->workspace_bytes && !workspace) || !aligned16(workspace) || !aligned16(reserve)) return RNN_BAD_WORKSPACE;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Ordered call(h, s);
+  if (call.rc != RNN_OK) return call.rc;
   if (h->tc) {
     DeltaTcArgs t{};
     t.a = r.a;
@@ -314,9 +343,9 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
     t.train = reserve != nullptr;
     t.num_sms = h->num_sms;
     int n = 0;
-    const int e = launch_delta_tc_forward(t, static_cast<cudaStream_t>(stream), &n);
+    const int e = launch_delta_tc_forward(t, s, &n);
     h->launches += n;
-    return static_cast<rnn_status_t>(e);
+    return call.done(e);
   }
   r.s_in = s0;
   r.s_out = sT;
@@ -325,9 +354,9 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
   r.o = o;
   r.ckpt = reserve ? at<float>(reserve, h->r_s0) : nullptr;
   r.e = reserve ? at<float>(reserve, h->r_e) : nullptr;
-  const int e = launch_delta_recur(r, h->bf16, static_cast<cudaStream_t>(stream));
+  const int e = launch_delta_recur(r, h->bf16, s);
   if (!e) ++h->launches;
-  return static_cast<rnn_status_t>(e);
+  return call.done(e);
 }
 
 rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const void* do_, const float* dsT, void* dq,
@@ -345,6 +374,8 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   DeviceGuard guard(h->device);
   if (!guard.ok) return RNN_CUDA_ERROR;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Ordered call(h, s);
+  if (call.rc != RNN_OK) return call.rc;
   if (h->tc) {
     DeltaTcBwdArgs t{};
     t.a = a;
@@ -363,7 +394,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
     int n = 0;
     const int e = launch_delta_tc_backward(t, s, &n);
     h->launches += n;
-    return static_cast<rnn_status_t>(e);
+    return call.done(e);
   }
   DeltaRecurBwdArgs b{};
   b.a = a;
@@ -374,7 +405,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   b.y = at<float>(workspace, h->b_y);
   b.num_sms = h->num_sms;
   int e = launch_delta_recur_bwd(b, h->bf16, s);
-  if (e) return static_cast<rnn_status_t>(e);
+  if (e) return call.done(e);
   ++h->launches;
   DeltaChunkBwdArgs c{};
   c.a = a;
@@ -386,7 +417,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   c.dq = dq; c.dk = dk; c.dv = dv; c.dg = dg; c.dbeta = dbeta;
   e = launch_delta_chunk_bwd(c, h->bf16, s);
   if (!e) ++h->launches;
-  return static_cast<rnn_status_t>(e);
+  return call.done(e);
 }
 
 rnn_status_t rnn_delta_step(rnn_delta_t h, const rnn_delta_in_t* in, float* state, int num_slots, const int* slots,
@@ -405,9 +436,12 @@ rnn_status_t rnn_delta_step(rnn_delta_t h, const rnn_delta_in_t* in, float* stat
   r.status = h->status;
   r.num_sms = h->num_sms;
   r.o = o;
-  const int e = launch_delta_recur(r, h->bf16, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Ordered call(h, s);
+  if (call.rc != RNN_OK) return call.rc;
+  const int e = launch_delta_recur(r, h->bf16, s);
   if (!e) ++h->launches;
-  return static_cast<rnn_status_t>(e);
+  return call.done(e);
 }
 
 rnn_status_t rnn_delta_sync_status(rnn_delta_t h, void* stream) {

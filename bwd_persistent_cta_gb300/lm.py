@@ -243,7 +243,8 @@ class DeltaRule(_Op):
         self._check(rnn_delta_sync_status(self.handle, self._on(stream)), "rnn_delta_sync_status")
 
     def set_seq_lengths(self, lengths):
-        """Valid tokens per sequence (batch ints), or None for full length."""
+        """Valid tokens per sequence (batch ints), or None for full length, for the calls made from now on; waits for the
+        calls before that have lengths of their own."""
         if lengths is not None and len(lengths) != self.desc.batch:
             raise ValueError("one length per sequence of the batch")
         self._check(rnn_delta_set_seq_lengths(self.handle, lengths), "rnn_delta_set_seq_lengths")

@@ -406,7 +406,11 @@ rnn_status_t rnn_delta_get_sizes(rnn_delta_t handle, size_t* workspace_bytes,
 /* Valid tokens per sequence, as rnn_set_seq_lengths: a host array of batch
  * ints in [0, seq_len], or NULL for full length.  Tokens at t >= lengths[b]
  * are not read: the state stays as it was, o is zero there and so are all
- * gradients; with length 0 the state passes through. */
+ * gradients; with length 0 the state passes through.  The lengths hold for the
+ * calls made from then on.  Calls made before keep theirs: setting new ones
+ * waits on the host until they have run (where a call was captured into a
+ * graph, until the device is idle: a replay reads the lengths set last).  A
+ * backward must see the lengths of its forward. */
 rnn_status_t rnn_delta_set_seq_lengths(rnn_delta_t handle, const int* lengths);
 
 /* Forward over whole sequences.

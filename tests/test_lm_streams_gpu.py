@@ -1,0 +1,103 @@
+"""Calls of DeltaRule and BlockNorm on streams.  A device-side delay holds one
+stream back, so that what is not ordered happens in the wrong order."""
+import numpy as np
+import pytest
+
+from oracle import lm_oracle as O
+
+from tests.test_delta_gpu import STATE_TOL, TOL, _close, _dev, _host, _inputs
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("q", "k", "v", "g", "beta")
+DELAY = 400_000_000            # cycles: about 0.2 s
+
+
+def _delay():
+    import torch
+    torch.cuda._sleep(DELAY)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lengths_change_behind_a_queued_forward(dtype):
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    T, B, H, D = 130, 3, 2, 64
+    first, second = [130, 20, 65], [3, 128, 0]
+    inp = _inputs(T, B, H, H, D, D, dtype, 401)
+    a = [inp[n] for n in NAMES]
+    op = R.DeltaRule(B, T, H, H, D, D, dtype=dtype)
+    s = torch.cuda.Stream()
+    x = [_dev(t, dtype) for t in a]
+    s0 = torch.from_numpy(inp["s0"]).cuda()
+    op.forward(*x, s0=s0, train=False)           # a kernel's first launch may wait for the device
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        op.set_seq_lengths(first)
+        _delay()
+        got = [op.forward(*x, s0=s0, train=False)]
+        op.set_seq_lengths(second)
+        got.append(op.forward(*x, s0=s0, train=False))
+    torch.cuda.synchronize()
+    for lens, (o, sT) in zip((first, second), got):
+        wo, ws, _ = O.delta_forward(*a, inp["s0"], lens)
+        _close(_host(o), wo, TOL[dtype], f"o of lengths {lens}")
+        _close(_host(sT), ws, STATE_TOL[dtype], f"state of lengths {lens}")
+
+
+@pytest.mark.parametrize("T", [3, 12])
+def test_lengths_change_behind_a_queued_step(T):
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    B, H, D = 3, 2, 64
+    first, second = [T, 1, 2], [1, T, 0]
+    inp = _inputs(T, B, H, H, D, D, "bf16", 402)
+    a = [inp[n] for n in NAMES]
+    op = R.DeltaRule(B, T, H, H, D, D)
+    s = torch.cuda.Stream()
+    x = [_dev(t, "bf16") for t in a]
+    st = torch.from_numpy(inp["s0"]).cuda()
+    op.step(*x, st.clone())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        op.set_seq_lengths(first)
+        _delay()
+        o1 = op.step(*x, st)
+        op.set_seq_lengths(second)
+        o2 = op.step(*x, st)
+    torch.cuda.synchronize()
+    w1, ws, _ = O.delta_forward(*a, inp["s0"], first)
+    w2, ws, _ = O.delta_forward(*a, ws, second)
+    _close(_host(o1), w1, TOL["bf16"], "first")
+    _close(_host(o2), w2, TOL["bf16"], "second")
+    _close(_host(st), ws, TOL["f32"], "state")
+
+
+def test_lengths_change_between_a_captured_graphs_replays():
+    """A graph reads the lengths that are set when it runs; setting new ones waits for a replay in flight."""
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    T, B, H, D = 40, 2, 1, 64
+    first, second = [40, 7], [12, 33]
+    inp = _inputs(T, B, H, H, D, D, "bf16", 403)
+    a = [inp[n] for n in NAMES]
+    op = R.DeltaRule(B, T, H, H, D, D)
+    x = [_dev(t, "bf16") for t in a]
+    op.set_seq_lengths(first)
+    op.forward(*x, train=False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, sT = op.forward(*x, train=False)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _delay()
+        graph.replay()
+        kept = o.clone(), sT.clone()
+        op.set_seq_lengths(second)
+        graph.replay()
+    torch.cuda.synchronize()
+    for lens, (oo, ss) in zip((first, second), (kept, (o, sT))):
+        wo, ws, _ = O.delta_forward(*a, None, lens)
+        _close(_host(oo), wo, TOL["bf16"], f"o of lengths {lens}")
+        _close(_host(ss), ws, STATE_TOL["bf16"], f"state of lengths {lens}")
