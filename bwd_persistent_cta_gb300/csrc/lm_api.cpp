@@ -23,7 +23,7 @@ struct rnn_delta_s {
   size_t es;
   int* d_len;
   int has_len;
-  CallOrder order;             // of the calls that read d_len
+  CallOrder order;             // of the calls that read d_len or use scratch
   unsigned int* status;        // device word
   uint64_t launches;
   // byte offsets.  Forward workspace (tensor cores): the tiles of prep; a
@@ -38,6 +38,7 @@ struct rnn_delta_s {
 struct rnn_norm_s {
   rnn_norm_desc_t desc;
   int device, num_sms, bf16;
+  CallOrder order;             // of the calls that use the workspace
   uint64_t launches;
 };
 
@@ -166,19 +167,19 @@ rnn_status_t delta_args(const rnn_delta_s* h, const rnn_delta_in_t* in, DeltaArg
   return RNN_OK;
 }
 
-// A call's place among the handle's calls that read the lengths (others share
-// nothing on the device that they change).
+// A call's place among the handle's calls that share something on the device:
+// lengths, workspace or reserve.
 struct Ordered {
-  rnn_delta_s* h;
+  CallOrder& order;
   cudaStream_t s;
   bool on;
   rnn_status_t rc = RNN_OK;
-  Ordered(rnn_delta_s* h_, cudaStream_t s_) : h(h_), s(s_), on(h_->has_len) {
-    if (on) rc = h->order.enter(s);
+  Ordered(CallOrder& order_, bool shares, cudaStream_t s_) : order(order_), s(s_), on(shares) {
+    if (on) rc = order.enter(s);
   }
   // The call's status; what was launched before a failure counts as well.
   rnn_status_t done(int e) {
-    const rnn_status_t l = on ? h->order.leave(s) : RNN_OK;
+    const rnn_status_t l = on ? order.leave(s) : RNN_OK;
     return e ? static_cast<rnn_status_t>(e) : l;
   }
 };
@@ -330,7 +331,7 @@ rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const fl
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ordered call(h, s);
+  Ordered call(h->order, h->has_len || h->tc || reserve, s);
   if (call.rc != RNN_OK) return call.rc;
   if (h->tc) {
     DeltaTcArgs t{};
@@ -374,7 +375,7 @@ rnn_status_t rnn_delta_backward(rnn_delta_t h, const rnn_delta_in_t* in, const v
   DeviceGuard guard(h->device);
   if (!guard.ok) return RNN_CUDA_ERROR;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ordered call(h, s);
+  Ordered call(h->order, true, s);
   if (call.rc != RNN_OK) return call.rc;
   if (h->tc) {
     DeltaTcBwdArgs t{};
@@ -437,7 +438,7 @@ rnn_status_t rnn_delta_step(rnn_delta_t h, const rnn_delta_in_t* in, float* stat
   r.num_sms = h->num_sms;
   r.o = o;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ordered call(h, s);
+  Ordered call(h->order, h->has_len, s);
   if (call.rc != RNN_OK) return call.rc;
   const int e = launch_delta_recur(r, h->bf16, s);
   if (!e) ++h->launches;
@@ -475,11 +476,18 @@ rnn_status_t rnn_norm_create(const rnn_norm_desc_t* desc, rnn_norm_t* out) {
   h->num_sms = sms;
   h->bf16 = desc->dtype == RNN_BF16;
   h->launches = 0;
+  if (h->order.create() != RNN_OK) {
+    delete h;
+    return RNN_CUDA_ERROR;
+  }
   *out = h;
   return RNN_OK;
 }
 
 rnn_status_t rnn_norm_destroy(rnn_norm_t h) {
+  if (!h) return RNN_OK;
+  DeviceGuard dg(h->device);
+  h->order.destroy();
   delete h;
   return RNN_OK;
 }
@@ -531,10 +539,13 @@ rnn_status_t rnn_norm_backward(rnn_norm_t h, const rnn_norm_in_t* in, const void
   a.dy = dy; a.dz = dz; a.dx = dx;
   a.dw_in = dw_in; a.dscale = dscale; a.dw_out = dw_out;
   a.partial = weights ? static_cast<float*>(workspace) : nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Ordered call(h->order, weights, s);
+  if (call.rc != RNN_OK) return call.rc;
   int n = 0;
-  const int e = launch_norm_backward(a, h->bf16, static_cast<cudaStream_t>(stream), &n);
+  const int e = launch_norm_backward(a, h->bf16, s, &n);
   h->launches += n;
-  return static_cast<rnn_status_t>(e);
+  return call.done(e);
 }
 
 uint64_t rnn_norm_launch_count(rnn_norm_t h) { return h ? h->launches : 0; }

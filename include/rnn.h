@@ -359,7 +359,11 @@ rnn_status_t rnn_noalloc_status(void* stream);
  * The conventions at the top of this file hold.  No kernel of these operators
  * waits for another CTA, so they need no resident grid and may overlap other
  * kernels; the chunk kernels' waits for their own copies are bounded all the
- * same (rnn_delta_sync_status). */
+ * same (rnn_delta_sync_status).  The calls of one handle that use lengths,
+ * workspace or reserve run in the order they are made, whatever their streams
+ * (a call on another stream than the last waits for it on the device); calls
+ * captured into a graph are ordered by the caller.  Calls that should overlap
+ * take a handle each. */
 typedef struct {
   int batch;           /* B >= 1                                                       */
   int seq_len;         /* T >= 1                                                       */
@@ -508,7 +512,8 @@ rnn_status_t rnn_norm_forward(rnn_norm_t handle, const rnn_norm_in_t* in, void* 
  *   dy, dz, dx      dense (out, each may be NULL)
  *   dw_in, dscale, dw_out  fp32 [cols] (out, overwritten, each may be NULL;
  *                   summed in a fixed order)
- *   workspace       required when a weight gradient is asked for */
+ *   workspace       required when a weight gradient is asked for; calls that use
+ *                   it run in the order they are made, as the delta rule's */
 rnn_status_t rnn_norm_backward(rnn_norm_t handle, const rnn_norm_in_t* in, const void* dx_out,
                                const void* dn_out, void* dy, void* dz, void* dx, float* dw_in,
                                float* dscale, float* dw_out, void* workspace, void* stream);

@@ -101,3 +101,52 @@ def test_lengths_change_between_a_captured_graphs_replays():
         wo, ws, _ = O.delta_forward(*a, None, lens)
         _close(_host(oo), wo, TOL["bf16"], f"o of lengths {lens}")
         _close(_host(ss), ws, STATE_TOL["bf16"], f"state of lengths {lens}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_later_call_on_another_stream_keeps_the_reserve(dtype):
+    """A training forward queued on one stream does not overwrite what a backward still waiting on another reads."""
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    shape = (90, 2, 1, 2, 64, 64)
+    one, two = _inputs(*shape, dtype, 404), _inputs(*shape, dtype, 405)
+    op = R.DeltaRule(2, 90, 1, 2, 64, 64, dtype=dtype)
+    x1, x2 = ([_dev(i[n], dtype) for n in NAMES] for i in (one, two))
+    do = _dev(one["do"], dtype)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    op.forward(*x1)
+    op.backward(do, *x1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        op.forward(*x1)
+        _delay()
+        grads = op.backward(do, *x1)
+    with torch.cuda.stream(s2):
+        op.forward(*x2)
+    torch.cuda.synchronize()
+    a = [one[n] for n in NAMES]
+    o, sT, kept = O.delta_forward(*a)
+    want = O.delta_backward(one["do"], *a, sT, kept)
+    for name, g, w in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, want):
+        _close(_host(g), w, TOL[dtype], name)
+
+
+def test_norm_gradients_on_two_streams_run_in_order():
+    """Two backward calls of one handle share its scratch, so the second waits for the first."""
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    op = R.BlockNorm(64, 256)
+    y, w = torch.randn(64, 256, device="cuda").bfloat16(), torch.ones(256, device="cuda").bfloat16()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    op.backward(y, None, y, w_in=w)
+    torch.cuda.synchronize()
+    first, second = torch.cuda.Event(), torch.cuda.Event()
+    with torch.cuda.stream(s1):
+        _delay()
+        op.backward(y, None, y, w_in=w)
+        first.record()
+    with torch.cuda.stream(s2):
+        op.backward(y, None, y, w_in=w)
+        second.record()
+    second.synchronize()
+    assert first.query()
