@@ -107,6 +107,7 @@ class _Op:
         import torch
         self.torch = torch
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._users = {}          # of each scratch buffer: raw streams
         self.device = torch.device(device if device is not None else "cuda")
         if self.device.index is None:     # pin the device current now: the handle is bound to it
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -122,12 +123,17 @@ class _Op:
         except Exception:
             pass
 
-    def _scratch(self, name: str, nbytes: int):
-        """The scratch buffer ``name``, allocated at its first use."""
+    def _scratch(self, name: str, nbytes: int, raw: int):
+        """The scratch buffer ``name``, allocated at its first use, for a call on the current stream (``raw``).  The
+        library orders the calls that share it; the allocator learns of every stream that uses it."""
         t = getattr(self, name, None)
         if t is None:
             t = self.torch.empty(max(nbytes, 256), dtype=self.torch.uint8, device=self.device)
             setattr(self, name, t)
+            self._users[name] = {raw}
+        elif raw not in self._users[name]:
+            self._users[name].add(raw)
+            t.record_stream(self.torch.cuda.current_stream(self.device))
         return t
 
     def _want(self, t, name: str, shape, dtype=None):
@@ -156,12 +162,28 @@ class _Op:
             raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype or self.tdtype}")
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
 
-    def _on(self, stream) -> int:
-        """The cudaStream_t of a call: ``stream``, else the device's current stream (its handle alone: making the
-        Stream object costs as much as the launch)."""
-        if stream is not None:
-            return stream.cuda_stream
+    def _on(self) -> int:
+        """The device's current stream (its handle alone: making the Stream object costs as much as the launch)."""
         return self.torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def _elsewhere(self, call, stream, *tensors, **more):
+        """``call`` made with ``stream`` current, for a caller whose current stream is another: what it allocates is
+        that stream's own memory, and neither its tensors nor the results are reused before both streams are done with
+        them.  Ordering the call after what made its inputs, and the results' use after the call, is the caller's."""
+        torch = self.torch
+        if stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}; the handle is on {self.device}")
+        here = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            out = call(*tensors, **more)
+        for t in (*tensors, *more.values()):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+        results = (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out
+        for t in results:
+            if t is not None:
+                t.record_stream(here)
+        return out
 
     def _rows(self, t, name: str, shape, lead: int, align: bool) -> int:
         """Row stride (elements) of ``t``: its first ``lead`` dimensions run over rows of one stride, the others are
@@ -214,7 +236,8 @@ class DeltaRule(_Op):
 
     q and k have ``heads_k`` heads of ``dim_k``, v and o ``heads_v`` heads of ``dim_v``, g (log decay) and beta
     [T, B, heads_v]; all in the dtype of the handle, the states fp32 [B, heads_v, dim_v, dim_k].  q, k, v, g and beta may
-    be slices of packed projections (rows of any one stride); every other tensor is dense."""
+    be slices of packed projections (rows of any one stride); every other tensor is dense.  Calls run on the current
+    stream, or on ``stream``."""
 
     _destroy = staticmethod(rnn_delta_destroy)
 
@@ -240,7 +263,8 @@ class DeltaRule(_Op):
 
     def sync(self, stream=None):
         """Wait for the stream and raise what a kernel reported."""
-        self._check(rnn_delta_sync_status(self.handle, self._on(stream)), "rnn_delta_sync_status")
+        raw = self._on() if stream is None else stream.cuda_stream
+        self._check(rnn_delta_sync_status(self.handle, raw), "rnn_delta_sync_status")
 
     def set_seq_lengths(self, lengths):
         """Valid tokens per sequence (batch ints), or None for full length, for the calls made from now on; waits for the
@@ -269,19 +293,24 @@ class DeltaRule(_Op):
 
     def forward(self, q, k, v, g, beta, s0=None, train=True, o=None, sT=None, stream=None):
         """(o, sT).  ``train`` keeps what backward needs until the next training forward."""
+        if stream is not None:
+            return self._elsewhere(self.forward, stream, q, k, v, g, beta, s0=s0, train=train, o=o, sT=sT)
         f32 = self.torch.float32
         x = self._inputs(q, k, v, g, beta)
         self._want(s0, "s0", self._s, f32)
         o, sT = self._out(o, "o", self._v, v), self._state(sT, "sT")
-        ws = self._scratch("workspace", self.workspace_bytes)
-        rs = self._scratch("reserve", self.reserve_bytes) if train else None
-        rc = rnn_delta_forward(self.handle, x, _p(s0), _p(o), _p(sT), _p(ws), _p(rs), self._on(stream))
+        raw = self._on()
+        ws = self._scratch("workspace", self.workspace_bytes, raw)
+        rs = self._scratch("reserve", self.reserve_bytes, raw) if train else None
+        rc = rnn_delta_forward(self.handle, x, _p(s0), _p(o), _p(sT), _p(ws), _p(rs), raw)
         self._check(rc, "rnn_delta_forward")
         return o, sT
 
     def backward(self, do, q, k, v, g, beta, s0=None, dsT=None, ds0=None, stream=None):
         """(dq, dk, dv, dg, dbeta, ds0) after a training forward of the same inputs.  s0 is accepted for symmetry: what
         backward needs of it is in the reserve."""
+        if stream is not None:
+            return self._elsewhere(self.backward, stream, do, q, k, v, g, beta, s0=s0, dsT=dsT, ds0=ds0)
         f32 = self.torch.float32
         if getattr(self, "reserve", None) is None:
             raise ValueError("backward needs a training forward first")
@@ -292,15 +321,19 @@ class DeltaRule(_Op):
         self._want(dsT, "dsT", self._s, f32)
         dq, dk, dv, dg, dbeta = (self._dense_like(t) for t in (q, k, v, g, beta))
         ds0 = self._state(ds0, "ds0")
-        ws = self._scratch("backward_workspace", self.backward_workspace_bytes)
+        raw = self._on()
+        ws = self._scratch("backward_workspace", self.backward_workspace_bytes, raw)
+        rs = self._scratch("reserve", self.reserve_bytes, raw)
         rc = rnn_delta_backward(self.handle, x, _p(do), _p(dsT), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta), _p(ds0),
-                                _p(ws), _p(self.reserve), self._on(stream))
+                                _p(ws), _p(rs), raw)
         self._check(rc, "rnn_delta_backward")
         return dq, dk, dv, dg, dbeta, ds0
 
     def step(self, q, k, v, g, beta, state, slots=None, o=None, stream=None):
         """seq_len new tokens of each sequence against ``state`` [num_slots, heads_v, dim_v, dim_k] fp32, updated in
         place; ``slots`` int32 [batch] names each sequence's state (a slot outside the pool skips the sequence)."""
+        if stream is not None:
+            return self._elsewhere(self.step, stream, q, k, v, g, beta, state, slots=slots, o=o)
         torch, d = self.torch, self.desc
         x = self._inputs(q, k, v, g, beta)
         if not isinstance(state, torch.Tensor) or state.dim() != 4:
@@ -315,7 +348,7 @@ class DeltaRule(_Op):
             if not slots.is_contiguous():
                 raise ValueError("slots must be contiguous")
         o = self._out(o, "o", self._v, v)
-        rc = rnn_delta_step(self.handle, x, state.data_ptr(), n, _p(slots), o.data_ptr(), self._on(stream))
+        rc = rnn_delta_step(self.handle, x, state.data_ptr(), n, _p(slots), o.data_ptr(), self._on())
         self._check(rc, "rnn_delta_step")
         return o
 
@@ -365,6 +398,9 @@ class BlockNorm(_Op):
 
     def forward(self, y, z=None, x=None, w_in=None, scale=None, w_out=None, x_out=None, n_out=None, stream=None):
         """(x_out, n_out); n_out is None without norm_out.  x_out may be x itself."""
+        if stream is not None:
+            return self._elsewhere(self.forward, stream, y, z=z, x=x, w_in=w_in, scale=scale, w_out=w_out, x_out=x_out,
+                                   n_out=n_out)
         if y is None:
             raise ValueError("y is required")
         a = self._inputs(y, z, x, w_in, scale, w_out)
@@ -379,13 +415,16 @@ class BlockNorm(_Op):
             n_out = self._dense_like(y)
         else:
             self._want(n_out, "n_out", self._full)
-        rc = rnn_norm_forward(self.handle, a, x_out.data_ptr(), _p(n_out), self._on(stream))
+        rc = rnn_norm_forward(self.handle, a, x_out.data_ptr(), _p(n_out), self._on())
         self._check(rc, "rnn_norm_forward")
         return x_out, n_out
 
     def backward(self, dx_out, dn_out, y, z=None, x=None, w_in=None, scale=None, w_out=None, stream=None):
         """A dict of the gradients dy, dz, dx (handle's dtype) and dw_in, dscale, dw_out (fp32); None where the handle
         or the call leaves the input out.  dx_out or dn_out may be None."""
+        if stream is not None:
+            return self._elsewhere(self.backward, stream, dx_out, dn_out, y, z=z, x=x, w_in=w_in, scale=scale,
+                                   w_out=w_out)
         d, torch = self.desc, self.torch
         if y is None:
             raise ValueError("y is required")
@@ -403,8 +442,8 @@ class BlockNorm(_Op):
         for name, t in (("dw_in", w_in), ("dscale", scale), ("dw_out", w_out)):
             out[name] = None if t is None else torch.empty_like(t, dtype=torch.float32)
             weights = weights or t is not None
-        ws = self._scratch("workspace", self.workspace_bytes) if weights else None
-        rc = rnn_norm_backward(self.handle, a, _p(dx_out), _p(dn_out), *(_p(t) for t in out.values()), _p(ws),
-                               self._on(stream))
+        raw = self._on()
+        ws = self._scratch("workspace", self.workspace_bytes, raw) if weights else None
+        rc = rnn_norm_backward(self.handle, a, _p(dx_out), _p(dn_out), *(_p(t) for t in out.values()), _p(ws), raw)
         self._check(rc, "rnn_norm_backward")
         return out

@@ -150,3 +150,96 @@ def test_norm_gradients_on_two_streams_run_in_order():
         second.record()
     second.synchronize()
     assert first.query()
+
+
+def _busy_block(like):
+    """A block of the current stream's pool that the stream still reads although the host has dropped it, and where the
+    reading ends up."""
+    import torch
+    x = torch.full_like(like, 3.0)
+    torch.cuda.synchronize()
+    _delay()
+    return x.clone()
+
+
+def test_outputs_on_a_stream_that_is_not_current():
+    """With ``stream=``, outputs do not take memory that the current stream has yet to read."""
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    s = torch.cuda.Stream()
+    T, B, H, D = 256, 8, 16, 128                 # 8 MB: blocks of their own
+    op = R.DeltaRule(B, T, H, H, D, D)
+    x = [_dev(t, "bf16") for t in (_inputs(T, B, H, H, D, D, "bf16", 406)[n] for n in NAMES)]
+    norm = R.BlockNorm(B * T, H * D)
+    one = R.DeltaRule(B, 1, H, H, D, D)
+    st = torch.zeros(B, H, D, D, device="cuda")
+    flat = x[2].view(B * T, H * D)
+    calls = [
+        (x[2], lambda: op.forward(*x, train=False, stream=s)),
+        (flat, lambda: norm.forward(flat, stream=s)),
+        (x[2], lambda: (op.forward(*x, stream=s), op.backward(x[2], *x, stream=s))),
+        (flat, lambda: norm.backward(flat, None, flat, stream=s)),
+        (x[2][:1].contiguous(), lambda: one.step(*(t[:1].contiguous() for t in x), st, stream=s)),
+    ]
+    for like, call in calls:
+        call()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        kept = _busy_block(like)
+        out = call()
+        torch.cuda.synchronize()
+        assert torch.all(kept == 3.0)
+        del out
+
+
+def test_outputs_dropped_while_the_current_stream_reads_them():
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    s = torch.cuda.Stream()
+    rows, cols = 2048, 2048
+    op = R.BlockNorm(rows, cols)
+    y = torch.randn(rows, cols, device="cuda").bfloat16()
+    zero = torch.zeros_like(y)
+    want, _ = op.forward(y)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    out, _ = op.forward(y, stream=s)
+    torch.cuda.synchronize()
+    _delay()
+    kept = out.clone()
+    del out
+    again, _ = op.forward(zero, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
+
+
+def test_inputs_dropped_while_another_stream_reads_them():
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    s = torch.cuda.Stream()
+    rows, cols = 2048, 2048
+    op = R.BlockNorm(rows, cols)
+    y = torch.randn(rows, cols, device="cuda").bfloat16()
+    want, _ = op.forward(y)
+    op.forward(y, stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        _delay()
+    out, _ = op.forward(y, stream=s)
+    del y
+    others = [torch.zeros(rows, cols, device="cuda", dtype=torch.bfloat16) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not any(t.any() for t in others)
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch
+    import bwd_persistent_cta_gb300 as R
+
+    class Other:
+        device, cuda_stream = torch.device("cuda", 7), 0
+
+    op = R.BlockNorm(4, 64)
+    y = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="stream"):
+        op.forward(y, stream=Other())
