@@ -111,6 +111,7 @@ _SIGS = {
     "rnn_norm_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 3),
     "rnn_norm_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 10),
     "rnn_norm_launch_count": (ctypes.c_uint64, [_P]),
+    "rnn_debug_step_drain": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "rnn_debug_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int,
                                       _P, ctypes.c_int64, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int, _P,
                                       ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int), ctypes.c_int,
@@ -300,6 +301,13 @@ def rnn_debug_simt_plan(mode: int, reset_after: int, is_bf16: int, bwd: int, hid
                                    int(ndir), int(num_sms), int(dwhh), buf)
     keys = ("nu", "nblk", "pp", "stream", "smem", "dwhh_default", "dwhh_possible")
     return dict(zip(keys, buf[:7])) if ok else None
+
+
+def rnn_debug_step_drain(turn: int, turns: int):
+    """[(stage, parity), ...] that a CTA of the serving step waits for when it gives up at ``turn`` of ``turns``."""
+    buf = (ctypes.c_int * 64)()
+    n = lib().rnn_debug_step_drain(int(turn), int(turns), buf)
+    return [(buf[2 * i], buf[2 * i + 1]) for i in range(n)]
 
 
 def rnn_debug_skip_arrival(handle, cta: int) -> int:

@@ -51,6 +51,22 @@ struct DeltaRecurArgs {
 };
 int launch_delta_recur(const DeltaRecurArgs& r, int is_bf16, cudaStream_t s);
 
+// The serving step's pipeline.  Turn n of a CTA's walk fills stage n % kUnits; the
+// phase of that fill has the parity of n / kUnits.  At turn n the fills of turns
+// n .. n + kUnits - 1 are under way, as far as the walk has that many.
+constexpr int kUnits = 4;
+struct StepFill {
+  int stage;
+  unsigned int parity;
+};
+__host__ __device__ constexpr StepFill step_fill(int turn) {
+  return {turn % kUnits, static_cast<unsigned int>(turn / kUnits) & 1u};
+}
+// The last turn whose fill is under way at turn ``turn`` of a walk of ``turns``.
+__host__ __device__ constexpr int step_last_fill(int turn, int turns) {
+  return turn + kUnits < turns ? turn + kUnits - 1 : turns - 1;
+}
+
 struct DeltaRecurBwdArgs {
   DeltaArgs a;
   const void* dout;

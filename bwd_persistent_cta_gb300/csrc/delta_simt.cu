@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 // Warp w computes rows 8 w .. 8 w + 7 and writes them back from registers.
 // 256 sequences of 32 heads of 128 x 128 (1.08 GB): 173 us, 6.2 TB/s; loads into
 // registers without the pipeline took 203 (8 rows a warp) to 213 us (4).
-constexpr int kUnits = 4;
 constexpr int kUnitRows = 32;
 constexpr uint64_t kStepTimeoutNs = 2000000000ull;     // of a wait for a unit's copy
 
@@ -358,17 +357,19 @@ __global__ void __launch_bounds__(kWarps * 32) delta_step_kernel(const DeltaRecu
   int turn = 0;
   for (int64_t u = blockIdx.x; u < units; u += stride, ++turn) {
     cur = nxt;
-    const int stage = turn % kUnits;
-    const bool late = !mbar_wait(&sm.full[stage], (turn / kUnits) & 1, kStepTimeoutNs);
+    const int stage = step_fill(turn).stage;
+    const bool late = !mbar_wait(&sm.full[stage], step_fill(turn).parity, kStepTimeoutNs);
     float S[R][VPL];
 #pragma unroll
     for (int i = 0; i < R; ++i)
       load_vec<float, VPL>(&sm.S[stage][(warp * R + i) * a.Dk + dk0], in && cur.len && warp * R + i < cur.rows, S[i]);
     if (__syncthreads_or(late)) {
-      // a copy that is still under way keeps the CTA for as long again
+      // copies that are still under way keep the CTA for as long again, each
       if (threadIdx.x == 0) {
         atomicCAS(r.status, 0u, static_cast<unsigned int>(RNN_TIMEOUT));
-        for (int i = 0; i < kUnits; ++i) mbar_wait(&sm.full[i], (turn + i) / kUnits & 1, kStepTimeoutNs);
+        const int turns = (units - 1 - static_cast<int>(blockIdx.x)) / stride + 1;
+        for (int t = turn; t <= step_last_fill(turn, turns); ++t)
+          mbar_wait(&sm.full[step_fill(t).stage], step_fill(t).parity, kStepTimeoutNs);
       }
       return;
     }

@@ -12,6 +12,7 @@
 #include "device_guard.h"
 #include "norm.h"
 #include "rnn.h"
+#include "rnn_debug.h"
 
 using namespace rnn;
 
@@ -549,5 +550,15 @@ rnn_status_t rnn_norm_backward(rnn_norm_t h, const rnn_norm_in_t* in, const void
 }
 
 uint64_t rnn_norm_launch_count(rnn_norm_t h) { return h ? h->launches : 0; }
+
+int rnn_debug_step_drain(int turn, int turns, int* out) {
+  if (!out || turn < 0 || turn >= turns) return 0;
+  int n = 0;
+  for (int t = turn; t <= step_last_fill(turn, turns); ++t, ++n) {
+    out[2 * n] = step_fill(t).stage;
+    out[2 * n + 1] = static_cast<int>(step_fill(t).parity);
+  }
+  return n;
+}
 
 }  // extern "C"

@@ -66,6 +66,12 @@ int rnn_debug_simt_plan(int mode, int reset_after, int is_bf16, int bwd, int hid
  * -1 (default) = off.  RNN_BAD_PARAM for a NULL handle or cta < -1. */
 rnn_status_t rnn_debug_skip_arrival(rnn_handle_t handle, int cta);
 
+/* Test hook: the copies that the serving step's kernel (rnn_delta_step over many
+ * states) waits for before a CTA gives up at turn ``turn`` of a walk of ``turns``
+ * (host arithmetic only): out[2*i ...] = {stage, parity of its phase}.  Returns
+ * their number, 0 for a turn outside the walk. */
+int rnn_debug_step_drain(int turn, int turns, int* out);
+
 /* Test hook: process-wide overrides of the kernel plans, for tests that must
  * reach a given configuration.  0 leaves a choice to the planner.
  *   max_ks_fwd, max_ks_bwd  1..16: cap the tensor-core persistent kernels' K
