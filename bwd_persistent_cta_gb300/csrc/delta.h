@@ -34,6 +34,19 @@ struct DeltaArgs {
 // differences of cumulative decays free of inf - inf.
 constexpr float kDecayFloor = -110.f;
 
+// Cumulative decays are unevaluated sums of two floats: the difference of two of
+// them stays exact to fp32 however many resets lie before both.
+struct TwoF {
+  float h, l;
+};
+__device__ __forceinline__ TwoF two_add(TwoF a, TwoF b) {
+  const float s = a.h + b.h, bb = s - a.h;
+  const float err = (a.h - (s - bb)) + (b.h - bb);
+  const float l = err + (a.l + b.l);
+  const float h = s + l;
+  return {h, l - (h - s)};
+}
+
 // --- fp32 kernels: every type and size --------------------------------------
 constexpr int kSimtChunk = 32;
 

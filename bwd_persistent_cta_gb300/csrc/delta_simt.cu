@@ -545,7 +545,7 @@ struct ChunkBwdSmem {
   float S0[kSlice][P], dS[kSlice][P];
   float E[kCb][kSlice + 1], Y[kCb][kSlice + 1], dO[kCb][kSlice + 1];
   float mP[kCb][kCb + 1], mA[kCb][kCb + 1], X[kCb][kCb + 1];
-  float G[kCb], eG[kCb], eE[kCb], beta[kCb], dG[kCb], w[kCb];
+  float Gh[kCb], Gl[kCb], eG[kCb], eE[kCb], beta[kCb], dG[kCb], w[kCb];
   float red[8];
 };
 
@@ -597,16 +597,17 @@ __global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBw
     if (tid < 32) {
       const bool ok = tid < nt;
       const int64_t row = a.row(b, t0 + (ok ? tid : 0));
-      float gg = ok ? to_f<T>(static_cast<const T*>(a.g)[row * a.g_row + h]) : 0.f;
-      gg = gg < kDecayFloor ? kDecayFloor : gg;
+      const float gg = ok ? to_f<T>(static_cast<const T*>(a.g)[row * a.g_row + h]) : 0.f;
+      TwoF G = {gg < kDecayFloor ? kDecayFloor : gg, 0.f};
 #pragma unroll
       for (int w = 1; w < 32; w <<= 1) {
-        const float up = __shfl_up_sync(kFull, gg, w);
-        if (tid >= w) gg += up;
+        const TwoF up = {__shfl_up_sync(kFull, G.h, w), __shfl_up_sync(kFull, G.l, w)};
+        if (tid >= w) G = two_add(up, G);
       }
-      sm.G[tid] = gg;
-      sm.eG[tid] = expf(gg);
-      sm.eE[tid] = expf(__shfl_sync(kFull, gg, 31) - gg);
+      sm.Gh[tid] = G.h;
+      sm.Gl[tid] = G.l;
+      sm.eG[tid] = expf(G.h + G.l);
+      sm.eE[tid] = expf((__shfl_sync(kFull, G.h, 31) - G.h) + (__shfl_sync(kFull, G.l, 31) - G.l));
       sm.beta[tid] = ok ? to_f<T>(static_cast<const T*>(a.beta)[row * a.beta_row + h]) : 0.f;
     }
     float N[4], Pm[4], dq1[M], dk1[M], dk3[M], frob = 0.f;
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBw
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int j = l + 8 * jj;
-      const float D = j <= i ? expf(sm.G[i] - sm.G[j]) : 0.f;
+      const float D = j <= i ? expf((sm.Gh[i] - sm.Gh[j]) + (sm.Gl[i] - sm.Gl[j])) : 0.f;
       const float mp = D * a.scale * sm.beta[j] * Pm[jj];
       const float ma = j < i ? -D * bi * sm.beta[j] * N[jj] : 0.f;
       sm.mP[i][j] = mp;

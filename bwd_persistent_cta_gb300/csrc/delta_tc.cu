@@ -229,18 +229,6 @@ __device__ __forceinline__ int dv_of_row(int r) { return 4 * (r >> 1) + (r & 1);
 // prep: everything of a chunk that does not depend on the state
 // ---------------------------------------------------------------------------
 constexpr int kXP = 68;              // pitch of the fp32 64 x 64 matrices: fragment rows on different banks
-struct TwoF {
-  float h, l;
-};
-// (a + b) as an unevaluated sum of two floats.
-__device__ __forceinline__ TwoF two_add(TwoF a, TwoF b) {
-  const float s = a.h + b.h, bb = s - a.h;
-  const float err = (a.h - (s - bb)) + (b.h - bb);
-  const float l = err + (a.l + b.l);
-  const float h = s + l;
-  return {h, l - (h - s)};
-}
-
 // C[16][8 NB] = sign cw (A (yw B)) by one warp, on fp32 matrices in shared memory
 // (pitch kXP): A [16][8 KB], row k of B weighted by yw[k] and row i of the result
 // by cw[i] where given.  Each factor is split into two tf32 parts (11 + 10 bits)
