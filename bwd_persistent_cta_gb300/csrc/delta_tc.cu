@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(128, TRAIN ? 4 : 6) delta_prep_kernel(const De
       const float be = fabsf(sm.beta[t]);
       sc[t] = eg;
       sc[64 + t] = ee;
-      sc[192 + t] = g2[i].h;
+      sc[kScG + t] = g2[i].h;
+      sc[kScGl + t] = g2[i].l;
       bu = fmaxf(bu, be * fmaxf(1.f, ee));
       by = fmaxf(by, be * eg);
       bo = fmaxf(bo, fabsf(a.scale) * eg);
@@ -733,7 +734,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
 template <int DK, int W>
 struct ScanStage {
   unsigned char K[kTc * DK * 2], Q[kTc * DK * 2], T[kTri], P[kTri];
-  float sc[kSc];
+  float sc[kScScan];
   SeqTile<W> x;
 };
 template <int DK, int W>
@@ -753,12 +754,12 @@ template <int DK, int W>
 __device__ __forceinline__ void scan_fetch(ScanStage<DK, W>& st, uint64_t* bar, const ScanSource& src, int c, int left) {
   if (threadIdx.x == 0) {
     fence_proxy_async_smem();
-    mbar_arrive_expect_tx(bar, 2 * kTc * DK * 2 + 2 * kTri + kSc * 4);
+    mbar_arrive_expect_tx(bar, 2 * kTc * DK * 2 + 2 * kTri + kScScan * 4);
     bulk_copy(smem_u32(st.K), src.k + static_cast<int64_t>(c) * kTc * DK * 2, kTc * DK * 2, bar);
     bulk_copy(smem_u32(st.Q), src.q + static_cast<int64_t>(c) * kTc * DK * 2, kTc * DK * 2, bar);
     bulk_copy(smem_u32(st.T), src.t + static_cast<int64_t>(c) * kTri, kTri, bar);
     bulk_copy(smem_u32(st.P), src.p + static_cast<int64_t>(c) * kTri, kTri, bar);
-    bulk_copy(smem_u32(st.sc), src.sc + static_cast<int64_t>(c) * kSc * 4, kSc * 4, bar);
+    bulk_copy(smem_u32(st.sc), src.sc + static_cast<int64_t>(c) * kSc * 4, kScScan * 4, bar);
   }
   const int t = threadIdx.x / (2 * W), ch = threadIdx.x % (2 * W);
   const __nv_bfloat16* x = src.x + 4 * c * src.x_step;
@@ -1659,7 +1660,7 @@ struct GradSmem {
   } st[2];
   unsigned char K[2][kTc * DK * 2], Q[2][kTc * DK * 2];
   unsigned char mP[kTc * 128], mA[kTc * 128];
-  float eG[kTc], eE[kTc], beta[kTc], G[kTc];
+  float eG[kTc], eE[kTc], beta[kTc], Gh[kTc], Gl[kTc];
   // per 16 value columns: the fp16 pair that brings S0, dS1, e, y to the head's
   // scale, the fp32 factor that does so from bf16 for do; and the head's inverse scales
   uint32_t ratio[5][16];
@@ -1815,7 +1816,8 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
         sm.eG[tid] = sc[tid];
         sm.eE[tid] = sc[64 + tid];
         sm.beta[tid] = sc[128 + tid];
-        sm.G[tid] = sc[192 + tid];
+        sm.Gh[tid] = sc[kScG + tid];
+        sm.Gl[tid] = sc[kScGl + tid];
       }
       if (warp >= 3 && warp < 8) {
         const int w = warp - 3;
@@ -2025,7 +2027,7 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 32 * rg + 16 * mt + 8 * (e >> 1) + r, j = 8 * (NJ * cq + n) + cc + (e & 1);
-            const float Db = j <= i ? __expf(sm.G[i] - sm.G[j]) * sm.beta[j] : 0.f;
+            const float Db = j <= i ? __expf((sm.Gh[i] - sm.Gh[j]) + (sm.Gl[i] - sm.Gl[j])) * sm.beta[j] : 0.f;
             const float nn = N[mt][n][e] * sN;
             const float wp = Db * (Pm[mt][n][e] * sP);
             const float wa = j < i ? -Db * sm.beta[i] * nn : 0.f;

@@ -26,8 +26,9 @@ namespace rnn {
 
 constexpr int kTc = 64;              // tokens a chunk
 constexpr int kTri = 80 * 128;       // bytes of a packed triangular tile
-// SC: [0,64) e^G, [64,128) e^{G_C - G}, [128,192) beta, [192,256) G, then
-enum { kScK = 256, kScQ, kScTH, kScTB, kScP, kScEnd, kScBu, kScBy, kScBo, kSc = 268 };
+// SC: [0,64) e^G, [64,128) e^{G_C - G}, [128,192) beta, [192,256) and from kScGl the
+// two parts of G, and the scales between.  The scans read the first kScScan.
+enum { kScG = 192, kScK = 256, kScQ, kScTH, kScTB, kScP, kScEnd, kScBu, kScBy, kScBo, kScScan = 268, kScGl = 268, kSc = 332 };
 
 struct DeltaTcBufs {
   void *k16, *q16, *th, *tb, *p;
