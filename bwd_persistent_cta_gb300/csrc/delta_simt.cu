@@ -766,8 +766,9 @@ __global__ void __launch_bounds__(256) delta_chunk_bwd_kernel(const DeltaChunkBw
   for (int x = tid; x < span * a.Dk; x += 256) {
     const int ti = x / a.Dk, d = x - ti * a.Dk;
     const int64_t at = a.row(b, t0 + ti) * qk_row + hk * a.Dk + d;
-    static_cast<T*>(r.dq)[at] = from_f<T>(sm.dQ[ti][d]);
-    static_cast<T*>(r.dk)[at] = from_f<T>(sm.dK[ti][d]);
+    // (a NaN in a valid token makes the sums of masked rows NaN as well)
+    static_cast<T*>(r.dq)[at] = from_f<T>(ti < nt ? sm.dQ[ti][d] : 0.f);
+    static_cast<T*>(r.dk)[at] = from_f<T>(ti < nt ? sm.dK[ti][d] : 0.f);
   }
 }
 

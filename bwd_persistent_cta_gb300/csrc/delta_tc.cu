@@ -877,10 +877,13 @@ __device__ __forceinline__ void frag_store_seq(const Frag& x, __nv_bfloat16* p, 
     if (t + 8 * n < left) *reinterpret_cast<uint2*>(p + n * step) = make_uint2(lo, hi);
   }
 }
-// Zero rows t0 .. T-1 of a warp's columns.
-__device__ __forceinline__ void zero_rows(__nv_bfloat16* base, const DeltaArgs& a, int64_t stride, int b, int t0, int lane) {
-  for (int t = t0 + (lane >> 2); t < a.T; t += 8)
-    *reinterpret_cast<uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) = make_uint2(0u, 0u);
+// Zero rows len .. T-1 of a warp's columns.  The last chunk has written its own
+// masked rows already, but not always zeros: a NaN in a token, or an infinity in
+// the state, reaches them as a product with zero.  The thread that wrote an
+// element there (of a warp that owns whole chunks) writes it again.
+__device__ __forceinline__ void zero_rows(__nv_bfloat16* base, const DeltaArgs& a, int64_t stride, int b, int len, int lane) {
+  for (int t = (len & ~7) + (lane >> 2); t < a.T; t += 8)
+    if (t >= len) *reinterpret_cast<uint2*>(base + a.row(b, t) * stride + 4 * (lane & 3)) = make_uint2(0u, 0u);
 }
 
 // ---------------------------------------------------------------------------
@@ -1028,7 +1031,7 @@ __global__ void __launch_bounds__(32 * W) delta_scan_fwd_kernel(const DeltaTcArg
     frag_scale(z, s.sc + 64, lane);
     state_update<DK>(S, s.sc[kScEnd], z, uf, ks, ui * s.sc[kScK], off);
   }
-  zero_rows(o, a, o_row, b, ncb * kTc, lane);
+  zero_rows(o, a, o_row, b, len, lane);
   if (p.s_out) state_store<DK>(S, p.s_out + s_off, DK, lane);
 }
 
@@ -1265,7 +1268,8 @@ __global__ void __launch_bounds__(128) delta_pair_fwd_kernel(const DeltaTcArgs p
     frag_scale(z, s.sc + 64, lane);
     state_update<DK>(S, s.sc[kScEnd], z, uf, ks, ui * s.sc[kScK], off);
   }
-  if (half == 0) zero_rows(o, a, o_row, b, ncb * kTc, lane);
+  pair_sync(pair);                  // both warps have written rows of the last chunk
+  if (half == 0) zero_rows(o, a, o_row, b, len, lane);
   if (p.s_out) state_store<DKW>(S, p.s_out + s_off, DK, lane);
 }
 
@@ -1472,7 +1476,7 @@ __global__ void __launch_bounds__(32 * W) delta_scan_bwd_kernel(const DeltaTcBwd
     state_update<DK>(S, s.sc[kScEnd], acc, af, qs, inv_scale(af) * s.sc[kScQ], off);
     state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
   }
-  zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, ncb * kTc, lane);
+  zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, len, lane);
   if (p.ds0) state_store<DK>(S, p.ds0 + s_off, DK, lane);
 }
 
@@ -1630,8 +1634,8 @@ __global__ void __launch_bounds__(128) delta_pair_bwd_kernel(const DeltaTcBwdArg
     state_update<DK>(S, s.sc[kScEnd], x, af, qs, inv_scale(af) * s.sc[kScQ], off);
     state_update<DK>(S, 1.f, z, xf, ks, inv_scale(xf) * s.sc[kScK], off);
   }
-  if (half == 0)
-    zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, ncb * kTc, lane);
+  pair_sync(pair);
+  if (half == 0) zero_rows(static_cast<__nv_bfloat16*>(p.dv) + static_cast<int64_t>(h) * a.Dv + dv0, a, o_row, b, len, lane);
   if (p.ds0) state_store<DKW>(S, p.ds0 + s_off, DK, lane);
 }
 
@@ -2175,6 +2179,14 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
       add(dk, t_[1], inv_scale(pf) * qi);
       add(dk, t_[2], inv_scale(af) * ki);
       if (cur.hh == per - 1) {
+        // masked rows are zeros, whatever the sums hold: a NaN in a token reaches them as a product with zero
+        if (nt < kTc) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (32 * rg + 16 * mt + 8 * (e >> 1) + r >= nt) dq[mt][0][e] = dq[mt][1][e] = dk[mt][0][e] = dk[mt][1][e] = 0.f;
+        }
         // lanes of a quad swap halves, so that each writes 8 bytes of one tile
         const bool odd = lane & 1;
         const int col = cq * 16 + (odd ? 8 : 0) + 2 * (cc & 4 ? 2 : 0);

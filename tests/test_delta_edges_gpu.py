@@ -2,9 +2,12 @@
 import numpy as np
 import pytest
 
-from tests.test_delta_gpu import TOL, _close, _inputs, _run, _want
+from tests.test_delta_gpu import TOL, _close, _dev, _host, _inputs, _run, _want
 
 pytestmark = pytest.mark.gpu
+
+NAMES = ("q", "k", "v", "g", "beta")
+GRADS = ("dq", "dk", "dv", "dg", "dbeta")
 
 
 @pytest.mark.parametrize("every", [2, 3, 4])
@@ -34,6 +37,54 @@ def test_bf16_gradients_do_not_depend_on_earlier_resets():
     plain = _run(inp, "bf16")
     inp["g"][:at] = -np.inf
     many = _run(inp, "bf16")
-    for n in ("o", "dq", "dk", "dv", "dg", "dbeta"):
+    for n in ("o",) + GRADS:
         a, b = plain[n][at:], many[n][at:]
         assert np.mean(a != b) <= 1 / 500, (n, np.mean(a != b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", NAMES + ("do",))
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_masked_tokens_stay_zero_beside_a_bad_value(dtype, name, bad):
+    """A NaN or an infinity in a valid token shows, but not in the masked tokens of its chunk."""
+    if name == "g" and bad == np.inf:
+        bad = 1e30                                 # an infinite growth
+    T, lens = 140, [71, 140, 0, 30]
+    inp = _inputs(T, 4, 2, 4, 64, 64, dtype, 503)
+    inp[name][70, 0] = bad
+    inp[name][20, 3] = bad
+    import bwd_persistent_cta_gb300 as R
+    import torch
+    op = R.DeltaRule(4, T, 2, 4, 64, 64, dtype=dtype)
+    op.set_seq_lengths(lens)
+    x = [_dev(inp[n], dtype) for n in NAMES]
+    s0 = torch.from_numpy(inp["s0"]).cuda()
+    o, sT = op.forward(*x, s0=s0)
+    grads = op.backward(_dev(inp["do"], dtype), *x)
+    out = dict(zip(GRADS, (_host(t) for t in grads)), o=_host(o))
+    for n, t in out.items():
+        for b, length in enumerate(lens):
+            assert np.all(t[length:, b] == 0.0), (n, b)
+    assert not all(np.all(np.isfinite(t[:71, 0])) for t in out.values())
+    if name != "do":
+        inp[name][70, 0] = inp[name][20, 3] = 0.5
+        _close(out["o"][:, 1:3], _want(inp, lens)["o"][:, 1:3], TOL[dtype], "other sequences")
+
+
+@pytest.mark.parametrize("H,D", [(70, 128), (160, 128), (160, 64)])
+def test_masked_tokens_stay_zero_with_many_heads(H, D):
+    """The same where a CTA takes four and eight slices of a head's value columns."""
+    import bwd_persistent_cta_gb300 as R
+    T, lens = 75, [70, 3]
+    inp = _inputs(T, 2, H, H, D, D, "bf16", 506)
+    inp["k"][66, 0] = inp["v"][1, 1] = np.nan
+    op = R.DeltaRule(2, T, H, H, D, D)
+    op.set_seq_lengths(lens)
+    x = [_dev(inp[n], "bf16") for n in NAMES]
+    o, _ = op.forward(*x)
+    grads = op.backward(_dev(inp["do"], "bf16"), *x)
+    for n, t in zip(("o",) + GRADS, (o,) + grads):
+        t = _host(t)
+        assert not np.all(np.isfinite(t)), n
+        for b, length in enumerate(lens):
+            assert np.all(t[length:, b] == 0.0), (n, b)
