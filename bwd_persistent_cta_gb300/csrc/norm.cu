@@ -282,6 +282,10 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(c
   }
 }
 
+// r^3 m, where r^3 alone may leave the range (a row's root mean square from 1e13
+// up or 1e-13 down): m is of the size of the row, so each product is in range.
+__device__ __forceinline__ float cube_times(float r, float m) { return r * (r * (r * m)); }
+
 // The gradients.  With r1, r2 the two inverse root means, h = dn * w_out:
 //   dc = dx' + r2 h - x' r2^3 mean(h x')                 (dx = dc)
 //   dw_out += dn x' r2,  dscale += dc b,  db = scale dc
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock, IT > 1 || sizeof(
         float s2[2] = {q0.x + q0.y, q1.x + q1.y};
         row_sum<TPR, 2>(s2, red[2 + odd]);
         r2 = rsqrtf(s2[0] * inv + a.eps);
-        m2 = r2 * r2 * r2 * s2[1] * inv;
+        m2 = cube_times(r2, s2[1] * inv);
       }
     }
     float2 h[IT][V2], q3 = both(0.f);
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock, IT > 1 || sizeof(
     if (a.norm_in) {
       float s3[1] = {q3.x + q3.y};
       row_sum<TPR, 1>(s3, red[4 + odd]);
-      m1 = r1 * r1 * r1 * s3[0] * inv;
+      m1 = cube_times(r1, s3[0] * inv);
     }
     if (a.dy) {
 #pragma unroll
