@@ -88,3 +88,16 @@ def test_masked_tokens_stay_zero_with_many_heads(H, D):
         assert not np.all(np.isfinite(t)), n
         for b, length in enumerate(lens):
             assert np.all(t[length:, b] == 0.0), (n, b)
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+@pytest.mark.parametrize("T,Dk,Dv", [(513, 64, 128), (700, 128, 64)])
+def test_fp32_error_does_not_grow_with_the_sequence(T, Dk, Dv, seed):
+    """Memories of a hundred to a thousand tokens.  16 * 2^-24 = 9.5e-7 for every tensor: a value passes sums of at most
+    256 products in trees or chains of 32 (below 6 * 2^-24 with random signs) and a dozen single roundings; no term counts
+    the tokens of the sequence, which would be another 2^-24 sqrt(T) = 23 * 2^-24 and more."""
+    tol = 16 * 2.0 ** -24
+    inp = _inputs(T, 1, 1, 2, Dk, Dv, "f32", 520 + seed, gate=0.05)
+    got, want = _run(inp, "f32"), _want(inp)
+    for n, w in want.items():
+        _close(got[n], w, tol, n)
