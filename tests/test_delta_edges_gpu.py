@@ -2,6 +2,8 @@
 import numpy as np
 import pytest
 
+from oracle import lm_oracle as O
+
 from tests.test_delta_gpu import TOL, _close, _dev, _host, _inputs, _run, _want
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +103,77 @@ def test_fp32_error_does_not_grow_with_the_sequence(T, Dk, Dv, seed):
     got, want = _run(inp, "f32"), _want(inp)
     for n, w in want.items():
         _close(got[n], w, tol, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+def test_finite_outputs_beside_a_bad_value_are_right(dtype, name):
+    """What stays finite in the sequence that holds a NaN is what it would be without it."""
+    import bwd_persistent_cta_gb300 as R
+    import torch
+    T, B, H, D = 150, 1, 1, 64
+    inp = _inputs(T, B, H, H, D, D, dtype, 504)
+    a = [inp[n] for n in NAMES]
+    wo, _, _ = O.delta_forward(*a, inp["s0"])
+    x = {n: inp[n].copy() for n in NAMES}
+    x[name][70, 0] = np.nan
+    op = R.DeltaRule(B, T, H, H, D, D, dtype=dtype)
+    o, sT = op.forward(*(_dev(x[n], dtype) for n in NAMES), s0=torch.from_numpy(inp["s0"]).cuda(), train=False)
+    o = _host(o)
+    _close(o[:64], wo[:64], TOL[dtype], "earlier chunk")
+    assert not np.all(np.isfinite(o[70]))
+    d = np.abs(o - wo)[np.isfinite(o)]
+    assert np.all(d <= 40 * TOL[dtype] * np.abs(wo).max())
+    if name != "q":
+        assert not np.any(np.isfinite(o[128:]).all(-1)) and not np.all(np.isfinite(_host(sT)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,B,Hk,Hv,Dk,Dv", [(8, 5, 1, 2, 64, 64), (17, 6, 2, 4, 128, 128), (33, 5, 2, 2, 128, 64),
+                                             (9, 4, 1, 1, 24, 40), (20, 3, 1, 1, 256, 72)])
+def test_step_of_many_tokens(T, B, Hk, Hv, Dk, Dv, dtype):
+    """Slots in any order, slots outside the pool, sequences of every length down to none, garbage behind the masks."""
+    import bwd_persistent_cta_gb300 as R
+    import torch
+    inp = _inputs(T, B, Hk, Hv, Dk, Dv, dtype, 505 + T)
+    lens = [T, 0, T - 1, 1, T // 2, 8][:B]
+    for b, n in enumerate(lens):
+        for name in NAMES:
+            inp[name][n:, b] = np.nan
+    pool = B + 4
+    rng = np.random.default_rng(9)
+    state = rng.normal(size=(pool, Hv, Dv, Dk)).astype(np.float32)
+    slots = rng.permutation(pool)[:B].astype(np.int32)
+    skipped = {2: -1} if B < 5 else {2: -1, 4: pool}
+    for b, s in skipped.items():
+        slots[b] = s
+    op = R.DeltaRule(B, T, Hk, Hv, Dk, Dv, dtype=dtype, batch_first=True)
+    op.set_seq_lengths(lens)
+    st = torch.from_numpy(state.copy()).cuda()
+    x = [_dev(inp[n], dtype, bfirst=True, packed=True) for n in NAMES]
+    o = _host(op.step(*x, st, slots=torch.from_numpy(slots).cuda()), True)
+    st = st.cpu().numpy()
+    a = [np.nan_to_num(inp[n]) for n in NAMES]
+    s0 = np.stack([state[s] if 0 <= s < pool else np.zeros_like(state[0]) for s in slots])
+    wo, ws, _ = O.delta_forward(*a, s0, lens)
+    want = state.astype(np.float64)
+    for b in range(B):
+        if b in skipped:
+            wo[:, b] = 0.0
+        else:
+            want[slots[b]] = ws[b]
+        assert np.all(o[lens[b]:, b] == 0.0)
+    _close(o, wo, TOL[dtype], "o")
+    _close(st.astype(np.float64), want, TOL["f32"], "state")
+    same = sorted(set(range(pool)) - {int(slots[b]) for b in range(B) if b not in skipped and lens[b]})
+    np.testing.assert_array_equal(st[same], state[same])
+
+
+@pytest.mark.parametrize("T,B,Hk,Hv,Dk,Dv", [(1500, 2, 1, 2, 128, 128), (1000, 1, 2, 4, 64, 96), (300, 1, 80, 80, 128, 128)])
+def test_bf16_states_hold_22_bits(T, B, Hk, Hv, Dk, Dv):
+    """States behind bf16 sequences.  What reaches a state is held as pairs of fp16, 22 bits below the largest of a tile:
+    four products on a value's way, each with up to three terms of 2^-23 of it, is 12 * 2^-23 = 1.4e-6."""
+    inp = _inputs(T, B, Hk, Hv, Dk, Dv, "bf16", 530, gate=0.2)
+    got, want = _run(inp, "bf16"), _want(inp)
+    for n in ("sT", "ds0"):
+        _close(got[n], want[n], 12 * 2.0 ** -23, n)
