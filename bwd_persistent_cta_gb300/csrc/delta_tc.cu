@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "delta_tc.h"
+#include "pair.cuh"
 
 namespace rnn {
 
@@ -71,23 +72,6 @@ __device__ __forceinline__ float warp_max(float m) {
   return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
-        "l"(reinterpret_cast<const unsigned long long&>(c)));
-  return r;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 lo2(const float (&x)[4]) { return make_float2(x[0], x[1]); }
 __device__ __forceinline__ float2 hi2(const float (&x)[4]) { return make_float2(x[2], x[3]); }
 __device__ __forceinline__ void set4(float (&x)[4], float2 lo, float2 hi) {

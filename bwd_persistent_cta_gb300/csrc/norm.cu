@@ -3,6 +3,7 @@
 // gradients of all of it in another.
 #include "common.cuh"
 #include "norm.h"
+#include "pair.cuh"
 
 namespace rnn {
 
@@ -81,31 +82,6 @@ __device__ __forceinline__ void raw_async(Raw<T, V>* slot, const void* base, int
   for (int i = 0; i < static_cast<int>(sizeof(Raw<T, V>)); i += 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst + i), "l"(ok ? src + i : src), "r"(n) : "memory");
 }
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
-        "l"(reinterpret_cast<const unsigned long long&>(c)));
-  return r;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Sums N values over the TPR consecutive threads of a row; every thread gets
 // the sums.  Rows wider than a warp go through shared memory, ``red`` holding
