@@ -4,6 +4,7 @@
 // gradients.
 #include "common.cuh"
 #include "delta.h"
+#include "pair.cuh"
 
 namespace rnn {
 
@@ -90,16 +91,78 @@ struct TokenStage {
   T k[kAhead][32 * VPL], q[kAhead][32 * VPL], x[kAhead][kWarps * R];   // x: v, or do
   float al[kAhead], bl[kAhead], beta[kAhead];                          // e^g in two parts
 };
-// A sequence's state is S + L, its decay al + bl: S is rounded once a token, and
-// over a memory of a thousand tokens those roundings would add up to thirty times
-// one, so L keeps what S lost and bl what al lost.  This is S + L <- al S + t, with
-// t = al L + bl S + u k from before.  Outputs and sums take S alone, within half a
-// last place.  Against 64 bits, 513 tokens of slow decay: 2.9e-6 without, 4e-7 with
-// (324 and 340 us forward and backward, 1024 rows of 64).
-__device__ __forceinline__ void carry_step(float& S, float& L, float al, float t) {
-  const float h = fmaf(al, S, t);
-  L = fmaf(al, S, -h) + t;
-  S = h;
+// The state of an fp32 sequence is S + L, its decay al + bl: S is rounded once a
+// token, and over a memory of a thousand tokens those roundings would add up to
+// thirty times one, so L keeps what S lost and bl what al lost.  Outputs and sums
+// take S alone, within half a last place.  Gradients against 64 bits, 513 tokens of
+// slow decay: up to 2.2e-6 without, 3.6e-7 with.  bf16 storage does without: its
+// outputs' own rounding is 2^-9.
+//
+// e^g - al, where al - 1 is exact; below one half a state is forgotten before its
+// roundings add up.
+__device__ __forceinline__ float decay_rest(float g, float al) {
+  return al >= 0.5f && al <= 2.f ? expm1f(g) - (al - 1.f) : 0.f;
+}
+// al L + bl S of a row, while the token's u is not yet known.
+template <int V>
+__device__ __forceinline__ void carry_early(const float (&S)[V], float (&L)[V], float al, float bl) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 l = fma2(both(al), make_float2(L[j], L[j + 1]), mul2(both(bl), make_float2(S[j], S[j + 1])));
+      L[j] = l.x;
+      L[j + 1] = l.y;
+    }
+  } else {
+    L[0] = fmaf(al, L[0], bl * S[0]);
+  }
+}
+// S + L <- al S + (L + u k).
+template <int V>
+__device__ __forceinline__ void carry_step(float (&S)[V], float (&L)[V], float al, float u, const float (&k)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 s = make_float2(S[j], S[j + 1]);
+      const float2 t = fma2(both(u), make_float2(k[j], k[j + 1]), make_float2(L[j], L[j + 1])), h = fma2(both(al), s, t);
+      const float2 l = add2(fma2(both(al), s, make_float2(-h.x, -h.y)), t);
+      S[j] = h.x;
+      S[j + 1] = h.y;
+      L[j] = l.x;
+      L[j + 1] = l.y;
+    }
+  } else {
+    const float t = fmaf(u, k[0], L[0]), h = fmaf(al, S[0], t);
+    L[0] = fmaf(al, S[0], -h) + t;
+    S[0] = h;
+  }
+}
+// A lane's part of a . b, and y = x + f a (two elements an instruction: worth it
+// where instructions count, with eight rows a warp; with two rows the recurrence of
+// 1024 rows of 64 took 164 us so and 158 without).
+template <int V>
+__device__ __forceinline__ float dot_part(const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+    float2 s = mul2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+#pragma unroll
+    for (int j = 2; j < V; j += 2) s = fma2(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), s);
+    return s.x + s.y;
+  } else {
+    return a[0] * b[0];
+  }
+}
+template <int V>
+__device__ __forceinline__ void add_times(float (&y)[V], const float (&x)[V], float f, const float (&a)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 s = fma2(both(f), make_float2(a[j], a[j + 1]), make_float2(x[j], x[j + 1]));
+      y[j] = s.x;
+      y[j + 1] = s.y;
+    }
+  } else {
+    y[0] = fmaf(f, a[0], x[0]);
+  }
 }
 struct TokenSource {
   const void *k, *q, *x;       // of this CTA's heads and value columns, token 0
@@ -138,10 +201,8 @@ __device__ __forceinline__ float2 stage_fetch(TokenStage<T, VPL, R>& st, const T
 template <typename T, int VPL, int R>
 __device__ __forceinline__ void stage_ready(TokenStage<T, VPL, R>& st, float2 gb) {
   if (threadIdx.x < TokenStage<T, VPL, R>::kAhead) {
-    // below one half a state is forgotten before its roundings add up
-    const float al = expf(gb.x);
-    st.al[threadIdx.x] = al;
-    st.bl[threadIdx.x] = al >= 0.5f && al <= 2.f ? expm1f(gb.x) - (al - 1.f) : 0.f;
+    st.al[threadIdx.x] = expf(gb.x);
+    if (sizeof(T) == 4) st.bl[threadIdx.x] = decay_rest(gb.x, st.al[threadIdx.x]);
     st.beta[threadIdx.x] = gb.y;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -154,10 +215,11 @@ __device__ __forceinline__ void stage_ready(TokenStage<T, VPL, R>& st, float2 gb
 // the warp.  Both are taken of the old state: S_t q = a (S q) + u (k . q).
 // One token costs the chain exp -> dot -> shuffles -> update.  AHEAD: tokens come
 // through shared memory a stage early (sequences); otherwise each is loaded one
-// token early (the serving step, where the state is what takes time).  Bound by
-// that chain: 0.29 us a token at 1024 rows of 64 in fp32 (0.56 when each token
-// was loaded one token early); the reverse below 0.27.
-template <typename T, int VPL, int R, bool AHEAD>
+// token early (the serving step, where the state is what takes time).  CARRY: with
+// the parts lost to rounding.  Bound by that chain: 0.31 us a token at 1024 rows of
+// 64 in fp32 (0.29 without CARRY; 0.56 when each token was loaded one token early);
+// the reverse 0.29.
+template <typename T, int VPL, int R, bool AHEAD, bool CARRY>
 __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRecurArgs r) {
   constexpr int kAhead = TokenStage<T, VPL, R>::kAhead;
   __shared__ __align__(16) TokenStage<T, VPL, R> st[AHEAD ? 2 : 1];
@@ -206,9 +268,9 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
     const bool ok = in && live && r.s_in != nullptr && dv0 + i < a.Dv;
     load_vec<float, VPL>(r.s_in + s_off + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, S[i]);
   }
-  float L[AHEAD ? R : 1][VPL];
+  float L[CARRY ? R : 1][VPL];
 #pragma unroll
-  for (int i = 0; i < (AHEAD ? R : 1); ++i)
+  for (int i = 0; i < (CARRY ? R : 1); ++i)
 #pragma unroll
     for (int j = 0; j < VPL; ++j) L[i][j] = 0.f;
   float kc[VPL], qc[VPL], vc = 0.f, al = 0.f, bl = 0.f, bc = 0.f;
@@ -244,6 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
       for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
       vc = vn; bc = bn;
       al = expf(gn);
+      if (CARRY) bl = decay_rest(gn, al);
       if (t + 1 < len) direct(t + 1);
     }
     if (r.ckpt && t % kSimtChunk == 0 && in) {
@@ -253,17 +316,29 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
         if (dv0 + i < a.Dv) store_state<VPL>(c + static_cast<int64_t>(dv0 + i) * a.Dk, S[i]);
     }
     float d[2 * R], kq = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2 * R; ++i) d[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      kq = fmaf(kc[j], qc[j], kq);
+    if constexpr (R == 8 && CARRY) {
+      kq = dot_part<VPL>(kc, qc);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        d[i] = fmaf(S[i][j], kc[j], d[i]);
-        d[R + i] = fmaf(S[i][j], qc[j], d[R + i]);
-        if (AHEAD) L[i][j] = fmaf(al, L[i][j], bl * S[i][j]);
+        d[i] = dot_part<VPL>(S[i], kc);
+        d[R + i] = dot_part<VPL>(S[i], qc);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * R; ++i) d[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        kq = fmaf(kc[j], qc[j], kq);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          d[i] = fmaf(S[i][j], kc[j], d[i]);
+          d[R + i] = fmaf(S[i][j], qc[j], d[R + i]);
+        }
+      }
+    }
+    if constexpr (CARRY) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) carry_early<VPL>(S[i], L[i], al, bl);
     }
     const float sum = warp_sum_many<2 * R>(d, lane);
 #pragma unroll
@@ -283,10 +358,11 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float ui = __shfl_sync(kFull, u, i);
+      if constexpr (CARRY) {
+        carry_step<VPL>(S[i], L[i], al, ui, kc);
+      } else {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        if (AHEAD) carry_step(S[i][j], L[i][j], al, fmaf(ui, kc[j], L[i][j]));
-        else S[i][j] = fmaf(al, S[i][j], ui * kc[j]);      // one rounding of the state's size
+        for (int j = 0; j < VPL; ++j) S[i][j] = fmaf(al, S[i][j], ui * kc[j]);      // one rounding of the state's size
       }
     }
   }
@@ -495,9 +571,10 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
     const bool ok = in && r.dsT != nullptr && dv0 + i < a.Dv;
     load_vec<float, VPL>(r.dsT + bh * head_elems + static_cast<int64_t>(dv0 + i) * a.Dk + dk0, ok, dS[i]);
   }
-  float L[R][VPL];
+  constexpr bool CARRY = sizeof(T) == 4;
+  float L[CARRY ? R : 1][VPL];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < (CARRY ? R : 1); ++i)
 #pragma unroll
     for (int j = 0; j < VPL; ++j) L[i][j] = 0.f;
   float* yt = r.y + ((bh * a.T + len - 1) * a.Dv + dv0 + lane);
@@ -522,11 +599,21 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       dd[i] = a.scale * __shfl_sync(kFull, dc, i);
-      d[i] = 0.f;
+      if constexpr (CARRY && R == 8) {
+        float x[VPL];
+        add_times<VPL>(x, dS[i], dd[i], qc);
+        d[i] = dot_part<VPL>(x, kc);
+      } else {
+        d[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        d[i] = fmaf(fmaf(dd[i], qc[j], dS[i][j]), kc[j], d[i]);
-        L[i][j] = fmaf(al, fmaf(dd[i], qc[j], L[i][j]), bl * dS[i][j]);
+        for (int j = 0; j < VPL; ++j) d[i] = fmaf(fmaf(dd[i], qc[j], dS[i][j]), kc[j], d[i]);
+      }
+    }
+    if constexpr (CARRY) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        add_times<VPL>(L[i], L[i], dd[i], qc);
+        carry_early<VPL>(dS[i], L[i], al, bl);
       }
     }
     const float sum = warp_sum_many<R>(d, lane);
@@ -537,8 +624,12 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float ei = __shfl_sync(kFull, de, i);
+      if constexpr (CARRY) {
+        carry_step<VPL>(dS[i], L[i], al, -al * ei, kc);
+      } else {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) carry_step(dS[i][j], L[i][j], al, fmaf(-al * ei, kc[j], L[i][j]));
+        for (int j = 0; j < VPL; ++j) dS[i][j] = fmaf(al, dS[i][j], al * fmaf(dd[i], qc[j], -ei * kc[j]));
+      }
     }
   }
   if (r.ds0 && in) {
@@ -813,18 +904,34 @@ bool few_rows(const DeltaArgs& a, int num_sms) {
   return static_cast<int64_t>(a.B) * a.Hv * a.Dv <= 16ll * num_sms;
 }
 
-// Sequences of at least this many tokens are staged.
+// Where warps are many, what counts is instructions, and eight rows a warp share a
+// token's (fp32, 256 tokens, forward and reverse: 65536 rows of 128 927 + 920 us
+// against 1106 + 1015 with four rows, 8192 rows of 64 121 + 113 against 137 + 120;
+// 4096 rows of 32 105 + 86 against 89 + 77).
+bool many_rows(const DeltaArgs& a, int num_sms) {
+  return static_cast<int64_t>(a.B) * a.Hv * a.Dv >= 48ll * num_sms;
+}
+
+// Sequences of at least this many tokens are staged (bf16, 4096 rows of 128, staged
+// and not: 4 tokens 6.7 and 7.6 us, 8 tokens 7.3 and 10.4, 32 tokens 17 and 29;
+// 98304 rows: 4 tokens 38.5 and 37.5, 8 tokens 56 and 58).
 constexpr int kAheadFrom = 8;
 
-template <typename T, int VPL, int R, bool AHEAD>
+template <typename T, int VPL, int R, bool AHEAD, bool CARRY>
 int recur(const DeltaRecurArgs& r, cudaStream_t s) {
   const int64_t groups = (r.a.Dv + kWarps * R - 1) / (kWarps * R);
-  delta_recur_kernel<T, VPL, R, AHEAD><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
+  delta_recur_kernel<T, VPL, R, AHEAD, CARRY><<<static_cast<unsigned>(groups * r.a.Hv * r.a.B), kWarps * 32, 0, s>>>(r);
   return check_launch();
 }
 template <typename T, int VPL>
 int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
-  if (r.a.T >= kAheadFrom) return few_rows(r.a, r.num_sms) ? recur<T, VPL, 2, true>(r, s) : recur<T, VPL, 4, true>(r, s);
+  constexpr bool f32 = sizeof(T) == 4;
+  if (r.a.T >= kAheadFrom) {
+    if constexpr (f32 && VPL <= 4) {
+      if (many_rows(r.a, r.num_sms)) return recur<T, VPL, 8, true, true>(r, s);
+    }
+    return few_rows(r.a, r.num_sms) ? recur<T, VPL, 2, true, f32>(r, s) : recur<T, VPL, 4, true, f32>(r, s);
+  }
   if constexpr (VPL <= 4) {
     // A step over more units than three CTAs an SM take in two turns.  With more
     // than two tokens the chain of a unit is longer than its transfer and the
@@ -842,9 +949,9 @@ int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
   if constexpr (VPL <= 4) {
     // several tokens for many states: bound by issue, where eight rows share a
     // token's work (48 sequences x 16 heads, four tokens: 25.6 against 27.6 us)
-    if (static_cast<int64_t>(r.a.B) * r.a.Hv * r.a.Dv >= 256ll * r.num_sms && r.a.T > 1) return recur<T, VPL, 8, false>(r, s);
+    if (static_cast<int64_t>(r.a.B) * r.a.Hv * r.a.Dv >= 256ll * r.num_sms && r.a.T > 1) return recur<T, VPL, 8, false, false>(r, s);
   }
-  return recur<T, VPL, 4, false>(r, s);
+  return recur<T, VPL, 4, false, false>(r, s);
 }
 template <typename T>
 int recur_t(const DeltaRecurArgs& r, cudaStream_t s) {
@@ -863,6 +970,9 @@ int recur_bwd(const DeltaRecurBwdArgs& r, cudaStream_t s) {
 }
 template <typename T, int VPL>
 int recur_bwd_v(const DeltaRecurBwdArgs& r, cudaStream_t s) {
+  if constexpr (sizeof(T) == 4 && VPL <= 4) {      // VPL 8 has no registers for eight rows
+    if (many_rows(r.a, r.num_sms)) return recur_bwd<T, VPL, 8>(r, s);
+  }
   return few_rows(r.a, r.num_sms) ? recur_bwd<T, VPL, 2>(r, s) : recur_bwd<T, VPL, 4>(r, s);
 }
 template <typename T>

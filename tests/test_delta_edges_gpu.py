@@ -4,7 +4,7 @@ import pytest
 
 from oracle import lm_oracle as O
 
-from tests.test_delta_gpu import TOL, _close, _dev, _host, _inputs, _run, _want
+from tests.test_delta_gpu import TOL, _close, _compare, _dev, _host, _inputs, _run, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,13 @@ def test_bf16_states_hold_22_bits(T, B, Hk, Hv, Dk, Dv):
     got, want = _run(inp, "bf16"), _want(inp)
     for n in ("sT", "ds0"):
         _close(got[n], want[n], 12 * 2.0 ** -23, n)
+
+
+@pytest.mark.parametrize("shape", [(75, 8, 8, 16, 64, 64), (70, 4, 16, 16, 128, 128), (40, 16, 16, 16, 24, 40),
+                                   (40, 2, 16, 16, 256, 256)], ids=str)
+def test_fp32_with_many_rows(shape):
+    """Enough rows of state that a warp takes eight, with lengths."""
+    T, B = shape[:2]
+    inp = _inputs(*shape, "f32", 540)
+    lens = [T - (b * T) // B for b in range(B)]
+    _compare(_run(inp, "f32", lens=lens, packed=True), _want(inp, lens), "f32")
