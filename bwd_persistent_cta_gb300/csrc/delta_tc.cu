@@ -180,7 +180,7 @@ struct LaneOffsets {
 // low), block row 3 in 48..63 and 64..79, block row 2 in 32..47 with what does
 // not fit beside block row 0 in lines 0..15.  A block's rows are 16 lines from
 // tri_line, two pieces from tri_piece; pieces are exchanged by (line & 7).  10 KB
-// instead of 16 let two CTAs of a scan share an SM.
+// instead of 16 let two scan CTAs of four warps share an SM where Dk is 64.
 __host__ __device__ constexpr int tri_line(int b, int kb, int part) {
   return b < 2 ? 16 * b : b == 2 ? (part && kb ? 0 : 32) : 48 + 16 * part;
 }
@@ -1259,25 +1259,40 @@ __global__ void __launch_bounds__(128) delta_pair_fwd_kernel(const DeltaTcArgs p
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
 
-// 16-column slices a scan CTA takes: 8 or 4, a warp each, or 2 with two warps
-// each.  One CTA is resident on an SM, and a chunk of D = 128 takes it 5.4, 3.25
-// or 2.5 us (measured, inference; the training forward and the reverse scan keep
-// the order), so what counts is the number of turns times that.
-int scan_slices(const DeltaArgs& a, int num_sms) {
+// 16-column slices a scan CTA takes: 8 or 4, a warp each, or 2 with two warps each;
+// 8 for Dk 128 only.  What counts is the number of turns times a chunk's time,
+// measured with 152 CTAs of 16 chunks, us:
+//            Dk 128: 8     4     2      Dk 64: 8     4     2
+//   inference       5.8   3.5   2.75          3.9   2.3   2.25
+//   training        6.9   4.3   3.0           4.5   2.7   2.6
+//   reverse         8.3   5.3   3.45          5.5   3.35  2.75
+// One CTA is resident on an SM, but two of 4 slices with Dk 64, which take 3.7, 4.4
+// and 5.1 together: never longer than one of 8, which is therefore not built.
+enum { kScanInfer, kScanTrain, kScanReverse };
+int scan_slices(const DeltaArgs& a, int num_sms, int kind) {
+  struct Choice {
+    int take, two;               // slices; whether two CTAs share an SM
+    double us[3], us2[3];
+  };
+  static const Choice c128[] = {{8, 0, {5.8, 6.9, 8.3}, {}}, {4, 0, {3.5, 4.3, 5.3}, {}}, {2, 0, {2.75, 3.0, 3.45}, {}}};
+  static const Choice c64[] = {{4, 1, {2.3, 2.7, 3.35}, {3.7, 4.4, 5.1}}, {2, 0, {2.25, 2.6, 2.75}, {}}};
   const int n = a.Dv / 16;
-  const int take[3] = {8, 4, 2};
-  const double us[3] = {5.4, 3.25, 2.5};
   int best = 2;
   double least = 1e30;
-  for (int i = 0; i < 3; ++i) {
-    if (n % take[i]) continue;
-    const int64_t ctas = static_cast<int64_t>(a.B) * a.Hv * (n / take[i]);
-    const double cost = static_cast<double>((ctas + num_sms - 1) / num_sms) * us[i];
+  auto weigh = [&](const Choice& c) {
+    if (n % c.take) return;
+    const int64_t ctas = static_cast<int64_t>(a.B) * a.Hv * (n / c.take), turns = (ctas + num_sms - 1) / num_sms;
+    const double cost = c.two ? static_cast<double>(turns / 2) * c.us2[kind] + static_cast<double>(turns % 2) * c.us[kind]
+                              : static_cast<double>(turns) * c.us[kind];
     if (cost < least) {
       least = cost;
-      best = take[i];
+      best = c.take;
     }
-  }
+  };
+  if (a.Dk == 64)
+    for (const Choice& c : c64) weigh(c);
+  else
+    for (const Choice& c : c128) weigh(c);
   return best;
 }
 
@@ -1294,11 +1309,12 @@ int forward(const DeltaTcArgs& t, cudaStream_t s, int* launches) {
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
-  const int w = scan_slices(t.a, t.num_sms);
+  const int w = scan_slices(t.a, t.num_sms, TRAIN ? kScanTrain : kScanInfer);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
-  if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
-  else if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
-  else delta_pair_fwd_kernel<DK, TRAIN><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
+  if constexpr (DK == 128)
+    if (w == 8) delta_scan_fwd_kernel<DK, TRAIN, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
+  if (w == 4) delta_scan_fwd_kernel<DK, TRAIN, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
+  if (w == 2) delta_pair_fwd_kernel<DK, TRAIN><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
   rc = check_launch();
   if (!rc) ++*launches;
   return rc;
@@ -2201,11 +2217,12 @@ __global__ void __launch_bounds__(GradSmem<DK>::NT) delta_grad_kernel(const Delt
 template <int DK>
 int backward(const DeltaTcBwdArgs& t, cudaStream_t s, int* launches) {
   const int gsm = sizeof(GradSmem<DK>);
-  const int w = scan_slices(t.a, t.num_sms);
+  const int w = scan_slices(t.a, t.num_sms, kScanReverse);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(t.a.B) * t.a.Hv * (t.a.Dv / (16 * w)));
-  if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
-  else if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
-  else delta_pair_bwd_kernel<DK><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
+  if constexpr (DK == 128)
+    if (w == 8) delta_scan_bwd_kernel<DK, 8><<<grid, 256, sizeof(ScanSmem<DK, 8>), s>>>(t);
+  if (w == 4) delta_scan_bwd_kernel<DK, 4><<<grid, 128, sizeof(ScanSmem<DK, 4>), s>>>(t);
+  if (w == 2) delta_pair_bwd_kernel<DK><<<grid, 128, sizeof(PairSmem<DK>), s>>>(t);
   int rc = check_launch();
   if (rc) return rc;
   ++*launches;
@@ -2222,12 +2239,13 @@ int init_scans() {
   return set_smem(delta_scan_fwd_kernel<DK, false, W>, smem) || set_smem(delta_scan_fwd_kernel<DK, true, W>, smem) ||
          set_smem(delta_scan_bwd_kernel<DK, W>, smem);
 }
+int init_wide() { return init_scans<128, 8>(); }
 template <int DK>
 int init() {
   const int gsm = sizeof(GradSmem<DK>);
   return set_smem(delta_prep_kernel<DK, false>, sizeof(PrepSmem<DK, false>)) ||
                  set_smem(delta_prep_kernel<DK, true>, sizeof(PrepSmem<DK, true>)) ||
-                 init_scans<DK, 4>() || init_scans<DK, 8>() || set_smem(delta_grad_kernel<DK>, gsm) ||
+                 init_scans<DK, 4>() || (DK == 128 && init_wide()) || set_smem(delta_grad_kernel<DK>, gsm) ||
                  set_smem(delta_pair_fwd_kernel<DK, false>, sizeof(PairSmem<DK>)) ||
                  set_smem(delta_pair_fwd_kernel<DK, true>, sizeof(PairSmem<DK>)) || set_smem(delta_pair_bwd_kernel<DK>, sizeof(PairSmem<DK>))
              ? RNN_CUDA_ERROR
