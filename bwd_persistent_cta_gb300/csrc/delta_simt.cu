@@ -899,7 +899,8 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 int vpl_of(int Dk) { return Dk <= 32 ? 1 : Dk <= 64 ? 2 : Dk <= 128 ? 4 : 8; }
 
 // Where four rows a warp would leave schedulers without one, two: a token's
-// chain is then shorter (fp32, 1024 rows of 64, 513 tokens: 149 against 168 us).
+// chain is then shorter (fp32, 513 tokens of 128, with two and four rows a warp:
+// 1024 rows 173 and 200 us, 2048 rows 194 and 201, 4096 rows 260 and 234).
 bool few_rows(const DeltaArgs& a, int num_sms) {
   return static_cast<int64_t>(a.B) * a.Hv * a.Dv <= 16ll * num_sms;
 }
@@ -935,8 +936,10 @@ int recur_v(const DeltaRecurArgs& r, cudaStream_t s) {
   if constexpr (VPL <= 4) {
     // A step over more units than three CTAs an SM take in two turns.  With more
     // than two tokens the chain of a unit is longer than its transfer and the
-    // recurrence's larger number of warps wins (256 sequences x 32 heads x 128 x 128,
-    // one token: 173 us against 203; 48 x 16, four tokens: 30.0 against 25.6).
+    // recurrence's larger number of warps wins (128 x 128, pipeline and recurrence:
+    // 256 sequences x 32 heads, one token 175 and 232 us, two 245 and 284, three 318
+    // and 325, four 393 and 371; 48 x 16, one 21.7 and 22.1, two 28.0 and 27.2, three
+    // 36.0 and 32.3).
     const int64_t units = static_cast<int64_t>((r.a.Dv + kUnitRows - 1) / kUnitRows) * r.a.Hv * r.a.B;
     if (r.status && r.a.T <= 2 && units >= 6 * r.num_sms && units + 3ll * kUnits * r.num_sms < (1ll << 31)) {
       const int smem = sizeof(StepSmem<VPL>);
