@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
 // that a pair on one side of a token cancels exactly instead of to rounding.
 // Thread (i, l) of 256 owns token i and key columns l, l + 8, ...; the value
 // columns pass in slices of 16, the next one on its way meanwhile.  Bound by
-// shared memory reads, one for each multiply-add or two: 62 us for 68 chunks of
+// shared memory reads, one for each multiply-add or two: 64 us for 68 chunks of
 // two heads of 64 x 128 (110 before slices were fetched early).
 constexpr int kCb = kSimtChunk;      // tokens
 constexpr int kSlice = 16;           // value columns a pass

@@ -354,8 +354,11 @@ rnn_status_t rnn_noalloc_status(void* stream);
  * Sequences are [T, B, heads, dim], or [B, T, heads, dim] with batch_first;
  * g and beta are [T, B, heads_v] (or [B, T, heads_v]).  Element type of
  * q, k, v, g, beta, o and their gradients is desc.dtype.  States (s0, sT, the
- * pool of rnn_delta_step, ds0, dsT) are fp32 [B, heads_v, dim_v, dim_k], and
- * every sum and state is held in fp32.
+ * pool of rnn_delta_step, ds0, dsT) are fp32 [B, heads_v, dim_v, dim_k]; sums are
+ * fp32, and so are the states on their way through a sequence.  With bf16 storage
+ * a product that reaches a state takes operands of 22 bits or more, one that ends
+ * in a bf16 output or gradient 11 bits (o, and what the reserve keeps of states
+ * and e for the gradients): against the 8 bits of the results.
  * The conventions at the top of this file hold.  No kernel of these operators
  * waits for another CTA, so they need no resident grid and may overlap other
  * kernels; the chunk kernels' waits for their own copies are bounded all the
