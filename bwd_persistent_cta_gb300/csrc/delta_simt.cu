@@ -83,13 +83,13 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
 }
 
 // Tokens on their way to a recurrence CTA: kAhead of them a stage, two stages
-// (at most 34 KB).  A token's chain of dependent arithmetic is shorter than one
+// (at most 37 KB).  A token's chain of dependent arithmetic is shorter than one
 // trip to memory, so what it reads has to be asked for many tokens earlier.
 template <typename T, int VPL, int R>
 struct TokenStage {
   static constexpr int kAhead = sizeof(T) * VPL > 16 ? 8 : 16;
   T k[kAhead][32 * VPL], q[kAhead][32 * VPL], x[kAhead][kWarps * R];   // x: v, or do
-  float al[kAhead], bl[kAhead], beta[kAhead];                          // e^g in two parts
+  float al[kAhead], bl[kAhead], beta[kAhead];                          // e^g in two parts (bl: fp32)
 };
 // The state of an fp32 sequence is S + L, its decay al + bl: S is rounded once a
 // token, and over a memory of a thousand tokens those roundings would add up to
@@ -221,6 +221,7 @@ __device__ __forceinline__ void stage_ready(TokenStage<T, VPL, R>& st, float2 gb
 // the reverse 0.29.
 template <typename T, int VPL, int R, bool AHEAD, bool CARRY>
 __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRecurArgs r) {
+  static_assert(AHEAD || !CARRY, "a few tokens' roundings do not add up");
   constexpr int kAhead = TokenStage<T, VPL, R>::kAhead;
   __shared__ __align__(16) TokenStage<T, VPL, R> st[AHEAD ? 2 : 1];
   const DeltaArgs& a = r.a;
@@ -299,14 +300,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_kernel(const DeltaRec
       load_vec<T, VPL>(&s.q[n][dk0], in, qc);
       vc = vin ? to_f<T>(s.x[n][warp * R + lane]) : 0.f;
       al = s.al[n];
-      bl = s.bl[n];
+      if (CARRY) bl = s.bl[n];
       bc = s.beta[n];
     } else {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) { kc[j] = kn[j]; qc[j] = qn[j]; }
       vc = vn; bc = bn;
       al = expf(gn);
-      if (CARRY) bl = decay_rest(gn, al);
       if (t + 1 < len) direct(t + 1);
     }
     if (r.ckpt && t % kSimtChunk == 0 && in) {
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recur_bwd_kernel(const Delt
     float kc[VPL], qc[VPL];
     load_vec<T, VPL>(&s.k[n][dk0], in, kc);
     load_vec<T, VPL>(&s.q[n][dk0], in, qc);
-    const float dc = vin ? to_f<T>(s.x[n][warp * R + lane]) : 0.f, al = s.al[n], bl = s.bl[n], bc = s.beta[n];
+    const float dc = vin ? to_f<T>(s.x[n][warp * R + lane]) : 0.f, al = s.al[n], bl = CARRY ? s.bl[n] : 0.f, bc = s.beta[n];
     if ((t % kSimtChunk == kSimtChunk - 1 || it == 0) && in) {
       float* c = r.ckpt + (bh * nc + t / kSimtChunk) * head_elems + dk0;
 #pragma unroll
