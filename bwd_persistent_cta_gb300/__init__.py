@@ -9,7 +9,8 @@ device memory and the current stream.
 ``RNN`` is a convenience wrapper that allocates the workspace / reserve with
 torch and calls the same entry points; ``DeltaRule`` (the gated delta rule) and
 ``BlockNorm`` (the norms, gate and residual around a block) do the same for
-theirs (``lm.py``).
+theirs (``lm.py``), and so do ``SelectiveScan``, ``CausalConv`` and ``GradClip``
+(``ssm.py``).
 """
 from __future__ import annotations
 
@@ -54,6 +55,28 @@ class rnn_norm_desc_t(ctypes.Structure):
 class rnn_norm_in_t(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("y", "z", "x", "w_in", "scale", "w_out")] +
                 [(n, ctypes.c_int64) for n in ("y_row", "z_row", "x_row")])
+
+
+class rnn_scan_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "seq_len", "channels", "states", "groups", "dtype", "batch_first",
+                                            "softplus")]
+
+
+class rnn_scan_in_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias")] +
+                [(n, ctypes.c_int64) for n in ("x_row", "dt_row", "z_row", "B_row", "C_row")])
+
+
+class rnn_scan_grad_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0")]
+
+
+class rnn_conv_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "seq_len", "channels", "width", "dtype", "batch_first", "act")]
+
+
+class rnn_conv_in_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "w", "bias")] + [("x_row", ctypes.c_int64)]
 
 
 class RnnError(RuntimeError):
@@ -111,6 +134,30 @@ _SIGS = {
     "rnn_norm_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 3),
     "rnn_norm_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_norm_in_t)] + [_P] * 10),
     "rnn_norm_launch_count": (ctypes.c_uint64, [_P]),
+    "rnn_scan_create": (ctypes.c_int, [ctypes.POINTER(rnn_scan_desc_t), ctypes.POINTER(_P)]),
+    "rnn_scan_destroy": (ctypes.c_int, [_P]),
+    "rnn_scan_get_sizes": (ctypes.c_int, [_P] + [ctypes.POINTER(ctypes.c_size_t)] * 3),
+    "rnn_scan_set_seq_lengths": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int)]),
+    "rnn_scan_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_scan_in_t)] + [_P] * 6),
+    "rnn_scan_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_scan_in_t), _P, _P, ctypes.POINTER(rnn_scan_grad_t)] +
+                          [_P] * 3),
+    "rnn_scan_step": (ctypes.c_int, [_P, ctypes.POINTER(rnn_scan_in_t), _P, ctypes.c_int, _P, _P, _P]),
+    "rnn_scan_launch_count": (ctypes.c_uint64, [_P]),
+    "rnn_conv_create": (ctypes.c_int, [ctypes.POINTER(rnn_conv_desc_t), ctypes.POINTER(_P)]),
+    "rnn_conv_destroy": (ctypes.c_int, [_P]),
+    "rnn_conv_get_sizes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rnn_conv_set_seq_lengths": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int)]),
+    "rnn_conv_forward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_conv_in_t)] + [_P] * 4),
+    "rnn_conv_backward": (ctypes.c_int, [_P, ctypes.POINTER(rnn_conv_in_t)] + [_P] * 9),
+    "rnn_conv_step": (ctypes.c_int, [_P, ctypes.POINTER(rnn_conv_in_t), _P, ctypes.c_int, _P, _P, _P]),
+    "rnn_conv_launch_count": (ctypes.c_uint64, [_P]),
+    "rnn_clip_create": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int),
+                                       ctypes.POINTER(_P)]),
+    "rnn_clip_destroy": (ctypes.c_int, [_P]),
+    "rnn_clip_get_sizes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rnn_clip_scale": (ctypes.c_int, [_P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
+    "rnn_clip_norm": (ctypes.c_int, [_P] * 5),
+    "rnn_clip_launch_count": (ctypes.c_uint64, [_P]),
     "rnn_debug_step_drain": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "rnn_debug_gemm": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int,
                                       _P, ctypes.c_int64, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int, _P,
@@ -535,3 +582,9 @@ from .lm import (  # noqa: E402
     rnn_delta_get_sizes, rnn_delta_launch_count, rnn_delta_set_seq_lengths, rnn_delta_step,
     rnn_delta_sync_status, rnn_norm_backward,
     rnn_norm_create, rnn_norm_destroy, rnn_norm_forward, rnn_norm_get_sizes, rnn_norm_launch_count)
+from .ssm import (  # noqa: E402
+    CausalConv, GradClip, SelectiveScan, rnn_clip_create, rnn_clip_destroy, rnn_clip_get_sizes, rnn_clip_launch_count,
+    rnn_clip_norm, rnn_clip_scale, rnn_conv_backward, rnn_conv_create, rnn_conv_destroy, rnn_conv_forward,
+    rnn_conv_get_sizes, rnn_conv_launch_count, rnn_conv_set_seq_lengths, rnn_conv_step, rnn_scan_backward,
+    rnn_scan_create, rnn_scan_destroy, rnn_scan_forward, rnn_scan_get_sizes, rnn_scan_launch_count,
+    rnn_scan_set_seq_lengths, rnn_scan_step)

@@ -3,13 +3,11 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstddef>
 #include <new>
 
-#include "call_order.h"
+#include "api_util.h"
 #include "delta.h"
 #include "delta_tc.h"
-#include "device_guard.h"
 #include "norm.h"
 #include "rnn.h"
 #include "rnn_debug.h"
@@ -45,10 +43,6 @@ struct rnn_norm_s {
 
 namespace {
 
-size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool flag(int v) { return v == 0 || v == 1; }
-
 rnn_status_t check_delta(const rnn_delta_desc_t* d) {
   if (!d) return RNN_BAD_PARAM;
   if (d->batch < 1 || d->seq_len < 1 || d->heads_k < 1 || d->heads_v < 1) return RNN_BAD_PARAM;
@@ -77,17 +71,6 @@ rnn_status_t check_norm(const rnn_norm_desc_t* d) {
   return RNN_OK;
 }
 
-// The current device, when it is one the kernels run on.
-rnn_status_t pick_device(int* dev, int* sms) {
-  if (cudaGetDevice(dev) != cudaSuccess) return RNN_CUDA_ERROR;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
-    return RNN_CUDA_ERROR;
-  return major == 10 && minor == 3 ? RNN_OK : RNN_NOT_SUPPORTED;
-}
-
 // From this many tokens on sequences run by chunks: where heads are many or
 // gradients follow (128 x 128, chunks and recurrence, kernels alone: 8 sequences x
 // 16 heads, 12 tokens 24 and 21 us, 16 tokens 25 and 26, training 56 and 124; 32 x
@@ -95,15 +78,6 @@ rnn_status_t pick_device(int* dev, int* sms) {
 // be faster token by token up to 48 tokens (4 heads, 16 tokens: 18 and 8.5 us) but
 // for the training forward, 45 and 99 with its backward, which shares the layout.
 constexpr int kTcMinTokens = 16;
-
-struct Bump {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    const size_t o = off;
-    off = al(off + bytes);
-    return o;
-  }
-};
 
 void delta_layout(rnn_delta_s* h) {
   const rnn_delta_desc_t& d = h->desc;
@@ -146,13 +120,6 @@ void delta_layout(rnn_delta_s* h) {
   h->bwd_workspace_bytes = b.off;
 }
 
-// A row stride in elements: 0 = dense; otherwise at least a row, and a
-// multiple of ``unit`` elements.
-bool row_ok(int64_t row, int64_t dense, int64_t unit, int64_t* out) {
-  *out = row ? row : dense;
-  return *out >= dense && *out % unit == 0;
-}
-
 rnn_status_t delta_args(const rnn_delta_s* h, const rnn_delta_in_t* in, DeltaArgs* a) {
   const rnn_delta_desc_t& d = h->desc;
   if (!in || !in->q || !in->k || !in->v || !in->g || !in->beta) return RNN_BAD_PARAM;
@@ -171,28 +138,6 @@ rnn_status_t delta_args(const rnn_delta_s* h, const rnn_delta_in_t* in, DeltaArg
   a->len = h->has_len ? h->d_len : nullptr;
   a->q = in->q; a->k = in->k; a->v = in->v; a->g = in->g; a->beta = in->beta;
   return RNN_OK;
-}
-
-// A call's place among the handle's calls that share something on the device:
-// lengths, workspace or reserve.
-struct Ordered {
-  CallOrder& order;
-  cudaStream_t s;
-  bool on;
-  rnn_status_t rc = RNN_OK;
-  Ordered(CallOrder& order_, bool shares, cudaStream_t s_) : order(order_), s(s_), on(shares) {
-    if (on) rc = order.enter(s);
-  }
-  // The call's status; what was launched before a failure counts as well.
-  rnn_status_t done(int e) {
-    const rnn_status_t l = on ? order.leave(s) : RNN_OK;
-    return e ? static_cast<rnn_status_t>(e) : l;
-  }
-};
-
-template <typename T>
-T* at(const void* base, size_t off) {
-  return reinterpret_cast<T*>(const_cast<char*>(static_cast<const char*>(base)) + off);
 }
 
 DeltaTcBufs tc_bufs(const rnn_delta_s* h, void* workspace, const void* reserve) {
@@ -305,26 +250,7 @@ rnn_status_t rnn_delta_set_seq_lengths(rnn_delta_t h, const int* lengths) {
   if (!h) return RNN_BAD_PARAM;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
-  if (!lengths) {
-    h->has_len = 0;
-    return RNN_OK;
-  }
-  const int B = h->desc.batch;
-  for (int b = 0; b < B; ++b)
-    if (lengths[b] < 0 || lengths[b] > h->desc.seq_len) return RNN_BAD_PARAM;
-  if (!h->d_len && cudaMalloc(&h->d_len, sizeof(int) * B) != cudaSuccess) {
-    h->d_len = nullptr;
-    return RNN_CUDA_ERROR;
-  }
-  // no call may still read the old lengths, and none may start before the new
-  // ones have landed: a copy from pageable memory can return earlier, and streams
-  // that do not wait for the legacy stream would not wait for it either
-  if (h->order.wait() != RNN_OK ||
-      cudaMemcpy(h->d_len, lengths, sizeof(int) * B, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)
-    return RNN_CUDA_ERROR;
-  h->has_len = 1;
-  return RNN_OK;
+  return set_lengths(h->order, lengths, h->desc.batch, h->desc.seq_len, &h->d_len, &h->has_len);
 }
 
 rnn_status_t rnn_delta_forward(rnn_delta_t h, const rnn_delta_in_t* in, const float* s0, void* o, float* sT,

@@ -99,7 +99,7 @@ def rnn_norm_launch_count(handle) -> int:
 
 # --- convenience wrappers (torch allocation + the calls above) ----------------
 class _Op:
-    """What the two wrappers share: the device, the handle's life and the tensor checks."""
+    """What the wrappers share: the device, the handle's life and the tensor checks."""
 
     def _bind(self, dtype: str, device):
         if dtype not in ("bf16", "f32"):
@@ -177,8 +177,9 @@ class _Op:
         with torch.cuda.stream(stream):
             out = call(*tensors, **more)
         for t in (*tensors, *more.values()):
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
+            for u in t if isinstance(t, (list, tuple)) else (t,):
+                if isinstance(u, torch.Tensor):
+                    u.record_stream(stream)
         results = (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out
         for t in results:
             if t is not None:

@@ -524,6 +524,192 @@ rnn_status_t rnn_norm_backward(rnn_norm_t handle, const rnn_norm_in_t* in, const
 /* Number of kernels this handle has launched since it was created. */
 uint64_t rnn_norm_launch_count(rnn_norm_t handle);
 
+/* ---------------------------------------------------------------------------
+ * Selective scan: the linear recurrence with a diagonal state, whose decay each
+ * channel and state has for itself and the input sets.  Per sequence and channel
+ * d, with ``states`` states a channel (n) and d's group of B and C:
+ *     delta_t = softplus(dt_t + dt_bias)          (dt_t + dt_bias without desc.softplus)
+ *     h_t[n]  = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t B_t[n]
+ *     y_t     = (sum_n C_t[n] h_t[n] + D x_t) * silu(z_t)
+ * without D, dt_bias or the gate z where their pointers are NULL.  Channel d reads
+ * group d / (channels / groups).  A < 0 in use.
+ *
+ * Sequences are [T, B, ..], or [B, T, ..] with batch_first.  Element type of x, dt,
+ * z, B, C, y and their gradients is desc.dtype; A, D, dt_bias, the states [B,
+ * channels, states] (h0, hT, the pool of rnn_scan_step, dh0, dhT) and the gradients
+ * of A, D and dt_bias are fp32, and so are all sums.  The conventions at the top of
+ * this file hold, but for what is said here; no kernel of these operators waits for
+ * another CTA or for a copy, so there is no status to ask for.  The calls of one
+ * handle that use lengths, workspace or reserve run in the order they are made,
+ * whatever their streams; calls captured into a graph are ordered by the caller.
+ * Calls that should overlap take a handle each. */
+typedef struct {
+  int batch;           /* B >= 1                                                       */
+  int seq_len;         /* T >= 1                                                       */
+  int channels;        /* 8..65536, a multiple of 8 * groups                           */
+  int states;          /* 8..64, a multiple of 8                                       */
+  int groups;          /* >= 1                                                         */
+  int dtype;           /* rnn_dtype_t                                                  */
+  int batch_first;     /* 0 = [T,B,...], 1 = [B,T,...]                                 */
+  int softplus;        /* 0 or 1                                                       */
+} rnn_scan_desc_t;
+
+typedef struct rnn_scan_s* rnn_scan_t;
+
+/* The inputs of one call.  *_row: elements from one (t, b) row to the next, so that
+ * x, dt, z, B and C may be slices of packed projections; 0 = dense.  x, dt and z
+ * must be 16-byte aligned with rows that are multiples of 16 bytes; B and C need
+ * only the alignment of their element. */
+typedef struct {
+  const void* x;          /* [.., channels]                       */
+  const void* dt;         /* [.., channels]                       */
+  const void* z;          /* [.., channels] or NULL = no gate     */
+  const void* B;          /* [.., groups, states]                 */
+  const void* C;          /* [.., groups, states]                 */
+  const void* A;          /* fp32 [channels, states]              */
+  const void* D;          /* fp32 [channels] or NULL              */
+  const void* dt_bias;    /* fp32 [channels] or NULL              */
+  int64_t x_row, dt_row, z_row, B_row, C_row;
+} rnn_scan_in_t;
+
+/* The gradients of one call (device, out, dense, overwritten; each may be NULL =
+ * not wanted). */
+typedef struct {
+  void* dx;               /* [.., channels]                       */
+  void* ddt;              /* [.., channels]                       */
+  void* dz;               /* [.., channels]                       */
+  void* dB;               /* [.., groups, states], summed over the group's channels */
+  void* dC;               /* [.., groups, states]                 */
+  void* dA;               /* fp32 [channels, states]              */
+  void* dD;               /* fp32 [channels]                      */
+  void* ddt_bias;         /* fp32 [channels]                      */
+  void* dh0;              /* fp32 [B, channels, states]           */
+} rnn_scan_grad_t;
+
+/* As rnn_delta_create / _destroy / _get_sizes / _set_seq_lengths: tokens at
+ * t >= lengths[b] are not read, the state stays as it was, y is zero there and so
+ * are all gradients. */
+rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* handle);
+rnn_status_t rnn_scan_destroy(rnn_scan_t handle);
+rnn_status_t rnn_scan_get_sizes(rnn_scan_t handle, size_t* workspace_bytes,
+                                size_t* backward_workspace_bytes, size_t* reserve_bytes);
+rnn_status_t rnn_scan_set_seq_lengths(rnn_scan_t handle, const int* lengths);
+
+/* Forward over whole sequences.
+ *   h0 (device, in, may be NULL = zero)   hT (device, out, may be NULL; may be h0)
+ *   y  [.., channels] (device, out, dense)
+ *   workspace (workspace_bytes)
+ *   reserve (reserve_bytes, out) - NULL runs inference. */
+rnn_status_t rnn_scan_forward(rnn_scan_t handle, const rnn_scan_in_t* in, const float* h0, void* y,
+                              float* hT, void* workspace, void* reserve, void* stream);
+
+/* Gradients.  Needs the reserve written by rnn_scan_forward with the same inputs
+ * and lengths (it holds what is needed of h0).
+ *   dy   gradient of y (dense)            dhT  gradient of hT (may be NULL = zero)
+ *   grad what is wanted; dz, dD and ddt_bias only where the input is there
+ *   workspace (backward_workspace_bytes)
+ * Sums over tokens, sequences and channels run in a fixed order. */
+rnn_status_t rnn_scan_backward(rnn_scan_t handle, const rnn_scan_in_t* in, const void* dy, const float* dhT,
+                               const rnn_scan_grad_t* grad, void* workspace, const void* reserve,
+                               void* stream);
+
+/* The serving form: seq_len new tokens of each sequence against a pool of states
+ * [num_slots, channels, states] fp32, updated in place; slots as rnn_delta_step. */
+rnn_status_t rnn_scan_step(rnn_scan_t handle, const rnn_scan_in_t* in, float* state, int num_slots,
+                           const int* slots, void* y, void* stream);
+
+/* Number of kernels this handle has launched since it was created. */
+uint64_t rnn_scan_launch_count(rnn_scan_t handle);
+
+/* ---------------------------------------------------------------------------
+ * Causal convolution: the short depthwise convolution over time that stands before
+ * the selective scan and the delta rule.  Per sequence and channel, x_t for t < 0
+ * being the state, the last width - 1 inputs before the sequence:
+ *     y_t = act(bias + sum_k w[k] x_{t - (width - 1) + k})
+ * act is silu, or the identity.  Element type of everything is desc.dtype but the
+ * gradients of w and bias, which are fp32, as are all sums.  States (s0, sT, the pool
+ * of rnn_conv_step, ds0, dsT) are [B, width - 1, channels], oldest input first.
+ * Layout, lengths, streams and calls as for the selective scan. */
+typedef struct {
+  int batch;           /* B >= 1                                                       */
+  int seq_len;         /* T >= 1                                                       */
+  int channels;        /* 8..65536, a multiple of 8                                    */
+  int width;           /* 2..4                                                         */
+  int dtype;           /* rnn_dtype_t                                                  */
+  int batch_first;     /* 0 = [T,B,...], 1 = [B,T,...]                                 */
+  int act;             /* RNN_GATE_NONE or RNN_GATE_SILU                               */
+} rnn_conv_desc_t;
+
+typedef struct rnn_conv_s* rnn_conv_t;
+
+/* The inputs of one call; x_row as above, 16-byte alignment as everywhere. */
+typedef struct {
+  const void* x;       /* [.., channels]                        */
+  const void* w;       /* [channels, width]                     */
+  const void* bias;    /* [channels] or NULL                    */
+  int64_t x_row;
+} rnn_conv_in_t;
+
+rnn_status_t rnn_conv_create(const rnn_conv_desc_t* desc, rnn_conv_t* handle);
+rnn_status_t rnn_conv_destroy(rnn_conv_t handle);
+/* Scratch of a backward call that wants dw or dbias (the others need none). */
+rnn_status_t rnn_conv_get_sizes(rnn_conv_t handle, size_t* backward_workspace_bytes);
+rnn_status_t rnn_conv_set_seq_lengths(rnn_conv_t handle, const int* lengths);
+
+/*   s0 (may be NULL = zero)   y (out, dense)   sT (out, may be NULL; may be s0): the
+ * last inputs of each sequence, those of s0 among them where it has fewer tokens. */
+rnn_status_t rnn_conv_forward(rnn_conv_t handle, const rnn_conv_in_t* in, const void* s0, void* y, void* sT,
+                              void* stream);
+
+/* Gradients of a forward call with these inputs.
+ *   dy (dense)   dsT (may be NULL = zero)
+ *   dx (dense), ds0, dw fp32 [channels, width], dbias fp32 [channels]: out, each may
+ *   be NULL; dbias only with a bias
+ *   workspace    required with dw or dbias */
+rnn_status_t rnn_conv_backward(rnn_conv_t handle, const rnn_conv_in_t* in, const void* s0, const void* dy,
+                               const void* dsT, void* dx, float* dw, float* dbias, void* ds0,
+                               void* workspace, void* stream);
+
+/* The serving form: seq_len new tokens of each sequence against a pool of states
+ * [num_slots, width - 1, channels], updated in place; slots as rnn_delta_step. */
+rnn_status_t rnn_conv_step(rnn_conv_t handle, const rnn_conv_in_t* in, void* state, int num_slots,
+                           const int* slots, void* y, void* stream);
+
+uint64_t rnn_conv_launch_count(rnn_conv_t handle);
+
+/* ---------------------------------------------------------------------------
+ * Gradient clipping: the norm of all gradients of a model together, and every one
+ * scaled by the same factor where it is over a limit - what keeps backpropagation
+ * through many steps in bounds.
+ *     norm = sqrt(sum over tensors and elements of g^2)
+ *     out  = g * min(1, max_norm / (norm + eps))
+ * The sum covers the whole range of fp32: squares that leave it are taken in 64 bits.
+ * Where the norm is not finite (a NaN or infinity among the gradients), or the factor
+ * is one, out is g as it is: the caller sees norm and may skip the update. */
+typedef struct rnn_clip_s* rnn_clip_t;
+
+/* A list of ``num`` tensors (1..65536): elements (0..2^40, 2^42 together) and
+ * rnn_dtype_t of each, host arrays.  Made on the current device, as rnn_delta_create. */
+rnn_status_t rnn_clip_create(int num, const int64_t* counts, const int* dtypes, rnn_clip_t* handle);
+rnn_status_t rnn_clip_destroy(rnn_clip_t handle);
+/* Scratch of a call. */
+rnn_status_t rnn_clip_get_sizes(rnn_clip_t handle, size_t* workspace_bytes);
+
+/*   grads    host array of num device pointers, aligned to their element only; those of
+ *            empty tensors are not looked at
+ *   out      the same, or NULL = in place; entry i may be grads[i], no other overlap
+ *   max_norm, eps  finite, >= 0
+ *   norm     device fp32 [1] (out)
+ *   workspace (workspace_bytes); calls of a handle run in the order they are made
+ * With out == NULL and max_norm == 0 the tensors become zero; rnn_clip_norm only
+ * writes the norm. */
+rnn_status_t rnn_clip_scale(rnn_clip_t handle, const void* const* grads, void* const* out, float max_norm,
+                            float eps, float* norm, void* workspace, void* stream);
+rnn_status_t rnn_clip_norm(rnn_clip_t handle, const void* const* grads, float* norm, void* workspace,
+                           void* stream);
+
+uint64_t rnn_clip_launch_count(rnn_clip_t handle);
+
 /* Static text for a status code. */
 const char* rnn_status_string(rnn_status_t status);
 
