@@ -9,6 +9,7 @@
 #include "pair.cuh"
 #include "scan.h"
 #include "vec.cuh"
+#include <cstdlib>
 
 namespace rnn {
 
@@ -17,6 +18,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int TT = kScanTile;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr float kLift = 2e-8f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -25,8 +27,11 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// 2^x.  bf16 storage takes the hardware's approximation (2^-22, 2e-8 low on
-// average).  fp32 storage takes the Taylor series of e^(f ln 2) on |f| <= 1/2, whose
+// 2^x.  bf16 storage takes the hardware's approximation, which is 5e-9 (|x| near
+// 1e-3) to 3e-8 (0.01 to 1) low on average: kLift, added to the exponent by the same
+// instruction that scales it, takes the middle of that out (states of 77 tokens, error
+// against 64 bits: 1.3e-6 without, 5.5e-7 with; training's dA 1.9e-6 and 1.0e-6).  fp32
+// storage takes the Taylor series of e^(f ln 2) on |f| <= 1/2, whose
 // last rounding is of 1 + something small: half a step, and no bias that a memory of
 // a thousand tokens would add up.  The ninth term is below 2^-27.
 template <typename T>
@@ -207,122 +212,250 @@ __device__ __forceinline__ void store_states(const float2 (&h)[C][NS / 2], float
         *reinterpret_cast<float2*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j) = h[c][j];
 }
 
+// The exponent of a token's decay: A log2(e) times its step.
+template <typename T>
+__device__ __forceinline__ float2 step2(float2 A2, float d) {
+  if constexpr (sizeof(T) == 2) return fma2(A2, both(d), both(kLift));
+  else return mul2(A2, both(d));
+}
 template <typename T>
 __device__ __forceinline__ float2 decay2(float2 x) { return make_float2(decay<T>(x.x), decay<T>(x.y)); }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename T, int NS, int C, bool TRAIN>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanFwdArgs f) {
-  using I = Items<C>;
-  constexpr int CT = I::CT, NP = 4 * NS, P = NS / 2;
-  __shared__ __align__(16) float sdt[TT][CT], sdx[TT][CT], sB[TT][NP], sC[TT][NP];
-  const ScanArgs& a = f.a;
-  const Where<C> w(a);
-  const int tid = threadIdx.x, lane = tid & 31, cl = lane & 7, sl = lane >> 3;
-  const int ch = (tid >> 5) * 8 * C + cl * C, n0 = sl * NS;
-  const int row = tid / I::VC, col = tid % I::VC * 8;
-  const bool in = col < w.width;
-  const int len = a.len ? a.len[w.b] : a.T;
-  const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
+// A warp works alone: it reads a tile of 16 tokens of its channels (the next tile's
+// loads in flight meanwhile), leaves the steps in shared memory, runs the recurrence
+// and finishes the outputs, with no barrier but its own.
+template <int C>
+struct Warp {
+  static constexpr int CT = 8 * C, VC = C, ROWS = 32 / VC, IT = TT / ROWS > 0 ? TT / ROWS : 1;
+  int b, g, seg, tile, c0, width;
+  __host__ __device__ static int per_group(const ScanArgs& a) { return (a.D / a.G + CT - 1) / CT; }
+  __device__ __forceinline__ Warp(const ScanArgs& a, int nseg) {
+    const int per = per_group(a), all = per * a.G;
+    tile = blockIdx.x % all;
+    const int r = blockIdx.x / all;
+    seg = r % nseg;
+    b = r / nseg;
+    g = tile / per;
+    const int dg = a.D / a.G, first = (tile - g * per) * CT;
+    c0 = g * dg + first;
+    width = dg - first < CT ? dg - first : CT;
+  }
+};
 
+// A tile's rows of B or C: [TT][4 NS] floats, zeros beyond N.  Vectors where the rows
+// start on 16-byte boundaries, else element by element (no tile ahead then).
+template <typename T, int NS>
+struct Tile {
+  static constexpr int NP = 4 * NS, VECS = TT * NP / 8, PER = VECS / 32 > 0 ? VECS / 32 : 1;
+  Raw<T, 8> v[PER];
+  __device__ __forceinline__ void load(const ScanArgs& a, const void* base, int64_t stride, bool vec, int b, int g, int t0, int n,
+                                       int lane) {
+    if (!vec) return;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 32 * i, t = e / (NP / 8), s = e % (NP / 8) * 8;
+      const bool ok = e < VECS && t < n && s < a.N;
+      load_or<T, 8>(v[i], base, ok ? a.row(b, t0 + t) * stride + g * a.N + s : 0, ok, 0.f);
+    }
+  }
+  __device__ __forceinline__ void store(float* to, const ScanArgs& a, const void* base, int64_t stride, bool vec, int b, int g,
+                                        int t0, int n, int lane) const {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= VECS) break;
+        float2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = v[i].pair(j);
+        store_vec<float, 8>(to + e * 8, f);
+      }
+    } else {
+#pragma unroll 8
+      for (int e = lane; e < TT * NP; e += 32) {
+        const int t = e / NP, s = e % NP;
+        to[e] = t < n && s < a.N ? to_f(static_cast<const T*>(base)[a.row(b, t0 + t) * stride + g * a.N + s]) : 0.f;
+      }
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ bool on_16(const void* base, int64_t stride) {
+  return ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(stride * sizeof(T))) & 15) == 0;
+}
+
+// The states of a thread after segments 0 .. seg - 1, from what each alone leaves.
+template <int C, int NS>
+__device__ __forceinline__ void join(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanFwdArgs& f, int b, int seg,
+                                     int len, int c0, int ch, int n0, int width) {
+  const ScanArgs& a = f.a;
+#pragma unroll 2
+  for (int i = 0; i < seg; ++i) {
+    if (i * f.seg >= len) break;
+    const int64_t at = (static_cast<int64_t>(b) * f.nseg + i) * a.D + c0;
+    float2 e[C][NS / 2];
+    load_states<C, NS>(e, f.ends + at * a.N, a.N, ch, n0, width);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float sum = ch + c < width ? f.sums[at + ch + c] : 0.f;
+#pragma unroll
+      for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<float>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
+    }
+  }
+}
+
+enum { kInfer = 0, kTrain = 1, kAlone = 2 };      // kAlone: only what a segment leaves by itself
+
+template <typename T, int NS, int C, int MODE>
+__global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
+  using W = Warp<C>;
+  constexpr int CT = W::CT, NP = 4 * NS, P = NS / 2;
+  constexpr bool OUT = MODE != kAlone;
+  __shared__ __align__(16) float sdt[TT][CT], sdx[TT][CT], sB[TT][NP], sC[OUT ? TT : 1][NP], sy[OUT ? TT : 1][CT];
+  const ScanArgs& a = f.a;
+  const W w(a, OUT ? f.nseg : f.nseg - 1);
+  const int lane = threadIdx.x, cl = lane & 7, sl = lane >> 3, ch = cl * C, n0 = sl * NS;
+  const int row = lane / W::VC, col = lane % W::VC * 8;
+  const bool in = col < w.width && row < TT;
+  const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * f.seg, end = begin + f.seg < a.T ? begin + f.seg : a.T;
+  const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
+  const bool vB = on_16<T>(a.Bm, a.B_row), vC = on_16<T>(a.Cm, a.C_row);
+
+  Raw<T, 8> x[W::IT], dt[W::IT], z[W::IT];
+  Tile<T, NS> rB, rC;
+  auto items = [&](Raw<T, 8> (&r)[W::IT], const void* base, int64_t stride, int t0) {
+#pragma unroll
+    for (int i = 0; i < W::IT; ++i) {
+      const int t = t0 + row + i * W::ROWS;
+      const bool ok = in && base && t < len && t < end;
+      load_or<T, 8>(r[i], base, ok ? a.row(w.b, t) * stride + w.c0 + col : 0, ok, 0.f);
+    }
+  };
+  auto fetch = [&](int t0) {
+    items(x, a.x, a.x_row, t0);
+    items(dt, a.dt, a.dt_row, t0);
+    if (OUT) items(z, a.z, a.z_row, t0);
+    rB.load(a, a.Bm, a.B_row, vB, w.b, w.g, t0, len - t0, lane);
+    if (OUT) rC.load(a, a.Cm, a.C_row, vC, w.b, w.g, t0, len - t0, lane);
+  };
+  fetch(begin);
   float2 A2[C][P], h[C][P];
   load_states<C, NS>(A2, a.A + static_cast<int64_t>(w.c0) * a.N, a.N, ch, n0, w.width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < P; ++j) A2[c][j] = mul2(A2[c][j], both(kLog2e));
-  load_states<C, NS>(h, f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
-  float bias[8], skip[8];
+  load_states<C, NS>(h, OUT && f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
+  if (!OUT && f.first && w.seg == 0) {
+    float2 h0[C][P];
+    load_states<C, NS>(h0, f.h0 + bD * a.N, a.N, ch, n0, w.width);
+    store_states<C, NS>(h0, f.first + bD * a.N, a.N, ch, n0, w.width);
+  }
+  if (OUT && w.seg) join<C, NS>(h, A2, f, w.b, w.seg, len, w.c0, ch, n0, w.width);
+  float bias[8], skip[8], sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     bias[j] = in && a.bias ? a.bias[w.c0 + col + j] : 0.f;
-    skip[j] = in && a.skip ? a.skip[w.c0 + col + j] : 0.f;
+    if (OUT) skip[j] = in && a.skip ? a.skip[w.c0 + col + j] : 0.f;
+    sum[j] = 0.f;
   }
-
-  Raw<T, 8> x[I::IT], dt[I::IT], z[I::IT], xn[I::IT], dtn[I::IT], zn[I::IT];
-  Rows<T, NS> rB, rC;
-  auto fetch = [&](int t0, Raw<T, 8> (&xx)[I::IT], Raw<T, 8> (&dd)[I::IT], Raw<T, 8> (&zz)[I::IT]) {
-    const int n = len - t0;
-    load_items<T, I::IT, I::ROWS>(xx, a, a.x, a.x_row, w.b, t0, n, row, w.c0 + col, in);
-    load_items<T, I::IT, I::ROWS>(dd, a, a.dt, a.dt_row, w.b, t0, n, row, w.c0 + col, in);
-    load_items<T, I::IT, I::ROWS>(zz, a, a.z, a.z_row, w.b, t0, n, row, w.c0 + col, in);
-    rB.load(a, a.Bm, a.B_row, w.b, w.g, t0, n);
-    rC.load(a, a.Cm, a.C_row, w.b, w.g, t0, n);
-  };
-  fetch(0, x, dt, z);
-  for (int t0 = 0; t0 < a.T; t0 += TT) {
-    if (TRAIN)
+  for (int t0 = begin; t0 < end; t0 += TT) {
+    if (MODE == kTrain)
       store_states<C, NS>(h, f.kept + ((static_cast<int64_t>(w.b) * a.tiles() + t0 / TT) * a.D + w.c0) * a.N, a.N, ch, n0,
                           w.width);
-#pragma unroll
-    for (int i = 0; i < I::IT; ++i) {
-      const int t = row + i * I::ROWS;
-      if (t >= TT) break;
-      float d[8], u[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 dp = dt[i].pair(j / 2), xp = x[i].pair(j / 2);
-        d[j] = (j & 1 ? dp.y : dp.x) + bias[j];
-        if (a.softplus) d[j] = softplus<T>(d[j]);
-        u[j] = d[j] * (j & 1 ? xp.y : xp.x);
-      }
-      *reinterpret_cast<float4*>(&sdt[t][col]) = make_float4(d[0], d[1], d[2], d[3]);
-      *reinterpret_cast<float4*>(&sdt[t][col + 4]) = make_float4(d[4], d[5], d[6], d[7]);
-      *reinterpret_cast<float4*>(&sdx[t][col]) = make_float4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<float4*>(&sdx[t][col + 4]) = make_float4(u[4], u[5], u[6], u[7]);
-    }
-    rB.store(&sB[0][0]);
-    rC.store(&sC[0][0]);
-    __syncthreads();
-    if (t0 + TT < a.T) fetch(t0 + TT, xn, dtn, zn);
     const int n = len - t0 < TT ? len - t0 : TT;
-#pragma unroll 4
-    for (int t = 0; t < n; ++t) {
+#pragma unroll
+    for (int i = 0; i < W::IT; ++i) {
+      const int t = row + i * W::ROWS;
+      if (t >= TT) break;
+      float2 d[4], u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = add2(dt[i].pair(j), make_float2(bias[2 * j], bias[2 * j + 1]));
+        if (a.softplus) d[j] = make_float2(softplus<T>(d[j].x), softplus<T>(d[j].y));
+        u[j] = mul2(d[j], x[i].pair(j));
+        if (!OUT && t < n) {
+          sum[2 * j] += d[j].x;
+          sum[2 * j + 1] += d[j].y;
+        }
+      }
+      store_vec<float, 8>(&sdt[t][col], d);
+      store_vec<float, 8>(&sdx[t][col], u);
+    }
+    rB.store(&sB[0][0], a, a.Bm, a.B_row, vB, w.b, w.g, t0, n, lane);
+    if (OUT) rC.store(&sC[0][0], a, a.Cm, a.C_row, vC, w.b, w.g, t0, n, lane);
+    Raw<T, 8> xo[W::IT], zo[W::IT];
+#pragma unroll
+    for (int i = 0; i < W::IT; ++i) {
+      xo[i] = x[i];
+      zo[i] = z[i];
+    }
+    __syncwarp();
+    if (t0 + TT < end) fetch(t0 + TT);
+    auto token = [&](int t) {
       float d[C], u[C], y[C];
       float2 Bv[P], Cv[P];
       lds<C>(d, &sdt[t][ch]);
       lds<C>(u, &sdx[t][ch]);
       lds2<P>(Bv, &sB[t][n0]);
-      lds2<P>(Cv, &sC[t][n0]);
+      if (OUT) lds2<P>(Cv, &sC[t][n0]);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float2 s = both(0.f);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const float2 e = decay2<T>(mul2(A2[c][j], both(d[c])));
+          const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
           h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
-          s = fma2(Cv[j], h[c][j], s);
+          if (OUT) s = j ? fma2(Cv[j], h[c][j], s) : mul2(Cv[j], h[c][j]);
         }
         y[c] = s.x + s.y;
       }
-      const float r = over_states<C>(y, sl);
-      // every lane has read this token's steps: their place takes its result
-      if (C == 4 || sl % (4 / C) == 0) sdt[t][ch + sl * C / 4] = r;
+      if (OUT) {
+        const float r = over_states<C>(y, sl);
+        if (C == 4 || sl % (4 / C) == 0) sy[t][ch + sl * C / 4] = r;
+      }
+    };
+    if (n == TT) {
+#pragma unroll 4
+      for (int t = 0; t < TT; ++t) token(t);
+    } else {
+      for (int t = 0; t < n; ++t) token(t);
     }
-    __syncthreads();
+    __syncwarp();
+    if (OUT) {
 #pragma unroll
-    for (int i = 0; i < I::IT; ++i) {
-      const int t = row + i * I::ROWS;
-      if (t >= TT) break;
-      if (in && t0 + t < a.T) {
+      for (int i = 0; i < W::IT; ++i) {
+        const int t = row + i * W::ROWS;
+        if (!in || t >= TT || t0 + t >= end) break;
         float2 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 s = *reinterpret_cast<const float2*>(&sdt[t][col + 2 * j]), xp = x[i].pair(j), zp = z[i].pair(j);
+          const float2 s = *reinterpret_cast<const float2*>(&sy[t][col + 2 * j]), xp = xo[i].pair(j), zp = zo[i].pair(j);
           v[j] = fma2(make_float2(skip[2 * j], skip[2 * j + 1]), xp, s);
           if (a.z) v[j] = mul2(v[j], make_float2(zp.x * sigmoid<T>(zp.x), zp.y * sigmoid<T>(zp.y)));
           if (t >= n) v[j] = both(0.f);
         }
         store_vec<T, 8>(static_cast<T*>(f.y) + a.row(w.b, t0 + t) * a.D + w.c0 + col, v);
       }
-      x[i] = xn[i];
-      dt[i] = dtn[i];
-      z[i] = zn[i];
     }
   }
-  if (f.hT) store_states<C, NS>(h, f.hT + bD * a.N, a.N, ch, n0, w.width);
+  if (OUT) {
+    if (f.hT && end == a.T) store_states<C, NS>(h, f.hT + bD * a.N, a.N, ch, n0, w.width);
+    return;
+  }
+  const int64_t at = (static_cast<int64_t>(w.b) * f.nseg + w.seg) * a.D + w.c0;
+  store_states<C, NS>(h, f.ends + at * a.N, a.N, ch, n0, w.width);
+  // the rows' sums of steps, in a fixed order
+#pragma unroll
+  for (int m = W::VC; m < 32; m <<= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += __shfl_xor_sync(kFull, sum[j], m);
+  if (row == 0 && in)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.sums[at + col + j] = sum[j];
 }
 
 // ---------------------------------------------------------------------------
@@ -445,7 +578,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanBwdArgs g_
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int j = 0; j < P; ++j)
-            h[t + 1][c][j] = fma2(decay2<T>(mul2(A2[c][j], both(d[c]))), h[t][c][j], mul2(Bv[j], both(u[c])));
+            h[t + 1][c][j] = fma2(decay2<T>(step2<T>(A2[c][j], d[c])), h[t][c][j], mul2(Bv[j], both(u[c])));
       }
     }
 #pragma unroll
@@ -465,7 +598,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanBwdArgs g_
           float2 q1 = both(0.f), q2 = both(0.f), q3 = both(0.f);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            const float2 e = decay2<T>(mul2(A2[c][j], both(d[c])));
+            const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
             g[c][j] = fma2(Cv[j], both(o[c]), g[c][j]);
             dC[j] = fma2(h[t + 1][c][j], both(o[c]), dC[j]);
             q3 = fma2(h[t + 1][c][j], Cv[j], q3);
@@ -641,10 +774,11 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs p) {
         const T* Bp = static_cast<const T*>(a.Bm) + r * a.B_row + g * a.N + n0;
         const T* Cp = static_cast<const T*>(a.Cm) + r * a.C_row + g * a.N + n0;
         const float e = dv * kLog2e, u = dv * xv;
-        h.x = fmaf(decay<T>(A.x * e), h.x, u * to_f(Bp[0]));
-        h.y = fmaf(decay<T>(A.y * e), h.y, u * to_f(Bp[1]));
-        h.z = fmaf(decay<T>(A.z * e), h.z, u * to_f(Bp[2]));
-        h.w = fmaf(decay<T>(A.w * e), h.w, u * to_f(Bp[3]));
+        const float lift = sizeof(T) == 2 ? kLift : 0.f;
+        h.x = fmaf(decay<T>(fmaf(A.x, e, lift)), h.x, u * to_f(Bp[0]));
+        h.y = fmaf(decay<T>(fmaf(A.y, e, lift)), h.y, u * to_f(Bp[1]));
+        h.z = fmaf(decay<T>(fmaf(A.z, e, lift)), h.z, u * to_f(Bp[2]));
+        h.w = fmaf(decay<T>(fmaf(A.w, e, lift)), h.w, u * to_f(Bp[3]));
         y = fmaf(to_f(Cp[3]), h.w, fmaf(to_f(Cp[2]), h.z, fmaf(to_f(Cp[1]), h.y, to_f(Cp[0]) * h.x)));
       }
     }
@@ -671,21 +805,29 @@ int lane_states(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 constexpr int fwd_channels(int NS) { return NS <= 4 ? 4 : NS == 8 ? 2 : 1; }
 constexpr int bwd_channels(int NS) { return NS <= 4 ? 2 : 1; }
 
-template <typename T, int NS>
-int fwd(const ScanFwdArgs& f, cudaStream_t s) {
-  constexpr int C = fwd_channels(NS);
-  const unsigned grid = static_cast<unsigned>(f.a.B) * f.a.G * Where<C>::per_group(f.a);
-  if (f.kept) scan_fwd_kernel<T, NS, C, true><<<grid, kThreads, 0, s>>>(f);
-  else scan_fwd_kernel<T, NS, C, false><<<grid, kThreads, 0, s>>>(f);
-  return check_launch();
+
+template <typename T, int NS, int C>
+int fwd(ScanFwdArgs f, cudaStream_t s, int* launches) {
+  const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Warp<C>::per_group(f.a);
+  int rc;
+  if (f.nseg > 1) {
+    scan_fwd_kernel<T, NS, C, kAlone><<<warps * (f.nseg - 1), 32, 0, s>>>(f);
+    if ((rc = check_launch())) return rc;
+    ++*launches;
+    if (f.first) f.h0 = f.first;
+  }
+  if (f.kept) scan_fwd_kernel<T, NS, C, kTrain><<<warps * f.nseg, 32, 0, s>>>(f);
+  else scan_fwd_kernel<T, NS, C, kInfer><<<warps * f.nseg, 32, 0, s>>>(f);
+  if (!(rc = check_launch())) ++*launches;
+  return rc;
 }
 template <typename T>
-int fwd_t(const ScanFwdArgs& f, cudaStream_t s) {
+int fwd_t(const ScanFwdArgs& f, cudaStream_t s, int* launches) {
   switch (lane_states(f.a.N)) {
-    case 2: return fwd<T, 2>(f, s);
-    case 4: return fwd<T, 4>(f, s);
-    case 8: return fwd<T, 8>(f, s);
-    default: return fwd<T, 16>(f, s);
+    case 2: return fwd<T, 2, 4>(f, s, launches);
+    case 4: return fwd<T, 4, 4>(f, s, launches);
+    case 8: return fwd<T, 8, 2>(f, s, launches);
+    default: return fwd<T, 16, 1>(f, s, launches);
   }
 }
 
@@ -755,10 +897,37 @@ int step_t(const ScanStepArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-int launch_scan_forward(const ScanFwdArgs& f, int is_bf16, cudaStream_t s, int* launches) {
-  const int rc = is_bf16 ? fwd_t<__nv_bfloat16>(f, s) : fwd_t<float>(f, s);
-  *launches = rc ? 0 : 1;
-  return rc;
+ScanSplit scan_split(const ScanArgs& a, int is_bf16) {
+  const int C = fwd_channels(lane_states(a.N)), per = (a.D / a.G + 8 * C - 1) / (8 * C);
+  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per, want = static_cast<int64_t>(a.num_sms) * 16;
+  const int tiles = a.tiles();
+  int64_t n = warps * 2 > want ? 1 : want / warps;
+  const char* env = getenv("V_NSEG");
+  if (env) n = atoi(env);
+  if (n > tiles / 4) n = tiles / 4;
+  if (n < 1) n = 1;
+  ScanSplit p{};
+  p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * kScanTile;
+  p.nseg = (a.T + p.len - 1) / p.len;
+  if (p.nseg == 1) return p;
+  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  const size_t rows = static_cast<size_t>(a.B) * p.nseg * a.D;
+  p.sums = up(rows * a.N * 4);
+  p.first = p.sums + up(rows * 4);
+  p.bytes = p.first + up(static_cast<size_t>(a.B) * a.D * a.N * 4);
+  return p;
+}
+
+int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStream_t s, int* launches) {
+  ScanFwdArgs f = f_;
+  const ScanSplit p = scan_split(f.a, is_bf16);
+  f.nseg = p.nseg;
+  f.seg = p.len;
+  f.ends = reinterpret_cast<float*>(static_cast<char*>(work) + p.ends);
+  f.sums = reinterpret_cast<float*>(static_cast<char*>(work) + p.sums);
+  f.first = p.nseg > 1 && f.h0 && f.h0 == f.hT ? reinterpret_cast<float*>(static_cast<char*>(work) + p.first) : nullptr;
+  *launches = 0;
+  return is_bf16 ? fwd_t<__nv_bfloat16>(f, s, launches) : fwd_t<float>(f, s, launches);
 }
 
 ScanBwdLayout scan_bwd_layout(const ScanArgs& a) {

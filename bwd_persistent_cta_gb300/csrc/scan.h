@@ -28,14 +28,26 @@ struct ScanArgs {
   __host__ __device__ int tiles() const { return (T + kScanTile - 1) / kScanTile; }
 };
 
+// A long sequence runs as several segments side by side.  ends: byte offset of [B][nseg]
+// [D][N], the state that each segment alone leaves; sums: of [B][nseg][D], the sum of its
+// steps; first: of [B][D][N], the initial state where the final one overwrites it.
+struct ScanSplit {
+  int nseg, len;               // segments, tokens of each (a multiple of the tile)
+  size_t ends, sums, first, bytes;
+};
+ScanSplit scan_split(const ScanArgs& a, int is_bf16);
+
 struct ScanFwdArgs {
   ScanArgs a;
   const float* h0;             // or null
   float* hT;                   // or null
   void* y;
   float* kept;                 // [B][tile][D][N] the state before each tile, or null
+  int nseg, seg;               // segments, tokens of each
+  float *ends, *sums;
+  float* first;                // where the first segment copies h0 to, or null
 };
-int launch_scan_forward(const ScanFwdArgs& f, int is_bf16, cudaStream_t s, int* launches);
+int launch_scan_forward(const ScanFwdArgs& f, void* work, int is_bf16, cudaStream_t s, int* launches);
 
 // Byte offsets of the backward's scratch: partial sums over channels (of dB and dC),
 // over tokens and sequences (of dA, dD and the bias).

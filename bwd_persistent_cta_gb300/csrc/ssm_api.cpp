@@ -190,7 +190,7 @@ rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* out) {
   h->bf16 = desc->dtype == RNN_BF16;
   h->es = h->bf16 ? 2 : 4;
   const ScanArgs a = scan_shape(h);
-  h->workspace_bytes = 0;
+  h->workspace_bytes = scan_split(a, h->bf16).bytes;
   h->bwd_workspace_bytes = scan_bwd_layout(a).bytes;
   h->reserve_bytes = al(static_cast<size_t>(a.B) * a.tiles() * a.D * a.N * 4);
   *out = h;
@@ -238,7 +238,7 @@ rnn_status_t rnn_scan_forward(rnn_scan_t h, const rnn_scan_in_t* in, const float
   f.y = y;
   f.kept = static_cast<float*>(reserve);
   int n = 0;
-  const int e = launch_scan_forward(f, h->bf16, s, &n);
+  const int e = launch_scan_forward(f, workspace, h->bf16, s, &n);
   h->launches += n;
   return call.done(e);
 }
