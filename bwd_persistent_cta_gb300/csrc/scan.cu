@@ -1,14 +1,18 @@
 // scan.cu - the selective scan: whole sequences forward and backward, and the
 // serving step.
 //
-// A warp holds 8 * C channels: lane = cl + 8 sl has the channels C cl .. and, of each,
-// the states NS sl .. of 4 NS (states beyond N are held as zeros).  So the sum over a
-// channel's states is two shuffles wide, the sum over a warp's channels three, and
-// B, C and the steps come from shared memory as broadcasts of 16 bytes.
+// What bounds it: for each token, channel and state one exponential (4 cycles of a
+// scheduler's special function unit for a warp) and four multiply-adds forward, two and
+// thirteen backward; memory is a third of that at 16 states.  So the recurrence is kept
+// at two values an instruction and everything around it small: a warp holds 8 * CL
+// channels' worth of states in registers, lane = cl + CL sl with C channels and NS states
+// of each, sums over a channel's states and over the warp's channels are a few shuffles,
+// and steps, B and C come from shared memory as broadcasts of 16 bytes.
 #include "common.cuh"
 #include "pair.cuh"
 #include "scan.h"
 #include "vec.cuh"
+
 #include <cstdlib>
 
 namespace rnn {
@@ -16,14 +20,17 @@ namespace rnn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int TT = kScanTile;
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLift = 2e-8f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -57,115 +64,49 @@ __device__ __forceinline__ float decay(float x) {
   }
 }
 
-// log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v|.  bf16 storage: log(1 + q) as
-// 2 artanh(q / (2 + q)), whose series in (q / (2 + q))^2 <= 1/9 ends after eight
-// terms (1e-8): relative accuracy at small steps, at a third of log1pf's instructions.
+// The exponent of a token's decay: A log2(e) times its step.
 template <typename T>
-__device__ __forceinline__ float softplus(float v) {
+__device__ __forceinline__ float2 step2(float2 A2, float d) {
+  if constexpr (sizeof(T) == 2) return fma2(A2, both(d), both(kLift));
+  else return mul2(A2, both(d));
+}
+template <typename T>
+__device__ __forceinline__ float2 decay2(float2 x) { return make_float2(decay<T>(x.x), decay<T>(x.y)); }
+
+// log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v|, two at a time.  bf16 storage: log(1 + q)
+// is 2 artanh(s), s = q / (2 + q) <= 1/3, as s times a polynomial in s^2 (interpolated at
+// the Chebyshev nodes of [0, 1/9], off by 4e-9): relative accuracy at small steps, in a
+// third of log1pf's instructions.
+template <typename T>
+__device__ __forceinline__ float2 softplus2(float2 v) {
   if constexpr (sizeof(T) == 2) {
-    const float q = ex2(-fabsf(v) * kLog2e), s = __fdividef(q, 2.f + q), w = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, w, 1.f / 13.f);
-    p = fmaf(p, w, 1.f / 11.f);
-    p = fmaf(p, w, 1.f / 9.f);
-    p = fmaf(p, w, 1.f / 7.f);
-    p = fmaf(p, w, 1.f / 5.f);
-    p = fmaf(p, w, 1.f / 3.f);
-    p = fmaf(p, w, 1.f);
-    return (v > 0.f ? v : v != v ? v : 0.f) + 2.f * s * p;
+    const float2 q = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+    const float2 d = add2(q, both(2.f)), s = mul2(q, make_float2(rcp(d.x), rcp(d.y))), w = mul2(s, s);
+    float2 p = fma2(both(0.28157778f), w, both(0.27965158f));
+    p = fma2(p, w, both(0.40024596f));
+    p = fma2(p, w, both(0.66666322f));
+    p = fma2(p, w, both(2.f));
+    return fma2(p, s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));       // a NaN comes in through s
   } else {
-    return (v > 0.f ? v : v != v ? v : 0.f) + log1pf(expf(-fabsf(v)));
+    return make_float2(fmaxf(v.x, 0.f) + log1pf(expf(-fabsf(v.x))), fmaxf(v.y, 0.f) + log1pf(expf(-fabsf(v.y))));
   }
 }
+// 1 / (1 + e^-v): with bf16 storage from the approximations, a few 2^-23 off.
 template <typename T>
-__device__ __forceinline__ float sigmoid(float v) {
-  if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-v));
-  else return sigm(v);
-}
-
-// Sums M values (a power of two, 2 or 4) over the four state lanes: lane sl ends up
-// with value (sl * M / 4), summed.
-template <int M>
-__device__ __forceinline__ float over_states(const float (&v)[M], int sl) {
-  if constexpr (M == 1) {
-    float r = v[0];
-    r += __shfl_xor_sync(kFull, r, 8);
-    return r + __shfl_xor_sync(kFull, r, 16);
-  } else if constexpr (M == 2) {
-    const bool up = sl & 2;
-    float r = (up ? v[1] : v[0]) + __shfl_xor_sync(kFull, up ? v[0] : v[1], 16);
-    return r + __shfl_xor_sync(kFull, r, 8);
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  if constexpr (sizeof(T) == 2) {
+    const float2 q = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(q.x), ex2(q.y)), both(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
   } else {
-    const bool up = sl & 2, odd = sl & 1;
-    const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(kFull, up ? v[0] : v[2], 16);
-    const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(kFull, up ? v[1] : v[3], 16);
-    return (odd ? b : a) + __shfl_xor_sync(kFull, odd ? a : b, 8);
+    return make_float2(sigm(v.x), sigm(v.y));
   }
 }
-
-// Which tile of channels a CTA has: of a group, so that its B and C are one row.
-template <int C>
-struct Where {
-  static constexpr int CT = kWarps * 8 * C;      // channels a CTA
-  int b, g, tile, c0, width;                     // channels c0 .. c0 + width - 1 of the group's
-  __host__ __device__ static int per_group(const ScanArgs& a) { return (a.D / a.G + CT - 1) / CT; }
-  __device__ __forceinline__ Where(const ScanArgs& a) {
-    const int per = per_group(a), all = per * a.G;
-    b = blockIdx.x / all;
-    tile = blockIdx.x - b * all;
-    g = tile / per;
-    const int dg = a.D / a.G, first = (tile - g * per) * CT;
-    c0 = g * dg + first;
-    width = dg - first < CT ? dg - first : CT;
-  }
-};
-
-// A thread's share of a [TT][CT] tile: vectors of 8 channels of tokens tid / VC,
-// tid / VC + step, ...; always the same channels.
-template <int C>
-struct Items {
-  static constexpr int CT = Where<C>::CT, VC = CT / 8, ROWS = kThreads / VC;
-  static constexpr int IT = (TT + ROWS - 1) / ROWS;
-};
-
-template <typename T, int IT, int ROWS>
-__device__ __forceinline__ void load_items(Raw<T, 8> (&r)[IT], const ScanArgs& a, const void* base, int64_t stride, int b,
-                                           int t0, int n, int row, int col, bool in) {
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int t = row + i * ROWS;
-    const bool ok = in && base && t < n;
-    load_or<T, 8>(r[i], base, ok ? a.row(b, t0 + t) * stride + col : 0, ok, 0.f);
-  }
-}
-
-// The tile's rows of B and C, element by element (their rows need no alignment).
-template <typename T, int NS>
-struct Rows {
-  static constexpr int NP = 4 * NS, PER = TT * NP / kThreads > 0 ? TT * NP / kThreads : 1;
-  T v[PER];
-  __device__ __forceinline__ void load(const ScanArgs& a, const void* base, int64_t stride, int b, int g, int t0, int n) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = threadIdx.x + i * kThreads, t = e / NP, s = e - t * NP;
-      v[i] = from_f<T>(0.f);
-      if (t < n && s < a.N)
-        v[i] = static_cast<const T*>(base)[a.row(b, t0 + t) * stride + g * a.N + s];
-    }
-  }
-  __device__ __forceinline__ void store(float* to) const {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = threadIdx.x + i * kThreads;
-      if (e < TT * NP) to[e] = to_f(v[i]);
-    }
-  }
-};
 
 template <int V>
 __device__ __forceinline__ void lds(float (&v)[V], const float* p) {
-  if constexpr (V == 1) v[0] = *p;
-  else if constexpr (V == 2) {
+  if constexpr (V == 1) {
+    v[0] = *p;
+  } else if constexpr (V == 2) {
     const float2 q = *reinterpret_cast<const float2*>(p);
     v[0] = q.x; v[1] = q.y;
   } else {
@@ -180,76 +121,81 @@ template <int P>
 __device__ __forceinline__ void lds2(float2 (&v)[P], const float* p) {
 #pragma unroll
   for (int i = 0; i < P; i += 2) {
-    if (P == 1) {
-      v[0] = *reinterpret_cast<const float2*>(p);
-    } else {
-      const float4 q = *reinterpret_cast<const float4*>(p + 2 * i);
-      v[i] = make_float2(q.x, q.y);
-      if (i + 1 < P) v[i + 1] = make_float2(q.z, q.w);
-    }
+    const float4 q = *reinterpret_cast<const float4*>(p + 2 * i);
+    v[i] = make_float2(q.x, q.y);
+    v[i + 1] = make_float2(q.z, q.w);
   }
 }
 
-// A thread's C x NS states (or rates) of [.., D, N] memory.
+// A thread's C x NS states (or rates) of [.., D, N] memory, zeros beyond D and N (NS
+// divides 8, and N is a multiple of 8).
 template <int C, int NS>
 __device__ __forceinline__ void load_states(float2 (&h)[C][NS / 2], const float* base, int N, int ch, int n0, int width) {
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    const bool ok = base && ch + c < width && n0 < N;
 #pragma unroll
-    for (int j = 0; j < NS / 2; ++j) {
-      h[c][j] = both(0.f);
-      if (base && ch + c < width && n0 + 2 * j < N)
-        h[c][j] = *reinterpret_cast<const float2*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j);
+    for (int j = 0; j < NS / 2; j += 2) {
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ok) q = *reinterpret_cast<const float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j);
+      h[c][j] = make_float2(q.x, q.y);
+      h[c][j + 1] = make_float2(q.z, q.w);
     }
+  }
 }
 template <int C, int NS>
 __device__ __forceinline__ void store_states(const float2 (&h)[C][NS / 2], float* base, int N, int ch, int n0, int width) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < NS / 2; ++j)
-      if (ch + c < width && n0 + 2 * j < N)
-        *reinterpret_cast<float2*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j) = h[c][j];
+    for (int j = 0; j < NS / 2; j += 2)
+      if (ch + c < width && n0 < N)
+        *reinterpret_cast<float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j) =
+            make_float4(h[c][j].x, h[c][j].y, h[c][j + 1].x, h[c][j + 1].y);
+}
+// The rates in units of log2(e).  A token behind the last one has a step of zero and must
+// leave the state as it is, so a rate of minus infinity is held as a large number.
+template <int C, int NS>
+__device__ __forceinline__ void load_rates(float2 (&A2)[C][NS / 2], const ScanArgs& a, int c0, int ch, int n0, int width) {
+  load_states<C, NS>(A2, a.A + static_cast<int64_t>(c0) * a.N, a.N, ch, n0, width);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < NS / 2; ++j) {
+      A2[c][j] = mul2(A2[c][j], both(kLog2e));
+      if (isinf(A2[c][j].x)) A2[c][j].x = copysignf(1e30f, A2[c][j].x);
+      if (isinf(A2[c][j].y)) A2[c][j].y = copysignf(1e30f, A2[c][j].y);
+    }
 }
 
-// The exponent of a token's decay: A log2(e) times its step.
-template <typename T>
-__device__ __forceinline__ float2 step2(float2 A2, float d) {
-  if constexpr (sizeof(T) == 2) return fma2(A2, both(d), both(kLift));
-  else return mul2(A2, both(d));
-}
-template <typename T>
-__device__ __forceinline__ float2 decay2(float2 x) { return make_float2(decay<T>(x.x), decay<T>(x.y)); }
-
-// ---------------------------------------------------------------------------
-// forward
-// ---------------------------------------------------------------------------
-// A warp works alone: it reads a tile of 16 tokens of its channels (the next tile's
-// loads in flight meanwhile), leaves the steps in shared memory, runs the recurrence
-// and finishes the outputs, with no barrier but its own.
-template <int C>
-struct Warp {
-  static constexpr int CT = 8 * C, VC = C, ROWS = 32 / VC, IT = TT / ROWS > 0 ? TT / ROWS : 1;
-  int b, g, seg, tile, c0, width;
+// Which channels of which segment a warp has: of one group, so that its B and C are one row.
+template <int CT>
+struct Where {
+  int b, g, seg, tile, c0, width;                // channels c0 .. c0 + width - 1; tile: of the group
   __host__ __device__ static int per_group(const ScanArgs& a) { return (a.D / a.G + CT - 1) / CT; }
-  __device__ __forceinline__ Warp(const ScanArgs& a, int nseg) {
+  __device__ __forceinline__ Where(const ScanArgs& a, int nseg, int at) {
     const int per = per_group(a), all = per * a.G;
-    tile = blockIdx.x % all;
-    const int r = blockIdx.x / all;
+    const int i = at % all, r = at / all;
     seg = r % nseg;
     b = r / nseg;
-    g = tile / per;
-    const int dg = a.D / a.G, first = (tile - g * per) * CT;
+    g = i / per;
+    tile = i - g * per;
+    const int dg = a.D / a.G, first = tile * CT;
     c0 = g * dg + first;
     width = dg - first < CT ? dg - first : CT;
   }
 };
 
-// A tile's rows of B or C: [TT][4 NS] floats, zeros beyond N.  Vectors where the rows
-// start on 16-byte boundaries, else element by element (no tile ahead then).
-template <typename T, int NS>
-struct Tile {
-  static constexpr int NP = 4 * NS, VECS = TT * NP / 8, PER = VECS / 32 > 0 ? VECS / 32 : 1;
+// A tile of TT rows of B or C as [TT][NP] floats, zeros beyond N and behind the last token.
+// Rows that start on 16-byte boundaries come as vectors, a tile ahead, others element by
+// element when they are needed.
+template <typename T>
+__device__ __forceinline__ bool on_16(const void* base, int64_t stride) {
+  return ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(stride * sizeof(T))) & 15) == 0;
+}
+template <typename T, int TT, int NP>
+struct Rows {
+  static constexpr int VECS = TT * NP / 8, PER = VECS / 32 > 0 ? VECS / 32 : 1;
   Raw<T, 8> v[PER];
   __device__ __forceinline__ void load(const ScanArgs& a, const void* base, int64_t stride, bool vec, int b, int g, int t0, int n,
                                        int lane) {
@@ -267,14 +213,14 @@ struct Tile {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
-        if (e >= VECS) break;
+        if (VECS < 32 && e >= VECS) break;
         float2 f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = v[i].pair(j);
         store_vec<float, 8>(to + e * 8, f);
       }
     } else {
-#pragma unroll 8
+#pragma unroll 4
       for (int e = lane; e < TT * NP; e += 32) {
         const int t = e / NP, s = e % NP;
         to[e] = t < n && s < a.N ? to_f(static_cast<const T*>(base)[a.row(b, t0 + t) * stride + g * a.N + s]) : 0.f;
@@ -282,50 +228,77 @@ struct Tile {
     }
   }
 };
-template <typename T>
-__device__ __forceinline__ bool on_16(const void* base, int64_t stride) {
-  return ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(stride * sizeof(T))) & 15) == 0;
-}
 
-// The states of a thread after segments 0 .. seg - 1, from what each alone leaves.
+// Adds one segment's own end to what went through it: h = exp(A sum) h + end.
 template <int C, int NS>
-__device__ __forceinline__ void join(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanFwdArgs& f, int b, int seg,
-                                     int len, int c0, int ch, int n0, int width) {
-  const ScanArgs& a = f.a;
-#pragma unroll 2
-  for (int i = 0; i < seg; ++i) {
-    if (i * f.seg >= len) break;
-    const int64_t at = (static_cast<int64_t>(b) * f.nseg + i) * a.D + c0;
-    float2 e[C][NS / 2];
-    load_states<C, NS>(e, f.ends + at * a.N, a.N, ch, n0, width);
+__device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanArgs& a, const ScanSegs& g,
+                                        int b, int i, int c0, int ch, int n0, int width) {
+  const int64_t at = (static_cast<int64_t>(b) * g.nseg + i) * a.D + c0;
+  float2 e[C][NS / 2];
+  load_states<C, NS>(e, g.ends + at * a.N, a.N, ch, n0, width);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float sum = ch + c < width ? f.sums[at + ch + c] : 0.f;
+  for (int c = 0; c < C; ++c) {
+    const float sum = ch + c < width ? g.sums[at + ch + c] : 0.f;
 #pragma unroll
-      for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<float>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
-    }
+    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<float>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
   }
 }
 
-enum { kInfer = 0, kTrain = 1, kAlone = 2 };      // kAlone: only what a segment leaves by itself
+// ---------------------------------------------------------------------------
+// forward, and what a segment leaves by itself in either direction
+// ---------------------------------------------------------------------------
+// A warp works alone: it reads a tile of 16 tokens of its channels (the next tile's
+// loads in flight meanwhile), leaves the steps in shared memory, runs the recurrence
+// and finishes the outputs, with no barrier but its own.  Eight states a lane: at 16
+// states two lanes share a channel, so a sum over the states is one exchange.
+constexpr int kTile = 16, kFwdNS = 8;
+enum { kInfer, kTrain, kAlone, kAloneBack };
 
-template <typename T, int NS, int C, int MODE>
+template <int SL, int C>
+struct Fwd {
+  static constexpr int CL = 32 / SL, CT = CL * C, NP = SL * kFwdNS, P = kFwdNS / 2;
+  static constexpr int VC = CT / 8, ROWS = 32 / VC, IT = kTile / ROWS > 0 ? kTile / ROWS : 1;
+  static constexpr int LD = CT + 4;      // a row in shared memory: rows of a store on banks of their own
+};
+
+// Sums C values over the SL state lanes; lane sl < C ends up with value sl (all of them
+// where SL is one).
+template <int SL, int C>
+__device__ __forceinline__ void over_states(float (&v)[C], int sl) {
+  constexpr int CL = 32 / SL;
+  if constexpr (SL > 1) {
+    int m = CL;
+    if constexpr (C == 2) {
+      const bool up = sl & 1;
+      v[0] = (up ? v[1] : v[0]) + __shfl_xor_sync(kFull, up ? v[0] : v[1], m);
+      m *= 2;
+    }
+#pragma unroll
+    for (; m < 32; m *= 2) v[0] += __shfl_xor_sync(kFull, v[0], m);
+  }
+}
+
+template <typename T, int SL, int C, int MODE>
 __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
-  using W = Warp<C>;
-  constexpr int CT = W::CT, NP = 4 * NS, P = NS / 2;
-  constexpr bool OUT = MODE != kAlone;
-  __shared__ __align__(16) float sdt[TT][CT], sdx[TT][CT], sB[TT][NP], sC[OUT ? TT : 1][NP], sy[OUT ? TT : 1][CT];
+  using W = Fwd<SL, C>;
+  constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, TT = kTile, LD = W::LD;
+  constexpr bool OUT = MODE == kInfer || MODE == kTrain, BACK = MODE == kAloneBack;
+  // backward, B is C and x is the gradient of the gated output
+  __shared__ __align__(16) float sdt[TT][LD], sdx[TT][LD], sB[TT][NP], sC[OUT ? TT : 1][NP], sy[OUT ? TT : 1][LD];
   const ScanArgs& a = f.a;
-  const W w(a, OUT ? f.nseg : f.nseg - 1);
-  const int lane = threadIdx.x, cl = lane & 7, sl = lane >> 3, ch = cl * C, n0 = sl * NS;
+  // forward the last segment, backward the first has no other that wants its end
+  Where<CT> w(a, OUT ? f.g.nseg : f.g.nseg - 1, blockIdx.x);
+  if (BACK) ++w.seg;
+  const int lane = threadIdx.x, cl = lane % W::CL, sl = lane / W::CL, ch = cl * C, n0 = sl * NS;
   const int row = lane / W::VC, col = lane % W::VC * 8;
   const bool in = col < w.width && row < TT;
-  const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * f.seg, end = begin + f.seg < a.T ? begin + f.seg : a.T;
+  const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * f.g.len, end = begin + f.g.len < a.T ? begin + f.g.len : a.T;
   const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
   const bool vB = on_16<T>(a.Bm, a.B_row), vC = on_16<T>(a.Cm, a.C_row);
+  const int tiles = (end - begin + TT - 1) / TT;
 
   Raw<T, 8> x[W::IT], dt[W::IT], z[W::IT];
-  Tile<T, NS> rB, rC;
+  Rows<T, TT, NP> rB, rC;
   auto items = [&](Raw<T, 8> (&r)[W::IT], const void* base, int64_t stride, int t0) {
 #pragma unroll
     for (int i = 0; i < W::IT; ++i) {
@@ -337,50 +310,50 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
   auto fetch = [&](int t0) {
     items(x, a.x, a.x_row, t0);
     items(dt, a.dt, a.dt_row, t0);
-    if (OUT) items(z, a.z, a.z_row, t0);
-    rB.load(a, a.Bm, a.B_row, vB, w.b, w.g, t0, len - t0, lane);
-    if (OUT) rC.load(a, a.Cm, a.C_row, vC, w.b, w.g, t0, len - t0, lane);
+    if (OUT || BACK) items(z, a.z, a.z_row, t0);
+    const int n = (len < end ? len : end) - t0;
+    rB.load(a, a.Bm, a.B_row, vB, w.b, w.g, t0, n, lane);
+    if (OUT) rC.load(a, a.Cm, a.C_row, vC, w.b, w.g, t0, n, lane);
   };
-  fetch(begin);
+  fetch(BACK ? begin + (tiles - 1) * TT : begin);
   float2 A2[C][P], h[C][P];
-  load_states<C, NS>(A2, a.A + static_cast<int64_t>(w.c0) * a.N, a.N, ch, n0, w.width);
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int j = 0; j < P; ++j) A2[c][j] = mul2(A2[c][j], both(kLog2e));
+  load_rates<C, NS>(A2, a, w.c0, ch, n0, w.width);
   load_states<C, NS>(h, OUT && f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
-  if (!OUT && f.first && w.seg == 0) {
+  if (MODE == kAlone && f.first && w.seg == 0) {
     float2 h0[C][P];
     load_states<C, NS>(h0, f.h0 + bD * a.N, a.N, ch, n0, w.width);
     store_states<C, NS>(h0, f.first + bD * a.N, a.N, ch, n0, w.width);
   }
-  if (OUT && w.seg) join<C, NS>(h, A2, f, w.b, w.seg, len, w.c0, ch, n0, w.width);
-  float bias[8], skip[8], sum[8];
+  if (OUT)
+#pragma unroll 2
+    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
+  float2 bias[4], skip[4], sum[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    bias[j] = in && a.bias ? a.bias[w.c0 + col + j] : 0.f;
-    if (OUT) skip[j] = in && a.skip ? a.skip[w.c0 + col + j] : 0.f;
-    sum[j] = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    bias[j] = in && a.bias ? *reinterpret_cast<const float2*>(a.bias + w.c0 + col + 2 * j) : both(0.f);
+    if (OUT) skip[j] = in && a.skip ? *reinterpret_cast<const float2*>(a.skip + w.c0 + col + 2 * j) : both(0.f);
+    sum[j] = both(0.f);
   }
-  for (int t0 = begin; t0 < end; t0 += TT) {
-    if (MODE == kTrain)
-      store_states<C, NS>(h, f.kept + ((static_cast<int64_t>(w.b) * a.tiles() + t0 / TT) * a.D + w.c0) * a.N, a.N, ch, n0,
-                          w.width);
-    const int n = len - t0 < TT ? len - t0 : TT;
+  for (int k = 0; k < tiles; ++k) {
+    const int t0 = begin + (BACK ? tiles - 1 - k : k) * TT, n = (len < end ? len : end) - t0;
 #pragma unroll
     for (int i = 0; i < W::IT; ++i) {
       const int t = row + i * W::ROWS;
-      if (t >= TT) break;
+      if (W::ROWS > TT && t >= TT) break;
       float2 d[4], u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = add2(dt[i].pair(j), make_float2(bias[2 * j], bias[2 * j + 1]));
-        if (a.softplus) d[j] = make_float2(softplus<T>(d[j].x), softplus<T>(d[j].y));
-        u[j] = mul2(d[j], x[i].pair(j));
-        if (!OUT && t < n) {
-          sum[2 * j] += d[j].x;
-          sum[2 * j + 1] += d[j].y;
+        d[j] = add2(dt[i].pair(j), bias[j]);
+        if (a.softplus) d[j] = softplus2<T>(d[j]);
+        if (t >= n) d[j] = both(0.f);                  // changes nothing
+        if constexpr (BACK) {
+          u[j] = x[i].pair(j);
+          const float2 zp = z[i].pair(j);
+          if (a.z) u[j] = mul2(u[j], mul2(zp, sigmoid2<T>(zp)));
+        } else {
+          u[j] = mul2(d[j], x[i].pair(j));
         }
+        if (!OUT) sum[j] = add2(sum[j], d[j]);
       }
       store_vec<float, 8>(&sdt[t][col], d);
       store_vec<float, 8>(&sdx[t][col], u);
@@ -394,35 +367,43 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
       zo[i] = z[i];
     }
     __syncwarp();
-    if (t0 + TT < end) fetch(t0 + TT);
-    auto token = [&](int t) {
-      float d[C], u[C], y[C];
-      float2 Bv[P], Cv[P];
-      lds<C>(d, &sdt[t][ch]);
-      lds<C>(u, &sdx[t][ch]);
-      lds2<P>(Bv, &sB[t][n0]);
-      if (OUT) lds2<P>(Cv, &sC[t][n0]);
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float2 s = both(0.f);
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
-          h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
-          if (OUT) s = j ? fma2(Cv[j], h[c][j], s) : mul2(Cv[j], h[c][j]);
-        }
-        y[c] = s.x + s.y;
-      }
-      if (OUT) {
-        const float r = over_states<C>(y, sl);
-        if (C == 4 || sl % (4 / C) == 0) sy[t][ch + sl * C / 4] = r;
-      }
-    };
-    if (n == TT) {
+    if (k + 1 < tiles) fetch(BACK ? t0 - TT : t0 + TT);
+#pragma unroll 1
+    for (int half = 0; half < TT; half += kScanKeep) {
+      if (MODE == kTrain && t0 + half < end)
+        store_states<C, NS>(h, f.kept + ((static_cast<int64_t>(w.b) * a.keeps() + (t0 + half) / kScanKeep) * a.D + w.c0) * a.N,
+                            a.N, ch, n0, w.width);
 #pragma unroll 4
-      for (int t = 0; t < TT; ++t) token(t);
-    } else {
-      for (int t = 0; t < n; ++t) token(t);
+      for (int q = 0; q < kScanKeep; ++q) {
+        const int t = BACK ? TT - 1 - half - q : half + q;
+        float d[C], u[C], y[C];
+        float2 Bv[P], Cv[P];
+        lds<C>(d, &sdt[t][ch]);
+        lds<C>(u, &sdx[t][ch]);
+        lds2<P>(Bv, &sB[t][n0]);
+        if (OUT) lds2<P>(Cv, &sC[t][n0]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float2 s = both(0.f);
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
+            if (BACK) h[c][j] = mul2(e, fma2(Bv[j], both(u[c]), h[c][j]));
+            else h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
+            if (OUT) s = j ? fma2(Cv[j], h[c][j], s) : mul2(Cv[j], h[c][j]);
+          }
+          y[c] = s.x + s.y;
+        }
+        if (OUT) {
+          over_states<SL, C>(y, sl);
+          if constexpr (SL == 1) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) sy[t][ch + c] = y[c];
+          } else {
+            if (SL <= C || sl < C) sy[t][ch + sl] = y[0];
+          }
+        }
+      }
     }
     __syncwarp();
     if (OUT) {
@@ -431,11 +412,12 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
         const int t = row + i * W::ROWS;
         if (!in || t >= TT || t0 + t >= end) break;
         float2 v[4];
+        lds2<4>(v, &sy[t][col]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 s = *reinterpret_cast<const float2*>(&sy[t][col + 2 * j]), xp = xo[i].pair(j), zp = zo[i].pair(j);
-          v[j] = fma2(make_float2(skip[2 * j], skip[2 * j + 1]), xp, s);
-          if (a.z) v[j] = mul2(v[j], make_float2(zp.x * sigmoid<T>(zp.x), zp.y * sigmoid<T>(zp.y)));
+          const float2 zp = zo[i].pair(j);
+          v[j] = fma2(skip[j], xo[i].pair(j), v[j]);
+          if (a.z) v[j] = mul2(v[j], mul2(zp, sigmoid2<T>(zp)));
           if (t >= n) v[j] = both(0.f);
         }
         store_vec<T, 8>(static_cast<T*>(f.y) + a.row(w.b, t0 + t) * a.D + w.c0 + col, v);
@@ -446,289 +428,340 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
     if (f.hT && end == a.T) store_states<C, NS>(h, f.hT + bD * a.N, a.N, ch, n0, w.width);
     return;
   }
-  const int64_t at = (static_cast<int64_t>(w.b) * f.nseg + w.seg) * a.D + w.c0;
-  store_states<C, NS>(h, f.ends + at * a.N, a.N, ch, n0, w.width);
+  const int64_t at = (static_cast<int64_t>(w.b) * f.g.nseg + w.seg) * a.D + w.c0;
+  store_states<C, NS>(h, f.g.ends + at * a.N, a.N, ch, n0, w.width);
   // the rows' sums of steps, in a fixed order
 #pragma unroll
   for (int m = W::VC; m < 32; m <<= 1)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += __shfl_xor_sync(kFull, sum[j], m);
+    for (int j = 0; j < 4; ++j) {
+      sum[j].x += __shfl_xor_sync(kFull, sum[j].x, m);
+      sum[j].y += __shfl_xor_sync(kFull, sum[j].y, m);
+    }
   if (row == 0 && in)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f.sums[at + col + j] = sum[j];
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(f.g.sums + at + col + 2 * j) = sum[j];
 }
 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// A CTA goes through its channels' tiles from the last to the first.  In each it
-// computes the tile's states again from the kept one, holds them in registers, and
+// A warp goes through its segment's tiles of eight tokens from the last to the first.  In
+// each it computes the tile's states again from the kept one, holds them in registers, and
 // runs the gradient g of the state back through the tile:
 //     g += dy_t C_t;  dC_t += dy_t h_t;  dB_t += g delta_t x_t;  s1_t = sum g B_t
 //     g = a_t g;  P = g h_{t-1};  s2_t = sum P A;  dA += P delta_t
-// then, channel by channel, dx = delta s1 + D dy, ddelta = x s1 + s2, and dz from y.
-template <typename T, int NS, int C>
-struct BwdSmem {
-  static constexpr int CT = Where<C>::CT, NP = 4 * NS;
-  float dt[TT][CT], dx[TT][CT], dy[TT][CT], s1[TT][CT], s2[TT][CT], y[TT][CT];
-  float B[TT][NP], C_[TT][NP];
-  float part[kWarps][TT][2 * NP];
+// then, channel by channel, dx = delta s1 + D dy, ddelta = x s1 + s2, and dz from y, which
+// is computed again like the states.  Four channels and four states a lane: sums over the
+// states (of s1, s2 and y) and over the channels (of dB and dC) then take the fewest
+// exchanges together, one a state and token.  Inputs and the kept state of the next tile
+// are on their way into shared memory meanwhile.
+constexpr int kBT = kScanKeep, kBNS = 4, kBC = 4, kBWarps = 4;
+
+template <typename T, int SL>
+struct Bwd {
+  static constexpr int CL = 32 / SL, CT = CL * kBC, NP = SL * kBNS, P = kBNS / 2;
+  static constexpr int VC = CT / 8, ROWS = 32 / VC, IT = kBT / ROWS > 0 ? kBT / ROWS : 1, LD = CT + 4;
+  struct Smem {                                  // of a warp
+    Raw<T, 8> raw[2][4][IT][32];                 // x, dt, z, dy of a lane's items
+    float4 kept[2][kBC][32];
+    float dt[kBT][LD], dx[kBT][LD], dy[kBT][LD], s1[kBT][LD], s2[kBT][LD], y[kBT][LD];
+    float B[kBT][NP], C[kBT][NP];
+    float4 acc[4][32];                           // a lane's sums for dD and the bias
+  };
+  float part[2][kBWarps][kBT][2 * NP];           // dB, dC of each warp
+  Smem w[kBWarps];
 };
 
-// Sums 2 NS values over the eight channel lanes; lane cl ends up with NS / 4 of them
-// (2 NS >= 8), or with one that two lanes share (2 NS = 4).
-template <int V>
-__device__ __forceinline__ void over_channels(float (&v)[V], int cl, float (&r)[V >= 8 ? V / 8 : 1]) {
+// Sums four values over the SL state lanes and writes them, channel by channel.
+template <int SL>
+__device__ __forceinline__ void states_out(const float2 (&a)[2], float* to, int sl) {
+  constexpr int CL = 32 / SL;
+  const bool up = sl & 1;
+  float v = (up ? a[1].x : a[0].x) + __shfl_xor_sync(kFull, up ? a[0].x : a[1].x, CL);
+  float u = (up ? a[1].y : a[0].y) + __shfl_xor_sync(kFull, up ? a[0].y : a[1].y, CL);
+  if constexpr (SL == 2) {
+    *reinterpret_cast<float2*>(to + 2 * (sl & 1)) = make_float2(v, u);
+  } else {
+    const bool odd = sl & 2;
+    v = (odd ? u : v) + __shfl_xor_sync(kFull, odd ? v : u, 2 * CL);
 #pragma unroll
-  for (int bit = 4, m = V; bit >= 1; bit >>= 1) {
-    if (m > 1) {
-      m /= 2;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        if (i < m) {
-          const bool up = cl & bit;
-          const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
-          v[i] = keep + __shfl_xor_sync(kFull, send, bit);
-        }
-    } else {
-      v[0] += __shfl_xor_sync(kFull, v[0], bit);
-    }
+    for (int m = 4 * CL; m < 32; m *= 2) v += __shfl_xor_sync(kFull, v, m);
+    if (SL == 4 || sl < 4) to[2 * (sl & 1) + ((sl >> 1) & 1)] = v;
   }
-#pragma unroll
-  for (int i = 0; i < (V >= 8 ? V / 8 : 1); ++i) r[i] = v[i];
 }
 
-template <typename T, int NS, int C>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanBwdArgs g_, float* bc, float* pA, float* pD, float* pbias) {
-  using I = Items<C>;
-  using S = BwdSmem<T, NS, C>;
-  constexpr int CT = I::CT, NP = 4 * NS, P = NS / 2;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  S& s = *reinterpret_cast<S*>(smem_raw);
-  const ScanArgs& a = g_.a;
-  const rnn_scan_grad_t& out = g_.grad;
-  const Where<C> w(a);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cl = lane & 7, sl = lane >> 3;
-  const int ch = warp * 8 * C + cl * C, n0 = sl * NS;
-  const int row = tid / I::VC, col = tid % I::VC * 8;
-  const bool in = col < w.width;
-  const int len = a.len ? a.len[w.b] : a.T;
-  const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
-  const int tiles_c = Where<C>::per_group(a);            // tiles of a group: the partial sums of dB and dC
+// Sums dB and dC (four states each) over the CL channel lanes and writes them.
+template <int CL, int NP>
+__device__ __forceinline__ void channels_out(const float2 (&dB)[2], const float2 (&dC)[2], float* to, int cl) {
+  const bool up = cl & 1;
+  float v[4];
+  const float b[4] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y}, c[4] = {dC[0].x, dC[0].y, dC[1].x, dC[1].y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (up ? c[i] : b[i]) + __shfl_xor_sync(kFull, up ? b[i] : c[i], 1);
+  to += up ? NP : 0;
+  if constexpr (CL == 2) {
+    *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    const bool hi = cl & 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = (hi ? v[i + 2] : v[i]) + __shfl_xor_sync(kFull, hi ? v[i] : v[i + 2], 2);
+    to += hi ? 2 : 0;
+    if constexpr (CL == 4) {
+      *reinterpret_cast<float2*>(to) = make_float2(v[0], v[1]);
+    } else {
+      const bool top = cl & 4;
+      v[0] = (top ? v[1] : v[0]) + __shfl_xor_sync(kFull, top ? v[0] : v[1], 4);
+#pragma unroll
+      for (int m = 8; m < CL; m *= 2) v[0] += __shfl_xor_sync(kFull, v[0], m);
+      if (CL == 8 || cl < 8) to[top ? 1 : 0] = v[0];
+    }
+  }
+}
 
+__device__ __forceinline__ void async16(void* to, const void* from, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_u32(to)), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+
+template <typename T, int SL>
+__global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArgs p) {
+  using W = Bwd<T, SL>;
+  constexpr int CT = W::CT, NP = W::NP, P = W::P, C = kBC, NS = kBNS, TT = kBT, CL = W::CL;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  W& all = *reinterpret_cast<W*>(smem_raw);
+  const ScanArgs& a = p.a;
+  const rnn_scan_grad_t& out = p.grad;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  typename W::Smem& s = all.w[warp];
+  // a CTA's warps have neighbouring channels of one group; those beyond it have none
+  const Where<CT * kBWarps> cta(a, p.g.nseg, blockIdx.x);
+  const int c0 = cta.c0 + warp * CT, width = cta.width - warp * CT < CT ? cta.width - warp * CT : CT;   // may be <= 0
+  const int cl = lane % CL, sl = lane / CL, ch = cl * C, n0 = sl * NS;
+  const int row = lane / W::VC, col = lane % W::VC * 8;
+  const bool in = col < width && row < TT;
+  const int b = cta.b;
+  const int len = a.len ? a.len[b] : a.T, begin = cta.seg * p.g.len, end = begin + p.g.len < a.T ? begin + p.g.len : a.T;
+  const int64_t bD = static_cast<int64_t>(b) * a.D + c0;
+  const bool vB = on_16<T>(a.Bm, a.B_row), vC = on_16<T>(a.Cm, a.C_row);
+  const int tiles = (end - begin + TT - 1) / TT, ctas_g = Where<CT * kBWarps>::per_group(a);
+  const int last = len < end ? len : end;
+
+  Rows<T, TT, NP> rB, rC;
+  auto fetch = [&](int t0, int stage) {
+    const void* base[4] = {a.x, a.dt, a.z, p.dy};
+    const int64_t stride[4] = {a.x_row, a.dt_row, a.z_row, a.D};
+#pragma unroll
+    for (int i = 0; i < W::IT; ++i) {
+      const int t = t0 + row + i * W::ROWS;
+      const bool ok = in && t < last;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool on = ok && base[k];
+        const T* from = static_cast<const T*>(on ? base[k] : a.A) + (on ? a.row(b, t) * stride[k] + c0 + col : 0);
+        char* to = reinterpret_cast<char*>(&s.raw[stage][k][i][lane]);
+#pragma unroll
+        for (int v = 0; v < static_cast<int>(sizeof(Raw<T, 8>)); v += 16)
+          async16(to + v, on ? reinterpret_cast<const char*>(from) + v : reinterpret_cast<const char*>(from), on);
+      }
+    }
+    const float* kept = p.kept + (static_cast<int64_t>(b) * a.keeps() + t0 / TT) * a.D * a.N + static_cast<int64_t>(c0) * a.N;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const bool ok = ch + c < width && n0 < a.N;
+      async16(&s.kept[stage][c][lane], ok ? kept + static_cast<int64_t>(ch + c) * a.N + n0 : p.kept, ok);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    rB.load(a, a.Bm, a.B_row, vB, b, cta.g, t0, last - t0, lane);
+    rC.load(a, a.Cm, a.C_row, vC, b, cta.g, t0, last - t0, lane);
+  };
+  fetch(begin + (tiles - 1) * TT, 0);
   float2 A2[C][P], g[C][P], dA[C][P];
-  load_states<C, NS>(A2, a.A + static_cast<int64_t>(w.c0) * a.N, a.N, ch, n0, w.width);
+  load_rates<C, NS>(A2, a, c0, ch, n0, width);
+  load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, width);
+#pragma unroll 2
+  for (int i = p.g.nseg - 1; i > cta.seg; --i)
+    if (i * p.g.len < len) through<C, NS>(g, A2, a, p.g, b, i, c0, ch, n0, width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      A2[c][j] = mul2(A2[c][j], both(kLog2e));
-      dA[c][j] = both(0.f);
-    }
-  load_states<C, NS>(g, g_.dhT ? g_.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
-  float bias[8], skip[8], dD[8], dbias[8];
+    for (int j = 0; j < P; ++j) dA[c][j] = both(0.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    bias[j] = in && a.bias ? a.bias[w.c0 + col + j] : 0.f;
-    skip[j] = in && a.skip ? a.skip[w.c0 + col + j] : 0.f;
-    dD[j] = dbias[j] = 0.f;
-  }
-  for (int tile = a.tiles() - 1; tile >= 0; --tile) {
-    const int t0 = tile * TT, n = len - t0 < 0 ? 0 : len - t0 < TT ? len - t0 : TT;
-    Raw<T, 8> x[I::IT], dt[I::IT], z[I::IT], dy[I::IT];
-    load_items<T, I::IT, I::ROWS>(x, a, a.x, a.x_row, w.b, t0, n, row, w.c0 + col, in);
-    load_items<T, I::IT, I::ROWS>(dt, a, a.dt, a.dt_row, w.b, t0, n, row, w.c0 + col, in);
-    load_items<T, I::IT, I::ROWS>(z, a, a.z, a.z_row, w.b, t0, n, row, w.c0 + col, in);
-    load_items<T, I::IT, I::ROWS>(dy, a, g_.dy, a.D, w.b, t0, n, row, w.c0 + col, in);
-    Rows<T, NS> rB, rC;
-    rB.load(a, a.Bm, a.B_row, w.b, w.g, t0, n);
-    rC.load(a, a.Cm, a.C_row, w.b, w.g, t0, n);
+  for (int i = 0; i < 4; ++i) s.acc[i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto vec = [&](const float* from, int j) {
+    return in && from ? *reinterpret_cast<const float2*>(from + c0 + col + 2 * j) : both(0.f);
+  };
+
+  for (int k = 0; k < tiles; ++k) {
+    const int stage = k & 1, t0 = begin + (tiles - 1 - k) * TT, n = last - t0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < I::IT; ++i) {
-      const int t = row + i * I::ROWS;
-      if (t >= TT) break;
+    for (int i = 0; i < W::IT; ++i) {
+      const int t = row + i * W::ROWS;
+      if (W::ROWS > TT && t >= TT) break;
+      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], z = s.raw[stage][2][i][lane],
+                      dy = s.raw[stage][3][i][lane];
+      float2 d[4], u[4], o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 dp = dt[i].pair(j), xp = x[i].pair(j), zp = z[i].pair(j), op = dy[i].pair(j);
-        float2 d = make_float2(dp.x + bias[2 * j], dp.y + bias[2 * j + 1]);
-        if (a.softplus) d = make_float2(softplus<T>(d.x), softplus<T>(d.y));
-        *reinterpret_cast<float2*>(&s.dt[t][col + 2 * j]) = d;
-        *reinterpret_cast<float2*>(&s.dx[t][col + 2 * j]) = mul2(d, xp);
-        float2 o = op;
-        if (a.z) o = mul2(o, make_float2(zp.x * sigmoid<T>(zp.x), zp.y * sigmoid<T>(zp.y)));
-        *reinterpret_cast<float2*>(&s.dy[t][col + 2 * j]) = o;
+        d[j] = add2(dt.pair(j), vec(a.bias, j));
+        if (a.softplus) d[j] = softplus2<T>(d[j]);
+        if (t >= n) d[j] = both(0.f);                  // changes nothing
+        u[j] = mul2(d[j], x.pair(j));
+        o[j] = dy.pair(j);
+        if (a.z) o[j] = mul2(o[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
       }
+      store_vec<float, 8>(&s.dt[t][col], d);
+      store_vec<float, 8>(&s.dx[t][col], u);
+      store_vec<float, 8>(&s.dy[t][col], o);
     }
-    rB.store(&s.B[0][0]);
-    rC.store(&s.C_[0][0]);
-    // the states of the tile, again
+    rB.store(&s.B[0][0], a, a.Bm, a.B_row, vB, b, cta.g, t0, n, lane);
+    rC.store(&s.C[0][0], a, a.Cm, a.C_row, vC, b, cta.g, t0, n, lane);
     float2 h[TT + 1][C][P];
-    load_states<C, NS>(h[0], g_.kept + ((static_cast<int64_t>(w.b) * a.tiles() + tile) * a.D + w.c0) * a.N, a.N, ch, n0,
-                       w.width);
-    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float4 q = s.kept[stage][c][lane];
+      h[0][c][0] = make_float2(q.x, q.y);
+      h[0][c][1] = make_float2(q.z, q.w);
+    }
+    __syncwarp();
+    if (k + 1 < tiles) fetch(t0 - TT, stage ^ 1);
+    // the states of the tile, again
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      if (t < n) {
-        float d[C], u[C];
-        float2 Bv[P];
-        lds<C>(d, &s.dt[t][ch]);
-        lds<C>(u, &s.dx[t][ch]);
-        lds2<P>(Bv, &s.B[t][n0]);
+      float d[C], u[C];
+      float2 Bv[P];
+      lds<C>(d, &s.dt[t][ch]);
+      lds<C>(u, &s.dx[t][ch]);
+      lds2<P>(Bv, &s.B[t][n0]);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int j = 0; j < P; ++j)
-            h[t + 1][c][j] = fma2(decay2<T>(step2<T>(A2[c][j], d[c])), h[t][c][j], mul2(Bv[j], both(u[c])));
-      }
+        for (int j = 0; j < P; ++j)
+          h[t + 1][c][j] = fma2(decay2<T>(step2<T>(A2[c][j], d[c])), h[t][c][j], mul2(Bv[j], both(u[c])));
     }
+    // the decays are computed again below: kept, they would take twice the states' registers
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int t = TT - 1; t >= 0; --t) {
-      if (t < n) {
-        float d[C], u[C], o[C], s1[C], s2[C], yy[C];
-        float2 Bv[P], Cv[P], dB[P], dC[P];
-        lds<C>(d, &s.dt[t][ch]);
-        lds<C>(u, &s.dx[t][ch]);
-        lds<C>(o, &s.dy[t][ch]);
-        lds2<P>(Bv, &s.B[t][n0]);
-        lds2<P>(Cv, &s.C_[t][n0]);
+      float d[C], u[C], o[C];
+      float2 Bv[P], Cv[P], dB[P], dC[P], s1[C / 2], s2[C / 2], yy[C / 2];
+      lds<C>(d, &s.dt[t][ch]);
+      lds<C>(u, &s.dx[t][ch]);
+      lds<C>(o, &s.dy[t][ch]);
+      lds2<P>(Bv, &s.B[t][n0]);
+      lds2<P>(Cv, &s.C[t][n0]);
 #pragma unroll
-        for (int j = 0; j < P; ++j) dB[j] = dC[j] = both(0.f);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float2 q1 = both(0.f), q2 = both(0.f), q3 = both(0.f);
-#pragma unroll
-          for (int j = 0; j < P; ++j) {
-            const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
-            g[c][j] = fma2(Cv[j], both(o[c]), g[c][j]);
-            dC[j] = fma2(h[t + 1][c][j], both(o[c]), dC[j]);
-            q3 = fma2(h[t + 1][c][j], Cv[j], q3);
-            dB[j] = fma2(g[c][j], both(u[c]), dB[j]);
-            q1 = fma2(g[c][j], Bv[j], q1);
-            g[c][j] = mul2(e, g[c][j]);
-            const float2 p = mul2(g[c][j], h[t][c][j]);
-            q2 = fma2(p, A2[c][j], q2);
-            dA[c][j] = fma2(p, both(d[c]), dA[c][j]);
-          }
-          s1[c] = q1.x + q1.y;
-          s2[c] = q2.x + q2.y;
-          yy[c] = q3.x + q3.y;
-        }
-        const float r1 = over_states<C>(s1, sl), r2 = over_states<C>(s2, sl), r3 = over_states<C>(yy, sl);
-        if (C == 4 || sl % (4 / C) == 0) {
-          const int c = ch + sl * C / 4;
-          s.s1[t][c] = r1;
-          s.s2[t][c] = r2 * kLn2;
-          s.y[t][c] = r3;
-        }
-        float v[2 * NS], r[2 * NS >= 8 ? NS / 4 : 1];
+      for (int c = 0; c < C; ++c) {
+        float2 q1, q2, q3;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          v[2 * j] = dB[j].x; v[2 * j + 1] = dB[j].y;
-          v[NS + 2 * j] = dC[j].x; v[NS + 2 * j + 1] = dC[j].y;
+          const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
+          g[c][j] = fma2(Cv[j], both(o[c]), g[c][j]);
+          dC[j] = c ? fma2(h[t + 1][c][j], both(o[c]), dC[j]) : mul2(h[t + 1][c][j], both(o[c]));
+          q3 = j ? fma2(h[t + 1][c][j], Cv[j], q3) : mul2(h[t + 1][c][j], Cv[j]);
+          dB[j] = c ? fma2(g[c][j], both(u[c]), dB[j]) : mul2(g[c][j], both(u[c]));
+          q1 = j ? fma2(g[c][j], Bv[j], q1) : mul2(g[c][j], Bv[j]);
+          g[c][j] = mul2(e, g[c][j]);
+          const float2 r = mul2(g[c][j], h[t][c][j]);
+          q2 = j ? fma2(r, A2[c][j], q2) : mul2(r, A2[c][j]);
+          dA[c][j] = fma2(r, both(d[c]), dA[c][j]);
         }
-        over_channels<2 * NS>(v, cl, r);
-        if constexpr (NS >= 4) {
-          // lane cl: values cl * NS / 4 .. of (dB, dC)
-#pragma unroll
-          for (int i = 0; i < NS / 4; ++i) {
-            const int k = cl * (NS / 4) + i;
-            s.part[warp][t][(k / NS) * NP + n0 + k % NS] = r[i];
-          }
-        } else if (!(cl & 1)) {
-          const int k = cl >> 1;
-          s.part[warp][t][(k / NS) * NP + n0 + k % NS] = r[0];
-        }
+        (c & 1 ? s1[c / 2].y : s1[c / 2].x) = q1.x + q1.y;
+        (c & 1 ? s2[c / 2].y : s2[c / 2].x) = q2.x + q2.y;
+        (c & 1 ? yy[c / 2].y : yy[c / 2].x) = q3.x + q3.y;
       }
+      states_out<SL>(s1, &s.s1[t][ch], sl);
+      states_out<SL>(s2, &s.s2[t][ch], sl);
+      states_out<SL>(yy, &s.y[t][ch], sl);
+      channels_out<CL, NP>(dB, dC, &all.part[stage][warp][t][n0], cl);
     }
-    __syncthreads();
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < I::IT; ++i) {
-      const int t = row + i * I::ROWS;
-      if (t >= TT) break;
-      if (!in || t0 + t >= a.T) continue;
-      float2 vx[4], vt[4], vz[4];
+    for (int i = 0; i < W::IT; ++i) {
+      const int t = row + i * W::ROWS;
+      if (!in || t >= TT || t0 + t >= end) break;
+      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], z = s.raw[stage][2][i][lane],
+                      dy = s.raw[stage][3][i][lane];
+      float2 vx[4], vt[4], vz[4], d[4], o[4], q1[4], q2[4], q3[4];
+      lds2<4>(d, &s.dt[t][col]);
+      lds2<4>(o, &s.dy[t][col]);
+      lds2<4>(q1, &s.s1[t][col]);
+      lds2<4>(q2, &s.s2[t][col]);
+      lds2<4>(q3, &s.y[t][col]);
       const bool live = t < n;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = col + 2 * j;
-        vx[j] = vt[j] = vz[j] = both(0.f);
-        if (live) {
-          const float2 d = *reinterpret_cast<const float2*>(&s.dt[t][c]), o = *reinterpret_cast<const float2*>(&s.dy[t][c]);
-          const float2 q1 = *reinterpret_cast<const float2*>(&s.s1[t][c]), q2 = *reinterpret_cast<const float2*>(&s.s2[t][c]);
-          const float2 q3 = *reinterpret_cast<const float2*>(&s.y[t][c]);
-          const float2 xp = x[i].pair(j), zp = z[i].pair(j), op = dy[i].pair(j), dp = dt[i].pair(j);
-          const float2 sk = make_float2(skip[2 * j], skip[2 * j + 1]);
-          vx[j] = fma2(d, q1, mul2(sk, o));
-          vt[j] = fma2(xp, q1, q2);
-          if (a.softplus) {
-            vt[j].x *= sigmoid<T>(dp.x + bias[2 * j]);
-            vt[j].y *= sigmoid<T>(dp.y + bias[2 * j + 1]);
-          }
-          dD[2 * j] += o.x * xp.x;
-          dD[2 * j + 1] += o.y * xp.y;
-          dbias[2 * j] += vt[j].x;
-          dbias[2 * j + 1] += vt[j].y;
-          if (a.z) {
-            const float2 yv = fma2(sk, xp, q3), sg = make_float2(sigmoid<T>(zp.x), sigmoid<T>(zp.y));
-            vz[j].x = op.x * yv.x * sg.x * (1.f + zp.x * (1.f - sg.x));
-            vz[j].y = op.y * yv.y * sg.y * (1.f + zp.y * (1.f - sg.y));
-          }
-        }
+        const float2 xp = x.pair(j), zp = z.pair(j), sk = vec(a.skip, j);
+        vx[j] = fma2(d[j], q1[j], mul2(sk, o[j]));
+        vt[j] = fma2(xp, q1[j], mul2(q2[j], both(kLn2)));
+        if (a.softplus) vt[j] = mul2(vt[j], sigmoid2<T>(add2(dt.pair(j), vec(a.bias, j))));
+        const float2 sg = sigmoid2<T>(zp), yv = fma2(sk, xp, q3[j]);
+        // sigma + z sigma (1 - sigma)
+        vz[j] = mul2(mul2(dy.pair(j), yv), fma2(mul2(zp, sg), make_float2(1.f - sg.x, 1.f - sg.y), sg));
+        if (!live) vx[j] = vt[j] = vz[j] = both(0.f);
+        q3[j] = live ? mul2(o[j], xp) : both(0.f);
       }
-      const int64_t at = a.row(w.b, t0 + t) * a.D + w.c0 + col;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float4 q = s.acc[j][lane];
+        s.acc[j][lane] = make_float4(q.x + q3[2 * j].x, q.y + q3[2 * j].y, q.z + q3[2 * j + 1].x, q.w + q3[2 * j + 1].y);
+        q = s.acc[2 + j][lane];
+        s.acc[2 + j][lane] = make_float4(q.x + vt[2 * j].x, q.y + vt[2 * j].y, q.z + vt[2 * j + 1].x, q.w + vt[2 * j + 1].y);
+      }
+      const int64_t at = a.row(b, t0 + t) * a.D + c0 + col;
       if (out.dx) store_vec<T, 8>(static_cast<T*>(out.dx) + at, vx);
       if (out.ddt) store_vec<T, 8>(static_cast<T*>(out.ddt) + at, vt);
       if (out.dz) store_vec<T, 8>(static_cast<T*>(out.dz) + at, vz);
     }
-    if (bc) {
-      for (int e = tid; e < TT * 2 * NP; e += kThreads) {
-        const int t = e / (2 * NP), k = e - t * 2 * NP;
-        if (t0 + t >= a.T) break;
+    if (p.bc) {
+      __syncthreads();                           // the other stage of part is free until the next one
+      for (int e = threadIdx.x; e < TT * 2 * NP; e += 32 * kBWarps) {
+        const int t = e / (2 * NP), q = e % (2 * NP);
+        if (t0 + t >= end) break;
         float v = 0.f;
-        if (t < n)
 #pragma unroll
-          for (int q = 0; q < kWarps; ++q) v += s.part[q][t][k];
-        bc[(((static_cast<int64_t>(w.b) * a.T + t0 + t) * a.G + w.g) * tiles_c + (w.tile - w.g * tiles_c)) * (2 * NP) + k] = v;
+        for (int i = 0; i < kBWarps; ++i) v += all.part[stage][i][t][q];
+        p.bc[(((static_cast<int64_t>(b) * a.T + t0 + t) * a.G + cta.g) * ctas_g + cta.tile) * (2 * NP) + q] = t < n ? v : 0.f;
       }
     }
-    __syncthreads();
   }
-  if (out.dh0) store_states<C, NS>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, w.width);
-  if (pA) store_states<C, NS>(dA, pA + bD * a.N, a.N, ch, n0, w.width);
-  // the threads that share channels, in order
-  float* fold = reinterpret_cast<float*>(smem_raw);        // [ROWS][CT] twice
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    fold[row * CT + col + j] = dD[j];
-    fold[(I::ROWS + row) * CT + col + j] = dbias[j];
-  }
-  __syncthreads();
-  for (int c = tid; c < w.width; c += kThreads) {
+  if (out.dh0 && begin == 0) store_states<C, NS>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, width);
+  const int64_t at = (static_cast<int64_t>(b) * p.g.nseg + cta.seg) * a.D + c0;
+  if (p.pA) store_states<C, NS>(dA, p.pA + at * a.N, a.N, ch, n0, width);
+  // the rows' sums, in order
+  __syncwarp();
+  for (int c = lane; c < width; c += 32) {
     float v = 0.f, u = 0.f;
-    for (int r = 0; r < I::ROWS; ++r) {
-      v += fold[r * CT + c];
-      u += fold[(I::ROWS + r) * CT + c];
+    for (int r = 0; r < W::ROWS && r < TT; ++r) {
+      const int l = r * W::VC + c / 8;
+      v += reinterpret_cast<const float*>(&s.acc[(c & 7) / 4][l])[c & 3];
+      u += reinterpret_cast<const float*>(&s.acc[2 + (c & 7) / 4][l])[c & 3];
     }
-    if (pD) pD[bD + c] = v;
-    if (pbias) pbias[bD + c] = u;
+    if (p.pD) p.pD[at + c] = v;
+    if (p.pbias) p.pbias[at + c] = u;
   }
 }
 
-// dB and dC: the sum over a group's tiles of channels, in order.
+// dB and dC: the sum over a group's CTAs, in order, four states a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int tiles, int NP, T* dB, T* dC) {
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.G, all = rows * 2 * NP;
+__global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int ctas, int NP, T* dB, T* dC) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.G, all = rows * (NP / 2);
   for (int64_t e = blockIdx.x * 256LL + threadIdx.x; e < all; e += gridDim.x * 256LL) {
-    const int64_t r = e / (2 * NP);
-    const int k = static_cast<int>(e - r * 2 * NP), n = k % NP;
-    if (n >= a.N) continue;
-    float v = 0.f;
-    for (int i = 0; i < tiles; ++i) v += bc[(r * tiles + i) * (2 * NP) + k];
+    const int64_t r = e / (NP / 2);
+    const int k = static_cast<int>(e - r * (NP / 2)) * 4, n = k % NP;
+    T* out = k < NP ? dB : dC;
+    if (n >= a.N || !out) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < ctas; ++i) {
+      const float4 q = *reinterpret_cast<const float4*>(bc + (r * ctas + i) * (2 * NP) + k);
+      v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
+    }
     const int g = static_cast<int>(r % a.G);
     const int64_t bt = r / a.G;
     const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * a.T);
-    T* out = k < NP ? dB : dC;
-    if (out) out[(a.row(b, t) * a.G + g) * a.N + n] = from_f<T>(v);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    Vec4<T>::store(out + (a.row(b, t) * a.G + g) * a.N + n, f);
   }
 }
 
@@ -769,7 +802,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs p) {
     if (t < n && in) {
       const float xv = to_f(static_cast<const T*>(a.x)[r * a.x_row + d]);
       float dv = to_f(static_cast<const T*>(a.dt)[r * a.dt_row + d]) + bias;
-      if (a.softplus) dv = softplus<T>(dv);
+      if (a.softplus) dv = softplus2<T>(both(dv)).x;
       if (st) {
         const T* Bp = static_cast<const T*>(a.Bm) + r * a.B_row + g * a.N + n0;
         const T* Cp = static_cast<const T*>(a.Cm) + r * a.C_row + g * a.N + n0;
@@ -789,7 +822,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs p) {
         y = fmaf(skip, to_f(static_cast<const T*>(a.x)[r * a.x_row + d]), y);
         if (a.z) {
           const float zv = to_f(static_cast<const T*>(a.z)[r * a.z_row + d]);
-          y *= zv * sigmoid<T>(zv);
+          y *= zv * sigmoid2<T>(both(zv)).x;
         }
       }
       static_cast<T*>(p.y)[r * a.D + d] = from_f<T>(t < n ? y : 0.f);
@@ -800,85 +833,89 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs p) {
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
 
-// States a lane: a quarter of the channel's, rounded up to a power of two.
-int lane_states(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-constexpr int fwd_channels(int NS) { return NS <= 4 ? 4 : NS == 8 ? 2 : 1; }
-constexpr int bwd_channels(int NS) { return NS <= 4 ? 2 : 1; }
+// Lanes a channel: eight states each forward, four backward, rounded up to a power of two.
+int fwd_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
+int fwd_width(int N) { return N <= 8 ? 32 : 2 * 32 / fwd_lanes(N); }      // channels a warp
+int bwd_width(int N) { return kBWarps * kBC * 16 / fwd_lanes(N); }         // channels a CTA
+int per_group(const ScanArgs& a, int width) { return (a.D / a.G + width - 1) / width; }
 
-
-template <typename T, int NS, int C>
+template <typename T, int SL, int C>
 int fwd(ScanFwdArgs f, cudaStream_t s, int* launches) {
-  const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Warp<C>::per_group(f.a);
+  const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<Fwd<SL, C>::CT>::per_group(f.a);
   int rc;
-  if (f.nseg > 1) {
-    scan_fwd_kernel<T, NS, C, kAlone><<<warps * (f.nseg - 1), 32, 0, s>>>(f);
+  if (f.g.nseg > 1) {
+    scan_fwd_kernel<T, SL, C, kAlone><<<warps * (f.g.nseg - 1), 32, 0, s>>>(f);
     if ((rc = check_launch())) return rc;
     ++*launches;
     if (f.first) f.h0 = f.first;
   }
-  if (f.kept) scan_fwd_kernel<T, NS, C, kTrain><<<warps * f.nseg, 32, 0, s>>>(f);
-  else scan_fwd_kernel<T, NS, C, kInfer><<<warps * f.nseg, 32, 0, s>>>(f);
+  if (f.kept) scan_fwd_kernel<T, SL, C, kTrain><<<warps * f.g.nseg, 32, 0, s>>>(f);
+  else scan_fwd_kernel<T, SL, C, kInfer><<<warps * f.g.nseg, 32, 0, s>>>(f);
   if (!(rc = check_launch())) ++*launches;
   return rc;
 }
 template <typename T>
 int fwd_t(const ScanFwdArgs& f, cudaStream_t s, int* launches) {
-  switch (lane_states(f.a.N)) {
-    case 2: return fwd<T, 2, 4>(f, s, launches);
-    case 4: return fwd<T, 4, 4>(f, s, launches);
-    case 8: return fwd<T, 8, 2>(f, s, launches);
-    default: return fwd<T, 16, 1>(f, s, launches);
+  switch (fwd_lanes(f.a.N)) {
+    case 1: return fwd<T, 1, 1>(f, s, launches);
+    case 2: return fwd<T, 2, 2>(f, s, launches);
+    case 4: return fwd<T, 4, 2>(f, s, launches);
+    default: return fwd<T, 8, 2>(f, s, launches);
   }
 }
 
-int bwd_tiles(const ScanArgs& a) {
-  const int C = bwd_channels(lane_states(a.N)), ct = kWarps * 8 * C;
-  return (a.D / a.G + ct - 1) / ct;
-}
-
-template <typename T, int NS>
-int bwd(const ScanBwdArgs& b, cudaStream_t s, float* bc, float* pA, float* pD, float* pbias) {
-  constexpr int C = bwd_channels(NS), smem = sizeof(BwdSmem<T, NS, C>);
-  static_assert(smem <= 227 * 1024 && smem >= 2 * Items<C>::ROWS * Items<C>::CT * 4, "the tile and the folded sums fit");
-  if (cudaFuncSetAttribute(scan_bwd_kernel<T, NS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return RNN_CUDA_ERROR;
-  const unsigned grid = static_cast<unsigned>(b.a.B) * b.a.G * Where<C>::per_group(b.a);
-  scan_bwd_kernel<T, NS, C><<<grid, kThreads, smem, s>>>(b, bc, pA, pD, pbias);
-  return check_launch();
-}
-
-template <typename T>
-int bwd_t(const ScanBwdArgs& b, cudaStream_t s, int* launches) {
-  const ScanArgs& a = b.a;
-  const ScanBwdLayout l = scan_bwd_layout(a);
-  auto part = [&](const void* want, size_t off) { return want ? reinterpret_cast<float*>(b.work + off) : nullptr; };
-  float *bc = part(b.grad.dB ? b.grad.dB : b.grad.dC, l.bc), *pA = part(b.grad.dA, l.dA), *pD = part(b.grad.dD, l.dD),
-        *pbias = part(b.grad.ddt_bias, l.dbias);
+template <typename T, int SL, int C>
+int bwd(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
   int rc;
-  switch (lane_states(a.N)) {
-    case 2: rc = bwd<T, 2>(b, s, bc, pA, pD, pbias); break;
-    case 4: rc = bwd<T, 4>(b, s, bc, pA, pD, pbias); break;
-    case 8: rc = bwd<T, 8>(b, s, bc, pA, pD, pbias); break;
-    default: rc = bwd<T, 16>(b, s, bc, pA, pD, pbias);
+  if (p.g.nseg > 1) {
+    ScanFwdArgs f{};
+    f.a = p.a;
+    f.a.x = p.dy;
+    f.a.x_row = p.a.D;
+    f.a.Bm = p.a.Cm;
+    f.a.B_row = p.a.C_row;
+    f.g = p.g;
+    const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<Fwd<SL, C>::CT>::per_group(f.a);
+    scan_fwd_kernel<T, SL, C, kAloneBack><<<warps * (p.g.nseg - 1), 32, 0, s>>>(f);
+    if ((rc = check_launch())) return rc;
+    ++*launches;
+  }
+  constexpr int smem = sizeof(Bwd<T, 2 * SL>);
+  static_assert(smem <= 227 * 1024, "a CTA's tiles fit");
+  if (cudaFuncSetAttribute(scan_bwd_kernel<T, 2 * SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return RNN_CUDA_ERROR;
+  const unsigned ctas = static_cast<unsigned>(p.a.B) * p.a.G * Where<Bwd<T, 2 * SL>::CT * kBWarps>::per_group(p.a);
+  scan_bwd_kernel<T, 2 * SL><<<ctas * p.g.nseg, 32 * kBWarps, smem, s>>>(p);
+  if (!(rc = check_launch())) ++*launches;
+  return rc;
+}
+template <typename T>
+int bwd_t(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
+  const ScanArgs& a = p.a;
+  int rc;
+  switch (fwd_lanes(a.N)) {
+    case 1: rc = bwd<T, 1, 1>(p, s, launches); break;
+    case 2: rc = bwd<T, 2, 2>(p, s, launches); break;
+    case 4: rc = bwd<T, 4, 2>(p, s, launches); break;
+    default: rc = bwd<T, 8, 2>(p, s, launches);
   }
   if (rc) return rc;
-  ++*launches;
-  if (bc) {
-    const int NP = 4 * lane_states(a.N);
-    const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * a.G * 2 * NP + 255) / 256;
+  if (p.bc) {
+    const int NP = 8 * fwd_lanes(a.N);
+    const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * a.G * (NP / 2) + 255) / 256;
     scan_bc_kernel<T><<<static_cast<unsigned>(blocks < 16 * a.num_sms ? blocks : 16 * a.num_sms), 256, 0, s>>>(
-        a, bc, bwd_tiles(a), NP, static_cast<T*>(b.grad.dB), static_cast<T*>(b.grad.dC));
+        a, p.bc, per_group(a, bwd_width(a.N)), NP, static_cast<T*>(p.grad.dB), static_cast<T*>(p.grad.dC));
     if ((rc = check_launch())) return rc;
     ++*launches;
   }
   auto sum = [&](const float* from, int64_t n, void* to) {
     if (!from || rc) return;
-    scan_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(from, a.B, n, static_cast<float*>(to));
+    scan_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(from, a.B * p.g.nseg, n, static_cast<float*>(to));
     if (!(rc = check_launch())) ++*launches;
   };
-  sum(pA, static_cast<int64_t>(a.D) * a.N, b.grad.dA);
-  sum(pD, a.D, b.grad.dD);
-  sum(pbias, a.D, b.grad.ddt_bias);
+  sum(p.pA, static_cast<int64_t>(a.D) * a.N, p.grad.dA);
+  sum(p.pD, a.D, p.grad.dD);
+  sum(p.pbias, a.D, p.grad.ddt_bias);
   return rc;
 }
 
@@ -895,61 +932,73 @@ int step_t(const ScanStepArgs& p, cudaStream_t s) {
   return p.a.N <= 32 ? step<T, 8>(p, s) : step<T, 16>(p, s);
 }
 
+size_t up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+ScanSegs segments(const ScanSplit& p, void* work) {
+  char* w = static_cast<char*>(work);
+  return {p.nseg, p.len, reinterpret_cast<float*>(w + p.ends), reinterpret_cast<float*>(w + p.sums)};
+}
+
 }  // namespace
 
-ScanSplit scan_split(const ScanArgs& a, int is_bf16) {
-  const int C = fwd_channels(lane_states(a.N)), per = (a.D / a.G + 8 * C - 1) / (8 * C);
-  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per, want = static_cast<int64_t>(a.num_sms) * 16;
-  const int tiles = a.tiles();
+ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward) {
+  const int width = backward ? bwd_width(a.N) / kBWarps : fwd_width(a.N);
+  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width), want = static_cast<int64_t>(a.num_sms) * (backward ? 8 : 16);
+  const int tiles = (a.T + kTile - 1) / kTile;
   int64_t n = warps * 2 > want ? 1 : want / warps;
-  const char* env = getenv("V_NSEG");
+  const char* env = getenv(backward ? "V_BSEG" : "V_NSEG");
   if (env) n = atoi(env);
   if (n > tiles / 4) n = tiles / 4;
   if (n < 1) n = 1;
   ScanSplit p{};
-  p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * kScanTile;
+  p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * kTile;
   p.nseg = (a.T + p.len - 1) / p.len;
   if (p.nseg == 1) return p;
-  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   const size_t rows = static_cast<size_t>(a.B) * p.nseg * a.D;
   p.sums = up(rows * a.N * 4);
   p.first = p.sums + up(rows * 4);
-  p.bytes = p.first + up(static_cast<size_t>(a.B) * a.D * a.N * 4);
+  p.bytes = p.first + (backward ? 0 : up(static_cast<size_t>(a.B) * a.D * a.N * 4));
   return p;
 }
 
 int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStream_t s, int* launches) {
   ScanFwdArgs f = f_;
-  const ScanSplit p = scan_split(f.a, is_bf16);
-  f.nseg = p.nseg;
-  f.seg = p.len;
-  f.ends = reinterpret_cast<float*>(static_cast<char*>(work) + p.ends);
-  f.sums = reinterpret_cast<float*>(static_cast<char*>(work) + p.sums);
+  const ScanSplit p = scan_split(f.a, is_bf16, 0);
+  f.g = segments(p, work);
   f.first = p.nseg > 1 && f.h0 && f.h0 == f.hT ? reinterpret_cast<float*>(static_cast<char*>(work) + p.first) : nullptr;
   *launches = 0;
   return is_bf16 ? fwd_t<__nv_bfloat16>(f, s, launches) : fwd_t<float>(f, s, launches);
 }
 
-ScanBwdLayout scan_bwd_layout(const ScanArgs& a) {
+ScanBwdLayout scan_bwd_layout(const ScanArgs& a, int is_bf16) {
+  const ScanSplit p = scan_split(a, is_bf16, 1);
   ScanBwdLayout l{};
-  size_t off = 0;
+  size_t off = p.bytes;
   auto take = [&](size_t n) {
     const size_t o = off;
-    off += (n * 4 + 255) & ~static_cast<size_t>(255);
+    off += up(n * 4);
     return o;
   };
-  const size_t bd = static_cast<size_t>(a.B) * a.D;
-  l.bc = take(static_cast<size_t>(a.B) * a.T * a.G * bwd_tiles(a) * 8 * lane_states(a.N));
-  l.dA = take(bd * a.N);
-  l.dD = take(bd);
-  l.dbias = take(bd);
+  const size_t rows = static_cast<size_t>(a.B) * p.nseg * a.D;
+  l.bc = take(static_cast<size_t>(a.B) * a.T * a.G * per_group(a, bwd_width(a.N)) * 16 * fwd_lanes(a.N));
+  l.dA = take(rows * a.N);
+  l.dD = take(rows);
+  l.dbias = take(rows);
   l.bytes = off;
   return l;
 }
 
 int launch_scan_backward(const ScanBwdArgs& b, int is_bf16, cudaStream_t s, int* launches) {
+  ScanBwdArgs p = b;
+  const ScanBwdLayout l = scan_bwd_layout(p.a, is_bf16);
+  p.g = segments(scan_split(p.a, is_bf16, 1), p.work);
+  auto part = [&](const void* want, size_t off) { return want ? reinterpret_cast<float*>(p.work + off) : nullptr; };
+  p.bc = part(p.grad.dB ? p.grad.dB : p.grad.dC, l.bc);
+  p.pA = part(p.grad.dA, l.dA);
+  p.pD = part(p.grad.dD, l.dD);
+  p.pbias = part(p.grad.ddt_bias, l.dbias);
   *launches = 0;
-  return is_bf16 ? bwd_t<__nv_bfloat16>(b, s, launches) : bwd_t<float>(b, s, launches);
+  return is_bf16 ? bwd_t<__nv_bfloat16>(p, s, launches) : bwd_t<float>(p, s, launches);
 }
 
 int launch_scan_step(const ScanStepArgs& p, int is_bf16, cudaStream_t s) {

@@ -9,9 +9,8 @@
 
 namespace rnn {
 
-// Tokens a tile: what a CTA stages at once, and the distance of the states that a
-// training forward keeps.
-constexpr int kScanTile = 16;
+// Tokens between the states that a training forward keeps.
+constexpr int kScanKeep = 8;
 
 struct ScanArgs {
   int B, T, D, N, G;
@@ -25,36 +24,43 @@ struct ScanArgs {
   __host__ __device__ int64_t row(int b, int t) const {
     return bfirst ? static_cast<int64_t>(b) * T + t : static_cast<int64_t>(t) * B + b;
   }
-  __host__ __device__ int tiles() const { return (T + kScanTile - 1) / kScanTile; }
+  __host__ __device__ int keeps() const { return (T + kScanKeep - 1) / kScanKeep; }
 };
 
-// A long sequence runs as several segments side by side.  ends: byte offset of [B][nseg]
-// [D][N], the state that each segment alone leaves; sums: of [B][nseg][D], the sum of its
-// steps; first: of [B][D][N], the initial state where the final one overwrites it.
+// A long sequence runs as several segments side by side: what each leaves by itself
+// (the state forward, its gradient backward, and the sum of its steps) is computed
+// first.  Byte offsets in the scratch of a call.
 struct ScanSplit {
-  int nseg, len;               // segments, tokens of each (a multiple of the tile)
-  size_t ends, sums, first, bytes;
+  int nseg, len;               // segments, tokens of each
+  size_t ends;                 // [B][nseg][D][N]
+  size_t sums;                 // [B][nseg][D]
+  size_t first;                // [B][D][N]: the initial state where the final one overwrites it
+  size_t bytes;
 };
-ScanSplit scan_split(const ScanArgs& a, int is_bf16);
+ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward);
+
+struct ScanSegs {
+  int nseg, len;
+  float *ends, *sums;
+};
 
 struct ScanFwdArgs {
   ScanArgs a;
   const float* h0;             // or null
   float* hT;                   // or null
   void* y;
-  float* kept;                 // [B][tile][D][N] the state before each tile, or null
-  int nseg, seg;               // segments, tokens of each
-  float *ends, *sums;
+  float* kept;                 // [B][keep][D][N] the state before every kScanKeep tokens, or null
+  ScanSegs g;
   float* first;                // where the first segment copies h0 to, or null
 };
 int launch_scan_forward(const ScanFwdArgs& f, void* work, int is_bf16, cudaStream_t s, int* launches);
 
-// Byte offsets of the backward's scratch: partial sums over channels (of dB and dC),
-// over tokens and sequences (of dA, dD and the bias).
+// Byte offsets of the backward's scratch behind its segments': partial sums over channels
+// (of dB and dC), over tokens and sequences (of dA, dD and the bias).
 struct ScanBwdLayout {
   size_t bc, dA, dD, dbias, bytes;
 };
-ScanBwdLayout scan_bwd_layout(const ScanArgs& a);
+ScanBwdLayout scan_bwd_layout(const ScanArgs& a, int is_bf16);
 
 struct ScanBwdArgs {
   ScanArgs a;
@@ -63,6 +69,8 @@ struct ScanBwdArgs {
   const float* kept;
   rnn_scan_grad_t grad;
   char* work;
+  ScanSegs g;
+  float *bc, *pA, *pD, *pbias; // partial sums, or null
 };
 int launch_scan_backward(const ScanBwdArgs& b, int is_bf16, cudaStream_t s, int* launches);
 

@@ -190,9 +190,9 @@ rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* out) {
   h->bf16 = desc->dtype == RNN_BF16;
   h->es = h->bf16 ? 2 : 4;
   const ScanArgs a = scan_shape(h);
-  h->workspace_bytes = scan_split(a, h->bf16).bytes;
-  h->bwd_workspace_bytes = scan_bwd_layout(a).bytes;
-  h->reserve_bytes = al(static_cast<size_t>(a.B) * a.tiles() * a.D * a.N * 4);
+  h->workspace_bytes = scan_split(a, h->bf16, 0).bytes;
+  h->bwd_workspace_bytes = scan_bwd_layout(a, h->bf16).bytes;
+  h->reserve_bytes = al(static_cast<size_t>(a.B) * a.keeps() * a.D * a.N * 4);
   *out = h;
   return RNN_OK;
 }

@@ -171,6 +171,29 @@ def test_long_memory(dtype):
     run(600, 2, 64, 16, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,lengths", [(128, [128, 1]), (257, [130, 257]), (400, [399, 0]), (513, [64, 512]), (600, [333, 65])])
+def test_segments_side_by_side(T, lengths, dtype):
+    """Long sequences of few channels run as several segments, some of them behind the last token."""
+    run(T, 2, 24, 16, dtype=dtype, lengths=lengths, poison=True)
+    run(T, 2, 40, 8, dtype=dtype, bfirst=True, packed=True, state=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_state_in_place_over_segments(dtype):
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    T, B, D, N = 512, 2, 24, 16
+    t = {n: v.cuda() for n, v in _inputs(T, B, D, N, 1, dtype, 12).items()}
+    op = R.SelectiveScan(B, T, D, N, dtype=dtype)
+    args = [t[n] for n in ("x", "dt", "A", "Bm", "Cm")]
+    y, hT = op.forward(*args, h0=t["h0"], train=False)
+    for _ in range(3):
+        h = t["h0"].clone()
+        y2, h2 = op.forward(*args, h0=h, hT=h, train=False)
+        assert h2.data_ptr() == h.data_ptr() and torch.equal(y, y2) and torch.equal(hT, h2)
+
+
 def test_training_and_inference_agree():
     import torch
     a = run(50, 2, 136, 16, train=False, check=False)
