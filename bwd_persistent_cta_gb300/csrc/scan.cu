@@ -195,42 +195,54 @@ __device__ __forceinline__ bool on_16(const void* base, int64_t stride) {
 }
 template <typename T, int TT, int NP>
 struct Rows {
-  static constexpr int VECS = TT * NP / 8, PER = VECS / 32 > 0 ? VECS / 32 : 1;
+  static constexpr int VECS = TT * NP / 8, PER = VECS / 32 > 0 ? VECS / 32 : 1, PT = 32 * 8 / NP;   // tokens between two of a lane's
   Raw<T, 8> v[PER];
-  __device__ __forceinline__ void load(const ScanArgs& a, const void* base, int64_t stride, bool vec, int b, int g, int t0, int n,
-                                       int lane) {
-    if (!vec) return;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i, t = e / (NP / 8), s = e % (NP / 8) * 8;
-      const bool ok = e < VECS && t < n && s < a.N;
-      load_or<T, 8>(v[i], base, ok ? a.row(b, t0 + t) * stride + g * a.N + s : 0, ok, 0.f);
-    }
+  const T* at;                 // the row of token 0 of the tile to come
+  int64_t token;               // elements from a token to the next
+  bool vec;
+  int t, s, N;                 // of the lane's first vector
+  __device__ __forceinline__ Rows(const ScanArgs& a, const void* base, int64_t stride, int b, int g, int t0, int lane) {
+    vec = on_16<T>(base, stride);
+    token = (a.bfirst ? 1 : a.B) * stride;
+    at = static_cast<const T*>(base) + a.row(b, t0) * stride + g * a.N;
+    N = a.N;
+    t = lane / (NP / 8);
+    s = lane % (NP / 8) * 8;
   }
-  __device__ __forceinline__ void store(float* to, const ScanArgs& a, const void* base, int64_t stride, bool vec, int b, int g,
-                                        int t0, int n, int lane) const {
+  // The tile whose first row is ``at``, n of its tokens, then on by ``move`` tokens.
+  __device__ __forceinline__ void load(int n, int move) {
     if (vec) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        if (VECS < 32 && e >= VECS) break;
+        const bool ok = (VECS >= 32 || t < TT) && t + i * PT < n && s < N;
+        load_or<T, 8>(v[i], at, ok ? (t + i * PT) * token + s : 0, ok, 0.f);
+      }
+      at += move * token;
+    }
+  }
+  __device__ __forceinline__ void store(float* to, int n, int move, int lane) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (VECS < 32 && t >= TT) break;
         float2 f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = v[i].pair(j);
-        store_vec<float, 8>(to + e * 8, f);
+        store_vec<float, 8>(to + (lane + 32 * i) * 8, f);
       }
     } else {
 #pragma unroll 4
       for (int e = lane; e < TT * NP; e += 32) {
-        const int t = e / NP, s = e % NP;
-        to[e] = t < n && s < a.N ? to_f(static_cast<const T*>(base)[a.row(b, t0 + t) * stride + g * a.N + s]) : 0.f;
+        const int q = e / NP, k = e % NP;
+        to[e] = q < n && k < N ? to_f(at[q * token + k]) : 0.f;
       }
+      at += move * token;
     }
   }
 };
 
 // Adds one segment's own end to what went through it: h = exp(A sum) h + end.
-template <int C, int NS>
+template <typename T, int C, int NS>
 __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanArgs& a, const ScanSegs& g,
                                         int b, int i, int c0, int ch, int n0, int width) {
   const int64_t at = (static_cast<int64_t>(b) * g.nseg + i) * a.D + c0;
@@ -240,25 +252,47 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
   for (int c = 0; c < C; ++c) {
     const float sum = ch + c < width ? g.sums[at + ch + c] : 0.f;
 #pragma unroll
-    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<float>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
+    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<T>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
   }
 }
 
 // ---------------------------------------------------------------------------
 // forward, and what a segment leaves by itself in either direction
 // ---------------------------------------------------------------------------
-// A warp works alone: it reads a tile of 16 tokens of its channels (the next tile's
-// loads in flight meanwhile), leaves the steps in shared memory, runs the recurrence
-// and finishes the outputs, with no barrier but its own.  Eight states a lane: at 16
-// states two lanes share a channel, so a sum over the states is one exchange.
-constexpr int kTile = 16, kFwdNS = 8;
+// A warp works alone: a tile of eight tokens of its channels is on its way into shared
+// memory while it works on the one before; it leaves the steps in shared memory, runs the
+// recurrence and finishes the outputs, with no barrier but its own.  Nothing but the
+// states, their rates and the next rows of B and C stays in registers, so that five warps
+// a scheduler hide the latencies of each other.  Eight states a lane: at 16 states two
+// lanes share a channel, and a sum over the states is one exchange.
+#ifndef V_OCC
+#define V_OCC 12
+#endif
+constexpr int kFwdNS = 8;
 enum { kInfer, kTrain, kAlone, kAloneBack };
 
-template <int SL, int C>
+__device__ __forceinline__ void async16(void* to, const void* from, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_u32(to)), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+// A thread's 8 elements to its own place, or zeros.
+template <typename T>
+__device__ __forceinline__ void async_item(Raw<T, 8>* to, const void* base, int64_t at, bool ok, const void* any) {
+  const char* from = ok ? reinterpret_cast<const char*>(static_cast<const T*>(base) + at) : static_cast<const char*>(any);
+#pragma unroll
+  for (int v = 0; v < static_cast<int>(sizeof(Raw<T, 8>)); v += 16)
+    async16(reinterpret_cast<char*>(to) + v, ok ? from + v : from, ok);
+}
+
+template <typename T, int SL, int C, bool OUT>
 struct Fwd {
   static constexpr int CL = 32 / SL, CT = CL * C, NP = SL * kFwdNS, P = kFwdNS / 2;
-  static constexpr int VC = CT / 8, ROWS = 32 / VC, IT = kTile / ROWS > 0 ? kTile / ROWS : 1;
+  static constexpr int VC = CT / 8, ROWS = 32 / VC, TT = ROWS < 16 ? ROWS : 16;     // an item a lane
+  static_assert(TT % kScanKeep == 0, "whole stretches between kept states");
   static constexpr int LD = CT + 4;      // a row in shared memory: rows of a store on banks of their own
+  Raw<T, 8> raw[2][3][32];               // x, dt, z of a lane's item
+  float bias[CT], skip[CT];
+  float dt[TT][LD], dx[TT][LD], y[OUT ? TT : 1][LD];
+  float B[TT][NP], C_[OUT ? TT : 1][NP];
 };
 
 // Sums C values over the SL state lanes; lane sl < C ends up with value sl (all of them
@@ -279,44 +313,48 @@ __device__ __forceinline__ void over_states(float (&v)[C], int sl) {
 }
 
 template <typename T, int SL, int C, int MODE>
-__global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
-  using W = Fwd<SL, C>;
-  constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, TT = kTile, LD = W::LD;
+__global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kernel(const ScanFwdArgs f) {
   constexpr bool OUT = MODE == kInfer || MODE == kTrain, BACK = MODE == kAloneBack;
-  // backward, B is C and x is the gradient of the gated output
-  __shared__ __align__(16) float sdt[TT][LD], sdx[TT][LD], sB[TT][NP], sC[OUT ? TT : 1][NP], sy[OUT ? TT : 1][LD];
+  using W = Fwd<T, SL, C, OUT>;
+  constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, TT = W::TT;
+  __shared__ __align__(16) W s;
   const ScanArgs& a = f.a;
   // forward the last segment, backward the first has no other that wants its end
   Where<CT> w(a, OUT ? f.g.nseg : f.g.nseg - 1, blockIdx.x);
   if (BACK) ++w.seg;
   const int lane = threadIdx.x, cl = lane % W::CL, sl = lane / W::CL, ch = cl * C, n0 = sl * NS;
   const int row = lane / W::VC, col = lane % W::VC * 8;
-  const bool in = col < w.width && row < TT;
+  const bool in = col < w.width && row < TT, gate = a.z != nullptr;
   const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * f.g.len, end = begin + f.g.len < a.T ? begin + f.g.len : a.T;
+  const int last = len < end ? len : end;
   const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
-  const bool vB = on_16<T>(a.Bm, a.B_row), vC = on_16<T>(a.Cm, a.C_row);
   const int tiles = (end - begin + TT - 1) / TT;
+  const int first = BACK ? begin + (tiles - 1) * TT : begin, move = BACK ? -TT : TT;
 
-  Raw<T, 8> x[W::IT], dt[W::IT], z[W::IT];
-  Rows<T, TT, NP> rB, rC;
-  auto items = [&](Raw<T, 8> (&r)[W::IT], const void* base, int64_t stride, int t0) {
-#pragma unroll
-    for (int i = 0; i < W::IT; ++i) {
-      const int t = t0 + row + i * W::ROWS;
-      const bool ok = in && base && t < len && t < end;
-      load_or<T, 8>(r[i], base, ok ? a.row(w.b, t) * stride + w.c0 + col : 0, ok, 0.f);
-    }
+  // where the lane's item of the tile to come lies; backward, x is the gradient of the
+  // gated output, and B is C
+  const int64_t hop = a.bfirst ? move : static_cast<int64_t>(move) * a.B, row0 = a.row(w.b, first + row);
+  const T *px = static_cast<const T*>(a.x) + row0 * a.x_row + w.c0 + col, *pdt = static_cast<const T*>(a.dt) + row0 * a.dt_row + w.c0 + col,
+          *pz = static_cast<const T*>(a.z) + row0 * a.z_row + w.c0 + col;
+  Rows<T, TT, NP> rB(a, a.Bm, a.B_row, w.b, w.g, first, lane), rC(a, OUT ? a.Cm : a.Bm, OUT ? a.C_row : a.B_row, w.b, w.g, first, lane);
+  auto fetch = [&](int t0, int stage) {
+    const bool ok = in && t0 + row < last;
+    async_item<T>(&s.raw[stage][0][lane], px, 0, ok, a.A);
+    async_item<T>(&s.raw[stage][1][lane], pdt, 0, ok, a.A);
+    if ((OUT || BACK) && gate) async_item<T>(&s.raw[stage][2][lane], pz, 0, ok, a.A);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    px += hop * a.x_row;
+    pdt += hop * a.dt_row;
+    pz += hop * a.z_row;
+    rB.load(last - t0, move);
+    if (OUT) rC.load(last - t0, move);
   };
-  auto fetch = [&](int t0) {
-    items(x, a.x, a.x_row, t0);
-    items(dt, a.dt, a.dt_row, t0);
-    if (OUT || BACK) items(z, a.z, a.z_row, t0);
-    const int n = (len < end ? len : end) - t0;
-    rB.load(a, a.Bm, a.B_row, vB, w.b, w.g, t0, n, lane);
-    if (OUT) rC.load(a, a.Cm, a.C_row, vC, w.b, w.g, t0, n, lane);
-  };
-  fetch(BACK ? begin + (tiles - 1) * TT : begin);
-  float2 A2[C][P], h[C][P];
+  fetch(first, 0);
+  for (int c = lane; c < CT; c += 32) {
+    s.bias[c] = a.bias && c < w.width ? a.bias[w.c0 + c] : 0.f;
+    s.skip[c] = OUT && a.skip && c < w.width ? a.skip[w.c0 + c] : 0.f;
+  }
+  float2 A2[C][P], h[C][P], sum[4];
   load_rates<C, NS>(A2, a, w.c0, ch, n0, w.width);
   load_states<C, NS>(h, OUT && f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
   if (MODE == kAlone && f.first && w.seg == 0) {
@@ -326,102 +364,108 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const ScanFwdArgs f) {
   }
   if (OUT)
 #pragma unroll 2
-    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
-  float2 bias[4], skip[4], sum[4];
+    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<T, C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bias[j] = in && a.bias ? *reinterpret_cast<const float2*>(a.bias + w.c0 + col + 2 * j) : both(0.f);
-    if (OUT) skip[j] = in && a.skip ? *reinterpret_cast<const float2*>(a.skip + w.c0 + col + 2 * j) : both(0.f);
-    sum[j] = both(0.f);
-  }
+  for (int j = 0; j < 4; ++j) sum[j] = both(0.f);
+  T* py = static_cast<T*>(f.y) + row0 * a.D + w.c0 + col;
+  float* pk = MODE == kTrain ? f.kept + ((static_cast<int64_t>(w.b) * a.keeps() + begin / kScanKeep) * a.D + w.c0) * a.N : nullptr;
+  __syncwarp();
   for (int k = 0; k < tiles; ++k) {
-    const int t0 = begin + (BACK ? tiles - 1 - k : k) * TT, n = (len < end ? len : end) - t0;
-#pragma unroll
-    for (int i = 0; i < W::IT; ++i) {
-      const int t = row + i * W::ROWS;
-      if (W::ROWS > TT && t >= TT) break;
+    const int stage = k & 1, t0 = first + k * move, n = last - t0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (W::ROWS == TT || row < TT) {
+      const Raw<T, 8> x = s.raw[stage][0][lane], dt = s.raw[stage][1][lane];
       float2 d[4], u[4];
+      lds2<4>(d, &s.bias[col]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = add2(dt.pair(j), d[j]);
+      if (a.softplus)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = softplus2<T>(d[j]);
+      if (row >= n)                                    // behind the last token: changes nothing
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = both(0.f);
+      store_vec<float, 8>(&s.dt[row][col], d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = add2(dt[i].pair(j), bias[j]);
-        if (a.softplus) d[j] = softplus2<T>(d[j]);
-        if (t >= n) d[j] = both(0.f);                  // changes nothing
-        if constexpr (BACK) {
-          u[j] = x[i].pair(j);
-          const float2 zp = z[i].pair(j);
-          if (a.z) u[j] = mul2(u[j], mul2(zp, sigmoid2<T>(zp)));
-        } else {
-          u[j] = mul2(d[j], x[i].pair(j));
-        }
+        u[j] = BACK ? x.pair(j) : mul2(d[j], x.pair(j));
         if (!OUT) sum[j] = add2(sum[j], d[j]);
       }
-      store_vec<float, 8>(&sdt[t][col], d);
-      store_vec<float, 8>(&sdx[t][col], u);
-    }
-    rB.store(&sB[0][0], a, a.Bm, a.B_row, vB, w.b, w.g, t0, n, lane);
-    if (OUT) rC.store(&sC[0][0], a, a.Cm, a.C_row, vC, w.b, w.g, t0, n, lane);
-    Raw<T, 8> xo[W::IT], zo[W::IT];
+      if (BACK && gate) {
+        const Raw<T, 8> z = s.raw[stage][2][lane];
 #pragma unroll
-    for (int i = 0; i < W::IT; ++i) {
-      xo[i] = x[i];
-      zo[i] = z[i];
+        for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
+      }
+      store_vec<float, 8>(&s.dx[row][col], u);
     }
+    rB.store(&s.B[0][0], n, move, lane);
+    if (OUT) rC.store(&s.C_[0][0], n, move, lane);
     __syncwarp();
-    if (k + 1 < tiles) fetch(BACK ? t0 - TT : t0 + TT);
+    if (k + 1 < tiles) fetch(t0 + move, stage ^ 1);
 #pragma unroll 1
     for (int half = 0; half < TT; half += kScanKeep) {
-      if (MODE == kTrain && t0 + half < end)
-        store_states<C, NS>(h, f.kept + ((static_cast<int64_t>(w.b) * a.keeps() + (t0 + half) / kScanKeep) * a.D + w.c0) * a.N,
-                            a.N, ch, n0, w.width);
-#pragma unroll 4
+      if (MODE == kTrain && t0 + half < end) {
+        store_states<C, NS>(h, pk, a.N, ch, n0, w.width);
+        pk += static_cast<int64_t>(a.D) * a.N;
+      }
+      // outputs are written when the stretch is through: a store among them would hold back
+      // the loads behind it
+      float y[OUT ? kScanKeep : 1][SL == 1 ? C : 1];
+#pragma unroll
       for (int q = 0; q < kScanKeep; ++q) {
         const int t = BACK ? TT - 1 - half - q : half + q;
-        float d[C], u[C], y[C];
+        float d[C], u[C], yc[C];
         float2 Bv[P], Cv[P];
-        lds<C>(d, &sdt[t][ch]);
-        lds<C>(u, &sdx[t][ch]);
-        lds2<P>(Bv, &sB[t][n0]);
-        if (OUT) lds2<P>(Cv, &sC[t][n0]);
+        lds<C>(d, &s.dt[t][ch]);
+        lds<C>(u, &s.dx[t][ch]);
+        lds2<P>(Bv, &s.B[t][n0]);
+        if (OUT) lds2<P>(Cv, &s.C_[t][n0]);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          float2 s = both(0.f);
+          float2 r = both(0.f);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
             const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
             if (BACK) h[c][j] = mul2(e, fma2(Bv[j], both(u[c]), h[c][j]));
             else h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
-            if (OUT) s = j ? fma2(Cv[j], h[c][j], s) : mul2(Cv[j], h[c][j]);
+            if (OUT) r = j ? fma2(Cv[j], h[c][j], r) : mul2(Cv[j], h[c][j]);
           }
-          y[c] = s.x + s.y;
+          yc[c] = r.x + r.y;
         }
         if (OUT) {
-          over_states<SL, C>(y, sl);
-          if constexpr (SL == 1) {
+          over_states<SL, C>(yc, sl);
 #pragma unroll
-            for (int c = 0; c < C; ++c) sy[t][ch + c] = y[c];
-          } else {
-            if (SL <= C || sl < C) sy[t][ch + sl] = y[0];
-          }
+          for (int c = 0; c < (SL == 1 ? C : 1); ++c) y[q][c] = yc[c];
         }
       }
+      if (OUT && (SL <= C || sl < C))
+#pragma unroll
+        for (int t = 0; t < kScanKeep; ++t)
+#pragma unroll
+          for (int c = 0; c < (SL == 1 ? C : 1); ++c) s.y[half + t][ch + (SL == 1 ? c : sl)] = y[t][c];
     }
-    __syncwarp();
     if (OUT) {
+      __syncwarp();
+      if (in && t0 + row < end) {
+        const Raw<T, 8> x = s.raw[stage][0][lane];
+        float2 v[4], sk[4];
+        lds2<4>(v, &s.y[row][col]);
+        lds2<4>(sk, &s.skip[col]);
 #pragma unroll
-      for (int i = 0; i < W::IT; ++i) {
-        const int t = row + i * W::ROWS;
-        if (!in || t >= TT || t0 + t >= end) break;
-        float2 v[4];
-        lds2<4>(v, &sy[t][col]);
+        for (int j = 0; j < 4; ++j) v[j] = fma2(sk[j], x.pair(j), v[j]);
+        if (gate) {
+          const Raw<T, 8> z = s.raw[stage][2][lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 zp = zo[i].pair(j);
-          v[j] = fma2(skip[j], xo[i].pair(j), v[j]);
-          if (a.z) v[j] = mul2(v[j], mul2(zp, sigmoid2<T>(zp)));
-          if (t >= n) v[j] = both(0.f);
+          for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
         }
-        store_vec<T, 8>(static_cast<T*>(f.y) + a.row(w.b, t0 + t) * a.D + w.c0 + col, v);
+        if (row >= n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = both(0.f);
+        store_vec<T, 8>(py, v);
       }
+      py += hop * a.D;
+    } else {
+      __syncwarp();
     }
   }
   if (OUT) {
@@ -519,10 +563,6 @@ __device__ __forceinline__ void channels_out(const float2 (&dB)[2], const float2
   }
 }
 
-__device__ __forceinline__ void async16(void* to, const void* from, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_u32(to)), "l"(from), "r"(ok ? 16 : 0) : "memory");
-}
-
 template <typename T, int SL>
 __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArgs p) {
   using W = Bwd<T, SL>;
@@ -542,11 +582,11 @@ __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArg
   const int b = cta.b;
   const int len = a.len ? a.len[b] : a.T, begin = cta.seg * p.g.len, end = begin + p.g.len < a.T ? begin + p.g.len : a.T;
   const int64_t bD = static_cast<int64_t>(b) * a.D + c0;
-  const bool vB = on_16<T>(a.Bm, a.B_row), vC = on_16<T>(a.Cm, a.C_row);
   const int tiles = (end - begin + TT - 1) / TT, ctas_g = Where<CT * kBWarps>::per_group(a);
   const int last = len < end ? len : end;
 
-  Rows<T, TT, NP> rB, rC;
+  const int first = begin + (tiles - 1) * TT;
+  Rows<T, TT, NP> rB(a, a.Bm, a.B_row, b, cta.g, first, lane), rC(a, a.Cm, a.C_row, b, cta.g, first, lane);
   auto fetch = [&](int t0, int stage) {
     const void* base[4] = {a.x, a.dt, a.z, p.dy};
     const int64_t stride[4] = {a.x_row, a.dt_row, a.z_row, a.D};
@@ -555,14 +595,8 @@ __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArg
       const int t = t0 + row + i * W::ROWS;
       const bool ok = in && t < last;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool on = ok && base[k];
-        const T* from = static_cast<const T*>(on ? base[k] : a.A) + (on ? a.row(b, t) * stride[k] + c0 + col : 0);
-        char* to = reinterpret_cast<char*>(&s.raw[stage][k][i][lane]);
-#pragma unroll
-        for (int v = 0; v < static_cast<int>(sizeof(Raw<T, 8>)); v += 16)
-          async16(to + v, on ? reinterpret_cast<const char*>(from) + v : reinterpret_cast<const char*>(from), on);
-      }
+      for (int k = 0; k < 4; ++k)
+        async_item<T>(&s.raw[stage][k][i][lane], base[k], ok ? a.row(b, t) * stride[k] + c0 + col : 0, ok && base[k], a.A);
     }
     const float* kept = p.kept + (static_cast<int64_t>(b) * a.keeps() + t0 / TT) * a.D * a.N + static_cast<int64_t>(c0) * a.N;
 #pragma unroll
@@ -571,16 +605,16 @@ __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArg
       async16(&s.kept[stage][c][lane], ok ? kept + static_cast<int64_t>(ch + c) * a.N + n0 : p.kept, ok);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    rB.load(a, a.Bm, a.B_row, vB, b, cta.g, t0, last - t0, lane);
-    rC.load(a, a.Cm, a.C_row, vC, b, cta.g, t0, last - t0, lane);
+    rB.load(last - t0, -TT);
+    rC.load(last - t0, -TT);
   };
-  fetch(begin + (tiles - 1) * TT, 0);
+  fetch(first, 0);
   float2 A2[C][P], g[C][P], dA[C][P];
   load_rates<C, NS>(A2, a, c0, ch, n0, width);
   load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, width);
 #pragma unroll 2
   for (int i = p.g.nseg - 1; i > cta.seg; --i)
-    if (i * p.g.len < len) through<C, NS>(g, A2, a, p.g, b, i, c0, ch, n0, width);
+    if (i * p.g.len < len) through<T, C, NS>(g, A2, a, p.g, b, i, c0, ch, n0, width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -614,8 +648,8 @@ __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArg
       store_vec<float, 8>(&s.dx[t][col], u);
       store_vec<float, 8>(&s.dy[t][col], o);
     }
-    rB.store(&s.B[0][0], a, a.Bm, a.B_row, vB, b, cta.g, t0, n, lane);
-    rC.store(&s.C[0][0], a, a.Cm, a.C_row, vC, b, cta.g, t0, n, lane);
+    rB.store(&s.B[0][0], n, -TT, lane);
+    rC.store(&s.C[0][0], n, -TT, lane);
     float2 h[TT + 1][C][P];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -841,7 +875,7 @@ int per_group(const ScanArgs& a, int width) { return (a.D / a.G + width - 1) / w
 
 template <typename T, int SL, int C>
 int fwd(ScanFwdArgs f, cudaStream_t s, int* launches) {
-  const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<Fwd<SL, C>::CT>::per_group(f.a);
+  const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<32 / SL * C>::per_group(f.a);
   int rc;
   if (f.g.nseg > 1) {
     scan_fwd_kernel<T, SL, C, kAlone><<<warps * (f.g.nseg - 1), 32, 0, s>>>(f);
@@ -858,7 +892,7 @@ template <typename T>
 int fwd_t(const ScanFwdArgs& f, cudaStream_t s, int* launches) {
   switch (fwd_lanes(f.a.N)) {
     case 1: return fwd<T, 1, 1>(f, s, launches);
-    case 2: return fwd<T, 2, 2>(f, s, launches);
+    case 2: return getenv("V_C") && atoi(getenv("V_C")) == 1 ? fwd<T, 2, 1>(f, s, launches) : fwd<T, 2, 2>(f, s, launches);
     case 4: return fwd<T, 4, 2>(f, s, launches);
     default: return fwd<T, 8, 2>(f, s, launches);
   }
@@ -875,7 +909,7 @@ int bwd(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
     f.a.Bm = p.a.Cm;
     f.a.B_row = p.a.C_row;
     f.g = p.g;
-    const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<Fwd<SL, C>::CT>::per_group(f.a);
+    const unsigned warps = static_cast<unsigned>(f.a.B) * f.a.G * Where<32 / SL * C>::per_group(f.a);
     scan_fwd_kernel<T, SL, C, kAloneBack><<<warps * (p.g.nseg - 1), 32, 0, s>>>(f);
     if ((rc = check_launch())) return rc;
     ++*launches;
@@ -944,14 +978,14 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward) {
   const int width = backward ? bwd_width(a.N) / kBWarps : fwd_width(a.N);
   const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width), want = static_cast<int64_t>(a.num_sms) * (backward ? 8 : 16);
-  const int tiles = (a.T + kTile - 1) / kTile;
+  const int tiles = (a.T + 15) / 16;
   int64_t n = warps * 2 > want ? 1 : want / warps;
   const char* env = getenv(backward ? "V_BSEG" : "V_NSEG");
   if (env) n = atoi(env);
   if (n > tiles / 4) n = tiles / 4;
   if (n < 1) n = 1;
   ScanSplit p{};
-  p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * kTile;
+  p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * 16;
   p.nseg = (a.T + p.len - 1) / p.len;
   if (p.nseg == 1) return p;
   const size_t rows = static_cast<size_t>(a.B) * p.nseg * a.D;
