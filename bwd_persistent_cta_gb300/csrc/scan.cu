@@ -282,14 +282,14 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 #ifndef V_OCC
 #define V_OCC 12
 #endif
-constexpr int kFwdNS = 8;
+constexpr int kFwdNS = 8, kStretch = 8;
 enum { kInfer, kTrain, kAlone, kAloneBack };
 
 template <typename T, int SL, int C, bool OUT>
 struct Fwd {
   static constexpr int CL = 32 / SL, CT = CL * C, NP = SL * kFwdNS, P = kFwdNS / 2;
   static constexpr int VC = CT / 8, ROWS = 32 / VC, TT = ROWS < 16 ? ROWS : 16;     // an item a lane
-  static_assert(TT % kScanKeep == 0, "whole stretches between kept states");
+  static_assert(TT % kStretch == 0 && kStretch % kScanKeep == 0, "whole stretches, whole distances between kept states");
   static constexpr int LD = CT + 4;      // a row in shared memory: rows of a store on banks of their own
   static constexpr int AHEAD = 3;        // tiles on their way
   using R = Rows<T, TT, NP>;
@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
     for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<T, C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int j = 0; j < 4; ++j) sum[j] = both(0.f);
+  float* pu = MODE == kTrain && gate ? f.ungated + row0 * a.D + w.c0 + col : nullptr;
   T* py = static_cast<T*>(f.y) + row0 * a.D + w.c0 + col;
   float* pk = MODE == kTrain ? f.kept + ((static_cast<int64_t>(w.b) * a.keeps() + begin / kScanKeep) * a.D + w.c0) * a.N : nullptr;
   __syncwarp();
@@ -410,16 +411,16 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
     __syncwarp();
     fetch(k + W::AHEAD < tiles ? t0 + W::AHEAD * move : last, (k + W::AHEAD) % (W::AHEAD + 1));
 #pragma unroll 1
-    for (int half = 0; half < TT; half += kScanKeep) {
-      if (MODE == kTrain && t0 + half < end) {
-        store_states<C, NS>(h, pk, a.N, ch, n0, w.width);
-        pk += static_cast<int64_t>(a.D) * a.N;
-      }
+    for (int half = 0; half < TT; half += kStretch) {
       // outputs are written when the stretch is through: a store among them would hold back
       // the loads behind it
-      float y[OUT ? kScanKeep : 1][SL == 1 ? C : 1];
+      float y[OUT ? kStretch : 1][SL == 1 ? C : 1];
 #pragma unroll
-      for (int q = 0; q < kScanKeep; ++q) {
+      for (int q = 0; q < kStretch; ++q) {
+        if (MODE == kTrain && q % kScanKeep == 0 && t0 + half + q < end) {
+          store_states<C, NS>(h, pk, a.N, ch, n0, w.width);
+          pk += static_cast<int64_t>(a.D) * a.N;
+        }
         const int t = BACK ? TT - 1 - half - q : half + q;
         float d[C], u[C], yc[C];
         float2 Bv[P], Cv[P];
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
       }
       if (OUT && (SL <= C || sl < C))
 #pragma unroll
-        for (int t = 0; t < kScanKeep; ++t)
+        for (int t = 0; t < kStretch; ++t)
 #pragma unroll
           for (int c = 0; c < (SL == 1 ? C : 1); ++c) s.y[half + t][ch + (SL == 1 ? c : sl)] = y[t][c];
     }
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
         for (int j = 0; j < 4; ++j) v[j] = fma2(sk[j], x.pair(j), v[j]);
         if (gate) {
           const Raw<T, 8> z = s.raw[stage][2][lane];
+          if (MODE == kTrain) store_vec<float, 8>(pu, v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
         }
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
         store_vec<T, 8>(py, v);
       }
       py += hop * a.D;
+      if (MODE == kTrain) pu += hop * a.D;
     } else {
       __syncwarp();
     }
@@ -497,282 +500,335 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// A warp goes through its segment's tiles of eight tokens from the last to the first.  In
-// each it computes the tile's states again from the kept one, holds them in registers, and
-// runs the gradient g of the state back through the tile:
+// A warp goes through its segment from the last token to the first, four tokens at a time:
+// it computes their decays and states again from the kept one, holds them in registers, and runs the
+// gradient g of the state back through them:
 //     g += dy_t C_t;  dC_t += dy_t h_t;  dB_t += g delta_t x_t;  s1_t = sum g B_t
 //     g = a_t g;  P = g h_{t-1};  s2_t = sum P A;  dA += P delta_t
-// then, channel by channel, dx = delta s1 + D dy, ddelta = x s1 + s2, and dz from y, which
-// is computed again like the states.  Four channels and four states a lane: sums over the
-// states (of s1, s2 and y) and over the channels (of dB and dC) then take the fewest
-// exchanges together, one a state and token.  Inputs and the kept state of the next tile
-// are on their way into shared memory meanwhile.
-constexpr int kBT = kScanKeep, kBNS = 4, kBC = 4, kBWarps = 4;
+// then, channel by channel, dx = delta s1 + D dy, ddelta = x s1 + s2, and dz from y as the
+// forward kept it before the gate.  Four channels and four states a lane: sums over the
+// states (of s1 and s2) and over the channels (of dB and dC) then take the fewest
+// exchanges together.  Inputs and kept states of the next tile of eight tokens are on
+// their way into shared memory meanwhile.
+constexpr int kBT = 8, kBSub = kScanKeep, kBNS = 4, kBC = 4;
 
 template <typename T, int SL>
 struct Bwd {
   static constexpr int CL = 32 / SL, CT = CL * kBC, NP = SL * kBNS, P = kBNS / 2;
   static constexpr int VC = CT / 8, ROWS = 32 / VC, IT = kBT / ROWS > 0 ? kBT / ROWS : 1, LD = CT + 4;
-  struct Smem {                                  // of a warp
-    Raw<T, 8> raw[2][4][IT][32];                 // x, dt, z, dy of a lane's items
-    typename Rows<T, kBT, NP>::Stage rawB[2], rawC[2];
-    float4 kept[2][kBC][32];
-    float dt[kBT][LD], dx[kBT][LD], dy[kBT][LD], s1[kBT][LD], s2[kBT][LD], y[kBT][LD];
-    float B[kBT][NP], C[kBT][NP];
-    float4 acc[4][32];                           // a lane's sums for dD and the bias
-  };
-  float part[2][kBWarps][kBT][2 * NP];           // dB, dC of each warp
-  Smem w[kBWarps];
+  static constexpr int OS = SL == 2 ? 2 : 1;               // channels of a lane's sums over states
+  static constexpr int OC = CL >= 8 ? 1 : 8 / CL;          // states of a lane's sums over channels
+  Raw<T, 8> raw[2][4][IT][32];                   // x, dt, z, dy of a lane's items
+  Raw<float, 8> y[2][IT][32];
+  typename Rows<T, kBT, NP>::Stage rawB[2], rawC[2];
+  float4 kept[2][kBT / kBSub][kBC][32];
+  float bias[CT], skip[CT];
+  float dt[kBT][LD], dx[kBT][LD], dy[kBT][LD], sg[kBT][LD], s1[kBT][LD], s2[kBT][LD];
+  float B[kBT][NP], C[kBT][NP];
+  float4 acc[4][32];                             // a lane's sums for dD and the bias
 };
 
-// Sums four values over the SL state lanes and writes them, channel by channel.
+// Sums four values over the SL state lanes: lane sl < 4 ends up with that of channel
+// 2 (sl & 1) + (sl >> 1), or, where SL is two, with two of them.
 template <int SL>
-__device__ __forceinline__ void states_out(const float2 (&a)[2], float* to, int sl) {
+__device__ __forceinline__ void sum_states(const float2 (&a)[2], int sl, float (&r)[SL == 2 ? 2 : 1]) {
   constexpr int CL = 32 / SL;
   const bool up = sl & 1;
   float v = (up ? a[1].x : a[0].x) + __shfl_xor_sync(kFull, up ? a[0].x : a[1].x, CL);
-  float u = (up ? a[1].y : a[0].y) + __shfl_xor_sync(kFull, up ? a[0].y : a[1].y, CL);
+  const float u = (up ? a[1].y : a[0].y) + __shfl_xor_sync(kFull, up ? a[0].y : a[1].y, CL);
   if constexpr (SL == 2) {
-    *reinterpret_cast<float2*>(to + 2 * (sl & 1)) = make_float2(v, u);
+    r[0] = v;
+    r[1] = u;
   } else {
     const bool odd = sl & 2;
     v = (odd ? u : v) + __shfl_xor_sync(kFull, odd ? v : u, 2 * CL);
 #pragma unroll
     for (int m = 4 * CL; m < 32; m *= 2) v += __shfl_xor_sync(kFull, v, m);
-    if (SL == 4 || sl < 4) to[2 * (sl & 1) + ((sl >> 1) & 1)] = v;
+    r[0] = v;
   }
 }
-
-// Sums dB and dC (four states each) over the CL channel lanes and writes them.
-template <int CL, int NP>
-__device__ __forceinline__ void channels_out(const float2 (&dB)[2], const float2 (&dC)[2], float* to, int cl) {
+// Sums dB and dC (four states each) over the CL channel lanes: lane cl ends up with OC
+// states of one of them.
+template <int CL, int OC>
+__device__ __forceinline__ void sum_channels(const float2 (&dB)[2], const float2 (&dC)[2], int cl, float (&r)[OC]) {
   const bool up = cl & 1;
   float v[4];
   const float b[4] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y}, c[4] = {dC[0].x, dC[0].y, dC[1].x, dC[1].y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = (up ? c[i] : b[i]) + __shfl_xor_sync(kFull, up ? b[i] : c[i], 1);
-  to += up ? NP : 0;
-  if constexpr (CL == 2) {
-    *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
+  if constexpr (CL > 2) {
     const bool hi = cl & 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) v[i] = (hi ? v[i + 2] : v[i]) + __shfl_xor_sync(kFull, hi ? v[i] : v[i + 2], 2);
-    to += hi ? 2 : 0;
-    if constexpr (CL == 4) {
-      *reinterpret_cast<float2*>(to) = make_float2(v[0], v[1]);
-    } else {
-      const bool top = cl & 4;
-      v[0] = (top ? v[1] : v[0]) + __shfl_xor_sync(kFull, top ? v[0] : v[1], 4);
-#pragma unroll
-      for (int m = 8; m < CL; m *= 2) v[0] += __shfl_xor_sync(kFull, v[0], m);
-      if (CL == 8 || cl < 8) to[top ? 1 : 0] = v[0];
-    }
   }
+  if constexpr (CL > 4) {
+    const bool top = cl & 4;
+    v[0] = (top ? v[1] : v[0]) + __shfl_xor_sync(kFull, top ? v[0] : v[1], 4);
+#pragma unroll
+    for (int m = 8; m < CL; m *= 2) v[0] += __shfl_xor_sync(kFull, v[0], m);
+  }
+#pragma unroll
+  for (int i = 0; i < OC; ++i) r[i] = v[i];
 }
 
 template <typename T, int SL>
-__global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArgs p) {
+__global__ void __launch_bounds__(32) scan_bwd_kernel(const ScanBwdArgs p) {
   using W = Bwd<T, SL>;
   constexpr int CT = W::CT, NP = W::NP, P = W::P, C = kBC, NS = kBNS, TT = kBT, CL = W::CL;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  W& all = *reinterpret_cast<W*>(smem_raw);
+  __shared__ __align__(16) W s;
   const ScanArgs& a = p.a;
   const rnn_scan_grad_t& out = p.grad;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  typename W::Smem& s = all.w[warp];
-  // a CTA's warps have neighbouring channels of one group; those beyond it have none
-  const Where<CT * kBWarps> cta(a, p.g.nseg, blockIdx.x);
-  const int c0 = cta.c0 + warp * CT, width = cta.width - warp * CT < CT ? cta.width - warp * CT : CT;   // may be <= 0
+  const int lane = threadIdx.x;
+  const Where<CT> w(a, p.g.nseg, blockIdx.x);
   const int cl = lane % CL, sl = lane / CL, ch = cl * C, n0 = sl * NS;
   const int row = lane / W::VC, col = lane % W::VC * 8;
-  const bool in = col < width && row < TT;
-  const int b = cta.b;
-  const int len = a.len ? a.len[b] : a.T, begin = cta.seg * p.g.len, end = begin + p.g.len < a.T ? begin + p.g.len : a.T;
-  const int64_t bD = static_cast<int64_t>(b) * a.D + c0;
-  const int tiles = (end - begin + TT - 1) / TT, ctas_g = Where<CT * kBWarps>::per_group(a);
-  const int last = len < end ? len : end;
+  const bool in = col < w.width && row < TT, gate = a.z != nullptr;
+  const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * p.g.len, end = begin + p.g.len < a.T ? begin + p.g.len : a.T;
+  const int64_t bD = static_cast<int64_t>(w.b) * a.D + w.c0;
+  const int tiles = (end - begin + TT - 1) / TT;
+  const int last = len < end ? len : end, first = begin + (tiles - 1) * TT;
 
-  const int first = begin + (tiles - 1) * TT;
-  Rows<T, TT, NP> rB(a, a.Bm, a.B_row, b, cta.g, first, lane), rC(a, a.Cm, a.C_row, b, cta.g, first, lane);
+  // where the lane's items of the tile to come lie, and a token's distance
+  const int64_t hop = a.bfirst ? 1 : a.B, row0 = a.row(w.b, first + row);
+  const T *px = static_cast<const T*>(a.x) + row0 * a.x_row + w.c0 + col, *pdt = static_cast<const T*>(a.dt) + row0 * a.dt_row + w.c0 + col,
+          *pz = static_cast<const T*>(a.z) + row0 * a.z_row + w.c0 + col, *pdy = static_cast<const T*>(p.dy) + row0 * a.D + w.c0 + col;
+  const float* py = p.ungated + row0 * a.D + w.c0 + col;
+  const int64_t DN = static_cast<int64_t>(a.D) * a.N;
+  const float* pk = p.kept + (static_cast<int64_t>(w.b) * a.keeps() + first / kBSub) * DN + static_cast<int64_t>(w.c0 + ch) * a.N + n0;
+  Rows<T, TT, NP> rB(a, a.Bm, a.B_row, w.b, w.g, first, lane), rC(a, a.Cm, a.C_row, w.b, w.g, first, lane);
   auto fetch = [&](int t0, int stage) {
-    const void* base[4] = {a.x, a.dt, a.z, p.dy};
-    const int64_t stride[4] = {a.x_row, a.dt_row, a.z_row, a.D};
 #pragma unroll
     for (int i = 0; i < W::IT; ++i) {
-      const int t = t0 + row + i * W::ROWS;
-      const bool ok = in && t < last;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        async_item<T>(&s.raw[stage][k][i][lane], base[k], ok ? a.row(b, t) * stride[k] + c0 + col : 0, ok && base[k], a.A);
+      const bool ok = in && t0 + row + i * W::ROWS < last;
+      const int64_t r = i * W::ROWS * hop;
+      async_item<T>(&s.raw[stage][0][i][lane], px, r * a.x_row, ok, a.A);
+      async_item<T>(&s.raw[stage][1][i][lane], pdt, r * a.dt_row, ok, a.A);
+      async_item<T>(&s.raw[stage][3][i][lane], pdy, r * a.D, ok, a.A);
+      if (gate) {
+        async_item<T>(&s.raw[stage][2][i][lane], pz, r * a.z_row, ok, a.A);
+        async_item<float>(&s.y[stage][i][lane], py, r * a.D, ok, a.A);
+      }
     }
-    const float* kept = p.kept + (static_cast<int64_t>(b) * a.keeps() + t0 / TT) * a.D * a.N + static_cast<int64_t>(c0) * a.N;
+    px -= TT * hop * a.x_row;
+    pdt -= TT * hop * a.dt_row;
+    pz -= TT * hop * a.z_row;
+    pdy -= TT * hop * a.D;
+    py -= TT * hop * a.D;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const bool ok = ch + c < width && n0 < a.N;
-      async16(&s.kept[stage][c][lane], ok ? kept + static_cast<int64_t>(ch + c) * a.N + n0 : p.kept, ok);
+    for (int q = 0; q < TT / kBSub; ++q) {
+      const float* from = pk + q * DN;
+      const bool on = n0 < a.N && t0 + q * kBSub < end;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const bool ok = on && ch + c < w.width;
+        async16(&s.kept[stage][q][c][lane], ok ? from : a.A, ok);
+        from += a.N;
+      }
     }
+    pk -= TT / kBSub * DN;
     rB.load(s.rawB[stage], last - t0, -TT, lane, a.A);
     rC.load(s.rawC[stage], last - t0, -TT, lane, a.A);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   fetch(first, 0);
+  for (int c = lane; c < CT; c += 32) {
+    s.bias[c] = a.bias && c < w.width ? a.bias[w.c0 + c] : 0.f;
+    s.skip[c] = a.skip && c < w.width ? a.skip[w.c0 + c] : 0.f;
+  }
   float2 A2[C][P], g[C][P], dA[C][P];
-  load_rates<C, NS>(A2, a, c0, ch, n0, width);
-  load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, width);
+  load_rates<C, NS>(A2, a, w.c0, ch, n0, w.width);
+  load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
 #pragma unroll 2
-  for (int i = p.g.nseg - 1; i > cta.seg; --i)
-    if (i * p.g.len < len) through<T, C, NS>(g, A2, a, p.g, b, i, c0, ch, n0, width);
+  for (int i = p.g.nseg - 1; i > w.seg; --i)
+    if (i * p.g.len < len) through<T, C, NS>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < P; ++j) dA[c][j] = both(0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) s.acc[i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto vec = [&](const float* from, int j) {
-    return in && from ? *reinterpret_cast<const float2*>(from + c0 + col + 2 * j) : both(0.f);
-  };
+  // a token's sums over the warp's channels go to memory as they are
+  const int on = CL >= 8 ? (cl & 1) * NP + (cl & 2) + ((cl >> 2) & 1) : CL == 4 ? (cl & 1) * NP + (cl & 2) : cl * NP;
+  const int64_t bc_token = static_cast<int64_t>(a.G) * Where<CT>::per_group(a) * (2 * NP);
+  float* pbc = p.bc + (static_cast<int64_t>(w.b) * a.T + first) * bc_token +
+               (static_cast<int64_t>(w.g) * Where<CT>::per_group(a) + w.tile) * (2 * NP) + n0 + on;
+  int64_t po = row0 * a.D + w.c0 + col;
+  __syncwarp();
 
   for (int k = 0; k < tiles; ++k) {
-    const int stage = k & 1, t0 = begin + (tiles - 1 - k) * TT, n = last - t0;
+    const int stage = k & 1, t0 = first - k * TT, n = last - t0;
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < W::IT; ++i) {
       const int t = row + i * W::ROWS;
       if (W::ROWS > TT && t >= TT) break;
-      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], z = s.raw[stage][2][i][lane],
-                      dy = s.raw[stage][3][i][lane];
+      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], dy = s.raw[stage][3][i][lane];
       float2 d[4], u[4], o[4];
+      lds2<4>(d, &s.bias[col]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = add2(dt.pair(j), d[j]);
+      if (a.softplus)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = softplus2<T>(d[j]);
+      if (t >= n)                                      // behind the last token: changes nothing
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = both(0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = add2(dt.pair(j), vec(a.bias, j));
-        if (a.softplus) d[j] = softplus2<T>(d[j]);
-        if (t >= n) d[j] = both(0.f);                  // changes nothing
         u[j] = mul2(d[j], x.pair(j));
         o[j] = dy.pair(j);
-        if (a.z) o[j] = mul2(o[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
       }
       store_vec<float, 8>(&s.dt[t][col], d);
       store_vec<float, 8>(&s.dx[t][col], u);
+      if (gate) {
+        const Raw<T, 8> z = s.raw[stage][2][i][lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[j] = sigmoid2<T>(z.pair(j));
+          o[j] = mul2(o[j], mul2(z.pair(j), d[j]));
+        }
+        store_vec<float, 8>(&s.sg[t][col], d);
+      }
       store_vec<float, 8>(&s.dy[t][col], o);
     }
     rB.store(&s.B[0][0], s.rawB[stage], n, -TT, lane);
     rC.store(&s.C[0][0], s.rawC[stage], n, -TT, lane);
-    float2 h[TT + 1][C][P];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float4 q = s.kept[stage][c][lane];
-      h[0][c][0] = make_float2(q.x, q.y);
-      h[0][c][1] = make_float2(q.z, q.w);
-    }
     __syncwarp();
     if (k + 1 < tiles) fetch(t0 - TT, stage ^ 1);
-    // the states of the tile, again
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      float d[C], u[C];
-      float2 Bv[P];
-      lds<C>(d, &s.dt[t][ch]);
-      lds<C>(u, &s.dx[t][ch]);
-      lds2<P>(Bv, &s.B[t][n0]);
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-          h[t + 1][c][j] = fma2(decay2<T>(step2<T>(A2[c][j], d[c])), h[t][c][j], mul2(Bv[j], both(u[c])));
-    }
-    // the decays are computed again below: kept, they would take twice the states' registers
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
-      float d[C], u[C], o[C];
-      float2 Bv[P], Cv[P], dB[P], dC[P], s1[C / 2], s2[C / 2], yy[C / 2];
-      lds<C>(d, &s.dt[t][ch]);
-      lds<C>(u, &s.dx[t][ch]);
-      lds<C>(o, &s.dy[t][ch]);
-      lds2<P>(Bv, &s.B[t][n0]);
-      lds2<P>(Cv, &s.C[t][n0]);
+#pragma unroll 1
+    for (int q0 = TT - kBSub; q0 >= 0; q0 -= kBSub) {
+      // the states of these tokens, again
+      float2 h[kBSub + 1][C][P];
+      float2 e[kBSub][C][P];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float2 q1, q2, q3;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
-          g[c][j] = fma2(Cv[j], both(o[c]), g[c][j]);
-          dC[j] = c ? fma2(h[t + 1][c][j], both(o[c]), dC[j]) : mul2(h[t + 1][c][j], both(o[c]));
-          q3 = j ? fma2(h[t + 1][c][j], Cv[j], q3) : mul2(h[t + 1][c][j], Cv[j]);
-          dB[j] = c ? fma2(g[c][j], both(u[c]), dB[j]) : mul2(g[c][j], both(u[c]));
-          q1 = j ? fma2(g[c][j], Bv[j], q1) : mul2(g[c][j], Bv[j]);
-          g[c][j] = mul2(e, g[c][j]);
-          const float2 r = mul2(g[c][j], h[t][c][j]);
-          q2 = j ? fma2(r, A2[c][j], q2) : mul2(r, A2[c][j]);
-          dA[c][j] = fma2(r, both(d[c]), dA[c][j]);
-        }
-        (c & 1 ? s1[c / 2].y : s1[c / 2].x) = q1.x + q1.y;
-        (c & 1 ? s2[c / 2].y : s2[c / 2].x) = q2.x + q2.y;
-        (c & 1 ? yy[c / 2].y : yy[c / 2].x) = q3.x + q3.y;
+        const float4 q = s.kept[stage][q0 / kBSub][c][lane];
+        h[0][c][0] = make_float2(q.x, q.y);
+        h[0][c][1] = make_float2(q.z, q.w);
       }
-      states_out<SL>(s1, &s.s1[t][ch], sl);
-      states_out<SL>(s2, &s.s2[t][ch], sl);
-      states_out<SL>(yy, &s.y[t][ch], sl);
-      channels_out<CL, NP>(dB, dC, &all.part[stage][warp][t][n0], cl);
+#pragma unroll
+      for (int q = 0; q < kBSub; ++q) {
+        float d[C], u[C];
+        float2 Bv[P];
+        lds<C>(d, &s.dt[q0 + q][ch]);
+        lds<C>(u, &s.dx[q0 + q][ch]);
+        lds2<P>(Bv, &s.B[q0 + q][n0]);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            e[q][c][j] = decay2<T>(step2<T>(A2[c][j], d[c]));
+            h[q + 1][c][j] = fma2(e[q][c][j], h[q][c][j], mul2(Bv[j], both(u[c])));
+          }
+      }
+      // sums are written when the tokens are through: a store among them would hold back the
+      // loads behind it
+      float o1[kBSub][W::OS], o2[kBSub][W::OS], oc[kBSub][W::OC];
+#pragma unroll
+      for (int q = kBSub - 1; q >= 0; --q) {
+        const int t = q0 + q;
+        float d[C], u[C], o[C];
+        float2 Bv[P], Cv[P], dB[P], dC[P], s1[C / 2], s2[C / 2];
+        lds<C>(d, &s.dt[t][ch]);
+        lds<C>(u, &s.dx[t][ch]);
+        lds<C>(o, &s.dy[t][ch]);
+        lds2<P>(Bv, &s.B[t][n0]);
+        lds2<P>(Cv, &s.C[t][n0]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float2 q1, q2;
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            g[c][j] = fma2(Cv[j], both(o[c]), g[c][j]);
+            dC[j] = c ? fma2(h[q + 1][c][j], both(o[c]), dC[j]) : mul2(h[q + 1][c][j], both(o[c]));
+            dB[j] = c ? fma2(g[c][j], both(u[c]), dB[j]) : mul2(g[c][j], both(u[c]));
+            q1 = j ? fma2(g[c][j], Bv[j], q1) : mul2(g[c][j], Bv[j]);
+            g[c][j] = mul2(e[q][c][j], g[c][j]);
+            const float2 r = mul2(g[c][j], h[q][c][j]);
+            q2 = j ? fma2(r, A2[c][j], q2) : mul2(r, A2[c][j]);
+            dA[c][j] = fma2(r, both(d[c]), dA[c][j]);
+          }
+          (c & 1 ? s1[c / 2].y : s1[c / 2].x) = q1.x + q1.y;
+          (c & 1 ? s2[c / 2].y : s2[c / 2].x) = q2.x + q2.y;
+        }
+        sum_states<SL>(s1, sl, o1[q]);
+        sum_states<SL>(s2, sl, o2[q]);
+        sum_channels<CL, W::OC>(dB, dC, cl, oc[q]);
+      }
+      const int och = ch + (SL == 2 ? 2 * sl : 2 * (sl & 1) + ((sl >> 1) & 1));
+      float* to = pbc + q0 * bc_token;
+#pragma unroll
+      for (int q = 0; q < kBSub; ++q) {
+        if (SL <= 4 || sl < 4)
+#pragma unroll
+          for (int i = 0; i < W::OS; ++i) {
+            s.s1[q0 + q][och + i] = o1[q][i];
+            s.s2[q0 + q][och + i] = o2[q][i];
+          }
+        if (p.bc && (CL <= 8 || cl < 8) && t0 + q0 + q < end)
+#pragma unroll
+          for (int i = 0; i < W::OC; ++i) to[i] = q0 + q < n ? oc[q][i] : 0.f;
+        to += bc_token;
+      }
     }
+    pbc -= TT * bc_token;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < W::IT; ++i) {
       const int t = row + i * W::ROWS;
       if (!in || t >= TT || t0 + t >= end) break;
-      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], z = s.raw[stage][2][i][lane],
-                      dy = s.raw[stage][3][i][lane];
-      float2 vx[4], vt[4], vz[4], d[4], o[4], q1[4], q2[4], q3[4];
-      lds2<4>(d, &s.dt[t][col]);
+      const Raw<T, 8> x = s.raw[stage][0][i][lane], dt = s.raw[stage][1][i][lane], dy = s.raw[stage][3][i][lane];
+      const int64_t at = po + i * W::ROWS * hop * a.D;
+      float2 v[4], o[4], q1[4], r[4];
       lds2<4>(o, &s.dy[t][col]);
       lds2<4>(q1, &s.s1[t][col]);
-      lds2<4>(q2, &s.s2[t][col]);
-      lds2<4>(q3, &s.y[t][col]);
-      const bool live = t < n;
+      lds2<4>(v, &s.dt[t][col]);
+      lds2<4>(r, &s.skip[col]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = t < n ? fma2(v[j], q1[j], mul2(r[j], o[j])) : both(0.f);
+      if (out.dx) store_vec<T, 8>(static_cast<T*>(out.dx) + at, v);
+      lds2<4>(v, &s.s2[t][col]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fma2(x.pair(j), q1[j], mul2(v[j], both(kLn2)));
+      if (a.softplus) {
+        lds2<4>(r, &s.bias[col]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], sigmoid2<T>(add2(dt.pair(j), r[j])));
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 xp = x.pair(j), zp = z.pair(j), sk = vec(a.skip, j);
-        vx[j] = fma2(d[j], q1[j], mul2(sk, o[j]));
-        vt[j] = fma2(xp, q1[j], mul2(q2[j], both(kLn2)));
-        if (a.softplus) vt[j] = mul2(vt[j], sigmoid2<T>(add2(dt.pair(j), vec(a.bias, j))));
-        const float2 sg = sigmoid2<T>(zp), yv = fma2(sk, xp, q3[j]);
-        // sigma + z sigma (1 - sigma)
-        vz[j] = mul2(mul2(dy.pair(j), yv), fma2(mul2(zp, sg), make_float2(1.f - sg.x, 1.f - sg.y), sg));
-        if (!live) vx[j] = vt[j] = vz[j] = both(0.f);
-        q3[j] = live ? mul2(o[j], xp) : both(0.f);
+        v[j] = t < n ? v[j] : both(0.f);
+        o[j] = t < n ? mul2(o[j], x.pair(j)) : both(0.f);
       }
+      if (out.ddt) store_vec<T, 8>(static_cast<T*>(out.ddt) + at, v);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float4 q = s.acc[j][lane];
-        s.acc[j][lane] = make_float4(q.x + q3[2 * j].x, q.y + q3[2 * j].y, q.z + q3[2 * j + 1].x, q.w + q3[2 * j + 1].y);
+        s.acc[j][lane] = make_float4(q.x + o[2 * j].x, q.y + o[2 * j].y, q.z + o[2 * j + 1].x, q.w + o[2 * j + 1].y);
         q = s.acc[2 + j][lane];
-        s.acc[2 + j][lane] = make_float4(q.x + vt[2 * j].x, q.y + vt[2 * j].y, q.z + vt[2 * j + 1].x, q.w + vt[2 * j + 1].y);
+        s.acc[2 + j][lane] = make_float4(q.x + v[2 * j].x, q.y + v[2 * j].y, q.z + v[2 * j + 1].x, q.w + v[2 * j + 1].y);
       }
-      const int64_t at = a.row(b, t0 + t) * a.D + c0 + col;
-      if (out.dx) store_vec<T, 8>(static_cast<T*>(out.dx) + at, vx);
-      if (out.ddt) store_vec<T, 8>(static_cast<T*>(out.ddt) + at, vt);
-      if (out.dz) store_vec<T, 8>(static_cast<T*>(out.dz) + at, vz);
-    }
-    if (p.bc) {
-      __syncthreads();                           // the other stage of part is free until the next one
-      for (int e = threadIdx.x; e < TT * 2 * NP; e += 32 * kBWarps) {
-        const int t = e / (2 * NP), q = e % (2 * NP);
-        if (t0 + t >= end) break;
-        float v = 0.f;
+      if (gate && out.dz) {
+        const Raw<T, 8> z = s.raw[stage][2][i][lane];
+        const Raw<float, 8> y = s.y[stage][i][lane];
+        lds2<4>(r, &s.sg[t][col]);
 #pragma unroll
-        for (int i = 0; i < kBWarps; ++i) v += all.part[stage][i][t][q];
-        p.bc[(((static_cast<int64_t>(b) * a.T + t0 + t) * a.G + cta.g) * ctas_g + cta.tile) * (2 * NP) + q] = t < n ? v : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          // sigma + z sigma (1 - sigma)
+          v[j] = mul2(mul2(dy.pair(j), y.pair(j)), fma2(mul2(z.pair(j), r[j]), make_float2(1.f - r[j].x, 1.f - r[j].y), r[j]));
+          if (t >= n) v[j] = both(0.f);
+        }
+        store_vec<T, 8>(static_cast<T*>(out.dz) + at, v);
       }
     }
+    po -= TT * hop * a.D;
   }
-  if (out.dh0 && begin == 0) store_states<C, NS>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, width);
-  const int64_t at = (static_cast<int64_t>(b) * p.g.nseg + cta.seg) * a.D + c0;
-  if (p.pA) store_states<C, NS>(dA, p.pA + at * a.N, a.N, ch, n0, width);
+  if (out.dh0 && begin == 0) store_states<C, NS>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, w.width);
+  const int64_t at = (static_cast<int64_t>(w.b) * p.g.nseg + w.seg) * a.D + w.c0;
+  if (p.pA) store_states<C, NS>(dA, p.pA + at * a.N, a.N, ch, n0, w.width);
   // the rows' sums, in order
   __syncwarp();
-  for (int c = lane; c < width; c += 32) {
+  for (int c = lane; c < w.width; c += 32) {
     float v = 0.f, u = 0.f;
     for (int r = 0; r < W::ROWS && r < TT; ++r) {
       const int l = r * W::VC + c / 8;
@@ -784,7 +840,7 @@ __global__ void __launch_bounds__(32 * kBWarps) scan_bwd_kernel(const ScanBwdArg
   }
 }
 
-// dB and dC: the sum over a group's CTAs, in order, four states a thread.
+// dB and dC: the sum over a group's warps, in order, four states a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int ctas, int NP, T* dB, T* dC) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.G, all = rows * (NP / 2);
@@ -878,7 +934,7 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 // Lanes a channel: eight states each forward, four backward, rounded up to a power of two.
 int fwd_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
 int fwd_width(int N) { return N <= 8 ? 32 : 2 * 32 / fwd_lanes(N); }      // channels a warp
-int bwd_width(int N) { return kBWarps * kBC * 16 / fwd_lanes(N); }         // channels a CTA
+int bwd_width(int N) { return kBC * 16 / fwd_lanes(N); }
 int per_group(const ScanArgs& a, int width) { return (a.D / a.G + width - 1) / width; }
 
 template <typename T, int SL, int C>
@@ -922,12 +978,9 @@ int bwd(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
     if ((rc = check_launch())) return rc;
     ++*launches;
   }
-  constexpr int smem = sizeof(Bwd<T, 2 * SL>);
-  static_assert(smem <= 227 * 1024, "a CTA's tiles fit");
-  if (cudaFuncSetAttribute(scan_bwd_kernel<T, 2 * SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return RNN_CUDA_ERROR;
-  const unsigned ctas = static_cast<unsigned>(p.a.B) * p.a.G * Where<Bwd<T, 2 * SL>::CT * kBWarps>::per_group(p.a);
-  scan_bwd_kernel<T, 2 * SL><<<ctas * p.g.nseg, 32 * kBWarps, smem, s>>>(p);
+  static_assert(sizeof(Bwd<T, 2 * SL>) <= 48 * 1024, "a warp's tiles fit");
+  const unsigned warps = static_cast<unsigned>(p.a.B) * p.a.G * Where<Bwd<T, 2 * SL>::CT>::per_group(p.a);
+  scan_bwd_kernel<T, 2 * SL><<<warps * p.g.nseg, 32, 0, s>>>(p);
   if (!(rc = check_launch())) ++*launches;
   return rc;
 }
@@ -984,7 +1037,7 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 }  // namespace
 
 ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward) {
-  const int width = backward ? bwd_width(a.N) / kBWarps : fwd_width(a.N);
+  const int width = backward ? bwd_width(a.N) : fwd_width(a.N);
   const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width), want = static_cast<int64_t>(a.num_sms) * (backward ? 8 : 16);
   const int tiles = (a.T + 15) / 16;
   int64_t n = warps * 2 > want ? 1 : want / warps;
@@ -1001,6 +1054,13 @@ ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward) {
   p.first = p.sums + up(rows * 4);
   p.bytes = p.first + (backward ? 0 : up(static_cast<size_t>(a.B) * a.D * a.N * 4));
   return p;
+}
+
+ScanReserve scan_reserve(const ScanArgs& a) {
+  ScanReserve r{};
+  r.ungated = up(static_cast<size_t>(a.B) * a.keeps() * a.D * a.N * 4);
+  r.bytes = r.ungated + up(static_cast<size_t>(a.B) * a.T * a.D * 4);
+  return r;
 }
 
 int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStream_t s, int* launches) {

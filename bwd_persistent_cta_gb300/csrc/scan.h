@@ -10,7 +10,7 @@
 namespace rnn {
 
 // Tokens between the states that a training forward keeps.
-constexpr int kScanKeep = 8;
+constexpr int kScanKeep = 4;
 
 struct ScanArgs {
   int B, T, D, N, G;
@@ -44,12 +44,19 @@ struct ScanSegs {
   float *ends, *sums;
 };
 
+// The reserve: what a training forward keeps.
+struct ScanReserve {
+  size_t kept, ungated, bytes;
+};
+ScanReserve scan_reserve(const ScanArgs& a);
+
 struct ScanFwdArgs {
   ScanArgs a;
   const float* h0;             // or null
   float* hT;                   // or null
   void* y;
   float* kept;                 // [B][keep][D][N] the state before every kScanKeep tokens, or null
+  float* ungated;              // [rows][D] y before its gate, or null
   ScanSegs g;
   float* first;                // where the first segment copies h0 to, or null
 };
@@ -66,7 +73,7 @@ struct ScanBwdArgs {
   ScanArgs a;
   const void* dy;
   const float* dhT;            // or null
-  const float* kept;
+  const float *kept, *ungated;
   rnn_scan_grad_t grad;
   char* work;
   ScanSegs g;

@@ -192,7 +192,7 @@ rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* out) {
   const ScanArgs a = scan_shape(h);
   h->workspace_bytes = scan_split(a, h->bf16, 0).bytes;
   h->bwd_workspace_bytes = scan_bwd_layout(a, h->bf16).bytes;
-  h->reserve_bytes = al(static_cast<size_t>(a.B) * a.keeps() * a.D * a.N * 4);
+  h->reserve_bytes = scan_reserve(a).bytes;
   *out = h;
   return RNN_OK;
 }
@@ -236,7 +236,10 @@ rnn_status_t rnn_scan_forward(rnn_scan_t h, const rnn_scan_in_t* in, const float
   f.h0 = h0;
   f.hT = hT;
   f.y = y;
-  f.kept = static_cast<float*>(reserve);
+  if (reserve) {
+    f.kept = at<float>(reserve, scan_reserve(f.a).kept);
+    f.ungated = f.a.z ? at<float>(reserve, scan_reserve(f.a).ungated) : nullptr;
+  }
   int n = 0;
   const int e = launch_scan_forward(f, workspace, h->bf16, s, &n);
   h->launches += n;
@@ -261,7 +264,8 @@ rnn_status_t rnn_scan_backward(rnn_scan_t h, const rnn_scan_in_t* in, const void
   if (call.rc != RNN_OK) return call.rc;
   b.dy = dy;
   b.dhT = dhT;
-  b.kept = static_cast<const float*>(reserve);
+  b.kept = at<float>(reserve, scan_reserve(b.a).kept);
+  b.ungated = at<float>(reserve, scan_reserve(b.a).ungated);
   b.grad = *grad;
   b.work = static_cast<char*>(workspace);
   int n = 0;
