@@ -31,18 +31,22 @@ struct Share {
   int64_t begin, end;          // elements
 };
 
-// Sums of squares of a few values.  Where fp32 would lose them (a sum above 2^100, or
-// so small that squares may have gone below the normal range) they are taken again in
-// 64 bits.
+// The sum of squares of a few values.  Where fp32 would lose it (above 2^100, or so small
+// that squares may have gone below the normal range) it is taken again in 64 bits.
 template <int N>
 __device__ __forceinline__ double squares(const float2 (&v)[N]) {
-  float2 q = both(0.f);
+  float2 q[2] = {both(0.f), both(0.f)};
 #pragma unroll
-  for (int i = 0; i < N; ++i) q = fma2(v[i], v[i], q);
-  const float s = q.x + q.y;
+  for (int i = 0; i < N; ++i) q[i & 1] = fma2(v[i], v[i], q[i & 1]);
+  const float2 p = add2(q[0], q[1]);
+  const float s = p.x + p.y;
   if (s >= 0x1p-80f && s <= 0x1p100f) return s;
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) most = fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+  if (most == 0.f && s == 0.f) return 0.0;               // gradients of rows that were not used
   double d = 0.0;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < N; ++i) d += static_cast<double>(v[i].x) * v[i].x + static_cast<double>(v[i].y) * v[i].y;
   return d;
 }
@@ -81,8 +85,20 @@ __device__ __forceinline__ double part_squares(const T* p, int64_t n) {
     const float2 one[1] = {make_float2(to_f(p[tail + tid]), 0.f)};
     sum += squares(one);
   }
-#pragma unroll 4
-  for (int64_t i = tid; i < vecs; i += kThreads) {
+  constexpr int U = 4;                     // vectors in flight
+  int64_t i = tid;
+  for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
+    Raw<T, V> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u].load(p + head + (i + u * kThreads) * V);
+    float2 v[U * V / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) v[u * V / 2 + j] = r[u].pair(j);
+    sum += squares(v);
+  }
+  for (; i < vecs; i += kThreads) {
     Raw<T, V> r;
     r.load(p + head + i * V);
     float2 v[V / 2];
@@ -145,8 +161,21 @@ __device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, float f)
   const int tid = threadIdx.x;
   if (tid < head) o[tid] = from_f<T>(to_f(p[tid]) * f);
   for (int64_t i = tail + tid; i < n; i += kThreads) o[i] = from_f<T>(to_f(p[i]) * f);
-#pragma unroll 4
-  for (int64_t i = tid; i < vecs; i += kThreads) {
+  constexpr int U = 4;
+  int64_t i = tid;
+  for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
+    Raw<T, V> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u].load(p + head + (i + u * kThreads) * V);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float2 v[V / 2];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) v[j] = mul2(r[u].pair(j), both(f));
+      store_vec<T, V>(o + head + (i + u * kThreads) * V, v);
+    }
+  }
+  for (; i < vecs; i += kThreads) {
     Raw<T, V> r;
     r.load(p + head + i * V);
     float2 v[V / 2];

@@ -1,9 +1,12 @@
 // conv.cu - the causal convolution over time: whole sequences forward and
 // backward, and the serving step.
 //
-// A thread has 8 channels and walks a stretch of tokens with the last W inputs in
-// registers, so each input is read once from memory (and W - 1 times more at the
-// start of a stretch, mostly from L2).
+// Memory bounds it.  A thread has 16 bytes of channels (forward; half as many backward in
+// bf16, for the registers) and walks a stretch of 32 tokens with the last W inputs in
+// registers, so each input is read once from memory (and W - 1 times more at the start
+// of a stretch, mostly from L2); it loads four tokens while it works on the four before,
+// since a store holds back the loads behind it.  A CTA has 128 channels of several
+// stretches, whose sums for the weights' gradients it adds before they go to memory.
 #include "common.cuh"
 #include "conv.h"
 #include "pair.cuh"
@@ -13,193 +16,291 @@ namespace rnn {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256, kStepThreads = 128;
 constexpr int kStretch = 32;      // tokens a thread
+constexpr int kSpan = 128;        // channels of a CTA; its threads of V channels have kThreads * V / kSpan stretches
+constexpr int kAhead = 4;         // tokens loaded at once
 
-template <typename T>
-__device__ __forceinline__ float2 sigm2(float2 v) {
-  if constexpr (sizeof(T) == 2)
-    return make_float2(__fdividef(1.f, 1.f + __expf(-v.x)), __fdividef(1.f, 1.f + __expf(-v.y)));
-  else
-    return make_float2(sigm(v.x), sigm(v.y));
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// The taps of a thread's 8 channels, [channels, W] in memory, as pairs of channels.
-template <typename T, int W>
-__device__ __forceinline__ void load_taps(float2 (&w)[W][4], const void* base, int64_t d) {
-  const T* p = static_cast<const T*>(base) + d * W;
+// The sigmoid; with bf16 storage from the approximations, a few 2^-23 off.
+template <typename T>
+__device__ __forceinline__ float2 sigm2(float2 v) {
+  if constexpr (sizeof(T) == 2) {
+    const float2 q = mul2(v, both(-1.4426950408889634f)), d = add2(make_float2(ex2(q.x), ex2(q.y)), both(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+  } else {
+    return make_float2(sigm(v.x), sigm(v.y));
+  }
+}
+
+// The taps of a thread's V channels, [channels, W] in memory, as pairs of channels.
+template <typename T, int W, int V>
+__device__ __forceinline__ void load_taps(float2 (&w)[W][V / 2], const void* base, int64_t d) {
+  float f[V * W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    Raw<T, V> r;
+    r.load(static_cast<const T*>(base) + d * W + V * i);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      f[V * i + 2 * j] = r.pair(j).x;
+      f[V * i + 2 * j + 1] = r.pair(j).y;
+    }
+  }
 #pragma unroll
   for (int k = 0; k < W; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[k][j] = make_float2(to_f(p[2 * j * W + k]), to_f(p[(2 * j + 1) * W + k]));
+    for (int j = 0; j < V / 2; ++j) w[k][j] = make_float2(f[2 * j * W + k], f[(2 * j + 1) * W + k]);
 }
-template <typename T>
-__device__ __forceinline__ void unpack(float2 (&v)[4], const Raw<T, 8>& r) {
+template <typename T, int V>
+__device__ __forceinline__ void unpack(float2 (&v)[V / 2], const Raw<T, V>& r) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = r.pair(j);
+  for (int j = 0; j < V / 2; ++j) v[j] = r.pair(j);
+}
+template <typename T, int V>
+__device__ __forceinline__ void put(void* to, const Raw<T, V>& r) {
+  float2 v[V / 2];
+  unpack<T, V>(v, r);
+  store_vec<T, V>(static_cast<T*>(to), v);
 }
 
 // Where the input of extended row e (e - (W - 1) is its token) lies: the state's rows
 // come first.
-template <typename T, int W>
-__device__ __forceinline__ void load_input(Raw<T, 8>& r, const ConvArgs& a, const void* s0, int b, int e, int len, int d) {
+template <typename T, int W, int V>
+__device__ __forceinline__ void load_input(Raw<T, V>& r, const ConvArgs& a, const void* s0, int b, int e, int len, int d) {
   const int t = e - (W - 1);
-  if (t >= 0) load_or<T, 8>(r, a.x, t < len ? a.row(b, t) * a.x_row + d : 0, t < len, 0.f);
-  else load_or<T, 8>(r, s0, (static_cast<int64_t>(b) * (W - 1) + e) * a.D + d, s0 != nullptr, 0.f);
+  if (t >= 0) load_or<T, V>(r, a.x, t < len ? a.row(b, t) * a.x_row + d : 0, t < len, 0.f);
+  else load_or<T, V>(r, s0, (static_cast<int64_t>(b) * (W - 1) + e) * a.D + d, s0 != nullptr, 0.f);
 }
 
+// A thread's channels and stretch; ``in`` is false beyond the last of either.
+template <int V>
 struct Spot {
-  int b, seg, d;
+  static constexpr int SIDE = kSpan / V, RUNS = kThreads / SIDE;
+  int b, seg, d, part;                       // part: the CTA's place among those of its channels
   bool in;
+  __host__ __device__ static int spans(const ConvArgs& a) { return (a.D + kSpan - 1) / kSpan; }
+  // CTAs over the stretches of all sequences.
+  __host__ __device__ static int parts(const ConvArgs& a) {
+    const int64_t all = static_cast<int64_t>(a.B) * ((a.T + kStretch - 1) / kStretch);
+    return static_cast<int>((all + RUNS - 1) / RUNS);
+  }
   __device__ __forceinline__ Spot(const ConvArgs& a) {
-    const int per = (a.D / 8 + kThreads - 1) / kThreads, segs = (a.T + kStretch - 1) / kStretch;
-    const int c = blockIdx.x % per, r = blockIdx.x / per;
-    seg = r % segs;
-    b = r / segs;
-    d = (c * kThreads + threadIdx.x) * 8;
-    in = d < a.D;
+    const int per = spans(a), segs = (a.T + kStretch - 1) / kStretch;
+    part = blockIdx.x / per;
+    const int64_t item = static_cast<int64_t>(part) * RUNS + threadIdx.x / SIDE;
+    b = static_cast<int>(item / segs);
+    seg = static_cast<int>(item - static_cast<int64_t>(b) * segs);
+    d = (blockIdx.x - part * per) * kSpan + threadIdx.x % SIDE * V;
+    in = d < a.D && b < a.B;
   }
 };
 
-template <typename T, int W>
+template <typename T, int W, int V>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvFwdArgs f) {
+  constexpr int U = kAhead, H = V / 2;
   const ConvArgs& a = f.a;
-  const Spot p(a);
+  const Spot<V> p(a);
   if (!p.in) return;
   const int len = a.len ? a.len[p.b] : a.T, t0 = p.seg * kStretch;
-  const int t1 = t0 + kStretch < a.T ? t0 + kStretch : a.T;
-  float2 w[W][4], bias[4], win[W][4];
-  load_taps<T, W>(w, a.w, p.d);
-  Raw<T, 8> r;
-  load_or<T, 8>(r, a.bias, p.d, a.bias != nullptr, 0.f);
-  unpack<T>(bias, r);
+  const int t1 = t0 + kStretch < a.T ? t0 + kStretch : a.T, last = len < t1 ? len : t1;
+  const int64_t hop = a.bfirst ? 1 : a.B, row0 = a.row(p.b, t0);
+  const T* px = static_cast<const T*>(a.x) + row0 * a.x_row + p.d;
+  T* py = static_cast<T*>(f.y) + row0 * a.D + p.d;
+  Raw<T, V> r[U];
+  auto load = [&](int t) {
 #pragma unroll
-  for (int k = 1; k < W; ++k) {
-    load_input<T, W>(r, a, f.s0, p.b, t0 + k - 1, len, p.d);
-    unpack<T>(win[k], r);
-  }
-  // the state out before anything else is written: sT may be s0
+    for (int i = 0; i < U; ++i) load_or<T, V>(r[i], px, i * hop * a.x_row, t + i < last, 0.f);
+    px += U * hop * a.x_row;
+  };
+  float2 w[W][H], bias[H], win[W][H];
+  Raw<T, V> q[W];
+  load_or<T, V>(q[0], a.bias, p.d, a.bias != nullptr, 0.f);
+#pragma unroll
+  for (int k = 1; k < W; ++k) load_input<T, W, V>(q[k], a, f.s0, p.b, t0 + k - 1, len, p.d);
+  load(t0);
+  load_taps<T, W, V>(w, a.w, p.d);
+  unpack<T, V>(bias, q[0]);
+#pragma unroll
+  for (int k = 1; k < W; ++k) unpack<T, V>(win[k], q[k]);
+  // the state out after the state in, which it may be
   if (p.seg == 0 && f.sT) {
-    Raw<T, 8> q[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) load_input<T, W>(q[k], a, f.s0, p.b, len + k, len, p.d);
+    for (int k = 0; k < W - 1; ++k) load_input<T, W, V>(q[k], a, f.s0, p.b, len + k, len, p.d);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-      *reinterpret_cast<Raw<T, 8>*>(static_cast<T*>(f.sT) + (static_cast<int64_t>(p.b) * (W - 1) + k) * a.D + p.d) = q[k];
+      put<T, V>(static_cast<T*>(f.sT) + (static_cast<int64_t>(p.b) * (W - 1) + k) * a.D + p.d, q[k]);
   }
-#pragma unroll 8
-  for (int t = t0; t < t1; ++t) {
-    load_or<T, 8>(r, a.x, t < len ? a.row(p.b, t) * a.x_row + p.d : 0, t < len, 0.f);
-    float2 v[4];
+  for (int t = t0; t < t1; t += U) {
+    Raw<T, V> x[U];
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k)
+    for (int i = 0; i < U; ++i) x[i] = r[i];
+    if (t + U < t1) load(t + U);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) win[k][j] = win[k + 1][j];
-    unpack<T>(win[W - 1], r);
+    for (int i = 0; i < U; ++i) {
+      float2 v[H];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = bias[j];
+      for (int k = 0; k + 1 < W; ++k)
 #pragma unroll
-      for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], win[k][j], v[j]);
-      if (a.silu) v[j] = mul2(v[j], sigm2<T>(v[j]));
-      if (t >= len) v[j] = both(0.f);
+        for (int j = 0; j < H; ++j) win[k][j] = win[k + 1][j];
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        win[W - 1][j] = x[i].pair(j);
+        v[j] = bias[j];
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], win[k][j], v[j]);
+        if (a.silu) v[j] = mul2(v[j], sigm2<T>(v[j]));
+        if (t + i >= len) v[j] = both(0.f);
+      }
+      if (t + i < t1) store_vec<T, V>(py + i * hop * a.D, v);
     }
-    store_vec<T, 8>(static_cast<T*>(f.y) + a.row(p.b, t) * a.D + p.d, v);
+    py += U * hop * a.D;
   }
 }
 
 // The gradients.  With dp_t = dy_t act'(pre_t): walking t forward, the last W values of
 // dp give sum_k w[k] dp_{t-k}, the gradient of extended row t (a row of the state for
 // t < W - 1, else token t - (W - 1)); x's window gives dw.
-template <typename T, int W>
+template <typename T, int W, int V>
 __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdArgs g) {
+  constexpr int U = kAhead, H = V / 2;
+  __shared__ float fold[kThreads * V];
   const ConvArgs& a = g.a;
-  const Spot p(a);
-  if (!p.in) return;
-  const int len = a.len ? a.len[p.b] : a.T, t0 = p.seg * kStretch;
-  const int t1 = t0 + kStretch < a.T ? t0 + kStretch : a.T;
-  float2 w[W][4], bias[4], win[W][4], dp[W][4], dw[W][4], db[4];
-  load_taps<T, W>(w, a.w, p.d);
-  Raw<T, 8> r;
-  load_or<T, 8>(r, a.bias, p.d, a.bias != nullptr, 0.f);
-  unpack<T>(bias, r);
+  const Spot<V> p(a);
+  float2 dw[W + 1][H];                       // and the bias's
 #pragma unroll
-  for (int k = 0; k < W; ++k)
+  for (int k = 0; k <= W; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) win[k][j] = dp[k][j] = dw[k][j] = db[j] = both(0.f);
+    for (int j = 0; j < H; ++j) dw[k][j] = both(0.f);
+  if (p.in) {
+    const int len = a.len ? a.len[p.b] : a.T, t0 = p.seg * kStretch;
+    const int t1 = t0 + kStretch < a.T ? t0 + kStretch : a.T, stop = t1 + W - 1, last = len < stop ? len : stop;
+    const int64_t hop = a.bfirst ? 1 : a.B, row0 = a.row(p.b, t0);
+    const T *px = static_cast<const T*>(a.x) + row0 * a.x_row + p.d, *pdy = static_cast<const T*>(g.dy) + row0 * a.D + p.d;
+    Raw<T, V> rx[U], ry[U];
+    auto load = [&](int t) {
 #pragma unroll
-  for (int k = 1; k < W; ++k) {
-    load_input<T, W>(r, a, g.s0, p.b, t0 + k - 1, len, p.d);
-    unpack<T>(win[k], r);
-  }
-#pragma unroll 4
-  for (int t = t0; t < t1 + W - 1; ++t) {
-    Raw<T, 8> rx, ry;
-    const bool ok = t < len;
-    load_or<T, 8>(rx, a.x, ok ? a.row(p.b, t) * a.x_row + p.d : 0, ok, 0.f);
-    load_or<T, 8>(ry, g.dy, ok ? a.row(p.b, t) * a.D + p.d : 0, ok, 0.f);
-#pragma unroll
-    for (int k = 0; k + 1 < W; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        win[k][j] = win[k + 1][j];
-        dp[W - 1 - k][j] = dp[W - 2 - k][j];
+      for (int i = 0; i < U; ++i) {
+        load_or<T, V>(rx[i], px, i * hop * a.x_row, t + i < last, 0.f);
+        load_or<T, V>(ry[i], pdy, i * hop * a.D, t + i < last, 0.f);
       }
-    unpack<T>(win[W - 1], rx);
-    unpack<T>(dp[0], ry);
-    float2 v[4];
+      px += U * hop * a.x_row;
+      pdy += U * hop * a.D;
+    };
+    float2 w[W][H], bias[H], win[W][H], dp[W][H];
+    Raw<T, V> q[W];
+    load_or<T, V>(q[0], a.bias, p.d, a.bias != nullptr, 0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (a.silu) {
-        float2 q = bias[j];
+    for (int k = 1; k < W; ++k) load_input<T, W, V>(q[k], a, g.s0, p.b, t0 + k - 1, len, p.d);
+    load(t0);
+    load_taps<T, W, V>(w, a.w, p.d);
+    unpack<T, V>(bias, q[0]);
 #pragma unroll
-        for (int k = 0; k < W; ++k) q = fma2(w[k][j], win[k][j], q);
-        const float2 s = sigm2<T>(q);
-        // s + q s (1 - s)
-        dp[0][j] = mul2(dp[0][j], fma2(mul2(q, s), make_float2(1.f - s.x, 1.f - s.y), s));
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+      for (int j = 0; j < H; ++j) win[k][j] = dp[k][j] = both(0.f);
+#pragma unroll
+    for (int k = 1; k < W; ++k) unpack<T, V>(win[k], q[k]);
+    T* pdx = static_cast<T*>(g.dx) + (row0 - (W - 1) * hop) * a.D + p.d;
+    for (int t = t0; t < stop; t += U) {
+      Raw<T, V> x[U], d[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = rx[i];
+        d[i] = ry[i];
       }
-      if (!ok) dp[0][j] = both(0.f);
-      if (t < t1) {
+      if (t + U < stop) load(t + U);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-          if (ok) dw[k][j] = fma2(dp[0][j], win[k][j], dw[k][j]);
-        db[j] = add2(db[j], dp[0][j]);
+      for (int i = 0; i < U; ++i) {
+        const int e = t + i;
+        const bool ok = e < len;
+#pragma unroll
+        for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            win[k][j] = win[k + 1][j];
+            dp[W - 1 - k][j] = dp[W - 2 - k][j];
+          }
+        float2 v[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          win[W - 1][j] = x[i].pair(j);
+          dp[0][j] = d[i].pair(j);
+          if (a.silu) {
+            float2 pre = bias[j];
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = fma2(w[k][j], win[k][j], pre);
+            const float2 s = sigm2<T>(pre);
+            // s + pre s (1 - s)
+            dp[0][j] = mul2(dp[0][j], fma2(mul2(pre, s), make_float2(1.f - s.x, 1.f - s.y), s));
+          }
+          if (!ok) dp[0][j] = both(0.f);
+          // the tokens behind the stretch belong to the next one's sums
+          if (ok && e < t1) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][j] = fma2(dp[0][j], win[k][j], dw[k][j]);
+            dw[W][j] = add2(dw[W][j], dp[0][j]);
+          }
+          v[j] = both(0.f);
+#pragma unroll
+          for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], dp[k][j], v[j]);
+        }
+        // extended row e of the state's gradient out
+        if (e >= len && e < len + W - 1 && g.dsT) {
+          Raw<T, V> r;
+          r.load(static_cast<const T*>(g.dsT) + (static_cast<int64_t>(p.b) * (W - 1) + e - len) * a.D + p.d);
+#pragma unroll
+          for (int j = 0; j < H; ++j) v[j] = add2(v[j], r.pair(j));
+        }
+        if (e >= t0 + W - 1) {
+          if (e - (W - 1) >= len)
+#pragma unroll
+            for (int j = 0; j < H; ++j) v[j] = both(0.f);
+          if (g.dx && e < stop) store_vec<T, V>(pdx + i * hop * a.D, v);
+        } else if (p.seg == 0 && g.ds0) {
+          store_vec<T, V>(static_cast<T*>(g.ds0) + (static_cast<int64_t>(p.b) * (W - 1) + e) * a.D + p.d, v);
+        }
       }
-      v[j] = both(0.f);
-#pragma unroll
-      for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], dp[k][j], v[j]);
-    }
-    // extended row t of the state's gradient out
-    if (t >= len && t < len + W - 1 && g.dsT) {
-      load_or<T, 8>(r, g.dsT, (static_cast<int64_t>(p.b) * (W - 1) + t - len) * a.D + p.d, true, 0.f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], r.pair(j));
-    }
-    if (t >= t0 + W - 1) {
-      const int s = t - (W - 1);
-      if (s >= len)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = both(0.f);
-      if (g.dx) store_vec<T, 8>(static_cast<T*>(g.dx) + a.row(p.b, s) * a.D + p.d, v);
-    } else if (p.seg == 0 && g.ds0) {
-      store_vec<T, 8>(static_cast<T*>(g.ds0) + (static_cast<int64_t>(p.b) * (W - 1) + t) * a.D + p.d, v);
+      pdx += U * hop * a.D;
     }
   }
   if (!g.partial) return;
-  float* out = g.partial + (static_cast<int64_t>(p.b) * ((a.T + kStretch - 1) / kStretch) + p.seg) * (W + 1) * a.D + p.d;
+  // the CTA's stretches, in order
 #pragma unroll
-  for (int k = 0; k < W; ++k) store_vec<float, 8>(out + static_cast<int64_t>(k) * a.D, dw[k]);
-  store_vec<float, 8>(out + static_cast<int64_t>(W) * a.D, db);
+  for (int k = 0; k <= W; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < H; ++j) *reinterpret_cast<float2*>(&fold[threadIdx.x * V + 2 * j]) = dw[k][j];
+    __syncthreads();
+    const int c = static_cast<int>(threadIdx.x), d = p.d / kSpan * kSpan + c;
+    if (c < kSpan && d < a.D) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < Spot<V>::RUNS; ++i) s += fold[i * kSpan + c];
+      g.partial[(static_cast<int64_t>(p.part) * (W + 1) + k) * a.D + d] = s;
+    }
+  }
 }
 
-// dw[d][k] and dbias[d]: the sums over the stretches, each of 8 groups in order and
-// then the groups in order; 32 channels of one tap a block.
+// dw[d][k] and dbias[d]: the sums over the CTAs, each of 8 groups in order and then the
+// groups in order; 32 channels of one tap a block.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* partial, int parts, int D, int W, float* dw,
                                                           float* dbias) {
   __shared__ float sm[8][32];
   const int k = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
   float s = 0.f;
   if (c < D)
+#pragma unroll 8
     for (int i = g; i < parts; i += 8) s += partial[(static_cast<int64_t>(i) * (W + 1) + k) * D + c];
   sm[g][threadIdx.x & 31] = s;
   __syncthreads();
@@ -212,10 +313,10 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* partial, 
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs p) {
+__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvStepArgs p) {
   const ConvArgs& a = p.a;
-  const int per = (a.D / 8 + kThreads - 1) / kThreads, b = blockIdx.x / per;
-  const int d = ((blockIdx.x - b * per) * kThreads + threadIdx.x) * 8;
+  const int per = (a.D / 8 + kStepThreads - 1) / kStepThreads, b = blockIdx.x / per;
+  const int d = ((blockIdx.x - b * per) * kStepThreads + threadIdx.x) * 8;
   if (d >= a.D) return;
   const int slot = p.slots ? p.slots[b] : b;
   const bool live = slot >= 0 && slot < p.num_slots;
@@ -225,9 +326,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
   Raw<T, 8> win[W];
   Raw<T, 8> r;
   if (len > 0) {
-    load_taps<T, W>(w, a.w, d);
+    load_taps<T, W, 8>(w, a.w, d);
     load_or<T, 8>(r, a.bias, d, a.bias != nullptr, 0.f);
-    unpack<T>(bias, r);
+    unpack<T, 8>(bias, r);
 #pragma unroll
     for (int k = 1; k < W; ++k) win[k].load(st + static_cast<int64_t>(k - 1) * a.D);
   }
@@ -257,51 +358,61 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
 
-int channel_ctas(const ConvArgs& a) { return (a.D / 8 + kThreads - 1) / kThreads; }
-int stretches(const ConvArgs& a) { return (a.T + kStretch - 1) / kStretch; }
-unsigned walk_ctas(const ConvArgs& a) {
-  return static_cast<unsigned>(a.B) * stretches(a) * channel_ctas(a);
-}
+// Channels a thread.
+template <typename T> constexpr int kFwdV = sizeof(T) == 2 ? 8 : 4;
+constexpr int kBwdV = 4;
 
-// CALL<type, width>(args)
-#define RNN_CONV_WIDTHS(KERNEL, T, GRID, ARGS)                                          \
-  switch ((ARGS).a.W) {                                                                 \
-    case 2: KERNEL<T, 2><<<GRID, kThreads, 0, s>>>(ARGS); break;                        \
-    case 3: KERNEL<T, 3><<<GRID, kThreads, 0, s>>>(ARGS); break;                        \
-    default: KERNEL<T, 4><<<GRID, kThreads, 0, s>>>(ARGS);                              \
+template <typename T, int W>
+int fwd(const ConvFwdArgs& f, cudaStream_t s) {
+  using S = Spot<kFwdV<T>>;
+  conv_fwd_kernel<T, W, kFwdV<T>><<<static_cast<unsigned>(S::parts(f.a)) * S::spans(f.a), kThreads, 0, s>>>(f);
+  return check_launch();
+}
+template <typename T, int W>
+int bwd(const ConvBwdArgs& b, cudaStream_t s) {
+  using S = Spot<kBwdV>;
+  conv_bwd_kernel<T, W, kBwdV><<<static_cast<unsigned>(S::parts(b.a)) * S::spans(b.a), kThreads, 0, s>>>(b);
+  return check_launch();
+}
+template <typename T, int W>
+int step(const ConvStepArgs& p, cudaStream_t s) {
+  conv_step_kernel<T, W><<<static_cast<unsigned>(p.a.B) * ((p.a.D / 8 + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(p);
+  return check_launch();
+}
+#define RNN_CONV_WIDTHS(CALL, T, ARGS)              \
+  switch ((ARGS).a.W) {                             \
+    case 2: return CALL<T, 2>(ARGS, s);             \
+    case 3: return CALL<T, 3>(ARGS, s);             \
+    default: return CALL<T, 4>(ARGS, s);            \
   }
+template <typename T> int fwd_t(const ConvFwdArgs& f, cudaStream_t s) { RNN_CONV_WIDTHS(fwd, T, f) }
+template <typename T> int bwd_t(const ConvBwdArgs& b, cudaStream_t s) { RNN_CONV_WIDTHS(bwd, T, b) }
+template <typename T> int step_t(const ConvStepArgs& p, cudaStream_t s) { RNN_CONV_WIDTHS(step, T, p) }
 
 }  // namespace
 
 size_t conv_workspace_bytes(const ConvArgs& a) {
-  return static_cast<size_t>(a.B) * stretches(a) * (a.W + 1) * a.D * 4;
+  return static_cast<size_t>(Spot<kBwdV>::parts(a)) * (a.W + 1) * a.D * 4;
 }
 
 int launch_conv_forward(const ConvFwdArgs& f, int is_bf16, cudaStream_t s) {
-  if (is_bf16) RNN_CONV_WIDTHS(conv_fwd_kernel, __nv_bfloat16, walk_ctas(f.a), f)
-  else RNN_CONV_WIDTHS(conv_fwd_kernel, float, walk_ctas(f.a), f)
-  return check_launch();
+  return is_bf16 ? fwd_t<__nv_bfloat16>(f, s) : fwd_t<float>(f, s);
 }
 
 int launch_conv_backward(const ConvBwdArgs& b, int is_bf16, cudaStream_t s, int* launches) {
   *launches = 0;
-  if (is_bf16) RNN_CONV_WIDTHS(conv_bwd_kernel, __nv_bfloat16, walk_ctas(b.a), b)
-  else RNN_CONV_WIDTHS(conv_bwd_kernel, float, walk_ctas(b.a), b)
-  int rc = check_launch();
+  int rc = is_bf16 ? bwd_t<__nv_bfloat16>(b, s) : bwd_t<float>(b, s);
   if (rc) return rc;
   *launches = 1;
   if (!b.partial) return 0;
-  conv_reduce_kernel<<<dim3((b.a.D + 31) / 32, b.a.W + 1), 256, 0, s>>>(b.partial, b.a.B * stretches(b.a), b.a.D, b.a.W,
-                                                                        b.dw, b.dbias);
+  conv_reduce_kernel<<<dim3((b.a.D + 31) / 32, b.a.W + 1), 256, 0, s>>>(b.partial, Spot<kBwdV>::parts(b.a), b.a.D, b.a.W, b.dw,
+                                                                        b.dbias);
   if (!(rc = check_launch())) *launches = 2;
   return rc;
 }
 
 int launch_conv_step(const ConvStepArgs& p, int is_bf16, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(p.a.B) * channel_ctas(p.a);
-  if (is_bf16) RNN_CONV_WIDTHS(conv_step_kernel, __nv_bfloat16, grid, p)
-  else RNN_CONV_WIDTHS(conv_step_kernel, float, grid, p)
-  return check_launch();
+  return is_bf16 ? step_t<__nv_bfloat16>(p, s) : step_t<float>(p, s);
 }
 
 }  // namespace rnn

@@ -36,7 +36,7 @@ struct ConvBwdArgs {
   const void *s0, *dy, *dsT;
   void *dx, *ds0;
   float *dw, *dbias;
-  float* partial;              // [CTA][W + 1][channels of the CTA], or null
+  float* partial;              // [CTA][W + 1][D], or null
 };
 int launch_conv_backward(const ConvBwdArgs& b, int is_bf16, cudaStream_t s, int* launches);
 

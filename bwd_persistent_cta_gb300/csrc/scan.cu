@@ -279,9 +279,7 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 // states, their rates and the next rows of B and C stays in registers, so that five warps
 // a scheduler hide the latencies of each other.  Eight states a lane: at 16 states two
 // lanes share a channel, and a sum over the states is one exchange.
-#ifndef V_OCC
-#define V_OCC 12
-#endif
+constexpr int kFwdWarps = 12;    // an SM
 constexpr int kFwdNS = 8, kStretch = 8;
 enum { kInfer, kTrain, kAlone, kAloneBack };
 
@@ -318,7 +316,7 @@ __device__ __forceinline__ void over_states(float (&v)[C], int sl) {
 }
 
 template <typename T, int SL, int C, int MODE>
-__global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kernel(const ScanFwdArgs f) {
+__global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdArgs f) {
   constexpr bool OUT = MODE == kInfer || MODE == kTrain, BACK = MODE == kAloneBack;
   using W = Fwd<T, SL, C, OUT>;
   constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, TT = W::TT;
@@ -510,6 +508,7 @@ __global__ void __launch_bounds__(32, sizeof(T) == 2 ? V_OCC : 12) scan_fwd_kern
 // states (of s1 and s2) and over the channels (of dB and dC) then take the fewest
 // exchanges together.  Inputs and kept states of the next tile of eight tokens are on
 // their way into shared memory meanwhile.
+constexpr int kBwdWarps = 8;     // an SM
 constexpr int kBT = 8, kBSub = kScanKeep, kBNS = 4, kBC = 4;
 
 template <typename T, int SL>
@@ -572,7 +571,7 @@ __device__ __forceinline__ void sum_channels(const float2 (&dB)[2], const float2
 }
 
 template <typename T, int SL>
-__global__ void __launch_bounds__(32) scan_bwd_kernel(const ScanBwdArgs p) {
+__global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdArgs p) {
   using W = Bwd<T, SL>;
   constexpr int CT = W::CT, NP = W::NP, P = W::P, C = kBC, NS = kBNS, TT = kBT, CL = W::CL;
   __shared__ __align__(16) W s;
@@ -840,21 +839,32 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const ScanBwdArgs p) {
   }
 }
 
-// dB and dC: the sum over a group's warps, in order, four states a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int ctas, int NP, T* dB, T* dC) {
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.G, all = rows * (NP / 2);
-  for (int64_t e = blockIdx.x * 256LL + threadIdx.x; e < all; e += gridDim.x * 256LL) {
-    const int64_t r = e / (NP / 2);
-    const int k = static_cast<int>(e - r * (NP / 2)) * 4, n = k % NP;
-    T* out = k < NP ? dB : dC;
-    if (n >= a.N || !out) continue;
+// dB and dC: the sum over the warps of a group, a warp for each token and group: its lanes
+// read whole rows of partial sums, 32 / V of them at a time (V vectors of four states a
+// row), each lane in order and then the lanes in order.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int parts, T* dB, T* dC) {
+  constexpr int NP = 2 * V, SUB = 32 / V;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.G;
+  const int lane = threadIdx.x & 31, k = lane % V * 4, sub = lane / V;
+  for (int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8LL) {
+    const float* from = bc + (r * parts + sub) * (2 * NP) + k;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < ctas; ++i) {
-      const float4 q = *reinterpret_cast<const float4*>(bc + (r * ctas + i) * (2 * NP) + k);
+#pragma unroll 8
+    for (int i = sub; i < parts; i += SUB, from += SUB * 2 * NP) {
+      const float4 q = *reinterpret_cast<const float4*>(from);
       v = make_float4(v.x + q.x, v.y + q.y, v.z + q.z, v.w + q.w);
     }
+#pragma unroll
+    for (int m = V; m < 32; m *= 2) {
+      v.x += __shfl_xor_sync(kFull, v.x, m);
+      v.y += __shfl_xor_sync(kFull, v.y, m);
+      v.z += __shfl_xor_sync(kFull, v.z, m);
+      v.w += __shfl_xor_sync(kFull, v.w, m);
+    }
+    T* out = k < NP ? dB : dC;
+    const int n = k % NP;
+    if (sub || n >= a.N || !out) continue;
     const int g = static_cast<int>(r % a.G);
     const int64_t bt = r / a.G;
     const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * a.T);
@@ -863,13 +873,26 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const fl
   }
 }
 
-// out[e] = sum over sequences of part[b][e], in order.
-__global__ void __launch_bounds__(256) scan_sum_kernel(const float* part, int B, int64_t n, float* out) {
-  const int64_t e = blockIdx.x * 256LL + threadIdx.x;
-  if (e >= n) return;
-  float v = 0.f;
-  for (int b = 0; b < B; ++b) v += part[b * n + e];
-  out[e] = v;
+// dA, dD and the bias's gradient: the sums over sequences and segments, in order.
+__global__ void __launch_bounds__(128) scan_sum_kernel(const ScanBwdArgs p) {
+  const ScanArgs& a = p.a;
+  const int parts = a.B * p.g.nseg;
+  const int64_t n[3] = {static_cast<int64_t>(a.D) * a.N, a.D, a.D};
+  int64_t e = blockIdx.x * 128LL + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (e < n[k]) {
+      const float* from = (k == 0 ? p.pA : k == 1 ? p.pD : p.pbias) + e;
+      float* to = static_cast<float*>(k == 0 ? p.grad.dA : k == 1 ? p.grad.dD : p.grad.ddt_bias);
+      if (!to) return;
+      float v = 0.f;
+#pragma unroll 8
+      for (int b = 0; b < parts; ++b) v += from[b * n[k]];
+      to[e] = v;
+      return;
+    }
+    e -= n[k];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -933,7 +956,7 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 
 // Lanes a channel: eight states each forward, four backward, rounded up to a power of two.
 int fwd_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
-int fwd_width(int N) { return N <= 8 ? 32 : 2 * 32 / fwd_lanes(N); }      // channels a warp
+int fwd_width(int N) { return (N <= 16 ? 32 : 64) / fwd_lanes(N); }      // channels a warp
 int bwd_width(int N) { return kBC * 16 / fwd_lanes(N); }
 int per_group(const ScanArgs& a, int width) { return (a.D / a.G + width - 1) / width; }
 
@@ -956,7 +979,7 @@ template <typename T>
 int fwd_t(const ScanFwdArgs& f, cudaStream_t s, int* launches) {
   switch (fwd_lanes(f.a.N)) {
     case 1: return fwd<T, 1, 1>(f, s, launches);
-    case 2: return getenv("V_C") && atoi(getenv("V_C")) == 1 ? fwd<T, 2, 1>(f, s, launches) : fwd<T, 2, 2>(f, s, launches);
+    case 2: return fwd<T, 2, 1>(f, s, launches);
     case 4: return fwd<T, 4, 2>(f, s, launches);
     default: return fwd<T, 8, 2>(f, s, launches);
   }
@@ -990,28 +1013,32 @@ int bwd_t(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
   int rc;
   switch (fwd_lanes(a.N)) {
     case 1: rc = bwd<T, 1, 1>(p, s, launches); break;
-    case 2: rc = bwd<T, 2, 2>(p, s, launches); break;
+    case 2: rc = bwd<T, 2, 1>(p, s, launches); break;
     case 4: rc = bwd<T, 4, 2>(p, s, launches); break;
     default: rc = bwd<T, 8, 2>(p, s, launches);
   }
   if (rc) return rc;
   if (p.bc) {
-    const int NP = 8 * fwd_lanes(a.N);
-    const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * a.G * (NP / 2) + 255) / 256;
-    scan_bc_kernel<T><<<static_cast<unsigned>(blocks < 16 * a.num_sms ? blocks : 16 * a.num_sms), 256, 0, s>>>(
-        a, p.bc, per_group(a, bwd_width(a.N)), NP, static_cast<T*>(p.grad.dB), static_cast<T*>(p.grad.dC));
+    const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * a.G + 7) / 8;
+    const unsigned grid = static_cast<unsigned>(blocks < 32 * a.num_sms ? blocks : 32 * a.num_sms);
+    const int parts = per_group(a, bwd_width(a.N));
+    T *dB = static_cast<T*>(p.grad.dB), *dC = static_cast<T*>(p.grad.dC);
+    switch (fwd_lanes(a.N)) {
+      case 1: scan_bc_kernel<T, 4><<<grid, 256, 0, s>>>(a, p.bc, parts, dB, dC); break;
+      case 2: scan_bc_kernel<T, 8><<<grid, 256, 0, s>>>(a, p.bc, parts, dB, dC); break;
+      case 4: scan_bc_kernel<T, 16><<<grid, 256, 0, s>>>(a, p.bc, parts, dB, dC); break;
+      default: scan_bc_kernel<T, 32><<<grid, 256, 0, s>>>(a, p.bc, parts, dB, dC);
+    }
     if ((rc = check_launch())) return rc;
     ++*launches;
   }
-  auto sum = [&](const float* from, int64_t n, void* to) {
-    if (!from || rc) return;
-    scan_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(from, a.B * p.g.nseg, n, static_cast<float*>(to));
-    if (!(rc = check_launch())) ++*launches;
-  };
-  sum(p.pA, static_cast<int64_t>(a.D) * a.N, p.grad.dA);
-  sum(p.pD, a.D, p.grad.dD);
-  sum(p.pbias, a.D, p.grad.ddt_bias);
-  return rc;
+  if (p.pA || p.pD || p.pbias) {
+    const int64_t n = static_cast<int64_t>(a.D) * (a.N + 2);
+    scan_sum_kernel<<<static_cast<unsigned>((n + 127) / 128), 128, 0, s>>>(p);
+    if ((rc = check_launch())) return rc;
+    ++*launches;
+  }
+  return 0;
 }
 
 template <typename T, int SL>
@@ -1036,15 +1063,17 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 
 }  // namespace
 
-ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward) {
-  const int width = backward ? bwd_width(a.N) : fwd_width(a.N);
-  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width), want = static_cast<int64_t>(a.num_sms) * (backward ? 8 : 16);
-  const int tiles = (a.T + 15) / 16;
-  int64_t n = warps * 2 > want ? 1 : want / warps;
+ScanSplit scan_split(const ScanArgs& a, int backward) {
+  const int width = backward ? bwd_width(a.N) : fwd_width(a.N), resident = (backward ? kBwdWarps : kFwdWarps) * a.num_sms;
+  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width);
+  int least = 64;
+  if (getenv("V_MIN")) least = atoi(getenv("V_MIN"));
+  int64_t n = warps >= (backward ? 4 : 5) * a.num_sms ? 1 : (backward ? 3 : 2) * resident / warps;
+  if (n > a.T / least) n = a.T / least;
+  if (n < 3) n = 1;
   const char* env = getenv(backward ? "V_BSEG" : "V_NSEG");
   if (env) n = atoi(env);
-  if (n > tiles / 4) n = tiles / 4;
-  if (n < 1) n = 1;
+  const int tiles = (a.T + 15) / 16;
   ScanSplit p{};
   p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * 16;
   p.nseg = (a.T + p.len - 1) / p.len;
@@ -1065,15 +1094,15 @@ ScanReserve scan_reserve(const ScanArgs& a) {
 
 int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStream_t s, int* launches) {
   ScanFwdArgs f = f_;
-  const ScanSplit p = scan_split(f.a, is_bf16, 0);
+  const ScanSplit p = scan_split(f.a, 0);
   f.g = segments(p, work);
   f.first = p.nseg > 1 && f.h0 && f.h0 == f.hT ? reinterpret_cast<float*>(static_cast<char*>(work) + p.first) : nullptr;
   *launches = 0;
   return is_bf16 ? fwd_t<__nv_bfloat16>(f, s, launches) : fwd_t<float>(f, s, launches);
 }
 
-ScanBwdLayout scan_bwd_layout(const ScanArgs& a, int is_bf16) {
-  const ScanSplit p = scan_split(a, is_bf16, 1);
+ScanBwdLayout scan_bwd_layout(const ScanArgs& a) {
+  const ScanSplit p = scan_split(a, 1);
   ScanBwdLayout l{};
   size_t off = p.bytes;
   auto take = [&](size_t n) {
@@ -1092,8 +1121,8 @@ ScanBwdLayout scan_bwd_layout(const ScanArgs& a, int is_bf16) {
 
 int launch_scan_backward(const ScanBwdArgs& b, int is_bf16, cudaStream_t s, int* launches) {
   ScanBwdArgs p = b;
-  const ScanBwdLayout l = scan_bwd_layout(p.a, is_bf16);
-  p.g = segments(scan_split(p.a, is_bf16, 1), p.work);
+  const ScanBwdLayout l = scan_bwd_layout(p.a);
+  p.g = segments(scan_split(p.a, 1), p.work);
   auto part = [&](const void* want, size_t off) { return want ? reinterpret_cast<float*>(p.work + off) : nullptr; };
   p.bc = part(p.grad.dB ? p.grad.dB : p.grad.dC, l.bc);
   p.pA = part(p.grad.dA, l.dA);

@@ -37,7 +37,7 @@ struct ScanSplit {
   size_t first;                // [B][D][N]: the initial state where the final one overwrites it
   size_t bytes;
 };
-ScanSplit scan_split(const ScanArgs& a, int is_bf16, int backward);
+ScanSplit scan_split(const ScanArgs& a, int backward);
 
 struct ScanSegs {
   int nseg, len;
@@ -67,7 +67,7 @@ int launch_scan_forward(const ScanFwdArgs& f, void* work, int is_bf16, cudaStrea
 struct ScanBwdLayout {
   size_t bc, dA, dD, dbias, bytes;
 };
-ScanBwdLayout scan_bwd_layout(const ScanArgs& a, int is_bf16);
+ScanBwdLayout scan_bwd_layout(const ScanArgs& a);
 
 struct ScanBwdArgs {
   ScanArgs a;

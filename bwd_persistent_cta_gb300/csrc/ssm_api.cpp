@@ -48,7 +48,8 @@ namespace {
 
 rnn_status_t check_sequences(int batch, int seq_len, int channels) {
   if (batch < 1 || seq_len < 1 || channels < 8 || channels > 65536 || channels % 8) return RNN_BAD_PARAM;
-  if (static_cast<long long>(seq_len) * batch > (1LL << 30)) return RNN_BAD_PARAM;
+  const long long rows = static_cast<long long>(seq_len) * batch;
+  if (rows > (1LL << 30) || rows * channels > (1LL << 43)) return RNN_BAD_PARAM;      // grids stay below 2^31 CTAs
   // CTAs of the largest grid: one for each 8 channels of a sequence
   return static_cast<long long>(batch) * (channels / 8) <= (1LL << 31) - 1 ? RNN_OK : RNN_BAD_PARAM;
 }
@@ -190,8 +191,8 @@ rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* out) {
   h->bf16 = desc->dtype == RNN_BF16;
   h->es = h->bf16 ? 2 : 4;
   const ScanArgs a = scan_shape(h);
-  h->workspace_bytes = scan_split(a, h->bf16, 0).bytes;
-  h->bwd_workspace_bytes = scan_bwd_layout(a, h->bf16).bytes;
+  h->workspace_bytes = scan_split(a, 0).bytes;
+  h->bwd_workspace_bytes = scan_bwd_layout(a).bytes;
   h->reserve_bytes = scan_reserve(a).bytes;
   *out = h;
   return RNN_OK;

@@ -378,6 +378,7 @@ class GradClip(_Op):
         self._bind("f32", device)
         torch = self.torch
         self.desc = list(zip(counts, (torch.bfloat16 if d == "bf16" else torch.float32 for d in dtypes)))
+        self._counts, self._dtypes = counts, [dt for _, dt in self.desc]
         with torch.cuda.device(self.device):
             self.handle = rnn_clip_create(counts, [RNN_BF16 if d == "bf16" else RNN_F32 for d in dtypes])
         self.workspace_bytes = rnn_clip_get_sizes(self.handle)
@@ -389,23 +390,25 @@ class GradClip(_Op):
         """The pointers of a list of tensors that are as the handle has them."""
         if len(tensors) != len(self.desc):
             raise ValueError(f"{name} has {len(tensors)} tensors; the handle has {len(self.desc)}")
-        device, ptrs = self.device, []
-        for t, (n, dt) in zip(tensors, self.desc):
-            try:
-                if t.dtype is dt and t.numel() == n and t.device == device and t.is_contiguous():
-                    ptrs.append(t.data_ptr())
-                    continue
-            except AttributeError:
-                pass
-            i = len(ptrs)
-            if not isinstance(t, self.torch.Tensor):
+        # one pass over what is usually right; what is wrong is found again below
+        torch, n = self.torch, len(tensors)
+        T = torch.Tensor
+        try:
+            if (list(map(T.numel, tensors)) == self._counts and list(map(T.get_device, tensors)) == [self.device.index] * n
+                    and [t.dtype for t in tensors] == self._dtypes and all(map(T.is_contiguous, tensors))):
+                return list(map(T.data_ptr, tensors))
+        except TypeError:
+            pass
+        for i, (t, (n, dt)) in enumerate(zip(tensors, self.desc)):
+            if not isinstance(t, T):
                 raise TypeError(f"{name}[{i}] must be a torch.Tensor, not {type(t).__name__}")
-            if t.device != device:
-                raise ValueError(f"{name}[{i}] is on {t.device}; the handle is on {device}")
+            if t.device != self.device:
+                raise ValueError(f"{name}[{i}] is on {t.device}; the handle is on {self.device}")
             if t.dtype != dt or t.numel() != n:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements of {t.dtype}; expected {n} of {dt}")
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        return ptrs
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+        raise ValueError(f"{name}: not as the handle has it")
 
     def _norm(self, norm):
         if norm is None:
