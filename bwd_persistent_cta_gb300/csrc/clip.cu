@@ -16,6 +16,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
+constexpr int kVectors = 8;       // of 16 bytes a thread, in flight at once
 
 template <int CAP>
 struct Pointers {
@@ -51,20 +52,25 @@ __device__ __forceinline__ double squares(const float2 (&v)[N]) {
   return d;
 }
 
-// Calls f(tensor, from, to) for the parts of the tensors that lie in the CTA's slice.
-template <typename F>
-__device__ __forceinline__ void walk(const Share& h, int64_t lo, int64_t hi, F f) {
-  int a = 0, b = h.num;                      // the last tensor that begins at or before lo
+// The last tensor that begins at or before element ``at``.
+__device__ __forceinline__ int tensor_at(const Share& h, int64_t at) {
+  int a = 0, b = h.num;
   while (b - a > 1) {
     const int m = (a + b) / 2;
-    if (h.start[h.first + m] <= lo) a = m;
+    if (h.start[h.first + m] <= at) a = m;
     else b = m;
   }
-  for (; lo < hi && a < h.num; ++a) {
-    const int64_t s = h.start[h.first + a], e = h.start[h.first + a + 1];
-    const int64_t to = e < hi ? e : hi;
-    if (to > lo) f(a, lo - s, to - s);
-    lo = to > lo ? to : lo;
+  return a;
+}
+// Calls f(tensor, from, to) for the parts of the tensors that lie in lo .. hi, from the
+// first to the last or the other way round.
+template <bool BACK, typename F>
+__device__ __forceinline__ void walk(const Share& h, int64_t lo, int64_t hi, F f) {
+  for (int i = tensor_at(h, BACK ? hi - 1 : lo); i >= 0 && i < h.num; i += BACK ? -1 : 1) {
+    const int64_t s = h.start[h.first + i], e = h.start[h.first + i + 1];
+    const int64_t from = s > lo ? s : lo, to = e < hi ? e : hi;
+    if (to > from) f(i, from - s, to - s);
+    if (BACK ? s <= lo : e >= hi) break;
   }
 }
 
@@ -85,7 +91,7 @@ __device__ __forceinline__ double part_squares(const T* p, int64_t n) {
     const float2 one[1] = {make_float2(to_f(p[tail + tid]), 0.f)};
     sum += squares(one);
   }
-  constexpr int U = 4;                     // vectors in flight
+  constexpr int U = kVectors;                   // vectors in flight
   int64_t i = tid;
   for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
     Raw<T, V> r[U];
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
   slice(h, &lo, &hi);
   double sum = 0.0;
   if (lo < hi)
-    walk(h, lo, hi, [&](int i, int64_t from, int64_t to) {
+    walk<false>(h, lo, hi, [&](int i, int64_t from, int64_t to) {
       if (h.dtype[h.first + i] == RNN_F32) sum += part_squares(static_cast<const float*>(ptr.in[i]) + from, to - from);
       else sum += part_squares(static_cast<const __nv_bfloat16*>(ptr.in[i]) + from, to - from);
     });
@@ -150,39 +156,47 @@ __device__ __forceinline__ float clip_factor(const double* partial, int parts, f
   return isfinite(n) && d > max_norm ? max_norm / d : 1.f;
 }
 
+// From the end of the part to its beginning: what the norm's kernel read last is still in
+// L2 (the last 126 MB of a long list), and outputs are stored past it.
 template <typename T>
 __device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, float f) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), U = kVectors;
   int64_t head = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
   if (head > n) head = n;
   // where the output lies otherwise on its boundaries, element by element
   const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
   const int64_t vecs = same ? (n - head) / V : 0, tail = head + vecs * V;
   const int tid = threadIdx.x;
-  if (tid < head) o[tid] = from_f<T>(to_f(p[tid]) * f);
   for (int64_t i = tail + tid; i < n; i += kThreads) o[i] = from_f<T>(to_f(p[i]) * f);
-  constexpr int U = 4;
-  int64_t i = tid;
-  for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
+  auto put = [&](const Raw<T, V>& r, int64_t i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      const float2 v = mul2(r.pair(j), both(f));
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 h = __float22bfloat162_rn(v);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[2 * j] = __float_as_uint(v.x);
+        w[2 * j + 1] = __float_as_uint(v.y);
+      }
+    }
+    __stcs(reinterpret_cast<uint4*>(o + head + i * V), make_uint4(w[0], w[1], w[2], w[3]));
+  };
+  int64_t i = vecs - 1 - tid;
+  for (; i - (U - 1) * kThreads >= 0; i -= U * kThreads) {
     Raw<T, V> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u].load(p + head + (i + u * kThreads) * V);
+    for (int u = 0; u < U; ++u) r[u].load(p + head + (i - u * kThreads) * V);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 v[V / 2];
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) v[j] = mul2(r[u].pair(j), both(f));
-      store_vec<T, V>(o + head + (i + u * kThreads) * V, v);
-    }
+    for (int u = 0; u < U; ++u) put(r[u], i - u * kThreads);
   }
-  for (; i < vecs; i += kThreads) {
+  for (; i >= 0; i -= kThreads) {
     Raw<T, V> r;
     r.load(p + head + i * V);
-    float2 v[V / 2];
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) v[j] = mul2(r.pair(j), both(f));
-    store_vec<T, V>(o + head + i * V, v);
+    put(r, i);
   }
+  if (tid < head) o[tid] = from_f<T>(to_f(p[tid]) * f);
 }
 
 template <int CAP>
@@ -193,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
   int64_t lo, hi;
   slice(h, &lo, &hi);
   if (lo >= hi) return;
-  walk(h, lo, hi, [&](int i, int64_t from, int64_t to) {
+  walk<true>(h, lo, hi, [&](int i, int64_t from, int64_t to) {
     // a factor of one leaves every element as it is: nothing to write in place
     if (f == 1.f && ptr.in[i] == ptr.out[i]) return;
     if (h.dtype[h.first + i] == RNN_F32)

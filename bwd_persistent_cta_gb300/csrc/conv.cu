@@ -107,7 +107,7 @@ struct Spot {
 };
 
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvFwdArgs f) {
+__global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const ConvFwdArgs f) {
   constexpr int U = kAhead, H = V / 2;
   const ConvArgs& a = f.a;
   const Spot<V> p(a);
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvFwdArgs f)
 // dp give sum_k w[k] dp_{t-k}, the gradient of extended row t (a row of the state for
 // t < W - 1, else token t - (W - 1)); x's window gives dw.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdArgs g) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) conv_bwd_kernel(const ConvBwdArgs g) {
   constexpr int U = kAhead, H = V / 2;
   __shared__ float fold[kThreads * V];
   const ConvArgs& a = g.a;

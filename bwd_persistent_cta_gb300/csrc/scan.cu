@@ -898,58 +898,88 @@ __global__ void __launch_bounds__(128) scan_sum_kernel(const ScanBwdArgs p) {
 // ---------------------------------------------------------------------------
 // the serving step
 // ---------------------------------------------------------------------------
-// SL lanes a channel, four states each.
+// SL lanes have CH = min(SL, 4) channels, four states of each a lane.  A lane prepares one
+// of the channels (its step, and at the end its output) and hands the step to the others.
+constexpr int kStepThreads = 128;
 template <typename T, int SL>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs p) {
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepArgs p) {
   const ScanArgs& a = p.a;
-  constexpr int PER = 256 / SL;
-  const int per = (a.D + PER - 1) / PER;
-  const int b = blockIdx.x / per, d = (blockIdx.x - b * per) * PER + threadIdx.x / SL, n0 = threadIdx.x % SL * 4;
-  const int len = a.len ? a.len[b] : a.T;
+  constexpr int CH = SL < 4 ? SL : 4, PER = kStepThreads / SL * CH;          // channels a CTA
+  const int dg = a.D / a.G, per = (dg + PER - 1) / PER, all = per * a.G;
+  const int b = blockIdx.x / all, tile = blockIdx.x - b * all, g = tile / per, sl = threadIdx.x % SL, n0 = sl * 4;
+  const int base = (tile - g * per) * PER + threadIdx.x / SL * CH, width = dg - base;    // of the group's channels; may be <= 0
+  const int mine = sl % CH, d = g * dg + base + mine;                        // the channel that the lane prepares
+  const bool own = mine < width, states = n0 < a.N;
   const int slot = p.slots ? p.slots[b] : b;
-  const bool in = d < a.D, live = slot >= 0 && slot < p.num_slots, st = in && live && n0 < a.N;
-  const int g = in ? d / (a.D / a.G) : 0;
-  float* at = p.state + (static_cast<int64_t>(slot) * a.D + d) * a.N + n0;
-  float4 h = make_float4(0.f, 0.f, 0.f, 0.f), A = h;
-  if (st) {
-    h = *reinterpret_cast<const float4*>(at);
-    A = *reinterpret_cast<const float4*>(a.A + static_cast<int64_t>(d) * a.N + n0);
+  const bool live = slot >= 0 && slot < p.num_slots;
+  const int n = live ? a.len ? a.len[b] : a.T : 0;
+  const int64_t at = static_cast<int64_t>(g * dg + base) * a.N + n0;
+  float* state = p.state + static_cast<int64_t>(live ? slot : 0) * a.D * a.N + at;
+  const float lift = sizeof(T) == 2 ? kLift : 0.f;
+  float4 h[CH], A[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    h[i] = A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < width && n > 0 && states) {
+      h[i] = *reinterpret_cast<const float4*>(state + static_cast<int64_t>(i) * a.N);
+      A[i] = *reinterpret_cast<const float4*>(a.A + at + static_cast<int64_t>(i) * a.N);
+    }
   }
-  const float bias = in && a.bias ? a.bias[d] : 0.f, skip = in && a.skip ? a.skip[d] : 0.f;
-  const int n = live ? len : 0;
+  const float bias = own && a.bias ? a.bias[d] : 0.f, skip = own && a.skip ? a.skip[d] : 0.f;
   for (int t = 0; t < a.T; ++t) {
     const int64_t r = a.row(b, t);
-    float y = 0.f;
-    if (t < n && in) {
-      const float xv = to_f(static_cast<const T*>(a.x)[r * a.x_row + d]);
-      float dv = to_f(static_cast<const T*>(a.dt)[r * a.dt_row + d]) + bias;
-      if (a.softplus) dv = softplus2<T>(both(dv)).x;
-      if (st) {
-        const T* Bp = static_cast<const T*>(a.Bm) + r * a.B_row + g * a.N + n0;
-        const T* Cp = static_cast<const T*>(a.Cm) + r * a.C_row + g * a.N + n0;
-        const float e = dv * kLog2e, u = dv * xv;
-        const float lift = sizeof(T) == 2 ? kLift : 0.f;
-        h.x = fmaf(decay<T>(fmaf(A.x, e, lift)), h.x, u * to_f(Bp[0]));
-        h.y = fmaf(decay<T>(fmaf(A.y, e, lift)), h.y, u * to_f(Bp[1]));
-        h.z = fmaf(decay<T>(fmaf(A.z, e, lift)), h.z, u * to_f(Bp[2]));
-        h.w = fmaf(decay<T>(fmaf(A.w, e, lift)), h.w, u * to_f(Bp[3]));
-        y = fmaf(to_f(Cp[3]), h.w, fmaf(to_f(Cp[2]), h.z, fmaf(to_f(Cp[1]), h.y, to_f(Cp[0]) * h.x)));
+    const bool on = t < n;
+    if (!on) {
+      if (own && sl < CH) static_cast<T*>(p.y)[r * a.D + d] = from_f<T>(0.f);
+      continue;                                          // the CTA's threads have one sequence
+    }
+    float xv = 0.f, dv = 0.f, zv = 0.f, Bv[4] = {}, Cv[4] = {};
+    if (own) {
+      xv = to_f(static_cast<const T*>(a.x)[r * a.x_row + d]);
+      dv = to_f(static_cast<const T*>(a.dt)[r * a.dt_row + d]);
+      if (a.z) zv = to_f(static_cast<const T*>(a.z)[r * a.z_row + d]);
+    }
+    if (states) {
+      const T *Bp = static_cast<const T*>(a.Bm) + r * a.B_row + g * a.N + n0, *Cp = static_cast<const T*>(a.Cm) + r * a.C_row + g * a.N + n0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        Bv[k] = to_f(Bp[k]);
+        Cv[k] = to_f(Cp[k]);
       }
     }
+    dv += bias;
+    if (a.softplus) dv = softplus2<T>(both(dv)).x;
+    const float e = dv * kLog2e, u = dv * xv;
+    float y[CH];
 #pragma unroll
-    for (int m = 1; m < SL; m <<= 1) y += __shfl_xor_sync(kFull, y, m);
-    if (in && threadIdx.x % SL == 0) {
-      if (t < n) {
-        y = fmaf(skip, to_f(static_cast<const T*>(a.x)[r * a.x_row + d]), y);
-        if (a.z) {
-          const float zv = to_f(static_cast<const T*>(a.z)[r * a.z_row + d]);
-          y *= zv * sigmoid2<T>(both(zv)).x;
-        }
-      }
-      static_cast<T*>(p.y)[r * a.D + d] = from_f<T>(t < n ? y : 0.f);
+    for (int i = 0; i < CH; ++i) {
+      const float ei = __shfl_sync(kFull, e, i, SL), ui = __shfl_sync(kFull, u, i, SL);
+      h[i].x = fmaf(decay<T>(fmaf(A[i].x, ei, lift)), h[i].x, ui * Bv[0]);
+      h[i].y = fmaf(decay<T>(fmaf(A[i].y, ei, lift)), h[i].y, ui * Bv[1]);
+      h[i].z = fmaf(decay<T>(fmaf(A[i].z, ei, lift)), h[i].z, ui * Bv[2]);
+      h[i].w = fmaf(decay<T>(fmaf(A[i].w, ei, lift)), h[i].w, ui * Bv[3]);
+      y[i] = fmaf(Cv[3], h[i].w, fmaf(Cv[2], h[i].z, fmaf(Cv[1], h[i].y, Cv[0] * h[i].x)));
+    }
+    // lane sl of each four ends up with the sum of channel sl
+    if constexpr (CH == 4) {
+      const bool up = sl & 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) y[i] = (up ? y[i + 2] : y[i]) + __shfl_xor_sync(kFull, up ? y[i] : y[i + 2], 2);
+    }
+    const bool odd = sl & 1;
+    float v = (odd ? y[1] : y[0]) + __shfl_xor_sync(kFull, odd ? y[0] : y[1], 1);
+#pragma unroll
+    for (int m = 4; m < SL; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
+    if (own && sl < CH) {
+      v = fmaf(skip, xv, v);
+      if (a.z) v *= zv * sigmoid2<T>(both(zv)).x;
+      static_cast<T*>(p.y)[r * a.D + d] = from_f<T>(v);
     }
   }
-  if (st && n > 0) *reinterpret_cast<float4*>(at) = h;
+  if (n > 0 && states)
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (i < width) *reinterpret_cast<float4*>(state + static_cast<int64_t>(i) * a.N) = h[i];
 }
 
 int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERROR; }
@@ -1043,8 +1073,8 @@ int bwd_t(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
 
 template <typename T, int SL>
 int step(const ScanStepArgs& p, cudaStream_t s) {
-  constexpr int PER = 256 / SL;
-  scan_step_kernel<T, SL><<<static_cast<unsigned>(p.a.B) * ((p.a.D + PER - 1) / PER), 256, 0, s>>>(p);
+  constexpr int PER = kStepThreads / SL * (SL < 4 ? SL : 4);
+  scan_step_kernel<T, SL><<<static_cast<unsigned>(p.a.B) * p.a.G * per_group(p.a, PER), kStepThreads, 0, s>>>(p);
   return check_launch();
 }
 template <typename T>
@@ -1066,8 +1096,7 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 ScanSplit scan_split(const ScanArgs& a, int backward) {
   const int width = backward ? bwd_width(a.N) : fwd_width(a.N), resident = (backward ? kBwdWarps : kFwdWarps) * a.num_sms;
   const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width);
-  int least = 64;
-  if (getenv("V_MIN")) least = atoi(getenv("V_MIN"));
+  constexpr int least = 32;
   int64_t n = warps >= (backward ? 4 : 5) * a.num_sms ? 1 : (backward ? 3 : 2) * resident / warps;
   if (n > a.T / least) n = a.T / least;
   if (n < 3) n = 1;
