@@ -34,72 +34,35 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
-// 2^x.  bf16 storage takes the hardware's approximation, which is 5e-9 (|x| near
-// 1e-3) to 3e-8 (0.01 to 1) low on average: kLift, added to the exponent by the same
-// instruction that scales it, takes the middle of that out (states of 77 tokens, error
-// against 64 bits: 1.3e-6 without, 5.5e-7 with; training's dA 1.9e-6 and 1.0e-6).  fp32
-// storage takes the Taylor series of e^(f ln 2) on |f| <= 1/2, whose
-// last rounding is of 1 + something small: half a step, and no bias that a memory of
-// a thousand tokens would add up.  The ninth term is below 2^-27.
-template <typename T>
-__device__ __forceinline__ float decay(float x) {
-  if constexpr (sizeof(T) == 2) {
-    return ex2(x);
-  } else {
-    const float r = rintf(x), u = (x - r) * kLn2;
-    float p = 1.f / 40320.f;
-    p = fmaf(p, u, 1.f / 5040.f);
-    p = fmaf(p, u, 1.f / 720.f);
-    p = fmaf(p, u, 1.f / 120.f);
-    p = fmaf(p, u, 1.f / 24.f);
-    p = fmaf(p, u, 1.f / 6.f);
-    p = fmaf(p, u, 0.5f);
-    p = fmaf(p, u, 1.f);
-    p = fmaf(p, u, 1.f);
-    // in two steps, so that results below and above the normal range round as they should
-    const float half = fminf(fmaxf(r, -250.f), 250.f) * 0.5f;
-    const int i = __float2int_rd(half), j = __float2int_ru(half);
-    const float s = __int_as_float((i + 127) << 23), t = __int_as_float((j + 127) << 23);
-    return x != x || r < -250.f || r > 250.f ? ex2(x) : p * s * t;
-  }
+// A token's decay 2^(A log2(e) delta), two states at a time, by the hardware's
+// approximation, which is 5e-9 (|x| near 1e-3) to 3e-8 (0.01 to 1) low on average: kLift,
+// added to the exponent by the same instruction that scales it, takes the middle of that
+// out, or a memory of many tokens would add it up (states of 77 tokens, error against 64
+// bits: 1.3e-6 without, 5.5e-7 with; training's dA 1.9e-6 and 9e-7).  A polynomial in fp32
+// that has no bias at all costs three times the whole recurrence in multiply-adds: 2.5
+// instead of 0.5 ms for 8 x 1024 tokens of 2048 channels and 32 states, and buys 1e-7.
+__device__ __forceinline__ float2 decay2(float2 A2, float d) {
+  const float2 x = fma2(A2, both(d), both(kLift));
+  return make_float2(ex2(x.x), ex2(x.y));
 }
 
-// The exponent of a token's decay: A log2(e) times its step.
-template <typename T>
-__device__ __forceinline__ float2 step2(float2 A2, float d) {
-  if constexpr (sizeof(T) == 2) return fma2(A2, both(d), both(kLift));
-  else return mul2(A2, both(d));
-}
-template <typename T>
-__device__ __forceinline__ float2 decay2(float2 x) { return make_float2(decay<T>(x.x), decay<T>(x.y)); }
-
-// log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v|, two at a time.  bf16 storage: log(1 + q)
-// is 2 artanh(s), s = q / (2 + q) <= 1/3, as s times a polynomial in s^2 (interpolated at
+// log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v|, two at a time.  log(1 + q) is
+// 2 artanh(s), s = q / (2 + q) <= 1/3, as s times a polynomial in s^2 (interpolated at
 // the Chebyshev nodes of [0, 1/9], off by 4e-9): relative accuracy at small steps, in a
 // third of log1pf's instructions.
-template <typename T>
 __device__ __forceinline__ float2 softplus2(float2 v) {
-  if constexpr (sizeof(T) == 2) {
-    const float2 q = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
-    const float2 d = add2(q, both(2.f)), s = mul2(q, make_float2(rcp(d.x), rcp(d.y))), w = mul2(s, s);
-    float2 p = fma2(both(0.28157778f), w, both(0.27965158f));
-    p = fma2(p, w, both(0.40024596f));
-    p = fma2(p, w, both(0.66666322f));
-    p = fma2(p, w, both(2.f));
-    return fma2(p, s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));       // a NaN comes in through s
-  } else {
-    return make_float2(fmaxf(v.x, 0.f) + log1pf(expf(-fabsf(v.x))), fmaxf(v.y, 0.f) + log1pf(expf(-fabsf(v.y))));
-  }
+  const float2 q = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+  const float2 d = add2(q, both(2.f)), s = mul2(q, make_float2(rcp(d.x), rcp(d.y))), w = mul2(s, s);
+  float2 p = fma2(both(0.28157778f), w, both(0.27965158f));
+  p = fma2(p, w, both(0.40024596f));
+  p = fma2(p, w, both(0.66666322f));
+  p = fma2(p, w, both(2.f));
+  return fma2(p, s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));         // a NaN comes in through s
 }
-// 1 / (1 + e^-v): with bf16 storage from the approximations, a few 2^-23 off.
-template <typename T>
+// 1 / (1 + e^-v) from the approximations, a few 2^-23 off.
 __device__ __forceinline__ float2 sigmoid2(float2 v) {
-  if constexpr (sizeof(T) == 2) {
-    const float2 q = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(q.x), ex2(q.y)), both(1.f));
-    return make_float2(rcp(d.x), rcp(d.y));
-  } else {
-    return make_float2(sigm(v.x), sigm(v.y));
-  }
+  const float2 q = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(q.x), ex2(q.y)), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
 
 template <int V>
@@ -256,7 +219,7 @@ struct Rows {
 };
 
 // Adds one segment's own end to what went through it: h = exp(A sum) h + end.
-template <typename T, int C, int NS>
+template <int C, int NS>
 __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanArgs& a, const ScanSegs& g,
                                         int b, int i, int c0, int ch, int n0, int width) {
   const int64_t at = (static_cast<int64_t>(b) * g.nseg + i) * a.D + c0;
@@ -266,7 +229,7 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
   for (int c = 0; c < C; ++c) {
     const float sum = ch + c < width ? g.sums[at + ch + c] : 0.f;
 #pragma unroll
-    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<T>(mul2(A2[c][j], both(sum))), h[c][j], e[c][j]);
+    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2(A2[c][j], sum), h[c][j], e[c][j]);
   }
 }
 
@@ -369,7 +332,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
   }
   if (OUT)
 #pragma unroll 2
-    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<T, C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
+    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int j = 0; j < 4; ++j) sum[j] = both(0.f);
   float* pu = MODE == kTrain && gate ? f.ungated + row0 * a.D + w.c0 + col : nullptr;
@@ -387,7 +350,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
       for (int j = 0; j < 4; ++j) d[j] = add2(dt.pair(j), d[j]);
       if (a.softplus)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = softplus2<T>(d[j]);
+        for (int j = 0; j < 4; ++j) d[j] = softplus2(d[j]);
       if (row >= n)                                    // behind the last token: changes nothing
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = both(0.f);
@@ -400,7 +363,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
       if (BACK && gate) {
         const Raw<T, 8> z = s.raw[stage][2][lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
+        for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], mul2(z.pair(j), sigmoid2(z.pair(j))));
       }
       store_vec<float, 8>(&s.dx[row][col], u);
     }
@@ -431,7 +394,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
           float2 r = both(0.f);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            const float2 e = decay2<T>(step2<T>(A2[c][j], d[c]));
+            const float2 e = decay2(A2[c][j], d[c]);
             if (BACK) h[c][j] = mul2(e, fma2(Bv[j], both(u[c]), h[c][j]));
             else h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
             if (OUT) r = j ? fma2(Cv[j], h[c][j], r) : mul2(Cv[j], h[c][j]);
@@ -463,7 +426,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
           const Raw<T, 8> z = s.raw[stage][2][lane];
           if (MODE == kTrain) store_vec<float, 8>(pu, v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], mul2(z.pair(j), sigmoid2<T>(z.pair(j))));
+          for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], mul2(z.pair(j), sigmoid2(z.pair(j))));
         }
         if (row >= n)
 #pragma unroll
@@ -639,7 +602,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
   load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
 #pragma unroll 2
   for (int i = p.g.nseg - 1; i > w.seg; --i)
-    if (i * p.g.len < len) through<T, C, NS>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
+    if (i * p.g.len < len) through<C, NS>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -668,7 +631,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
       for (int j = 0; j < 4; ++j) d[j] = add2(dt.pair(j), d[j]);
       if (a.softplus)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = softplus2<T>(d[j]);
+        for (int j = 0; j < 4; ++j) d[j] = softplus2(d[j]);
       if (t >= n)                                      // behind the last token: changes nothing
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = both(0.f);
@@ -683,7 +646,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
         const Raw<T, 8> z = s.raw[stage][2][i][lane];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          d[j] = sigmoid2<T>(z.pair(j));
+          d[j] = sigmoid2(z.pair(j));
           o[j] = mul2(o[j], mul2(z.pair(j), d[j]));
         }
         store_vec<float, 8>(&s.sg[t][col], d);
@@ -716,7 +679,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            e[q][c][j] = decay2<T>(step2<T>(A2[c][j], d[c]));
+            e[q][c][j] = decay2(A2[c][j], d[c]);
             h[q + 1][c][j] = fma2(e[q][c][j], h[q][c][j], mul2(Bv[j], both(u[c])));
           }
       }
@@ -792,7 +755,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
       if (a.softplus) {
         lds2<4>(r, &s.bias[col]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], sigmoid2<T>(add2(dt.pair(j), r[j])));
+        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], sigmoid2(add2(dt.pair(j), r[j])));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -915,7 +878,6 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
   const int n = live ? a.len ? a.len[b] : a.T : 0;
   const int64_t at = static_cast<int64_t>(g * dg + base) * a.N + n0;
   float* state = p.state + static_cast<int64_t>(live ? slot : 0) * a.D * a.N + at;
-  const float lift = sizeof(T) == 2 ? kLift : 0.f;
   float4 h[CH], A[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -948,16 +910,16 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
       }
     }
     dv += bias;
-    if (a.softplus) dv = softplus2<T>(both(dv)).x;
+    if (a.softplus) dv = softplus2(both(dv)).x;
     const float e = dv * kLog2e, u = dv * xv;
     float y[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const float ei = __shfl_sync(kFull, e, i, SL), ui = __shfl_sync(kFull, u, i, SL);
-      h[i].x = fmaf(decay<T>(fmaf(A[i].x, ei, lift)), h[i].x, ui * Bv[0]);
-      h[i].y = fmaf(decay<T>(fmaf(A[i].y, ei, lift)), h[i].y, ui * Bv[1]);
-      h[i].z = fmaf(decay<T>(fmaf(A[i].z, ei, lift)), h[i].z, ui * Bv[2]);
-      h[i].w = fmaf(decay<T>(fmaf(A[i].w, ei, lift)), h[i].w, ui * Bv[3]);
+      h[i].x = fmaf(ex2(fmaf(A[i].x, ei, kLift)), h[i].x, ui * Bv[0]);
+      h[i].y = fmaf(ex2(fmaf(A[i].y, ei, kLift)), h[i].y, ui * Bv[1]);
+      h[i].z = fmaf(ex2(fmaf(A[i].z, ei, kLift)), h[i].z, ui * Bv[2]);
+      h[i].w = fmaf(ex2(fmaf(A[i].w, ei, kLift)), h[i].w, ui * Bv[3]);
       y[i] = fmaf(Cv[3], h[i].w, fmaf(Cv[2], h[i].z, fmaf(Cv[1], h[i].y, Cv[0] * h[i].x)));
     }
     // lane sl of each four ends up with the sum of channel sl
@@ -972,7 +934,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
     for (int m = 4; m < SL; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
     if (own && sl < CH) {
       v = fmaf(skip, xv, v);
-      if (a.z) v *= zv * sigmoid2<T>(both(zv)).x;
+      if (a.z) v *= zv * sigmoid2(both(zv)).x;
       static_cast<T*>(p.y)[r * a.D + d] = from_f<T>(v);
     }
   }
