@@ -2,8 +2,10 @@
 // clipping: descriptor and argument checks, buffer sizes and the launches of each call.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "api_util.h"
@@ -40,6 +42,7 @@ struct rnn_clip_s {
   int* d_dtype;
   std::vector<int64_t> start;
   std::vector<int> dtype;
+  std::vector<std::pair<uintptr_t, uintptr_t>> ranges;    // scratch of a call's checks
   CallOrder order;
   uint64_t launches;
 };
@@ -140,6 +143,21 @@ rnn_status_t make(H** out) {
   return RNN_OK;
 }
 
+// Whether two of the tensors that a call writes share memory (a tensor listed twice would
+// be scaled once or twice, as it happens).
+bool overlap(rnn_clip_t h, const void* const* out) {
+  auto& r = h->ranges;
+  r.clear();                                             // holds num of them without allocating
+  for (int i = 0; i < h->num; ++i) {
+    const uint64_t bytes = static_cast<uint64_t>(h->start[i + 1] - h->start[i]) * (h->dtype[i] == RNN_F32 ? 4 : 2);
+    if (bytes) r.emplace_back(reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + bytes);
+  }
+  if (!std::is_sorted(r.begin(), r.end())) std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return true;
+  return false;
+}
+
 rnn_status_t clip_call(rnn_clip_t h, const void* const* grads, void* const* out, float max_norm, float eps, float* norm,
                        void* workspace, void* stream, int scale) {
   if (!h || !grads || !norm || !aligned(norm, 4)) return RNN_BAD_PARAM;
@@ -150,6 +168,7 @@ rnn_status_t clip_call(rnn_clip_t h, const void* const* grads, void* const* out,
     if (!grads[i] || !aligned(grads[i], es)) return RNN_BAD_PARAM;
     if (out && (!out[i] || !aligned(out[i], es))) return RNN_BAD_PARAM;
   }
+  if (scale && overlap(h, out ? static_cast<const void* const*>(out) : grads)) return RNN_BAD_PARAM;
   if (!workspace || !aligned16(workspace)) return RNN_BAD_WORKSPACE;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
@@ -415,6 +434,7 @@ rnn_status_t rnn_clip_create(int num, const int64_t* counts, const int* dtypes, 
   if (rc != RNN_OK) return rc;
   try {
     h->dtype.assign(dtypes, dtypes + num);
+    h->ranges.reserve(num);
     h->start.assign(1, 0);
     h->start.reserve(num + 1);
     for (int i = 0; i < num; ++i) h->start.push_back(h->start[i] + counts[i]);

@@ -545,7 +545,7 @@ uint64_t rnn_norm_launch_count(rnn_norm_t handle);
  * Calls that should overlap take a handle each. */
 typedef struct {
   int batch;           /* B >= 1                                                       */
-  int seq_len;         /* T >= 1                                                       */
+  int seq_len;         /* T >= 1; batch * seq_len * channels at most 2^43              */
   int channels;        /* 8..65536, a multiple of 8 * groups                           */
   int states;          /* 8..64, a multiple of 8                                       */
   int groups;          /* >= 1                                                         */
@@ -588,7 +588,8 @@ typedef struct {
 
 /* As rnn_delta_create / _destroy / _get_sizes / _set_seq_lengths: tokens at
  * t >= lengths[b] are not read, the state stays as it was, y is zero there and so
- * are all gradients. */
+ * are all gradients.  The reserve holds the states before every four tokens and y
+ * before its gate: channels * (states + 4) bytes a token. */
 rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* handle);
 rnn_status_t rnn_scan_destroy(rnn_scan_t handle);
 rnn_status_t rnn_scan_get_sizes(rnn_scan_t handle, size_t* workspace_bytes,
@@ -697,12 +698,13 @@ rnn_status_t rnn_clip_get_sizes(rnn_clip_t handle, size_t* workspace_bytes);
 
 /*   grads    host array of num device pointers, aligned to their element only; those of
  *            empty tensors are not looked at
- *   out      the same, or NULL = in place; entry i may be grads[i], no other overlap
+ *   out      the same, or NULL = in place; entry i may be grads[i], and overlaps no other
+ *            grads.  Tensors written twice (a tensor listed twice in place, slices that
+ *            overlap) are RNN_BAD_PARAM
  *   max_norm, eps  finite, >= 0
- *   norm     device fp32 [1] (out)
+ *   norm     device fp32 [1] (out), 4-byte aligned
  *   workspace (workspace_bytes); calls of a handle run in the order they are made
- * With out == NULL and max_norm == 0 the tensors become zero; rnn_clip_norm only
- * writes the norm. */
+ * rnn_clip_norm only writes the norm. */
 rnn_status_t rnn_clip_scale(rnn_clip_t handle, const void* const* grads, void* const* out, float max_norm,
                             float eps, float* norm, void* workspace, void* stream);
 rnn_status_t rnn_clip_norm(rnn_clip_t handle, const void* const* grads, float* norm, void* workspace,

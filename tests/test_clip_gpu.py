@@ -170,6 +170,12 @@ def test_refusals():
         assert call(**kw) == bad, kw
     for kw in (dict(work=None), dict(work=ws.data_ptr() + 8)):
         assert call(**kw) == R.RNN_BAD_WORKSPACE, kw
+    # memory that two tensors share is not written; the norm of such a list is still one
+    for kw in (dict(grads=(p, None, p + 398)), dict(grads=(p, None, p)), dict(out=(p + 1024, None, p + 1022)),
+               dict(out=(p + 1024, None, p + 1422))):
+        assert call(**kw) == bad, kw
+    assert call(grads=(p, None, p + 400)) == R.RNN_OK and call(grads=(p, None, p), out=(p, None, p + 1024)) == R.RNN_OK
+    assert R.rnn_clip_norm(op.handle, (p, None, p), p + 2048, ws.data_ptr()) == R.RNN_OK
     assert R.rnn_clip_norm(op.handle, (p, None, None), p + 2048, ws.data_ptr()) == bad
     t = [torch.zeros(100, device="cuda"), torch.zeros(0, device="cuda"), torch.zeros(50, device="cuda").bfloat16()]
     for wrong in (t[:2], [t[0], t[1], t[2].float()], [t[0][:50], t[1], t[2]], [t[0], t[1], torch.zeros(50).bfloat16()],
