@@ -4,6 +4,7 @@ entry points under their own names, and ``SelectiveScan`` / ``CausalConv`` /
 pointers) and call them.  ``include/rnn.h`` has the definitions."""
 from __future__ import annotations
 
+import array
 import ctypes
 
 from . import (RNN_BF16, RNN_F32, RNN_GATE_NONE, RNN_GATE_SILU, RNN_OK, RnnError, _p, _P, lib, rnn_conv_desc_t,
@@ -124,16 +125,23 @@ def rnn_clip_get_sizes(handle: int) -> int:
 
 
 def _pointers(ptrs):
-    return None if ptrs is None else (_P * len(ptrs))(*ptrs)
+    """A host array of the pointers (None stands for NULL)."""
+    return None if ptrs is None else array.array("Q", [p or 0 for p in ptrs])
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def rnn_clip_scale(handle, grads, out, max_norm, eps, norm, workspace, stream=None) -> int:
     """grads, out: device pointers of each tensor (out may be None)."""
-    return lib().rnn_clip_scale(handle, _pointers(grads), _pointers(out), max_norm, eps, norm, workspace, stream)
+    g, o = _pointers(grads), _pointers(out)
+    return lib().rnn_clip_scale(handle, _address(g), _address(o), max_norm, eps, norm, workspace, stream)
 
 
 def rnn_clip_norm(handle, grads, norm, workspace, stream=None) -> int:
-    return lib().rnn_clip_norm(handle, _pointers(grads), norm, workspace, stream)
+    g = _pointers(grads)
+    return lib().rnn_clip_norm(handle, _address(g), norm, workspace, stream)
 
 
 def rnn_clip_launch_count(handle) -> int:
@@ -151,10 +159,17 @@ class _Sequences(_Op):
             raise ValueError("one length per sequence of the batch")
         self._check(self._lengths(self.handle, lengths), self._lengths.__name__)
 
-    def _out(self, t, name, shape, dtype=None):
+    def _out(self, t, name, like):
+        """The output ``t``, or a new one of the shape and dtype of the input ``like``."""
         if t is None:
-            return self.torch.empty(shape, dtype=dtype or self.tdtype, device=self.device)
-        self._want(t, name, shape, dtype)
+            return self._dense_like(like)
+        self._want(t, name, like.shape)
+        return t
+
+    def _state(self, t, name, dtype):
+        if t is None:
+            return self.torch.empty(self._s, dtype=dtype, device=self.device)
+        self._want(t, name, self._s, dtype)
         return t
 
     def _pool(self, state, slots, shape, dtype):
@@ -226,7 +241,7 @@ class SelectiveScan(_Sequences):
         f32 = self.torch.float32
         a = self._inputs(x, dt, A, B, C, z, D, dt_bias)
         self._want(h0, "h0", self._s, f32)
-        y, hT = self._out(y, "y", self._x), self._out(hT, "hT", self._s, f32)
+        y, hT = self._out(y, "y", x), self._state(hT, "hT", f32)
         raw = self._on()
         ws = self._scratch("workspace", self.workspace_bytes, raw) if self.workspace_bytes else None
         rs = self._scratch("reserve", self.reserve_bytes, raw) if train else None
@@ -247,12 +262,10 @@ class SelectiveScan(_Sequences):
         a = self._inputs(x, dt, A, B, C, z, D, dt_bias)
         self._want(dy, "dy", self._x)
         self._want(dhT, "dhT", self._s, f32)
-        new = self._out
-        out = {"dx": new(None, "", self._x), "ddt": new(None, "", self._x),
-               "dz": None if z is None else new(None, "", self._x),
-               "dB": new(None, "", self._bc), "dC": new(None, "", self._bc), "dA": new(None, "", self._a, f32),
-               "dD": None if D is None else new(None, "", self._d, f32),
-               "ddt_bias": None if dt_bias is None else new(None, "", self._d, f32), "dh0": new(None, "", self._s, f32)}
+        new = self._dense_like
+        out = {"dx": new(x), "ddt": new(x), "dz": None if z is None else new(x), "dB": new(B), "dC": new(B), "dA": new(A),
+               "dD": None if D is None else new(D), "ddt_bias": None if dt_bias is None else new(dt_bias),
+               "dh0": self._state(None, "dh0", f32)}
         raw = self._on()
         ws = self._scratch("backward_workspace", self.backward_workspace_bytes, raw)
         rs = self._scratch("reserve", self.reserve_bytes, raw)
@@ -268,7 +281,7 @@ class SelectiveScan(_Sequences):
             return self._elsewhere(self.step, stream, x, dt, A, B, C, state, z=z, D=D, dt_bias=dt_bias, slots=slots, y=y)
         a = self._inputs(x, dt, A, B, C, z, D, dt_bias)
         n = self._pool(state, slots, self._a, self.torch.float32)
-        y = self._out(y, "y", self._x)
+        y = self._out(y, "y", x)
         rc = rnn_scan_step(self.handle, a, state.data_ptr(), n, _p(slots), y.data_ptr(), self._on())
         self._check(rc, "rnn_scan_step")
         return y
@@ -320,7 +333,7 @@ class CausalConv(_Sequences):
             return self._elsewhere(self.forward, stream, x, w, bias=bias, s0=s0, y=y, sT=sT)
         a = self._inputs(x, w, bias)
         self._want(s0, "s0", self._s)
-        y, sT = self._out(y, "y", self._x), self._out(sT, "sT", self._s)
+        y, sT = self._out(y, "y", x), self._state(sT, "sT", self.tdtype)
         rc = rnn_conv_forward(self.handle, a, _p(s0), y.data_ptr(), sT.data_ptr(), self._on())
         self._check(rc, "rnn_conv_forward")
         return y, sT
@@ -337,9 +350,9 @@ class CausalConv(_Sequences):
         self._want(dy, "dy", self._x)
         self._want(s0, "s0", self._s)
         self._want(dsT, "dsT", self._s)
-        new = self._out
-        out = {"dx": new(None, "", self._x), "dw": new(None, "", self._w, f32),
-               "dbias": None if bias is None else new(None, "", self._b, f32), "ds0": new(None, "", self._s)}
+        torch = self.torch
+        out = {"dx": self._dense_like(x), "dw": torch.empty_like(w, dtype=f32),
+               "dbias": None if bias is None else torch.empty_like(bias, dtype=f32), "ds0": self._state(None, "ds0", self.tdtype)}
         raw = self._on()
         ws = self._scratch("backward_workspace", self.backward_workspace_bytes, raw)
         rc = rnn_conv_backward(self.handle, a, _p(s0), dy.data_ptr(), _p(dsT), *(_p(t) for t in out.values()), _p(ws), raw)
@@ -353,7 +366,7 @@ class CausalConv(_Sequences):
             return self._elsewhere(self.step, stream, x, w, state, bias=bias, slots=slots, y=y)
         a = self._inputs(x, w, bias)
         n = self._pool(state, slots, self._s[1:], self.tdtype)
-        y = self._out(y, "y", self._x)
+        y = self._out(y, "y", x)
         rc = rnn_conv_step(self.handle, a, state.data_ptr(), n, _p(slots), y.data_ptr(), self._on())
         self._check(rc, "rnn_conv_step")
         return y
