@@ -12,6 +12,8 @@
 #include "pair.cuh"
 #include "vec.cuh"
 
+#include <type_traits>
+
 namespace rnn {
 
 namespace {
@@ -106,7 +108,7 @@ struct Spot {
   }
 };
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const ConvFwdArgs f) {
   constexpr int U = kAhead, H = V / 2;
   const ConvArgs& a = f.a;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const ConvFwdArgs
         v[j] = bias[j];
 #pragma unroll
         for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], win[k][j], v[j]);
-        if (a.silu) v[j] = mul2(v[j], sigm2<T>(v[j]));
+        if (SILU) v[j] = mul2(v[j], sigm2<T>(v[j]));
         if (t + i >= len) v[j] = both(0.f);
       }
       if (t + i < t1) store_vec<T, V>(py + i * hop * a.D, v);
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_fwd_kernel(const ConvFwdArgs
 // The gradients.  With dp_t = dy_t act'(pre_t): walking t forward, the last W values of
 // dp give sum_k w[k] dp_{t-k}, the gradient of extended row t (a row of the state for
 // t < W - 1, else token t - (W - 1)); x's window gives dw.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) conv_bwd_kernel(const ConvBwdArgs g) {
   constexpr int U = kAhead, H = V / 2;
   __shared__ float fold[kThreads * V];
@@ -212,7 +214,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) conv_bwd_ker
 #pragma unroll
     for (int k = 1; k < W; ++k) unpack<T, V>(win[k], q[k]);
     T* pdx = static_cast<T*>(g.dx) + (row0 - (W - 1) * hop) * a.D + p.d;
-    for (int t = t0; t < stop; t += U) {
+    // U rows; INSIDE: all of them valid tokens of the stretch, whose rows out are tokens of
+    // it too (U >= W - 1, so all but the first and the last ones)
+    static_assert(U >= W - 1, "the rows out of the second U are tokens of the stretch");
+    auto rows = [&](auto inside, int t) {
+      constexpr bool INSIDE = decltype(inside)::value;
       Raw<T, V> x[U], d[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) conv_bwd_ker
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int e = t + i;
-        const bool ok = e < len;
+        const bool ok = INSIDE || e < len;
 #pragma unroll
         for (int k = 0; k + 1 < W; ++k)
 #pragma unroll
@@ -236,43 +242,52 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) conv_bwd_ker
         for (int j = 0; j < H; ++j) {
           win[W - 1][j] = x[i].pair(j);
           dp[0][j] = d[i].pair(j);
-          if (a.silu) {
+          if (SILU) {
             float2 pre = bias[j];
 #pragma unroll
             for (int k = 0; k < W; ++k) pre = fma2(w[k][j], win[k][j], pre);
             const float2 s = sigm2<T>(pre);
             // s + pre s (1 - s)
-            dp[0][j] = mul2(dp[0][j], fma2(mul2(pre, s), make_float2(1.f - s.x, 1.f - s.y), s));
+            dp[0][j] = mul2(dp[0][j], fma2(mul2(pre, s), add2(both(1.f), mul2(s, both(-1.f))), s));
           }
           if (!ok) dp[0][j] = both(0.f);
           // the tokens behind the stretch belong to the next one's sums
-          if (ok && e < t1) {
+          if (INSIDE || (ok && e < t1)) {
 #pragma unroll
             for (int k = 0; k < W; ++k) dw[k][j] = fma2(dp[0][j], win[k][j], dw[k][j]);
             dw[W][j] = add2(dw[W][j], dp[0][j]);
           }
-          v[j] = both(0.f);
+          v[j] = mul2(w[0][j], dp[0][j]);
 #pragma unroll
-          for (int k = 0; k < W; ++k) v[j] = fma2(w[k][j], dp[k][j], v[j]);
+          for (int k = 1; k < W; ++k) v[j] = fma2(w[k][j], dp[k][j], v[j]);
         }
-        // extended row e of the state's gradient out
-        if (e >= len && e < len + W - 1 && g.dsT) {
-          Raw<T, V> r;
-          r.load(static_cast<const T*>(g.dsT) + (static_cast<int64_t>(p.b) * (W - 1) + e - len) * a.D + p.d);
+        if (INSIDE) {
+          if (g.dx) store_vec<T, V>(pdx, v);
+        } else {
+          // extended row e of the state's gradient out
+          if (e >= len && e < len + W - 1 && g.dsT) {
+            Raw<T, V> r;
+            r.load(static_cast<const T*>(g.dsT) + (static_cast<int64_t>(p.b) * (W - 1) + e - len) * a.D + p.d);
 #pragma unroll
-          for (int j = 0; j < H; ++j) v[j] = add2(v[j], r.pair(j));
-        }
-        if (e >= t0 + W - 1) {
-          if (e - (W - 1) >= len)
+            for (int j = 0; j < H; ++j) v[j] = add2(v[j], r.pair(j));
+          }
+          if (e >= t0 + W - 1) {
+            if (e - (W - 1) >= len)
 #pragma unroll
-            for (int j = 0; j < H; ++j) v[j] = both(0.f);
-          if (g.dx && e < stop) store_vec<T, V>(pdx + i * hop * a.D, v);
-        } else if (p.seg == 0 && g.ds0) {
-          store_vec<T, V>(static_cast<T*>(g.ds0) + (static_cast<int64_t>(p.b) * (W - 1) + e) * a.D + p.d, v);
+              for (int j = 0; j < H; ++j) v[j] = both(0.f);
+            if (g.dx && e < stop) store_vec<T, V>(pdx, v);
+          } else if (p.seg == 0 && g.ds0) {
+            store_vec<T, V>(static_cast<T*>(g.ds0) + (static_cast<int64_t>(p.b) * (W - 1) + e) * a.D + p.d, v);
+          }
         }
+        pdx += hop * a.D;
       }
-      pdx += U * hop * a.D;
-    }
+    };
+    rows(std::false_type{}, t0);
+    int t = t0 + U;
+    const int valid = len < t1 ? len : t1;
+    for (; t + U <= valid; t += U) rows(std::true_type{}, t);
+    for (; t < stop; t += U) rows(std::false_type{}, t);
   }
   if (!g.partial) return;
   // the CTA's stretches, in order
@@ -365,13 +380,17 @@ constexpr int kBwdV = 4;
 template <typename T, int W>
 int fwd(const ConvFwdArgs& f, cudaStream_t s) {
   using S = Spot<kFwdV<T>>;
-  conv_fwd_kernel<T, W, kFwdV<T>><<<static_cast<unsigned>(S::parts(f.a)) * S::spans(f.a), kThreads, 0, s>>>(f);
+  const unsigned grid = static_cast<unsigned>(S::parts(f.a)) * S::spans(f.a);
+  if (f.a.silu) conv_fwd_kernel<T, W, kFwdV<T>, true><<<grid, kThreads, 0, s>>>(f);
+  else conv_fwd_kernel<T, W, kFwdV<T>, false><<<grid, kThreads, 0, s>>>(f);
   return check_launch();
 }
 template <typename T, int W>
 int bwd(const ConvBwdArgs& b, cudaStream_t s) {
   using S = Spot<kBwdV>;
-  conv_bwd_kernel<T, W, kBwdV><<<static_cast<unsigned>(S::parts(b.a)) * S::spans(b.a), kThreads, 0, s>>>(b);
+  const unsigned grid = static_cast<unsigned>(S::parts(b.a)) * S::spans(b.a);
+  if (b.a.silu) conv_bwd_kernel<T, W, kBwdV, true><<<grid, kThreads, 0, s>>>(b);
+  else conv_bwd_kernel<T, W, kBwdV, false><<<grid, kThreads, 0, s>>>(b);
   return check_launch();
 }
 template <typename T, int W>
