@@ -13,6 +13,8 @@
 #include "scan.h"
 #include "vec.cuh"
 
+#include <algorithm>
+
 namespace rnn {
 
 namespace {
@@ -946,7 +948,7 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 
 // Lanes a channel: eight states each forward, four backward, rounded up to a power of two.
 int fwd_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
-int fwd_width(int N) { return (N <= 16 ? 32 : 64) / fwd_lanes(N); }      // channels a warp
+int fwd_width(int N, bool split) { return (N <= 8 || (N <= 16 && !split) ? 32 : 64) / fwd_lanes(N); }
 int bwd_width(int N) { return kBC * 16 / fwd_lanes(N); }
 int per_group(const ScanArgs& a, int width) { return (a.D / a.G + width - 1) / width; }
 
@@ -969,7 +971,7 @@ template <typename T>
 int fwd_t(const ScanFwdArgs& f, cudaStream_t s, int* launches) {
   switch (fwd_lanes(f.a.N)) {
     case 1: return fwd<T, 1, 1>(f, s, launches);
-    case 2: return fwd<T, 2, 1>(f, s, launches);
+    case 2: return f.g.nseg > 1 ? fwd<T, 2, 2>(f, s, launches) : fwd<T, 2, 1>(f, s, launches);
     case 4: return fwd<T, 4, 2>(f, s, launches);
     default: return fwd<T, 8, 2>(f, s, launches);
   }
@@ -1003,7 +1005,7 @@ int bwd_t(const ScanBwdArgs& p, cudaStream_t s, int* launches) {
   int rc;
   switch (fwd_lanes(a.N)) {
     case 1: rc = bwd<T, 1, 1>(p, s, launches); break;
-    case 2: rc = bwd<T, 2, 1>(p, s, launches); break;
+    case 2: rc = bwd<T, 2, 2>(p, s, launches); break;
     case 4: rc = bwd<T, 4, 2>(p, s, launches); break;
     default: rc = bwd<T, 8, 2>(p, s, launches);
   }
@@ -1055,19 +1057,26 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 
 // Segments.  Forward, a warp's tokens follow one another every 85 to 110 ns as long as a
 // scheduler has at most two warps, and a second pass over the tokens (what each segment
-// leaves by itself) costs half as much again: 8 sequences of 2048 channels (1024 warps),
-// 1000 tokens, 108 us in one piece and 147 in two; 1 x 4096 channels (256 warps), 16384
-// tokens, 1.4 ms in one piece, 614 us in 6, 547 in 14, 555 in 28.  So they begin below five
-// warps an SM, and fill the SMs about twice.  Backward, where an SM holds eight warps: 512
-// warps, 2048 tokens, 744 us in one piece, 648 in 2, 625 in 8; from four warps an SM on it
-// is in one piece.  A segment has 32 tokens at least (513 tokens of 3 x 528 channels, fp32,
-// when a token still cost three times as much: 309 us with 64, 224 with 32, 265 with 16).
+// leaves by itself) costs half as much again: 8 sequences of 2048 channels (1024 warps of 16
+// channels), 1000 tokens, 108 us in one piece and 147 in two; 4 of 2048 tokens (512 warps),
+// 200 in one piece and 150 in eight; 1 x 4096 channels (256 warps), 16384 tokens, 1.4 ms in
+// one piece, 610 us in 8, 500 in 14, 506 in 28.  So they begin below five warps an SM, then
+// of 32 channels (two a lane: 547 and 500 us in 14 pieces), and fill the SMs once, with 64
+// tokens a segment at least (512 tokens of 4096 channels: 34.8 us in 8, 36.9 in 14, 41 in
+// 28).  Backward, where an SM holds eight warps: 512 warps, 2048 tokens, 744 us in one
+// piece, 648 in 2, 625 in 8; from four warps an SM on it is in one piece, else it fills
+// the SMs three times, with 32 tokens a segment at least (513 tokens of 3 x 528 channels,
+// fp32: 50 us, 60 with 64).
 ScanSplit scan_split(const ScanArgs& a, int backward) {
-  const int width = backward ? bwd_width(a.N) : fwd_width(a.N), resident = (backward ? kBwdWarps : kFwdWarps) * a.num_sms;
-  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, width);
-  constexpr int least = 32;
-  int64_t n = warps >= (backward ? 4 : 5) * a.num_sms ? 1 : (backward ? 3 : 2) * resident / warps;
-  if (n > a.T / least) n = a.T / least;
+  int64_t n = 1;
+  const int64_t all = static_cast<int64_t>(a.B) * a.G;
+  if (backward) {
+    const int64_t warps = all * per_group(a, bwd_width(a.N));
+    if (warps < 4 * a.num_sms) n = std::min<int64_t>(3 * kBwdWarps * a.num_sms / warps, a.T / 32);
+  } else {
+    const int64_t warps = all * per_group(a, fwd_width(a.N, false));
+    if (warps < 5 * a.num_sms) n = std::min<int64_t>(kFwdWarps * a.num_sms / (all * per_group(a, fwd_width(a.N, true))), a.T / 64);
+  }
   if (n < 3) n = 1;
   const int tiles = (a.T + 15) / 16;
   ScanSplit p{};
