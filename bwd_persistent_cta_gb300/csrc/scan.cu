@@ -2,12 +2,12 @@
 // serving step.
 //
 // What bounds it: for each token, channel and state one exponential (4 cycles of a
-// scheduler's special function unit for a warp) and four multiply-adds forward, two and
-// thirteen backward; memory is a third of that at 16 states.  So the recurrence is kept
-// at two values an instruction and everything around it small: a warp holds 8 * CL
-// channels' worth of states in registers, lane = cl + CL sl with C channels and NS states
-// of each, sums over a channel's states and over the warp's channels are a few shuffles,
-// and steps, B and C come from shared memory as broadcasts of 16 bytes.
+// scheduler's special function unit for a warp) and four multiply-adds forward, one and
+// twelve backward; memory is a third of that at 16 states.  So the recurrence is kept at
+// two values an instruction and everything around it small: a warp holds the states of its
+// channels in registers, lane = cl + CL sl with C channels and NS states of each, sums over
+// a channel's states and over the warp's channels are a few shuffles, and steps, B and C
+// come from shared memory as broadcasts of 16 bytes.
 #include "common.cuh"
 #include "pair.cuh"
 #include "scan.h"
@@ -80,47 +80,48 @@ __device__ __forceinline__ void lds(float (&v)[V], const float* p) {
     }
   }
 }
-template <int P>
+// 2 P values, four of them every HOP.
+template <int P, int HOP = 4>
 __device__ __forceinline__ void lds2(float2 (&v)[P], const float* p) {
 #pragma unroll
   for (int i = 0; i < P; i += 2) {
-    const float4 q = *reinterpret_cast<const float4*>(p + 2 * i);
+    const float4 q = *reinterpret_cast<const float4*>(p + i / 2 * HOP);
     v[i] = make_float2(q.x, q.y);
     v[i + 1] = make_float2(q.z, q.w);
   }
 }
 
-// A thread's C x NS states (or rates) of [.., D, N] memory, zeros beyond D and N (NS
-// divides 8, and N is a multiple of 8).
-template <int C, int NS>
+// A thread's C x NS states (or rates) of [.., D, N] memory, four of them every HOP from n0
+// on, zeros beyond D and N (a multiple of 8).  The lanes of a channel take turns of four
+// states, so that a store covers whole sectors.
+template <int C, int NS, int HOP>
 __device__ __forceinline__ void load_states(float2 (&h)[C][NS / 2], const float* base, int N, int ch, int n0, int width) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const bool ok = base && ch + c < width && n0 < N;
+  for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < NS / 2; j += 2) {
+    for (int k = 0; k < NS / 4; ++k) {
       float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ok) q = *reinterpret_cast<const float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j);
-      h[c][j] = make_float2(q.x, q.y);
-      h[c][j + 1] = make_float2(q.z, q.w);
+      if (base && ch + c < width && n0 + k * HOP < N)
+        q = *reinterpret_cast<const float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + k * HOP);
+      h[c][2 * k] = make_float2(q.x, q.y);
+      h[c][2 * k + 1] = make_float2(q.z, q.w);
     }
-  }
 }
-template <int C, int NS>
+template <int C, int NS, int HOP>
 __device__ __forceinline__ void store_states(const float2 (&h)[C][NS / 2], float* base, int N, int ch, int n0, int width) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < NS / 2; j += 2)
-      if (ch + c < width && n0 < N)
-        *reinterpret_cast<float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + 2 * j) =
-            make_float4(h[c][j].x, h[c][j].y, h[c][j + 1].x, h[c][j + 1].y);
+    for (int k = 0; k < NS / 4; ++k)
+      if (ch + c < width && n0 + k * HOP < N)
+        *reinterpret_cast<float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + k * HOP) =
+            make_float4(h[c][2 * k].x, h[c][2 * k].y, h[c][2 * k + 1].x, h[c][2 * k + 1].y);
 }
 // The rates in units of log2(e).  A token behind the last one has a step of zero and must
 // leave the state as it is, so a rate of minus infinity is held as a large number.
-template <int C, int NS>
+template <int C, int NS, int HOP>
 __device__ __forceinline__ void load_rates(float2 (&A2)[C][NS / 2], const ScanArgs& a, int c0, int ch, int n0, int width) {
-  load_states<C, NS>(A2, a.A + static_cast<int64_t>(c0) * a.N, a.N, ch, n0, width);
+  load_states<C, NS, HOP>(A2, a.A + static_cast<int64_t>(c0) * a.N, a.N, ch, n0, width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -219,12 +220,12 @@ struct Rows {
 };
 
 // Adds one segment's own end to what went through it: h = exp(A sum) h + end.
-template <int C, int NS>
+template <int C, int NS, int HOP>
 __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanArgs& a, const ScanSegs& g,
                                         int b, int i, int c0, int ch, int n0, int width) {
   const int64_t at = (static_cast<int64_t>(b) * g.nseg + i) * a.D + c0;
   float2 e[C][NS / 2];
-  load_states<C, NS>(e, g.ends + at * a.N, a.N, ch, n0, width);
+  load_states<C, NS, HOP>(e, g.ends + at * a.N, a.N, ch, n0, width);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const float sum = ch + c < width ? g.sums[at + ch + c] : 0.f;
@@ -239,10 +240,16 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 // A warp works alone: a tile of eight tokens of its channels is on its way into shared
 // memory while it works on the one before; it leaves the steps in shared memory, runs the
 // recurrence and finishes the outputs, with no barrier but its own.  Nothing but the
-// states, their rates and the next rows of B and C stays in registers, so that five warps
-// a scheduler hide the latencies of each other.  Eight states a lane: at 16 states two
-// lanes share a channel, and a sum over the states is one exchange.
-constexpr int kFwdWarps = 12;    // an SM
+// states, their rates and the token at hand stays in registers, so that three warps a
+// scheduler hide the latencies of each other.  Eight states a lane: at 16 states two lanes
+// share a channel, and a sum over the states is one exchange.
+//
+// Measured, bf16: 8 x 2048 tokens of 2048 channels and 16 states, keeping for the gradients,
+// 255 us (2.7 TB/s; 115 us are the exponentials alone), 8 x 1000 tokens without 108 us.
+// Warps an SM holds: up to 16 states 12 (the former 255 us; 16, with 128 registers, 288);
+// above that the two channels a lane need more than 168 registers, and 8 leave 255 (8 x 1024
+// tokens of 2048 channels and 64 states, 499 us with 12, which spill 36 bytes, 397 with 8).
+constexpr int fwd_warps(int SL) { return SL > 2 ? 8 : 12; }
 constexpr int kFwdNS = 8, kStretch = 8;
 enum { kInfer, kTrain, kAlone, kAloneBack };
 
@@ -279,16 +286,16 @@ __device__ __forceinline__ void over_states(float (&v)[C], int sl) {
 }
 
 template <typename T, int SL, int C, int MODE>
-__global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdArgs f) {
+__global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanFwdArgs f) {
   constexpr bool OUT = MODE == kInfer || MODE == kTrain, BACK = MODE == kAloneBack;
   using W = Fwd<T, SL, C, OUT>;
-  constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, TT = W::TT;
+  constexpr int CT = W::CT, NP = W::NP, P = W::P, NS = kFwdNS, HOP = 4 * SL, TT = W::TT;
   __shared__ __align__(16) W s;
   const ScanArgs& a = f.a;
   // forward the last segment, backward the first has no other that wants its end
   Where<CT> w(a, OUT ? f.g.nseg : f.g.nseg - 1, blockIdx.x);
   if (BACK) ++w.seg;
-  const int lane = threadIdx.x, cl = lane % W::CL, sl = lane / W::CL, ch = cl * C, n0 = sl * NS;
+  const int lane = threadIdx.x, cl = lane % W::CL, sl = lane / W::CL, ch = cl * C, n0 = sl * 4;
   const int row = lane / W::VC, col = lane % W::VC * 8;
   const bool in = col < w.width && row < TT, gate = a.z != nullptr;
   const int len = a.len ? a.len[w.b] : a.T, begin = w.seg * f.g.len, end = begin + f.g.len < a.T ? begin + f.g.len : a.T;
@@ -323,16 +330,16 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
     s.skip[c] = OUT && a.skip && c < w.width ? a.skip[w.c0 + c] : 0.f;
   }
   float2 A2[C][P], h[C][P], sum[4];
-  load_rates<C, NS>(A2, a, w.c0, ch, n0, w.width);
-  load_states<C, NS>(h, OUT && f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
+  load_rates<C, NS, HOP>(A2, a, w.c0, ch, n0, w.width);
+  load_states<C, NS, HOP>(h, OUT && f.h0 ? f.h0 + bD * a.N : nullptr, a.N, ch, n0, w.width);
   if (MODE == kAlone && f.first && w.seg == 0) {
     float2 h0[C][P];
-    load_states<C, NS>(h0, f.h0 + bD * a.N, a.N, ch, n0, w.width);
-    store_states<C, NS>(h0, f.first + bD * a.N, a.N, ch, n0, w.width);
+    load_states<C, NS, HOP>(h0, f.h0 + bD * a.N, a.N, ch, n0, w.width);
+    store_states<C, NS, HOP>(h0, f.first + bD * a.N, a.N, ch, n0, w.width);
   }
   if (OUT)
 #pragma unroll 2
-    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
+    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS, HOP>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int j = 0; j < 4; ++j) sum[j] = both(0.f);
   float* pu = MODE == kTrain && gate ? f.ungated + row0 * a.D + w.c0 + col : nullptr;
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
 #pragma unroll
       for (int q = 0; q < kStretch; ++q) {
         if (MODE == kTrain && q % kScanKeep == 0 && t0 + half + q < end) {
-          store_states<C, NS>(h, pk, a.N, ch, n0, w.width);
+          store_states<C, NS, HOP>(h, pk, a.N, ch, n0, w.width);
           pk += static_cast<int64_t>(a.D) * a.N;
         }
         const int t = BACK ? TT - 1 - half - q : half + q;
@@ -387,8 +394,8 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
         float2 Bv[P], Cv[P];
         lds<C>(d, &s.dt[t][ch]);
         lds<C>(u, &s.dx[t][ch]);
-        lds2<P>(Bv, &s.B[t][n0]);
-        if (OUT) lds2<P>(Cv, &s.C_[t][n0]);
+        lds2<P, HOP>(Bv, &s.B[t][n0]);
+        if (OUT) lds2<P, HOP>(Cv, &s.C_[t][n0]);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           float2 r = both(0.f);
@@ -440,11 +447,11 @@ __global__ void __launch_bounds__(32, kFwdWarps) scan_fwd_kernel(const ScanFwdAr
     }
   }
   if (OUT) {
-    if (f.hT && end == a.T) store_states<C, NS>(h, f.hT + bD * a.N, a.N, ch, n0, w.width);
+    if (f.hT && end == a.T) store_states<C, NS, HOP>(h, f.hT + bD * a.N, a.N, ch, n0, w.width);
     return;
   }
   const int64_t at = (static_cast<int64_t>(w.b) * f.g.nseg + w.seg) * a.D + w.c0;
-  store_states<C, NS>(h, f.g.ends + at * a.N, a.N, ch, n0, w.width);
+  store_states<C, NS, HOP>(h, f.g.ends + at * a.N, a.N, ch, n0, w.width);
   // the rows' sums of steps, in a fixed order
 #pragma unroll
   for (int m = W::VC; m < 32; m <<= 1)
@@ -598,11 +605,11 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
     s.skip[c] = a.skip && c < w.width ? a.skip[w.c0 + c] : 0.f;
   }
   float2 A2[C][P], g[C][P], dA[C][P];
-  load_rates<C, NS>(A2, a, w.c0, ch, n0, w.width);
-  load_states<C, NS>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
+  load_rates<C, NS, 4>(A2, a, w.c0, ch, n0, w.width);
+  load_states<C, NS, 4>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
 #pragma unroll 2
   for (int i = p.g.nseg - 1; i > w.seg; --i)
-    if (i * p.g.len < len) through<C, NS>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
+    if (i * p.g.len < len) through<C, NS, 4>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -785,9 +792,9 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
     }
     po -= TT * hop * a.D;
   }
-  if (out.dh0 && begin == 0) store_states<C, NS>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, w.width);
+  if (out.dh0 && begin == 0) store_states<C, NS, 4>(g, static_cast<float*>(out.dh0) + bD * a.N, a.N, ch, n0, w.width);
   const int64_t at = (static_cast<int64_t>(w.b) * p.g.nseg + w.seg) * a.D + w.c0;
-  if (p.pA) store_states<C, NS>(dA, p.pA + at * a.N, a.N, ch, n0, w.width);
+  if (p.pA) store_states<C, NS, 4>(dA, p.pA + at * a.N, a.N, ch, n0, w.width);
   // the rows' sums, in order
   __syncwarp();
   for (int c = lane; c < w.width; c += 32) {
@@ -1055,29 +1062,10 @@ ScanSegs segments(const ScanSplit& p, void* work) {
 
 }  // namespace
 
-// Segments.  Forward, a warp's tokens follow one another every 85 to 110 ns as long as a
-// scheduler has at most two warps, and a second pass over the tokens (what each segment
-// leaves by itself) costs half as much again: 8 sequences of 2048 channels (1024 warps of 16
-// channels), 1000 tokens, 108 us in one piece and 147 in two; 4 of 2048 tokens (512 warps),
-// 200 in one piece and 150 in eight; 1 x 4096 channels (256 warps), 16384 tokens, 1.4 ms in
-// one piece, 610 us in 8, 500 in 14, 506 in 28.  So they begin below five warps an SM, then
-// of 32 channels (two a lane: 547 and 500 us in 14 pieces), and fill the SMs once, with 64
-// tokens a segment at least (512 tokens of 4096 channels: 34.8 us in 8, 36.9 in 14, 41 in
-// 28).  Backward, where an SM holds eight warps: 512 warps, 2048 tokens, 744 us in one
-// piece, 648 in 2, 625 in 8; from four warps an SM on it is in one piece, else it fills
-// the SMs three times, with 32 tokens a segment at least (513 tokens of 3 x 528 channels,
-// fp32: 50 us, 60 with 64).
-ScanSplit scan_split(const ScanArgs& a, int backward) {
-  int64_t n = 1;
-  const int64_t all = static_cast<int64_t>(a.B) * a.G;
-  if (backward) {
-    const int64_t warps = all * per_group(a, bwd_width(a.N));
-    if (warps < 4 * a.num_sms) n = std::min<int64_t>(3 * kBwdWarps * a.num_sms / warps, a.T / 32);
-  } else {
-    const int64_t warps = all * per_group(a, fwd_width(a.N, false));
-    if (warps < 5 * a.num_sms) n = std::min<int64_t>(kFwdWarps * a.num_sms / (all * per_group(a, fwd_width(a.N, true))), a.T / 64);
-  }
-  if (n < 3) n = 1;
+namespace {
+
+// n segments, as near as whole tiles allow.
+ScanSplit split(const ScanArgs& a, int64_t n, bool first) {
   const int tiles = (a.T + 15) / 16;
   ScanSplit p{};
   p.len = (tiles + static_cast<int>(n) - 1) / static_cast<int>(n) * 16;
@@ -1086,8 +1074,47 @@ ScanSplit scan_split(const ScanArgs& a, int backward) {
   const size_t rows = static_cast<size_t>(a.B) * p.nseg * a.D;
   p.sums = up(rows * a.N * 4);
   p.first = p.sums + up(rows * 4);
-  p.bytes = p.first + (backward ? 0 : up(static_cast<size_t>(a.B) * a.D * a.N * 4));
+  p.bytes = p.first + (first ? up(static_cast<size_t>(a.B) * a.D * a.N * 4) : 0);
   return p;
+}
+
+}  // namespace
+
+// Segments.  Forward, a warp's tokens follow one another every 85 to 110 ns as long as a
+// scheduler has at most two warps, and a second pass over the tokens (what each segment
+// leaves by itself) costs half as much again.  So they begin below five warps an SM, and
+// then have 32 channels a warp (two a lane: 1 x 16384 tokens of 4096 channels 500 us, 547
+// with one a lane; 1.1 ms in one piece).  They fill the SMs once: in bf16 with the 12 warps
+// that an SM holds (4 x 2048 tokens of 2048 channels 141 us in 7 pieces, 164 in 4, 158 in
+// one), in fp32, whose tiles take more of the shared memory's time, and above 16 states
+// with 8 (190, 172 and 172 us), and above 32 pieces with 8 as well, since each loads what
+// all before it left (1 x 4096 tokens of 1024 channels 70 us in 52 pieces, 59 in 37).
+// Fewer than five do not pay up to 16 states (8 x 1024 tokens of 2048 channels, 8 states,
+// fp32: 108 us in one piece, 128 in three; training 121 and 148), above that fewer than
+// three (2 x 1024 tokens of 1024 channels, 64 states: 125 us in one piece, 104 in four; 4 x
+// 1024 of 2048, 32 states: 113 and 125 in two).  64 tokens each at least (300 tokens of
+// 2048 channels 29 us, 43 with 128).
+ScanSplit scan_split_forward(const ScanArgs& a, int is_bf16) {
+  const int64_t all = static_cast<int64_t>(a.B) * a.G, wide = all * per_group(a, fwd_width(a.N, true));
+  int64_t n = 1;
+  if (all * per_group(a, fwd_width(a.N, false)) < 5 * a.num_sms) {
+    n = (is_bf16 && a.N <= 16 ? 12 : 8) * a.num_sms / wide;
+    if (n > 32) n = std::max<int64_t>(8 * a.num_sms / wide, 32);
+    n = std::min<int64_t>(n, a.T / 64);
+    if (n < (a.N <= 16 ? 5 : 3)) n = 1;
+  }
+  return split(a, n, true);
+}
+
+// Backward, where an SM holds eight warps: 512 warps, 2048 tokens, 744 us in one piece, 648
+// in 2, 625 in 8; from four warps an SM on it is in one piece, else it fills the SMs three
+// times, with 32 tokens a segment at least (513 tokens of 3 x 528 channels, fp32: 50 us, 60
+// with 64).
+ScanSplit scan_split_backward(const ScanArgs& a) {
+  const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, bwd_width(a.N));
+  int64_t n = 1;
+  if (warps < 4 * a.num_sms) n = std::min<int64_t>(3 * kBwdWarps * a.num_sms / warps, a.T / 32);
+  return split(a, n < 3 ? 1 : n, false);
 }
 
 ScanReserve scan_reserve(const ScanArgs& a) {
@@ -1099,7 +1126,7 @@ ScanReserve scan_reserve(const ScanArgs& a) {
 
 int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStream_t s, int* launches) {
   ScanFwdArgs f = f_;
-  const ScanSplit p = scan_split(f.a, 0);
+  const ScanSplit p = scan_split_forward(f.a, is_bf16);
   f.g = segments(p, work);
   f.first = p.nseg > 1 && f.h0 && f.h0 == f.hT ? reinterpret_cast<float*>(static_cast<char*>(work) + p.first) : nullptr;
   *launches = 0;
@@ -1107,7 +1134,7 @@ int launch_scan_forward(const ScanFwdArgs& f_, void* work, int is_bf16, cudaStre
 }
 
 ScanBwdLayout scan_bwd_layout(const ScanArgs& a) {
-  const ScanSplit p = scan_split(a, 1);
+  const ScanSplit p = scan_split_backward(a);
   ScanBwdLayout l{};
   size_t off = p.bytes;
   auto take = [&](size_t n) {
@@ -1127,7 +1154,7 @@ ScanBwdLayout scan_bwd_layout(const ScanArgs& a) {
 int launch_scan_backward(const ScanBwdArgs& b, int is_bf16, cudaStream_t s, int* launches) {
   ScanBwdArgs p = b;
   const ScanBwdLayout l = scan_bwd_layout(p.a);
-  p.g = segments(scan_split(p.a, 1), p.work);
+  p.g = segments(scan_split_backward(p.a), p.work);
   auto part = [&](const void* want, size_t off) { return want ? reinterpret_cast<float*>(p.work + off) : nullptr; };
   p.bc = part(p.grad.dB ? p.grad.dB : p.grad.dC, l.bc);
   p.pA = part(p.grad.dA, l.dA);

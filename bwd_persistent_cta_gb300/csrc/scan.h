@@ -37,7 +37,8 @@ struct ScanSplit {
   size_t first;                // [B][D][N]: the initial state where the final one overwrites it
   size_t bytes;
 };
-ScanSplit scan_split(const ScanArgs& a, int backward);
+ScanSplit scan_split_forward(const ScanArgs& a, int is_bf16);
+ScanSplit scan_split_backward(const ScanArgs& a);
 
 struct ScanSegs {
   int nseg, len;

@@ -210,7 +210,7 @@ rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* out) {
   h->bf16 = desc->dtype == RNN_BF16;
   h->es = h->bf16 ? 2 : 4;
   const ScanArgs a = scan_shape(h);
-  h->workspace_bytes = scan_split(a, 0).bytes;
+  h->workspace_bytes = scan_split_forward(a, h->bf16).bytes;
   h->bwd_workspace_bytes = scan_bwd_layout(a).bytes;
   h->reserve_bytes = scan_reserve(a).bytes;
   *out = h;
