@@ -17,7 +17,8 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 // Vectors of 16 bytes a thread, in flight at once: the norm's sums take registers of their
-// own (252 MB of bf16: 50 us with four, 61 with eight; scaling them 83 and 81).
+// own (252 MB of gradients: 50 us, 5.0 TB/s, with four, 61 with eight; scaling them, in place,
+// 81 us, 6.2 TB/s, with eight, 83 with four).
 constexpr int kNormVectors = 4, kScaleVectors = 8;
 
 template <int CAP>

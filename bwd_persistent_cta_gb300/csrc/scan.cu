@@ -245,7 +245,8 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 // share a channel, and a sum over the states is one exchange.
 //
 // Measured, bf16: 8 x 2048 tokens of 2048 channels and 16 states, keeping for the gradients,
-// 255 us (2.7 TB/s; 115 us are the exponentials alone), 8 x 1000 tokens without 108 us.
+// 255 us (3.7 TB/s with what it keeps; 57 us are the exponentials alone, 79 the
+// multiply-adds), 8 x 1000 tokens without keeping 108 us.
 // Warps an SM holds: up to 16 states 12 (the former 255 us; 16, with 128 registers, 288);
 // above that the two channels a lane need more than 168 registers, and 8 leave 255 (8 x 1024
 // tokens of 2048 channels and 64 states, 499 us with 12, which spill 36 bytes, 397 with 8).
@@ -469,8 +470,8 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
 // backward
 // ---------------------------------------------------------------------------
 // A warp goes through its segment from the last token to the first, four tokens at a time:
-// it computes their decays and states again from the kept one, holds them in registers, and runs the
-// gradient g of the state back through them:
+// it computes their decays and states again from the kept one, holds them in registers, and
+// runs the gradient g of the state back through them:
 //     g += dy_t C_t;  dC_t += dy_t h_t;  dB_t += g delta_t x_t;  s1_t = sum g B_t
 //     g = a_t g;  P = g h_{t-1};  s2_t = sum P A;  dA += P delta_t
 // then, channel by channel, dx = delta s1 + D dy, ddelta = x s1 + s2, and dz from y as the
@@ -478,6 +479,13 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
 // states (of s1 and s2) and over the channels (of dB and dC) then take the fewest
 // exchanges together.  Inputs and kept states of the next tile of eight tokens are on
 // their way into shared memory meanwhile.
+//
+// Measured, bf16: 8 x 2048 tokens of 2048 channels and 16 states 612 us: 100 what the
+// segments leave by themselves, 485 this kernel (2.9 TB/s; 57 us are its exponentials
+// alone, 215 its multiply-adds), 23 and 5 the sums behind it.  Issue bounds it, 55 % of
+// the slots with two warps a scheduler: states and decays of the four tokens take the
+// registers.  Kept states eight tokens apart leave no room for the decays, and computing
+// them twice cost 110 us.
 constexpr int kBwdWarps = 8;     // an SM
 constexpr int kBT = 8, kBSub = kScanKeep, kBNS = 4, kBC = 4;
 
@@ -811,7 +819,8 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
 
 // dB and dC: the sum over the warps of a group, a warp for each token and group: its lanes
 // read whole rows of partial sums, 32 / V of them at a time (V vectors of four states a
-// row), each lane in order and then the lanes in order.
+// row), each lane in order and then the lanes in order.  Memory bounds it: 134 MB (16384
+// tokens, 64 warps of 32 channels, 16 states) in 23 us, 5.8 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) scan_bc_kernel(const ScanArgs a, const float* bc, int parts, T* dB, T* dC) {
   constexpr int NP = 2 * V, SUB = 32 / V;
@@ -870,6 +879,8 @@ __global__ void __launch_bounds__(128) scan_sum_kernel(const ScanBwdArgs p) {
 // ---------------------------------------------------------------------------
 // SL lanes have CH = min(SL, 4) channels, four states of each a lane.  A lane prepares one
 // of the channels (its step, and at the end its output) and hands the step to the others.
+// Memory bounds it, the states in and out: 256 sequences of 4096 channels and 16 states in
+// 27 us, 5.3 TB/s; four tokens of each in 59 us, where issue does.
 constexpr int kStepThreads = 128;
 template <typename T, int SL>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepArgs p) {
