@@ -249,7 +249,9 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 // multiply-adds), 8 x 1000 tokens without keeping 108 us.
 // Warps an SM holds: up to 16 states 12 (the former 255 us; 16, with 128 registers, 288);
 // above that the two channels a lane need more than 168 registers, and 8 leave 255 (8 x 1024
-// tokens of 2048 channels and 64 states, 499 us with 12, which spill 36 bytes, 397 with 8).
+// tokens of 2048 channels and 64 states, 499 us with 12, which spill 36 bytes, 397 with 8,
+// 350 since they fit the shared memory).  Kept states that go out through shared memory by
+// bulk copies, one a warp and four tokens, cost more than the lanes' stores: 311 us.
 constexpr int fwd_warps(int SL) { return SL > 2 ? 8 : 12; }
 constexpr int kFwdNS = 8, kStretch = 8;
 enum { kInfer, kTrain, kAlone, kAloneBack };
@@ -260,7 +262,12 @@ struct Fwd {
   static constexpr int VC = CT / 8, ROWS = 32 / VC, TT = ROWS < 16 ? ROWS : 16;     // an item a lane
   static_assert(TT % kStretch == 0 && kStretch % kScanKeep == 0, "whole stretches, whole distances between kept states");
   static constexpr int LD = CT + 4;      // a row in shared memory: rows of a store on banks of their own
-  static constexpr int AHEAD = 3;        // tiles on their way
+  // Tiles on their way.  Where the warps that an SM can hold by their registers would not
+  // fit its shared memory with three, one: fp32, 8 x 1024 tokens of 2048 channels, 32 states
+  // 176 us, 240 with three; 64 states bf16 350 and 399, fp32 432 and 530; fp32, 16 states, 4
+  // x 2048 tokens 150 and 190.  With few short tiles a warp (8 states) one is too late: 137
+  // us, 100 with three.
+  static constexpr int AHEAD = SL > 2 || (SL == 2 && sizeof(T) == 4) ? 1 : 3;
   using R = Rows<T, TT, NP>;
   Raw<T, 8> raw[AHEAD + 1][3][32];       // x, dt, z of a lane's item
   typename R::Stage rawB[AHEAD + 1], rawC[OUT ? AHEAD + 1 : 1];
@@ -1095,21 +1102,22 @@ ScanSplit split(const ScanArgs& a, int64_t n, bool first) {
 // scheduler has at most two warps, and a second pass over the tokens (what each segment
 // leaves by itself) costs half as much again.  So they begin below five warps an SM, and
 // then have 32 channels a warp (two a lane: 1 x 16384 tokens of 4096 channels 500 us, 547
-// with one a lane; 1.1 ms in one piece).  They fill the SMs once: in bf16 with the 12 warps
-// that an SM holds (4 x 2048 tokens of 2048 channels 141 us in 7 pieces, 164 in 4, 158 in
-// one), in fp32, whose tiles take more of the shared memory's time, and above 16 states
-// with 8 (190, 172 and 172 us), and above 32 pieces with 8 as well, since each loads what
-// all before it left (1 x 4096 tokens of 1024 channels 70 us in 52 pieces, 59 in 37).
-// Fewer than five do not pay up to 16 states (8 x 1024 tokens of 2048 channels, 8 states,
-// fp32: 108 us in one piece, 128 in three; training 121 and 148), above that fewer than
-// three (2 x 1024 tokens of 1024 channels, 64 states: 125 us in one piece, 104 in four; 4 x
-// 1024 of 2048, 32 states: 113 and 125 in two).  64 tokens each at least (300 tokens of
-// 2048 channels 29 us, 43 with 128).
+// with one a lane; 1.1 ms in one piece).  They fill the SMs once with as many warps as these
+// hold: 12, above 16 states (registers) and in fp32 up to 8 states (shared memory) 8.  4 x
+// 2048 tokens of 2048 channels, 16 states: bf16 141 us in 7 pieces, 164 in 4, 158 in one,
+// fp32 150, 174, 172; 2 x 2048 tokens of 2048 channels, 8 states, fp32: 72 us with 8 warps
+// an SM, 86 with 12.  Above 32 pieces it is 8 always, since each loads what all before it
+// left (1 x 4096 tokens of 1024 channels, bf16, 70 us in 52 pieces, 59 in 37).  Fewer than
+// five do not pay up to 16 states (8 x 1024 tokens of 2048 channels, 8 states, fp32: 108 us
+// in one piece, 128 in three; training 121 and 148), above that fewer than three (2 x 1024
+// tokens of 1024 channels, 64 states: 125 us in one piece, 104 in four; 4 x 1024 of 2048, 32
+// states: 113 and 125 in two).  64 tokens each at least (300 tokens of 2048 channels 29 us,
+// 43 with 128).
 ScanSplit scan_split_forward(const ScanArgs& a, int is_bf16) {
   const int64_t all = static_cast<int64_t>(a.B) * a.G, wide = all * per_group(a, fwd_width(a.N, true));
   int64_t n = 1;
   if (all * per_group(a, fwd_width(a.N, false)) < 5 * a.num_sms) {
-    n = (is_bf16 && a.N <= 16 ? 12 : 8) * a.num_sms / wide;
+    n = (a.N > 16 || (a.N <= 8 && !is_bf16) ? 8 : 12) * a.num_sms / wide;
     if (n > 32) n = std::max<int64_t>(8 * a.num_sms / wide, 32);
     n = std::min<int64_t>(n, a.T / 64);
     if (n < (a.N <= 16 ? 5 : 3)) n = 1;
