@@ -76,7 +76,7 @@ def _odd(t, bfirst):
 
 
 def run(T, B, D, N, G=1, dtype="bf16", lengths=None, bfirst=False, packed=False, state=True, softplus=True, z=True,
-        skip=True, bias=True, train=True, seed=0, poison=False, check=True):
+        skip=True, bias=True, train=True, seed=0, poison=False, check=True, slack=1):
     import torch
     import bwd_persistent_cta_gb300 as R
     t = _inputs(T, B, D, N, G, dtype, seed + T + D + N, softplus)
@@ -105,19 +105,19 @@ def run(T, B, D, N, G=1, dtype="bf16", lengths=None, bfirst=False, packed=False,
     fwd = {n: host[n] for n in ("x", "dt", "A", "Bm", "Cm", "z", "D", "dt_bias", "h0")}
     wy, wh, kept = O.scan_forward(**fwd, lengths=lengths, softplus=softplus)
     order = lambda a: a.transpose(0, 1) if bfirst else a  # noqa: E731
-    _close(order(y), wy, OUT_TOL[dtype], "y")
-    _close(hT, wh, STATE_TOL[dtype], "hT")
+    _close(order(y), wy, slack * OUT_TOL[dtype], "y")
+    _close(hT, wh, slack * STATE_TOL[dtype], "hT")
     if train:
         want = O.scan_backward(host["dy"], *(host[n] for n in ("x", "dt", "A", "Bm", "Cm")), kept, host["z"], host["D"],
                                host["dhT"], lengths, softplus)
         for n in ("dx", "ddt", "dz", "dB", "dC"):
             assert (d[n] is None) == (n == "dz" and not z)
             if d[n] is not None:
-                _close(order(d[n]), want[n], OUT_TOL[dtype], n)
+                _close(order(d[n]), want[n], slack * OUT_TOL[dtype], n)
         for n, on in (("dA", True), ("dD", skip), ("ddt_bias", bias), ("dh0", True)):
             assert (d[n] is not None) == on
             if on:
-                _close(d[n], want[n], GRAD_TOL[dtype], n)
+                _close(d[n], want[n], slack * GRAD_TOL[dtype], n)
     if lengths is not None:
         for b, length in enumerate(lengths):
             for v in [y] + [d[n] for n in ("dx", "ddt", "dz", "dB", "dC") if d.get(n) is not None]:
@@ -177,6 +177,14 @@ def test_segments_side_by_side(T, lengths, dtype):
     """Long sequences of few channels run as several segments, some of them behind the last token."""
     run(T, 2, 24, 16, dtype=dtype, lengths=lengths, poison=True)
     run(T, 2, 40, 8, dtype=dtype, bfirst=True, packed=True, state=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [8, 16, 40])
+def test_many_segments(N, dtype):
+    """As many segments as the length allows, one sequence ending early.  Roundings of the decays add up
+    over a state's memory, which is the sequence at most: 2200 tokens here, 600 in the other tests."""
+    run(2200, 2, 16, N, dtype=dtype, lengths=[2200, 1300], poison=True, bfirst=True, slack=2200 / 600)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
