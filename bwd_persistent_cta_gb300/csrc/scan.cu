@@ -887,7 +887,8 @@ __global__ void __launch_bounds__(128) scan_sum_kernel(const ScanBwdArgs p) {
 // SL lanes have CH = min(SL, 4) channels, four states of each a lane.  A lane prepares one
 // of the channels (its step, and at the end its output) and hands the step to the others.
 // Memory bounds it, the states in and out: 256 sequences of 4096 channels and 16 states in
-// 27 us, 5.3 TB/s; four tokens of each in 59 us, where issue does.
+// 27 us, 5.3 TB/s (a cold call 33; 35 with 56 registers a thread for more warps, 45 with
+// 42); four tokens of each in 59 us, where issue does.
 constexpr int kStepThreads = 128;
 template <typename T, int SL>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepArgs p) {
