@@ -117,8 +117,10 @@ __device__ __forceinline__ void store_states(const float2 (&h)[C][NS / 2], float
         *reinterpret_cast<float4*>(base + static_cast<int64_t>(ch + c) * N + n0 + k * HOP) =
             make_float4(h[c][2 * k].x, h[c][2 * k].y, h[c][2 * k + 1].x, h[c][2 * k + 1].y);
 }
-// The rates in units of log2(e).  A token behind the last one has a step of zero and must
-// leave the state as it is, so a rate of minus infinity is held as a large number.
+// A token behind the last one, and one whose step is zero, must leave the state as it is, so
+// a rate of minus infinity is held as a large number: a reset at every step above 1e-28.
+__device__ __forceinline__ float finite_rate(float a) { return isinf(a) ? copysignf(1e30f, a) : a; }
+// The rates in units of log2(e).
 template <int C, int NS, int HOP>
 __device__ __forceinline__ void load_rates(float2 (&A2)[C][NS / 2], const ScanArgs& a, int c0, int ch, int n0, int width) {
   load_states<C, NS, HOP>(A2, a.A + static_cast<int64_t>(c0) * a.N, a.N, ch, n0, width);
@@ -127,8 +129,7 @@ __device__ __forceinline__ void load_rates(float2 (&A2)[C][NS / 2], const ScanAr
 #pragma unroll
     for (int j = 0; j < NS / 2; ++j) {
       A2[c][j] = mul2(A2[c][j], both(kLog2e));
-      if (isinf(A2[c][j].x)) A2[c][j].x = copysignf(1e30f, A2[c][j].x);
-      if (isinf(A2[c][j].y)) A2[c][j].y = copysignf(1e30f, A2[c][j].y);
+      A2[c][j] = make_float2(finite_rate(A2[c][j].x), finite_rate(A2[c][j].y));
     }
 }
 
@@ -910,7 +911,8 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
     h[i] = A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < width && n > 0 && states) {
       h[i] = *reinterpret_cast<const float4*>(state + static_cast<int64_t>(i) * a.N);
-      A[i] = *reinterpret_cast<const float4*>(a.A + at + static_cast<int64_t>(i) * a.N);
+      const float4 q = *reinterpret_cast<const float4*>(a.A + at + static_cast<int64_t>(i) * a.N);
+      A[i] = make_float4(finite_rate(q.x), finite_rate(q.y), finite_rate(q.z), finite_rate(q.w));
     }
   }
   const float bias = own && a.bias ? a.bias[d] : 0.f, skip = own && a.skip ? a.skip[d] : 0.f;
