@@ -149,20 +149,43 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_consta
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The norm and the factor, from the partial sums of all launches.
-__device__ __forceinline__ float clip_factor(const double* partial, int parts, float max_norm, float eps, float* norm, double* sm) {
+// What every element is multiplied by: ``by``, then ``then`` twice.
+struct Factor {
+  float by, then;
+  __device__ __forceinline__ bool one() const { return by == 1.f && then == 1.f; }
+  __device__ __forceinline__ float2 of(float2 v) const { return mul2(mul2(mul2(v, both(by)), both(then)), both(then)); }
+  __device__ __forceinline__ float of(float v) const { return v * by * then * then; }
+};
+// The norm and the factor, from the partial sums of all launches.  Both stay in 64 bits until
+// they are done with: the sum cannot overflow there, so a norm that is not finite means a NaN
+// or infinity among the gradients, while finite ones may have a norm that fp32 cannot hold.
+// A factor below the normal numbers would lose bits: powers of two, exact, are multiplied
+// behind it.
+__device__ __forceinline__ Factor clip_factor(const double* partial, int parts, float max_norm, float eps, float* norm, double* sm) {
   double v = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) v += partial[i];
-  const float n = static_cast<float>(sqrt(block_sum(v, sm)));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-  const float d = n + eps;
-  return isfinite(n) && d > max_norm ? max_norm / d : 1.f;
+  v = block_sum(v, sm);
+  __shared__ Factor f;
+  // one thread: the root and the quotient by all 256 took 7 us of a large list's 495
+  if (threadIdx.x == 0) {
+    const double n = sqrt(v), d = n + eps;
+    if (norm && blockIdx.x == 0) *norm = static_cast<float>(n);
+    f = {1.f, 1.f};
+    if (isfinite(n) && d > max_norm) {
+      const double m = max_norm / d;           // 2^-298 at least: 2^42 elements
+      if (m >= 0x1p-100) f.by = static_cast<float>(m);
+      else if (m >= 0x1p-200) f = {static_cast<float>(m * 0x1p100), 0x1p-50f};
+      else f = {static_cast<float>(m * 0x1p200), 0x1p-100f};
+    }
+  }
+  __syncthreads();
+  return f;
 }
 
 // From the end of the part to its beginning: what the norm's kernel read last is still in
 // L2 (the last 126 MB of a long list), and outputs are stored past it.
 template <typename T>
-__device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, float f) {
+__device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, const Factor f) {
   constexpr int V = 16 / sizeof(T), U = kScaleVectors;
   int64_t head = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
   if (head > n) head = n;
@@ -170,12 +193,12 @@ __device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, float f)
   const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
   const int64_t vecs = same ? (n - head) / V : 0, tail = head + vecs * V;
   const int tid = threadIdx.x;
-  for (int64_t i = tail + tid; i < n; i += kThreads) o[i] = from_f<T>(to_f(p[i]) * f);
+  for (int64_t i = tail + tid; i < n; i += kThreads) o[i] = from_f<T>(f.of(to_f(p[i])));
   auto put = [&](const Raw<T, V>& r, int64_t i) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) {
-      const float2 v = mul2(r.pair(j), both(f));
+      const float2 v = f.of(r.pair(j));
       if constexpr (sizeof(T) == 2) {
         const __nv_bfloat162 h = __float22bfloat162_rn(v);
         w[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -199,20 +222,20 @@ __device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, float f)
     r.load(p + head + i * V);
     put(r, i);
   }
-  if (tid < head) o[tid] = from_f<T>(to_f(p[tid]) * f);
+  if (tid < head) o[tid] = from_f<T>(f.of(to_f(p[tid])));
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Pointers<CAP> ptr, const Share h, const double* partial,
                                                               int parts, float max_norm, float eps, float* norm) {
   __shared__ double sm[kThreads / 32];
-  const float f = clip_factor(partial, parts, max_norm, eps, norm, sm);
+  const Factor f = clip_factor(partial, parts, max_norm, eps, norm, sm);
   int64_t lo, hi;
   slice(h, &lo, &hi);
   if (lo >= hi) return;
   walk<true>(h, lo, hi, [&](int i, int64_t from, int64_t to) {
     // a factor of one leaves every element as it is: nothing to write in place
-    if (f == 1.f && ptr.in[i] == ptr.out[i]) return;
+    if (f.one() && ptr.in[i] == ptr.out[i]) return;
     if (h.dtype[h.first + i] == RNN_F32)
       part_scale(static_cast<const float*>(ptr.in[i]) + from, static_cast<float*>(ptr.out[i]) + from, to - from, f);
     else

@@ -431,7 +431,8 @@ class GradClip(_Op):
 
     def clip(self, grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, stream=None):
         """Scales ``grads`` by min(1, max_norm / (norm + eps)), in place or into the tensors of ``out``, and returns the
-        norm before it (fp32 [1] on the device).  Where the norm is not finite the values stay as they are."""
+        norm before it (fp32 [1] on the device; infinity where fp32 cannot hold it).  With a NaN or infinity among
+        them the values stay as they are."""
         if stream is not None:
             return self._elsewhere(self.clip, stream, grads, max_norm, eps=eps, out=out, norm=norm)
         p = self._tensors(grads, "grads")

@@ -684,9 +684,11 @@ uint64_t rnn_conv_launch_count(rnn_conv_t handle);
  * through many steps in bounds.
  *     norm = sqrt(sum over tensors and elements of g^2)
  *     out  = g * min(1, max_norm / (norm + eps))
- * The sum covers the whole range of fp32: squares that leave it are taken in 64 bits.
- * Where the norm is not finite (a NaN or infinity among the gradients), or the factor
- * is one, out is g as it is: the caller sees norm and may skip the update. */
+ * The sum covers the whole range of fp32: squares that leave it are taken in 64 bits,
+ * and so are the norm and the factor until the elements are multiplied.  Finite
+ * gradients are scaled even where their norm is above the largest fp32 number, which
+ * ``norm`` then gives as infinity.  With a NaN or infinity among the gradients, or where
+ * the factor is one, out is g as it is: the caller may skip the update. */
 typedef struct rnn_clip_s* rnn_clip_t;
 
 /* A list of ``num`` tensors (1..65536): elements (0..2^40, 2^42 together) and
