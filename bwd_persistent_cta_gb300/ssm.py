@@ -376,7 +376,8 @@ class GradClip(_Op):
     """The norm of a list of gradients together, and their scaling where it is over a limit, bound to a device.
 
     ``counts`` are the elements of each tensor, ``dtypes`` "f32" or "bf16" for all of them or one for each.  Tensors are
-    contiguous, of any shape and alignment (slices of a flat gradient among them)."""
+    contiguous, of any shape and alignment (slices of a flat gradient among them), in a list or anything that can be
+    gone through (``dict.values()``)."""
 
     _destroy = staticmethod(rnn_clip_destroy)
 
@@ -398,6 +399,12 @@ class GradClip(_Op):
 
     def launches(self) -> int:
         return rnn_clip_launch_count(self.handle)
+
+    @staticmethod
+    def _listed(tensors):
+        """A dict's values or a generator as a list: it is gone through more than once, and a call on another stream
+        has to name each tensor to the allocator."""
+        return tensors if isinstance(tensors, (list, tuple)) else list(tensors)
 
     def _tensors(self, tensors, name):
         """The pointers of a list of tensors that are as the handle has them."""
@@ -433,6 +440,7 @@ class GradClip(_Op):
         """Scales ``grads`` by min(1, max_norm / (norm + eps)), in place or into the tensors of ``out``, and returns the
         norm before it (fp32 [1] on the device; infinity where fp32 cannot hold it).  With a NaN or infinity among
         them the values stay as they are."""
+        grads, out = self._listed(grads), None if out is None else self._listed(out)
         if stream is not None:
             return self._elsewhere(self.clip, stream, grads, max_norm, eps=eps, out=out, norm=norm)
         p = self._tensors(grads, "grads")
@@ -446,6 +454,7 @@ class GradClip(_Op):
 
     def norm(self, grads, norm=None, stream=None):
         """The norm of ``grads`` together (fp32 [1] on the device)."""
+        grads = self._listed(grads)
         if stream is not None:
             return self._elsewhere(self.norm, stream, grads, norm=norm)
         p = self._tensors(grads, "grads")
