@@ -225,17 +225,21 @@ __device__ __forceinline__ void part_scale(const T* p, T* o, int64_t n, const Fa
   if (tid < head) o[tid] = from_f<T>(f.of(to_f(p[tid])));
 }
 
+// Which tensors a launch scales.
+enum { kAll, kApart, kInPlace };
+
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Pointers<CAP> ptr, const Share h, const double* partial,
-                                                              int parts, float max_norm, float eps, float* norm) {
+                                                              int parts, float max_norm, float eps, float* norm, int which) {
   __shared__ double sm[kThreads / 32];
   const Factor f = clip_factor(partial, parts, max_norm, eps, norm, sm);
   int64_t lo, hi;
   slice(h, &lo, &hi);
   if (lo >= hi) return;
   walk<true>(h, lo, hi, [&](int i, int64_t from, int64_t to) {
+    const bool inplace = ptr.in[i] == ptr.out[i];
     // a factor of one leaves every element as it is: nothing to write in place
-    if (f.one() && ptr.in[i] == ptr.out[i]) return;
+    if (inplace ? f.one() || which == kApart : which == kInPlace) return;
     if (h.dtype[h.first + i] == RNN_F32)
       part_scale(static_cast<const float*>(ptr.in[i]) + from, static_cast<float*>(ptr.out[i]) + from, to - from, f);
     else
@@ -253,13 +257,13 @@ int check_launch() { return cudaGetLastError() == cudaSuccess ? 0 : RNN_CUDA_ERR
 int most_ctas(int num_sms) { return num_sms * (2048 / kThreads); }
 
 template <int CAP>
-int group(const ClipArgs& c, const Share& h, int ctas, bool scale, double* mine, int parts, bool first, cudaStream_t s) {
+int group(const ClipArgs& c, const Share& h, int ctas, bool scale, int which, double* mine, int parts, bool first, cudaStream_t s) {
   Pointers<CAP> p;
   for (int i = 0; i < h.num; ++i) {
     p.in[i] = c.grads[h.first + i];
     p.out[i] = c.out ? c.out[h.first + i] : const_cast<void*>(c.grads[h.first + i]);
   }
-  if (scale) clip_scale_kernel<CAP><<<ctas, kThreads, 0, s>>>(p, h, c.partial, parts, c.max_norm, c.eps, first ? c.norm : nullptr);
+  if (scale) clip_scale_kernel<CAP><<<ctas, kThreads, 0, s>>>(p, h, c.partial, parts, c.max_norm, c.eps, first ? c.norm : nullptr, which);
   else clip_norm_kernel<CAP><<<ctas, kThreads, 0, s>>>(p, h, mine);
   return check_launch();
 }
@@ -275,7 +279,7 @@ int launch_clip(const ClipArgs& c, cudaStream_t s, int* launches) {
   *launches = 0;
   const int groups = (c.num + kClipGroup - 1) / kClipGroup;
   int rc = 0, parts = 0;
-  for (int pass = 0; pass < (c.scale ? 2 : 1); ++pass) {
+  for (int pass = 0; pass < (c.scale ? c.split ? 3 : 2 : 1); ++pass) {
     int at = 0;
     for (int g = 0; g < groups; ++g) {
       Share h{c.start, c.dtype, g * kClipGroup, 0, 0, 0};
@@ -285,9 +289,10 @@ int launch_clip(const ClipArgs& c, cudaStream_t s, int* launches) {
       // at least 2048 elements a CTA
       const int64_t want = (h.end - h.begin + 2047) / 2048;
       const int most = most_ctas(c.num_sms), ctas = want < 1 ? 1 : want < most ? static_cast<int>(want) : most;
-      const bool scale = pass == 1;
-      rc = h.num <= 100 ? group<100>(c, h, ctas, scale, c.partial + at, parts, g == 0, s)
-                        : group<kClipGroup>(c, h, ctas, scale, c.partial + at, parts, g == 0, s);
+      const bool scale = pass > 0, first = pass == 1 && g == 0;
+      const int which = c.split ? pass == 1 ? kApart : kInPlace : kAll;
+      rc = h.num <= 100 ? group<100>(c, h, ctas, scale, which, c.partial + at, parts, first, s)
+                        : group<kClipGroup>(c, h, ctas, scale, which, c.partial + at, parts, first, s);
       if (rc) return rc;
       ++*launches;
       at += ctas;

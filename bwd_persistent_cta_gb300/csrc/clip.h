@@ -24,6 +24,7 @@ struct ClipArgs {
   float* norm;
   double* partial;             // [launch][CTA]
   int scale;                   // 0: the norm alone
+  int split;                   // tensors scaled in place go last: others read their memory
   int num_sms;
 };
 size_t clip_workspace_bytes(int num, int num_sms);

@@ -16,6 +16,8 @@
 
 using namespace rnn;
 
+using Ranges = std::vector<std::pair<uintptr_t, uintptr_t>>;
+
 struct rnn_scan_s {
   rnn_scan_desc_t desc;
   int device, num_sms, bf16;
@@ -42,7 +44,7 @@ struct rnn_clip_s {
   int* d_dtype;
   std::vector<int64_t> start;
   std::vector<int> dtype;
-  std::vector<std::pair<uintptr_t, uintptr_t>> ranges;    // scratch of a call's checks
+  Ranges inplace, apart, reads;        // scratch of a call's checks
   CallOrder order;
   uint64_t launches;
 };
@@ -143,19 +145,53 @@ rnn_status_t make(H** out) {
   return RNN_OK;
 }
 
-// Whether two of the tensors that a call writes share memory (a tensor listed twice would
-// be scaled once or twice, as it happens).
-bool overlap(rnn_clip_t h, const void* const* out) {
-  auto& r = h->ranges;
-  r.clear();                                             // holds num of them without allocating
-  for (int i = 0; i < h->num; ++i) {
-    const uint64_t bytes = static_cast<uint64_t>(h->start[i + 1] - h->start[i]) * (h->dtype[i] == RNN_F32 ? 4 : 2);
-    if (bytes) r.emplace_back(reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + bytes);
-  }
+void add(Ranges& r, const void* p, uint64_t bytes) {                        // within its capacity
+  r.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes);
+}
+// Sorts them; whether no two overlap.
+bool disjoint(Ranges& r) {
   if (!std::is_sorted(r.begin(), r.end())) std::sort(r.begin(), r.end());
   for (size_t i = 1; i < r.size(); ++i)
-    if (r[i].first < r[i - 1].second) return true;
+    if (r[i].first < r[i - 1].second) return false;
+  return true;
+}
+// Whether any of ``w``, sorted and disjoint, overlaps any of ``r``, sorted.
+bool meet(const Ranges& w, const Ranges& r) {
+  size_t j = 0;                              // the first that ends behind the other's beginning
+  for (const auto& x : r) {
+    while (j < w.size() && w[j].second <= x.first) ++j;
+    if (j < w.size() && w[j].first < x.second) return true;
+  }
   return false;
+}
+// What a call writes is written once (a tensor listed twice would be scaled once or twice, as
+// it happens), and an output other than its own gradient lies apart from all that is read, the
+// norm from everything.  False where it is not so.  A gradient scaled in place may share memory
+// with others whose outputs lie elsewhere: ``split``, those go first.
+bool memory_ok(rnn_clip_t h, const void* const* grads, void* const* out, const float* norm, int* split) {
+  auto &w = h->inplace, &a = h->apart, &r = h->reads;
+  w.clear();
+  a.clear();
+  r.clear();
+  for (int i = 0; i < h->num; ++i) {
+    const uint64_t bytes = static_cast<uint64_t>(h->start[i + 1] - h->start[i]) * (h->dtype[i] == RNN_F32 ? 4 : 2);
+    if (!bytes) continue;
+    if (!out || out[i] == grads[i]) {
+      add(w, grads[i], bytes);
+    } else {
+      add(a, out[i], bytes);
+      add(r, grads[i], bytes);
+    }
+  }
+  const uintptr_t n = reinterpret_cast<uintptr_t>(norm);
+  for (const Ranges* v : {&w, &a, &r})
+    for (const auto& x : *v)
+      if (n < x.second && n + sizeof(float) > x.first) return false;
+  if (!disjoint(w) || !disjoint(a)) return false;
+  disjoint(r);                               // gradients that are only read may overlap
+  if (meet(w, a) || meet(a, r)) return false;
+  *split = meet(w, r);
+  return true;
 }
 
 rnn_status_t clip_call(rnn_clip_t h, const void* const* grads, void* const* out, float max_norm, float eps, float* norm,
@@ -168,7 +204,8 @@ rnn_status_t clip_call(rnn_clip_t h, const void* const* grads, void* const* out,
     if (!grads[i] || !aligned(grads[i], es)) return RNN_BAD_PARAM;
     if (out && (!out[i] || !aligned(out[i], es))) return RNN_BAD_PARAM;
   }
-  if (scale && overlap(h, out ? static_cast<const void* const*>(out) : grads)) return RNN_BAD_PARAM;
+  int split = 0;
+  if (scale && !memory_ok(h, grads, out, norm, &split)) return RNN_BAD_PARAM;
   if (!workspace || !aligned16(workspace)) return RNN_BAD_WORKSPACE;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
@@ -187,6 +224,7 @@ rnn_status_t clip_call(rnn_clip_t h, const void* const* grads, void* const* out,
   c.norm = norm;
   c.partial = static_cast<double*>(workspace);
   c.scale = scale;
+  c.split = split;
   c.num_sms = h->num_sms;
   int n = 0;
   const int e = launch_clip(c, s, &n);
@@ -434,7 +472,9 @@ rnn_status_t rnn_clip_create(int num, const int64_t* counts, const int* dtypes, 
   if (rc != RNN_OK) return rc;
   try {
     h->dtype.assign(dtypes, dtypes + num);
-    h->ranges.reserve(num);
+    h->inplace.reserve(num);
+    h->apart.reserve(num);
+    h->reads.reserve(num);
     h->start.assign(1, 0);
     h->start.reserve(num + 1);
     for (int i = 0; i < num; ++i) h->start.push_back(h->start[i] + counts[i]);

@@ -700,9 +700,11 @@ rnn_status_t rnn_clip_get_sizes(rnn_clip_t handle, size_t* workspace_bytes);
 
 /*   grads    host array of num device pointers, aligned to their element only; those of
  *            empty tensors are not looked at
- *   out      the same, or NULL = in place; entry i may be grads[i], and overlaps no other
- *            grads.  Tensors written twice (a tensor listed twice in place, slices that
- *            overlap) are RNN_BAD_PARAM
+ *   out      the same, or NULL = in place; entry i is grads[i], or memory that overlaps
+ *            no gradient.  Tensors written twice (a tensor listed twice in place, slices
+ *            that overlap), and outputs or a norm over what is read, are RNN_BAD_PARAM.
+ *            A tensor scaled in place may share memory with gradients whose outputs lie
+ *            elsewhere: these get the values from before
  *   max_norm, eps  finite, >= 0
  *   norm     device fp32 [1] (out), 4-byte aligned
  *   workspace (workspace_bytes); calls of a handle run in the order they are made
