@@ -127,6 +127,24 @@ rnn_status_t conv_args(const rnn_conv_s* h, const rnn_conv_in_t* in, ConvArgs* a
   return RNN_OK;
 }
 
+// Whether dense memory shares any with the rows (of ``row`` bytes, every ``hop`` bytes) of a
+// sequence's input; the gaps of a packed projection are not part of it.
+bool over_rows(const void* to, int64_t bytes, const void* from, int64_t row, int64_t hop, int64_t rows) {
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(to)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(from));
+  if (at < 0) return at + bytes > 0;
+  const int64_t r = at / hop, in = at - r * hop;
+  return r < rows && (in < row || (in + bytes > hop && r + 1 < rows));
+}
+// An output of a whole sequence over x, of which threads read tokens that are others' to write.
+bool over_x(const rnn_conv_s* h, const ConvArgs& a, const void* out) {
+  const int64_t es = h->bf16 ? 2 : 4, rows = static_cast<int64_t>(a.B) * a.T;
+  return over_rows(out, rows * a.D * es, a.x, a.D * es, a.x_row * es, rows);
+}
+bool over_dense(const rnn_conv_s* h, const ConvArgs& a, const void* out, const void* in) {
+  const int64_t bytes = static_cast<int64_t>(a.B) * a.T * a.D * (h->bf16 ? 2 : 4);
+  return over_rows(out, bytes, in, bytes, bytes, 1);
+}
+
 // A new handle of type H with its device and call order; null after a failure.
 template <typename H>
 rnn_status_t make(H** out) {
@@ -395,6 +413,7 @@ rnn_status_t rnn_conv_forward(rnn_conv_t h, const rnn_conv_in_t* in, const void*
   ConvFwdArgs f{};
   const rnn_status_t rc = conv_args(h, in, &f.a);
   if (rc != RNN_OK) return rc;
+  if (over_x(h, f.a, y)) return RNN_BAD_PARAM;
   DeviceGuard dg(h->device);
   if (!dg.ok) return RNN_CUDA_ERROR;
   f.s0 = s0;
@@ -418,6 +437,7 @@ rnn_status_t rnn_conv_backward(rnn_conv_t h, const rnn_conv_in_t* in, const void
   const rnn_status_t rc = conv_args(h, in, &b.a);
   if (rc != RNN_OK) return rc;
   if (dbias && !in->bias) return RNN_BAD_PARAM;
+  if (dx && (over_x(h, b.a, dx) || over_dense(h, b.a, dx, dy))) return RNN_BAD_PARAM;
   const bool weights = dw || dbias;
   if ((weights && !workspace) || !aligned16(workspace)) return RNN_BAD_WORKSPACE;
   DeviceGuard dg(h->device);

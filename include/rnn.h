@@ -541,8 +541,10 @@ uint64_t rnn_norm_launch_count(rnn_norm_t handle);
  * this file hold, but for what is said here; no kernel of these operators waits for
  * another CTA or for a copy, so there is no status to ask for.  The calls of one
  * handle that use lengths, workspace or reserve run in the order they are made,
- * whatever their streams; calls captured into a graph are ordered by the caller.
- * Calls that should overlap take a handle each. */
+ * whatever their streams; calls captured into a graph are ordered by the caller, and
+ * the handle and its workspace live as long as the graph.  Calls that should overlap
+ * take a handle each.  Outputs share no memory with inputs or each other but where
+ * that is said. */
 typedef struct {
   int batch;           /* B >= 1                                                       */
   int seq_len;         /* T >= 1; batch * seq_len * channels at most 2^43              */
@@ -658,14 +660,15 @@ rnn_status_t rnn_conv_get_sizes(rnn_conv_t handle, size_t* backward_workspace_by
 rnn_status_t rnn_conv_set_seq_lengths(rnn_conv_t handle, const int* lengths);
 
 /*   s0 (may be NULL = zero)   y (out, dense)   sT (out, may be NULL; may be s0): the
- * last inputs of each sequence, those of s0 among them where it has fewer tokens. */
+ * last inputs of each sequence, those of s0 among them where it has fewer tokens.
+ * y over any of x is RNN_BAD_PARAM. */
 rnn_status_t rnn_conv_forward(rnn_conv_t handle, const rnn_conv_in_t* in, const void* s0, void* y, void* sT,
                               void* stream);
 
 /* Gradients of a forward call with these inputs.
  *   dy (dense)   dsT (may be NULL = zero)
  *   dx (dense), ds0, dw fp32 [channels, width], dbias fp32 [channels]: out, each may
- *   be NULL; dbias only with a bias
+ *   be NULL; dbias only with a bias; dx over any of x or dy is RNN_BAD_PARAM
  *   workspace    required with dw or dbias */
 rnn_status_t rnn_conv_backward(rnn_conv_t handle, const rnn_conv_in_t* in, const void* s0, const void* dy,
                                const void* dsT, void* dx, float* dw, float* dbias, void* ds0,
