@@ -14,13 +14,13 @@
 #include "vec.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace rnn {
 
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLift = 2e-8f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -35,21 +35,44 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // A token's decay 2^(A log2(e) delta), two states at a time, by the hardware's
-// approximation, which is 5e-9 (|x| near 1e-3) to 3e-8 (0.01 to 1) low on average: kLift,
-// added to the exponent by the same instruction that scales it, takes the middle of that
-// out, or a memory of many tokens would add it up (states of 77 tokens, error against 64
-// bits: 1.3e-6 without, 5.5e-7 with; training's dA 1.9e-6 and 9e-7).  A polynomial in fp32
-// that has no bias at all costs three times the whole recurrence in multiply-adds: 2.5
-// instead of 0.5 ms for 8 x 1024 tokens of 2048 channels and 32 states, and buys 1e-7.
+// approximation, which is low on average by (relative, in bins of |x|): 8e-9 to 5e-9 from
+// 1e-5 to 2e-3, 1e-8 at 4e-3, 1.6e-8 at 6e-3, 1e-8 to 3e-8 from 0.01 to 0.8, 5e-8 above one;
+// below 1.2e-7 it is exactly one (a token behind the last leaves the state as it is).
+// A memory of M tokens would add that up M times, so the exponent is lifted by it.
+//
+// bf16 storage: one constant, which the multiply-add that makes the exponent adds for
+// nothing.  It is the middle, so decays nearer to one than 2^-0.002 come out 8e-9 high: a
+// state that remembers 1e4 tokens 8e-5, against inputs that are rounded at 2e-3 each.
+//
+// fp32 storage: what belongs to the size of the exponent, a constant and a slope up to a
+// knee (states of 8192 tokens, error against 64 bits 4.9e-5 with one constant, 1.5e-5 so).
+// W tokens' slope at once: a bias is a sum over many tokens, so a sequence adds it at one
+// token in four.  8 x 1024 tokens of 2048 channels and 64 states 440 us, 432 with the constant,
+// 473 with the slope at every token.  A polynomial for exponents below 2^-6, which would
+// also take the approximation's own roundings out (3e-8 instead of 1.7e-8): 538 us.
+constexpr float kLift = 2e-8f, kLow = 9e-9f, kSlope = 2.7e-6f, kKnee = 0.0085f;
+template <typename T, int W = 1>
 __device__ __forceinline__ float2 decay2(float2 A2, float d) {
-  const float2 x = fma2(A2, both(d), both(kLift));
+  float2 x = fma2(A2, both(d), both(sizeof(T) == 2 ? kLift : kLow));
+  if constexpr (sizeof(T) == 4 && W > 0)
+    x = fma2(make_float2(fminf(fabsf(x.x), kKnee), fminf(fabsf(x.y), kKnee)), both(W * kSlope), x);
   return make_float2(ex2(x.x), ex2(x.y));
+}
+
+// The same for one state; ``slope`` is that of the tokens whose lift this one adds.
+template <typename T, bool ADDS>
+__device__ __forceinline__ float decay1(float A2, float d, float slope) {
+  float x = fmaf(A2, d, sizeof(T) == 2 ? kLift : kLow);
+  if (sizeof(T) == 4 && ADDS) x = fmaf(fminf(fabsf(x), kKnee), slope, x);
+  return ex2(x);
 }
 
 // log(1 + e^v) = max(v, 0) + log(1 + q), q = e^-|v|, two at a time.  log(1 + q) is
 // 2 artanh(s), s = q / (2 + q) <= 1/3, as s times a polynomial in s^2 (interpolated at
-// the Chebyshev nodes of [0, 1/9], off by 4e-9): relative accuracy at small steps, in a
-// third of log1pf's instructions.
+// the Chebyshev nodes of [0, 1/9], off by 1.5e-8, the logarithm by 5e-9 or a relative
+// 8e-9), in a third of log1pf's instructions.  The exponent |v| log2(e) is rounded, and with
+// it q by a relative |v| 2^-24 or so: 2 to 4e-7 of the steps in use (v of -7 to -2), which
+// scales a channel's rates by as much; expf would hold 1e-7 for ten more instructions.
 __device__ __forceinline__ float2 softplus2(float2 v) {
   const float2 q = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
   const float2 d = add2(q, both(2.f)), s = mul2(q, make_float2(rcp(d.x), rcp(d.y))), w = mul2(s, s);
@@ -59,7 +82,7 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   p = fma2(p, w, both(2.f));
   return fma2(p, s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));         // a NaN comes in through s
 }
-// 1 / (1 + e^-v) from the approximations, a few 2^-23 off.
+// 1 / (1 + e^-v) from the approximations, a few 2^-24 off and, for negative v, |v| 2^-24 more.
 __device__ __forceinline__ float2 sigmoid2(float2 v) {
   const float2 q = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(q.x), ex2(q.y)), both(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
@@ -119,7 +142,11 @@ __device__ __forceinline__ void store_states(const float2 (&h)[C][NS / 2], float
 }
 // A token behind the last one, and one whose step is zero, must leave the state as it is, so
 // a rate of minus infinity is held as a large number: a reset at every step above 1e-28.
-__device__ __forceinline__ float finite_rate(float a) { return isinf(a) ? copysignf(1e30f, a) : a; }
+__device__ __forceinline__ float finite_rate(float a) {
+  float r;
+  asm("{.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;}" : "=f"(r) : "f"(a), "f"(-1e30f), "f"(1e30f));
+  return r;
+}
 // The rates in units of log2(e).
 template <int C, int NS, int HOP>
 __device__ __forceinline__ void load_rates(float2 (&A2)[C][NS / 2], const ScanArgs& a, int c0, int ch, int n0, int width) {
@@ -221,7 +248,7 @@ struct Rows {
 };
 
 // Adds one segment's own end to what went through it: h = exp(A sum) h + end.
-template <int C, int NS, int HOP>
+template <typename T, int C, int NS, int HOP>
 __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A2)[C][NS / 2], const ScanArgs& a, const ScanSegs& g,
                                         int b, int i, int c0, int ch, int n0, int width) {
   const int64_t at = (static_cast<int64_t>(b) * g.nseg + i) * a.D + c0;
@@ -231,7 +258,7 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
   for (int c = 0; c < C; ++c) {
     const float sum = ch + c < width ? g.sums[at + ch + c] : 0.f;
 #pragma unroll
-    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2(A2[c][j], sum), h[c][j], e[c][j]);
+    for (int j = 0; j < NS / 2; ++j) h[c][j] = fma2(decay2<T>(A2[c][j], sum), h[c][j], e[c][j]);
   }
 }
 
@@ -348,7 +375,7 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
   }
   if (OUT)
 #pragma unroll 2
-    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<C, NS, HOP>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
+    for (int i = 0; i < w.seg && i * f.g.len < len; ++i) through<T, C, NS, HOP>(h, A2, a, f.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int j = 0; j < 4; ++j) sum[j] = both(0.f);
   float* pu = MODE == kTrain && gate ? f.ungated + row0 * a.D + w.c0 + col : nullptr;
@@ -399,6 +426,7 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
           pk += static_cast<int64_t>(a.D) * a.N;
         }
         const int t = BACK ? TT - 1 - half - q : half + q;
+        const bool t4 = q % 4 == (BACK ? 3 : 0);             // t is a multiple of four
         float d[C], u[C], yc[C];
         float2 Bv[P], Cv[P];
         lds<C>(d, &s.dt[t][ch]);
@@ -410,7 +438,7 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
           float2 r = both(0.f);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            const float2 e = decay2(A2[c][j], d[c]);
+            const float2 e = t4 ? decay2<T, 4>(A2[c][j], d[c]) : decay2<T, 0>(A2[c][j], d[c]);
             if (BACK) h[c][j] = mul2(e, fma2(Bv[j], both(u[c]), h[c][j]));
             else h[c][j] = fma2(e, h[c][j], mul2(Bv[j], both(u[c])));
             if (OUT) r = j ? fma2(Cv[j], h[c][j], r) : mul2(Cv[j], h[c][j]);
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
   load_states<C, NS, 4>(g, p.dhT ? p.dhT + bD * a.N : nullptr, a.N, ch, n0, w.width);
 #pragma unroll 2
   for (int i = p.g.nseg - 1; i > w.seg; --i)
-    if (i * p.g.len < len) through<C, NS, 4>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
+    if (i * p.g.len < len) through<T, C, NS, 4>(g, A2, a, p.g, w.b, i, w.c0, ch, n0, w.width);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -702,7 +730,7 @@ __global__ void __launch_bounds__(32, kBwdWarps) scan_bwd_kernel(const ScanBwdAr
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            e[q][c][j] = decay2(A2[c][j], d[c]);
+            e[q][c][j] = q % 4 ? decay2<T, 0>(A2[c][j], d[c]) : decay2<T, 4>(A2[c][j], d[c]);
             h[q + 1][c][j] = fma2(e[q][c][j], h[q][c][j], mul2(Bv[j], both(u[c])));
           }
       }
@@ -911,8 +939,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
     h[i] = A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < width && n > 0 && states) {
       h[i] = *reinterpret_cast<const float4*>(state + static_cast<int64_t>(i) * a.N);
-      const float4 q = *reinterpret_cast<const float4*>(a.A + at + static_cast<int64_t>(i) * a.N);
-      A[i] = make_float4(finite_rate(q.x), finite_rate(q.y), finite_rate(q.z), finite_rate(q.w));
+      A[i] = *reinterpret_cast<const float4*>(a.A + at + static_cast<int64_t>(i) * a.N);
     }
   }
   const float bias = own && a.bias ? a.bias[d] : 0.f, skip = own && a.skip ? a.skip[d] : 0.f;
@@ -940,16 +967,26 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
     dv += bias;
     if (a.softplus) dv = softplus2(both(dv)).x;
     const float e = dv * kLog2e, u = dv * xv;
-    float y[CH];
+    // only a step next to zero needs it, and at the start of the kernel the rates would be
+    // waited for before a token is asked for (28.1 us become 30.7)
+    if (__any_sync(kFull, own && fabsf(e) < 1e-20f))
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float ei = __shfl_sync(kFull, e, i, SL), ui = __shfl_sync(kFull, u, i, SL);
-      h[i].x = fmaf(ex2(fmaf(A[i].x, ei, kLift)), h[i].x, ui * Bv[0]);
-      h[i].y = fmaf(ex2(fmaf(A[i].y, ei, kLift)), h[i].y, ui * Bv[1]);
-      h[i].z = fmaf(ex2(fmaf(A[i].z, ei, kLift)), h[i].z, ui * Bv[2]);
-      h[i].w = fmaf(ex2(fmaf(A[i].w, ei, kLift)), h[i].w, ui * Bv[3]);
-      y[i] = fmaf(Cv[3], h[i].w, fmaf(Cv[2], h[i].z, fmaf(Cv[1], h[i].y, Cv[0] * h[i].x)));
-    }
+      for (int i = 0; i < CH; ++i) A[i] = make_float4(finite_rate(A[i].x), finite_rate(A[i].y), finite_rate(A[i].z), finite_rate(A[i].w));
+    float y[CH];
+    auto update = [&](auto adds) {
+      const float slope = decltype(adds)::value ? kSlope * static_cast<float>(n - t < 4 ? n - t : 4) : 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const float ei = __shfl_sync(kFull, e, i, SL), ui = __shfl_sync(kFull, u, i, SL);
+        h[i].x = fmaf(decay1<T, decltype(adds)::value>(A[i].x, ei, slope), h[i].x, ui * Bv[0]);
+        h[i].y = fmaf(decay1<T, decltype(adds)::value>(A[i].y, ei, slope), h[i].y, ui * Bv[1]);
+        h[i].z = fmaf(decay1<T, decltype(adds)::value>(A[i].z, ei, slope), h[i].z, ui * Bv[2]);
+        h[i].w = fmaf(decay1<T, decltype(adds)::value>(A[i].w, ei, slope), h[i].w, ui * Bv[3]);
+        y[i] = fmaf(Cv[3], h[i].w, fmaf(Cv[2], h[i].z, fmaf(Cv[1], h[i].y, Cv[0] * h[i].x)));
+      }
+    };
+    if (sizeof(T) == 4 && t % 4 == 0) update(std::true_type{});
+    else update(std::false_type{});
     // lane sl of each four ends up with the sum of channel sl
     if constexpr (CH == 4) {
       const bool up = sl & 2;
