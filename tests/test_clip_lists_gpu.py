@@ -1,6 +1,8 @@
-"""Which lists of tensors clipping takes."""
+"""Which lists of tensors clipping takes, the flat weight gradient of recurrent layers among them."""
+import numpy as np
 import pytest
 
+from oracle import ssm_oracle as O
 from tests.test_lm_streams_gpu import _delay
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +85,30 @@ def test_a_view_of_a_tensor_that_is_scaled_in_place(num):
     for got, want in ((whole, keep), (out[1], keep[7:1_500_007]), (out[2], keep[1_400_001:2_900_001])):
         # the norm given back, its sum with eps, the factor and the product: four roundings
         assert ((got.double() - want.double() * f).abs() <= 2.0 ** -22 * f * want.double().abs()).all()
+
+
+@pytest.mark.parametrize("mode,dtype", [("lstm", "bf16"), ("gru", "f32")])
+def test_weight_gradients_of_recurrent_layers(mode, dtype):
+    """The flat fp32 dw of a stack beside another operator's gradients, clipped in place."""
+    import torch
+    import bwd_persistent_cta_gb300 as R
+    T, B, I, H = 12, 8, 40, 64
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    net = R.RNN(mode, I, H, T, B, num_layers=2, bidirectional=True, dtype=dtype)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
+    w = (0.1 * rnd(net.weight_count)).to(td)
+    x, dy = rnd(T, B, I).to(td), rnd(T, B, 2 * H).to(td)
+    net.forward(x, w)
+    net.backward_data(dy, w)
+    dw = net.backward_weights(x)
+    net.sync()
+    other = rnd(333).bfloat16()
+    host = [t.double().cpu().numpy() for t in (dw, other)]
+    assert dw.dtype == torch.float32 and np.abs(host[0]).max() > 0
+    limit = 0.25 * float(np.sqrt(sum((h ** 2).sum() for h in host)))
+    norm, want = O.clip(host, float(np.float32(limit)))
+    got = R.GradClip([dw.numel(), 333], ["f32", "bf16"]).clip([dw, other], limit)
+    assert abs(got.item() - norm) <= 2.0 ** -22 * norm
+    for t, v, tol in ((dw, want[0], 2.0 ** -22), (other, want[1], 2.0 ** -8)):
+        assert np.all(np.abs(t.double().cpu().numpy() - v) <= tol * np.abs(v) + 2.0 ** -133)
