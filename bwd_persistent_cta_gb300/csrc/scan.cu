@@ -265,10 +265,10 @@ __device__ __forceinline__ void through(float2 (&h)[C][NS / 2], const float2 (&A
 // ---------------------------------------------------------------------------
 // forward, and what a segment leaves by itself in either direction
 // ---------------------------------------------------------------------------
-// A warp works alone: a tile of eight tokens of its channels is on its way into shared
-// memory while it works on the one before; it leaves the steps in shared memory, runs the
-// recurrence and finishes the outputs, with no barrier but its own.  Nothing but the
-// states, their rates and the token at hand stays in registers, so that three warps a
+// A warp works alone: one or three tiles of 8 or 16 tokens of its channels are on their way
+// into shared memory while it works on the one before; it leaves the steps in shared memory,
+// runs the recurrence and finishes the outputs, with no barrier but its own.  Nothing but the
+// states, their rates and the token at hand stays in registers, so that two or three warps a
 // scheduler hide the latencies of each other.  Eight states a lane: at 16 states two lanes
 // share a channel, and a sum over the states is one exchange.
 //
@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(32, fwd_warps(SL)) scan_fwd_kernel(const ScanF
 // the slots with two warps a scheduler: states and decays of the four tokens take the
 // registers.  Kept states eight tokens apart leave no room for the decays, and computing
 // them twice cost 110 us.
-constexpr int kBwdWarps = 8;     // an SM
+// Warps an SM: what the registers allow.  Shared memory leaves as many in bf16 above 8 states,
+// 5 up to there, and in fp32 4, 6, 7 and 6 at 8, 16, 32 and 64 states.
+constexpr int kBwdWarps = 8;
 constexpr int kBT = 8, kBSub = kScanKeep, kBNS = 4, kBC = 4;
 
 template <typename T, int SL>
@@ -916,8 +918,8 @@ __global__ void __launch_bounds__(128) scan_sum_kernel(const ScanBwdArgs p) {
 // SL lanes have CH = min(SL, 4) channels, four states of each a lane.  A lane prepares one
 // of the channels (its step, and at the end its output) and hands the step to the others.
 // Memory bounds it, the states in and out: 256 sequences of 4096 channels and 16 states in
-// 27 us, 5.3 TB/s (a cold call 33; 35 with 56 registers a thread for more warps, 45 with
-// 42); four tokens of each in 59 us, where issue does.
+// 28 us, 5.2 TB/s (a cold call 33; 35 with 56 registers a thread for more warps, 45 with
+// 42); four tokens of each in 56 us (cold 59), where issue does.
 constexpr int kStepThreads = 128;
 template <typename T, int SL>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepArgs p) {
@@ -1151,8 +1153,9 @@ ScanSplit split(const ScanArgs& a, int64_t n, bool first) {
 // five do not pay up to 16 states (8 x 1024 tokens of 2048 channels, 8 states, fp32: 108 us
 // in one piece, 128 in three; training 121 and 148), above that fewer than three (2 x 1024
 // tokens of 1024 channels, 64 states: 125 us in one piece, 104 in four; 4 x 1024 of 2048, 32
-// states: 113 and 125 in two).  64 tokens each at least (300 tokens of 2048 channels 29 us,
-// 43 with 128).
+// states: 113 and 125 in two).  64 tokens each at least, so up to 16 states less than 320 tokens
+// are one piece (1 x 300 tokens of 2048 channels, bf16, 16 states 23 us and 23 in four pieces,
+// 8 states 30 and 17; in nine pieces of 32 tokens 17 and 13, but 4 x 300 25 and 29).
 ScanSplit scan_split_forward(const ScanArgs& a, int is_bf16) {
   const int64_t all = static_cast<int64_t>(a.B) * a.G, wide = all * per_group(a, fwd_width(a.N, true));
   int64_t n = 1;
@@ -1165,10 +1168,10 @@ ScanSplit scan_split_forward(const ScanArgs& a, int is_bf16) {
   return split(a, n, true);
 }
 
-// Backward, where an SM holds eight warps: 512 warps, 2048 tokens, 744 us in one piece, 648
-// in 2, 625 in 8; from four warps an SM on it is in one piece, else it fills the SMs three
-// times, with 32 tokens a segment at least (513 tokens of 3 x 528 channels, fp32: 50 us, 60
-// with 64).
+// Backward, reckoned with eight warps an SM (16 states: 512 warps, 2048 tokens, bf16, 744 us in
+// one piece, 648 in 2, 625 in 8): from four warps an SM on it is in one piece, else it fills the
+// SMs three times, with 32 tokens a segment at least (513 tokens of 3 x 528 channels, fp32: 50
+// us, 60 with 64).  Where shared memory holds fewer warps it is the same rule, not measured.
 ScanSplit scan_split_backward(const ScanArgs& a) {
   const int64_t warps = static_cast<int64_t>(a.B) * a.G * per_group(a, bwd_width(a.N));
   int64_t n = 1;

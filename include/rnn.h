@@ -591,7 +591,9 @@ typedef struct {
 /* As rnn_delta_create / _destroy / _get_sizes / _set_seq_lengths: tokens at
  * t >= lengths[b] are not read, the state stays as it was, y is zero there and so
  * are all gradients.  The reserve holds the states before every four tokens and y
- * before its gate: channels * (states + 4) bytes a token. */
+ * before its gate: channels * (states + 4) bytes a token.  The backward workspace is
+ * mostly partial sums of dB and dC: 1, 4, 16 and 64 bytes a token and channel at up to
+ * 8, 16, 32 and 64 states (more where a group has fewer than 64, 32, 16 or 8 channels). */
 rnn_status_t rnn_scan_create(const rnn_scan_desc_t* desc, rnn_scan_t* handle);
 rnn_status_t rnn_scan_destroy(rnn_scan_t handle);
 rnn_status_t rnn_scan_get_sizes(rnn_scan_t handle, size_t* workspace_bytes,
@@ -710,7 +712,8 @@ rnn_status_t rnn_clip_get_sizes(rnn_clip_t handle, size_t* workspace_bytes);
  *            elsewhere: these get the values from before
  *   max_norm, eps  finite, >= 0
  *   norm     device fp32 [1] (out), 4-byte aligned
- *   workspace (workspace_bytes); calls of a handle run in the order they are made
+ *   workspace (workspace_bytes); calls of a handle run in the order they are made, and
+ *            a graph that captured one needs the handle and the workspace as long as it lives
  * rnn_clip_norm only writes the norm. */
 rnn_status_t rnn_clip_scale(rnn_clip_t handle, const void* const* grads, void* const* out, float max_norm,
                             float eps, float* norm, void* workspace, void* stream);
