@@ -328,7 +328,7 @@ class CausalConv(_Sequences):
         return rnn_conv_in_t(x.data_ptr(), w.data_ptr(), _p(bias), self._rows(x, "x", self._x, 2, True))
 
     def forward(self, x, w, bias=None, s0=None, y=None, sT=None, stream=None):
-        """(y, sT).  sT may be s0."""
+        """(y, sT).  sT may be s0; y lies apart from x."""
         if stream is not None:
             return self._elsewhere(self.forward, stream, x, w, bias=bias, s0=s0, y=y, sT=sT)
         a = self._inputs(x, w, bias)
@@ -437,9 +437,9 @@ class GradClip(_Op):
         return norm
 
     def clip(self, grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, stream=None):
-        """Scales ``grads`` by min(1, max_norm / (norm + eps)), in place or into the tensors of ``out``, and returns the
-        norm before it (fp32 [1] on the device; infinity where fp32 cannot hold it).  With a NaN or infinity among
-        them the values stay as they are."""
+        """Scales ``grads`` by min(1, max_norm / (norm + eps)), in place or into the tensors of ``out`` (each its gradient,
+        or memory that no gradient shares; nothing is written twice), and returns the norm before it (fp32 [1] on the
+        device; infinity where fp32 cannot hold it).  With a NaN or infinity among them the values stay as they are."""
         grads, out = self._listed(grads), None if out is None else self._listed(out)
         if stream is not None:
             return self._elsewhere(self.clip, stream, grads, max_norm, eps=eps, out=out, norm=norm)

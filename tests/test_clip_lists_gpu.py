@@ -53,7 +53,7 @@ def test_outputs_over_other_tensors_are_refused():
     def call(out, norm=p + 4096, grads=g):
         return R.rnn_clip_scale(op.handle, grads, out, 1.0, 1e-6, norm, ws.data_ptr())
 
-    for out in (g, (p + 2048, None, p + 3072), (p, None, p + 2048), (p + 2048, p, p + 1024), (p + 400, None, p + 1124),
+    for out in (g, (p + 2048, None, p + 3584), (p, None, p + 2048), (p + 2048, p, p + 1024), (p + 400, None, p + 1124),
                 (p + 2048, None, p + 924)):
         assert call(out) == R.RNN_OK, out
     # over the other gradient, over a shifted part of its own, and over both
@@ -61,12 +61,12 @@ def test_outputs_over_other_tensors_are_refused():
                 (p, None, p + 1026), (p + 1024, None, p), (p + 628, None, p + 2048), (p + 1120, None, p + 2048)):
         assert call(out) == R.RNN_BAD_PARAM, out
     for norm in (p, p + 396, p + 1024, p + 1120):
-        assert call(None, norm) == R.RNN_BAD_PARAM and call((p + 2048, None, p + 3072), norm) == R.RNN_BAD_PARAM, norm
-    for norm in (p + 2048, p + 3168):
-        assert call((p + 2048, None, p + 3072), norm) == R.RNN_BAD_PARAM, norm
+        assert call(None, norm) == R.RNN_BAD_PARAM and call((p + 2048, None, p + 3584), norm) == R.RNN_BAD_PARAM, norm
+    for norm in (p + 2048, p + 3680):
+        assert call((p + 2048, None, p + 3584), norm) == R.RNN_BAD_PARAM, norm
     assert call(None, p + 400) == R.RNN_OK and call(None, p + 1124) == R.RNN_OK
     # two gradients may share memory that is only read
-    assert call((p + 2048, None, p + 3072), grads=(p, None, p + 200)) == R.RNN_OK
+    assert call((p + 2048, None, p + 3584), grads=(p, None, p + 200)) == R.RNN_OK
     torch.cuda.synchronize()
 
 
